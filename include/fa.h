@@ -221,6 +221,101 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
                     int window_left, const int32_t* seqlens_k, int num_ctas, void* workspace,
                     size_t workspace_bytes, void* stream);
 
+/* Attention over a paged key/value cache. The page "FlashAttention — L3
+ * Cross-Paper Synthesis" (section 3) names short-query attention over a cache,
+ * bound by reading K and V from HBM, as left unoptimised; a server keeps that
+ * cache in pages, so that sequences of any length share one pool, and quantises
+ * it, which halves the bytes to read. Three calls work on it: fa_paged_write
+ * (new rows enter the cache), fa_paged_read (rows come back out of it) and
+ * fa_paged_attn (attention of the new tokens, one per sequence or a chunk).
+ *
+ * The cache, a pool of pages shared by all sequences:
+ *   k_pages, v_pages: row r of page p and K/V head h is the d values from element
+ *     p * stride_page + h * stride_head + r * stride_row on (the strides count
+ *     elements and are the same for both), so [num_pages, H_kv, page_size, d],
+ *     [num_pages, page_size, H_kv, d] and views into larger tensors all do. Base
+ *     pointers are 16-byte aligned, and the strides are positive multiples of
+ *     16 bytes, below 2^40 bytes.
+ *   type: FA_CACHE_BF16 (bf16 values) or FA_CACHE_E4M3 (one e4m3 code per value and
+ *     one scale byte per row, k_scale and v_scale: uint8 [num_pages, H_kv,
+ *     page_size], contiguous; NULL for bf16). A quantised value is code * 2^E with
+ *     scale byte E + 127, E the smallest exponent in [-117, 7] that keeps the row's
+ *     largest magnitude within 448 * 2^E (0 for a row of zeros); codes are rounded
+ *     to nearest even and saturate (magnitudes above 57344 = 448 * 2^7). A row that
+ *     holds a NaN or an infinity gets scale byte 255 and code 0x7F throughout and
+ *     counts as NaN. Both products and read-back use code * 2^E, which is exact in
+ *     bf16. Scale bytes 135 to 254 are never written; they count as 134.
+ *   page_size: a multiple of 16; d: 64 or 128.
+ * The batch, B sequences (device pointers):
+ *   page_table: int32, row b at b * table_stride; its entry i < max_pages names the
+ *     page of positions i * page_size .. of sequence b. Entries past a sequence's
+ *     length are not read. max_pages * page_size < 2^31 - 256.
+ *   kv_lens: int32 [B], the length of each sequence, its new tokens included.
+ *   cu_seqlens_q: int32 [B + 1], new tokens of sequence b are rows cu[b] .. cu[b+1]
+ *     of the T packed token rows (none is possible), the last positions of the
+ *     sequence: token i of n sits at position kv_lens[b] - n + i. Rows from cu[B] on
+ *     are neither read nor written. NULL: max_q rows each, T = B * max_q.
+ * What lies on the device is checked there, before any access: offsets out of order
+ * or beyond T, a length outside [0, max_pages * page_size], a page number outside
+ * [0, num_pages) and, for fa_paged_attn, a sequence with more than max_q new tokens.
+ * Each is reported as FA_ERR_INVALID_ARG by fa_device_status; such a page reads as
+ * zeros and is not written, such a length counts as 0 and such a sequence has no
+ * new tokens. Pages that two sequences share are fine to read; where a write's
+ * positions lead to the same row of a page twice, one of the two stays. */
+typedef enum { FA_CACHE_BF16 = 0, FA_CACHE_E4M3 = 1 } fa_cache_type;
+
+/* Stores k_new and v_new into the pages at their positions. k_new, v_new: bf16 [T,
+ * H_kv, d], token t at t * k_stride and t * v_stride (elements, multiples of 8), heads
+ * and d contiguous, 16-byte aligned. Tokens at negative positions (a length below the
+ * number of new tokens) are not stored. Deterministic.
+ * Errors: FA_ERR_INVALID_ARG (null or unaligned pointers, sizes, strides),
+ * FA_ERR_UNSUPPORTED (d, type, page_size not a multiple of 16), FA_ERR_CUDA.
+ * Asynchronous on `stream`; nothing is allocated. T = 0 is allowed and does nothing. */
+fa_status fa_paged_write(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                         uint8_t* k_scale, uint8_t* v_scale, int type, int num_pages,
+                         int page_size, int H_kv, int d, int64_t stride_page, int64_t stride_head,
+                         int64_t stride_row, const int32_t* page_table, int64_t table_stride,
+                         int max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens_q, int B,
+                         int T, int max_q, int64_t k_stride, int64_t v_stride, void* stream);
+
+/* Copies positions 0 .. N - 1 of every sequence out of the pages, dequantised, into
+ * k_out and v_out: bf16 [B, H_kv, N, d], contiguous, 16-byte aligned, the layout that
+ * fa_fwd, fa_decode (with seqlens_k = kv_lens) and fa_fp8_quantize take. Positions at or
+ * behind a sequence's length are written as zeros. Errors and conventions as above. */
+fa_status fa_paged_read(const void* k_pages, const void* v_pages, const uint8_t* k_scale,
+                        const uint8_t* v_scale, int type, int num_pages, int page_size, int H_kv,
+                        int d, int64_t stride_page, int64_t stride_head, int64_t stride_row,
+                        const int32_t* page_table, int64_t table_stride, int max_pages,
+                        const int32_t* kv_lens, int B, int N, void* k_out, void* v_out,
+                        void* stream);
+
+/* Attention of the new tokens over the cache, which holds their own keys and values
+ * already. q: bf16 [T, H, d], token t at t * q_stride (elements, a multiple of 8), 16-byte
+ * aligned; query head h reads K/V head h / (H / H_kv), H / H_kv <= 128. The token at
+ * position p of a sequence of length L sees keys j < L, with causal j <= p, and with
+ * window_left >= 0 only j >= p - window_left. Writes o (bf16 [T, H, d], contiguous,
+ * 16-byte aligned) and lse (fp32 [T, H], natural log); a row that sees no key gets O = 0
+ * and lse = -inf. Cached rows of positions below a sequence's length are expected to be
+ * finite (a NaN or an infinity there may reach every new token of the sequence); what lies
+ * behind the length, in the same page too, does not matter.
+ *   max_q: the largest number of new tokens of one sequence (a bound on it is enough).
+ *   workspace: fa_paged_workspace_size(H, H_kv, d, max_q) bytes, 16-byte aligned; its
+ *   contents on entry do not matter.
+ * The work of a call is divided among the SMs by the lengths found on the device, so a
+ * captured call may be replayed with other lengths. Results do not depend on atomics.
+ * Errors: FA_ERR_INVALID_ARG (as above, H not a multiple of H_kv, scale not positive and
+ * finite, window_left < -1, max_q < 1, T * H >= 2^31), FA_ERR_UNSUPPORTED (H / H_kv >
+ * 128, and as above), FA_ERR_WORKSPACE, FA_ERR_CUDA. */
+size_t fa_paged_workspace_size(int H, int H_kv, int d, int max_q);
+fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
+                        const uint8_t* k_scale, const uint8_t* v_scale, void* o, float* lse,
+                        int type, int num_pages, int page_size, int H, int H_kv, int d,
+                        int64_t stride_page, int64_t stride_head, int64_t stride_row,
+                        const int32_t* page_table, int64_t table_stride, int max_pages,
+                        const int32_t* kv_lens, const int32_t* cu_seqlens_q, int B, int T,
+                        int max_q, int64_t q_stride, float scale, int causal, int window_left,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* FP8 forward with incoherent processing (FA-3's FP8 path, which the
  * cross-paper synthesis page on FlashAttention names in its section 2), head
  * dimension 128, forward only.
@@ -300,7 +395,8 @@ fa_status fa_butterfly_mask(uint8_t* mask_host, int nb);
 
 /* Reads the status word of the current device after synchronising `stream`;
  * returns FA_OK or the first device-side error recorded since the last clear:
- * FA_ERR_TIMEOUT (a bounded wait ran out), or FA_ERR_CUDA when a kernel found
+ * FA_ERR_TIMEOUT (a bounded wait ran out), FA_ERR_INVALID_ARG when a paged call
+ * met a length, offset or page number out of range (see there), or FA_ERR_CUDA when a kernel found
  * its launch unusable and returned without work (the d = 128 forward and the
  * d = 128 key-tile backward kernel use nearly all 227 KB of shared memory with
  * no alignment slack and check that their dynamic shared memory starts on a

@@ -9,7 +9,9 @@ the library is missing or fails to load, calls raise.
 
 ``fwd`` / ``bwd`` are conveniences that allocate the outputs (and the backward
 workspace) with torch and call ``fa_fwd`` / ``fa_bwd``; ``decode`` does the
-same for ``fa_decode`` (short query blocks over a K/V cache).
+same for ``fa_decode`` (short query blocks over a K/V cache). ``paged_write``,
+``paged_read`` and ``paged_attn`` work on a cache held in pages, in bf16 or
+quantised to e4m3 (``paged_cache`` allocates one).
 """
 from __future__ import annotations
 
@@ -30,11 +32,15 @@ FA_ERR_CUDA = 3
 FA_ERR_WORKSPACE = 4
 FA_ERR_TIMEOUT = 5
 
+FA_CACHE_BF16 = 0
+FA_CACHE_E4M3 = 1
+
 # Symbols declared in include/fa.h.
 EXPORTS = (
     "fa_fwd", "fa_bwd", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_window", "fa_bwd_window",
     "fa_bwd_workspace_size", "fa_bwd_preprocess",
     "fa_bwd_dkdv", "fa_bwd_dq", "fa_decode", "fa_decode_workspace_size",
+    "fa_paged_write", "fa_paged_read", "fa_paged_attn", "fa_paged_workspace_size",
     "fa_fp8_workspace_size", "fa_fp8_vt_stride", "fa_fp8_quantize", "fa_fwd_fp8",
     "fa_fp8_quantize_gqa", "fa_fwd_fp8_gqa",
     "fa_bwd_noalloc", "fa_dropout_p8", "fa_debug_dropout_keep",
@@ -102,6 +108,17 @@ def load(build_if_missing: bool = False):
         lib.fa_decode_workspace_size.restype = sz
         lib.fa_decode.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp, i, vp, sz, vp]
         lib.fa_decode.restype = i
+        i64 = ctypes.c_int64
+        cache = [i, i, i, i, i, i64, i64, i64, vp, i64, i, vp]  # type .. d, strides, table, lengths
+        lib.fa_paged_write.argtypes = [vp] * 6 + cache + [vp, i, i, i, i64, i64, vp]
+        lib.fa_paged_write.restype = i
+        lib.fa_paged_read.argtypes = [vp] * 4 + cache + [i, i, vp, vp, vp]
+        lib.fa_paged_read.restype = i
+        lib.fa_paged_workspace_size.argtypes = [i, i, i, i]
+        lib.fa_paged_workspace_size.restype = sz
+        lib.fa_paged_attn.argtypes = ([vp] * 7 + [i, i, i, i, i, i, i64, i64, i64, vp, i64, i, vp]
+                                      + [vp, i, i, i, i64, f, i, i, vp, sz, vp])
+        lib.fa_paged_attn.restype = i
         lib.fa_fp8_workspace_size.argtypes = [i, i, i]
         lib.fa_fp8_workspace_size.restype = sz
         lib.fa_fp8_vt_stride.argtypes = [i]
@@ -310,6 +327,43 @@ def fa_decode(q, k_cache, v_cache, o, lse, B, H, H_kv, Nq, Nk, d, scale, causal=
                             _stream(stream))
 
 
+def fa_paged_write(k_new, v_new, k_pages, v_pages, k_scale, v_scale, type, num_pages, page_size,
+                   H_kv, d, stride_page, stride_head, stride_row, page_table, table_stride,
+                   max_pages, kv_lens, cu_seqlens_q, B, T, max_q, k_stride, v_stride,
+                   stream=None) -> int:
+    return load().fa_paged_write(_ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages),
+                                 _ptr(k_scale), _ptr(v_scale), type, num_pages, page_size, H_kv, d,
+                                 stride_page, stride_head, stride_row, _ptr(page_table),
+                                 table_stride, max_pages, _ptr(kv_lens), _ptr(cu_seqlens_q), B, T,
+                                 max_q, k_stride, v_stride, _stream(stream))
+
+
+def fa_paged_read(k_pages, v_pages, k_scale, v_scale, type, num_pages, page_size, H_kv, d,
+                  stride_page, stride_head, stride_row, page_table, table_stride, max_pages,
+                  kv_lens, B, N, k_out, v_out, stream=None) -> int:
+    return load().fa_paged_read(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), type,
+                                num_pages, page_size, H_kv, d, stride_page, stride_head,
+                                stride_row, _ptr(page_table), table_stride, max_pages,
+                                _ptr(kv_lens), B, N, _ptr(k_out), _ptr(v_out), _stream(stream))
+
+
+def fa_paged_workspace_size(H, H_kv, d, max_q) -> int:
+    return int(load().fa_paged_workspace_size(H, H_kv, d, max_q))
+
+
+def fa_paged_attn(q, k_pages, v_pages, k_scale, v_scale, o, lse, type, num_pages, page_size, H,
+                  H_kv, d, stride_page, stride_head, stride_row, page_table, table_stride,
+                  max_pages, kv_lens, cu_seqlens_q, B, T, max_q, q_stride, scale, causal=False,
+                  window_left=-1, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load().fa_paged_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+                                _ptr(v_scale), _ptr(o), _ptr(lse), type, num_pages, page_size, H,
+                                H_kv, d, stride_page, stride_head, stride_row, _ptr(page_table),
+                                table_stride, max_pages, _ptr(kv_lens), _ptr(cu_seqlens_q), B, T,
+                                max_q, q_stride, float(scale), int(bool(causal)),
+                                int(window_left), _ptr(workspace), int(workspace_bytes),
+                                _stream(stream))
+
+
 def fa_fp8_workspace_size(B, H, d) -> int:
     return int(load().fa_fp8_workspace_size(B, H, d))
 
@@ -500,4 +554,161 @@ def fwd_fp8(qz, scale, causal=False, seqlens_k=None, stream=None):
     else:
         st = fa_fwd_fp8_gqa(*args, B, H, Hkv, N, d, scale, causal, seqlens_k, stream)
     _check(st, "fa_fwd_fp8")
+    return o, lse
+
+
+# ------------------------------------------------------------- paged caches
+
+def paged_cache(num_pages, page_size, H_kv, d, e4m3=False, device="cuda"):
+    """Allocate an empty paged cache: dict(k_pages, v_pages [num_pages, H_kv, page_size, d],
+    bf16, or uint8 e4m3 codes with k_scale, v_scale uint8 [num_pages, H_kv, page_size];
+    these are None for bf16). The keywords are those of paged_write, paged_read and
+    paged_attn."""
+    shape = (num_pages, H_kv, page_size, d)
+    out = {}
+    for n in ("k", "v"):
+        out[n + "_pages"] = torch.empty(shape, dtype=torch.uint8 if e4m3 else torch.bfloat16,
+                                        device=device)
+        out[n + "_scale"] = (torch.empty(shape[:3], dtype=torch.uint8, device=device) if e4m3
+                             else None)
+    return out
+
+
+def _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale):
+    """Arguments that the paged calls share, checked: (cache type .. d and strides, then the
+    table and the lengths) as the C entry points take them, and B."""
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages and v_pages must be alike, [num_pages, H_kv, page_size, d]")
+    P, Hkv, page, d = k_pages.shape
+    st = k_pages.stride()
+    if v_pages.stride() != st or (d > 1 and st[3] != 1):
+        raise ValueError("k_pages and v_pages must have the same strides, with d contiguous")
+    dev = k_pages.device
+    if dev.type != "cuda" or v_pages.device != dev:
+        raise ValueError("k_pages and v_pages must be CUDA tensors on one device")
+    if k_pages.dtype == torch.bfloat16:
+        kind = FA_CACHE_BF16
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no scales")
+    elif k_pages.dtype in (torch.uint8, torch.float8_e4m3fn):
+        kind = FA_CACHE_E4M3
+        for t in (k_scale, v_scale):
+            if (t is None or t.dtype != torch.uint8 or t.shape != (P, Hkv, page)
+                    or not t.is_contiguous() or t.device != dev):
+                raise ValueError("an e4m3 cache needs k_scale and v_scale, contiguous uint8 "
+                                 f"[{P}, {Hkv}, {page}] on {dev}")
+    else:
+        raise ValueError("pages must be bf16, or e4m3 codes (uint8 or float8_e4m3fn)")
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev
+            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError(f"page_table must be int32 [B, max_pages] on {dev}, rows contiguous")
+    B, width = page_table.shape
+    if (kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or kv_lens.device != dev
+            or not kv_lens.is_contiguous()):
+        raise ValueError(f"kv_lens must be contiguous int32 [{B}] on {dev}")
+    # the stride of a dimension of size one is never used: any valid one stands for it
+    sr = st[2] if page > 1 else d
+    sh = st[1] if Hkv > 1 else sr * page
+    sp = st[0] if P > 1 else sh * Hkv
+    ts = page_table.stride(0) if B > 1 else width
+    return (kind, P, page), (Hkv, d, sp, sh, sr, page_table, ts, width, kv_lens), B
+
+
+def _new_rows(name, x, heads, d, dev):
+    """Token stride of packed rows [T, heads, d] with heads and d contiguous."""
+    if (x.dtype != torch.bfloat16 or x.dim() != 3 or tuple(x.shape[1:]) != (heads, d)
+            or x.device != dev or x.stride(2) != 1 or (heads > 1 and x.stride(1) != d)):
+        raise ValueError(f"{name} must be bf16 [T, {heads}, {d}] on {dev}, heads and d contiguous")
+    return x.stride(0) if x.shape[0] > 1 else heads * d
+
+
+def _offsets(cu, B, T, max_q, dev):
+    """max_q of a batch of T packed rows; checks cu_seqlens_q."""
+    if cu is None:
+        if T % B != 0 or (max_q is not None and max_q * B != T):
+            raise ValueError("without cu_seqlens_q the rows must be B times max_q")
+        return T // B
+    if (cu.dtype != torch.int32 or cu.shape != (B + 1,) or cu.device != dev
+            or not cu.is_contiguous()):
+        raise ValueError(f"cu_seqlens_q must be contiguous int32 [{B + 1}] on {dev}")
+    return T if max_q is None else max_q
+
+
+def _used_on(stream, *tensors):
+    """Tell the allocator that tensors made here are used on a stream other than the
+    current one, so that their memory is not handed out again before that work is done."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def paged_write(k_new, v_new, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None,
+                k_scale=None, v_scale=None, stream=None):
+    """Store new rows k_new, v_new [T, H_kv, d] into the pages (fa_paged_write). The new tokens
+    of sequence b are rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] (T / B each without
+    cu_seqlens_q) and take its last positions, kv_lens [B] counting them already."""
+    head, batch, B = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
+    dev, T = k_pages.device, k_new.shape[0]
+    ks = _new_rows("k_new", k_new, batch[0], batch[1], dev)
+    vs = _new_rows("v_new", v_new, batch[0], batch[1], dev)
+    if v_new.shape[0] != T:
+        raise ValueError("k_new and v_new must have the same number of rows")
+    n = _offsets(cu_seqlens_q, B, T, None, dev)
+    with torch.cuda.device(dev):
+        _check(fa_paged_write(k_new, v_new, k_pages, v_pages, k_scale, v_scale, *head, *batch,
+                              cu_seqlens_q, B, T, n, ks, vs, stream), "fa_paged_write")
+
+
+def paged_read(k_pages, v_pages, page_table, kv_lens, N, k_scale=None, v_scale=None, stream=None):
+    """Copy positions 0 .. N - 1 of every sequence out of the pages (fa_paged_read): k and v,
+    bf16 [B, H_kv, N, d], zeros behind each sequence. fwd and decode take them with
+    seqlens_k=kv_lens."""
+    head, batch, B = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
+    dev = k_pages.device
+    k, v = (torch.empty((B, batch[0], N, batch[1]), dtype=torch.bfloat16, device=dev)
+            for _ in range(2))
+    with torch.cuda.device(dev):
+        _check(fa_paged_read(k_pages, v_pages, k_scale, v_scale, *head, *batch, B, N, k, v,
+                             stream), "fa_paged_read")
+        _used_on(stream, k, v)
+    return k, v
+
+
+def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_q=None, scale=None,
+               causal=False, window_left=-1, k_scale=None, v_scale=None, out=None, stream=None):
+    """Attention of the new tokens q [T, H, d] over the cache (fa_paged_attn). The tokens of
+    sequence b are rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] (T / B each without
+    cu_seqlens_q); max_q bounds their number (T where it is not given: pass it for single
+    tokens, whose kernel is another). Returns (o [T, H, d] bf16, lse [T, H] fp32); rows that
+    belong to no sequence are not written. out = (o, lse) gives the buffers."""
+    head, batch, B = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
+    dev, Hkv, d = k_pages.device, batch[0], batch[1]
+    if q.dim() != 3:
+        raise ValueError("q must be [T, H, d]")
+    T, H = q.shape[0], q.shape[1]
+    qs = _new_rows("q", q, H, d, dev)
+    n = _offsets(cu_seqlens_q, B, T, max_q, dev)
+    if out is None:
+        o = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        o, lse = out
+        if (o.dtype != torch.bfloat16 or o.shape != (T, H, d) or not o.is_contiguous()
+                or lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()
+                or o.device != dev or lse.device != dev):
+            raise ValueError(f"out must be contiguous: bf16 [{T}, {H}, {d}] and fp32 [{T}, {H}]")
+    if T == 0:
+        return o, lse
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with torch.cuda.device(dev):
+        ws_bytes = fa_paged_workspace_size(H, Hkv, d, n)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        _check(fa_paged_attn(q, k_pages, v_pages, k_scale, v_scale, o, lse, *head, H, *batch,
+                             cu_seqlens_q, B, T, n, qs, scale, causal, window_left, ws, ws_bytes,
+                             stream), "fa_paged_attn")
+        _used_on(stream, *((o, lse, ws) if out is None else (ws,)))
     return o, lse

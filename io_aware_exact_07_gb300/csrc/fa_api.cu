@@ -14,6 +14,7 @@
 #include "fa_decode.h"
 #include "fa_fp8.h"
 #include "fa_kernels.h"
+#include "fa_paged.h"
 
 namespace {
 
@@ -645,6 +646,153 @@ fa_status fa_fwd_fp8(const void* q8, const void* k8, const void* vt8, const floa
                      int d, float scale, int causal, const int32_t* seqlens_k, void* stream) {
   return fa_fwd_fp8_gqa(q8, k8, vt8, s_q, s_k, s_v, o, lse, B, H, H, N, d, scale, causal,
                         seqlens_k, stream);
+}
+
+// Shared validation of the paged calls; fills `a` on success.
+static fa_status paged_args(const void* k, const void* v, const uint8_t* ks, const uint8_t* vs,
+                            int type, int num_pages, int page_size, int Hkv, int d, int64_t sp,
+                            int64_t sh, int64_t sr, const int32_t* table, int64_t table_stride,
+                            int max_pages, const int32_t* kv_lens, const int32_t* cu, int B, int T,
+                            int max_q, fa::PagedArgs* a) {
+  if (num_pages < 1 || page_size < 1 || Hkv < 1 || B < 1 || T < 0 || max_pages < 1 || max_q < 0)
+    return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (type != FA_CACHE_BF16 && type != FA_CACHE_E4M3) return FA_ERR_UNSUPPORTED;
+  if (page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+  const bool e4m3 = type == FA_CACHE_E4M3;
+  if (static_cast<long long>(max_pages) * page_size >= (1ll << 31) - 256) return FA_ERR_INVALID_ARG;
+  if (!k || !v || !table || !kv_lens || (e4m3 && (!ks || !vs))) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return FA_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(table), static_cast<const void*>(kv_lens),
+                        static_cast<const void*>(cu)})
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  const int64_t unit = e4m3 ? 16 : 8;              // elements in 16 bytes
+  const int64_t most = (1ll << 40) / (e4m3 ? 1 : 2);
+  for (const int64_t x : {sp, sh, sr})
+    if (x < unit || x % unit != 0 || x >= most) return FA_ERR_INVALID_ARG;
+  if (table_stride < max_pages) return FA_ERR_INVALID_ARG;
+  if (cu == nullptr && static_cast<long long>(B) * max_q != T) return FA_ERR_INVALID_ARG;
+  a->k = static_cast<uint8_t*>(const_cast<void*>(k));
+  a->v = static_cast<uint8_t*>(const_cast<void*>(v));
+  a->k_scale = const_cast<uint8_t*>(ks);
+  a->v_scale = const_cast<uint8_t*>(vs);
+  a->num_pages = num_pages;
+  a->page_size = page_size;
+  a->Hkv = Hkv;
+  a->d = d;
+  a->stride_page = sp;
+  a->stride_head = sh;
+  a->stride_row = sr;
+  a->table = table;
+  a->table_stride = table_stride;
+  a->max_pages = max_pages;
+  a->kv_lens = kv_lens;
+  a->cu = cu;
+  a->B = B;
+  a->T = T;
+  a->max_q = max_q;
+  a->status = nullptr;
+  return FA_OK;
+}
+
+fa_status fa_paged_write(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                         uint8_t* k_scale, uint8_t* v_scale, int type, int num_pages,
+                         int page_size, int H_kv, int d, int64_t stride_page, int64_t stride_head,
+                         int64_t stride_row, const int32_t* page_table, int64_t table_stride,
+                         int max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens_q, int B,
+                         int T, int max_q, int64_t k_stride, int64_t v_stride, void* stream) {
+  fa::PagedWriteArgs a;
+  fa_status st = paged_args(k_pages, v_pages, k_scale, v_scale, type, num_pages, page_size, H_kv,
+                            d, stride_page, stride_head, stride_row, page_table, table_stride,
+                            max_pages, kv_lens, cu_seqlens_q, B, T, max_q, &a.c);
+  if (st != FA_OK) return st;
+  const int64_t row = static_cast<int64_t>(H_kv) * d;
+  if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return FA_ERR_INVALID_ARG;
+  if (T == 0) return FA_OK;
+  if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return FA_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  if ((st = device_info(&di)) != FA_OK) return st;
+  a.c.status = di->status;
+  a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  cudaError_t e = fa::launch_paged_write(a, type == FA_CACHE_E4M3,
+                                         static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_paged_read(const void* k_pages, const void* v_pages, const uint8_t* k_scale,
+                        const uint8_t* v_scale, int type, int num_pages, int page_size, int H_kv,
+                        int d, int64_t stride_page, int64_t stride_head, int64_t stride_row,
+                        const int32_t* page_table, int64_t table_stride, int max_pages,
+                        const int32_t* kv_lens, int B, int N, void* k_out, void* v_out,
+                        void* stream) {
+  fa::PagedReadArgs a;
+  fa_status st = paged_args(k_pages, v_pages, k_scale, v_scale, type, num_pages, page_size, H_kv,
+                            d, stride_page, stride_head, stride_row, page_table, table_stride,
+                            max_pages, kv_lens, nullptr, B, 0, 0, &a.c);
+  if (st != FA_OK) return st;
+  if (N < 1 || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
+    return FA_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  if ((st = device_info(&di)) != FA_OK) return st;
+  a.c.status = di->status;
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.N = N;
+  cudaError_t e = fa::launch_paged_read(a, type == FA_CACHE_E4M3,
+                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_paged_workspace_size(int H, int H_kv, int d, int max_q) {
+  (void)H;
+  (void)H_kv;
+  (void)d;
+  (void)max_q;
+  return 0;
+}
+
+fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
+                        const uint8_t* k_scale, const uint8_t* v_scale, void* o, float* lse,
+                        int type, int num_pages, int page_size, int H, int H_kv, int d,
+                        int64_t stride_page, int64_t stride_head, int64_t stride_row,
+                        const int32_t* page_table, int64_t table_stride, int max_pages,
+                        const int32_t* kv_lens, const int32_t* cu_seqlens_q, int B, int T,
+                        int max_q, int64_t q_stride, float scale, int causal, int window_left,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  fa::PagedAttnArgs a;
+  fa_status st = paged_args(k_pages, v_pages, k_scale, v_scale, type, num_pages, page_size, H_kv,
+                            d, stride_page, stride_head, stride_row, page_table, table_stride,
+                            max_pages, kv_lens, cu_seqlens_q, B, T, max_q, &a.c);
+  if (st != FA_OK) return st;
+  if (H < 1 || H % H_kv != 0 || max_q < 1 || window_left < -1) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (q_stride < static_cast<int64_t>(H) * d || q_stride % 8 != 0) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(T) * H >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+  if (H / H_kv > 128) return FA_ERR_UNSUPPORTED;
+  if (T == 0) return FA_OK;
+  if (!q || !o || !lse || !aligned16(q) || !aligned16(o)) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  const size_t ws = fa_paged_workspace_size(H, H_kv, d, max_q);
+  if (ws > 0 && (workspace == nullptr || workspace_bytes < ws || !aligned16(workspace)))
+    return FA_ERR_WORKSPACE;
+  DeviceInfo* di = nullptr;
+  if ((st = device_info(&di)) != FA_OK) return st;
+  a.c.status = di->status;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
+  a.H = H;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.scale_log2 = scale * fa::kLog2e;
+  a.causal = causal ? 1 : 0;
+  a.wl = window_left;
+  cudaError_t e = fa::launch_paged_attn(a, type == FA_CACHE_E4M3,
+                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_dropout_p8(float dropout_p) { return p8_of(dropout_p); }

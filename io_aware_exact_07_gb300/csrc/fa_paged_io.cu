@@ -1,0 +1,197 @@
+// Writing new key and value rows into a paged cache, and reading a paged cache back
+// into contiguous rows (IO-aware in the sense of the method: a quantised cache halves
+// the bytes that attention over it, bound by reading K and V, has to move).
+//
+// A row is the d values of one K/V head at one position. Quantised rows are e4m3 codes
+// with one power-of-two scale per row: E is the smallest exponent in [kScaleMin,
+// kScaleMax] with max |x| <= 448 * 2^E (0 for a row of zeros), and the codes are
+// x * 2^-E rounded to the nearest, ties to even, saturating at 448. A power of two costs
+// e4m3 no precision (its significand does not depend on the scale), makes x * 2^-E and
+// code * 2^E exact, so that only the one rounding to e4m3 is lost, and lets the scale be
+// one byte. A row that holds a NaN or an infinity is marked by its scale byte and reads
+// back as NaN.
+//
+// Both kernels move each byte once and compute little: HBM bounds large calls, the
+// launch and three dependent loads (offsets, page table, rows) the smallest.
+#include <cuda_fp8.h>
+
+#include "fa_paged.h"
+
+namespace fa {
+
+namespace {
+
+constexpr int kIoWarps = 8;
+constexpr int kReadRows = 16;  // rows per warp; a page holds a multiple of it
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// Exponent of the scale of a row whose largest magnitude has the bf16 bits `top`
+// (finite): with top = 1.m * 2^x, 448 = 1.75 * 2^8 is reached from m = 96 / 128 on.
+__device__ __forceinline__ int scale_exponent(uint32_t top) {
+  if (top == 0u) return 0;
+  const int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0);
+  return e < kScaleMin ? kScaleMin : (e > kScaleMax ? kScaleMax : e);
+}
+
+__device__ __forceinline__ uint32_t codes2(uint32_t pair, float f) {
+  const float lo = __uint_as_float(pair << 16) * f;
+  const float hi = __uint_as_float(pair & 0xFFFF0000u) * f;
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+}  // namespace
+
+// One warp takes rows of one token: D / 8 lanes hold a row (16 bytes each), so a pass
+// covers 2 (d = 128) or 4 (d = 64) of the token's 2 Hkv rows (K's heads, then V's).
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kIoWarps * 32) fa_paged_write_kernel(const PagedWriteArgs a,
+                                                                       int warps_per_token) {
+  constexpr int kLanes = D / 8;
+  constexpr int kRows = 32 / kLanes;
+  const int lane = threadIdx.x & 31;
+  const long long task = static_cast<long long>(blockIdx.x) * kIoWarps + (threadIdx.x >> 5);
+  const int t = static_cast<int>(task / warps_per_token);
+  const int sub = static_cast<int>(task - static_cast<long long>(t) * warps_per_token);
+  if (t >= a.c.T) return;
+  const int b = paged_find_seq(a.c, t);
+  if (b >= a.c.B) return;  // a token behind the last sequence
+  const PagedSeq s = paged_seq(a.c, b);
+  const int pos = s.len - s.nq + (t - s.t0);
+  if (t < s.t0 || t >= s.t0 + s.nq || pos < 0) return;
+  const int page = paged_page(a.c, b, pos);
+  if (page < 0) return;
+  const int slot = pos % a.c.page_size;
+  const int u = lane % kLanes;  // 16-byte unit of the row
+  for (int r0 = sub * kRows; r0 < 2 * a.c.Hkv; r0 += warps_per_token * kRows) {
+    const int r = r0 + lane / kLanes;
+    const bool real = r < 2 * a.c.Hkv;
+    const bool is_v = r >= a.c.Hkv;
+    const int h = is_v ? r - a.c.Hkv : r;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (real)
+      x = *reinterpret_cast<const uint4*>((is_v ? a.v_new + t * a.v_stride : a.k_new + t * a.k_stride) +
+                                          h * D + u * 8);
+    const long long at = page * a.c.stride_page + h * a.c.stride_head + slot * a.c.stride_row + u * 8;
+    uint8_t* base = is_v ? a.c.v : a.c.k;
+    if constexpr (!E4M3) {
+      if (real) *reinterpret_cast<uint4*>(base + at * 2) = x;
+    } else {
+      constexpr uint32_t kAbs = 0x7FFF7FFFu;
+      const uint32_t m2 = max2(max2(x.x & kAbs, x.y & kAbs), max2(x.z & kAbs, x.w & kAbs));
+      uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool finite = top < 0x7F80u;
+      const int e = finite ? scale_exponent(top) : 0;
+      const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-E
+      uint2 w;
+      w.x = codes2(x.x, f) | codes2(x.y, f) << 16;
+      w.y = codes2(x.z, f) | codes2(x.w, f) << 16;
+      if (!finite) w = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+      if (real) {
+        *reinterpret_cast<uint2*>(base + at) = w;
+        if (u == 0)
+          (is_v ? a.c.v_scale : a.c.k_scale)[(static_cast<long long>(page) * a.c.Hkv + h) *
+                                                 a.c.page_size + slot] =
+              static_cast<uint8_t>(finite ? e + 127 : kScaleNaN);
+      }
+    }
+  }
+}
+
+// One warp copies kReadRows positions of one K/V head, which lie in one page.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kIoWarps * 32) fa_paged_read_kernel(const PagedReadArgs a,
+                                                                      int groups) {
+  const int lane = threadIdx.x & 31;
+  long long task = static_cast<long long>(blockIdx.x) * kIoWarps + (threadIdx.x >> 5);
+  const int g = static_cast<int>(task % groups);
+  task /= groups;
+  const int h = static_cast<int>(task % a.c.Hkv);
+  task /= a.c.Hkv;
+  const int b = static_cast<int>(task >> 1);
+  if (b >= a.c.B) return;
+  const bool is_v = (task & 1) != 0;
+  const int j0 = g * kReadRows;
+  const int len = paged_seq(a.c, b).len;
+  const int page = j0 < len ? paged_page(a.c, b, j0) : -1;
+  const int slot = j0 % a.c.page_size;
+  // rows of this group that the cache holds; the others are written as zeros
+  const int have = page < 0 ? 0 : min(kReadRows, len - j0);
+  const int rows = min(kReadRows, a.N - j0);
+  const long long src = page * a.c.stride_page + h * a.c.stride_head + slot * a.c.stride_row;
+  __nv_bfloat16* dst = (is_v ? a.v_out : a.k_out) +
+                       ((static_cast<long long>(b) * a.c.Hkv + h) * a.N + j0) * D;
+  const uint8_t* base = is_v ? a.c.v : a.c.k;
+  if constexpr (!E4M3) {
+    constexpr int kUnits = D / 8;                    // 16-byte units of a row
+    constexpr int kPasses = kReadRows * kUnits / 32;
+    uint4 x[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = (i * 32 + lane) / kUnits, u = lane % kUnits;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < have)
+        x[i] = *reinterpret_cast<const uint4*>(base + (src + r * a.c.stride_row + u * 8) * 2);
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = (i * 32 + lane) / kUnits, u = lane % kUnits;
+      if (r < rows) *reinterpret_cast<uint4*>(dst + r * D + u * 8) = x[i];
+    }
+  } else {
+    constexpr int kUnits = D / 8;                    // 8-byte units of a row of codes
+    constexpr int kPasses = kReadRows * kUnits / 32;
+    const uint8_t* scales = (is_v ? a.c.v_scale : a.c.k_scale) +
+                            (static_cast<long long>(page) * a.c.Hkv + h) * a.c.page_size + slot;
+    uint2 x[kPasses];
+    int sc[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = (i * 32 + lane) / kUnits, u = lane % kUnits;
+      x[i] = make_uint2(0u, 0u);
+      sc[i] = 127;
+      if (r < have) {
+        x[i] = *reinterpret_cast<const uint2*>(base + src + r * a.c.stride_row + u * 8);
+        sc[i] = scales[r];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = (i * 32 + lane) / kUnits, u = lane % kUnits;
+      const uint32_t f = e4m3_factor(sc[i]);
+      if (r < rows)
+        *reinterpret_cast<uint4*>(dst + r * D + u * 8) = make_uint4(
+            e4m3_lo(x[i].x, f), e4m3_hi(x[i].x, f), e4m3_lo(x[i].y, f), e4m3_hi(x[i].y, f));
+    }
+  }
+}
+
+cudaError_t launch_paged_write(const PagedWriteArgs& a, bool e4m3, cudaStream_t stream) {
+  const int rows = a.c.d == 64 ? 4 : 2;
+  const int warps_per_token = (2 * a.c.Hkv + rows - 1) / rows;
+  const long long tasks = static_cast<long long>(a.c.T) * warps_per_token;
+  const long long blocks = (tasks + kIoWarps - 1) / kIoWarps;
+  if (blocks <= 0) return cudaSuccess;
+  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  auto kern = a.c.d == 64 ? (e4m3 ? fa_paged_write_kernel<64, true> : fa_paged_write_kernel<64, false>)
+                          : (e4m3 ? fa_paged_write_kernel<128, true>
+                                  : fa_paged_write_kernel<128, false>);
+  kern<<<static_cast<unsigned>(blocks), kIoWarps * 32, 0, stream>>>(a, warps_per_token);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_read(const PagedReadArgs& a, bool e4m3, cudaStream_t stream) {
+  const int groups = (a.N + kReadRows - 1) / kReadRows;
+  const long long tasks = 2ll * a.c.B * a.c.Hkv * groups;
+  const long long blocks = (tasks + kIoWarps - 1) / kIoWarps;
+  if (blocks <= 0) return cudaSuccess;
+  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  auto kern = a.c.d == 64 ? (e4m3 ? fa_paged_read_kernel<64, true> : fa_paged_read_kernel<64, false>)
+                          : (e4m3 ? fa_paged_read_kernel<128, true> : fa_paged_read_kernel<128, false>);
+  kern<<<static_cast<unsigned>(blocks), kIoWarps * 32, 0, stream>>>(a, groups);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -382,3 +382,77 @@ def fwd_fp8(q8, k8, v8, s_q, s_k, s_v, scale, causal=False, seqlens_k=None):
     kh = e4m3_decode(k8) * np.asarray(s_k, dtype=np.float64)[:, :, None, None]
     vh = e4m3_decode(v8) * np.asarray(s_v, dtype=np.float64)[:, :, None, :]
     return fwd_gqa(qh, kh, vh, scale, causal=causal, seqlens_k=seqlens_k)
+
+
+# ------------------------------------------------------------------ paged caches
+
+SCALE_MIN, SCALE_MAX, SCALE_NAN = -117, 7, 255
+
+
+def quantize_rows(x):
+    """e4m3 codes and scale bytes (uint8) of rows [..., d]: the scale of a row is 2^E, E the
+    smallest integer in [-117, 7] with max |x| <= 448 * 2^E (0 for a row of zeros), byte
+    E + 127; codes = nearest e4m3 of x / 2^E, ties to even, saturating. A row with a NaN or
+    an infinity: byte 255, codes 0x7F."""
+    x = np.asarray(x, dtype=np.float64)
+    bad = ~np.isfinite(x).all(axis=-1)
+    x = np.where(bad[..., None], 0.0, x)
+    top = np.abs(x).max(axis=-1)
+    e = np.full(top.shape, SCALE_MAX)
+    for n in range(SCALE_MAX, SCALE_MIN - 1, -1):  # the smallest that still holds the row
+        e = np.where(top <= np.ldexp(E4M3_MAX, n), n, e)
+    e = np.where(top == 0, 0, e)
+    codes = e4m3_encode(np.ldexp(x, -e[..., None]))
+    codes = np.where(np.signbit(x), codes | 0x80, codes)  # -0 keeps its sign
+    codes = np.where(bad[..., None], 0x7F, codes).astype(np.uint8)
+    return codes, np.where(bad, SCALE_NAN, e + 127).astype(np.uint8)
+
+
+def dequantize_rows(codes, scale):
+    """Values code * 2^(byte - 127) of rows [..., d]; NaN for rows of scale byte 255."""
+    s = np.asarray(scale).astype(np.int64)[..., None]
+    return np.where(s == SCALE_NAN, np.nan, np.ldexp(e4m3_decode(codes), s - 127))
+
+
+def paged_positions(table, page_size, b, positions):
+    """(page, row in the page) of each position of sequence b."""
+    positions = np.asarray(positions)
+    return np.asarray(table)[b, positions // page_size], positions % page_size
+
+
+def fwd_paged(q, k, v, cu, kv_lens, scale, causal=False, window_left=-1):
+    """Attention of packed new tokens q [T, H, d] over sequences given as lists of
+    contiguous rows, k[b], v[b] [L_b, H_kv, d], in fp64 from the definition: token i of the
+    n = cu[b+1] - cu[b] of sequence b sits at position p = L_b - n + i and sees keys j < L_b,
+    with causal j <= p, with window_left >= 0 j >= p - window_left. Returns (o [T, H, d], lse
+    [T, H], o_abs [T, H, d] = sum_j P_ij |v_j|); rows without keys, and those of no sequence,
+    have O = 0, lse = -inf."""
+    q = _f64(q)
+    T, H, d = q.shape
+    o, o_abs = np.zeros((T, H, d)), np.zeros((T, H, d))
+    lse = np.full((T, H), -np.inf)
+    for b in range(len(kv_lens)):
+        t0, t1, L = int(cu[b]), int(cu[b + 1]), int(kv_lens[b])
+        if t1 == t0 or L == 0:
+            continue
+        kb, vb = _f64(k[b]), _f64(v[b])
+        pos = L - (t1 - t0) + np.arange(t1 - t0)[:, None]
+        j = np.arange(L)[None]
+        seen = np.ones((t1 - t0, L), dtype=bool)
+        if causal:
+            seen &= j <= pos
+        if window_left >= 0:
+            seen &= j >= pos - window_left
+        G = _group(H, kb.shape[1])
+        for h in range(H):
+            z = np.where(seen, scale * (q[t0:t1, h] @ kb[:L, h // G].T), -np.inf)
+            m = z.max(axis=1, keepdims=True)
+            e = np.exp(z - np.where(np.isneginf(m), 0.0, m))
+            den = e.sum(axis=1)
+            some = den > 0
+            p = e / np.where(some, den, 1.0)[:, None]
+            o[t0:t1, h] = p @ vb[:L, h // G]
+            o_abs[t0:t1, h] = p @ np.abs(vb[:L, h // G])
+            with np.errstate(divide="ignore"):
+                lse[t0:t1, h] = np.where(some, m[:, 0] + np.log(den), -np.inf)
+    return o, lse, o_abs
