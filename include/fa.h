@@ -238,7 +238,7 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
  *     16 bytes, below 2^40 bytes.
  *   type: FA_CACHE_BF16 (bf16 values) or FA_CACHE_E4M3 (one e4m3 code per value and
  *     one scale byte per row, k_scale and v_scale: uint8 [num_pages, H_kv,
- *     page_size], contiguous; NULL for bf16). A quantised value is code * 2^E with
+ *     page_size], contiguous, 16-byte aligned; not used for bf16). A quantised value is code * 2^E with
  *     scale byte E + 127, E the smallest exponent in [-117, 7] that keeps the row's
  *     largest magnitude within 448 * 2^E (0 for a row of zeros); codes are rounded
  *     to nearest even and saturate (magnitudes above 57344 = 448 * 2^7). A row that

@@ -663,6 +663,7 @@ static fa_status paged_args(const void* k, const void* v, const uint8_t* ks, con
   if (static_cast<long long>(max_pages) * page_size >= (1ll << 31) - 256) return FA_ERR_INVALID_ARG;
   if (!k || !v || !table || !kv_lens || (e4m3 && (!ks || !vs))) return FA_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v)) return FA_ERR_INVALID_ARG;
+  if (e4m3 && (!aligned16(ks) || !aligned16(vs))) return FA_ERR_INVALID_ARG;
   for (const void* p : {static_cast<const void*>(table), static_cast<const void*>(kv_lens),
                         static_cast<const void*>(cu)})
     if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return FA_ERR_INVALID_ARG;
@@ -747,12 +748,29 @@ fa_status fa_paged_read(const void* k_pages, const void* v_pages, const uint8_t*
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// Workspace of fa_paged_attn: one header per CTA, then the pieces' lse and outputs.
+struct PagedWorkspace {
+  int ctas, rows;
+  size_t lse_off, o_off, bytes;
+};
+static PagedWorkspace paged_workspace(int G, int d, int max_q, int num_sms) {
+  PagedWorkspace w;
+  const long long rows = static_cast<long long>(G) * max_q;
+  w.ctas = num_sms;
+  w.rows = rows <= 8 ? 8 : fa::kStepRows;
+  const size_t slots = 2 * static_cast<size_t>(w.ctas) * w.rows;
+  w.lse_off = round256(static_cast<size_t>(w.ctas) * 16);
+  w.o_off = w.lse_off + round256(slots * sizeof(float));
+  w.bytes = rows > fa::kStepRows ? 0 : w.o_off + round256(slots * d * sizeof(float));
+  return w;
+}
+
 size_t fa_paged_workspace_size(int H, int H_kv, int d, int max_q) {
-  (void)H;
-  (void)H_kv;
-  (void)d;
-  (void)max_q;
-  return 0;
+  DeviceInfo* di = nullptr;
+  if (H < 1 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128) || max_q < 1 ||
+      device_info(&di) != FA_OK)
+    return 0;
+  return paged_workspace(H / H_kv, d, max_q, di->num_sms).bytes;
 }
 
 fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
@@ -776,11 +794,15 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   if (T == 0) return FA_OK;
   if (!q || !o || !lse || !aligned16(q) || !aligned16(o)) return FA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_INVALID_ARG;
-  const size_t ws = fa_paged_workspace_size(H, H_kv, d, max_q);
-  if (ws > 0 && (workspace == nullptr || workspace_bytes < ws || !aligned16(workspace)))
-    return FA_ERR_WORKSPACE;
   DeviceInfo* di = nullptr;
   if ((st = device_info(&di)) != FA_OK) return st;
+  const PagedWorkspace w = paged_workspace(H / H_kv, d, max_q, di->num_sms);
+  if (w.bytes > 0 && (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace)))
+    return FA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.headers = ws;
+  a.lse_part = reinterpret_cast<float*>(ws + w.lse_off);
+  a.o_part = reinterpret_cast<float*>(ws + w.o_off);
   a.c.status = di->status;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
@@ -790,8 +812,10 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   a.scale_log2 = scale * fa::kLog2e;
   a.causal = causal ? 1 : 0;
   a.wl = window_left;
-  cudaError_t e = fa::launch_paged_attn(a, type == FA_CACHE_E4M3,
-                                        static_cast<cudaStream_t>(stream));
+  const bool e4m3 = type == FA_CACHE_E4M3;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = w.bytes > 0 ? fa::launch_paged_step(a, e4m3, w.ctas, cs)
+                              : fa::launch_paged_attn(a, e4m3, cs);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

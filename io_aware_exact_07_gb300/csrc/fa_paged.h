@@ -148,10 +148,17 @@ struct PagedAttnArgs {
   float scale_log2;             // scale * log2(e)
   int causal;
   int wl;                       // sliding window (-1: none)
+  // Workspace of calls whose work is cut between CTAs: a header per CTA and two pieces,
+  // each of `rows` query rows: o_part [ctas, 2, rows, d], lse_part [ctas, 2, rows] (log2).
+  void* headers;                // [ctas] int4
+  float* o_part;
+  float* lse_part;
 };
+constexpr int kStepRows = 16;   // most query rows per K/V head of the step kernel
 
 cudaError_t launch_paged_write(const PagedWriteArgs& a, bool e4m3, cudaStream_t stream);
 cudaError_t launch_paged_read(const PagedReadArgs& a, bool e4m3, cudaStream_t stream);
+cudaError_t launch_paged_step(const PagedAttnArgs& a, bool e4m3, int ctas, cudaStream_t stream);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool e4m3, cudaStream_t stream);
 
 }  // namespace fa

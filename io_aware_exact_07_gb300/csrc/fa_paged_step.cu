@@ -1,0 +1,713 @@
+// Attention of few new tokens per sequence over a paged cache (a decode step: one new
+// token, or a handful of drafted ones): at most 16 query rows per K/V head, G = H / Hkv
+// heads times nq tokens. The page "FlashAttention — L3 Cross-Paper Synthesis" (section 3)
+// names this case, bound by reading K and V, as left unoptimised. HBM is the bound, so the
+// kernel is a stream of K and V through shared memory, each byte read once per K/V head:
+//
+//  - Every warp is on its own: it takes 16 keys of each 128-key block, brings their K and V
+//    rows into its own ring of stages with cp.async, and keeps its own softmax state, so
+//    that the main loop has no block barrier and loads run ahead across heads and sequences.
+//    16 keys lie in one page (its size is a multiple of 16), so one table entry serves them.
+//  - S^T = K Q^T and O^T += V^T P^T with m16n8k16 products: the keys (then the columns of V)
+//    are the 16 rows, the query rows the 8 columns. With at most 8 (or 16) query rows the
+//    products are far below what bounds the kernel (128-row tensor-memory tiles would hold
+//    at least 112 empty rows); keeping S and P in registers saves the handshakes that a
+//    short sequence cannot hide.
+//  - The order of the columns d within a product is free as long as both operands share
+//    it: a thread takes the 16 bytes of a row that it can load at once. e4m3 rows are
+//    turned into bf16 (exactly) between shared memory and the product, in registers.
+//  - The (sequence, K/V head, 128-key block) list is cut into equal runs, one per CTA, by
+//    the lengths found on the device. A head that falls into one run is written directly;
+//    one cut by a run's end leaves normalised pieces, merged by a second, small kernel with
+//    the two-block rule of the online softmax.
+#include "fa_paged.h"
+
+namespace fa {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kChunk = 16;                  // keys of a warp's step
+constexpr int kBlock = kWarps * kChunk;     // keys of a block
+constexpr float kRescale = 8.0f;            // log2 units: rescale O when m grows by > 2^8
+constexpr int kSmemMax = 232448;
+
+template <int D, bool E4M3, int NT>
+struct StepL {
+  static constexpr int kRows = 8 * NT;                    // query rows
+  static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
+  static constexpr int kUnits = kRowBytes / 16;           // 16-byte units of a row
+  static constexpr int kTileBytes = kChunk * kRowBytes;   // 16 K rows, or V rows
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kScaleBytes = E4M3 ? 32 : 0;       // K's and V's 16 scale bytes
+  static constexpr int kPitch = D + 4;                    // merge buffer row, in floats
+  static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
+  static constexpr int kMlBytes = kWarps * kRows * 8;
+  static constexpr int kFixed = kMergeBytes + kMlBytes + 256;
+  static constexpr int kFit = (kSmemMax - kFixed) / (kWarps * (kStageBytes + kScaleBytes));
+  static constexpr int kStages = kFit < 6 ? kFit : 6;
+  static_assert(kStages >= 2, "the ring needs two stages");
+  static constexpr int kRingOff = 0;
+  static constexpr int kScaleOff = kWarps * kStages * kStageBytes;
+  static constexpr int kMergeOff = kScaleOff + kWarps * kStages * kScaleBytes;
+  static constexpr int kMlOff = kMergeOff + kMergeBytes;
+  static constexpr int kPlanOff = kMlOff + kMlBytes;
+  static constexpr int kSmemBytes = kPlanOff + 256;
+  static_assert(kSmemBytes <= kSmemMax, "more shared memory than one CTA may hold");
+};
+
+// Where unit `u` (16 bytes) of row `row` lies in a tile. The exclusive-or spreads the rows
+// that one load instruction touches over all banks: K rows come in pairs (2 p, 2 p + 1),
+// 4 units each; V as eight rows with one unit each (bf16), or as four rows (2 c) with two
+// units each (e4m3). At e4m3 and d = 64, where a row has 4 units, V's even rows come first.
+template <int D, bool E4M3>
+__device__ __forceinline__ int k_unit(int row, int u) {
+  if constexpr (!E4M3) return row * (D / 8) + (u ^ (((row & 1) << 2) | ((row >> 1) & 3)));
+  if constexpr (D == 128) return row * 8 + (u ^ ((row & 1) << 2));
+  return row * 4 + u;
+}
+template <int D, bool E4M3>
+__device__ __forceinline__ int v_unit(int row, int u) {
+  if constexpr (!E4M3) return row * (D / 8) + (u ^ (((row & 1) << 2) | ((row >> 1) & 3)));
+  if constexpr (D == 128) return row * 8 + (u ^ (((row >> 1) & 3) << 1));
+  const int slot = (row >> 1) | ((row & 1) << 3);
+  return slot * 4 + (u ^ (((slot >> 1) & 1) << 1));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t saddr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(saddr) : "memory");
+  return r;
+}
+__device__ __forceinline__ int ld_shared_u8(uint32_t saddr) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(saddr) : "memory");
+  return static_cast<int>(r);
+}
+
+// Key blocks [first, first + n) of a sequence that hold a key some new token sees: with a
+// sliding window the first token sees the lowest. A sequence with new tokens has at least
+// one block (its rows have to be written), one without has none.
+struct Span {
+  int first, n;
+};
+__device__ __forceinline__ Span span_of(const PagedAttnArgs& a, const PagedSeq& s) {
+  Span r;
+  const int lo = a.wl >= 0 ? s.len - s.nq - a.wl : 0;
+  r.first = lo > 0 ? lo / kBlock : 0;
+  r.n = (s.len + kBlock - 1) / kBlock - r.first;
+  if (r.n < 1) r.n = 1;
+  if (s.nq <= 0) r.n = 0;
+  return r;
+}
+
+// A place in the list of (sequence, K/V head, key block).
+struct Walk {
+  int b, h;          // sequence (B past the end), K/V head
+  int blk, end;      // key block, end of the sequence's blocks
+  int first;
+  PagedSeq s;
+  __device__ __forceinline__ void load(const PagedAttnArgs& a) {
+    s = paged_attn_seq(a.c, b);
+    const Span sp = span_of(a, s);
+    first = sp.first;
+    end = first + sp.n;
+  }
+  // Next place; past the last sequence an empty one that is never left.
+  __device__ __forceinline__ void next(const PagedAttnArgs& a) {
+    if (b >= a.c.B || ++blk < end) return;
+    if (++h == a.c.Hkv) {
+      h = 0;
+      do {
+        ++b;
+        if (b >= a.c.B) {
+          s.nq = s.len = first = blk = 0;
+          end = 0x7FFFFFFF;
+          return;
+        }
+        load(a);
+      } while (first == end);
+    }
+    blk = first;
+  }
+};
+
+// Sum over the block's threads, and the exclusive prefix of each.
+__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();  // earlier readers of warp_sums are done
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const long long y = warp_sums[w];
+    if (w < warp) before += y;
+    all += y;
+  }
+  *total = all;
+  return before + inc - x;
+}
+
+}  // namespace
+
+template <int D, bool E4M3, int NT>
+__global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedAttnArgs a) {
+  using L = StepL<D, E4M3, NT>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g8 = lane >> 2, c4 = lane & 3;
+  const int G = a.H / a.c.Hkv;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- this CTA's run [lo, hi) of the list
+  struct Plan {
+    long long warp_sums[kWarps];
+    int b;
+    int rem_h, rem_blk;
+  };
+  Plan* plan = reinterpret_cast<Plan*>(smem + L::kPlanOff);
+  static_assert(sizeof(Plan) <= 256, "plan area");
+  auto weight = [&](int b) -> long long {
+    if (b >= a.c.B) return 0;
+    return static_cast<long long>(span_of(a, paged_attn_seq(a.c, b)).n) * a.c.Hkv;
+  };
+  long long total = 0, x0 = 0;
+  for (int b0 = 0; b0 < a.c.B; b0 += kThreads) {
+    const long long x = weight(b0 + tid);
+    if (b0 == 0) x0 = x;
+    long long sum;
+    block_scan(x, plan->warp_sums, &sum);
+    total += sum;
+  }
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long lo = per * blockIdx.x;
+  const long long hi = lo + per < total ? lo + per : total;
+  int4* headers = reinterpret_cast<int4*>(a.headers);
+  if (lo >= hi) {
+    if (tid == 0) headers[blockIdx.x] = make_int4(-1, 0, 1, 0);
+    return;
+  }
+  {
+    long long base = 0;
+    for (int b0 = 0; b0 < a.c.B && base <= lo; b0 += kThreads) {
+      const long long x = b0 == 0 ? x0 : weight(b0 + tid);
+      long long sum;
+      const long long at = base + block_scan(x, plan->warp_sums, &sum);
+      if (at <= lo && lo < at + x) {
+        const long long n = x / a.c.Hkv;
+        plan->b = b0 + tid;
+        plan->rem_h = static_cast<int>((lo - at) / n);
+        plan->rem_blk = static_cast<int>((lo - at) % n);
+      }
+      base += sum;
+    }
+  }
+  __syncthreads();
+  Walk cw;  // the block being computed
+  cw.b = plan->b;
+  cw.h = plan->rem_h;
+  cw.load(a);
+  const bool starts_mid = plan->rem_blk != 0;
+  cw.blk = cw.first + plan->rem_blk;
+
+  // ---- loads
+  const uint32_t ring = smem_u32(smem + L::kRingOff) + warp * L::kStages * L::kStageBytes;
+  const uint32_t scale_ring = smem_u32(smem + L::kScaleOff) + warp * L::kStages * L::kScaleBytes;
+  constexpr int kRowsPer = 32 / L::kUnits;        // rows that the lanes cover at once
+  constexpr int kLoads = kChunk / kRowsPer;
+  const int lrow = lane / L::kUnits, lunit = lane % L::kUnits;
+  constexpr int kEs = E4M3 ? 1 : 2;
+  const long long row_bytes = a.c.stride_row * kEs;
+  Walk lw = cw;  // the block to load next
+  auto chunk_of = [&](const Walk& w) { return w.blk * kBlock + warp * kChunk; };
+  auto page_of = [&](const Walk& w) {
+    const int j = chunk_of(w);
+    return j < w.s.len ? paged_page(a.c, w.b, j) : -1;
+  };
+  int lpage = page_of(lw);
+  auto issue = [&](int stage) {
+    const int j = chunk_of(lw);
+    const int have = lpage >= 0 ? lw.s.len - j : 0;  // rows of the chunk that the cache holds
+    const int slot = j % a.c.page_size;
+    const int page = lpage >= 0 ? lpage : 0;
+    const long long at = (page * a.c.stride_page + lw.h * a.c.stride_head +
+                          (slot + lrow) * a.c.stride_row) * kEs + lunit * 16;
+    const uint32_t dk = ring + stage * L::kStageBytes, dv = dk + L::kTileBytes;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = lrow + i * kRowsPer;
+      const bool real = r < have;
+      const long long off = real ? at + i * kRowsPer * row_bytes : 0;
+      cp_async16(dk + k_unit<D, E4M3>(r, lunit) * 16, a.c.k + off, real);
+      cp_async16(dv + v_unit<D, E4M3>(r, lunit) * 16, a.c.v + off, real);
+    }
+    if constexpr (E4M3) {
+      if (lane < 2) {  // the 16 rows' scale bytes lie next to each other
+        const long long so =
+            (static_cast<long long>(page) * a.c.Hkv + lw.h) * a.c.page_size + slot;
+        cp_async16(scale_ring + stage * L::kScaleBytes + lane * 16,
+                   (lane ? a.c.v_scale : a.c.k_scale) + so, have > 0);
+      }
+    }
+    lw.next(a);
+    lpage = page_of(lw);
+  };
+  // ---- query rows of a K/V head: row r = t * G + g; the rows' columns in the order of the
+  // products, two registers per 16 columns
+  auto load_q = [&](const Walk& w, uint32_t(&q)[NT][D / 8]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = n * 8 + g8;
+      const bool real = r < w.s.nq * G;
+      const int t = r / G;
+      const __nv_bfloat16* p = a.q + (w.s.t0 + t) * a.q_stride + (w.h * G + (r - t * G)) * D;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        // bf16: columns 32 i + 8 c4 ..; e4m3: 64 (i / 2) + 16 c4 + 8 (i % 2) ..
+        const int col = E4M3 ? (i >> 1) * 64 + c4 * 16 + (i & 1) * 8 : i * 32 + c4 * 8;
+        const uint4 x = real ? *reinterpret_cast<const uint4*>(p + col) : make_uint4(0u, 0u, 0u, 0u);
+        q[n][4 * i] = x.x;
+        q[n][4 * i + 1] = x.y;
+        q[n][4 * i + 2] = x.z;
+        q[n][4 * i + 3] = x.w;
+      }
+    }
+  };
+  uint32_t q[NT][D / 8];
+  load_q(cw, q);
+
+  const long long steps = hi - lo;
+#pragma unroll
+  for (int s = 0; s < L::kStages - 1; ++s) {
+    if (s < steps) issue(s);
+    cp_async_commit();
+  }
+
+  float o[NT][D / 16][4];
+  float m_ref[NT][2], l_sum[NT][2];  // rows 2 c4, 2 c4 + 1 of each group of eight
+  auto clear = [&]() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m_ref[n][e] = -INFINITY;
+        l_sum[n][e] = 0.f;
+      }
+    }
+  };
+  clear();
+  bool first_piece = true, ended0 = false;
+  int slot1_b = -1, slot1_h = 0;
+  float* merge = reinterpret_cast<float*>(smem + L::kMergeOff);
+  float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
+  int stage = 0;
+  int piece_blk = cw.blk;  // first block of the piece
+  for (long long i = 0; i < steps; ++i) {
+    cp_async_wait<L::kStages - 2>();
+    __syncwarp();  // the stage has landed for every lane; the last one has been read by all
+    if (i + L::kStages - 1 < steps) issue(stage == 0 ? L::kStages - 1 : stage - 1);
+    cp_async_commit();
+    Walk nw = cw;
+    nw.next(a);
+    const bool ends = nw.b != cw.b || nw.h != cw.h;  // the unit's last block
+    uint32_t qn[NT][D / 8];
+    if (ends && i + 1 < steps) load_q(nw, qn);
+
+    const int j0 = chunk_of(cw);
+    const int pos0 = cw.s.len - cw.s.nq;  // position of the first new token
+    const int key_min = a.wl >= 0 ? pos0 - a.wl : 0;
+    if (j0 < cw.s.len && j0 + kChunk > key_min) {
+      const uint32_t sk = ring + stage * L::kStageBytes, sv = sk + L::kTileBytes;
+      // factor of key k of the chunk (e4m3); behind the sequence, where the codes are filled
+      // with zeros and the scale byte may be anything, 0
+      auto factor = [&](uint32_t scales, int k) {
+        return j0 + k < cw.s.len ? e4m3_factor(ld_shared_u8(scales + k)) : 0u;
+      };
+      // ---- S^T = K Q^T: keys g8 and g8 + 8, query rows 2 c4 and 2 c4 + 1
+      float s[NT][4], s2[NT][4];  // two chains of products
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
+      if constexpr (!E4M3) {
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          const uint4 k0 = ld_shared_v4(sk + k_unit<D, E4M3>(g8, 4 * x + c4) * 16);
+          const uint4 k1 = ld_shared_v4(sk + k_unit<D, E4M3>(g8 + 8, 4 * x + c4) * 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816(s[n], k0.x, k1.x, k0.y, k1.y, q[n][4 * x], q[n][4 * x + 1]);
+            mma16816(s2[n], k0.z, k1.z, k0.w, k1.w, q[n][4 * x + 2], q[n][4 * x + 3]);
+          }
+        }
+      } else {
+        const uint32_t ss = scale_ring + stage * L::kScaleBytes;
+        const uint32_t f0 = factor(ss, g8), f1 = factor(ss, g8 + 8);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          const uint4 k0 = ld_shared_v4(sk + k_unit<D, E4M3>(g8, 4 * x + c4) * 16);
+          const uint4 k1 = ld_shared_v4(sk + k_unit<D, E4M3>(g8 + 8, 4 * x + c4) * 16);
+          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t a0 = e4m3_lo(w0[w], f0), a2 = e4m3_hi(w0[w], f0);
+            const uint32_t a1 = e4m3_lo(w1[w], f1), a3 = e4m3_hi(w1[w], f1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(w & 1 ? s2[n] : s[n], a0, a1, a2, a3, q[n][8 * x + 2 * w],
+                       q[n][8 * x + 2 * w + 1]);
+          }
+        }
+      }
+      // ---- masks, running maximum, P
+      bool grow = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + s2[n][e]) * a.scale_log2;
+      }
+      const int last_lo = a.wl >= 0 ? cw.s.len - 1 - a.wl : 0;  // first key of the last token
+      const int first_hi = a.causal ? pos0 + 1 : cw.s.len;      // end of the first token's keys
+      if (j0 < last_lo || j0 + kChunk > first_hi) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = j0 + g8 + (e >> 1) * 8;
+            const int pos = pos0 + (n * 8 + 2 * c4 + (e & 1)) / G;
+            if (key >= cw.s.len || (a.causal && key > pos) || (a.wl >= 0 && key < pos - a.wl))
+              s[n][e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          grow |= fmaxf(s[n][e], s[n][e + 2]) > m_ref[n][e] + kRescale;
+      // The reference maximum moves only when a score exceeds it by more than 2^8 (so P
+      // stays below 2^8): most steps need one vote instead of the row maxima.
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(s[n][e], s[n][e + 2]);
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+            const float m_new = fmaxf(m_ref[n][e], mx);
+            const float alpha = m_new == -INFINITY ? 1.f : ex2_approx(m_ref[n][e] - m_new);
+            m_ref[n][e] = m_new;
+            l_sum[n][e] *= alpha;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              o[n][x][e] *= alpha;
+              o[n][x][e + 2] *= alpha;
+            }
+          }
+      }
+      uint32_t p0[NT], p1[NT];  // P^T as the second operand: keys 2 c4 (+ 8) .., query row g8
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float m = m_ref[n][e & 1];
+          p[e] = ex2_approx(s[n][e] - (m == -INFINITY ? 0.f : m));
+        }
+        l_sum[n][0] += p[0] + p[2];
+        l_sum[n][1] += p[1] + p[3];
+        // P is rounded to bf16 for the product (at most 2^-8 of each weight); the sum keeps fp32
+        p0[n] = movmatrix_t(pack_bf16x2(p[0], p[1]));
+        p1[n] = movmatrix_t(pack_bf16x2(p[2], p[3]));
+      }
+      // ---- O^T += V^T P^T
+      if constexpr (!E4M3) {
+        const int key = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          uint32_t v[4];
+          ldmatrix4_t(sv + v_unit<D, E4M3>(key, 2 * x + ((lane >> 3) & 1)) * 16, v);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(o[n][x], v[0], v[1], v[2], v[3], p0[n], p1[n]);
+        }
+      } else {
+        const uint32_t ss = scale_ring + stage * L::kScaleBytes + 16;
+        uint32_t f[2];  // factors of keys 2 c4, 2 c4 + 1 and of 2 c4 + 8, 2 c4 + 9
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          f[e] = prmt(factor(ss, 2 * c4 + 8 * e), factor(ss, 2 * c4 + 8 * e + 1), 0x5410u);
+        constexpr int kWords = D / 32;  // words of a thread's columns, D / 8 of them, per key
+        uint32_t v[4][kWords];          // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = 2 * c4 + (e & 1) + (e >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 y = ld_shared_v4(sv + v_unit<D, E4M3>(key, g8) * 16);
+            v[e][0] = y.x;
+            v[e][1] = y.y;
+            v[e][kWords - 2] = y.z;
+            v[e][kWords - 1] = y.w;
+          } else {
+            const uint2 y = ld_shared_v2(sv + v_unit<D, E4M3>(key, g8 >> 1) * 16 + (g8 & 1) * 8);
+            v[e][0] = y.x;
+            v[e][1] = y.y;
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {  // columns (D / 8) g8 + 2 x and + 1
+          uint32_t r[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int byte = 2 * (x & 1) + (e & 1);
+            const uint32_t sel = 0x4000u + 0x1010u * static_cast<uint32_t>(byte);
+            r[e] = mul_bf16x2(
+                e4m3_bits(prmt(v[e >> 1 << 1][x >> 1], v[(e >> 1 << 1) + 1][x >> 1], sel)), f[e >> 1]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(o[n][x], r[0], r[1], r[2], r[3], p0[n], p1[n]);
+        }
+      }
+    }
+    stage = stage + 1 == L::kStages ? 0 : stage + 1;
+
+    if (ends || i + 1 == steps) {
+      // ---- merge the warps' states of this piece
+      const int M = cw.s.nq * G;
+      __syncthreads();  // the last merge's readers are done
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float l = l_sum[n][e];
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+          const int r = n * 8 + 2 * c4 + e;
+          if (r < M) {
+            if (g8 == 0) ml[warp * L::kRows + r] = make_float2(m_ref[n][e], l);
+            float* dst = merge + (warp * L::kRows + r) * L::kPitch;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              dst[E4M3 ? (D / 8) * g8 + 2 * x : 16 * x + g8] = o[n][x][e];
+              dst[E4M3 ? (D / 8) * g8 + 2 * x + 1 : 16 * x + g8 + 8] = o[n][x][e + 2];
+            }
+          }
+        }
+      __syncthreads();
+      const bool from_start = piece_blk == cw.first;
+      const bool direct = from_start && ends;
+      // slot 0: the piece began in an earlier CTA's run; slot 1: it goes on in the next's
+      const int slot = from_start ? 1 : 0;
+      for (int it = tid; it < M * (D / 4); it += kThreads) {
+        const int r = it / (D / 4), d0 = (it % (D / 4)) * 4;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * L::kRows + r].x);
+        const float mu = m == -INFINITY ? 0.f : m;
+        float l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 z = ml[w * L::kRows + r];
+          const float k = ex2_approx(z.x - mu);
+          l += k * z.y;
+          const float4 v = *reinterpret_cast<const float4*>(merge + (w * L::kRows + r) * L::kPitch + d0);
+          y[0] += k * v.x;
+          y[1] += k * v.y;
+          y[2] += k * v.z;
+          y[3] += k * v.w;
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;  // log2 units
+        if (direct) {
+          const int t = r / G;
+          const long long row = static_cast<long long>(cw.s.t0 + t) * a.H + cw.h * G + (r - t * G);
+          *reinterpret_cast<uint2*>(a.o + row * D + d0) = make_uint2(
+              pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv));
+          if (d0 == 0) a.lse[row] = lse2 * kLn2;
+        } else {
+          const long long row = (2ll * blockIdx.x + slot) * L::kRows + r;
+          *reinterpret_cast<float4*>(a.o_part + row * D + d0) =
+              make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+          if (d0 == 0) a.lse_part[row] = lse2;
+        }
+      }
+      if (first_piece && starts_mid) ended0 = ends;
+      if (!ends && from_start) {
+        slot1_b = cw.b;
+        slot1_h = cw.h;
+      }
+      first_piece = false;
+      clear();
+      piece_blk = nw.blk;
+      if (ends) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < D / 8; ++e) q[n][e] = qn[n][e];
+      }
+    }
+    cw = nw;
+  }
+  cp_async_wait<0>();
+  if (tid == 0) headers[blockIdx.x] = make_int4(slot1_b, slot1_h, !starts_mid || ended0, 0);
+}
+
+// Merge of the pieces of a head that runs' ends have cut: with lse_s and the normalised O_s
+// of piece s, O = sum_s 2^(lse_s - m) O_s / sum_s 2^(lse_s - m), m = max_s lse_s. Block (c, r)
+// takes query row r of the head that CTA c's run began and did not end; the next CTAs'
+// pieces follow until one ends it. In the order of the pieces, so always the same result.
+template <int D>
+__global__ void __launch_bounds__(kThreads) fa_paged_step_merge_kernel(const PagedAttnArgs a, int ctas,
+                                                                       int rows) {
+  constexpr int kPer = D / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = blockIdx.x, r = blockIdx.y;
+  __shared__ int n_more;
+  __shared__ float mx[kWarps], dens[kWarps];
+  __shared__ float acc_s[kWarps][D];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4* headers = reinterpret_cast<const int4*>(a.headers);
+  const int4 hd = headers[c];
+  if (hd.x < 0) return;
+  const PagedSeq s = paged_attn_seq(a.c, hd.x);
+  const int G = a.H / a.c.Hkv;
+  if (r >= s.nq * G) return;
+  if (tid == 0) n_more = ctas - 1 - c;
+  __syncthreads();
+  for (int i = c + 1 + tid; i < ctas; i += kThreads)
+    if (headers[i].z != 0) {
+      atomicMin(&n_more, i - c);
+      break;
+    }
+  __syncthreads();
+  const int n = 1 + n_more;  // pieces: slot 1 of CTA c, slot 0 of the n - 1 after it
+  auto row_of = [&](int i) { return (2ll * (c + i) + (i == 0 ? 1 : 0)) * rows + r; };
+  float m = -INFINITY;
+  for (int i = tid; i < n; i += kThreads) m = fmaxf(m, a.lse_part[row_of(i)]);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  if (lane == 0) mx[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, mx[w]);
+  const float mu = m == -INFINITY ? 0.f : m;
+  float den = 0.f, acc[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += kWarps) {
+    const long long row = row_of(i);
+    const float w = ex2_approx(a.lse_part[row] - mu);
+    den += w;
+    const float* p = a.o_part + row * D + lane * kPer;
+    if constexpr (kPer == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      acc[0] += w * v.x;
+      acc[1] += w * v.y;
+      acc[2] += w * v.z;
+      acc[3] += w * v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(p);
+      acc[0] += w * v.x;
+      acc[1] += w * v.y;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc_s[warp][lane * kPer + k] = acc[k];
+  if (lane == 0) dens[warp] = den;
+  __syncthreads();
+  if (tid < D) {
+    float y = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      y += acc_s[w][tid];
+      l += dens[w];
+    }
+    const int t = r / G;
+    const long long row = static_cast<long long>(s.t0 + t) * a.H + hd.y * G + (r - t * G);
+    a.o[row * D + tid] = __float2bfloat16(l > 0.f ? y / l : 0.f);
+    if (tid == 0) a.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+  }
+}
+
+namespace {
+
+template <int D, bool E4M3, int NT>
+cudaError_t launch_impl(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
+  using L = StepL<D, E4M3, NT>;
+  auto kern = fa_paged_step_kernel<D, E4M3, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       L::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, kThreads, L::kSmemBytes, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // The merge may be scheduled while the step runs; its blocks wait for the step's end
+  // before they read anything.
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, (a.H / a.c.Hkv) * a.c.max_q);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_paged_step_merge_kernel<D>, a, ctas, L::kRows);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_rows(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
+  const int rows = (a.H / a.c.Hkv) * a.c.max_q;
+  return rows <= 8 ? launch_impl<D, E4M3, 1>(a, ctas, stream)
+                   : launch_impl<D, E4M3, 2>(a, ctas, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_step(const PagedAttnArgs& a, bool e4m3, int ctas, cudaStream_t stream) {
+  if (a.c.d == 64)
+    return e4m3 ? launch_rows<64, true>(a, ctas, stream) : launch_rows<64, false>(a, ctas, stream);
+  return e4m3 ? launch_rows<128, true>(a, ctas, stream) : launch_rows<128, false>(a, ctas, stream);
+}
+
+}  // namespace fa

@@ -43,7 +43,8 @@ class Batch:
         shape = (self.P, Hkv, page, d)
         dtype = torch.uint8 if e4m3 else torch.bfloat16
         self.pages = {n: torch.full(shape, 0x7E if e4m3 else garbage, dtype=dtype) for n in "kv"}
-        self.scale = {n: torch.full(shape[:3], 133, dtype=torch.uint8) if e4m3 else None
+        self.scale = {n: torch.full(shape[:3], 255 if math.isnan(garbage) else 133,
+                                    dtype=torch.uint8) if e4m3 else None
                       for n in "kv"}
         self.layout = layout
 

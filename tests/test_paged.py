@@ -176,10 +176,11 @@ def test_rows_without_keys(nq, e4m3):
 
 @pytest.mark.parametrize("nq,max_q", [([1, 1], 1), ([70, 3], 70)])
 @pytest.mark.parametrize("d", [64, 128])
-def test_what_lies_behind_a_sequence_does_not_matter(nq, max_q, d):
-    # NaN in every row of the pool that no position of a sequence below its length takes,
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_what_lies_behind_a_sequence_does_not_matter(nq, max_q, d, e4m3):
+    # NaN (scale byte 255 in a quantised cache) in every row of the pool that no position of a sequence below its length takes,
     # within the last pages too
-    b = Batch(nq, [130, 75], 64, 2, d, G=2, seed=10, garbage=float("nan"), extra_rows=5)
+    b = Batch(nq, [130, 75], 64, 2, d, e4m3, G=2, seed=10, garbage=float("nan"), extra_rows=5)
     x = b.fill().on(DEV)
     o = torch.full((b.T, b.H, d), 7.0, dtype=torch.bfloat16, device=DEV)
     lse = torch.full((b.T, b.H), 7.0, device=DEV)
@@ -431,6 +432,27 @@ def test_prefill_then_steps_then_read_back(e4m3):
     sync()
     ends = [int(b.cu[1]) - 1, int(b.cu[2]) - 1]
     check_attn(o[:, :, 0], lse[:, :, 0], tuple(r[ends] for r in whole))
+
+
+def test_workspace_is_checked():
+    lib = fa.load()
+    b = Batch([1, 1], [300, 40], 16, 2, 64, G=2, seed=24)
+    x = b.fill().on(DEV)
+    o, lse = torch.empty_like(x.q), torch.empty((2, 4), device=DEV)
+    P, Hkv, page, d = x.k.shape
+    need = fa.fa_paged_workspace_size(4, 2, 64, 1)
+    assert need > 0 and fa.fa_paged_workspace_size(4, 3, 64, 1) == 0
+    ws = torch.empty(need + 16, dtype=torch.uint8, device=DEV)
+    for at, size, status in ((None, need, 4), (ws.data_ptr(), need - 1, 4),
+                             (ws.data_ptr() + 8, need, 4), (ws.data_ptr(), need, 0)):
+        assert lib.fa_paged_attn(x.q.data_ptr(), x.k.data_ptr(), x.v.data_ptr(), None, None,
+                                 o.data_ptr(), lse.data_ptr(), 0, P, page, 4, Hkv, d,
+                                 *x.k.stride()[:3], x.table.data_ptr(), x.table.stride(0),
+                                 x.table.shape[1], x.kv.data_ptr(), x.cu.data_ptr(), 2, 2, 1,
+                                 4 * d, 0.125, 1, -1, at, size,
+                                 torch.cuda.current_stream().cuda_stream) == status
+    sync()
+    check_attn(o, lse, b.oracle(True))
 
 
 def test_binding_refusals_on_the_gpu():

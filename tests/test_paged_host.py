@@ -52,7 +52,7 @@ def attn(lib, q=A, k=A, v=A, ks=None, vs=None, o=A, lse=A, H=4, cu=A, B=2, T=5, 
     (dict(table=A + 2), 1), (dict(kv=A + 1), 1), (dict(num_pages=0), 1), (dict(page_size=0), 1),
     (dict(page_size=24), 2), (dict(H_kv=0), 1), (dict(d=96), 2), (dict(d=0), 2), (dict(type=2), 2),
     (dict(type=-1), 2), (dict(type=1), 1),  # e4m3 without scales
-    (dict(type=1, ks=A), 1), (dict(sp=0), 1), (dict(sh=-64), 1), (dict(sr=60), 1),
+    (dict(type=1, ks=A), 1), (dict(type=1, ks=A + 8, vs=A), 1), (dict(sp=0), 1), (dict(sh=-64), 1), (dict(sr=60), 1),
     (dict(sp=1 << 40), 1), (dict(type=1, ks=A, vs=A, sr=72), 1),  # 72 codes: not 16-byte rows
     (dict(max_pages=0), 1), (dict(ts=2), 1), (dict(B=0), 1),
     (dict(max_pages=1 << 27, ts=1 << 27), 1),  # positions beyond 32 bits
