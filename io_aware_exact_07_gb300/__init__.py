@@ -16,6 +16,7 @@ quantised to e4m3 (``paged_cache`` allocates one).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -575,74 +576,108 @@ def paged_cache(num_pages, page_size, H_kv, d, e4m3=False, device="cuda"):
 
 
 def _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale):
-    """Arguments that the paged calls share, checked: (cache type .. d and strides, then the
-    table and the lengths) as the C entry points take them, and B."""
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+    """Arguments that the paged calls share, checked: (cache type .. page_size), then (H_kv ..
+    kv_lens), as the C entry points take them, B and the device's index."""
+    shape, st, dtype = k_pages.shape, k_pages.stride(), k_pages.dtype
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype != dtype:
         raise ValueError("k_pages and v_pages must be alike, [num_pages, H_kv, page_size, d]")
-    P, Hkv, page, d = k_pages.shape
-    st = k_pages.stride()
-    if v_pages.stride() != st or (d > 1 and st[3] != 1):
+    P, Hkv, page, d = shape
+    if v_pages.stride() != st or (st[3] != 1 and d > 1):
         raise ValueError("k_pages and v_pages must have the same strides, with d contiguous")
-    dev = k_pages.device
-    if dev.type != "cuda" or v_pages.device != dev:
+    dev = k_pages.get_device()
+    if dev < 0 or v_pages.get_device() != dev:
         raise ValueError("k_pages and v_pages must be CUDA tensors on one device")
-    if k_pages.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         kind = FA_CACHE_BF16
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 cache has no scales")
-    elif k_pages.dtype in (torch.uint8, torch.float8_e4m3fn):
+    elif dtype in (torch.uint8, torch.float8_e4m3fn):
         kind = FA_CACHE_E4M3
         for t in (k_scale, v_scale):
-            if (t is None or t.dtype != torch.uint8 or t.shape != (P, Hkv, page)
-                    or not t.is_contiguous() or t.device != dev):
+            if (t is None or t.dtype != torch.uint8 or t.shape != shape[:3]
+                    or not t.is_contiguous() or t.get_device() != dev):
                 raise ValueError("an e4m3 cache needs k_scale and v_scale, contiguous uint8 "
-                                 f"[{P}, {Hkv}, {page}] on {dev}")
+                                 f"[{P}, {Hkv}, {page}], on the pages' device")
     else:
         raise ValueError("pages must be bf16, or e4m3 codes (uint8 or float8_e4m3fn)")
-    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev
-            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
-        raise ValueError(f"page_table must be int32 [B, max_pages] on {dev}, rows contiguous")
-    B, width = page_table.shape
-    if (kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or kv_lens.device != dev
+    table = page_table.shape
+    if page_table.dtype != torch.int32 or len(table) != 2 or page_table.get_device() != dev:
+        raise ValueError("page_table must be int32 [B, max_pages], on the pages' device")
+    B, width = table
+    ts, tc = page_table.stride()
+    if tc != 1 and width > 1:
+        raise ValueError("the rows of page_table must be contiguous")
+    if (kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or kv_lens.get_device() != dev
             or not kv_lens.is_contiguous()):
-        raise ValueError(f"kv_lens must be contiguous int32 [{B}] on {dev}")
+        raise ValueError(f"kv_lens must be contiguous int32 [{B}], on the pages' device")
     # the stride of a dimension of size one is never used: any valid one stands for it
     sr = st[2] if page > 1 else d
     sh = st[1] if Hkv > 1 else sr * page
     sp = st[0] if P > 1 else sh * Hkv
-    ts = page_table.stride(0) if B > 1 else width
-    return (kind, P, page), (Hkv, d, sp, sh, sr, page_table, ts, width, kv_lens), B
+    return ((kind, P, page), (Hkv, d, sp, sh, sr, page_table.data_ptr(),
+                              ts if B > 1 else width, width, kv_lens.data_ptr()), B, dev)
 
 
 def _new_rows(name, x, heads, d, dev):
     """Token stride of packed rows [T, heads, d] with heads and d contiguous."""
-    if (x.dtype != torch.bfloat16 or x.dim() != 3 or tuple(x.shape[1:]) != (heads, d)
-            or x.device != dev or x.stride(2) != 1 or (heads > 1 and x.stride(1) != d)):
-        raise ValueError(f"{name} must be bf16 [T, {heads}, {d}] on {dev}, heads and d contiguous")
-    return x.stride(0) if x.shape[0] > 1 else heads * d
+    shape = x.shape
+    if (x.dtype != torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != d
+            or x.get_device() != dev):
+        raise ValueError(f"{name} must be bf16 [T, {heads}, {d}], on the pages' device")
+    st, sh, sd = x.stride()
+    if sd != 1 or (sh != d and heads > 1):
+        raise ValueError(f"heads and d of {name} must be contiguous")
+    return st if shape[0] > 1 else heads * d
 
 
 def _offsets(cu, B, T, max_q, dev):
-    """max_q of a batch of T packed rows; checks cu_seqlens_q."""
+    """Pointer of cu_seqlens_q (checked) and max_q of a batch of T packed rows."""
     if cu is None:
         if T % B != 0 or (max_q is not None and max_q * B != T):
             raise ValueError("without cu_seqlens_q the rows must be B times max_q")
-        return T // B
-    if (cu.dtype != torch.int32 or cu.shape != (B + 1,) or cu.device != dev
+        return None, T // B
+    if (cu.dtype != torch.int32 or cu.shape != (B + 1,) or cu.get_device() != dev
             or not cu.is_contiguous()):
-        raise ValueError(f"cu_seqlens_q must be contiguous int32 [{B + 1}] on {dev}")
-    return T if max_q is None else max_q
+        raise ValueError(f"cu_seqlens_q must be contiguous int32 [{B + 1}], on the pages' device")
+    return cu.data_ptr(), T if max_q is None else max_q
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, dev, stream, *args):
+    """Call a C entry point on device `dev` and a stream of it (the current one if None)."""
+    if stream is None:
+        # the raw handle of the current stream, without a Stream object around it: a
+        # decode step makes this call in microseconds
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    f = getattr(load() if _lib is None else _lib, name)
+    if torch.cuda.current_device() == dev:
+        status = f(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, handle)
+    if status != FA_OK:
+        raise FAError(status, name)
 
 
 def _used_on(stream, *tensors):
     """Tell the allocator that tensors made here are used on a stream other than the
     current one, so that their memory is not handed out again before that work is done."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream))
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+@functools.lru_cache(maxsize=None)
+def _paged_workspace_bytes(H, H_kv, d, max_q, dev):
+    with torch.cuda.device(dev):  # depends on the device's number of SMs
+        return fa_paged_workspace_size(H, H_kv, d, max_q)
 
 
 def paged_write(k_new, v_new, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None,
@@ -650,29 +685,28 @@ def paged_write(k_new, v_new, k_pages, v_pages, page_table, kv_lens, cu_seqlens_
     """Store new rows k_new, v_new [T, H_kv, d] into the pages (fa_paged_write). The new tokens
     of sequence b are rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] (T / B each without
     cu_seqlens_q) and take its last positions, kv_lens [B] counting them already."""
-    head, batch, B = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
-    dev, T = k_pages.device, k_new.shape[0]
+    head, batch, B, dev = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
+    T = k_new.shape[0]
     ks = _new_rows("k_new", k_new, batch[0], batch[1], dev)
     vs = _new_rows("v_new", v_new, batch[0], batch[1], dev)
     if v_new.shape[0] != T:
         raise ValueError("k_new and v_new must have the same number of rows")
-    n = _offsets(cu_seqlens_q, B, T, None, dev)
-    with torch.cuda.device(dev):
-        _check(fa_paged_write(k_new, v_new, k_pages, v_pages, k_scale, v_scale, *head, *batch,
-                              cu_seqlens_q, B, T, n, ks, vs, stream), "fa_paged_write")
+    cu, n = _offsets(cu_seqlens_q, B, T, None, dev)
+    _call("fa_paged_write", dev, stream, k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
+          v_pages.data_ptr(), _data(k_scale), _data(v_scale), *head, *batch, cu, B, T, n, ks, vs)
 
 
 def paged_read(k_pages, v_pages, page_table, kv_lens, N, k_scale=None, v_scale=None, stream=None):
     """Copy positions 0 .. N - 1 of every sequence out of the pages (fa_paged_read): k and v,
     bf16 [B, H_kv, N, d], zeros behind each sequence. fwd and decode take them with
     seqlens_k=kv_lens."""
-    head, batch, B = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
-    dev = k_pages.device
-    k, v = (torch.empty((B, batch[0], N, batch[1]), dtype=torch.bfloat16, device=dev)
-            for _ in range(2))
-    with torch.cuda.device(dev):
-        _check(fa_paged_read(k_pages, v_pages, k_scale, v_scale, *head, *batch, B, N, k, v,
-                             stream), "fa_paged_read")
+    head, batch, B, dev = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
+    shape, device = (B, batch[0], N, batch[1]), k_pages.device
+    k = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    v = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    _call("fa_paged_read", dev, stream, k_pages.data_ptr(), v_pages.data_ptr(), _data(k_scale),
+          _data(v_scale), *head, *batch, B, N, k.data_ptr(), v.data_ptr())
+    if stream is not None:
         _used_on(stream, k, v)
     return k, v
 
@@ -684,31 +718,32 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
     cu_seqlens_q); max_q bounds their number (T where it is not given: pass it for single
     tokens, whose kernel is another). Returns (o [T, H, d] bf16, lse [T, H] fp32); rows that
     belong to no sequence are not written. out = (o, lse) gives the buffers."""
-    head, batch, B = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
-    dev, Hkv, d = k_pages.device, batch[0], batch[1]
+    head, batch, B, dev = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
+    Hkv, d = batch[0], batch[1]
     if q.dim() != 3:
         raise ValueError("q must be [T, H, d]")
     T, H = q.shape[0], q.shape[1]
     qs = _new_rows("q", q, H, d, dev)
-    n = _offsets(cu_seqlens_q, B, T, max_q, dev)
+    cu, n = _offsets(cu_seqlens_q, B, T, max_q, dev)
+    device = k_pages.device
     if out is None:
-        o = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        o = torch.empty((T, H, d), dtype=torch.bfloat16, device=device)
+        lse = torch.empty((T, H), dtype=torch.float32, device=device)
     else:
         o, lse = out
         if (o.dtype != torch.bfloat16 or o.shape != (T, H, d) or not o.is_contiguous()
                 or lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()
-                or o.device != dev or lse.device != dev):
+                or o.get_device() != dev or lse.get_device() != dev):
             raise ValueError(f"out must be contiguous: bf16 [{T}, {H}, {d}] and fp32 [{T}, {H}]")
     if T == 0:
         return o, lse
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with torch.cuda.device(dev):
-        ws_bytes = fa_paged_workspace_size(H, Hkv, d, n)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-        _check(fa_paged_attn(q, k_pages, v_pages, k_scale, v_scale, o, lse, *head, H, *batch,
-                             cu_seqlens_q, B, T, n, qs, scale, causal, window_left, ws, ws_bytes,
-                             stream), "fa_paged_attn")
+    ws, ws_bytes = None, _paged_workspace_bytes(H, Hkv, d, n, dev)
+    if ws_bytes:
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    _call("fa_paged_attn", dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+          _data(k_scale), _data(v_scale), o.data_ptr(), lse.data_ptr(), *head, H, *batch, cu, B, T,
+          n, qs, 1.0 / math.sqrt(d) if scale is None else float(scale), bool(causal),
+          window_left, _data(ws), ws_bytes)
+    if stream is not None:
         _used_on(stream, *((o, lse, ws) if out is None else (ws,)))
     return o, lse

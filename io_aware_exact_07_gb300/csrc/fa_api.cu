@@ -130,6 +130,45 @@ bool encode_map_u8(CUtensorMap* m, const void* base, int outer, int rows, int in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Packed tokens [T, H, d] bf16, `stride` elements apart: boxes of 64 columns x heads x tokens,
+// 128-byte swizzle.
+bool encode_map_tokens(CUtensorMap* m, const void* base, int T, int H, int d, int64_t stride,
+                       int heads, int tokens) {
+  EncodeTiledFn enc = encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H),
+                        static_cast<cuuint64_t>(T)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+  cuuint32_t elem[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pages of a cache, [num_pages, H_kv, page_size, d] in the cache's strides: boxes of 64 bf16
+// columns (128-byte swizzle) or of d codes (as they are) x rows; out-of-range pages read as zero.
+bool encode_map_pages(CUtensorMap* m, const void* base, const fa::PagedArgs& c, bool e4m3,
+                      int rows) {
+  EncodeTiledFn enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t es = e4m3 ? 1 : 2;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page_size),
+                        static_cast<cuuint64_t>(c.Hkv), static_cast<cuuint64_t>(c.num_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.stride_row) * es,
+                           static_cast<cuuint64_t>(c.stride_head) * es,
+                           static_cast<cuuint64_t>(c.stride_page) * es};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(e4m3 ? c.d : 64), static_cast<cuuint32_t>(rows), 1,
+                       1};
+  cuuint32_t elem[4] = {1, 1, 1, 1};
+  return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 fa::MaskParams make_mask(int B, int H, int Hkv, int N, int causal, const uint8_t* bm,
                          const int32_t* sl, int wl = -1, int wr = -1) {
   fa::MaskParams m;
@@ -757,11 +796,11 @@ static PagedWorkspace paged_workspace(int G, int d, int max_q, int num_sms) {
   PagedWorkspace w;
   const long long rows = static_cast<long long>(G) * max_q;
   w.ctas = num_sms;
-  w.rows = rows <= 8 ? 8 : fa::kStepRows;
+  w.rows = rows <= 8 ? 8 : rows <= fa::kStepRows ? fa::kStepRows : fa::kTile;
   const size_t slots = 2 * static_cast<size_t>(w.ctas) * w.rows;
   w.lse_off = round256(static_cast<size_t>(w.ctas) * 16);
   w.o_off = w.lse_off + round256(slots * sizeof(float));
-  w.bytes = rows > fa::kStepRows ? 0 : w.o_off + round256(slots * d * sizeof(float));
+  w.bytes = w.o_off + round256(slots * d * sizeof(float));
   return w;
 }
 
@@ -797,7 +836,7 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   DeviceInfo* di = nullptr;
   if ((st = device_info(&di)) != FA_OK) return st;
   const PagedWorkspace w = paged_workspace(H / H_kv, d, max_q, di->num_sms);
-  if (w.bytes > 0 && (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace)))
+  if (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace))
     return FA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.headers = ws;
@@ -814,8 +853,21 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   a.wl = window_left;
   const bool e4m3 = type == FA_CACHE_E4M3;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  cudaError_t e = w.bytes > 0 ? fa::launch_paged_step(a, e4m3, w.ctas, cs)
-                              : fa::launch_paged_attn(a, e4m3, cs);
+  cudaError_t e;
+  if (w.rows <= fa::kStepRows) {
+    e = fa::launch_paged_step(a, e4m3, w.ctas, cs);
+  } else {
+    a.sync = make_sync(di, kStallForward);
+    const int G = H / H_kv;
+    int box = 128;  // rows of a page that a key tile can take at once
+    while (page_size % box != 0) box /= 2;
+    CUtensorMap tq, tk, tv;
+    if (!encode_map_tokens(&tq, q, T, H, d, q_stride, G, fa::kTile / G) ||
+        !encode_map_pages(&tk, k_pages, a.c, e4m3, box) ||
+        !encode_map_pages(&tv, v_pages, a.c, e4m3, box))
+      return FA_ERR_CUDA;
+    e = fa::launch_paged_chunk(tq, tk, tv, a, e4m3, box, w.ctas, cs);
+  }
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

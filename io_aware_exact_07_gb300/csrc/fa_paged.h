@@ -153,12 +153,17 @@ struct PagedAttnArgs {
   void* headers;                // [ctas] int4
   float* o_part;
   float* lse_part;
+  SyncParams sync;
 };
 constexpr int kStepRows = 16;   // most query rows per K/V head of the step kernel
 
 cudaError_t launch_paged_write(const PagedWriteArgs& a, bool e4m3, cudaStream_t stream);
 cudaError_t launch_paged_read(const PagedReadArgs& a, bool e4m3, cudaStream_t stream);
 cudaError_t launch_paged_step(const PagedAttnArgs& a, bool e4m3, int ctas, cudaStream_t stream);
-cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool e4m3, cudaStream_t stream);
+// tq: [T, H, d] with boxes of (64 columns, H / Hkv heads, 128 / (H / Hkv) tokens); tk, tv:
+// [num_pages, Hkv, page_size, d] with boxes of 64 bf16 columns or d codes times box_rows rows.
+cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const PagedAttnArgs& a, bool e4m3, int box_rows, int ctas,
+                               cudaStream_t stream);
 
 }  // namespace fa

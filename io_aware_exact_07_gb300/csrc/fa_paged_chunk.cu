@@ -1,0 +1,1112 @@
+// Attention of chunks of new tokens over a paged cache: tiled S = Q K^T, online softmax and
+// O += P V on the tensor cores, as in the contiguous forward (FlashAttention deep-read
+// report, sections 2.4 and 3.2), with pages gathered tile by tile, ragged batches and query
+// heads that share K/V heads.
+//
+// A query tile is 128 rows of one K/V head: TT = 128 / G tokens times the G = H / Hkv heads
+// that read it (row r = t * G + g), so that K and V are read once for all of them. The list
+// of (sequence, K/V head, query tile, 128-key tile) places is cut into equal runs, one per
+// CTA (one CTA per SM): chunks of any lengths keep all SMs equally busy, and few query tiles
+// over a long cache are split along the keys. A query tile cut by a run's end leaves
+// normalised pieces for the merge kernel.
+//
+// Roles of a CTA (the head-dimension-128 forward's shape, here for 64 too):
+//   warps 0-3, 4-7  softmax warpgroups g = 0, 1: key tiles at even and odd positions of a
+//                   piece (thread = query row), each with its own m, l, O in tensor memory;
+//                   the epilogue merges the two
+//   warp 8          Q, and K tiles (bf16: into the K ring; e4m3: code tiles of K and V into
+//                   the staging ring), one box per page (or 16 .. 128 rows of it)
+//   warp 9, 10      S issuer, PV issuer (one lane each)
+//   warp 11         V tiles (bf16)
+//   warps 12-15     e4m3 only: turn staged codes into the bf16 tiles that the products read,
+//                   exactly, with the rows' scales folded in; all else is as for bf16
+// Keys behind a sequence are masked by their number; V's rows there are made zero, since a
+// weight of zero would not hide a NaN.
+//
+// Bounds: for chunks the exponentials (one per score, 16 a cycle and SM) and the tensor core
+// (512 cycles of products per 128 x 128 tile at d = 128); for few rows HBM.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fa_paged_plan.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kSoftmaxWarps = 8;
+constexpr int kQkWarp = 8;
+constexpr int kSIssuer = 9;
+constexpr int kPvIssuer = 10;
+constexpr int kVWarp = 11;
+constexpr int kConvWarp = 12;  // first of four (e4m3)
+constexpr float kRescale = 8.0f;  // log2 units: rescale O when m grows by > 2^8
+
+template <int D, bool E4M3>
+struct ChunkL {
+  static constexpr int kWarps = E4M3 ? 16 : 12;
+  static constexpr int kThreads = kWarps * 32;
+  // Registers per thread at launch, and as the warpgroups share them out afterwards.
+  static constexpr int kRegsLaunch = E4M3 ? 128 : 168;
+  static constexpr int kRegsSoftmax = E4M3 ? 184 : 200;
+  static constexpr int kRegsAux = E4M3 ? 72 : 96;
+  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsAux <= kThreads * kRegsLaunch,
+                "register reallocation exceeds the block's launch allocation");
+  static constexpr int kTileBytes = kTile * D * 2;   // a 128 x D bf16 tile
+  static constexpr int kPBytes = kTile * kTile * 2;  // P_g
+  static constexpr int kChunks = D / 64;             // 64-column (128-byte) swizzle chunks
+  static constexpr int kCodeBytes = kTile * D;       // a staged tile of codes
+  // At e4m3 and d = 128 one K tile suffices: a K tile is read by its S product while the
+  // next V tile is converted. That leaves room for two staged tiles.
+  static constexpr int kKStages = D == 64 ? (E4M3 ? 2 : 4) : (E4M3 ? 1 : 2);
+  static constexpr int kVStages = D == 64 ? (E4M3 ? 3 : 4) : 2;
+  static constexpr int kCStages = E4M3 ? (D == 64 ? 4 : 2) : 0;
+  static constexpr int kMaxStages = 4;
+  static constexpr int kQOff = 0;
+  static constexpr int kKOff = kTileBytes;
+  static constexpr int kVOff = kKOff + kKStages * kTileBytes;
+  static constexpr int kPOff = kVOff + kVStages * kTileBytes;
+  static constexpr int kCOff = kPOff + 2 * kPBytes;
+  static constexpr int kBarOff = kCOff + kCStages * kCodeBytes;
+  // q_full, q_empty, K, V and staging rings (full, empty), s_full[2], s_free[2], p_full[2],
+  // pv_done[2], o_free, xbar[4], v_tail, drain, drain2, stall
+  static constexpr int kNumBars = 2 + 6 * kMaxStages + 8 + 1 + 4 + 4;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // abort flag, PV count, TMEM address
+  static constexpr int kXchOff = (kMiscOff + 16 + 15) / 16 * 16;  // (m, l) per warpgroup and row
+  // the plan's scratch is used before the exchange area is
+  static constexpr int kPlanOff = kXchOff;
+  static constexpr int kSmemBytes = kXchOff + 2 * kTile * 8;
+  static_assert(kSmemBytes <= 232448, "shared memory exceeds the per-block limit");
+  __device__ static constexpr uint32_t col_s(int g) { return 128u * static_cast<uint32_t>(g); }
+  __device__ static constexpr uint32_t col_o(int g) { return 256u + 128u * static_cast<uint32_t>(g); }
+};
+
+struct Bars {
+  uint32_t q_full, q_empty;
+  BarRun k_full, k_empty, v_full, v_empty, c_full, c_empty;  // ring stages
+  BarRun s_full, s_free, p_full, pv_done;                    // per softmax warpgroup
+  uint32_t o_free;
+  BarRun xbar;
+  uint32_t v_tail, drain, drain2, stall;
+};
+
+// Key tiles of a unit (query tile qt of a sequence): places n >= 1, of which the first nr
+// are tiles jf, jf + 1, ... (a unit whose rows see no key has one place and no tile).
+struct Tiles {
+  int jf, nr, n;
+};
+__device__ __forceinline__ Tiles tiles_of(const PagedAttnArgs& a, const PagedSeq& s, int tt, int qt) {
+  const int t_lo = qt * tt, t_hi = min(s.nq, t_lo + tt);
+  const int pos = s.len - s.nq;
+  const int hi = a.causal ? min(s.len, pos + t_hi) : s.len;  // keys [lo, hi) for some row
+  const int lo = a.wl >= 0 ? max(0, pos + t_lo - a.wl) : 0;
+  Tiles r;
+  r.jf = lo / kTile;
+  r.nr = hi > lo ? (hi + kTile - 1) / kTile - r.jf : 0;
+  r.n = r.nr > 0 ? r.nr : 1;
+  return r;
+}
+
+// A CTA's run: units one after another, cut at its ends. Every role walks the same run.
+struct Walk {
+  int b, h, qt, n_qt;
+  int at;            // place in the unit at which the piece begins
+  long long left;    // places left in the run
+  PagedSeq s;
+  Tiles u;
+  // the current piece
+  int j0, nt;        // its key tiles: j0, j0 + 1, ..., nt of them
+  bool from_start, ends;
+
+  __device__ __forceinline__ void seq(const PagedAttnArgs& a, int tt) {
+    s = paged_attn_seq(a.c, b);
+    n_qt = (s.nq + tt - 1) / tt;
+  }
+  __device__ __forceinline__ void piece(const PagedAttnArgs& a, int tt) {
+    u = tiles_of(a, s, tt, qt);
+    const int take = left < u.n - at ? static_cast<int>(left) : u.n - at;
+    j0 = u.jf + at;
+    const int end = u.jf + u.nr;
+    nt = min(j0 + take, end) - j0;
+    if (nt < 0) nt = 0;
+    from_start = at == 0;
+    ends = at + take == u.n;
+    left -= take;
+  }
+  // Next piece; false at the end of the run.
+  __device__ __forceinline__ bool next(const PagedAttnArgs& a, int tt) {
+    if (left <= 0) return false;
+    at = 0;
+    if (++qt == n_qt) {
+      qt = 0;
+      if (++h == a.c.Hkv) {
+        h = 0;
+        do {
+          if (++b >= a.c.B) return false;
+          seq(a, tt);
+        } while (n_qt == 0);
+      }
+    }
+    piece(a, tt);
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                            int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+// Scores of keys outside [lo, hi) of a tile are masked.
+__device__ __forceinline__ void mask_row(float* s, int lo, int hi) {
+#pragma unroll
+  for (int k = 0; k < 128; ++k)
+    if (k >= hi || k < lo) s[k] = -INFINITY;
+}
+
+}  // namespace
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
+    fa_paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const PagedAttnArgs args,
+                          const int box_rows) {
+  using L = ChunkL<D, E4M3>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  PieceHeader* headers = static_cast<PieceHeader*>(args.headers);
+  pdl_launch_dependents();
+  if ((smem_u32(smem) & 1023u) != 0u) {
+    if (threadIdx.x == 0) {
+      record_error(args.sync.status, kStatusCuda);
+      headers[blockIdx.x] = PieceHeader{-1, 0, 1, 0};
+    }
+    return;
+  }
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int G = args.H / args.c.Hkv;
+  const int tt = kTile / G;  // tokens of a query tile
+
+  // ---- this CTA's run of the list
+  struct Plan {
+    long long warp_sums[L::kWarps];
+    long long rem;
+    int b, h, qt, at;
+  };
+  static_assert(sizeof(Plan) <= 2 * kTile * 8, "plan scratch");
+  Plan* plan = reinterpret_cast<Plan*>(smem + L::kPlanOff);
+  // Places of one K/V head of sequence b; long chunks are summed by the whole warp.
+  auto head_places = [&](int b) -> long long {
+    PagedSeq s = {0, 0, 0};
+    if (b < args.c.B) s = paged_attn_seq(args.c, b);
+    const int n_qt = (s.nq + tt - 1) / tt;
+    long long sum = 0;
+    if (n_qt <= 2)
+      for (int i = 0; i < n_qt; ++i) sum += tiles_of(args, s, tt, i).n;
+    unsigned todo = __ballot_sync(0xffffffffu, n_qt > 2);
+    while (todo != 0u) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      PagedSeq z;
+      z.t0 = 0;
+      z.nq = __shfl_sync(0xffffffffu, s.nq, src);
+      z.len = __shfl_sync(0xffffffffu, s.len, src);
+      const int n = (z.nq + tt - 1) / tt;
+      long long part = 0;
+      for (int i = lane; i < n; i += 32) part += tiles_of(args, z, tt, i).n;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) part += __shfl_xor_sync(0xffffffffu, part, k);
+      if (lane == src) sum = part;
+    }
+    return sum;
+  };
+  long long total = 0, x0 = 0;
+  for (int b0 = 0; b0 < args.c.B; b0 += L::kThreads) {
+    const long long x = head_places(b0 + tid) * args.c.Hkv;
+    if (b0 == 0) x0 = x;
+    long long sum;
+    block_scan<L::kWarps>(x, plan->warp_sums, &sum);
+    total += sum;
+  }
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long lo = per * blockIdx.x;
+  const long long hi = lo + per < total ? lo + per : total;
+  if (lo >= hi) {
+    if (tid == 0) headers[blockIdx.x] = PieceHeader{-1, 0, 1, 0};
+    return;
+  }
+  {
+    long long base = 0;
+    for (int b0 = 0; b0 < args.c.B && base <= lo; b0 += L::kThreads) {
+      const long long x = b0 == 0 ? x0 : head_places(b0 + tid) * args.c.Hkv;
+      long long sum;
+      const long long at = base + block_scan<L::kWarps>(x, plan->warp_sums, &sum);
+      if (at <= lo && lo < at + x) {
+        const long long one = x / args.c.Hkv;  // places of one head
+        plan->b = b0 + tid;
+        plan->h = static_cast<int>((lo - at) / one);
+        plan->rem = (lo - at) % one;
+      }
+      base += sum;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // the query tile within the head: 32 at a time
+    const PagedSeq s = paged_attn_seq(args.c, plan->b);
+    const int n_qt = (s.nq + tt - 1) / tt;
+    long long rem = plan->rem;
+    for (int i0 = 0; i0 < n_qt; i0 += 32) {
+      const int n = i0 + lane < n_qt ? tiles_of(args, s, tt, i0 + lane).n : 0;
+      long long inc = n;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, k);
+        if (lane >= k) inc += y;
+      }
+      if (inc - n <= rem && rem < inc) {
+        plan->qt = i0 + lane;
+        plan->at = static_cast<int>(rem - (inc - n));
+      }
+      const long long all = __shfl_sync(0xffffffffu, inc, 31);
+      if (rem < all) break;
+      rem -= all;
+    }
+  }
+
+  uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
+  // pieces whose PVs have all been issued: a count, not a barrier phase, since the PV issuer
+  // may run several pieces without key tiles ahead of the S issuer
+  volatile int* pv_units = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff + 8);
+  Bars bars;
+  {
+    int i = 0;
+    auto nb = [&]() { return smem_u32(&bar_mem[i++]); };
+    auto run = [&](int n) {
+      const BarRun r{smem_u32(&bar_mem[i])};
+      i += n;
+      return r;
+    };
+    bars.q_full = nb();
+    bars.q_empty = nb();
+    bars.k_full = run(L::kMaxStages);
+    bars.k_empty = run(L::kMaxStages);
+    bars.v_full = run(L::kMaxStages);
+    bars.v_empty = run(L::kMaxStages);
+    bars.c_full = run(L::kMaxStages);
+    bars.c_empty = run(L::kMaxStages);
+    bars.s_full = run(2);
+    bars.s_free = run(2);
+    bars.p_full = run(2);
+    bars.pv_done = run(2);
+    bars.o_free = nb();
+    bars.xbar = run(4);
+    bars.v_tail = nb();
+    bars.drain = nb();
+    bars.drain2 = nb();
+    bars.stall = nb();
+  }
+  if (tid == 0) {
+    *abort_flag = 0;
+    *pv_units = 0;
+    mbar_init(bars.q_full, 1);
+    mbar_init(bars.q_empty, 1);
+    for (int s = 0; s < L::kMaxStages; ++s) {
+      // e4m3: the four converter warps arrive; bf16: the producer, with the bytes expected
+      mbar_init(bars.k_full[s], E4M3 ? 4 : 1);
+      mbar_init(bars.v_full[s], E4M3 ? 4 : 1);
+      mbar_init(bars.k_empty[s], 1);
+      mbar_init(bars.v_empty[s], 1);
+      mbar_init(bars.c_full[s], 1);
+      mbar_init(bars.c_empty[s], 4);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(bars.s_full[g], 1);
+      mbar_init(bars.s_free[g], 128);
+      mbar_init(bars.p_full[g], 128);
+      mbar_init(bars.pv_done[g], 1);
+    }
+    // o_free: the 256 softmax threads at the end of each epilogue, plus the PV issuer once
+    // per piece after its own wait on the previous phase, so that no phase can complete
+    // while the PV issuer still waits on the one before it
+    mbar_init(bars.o_free, 257);
+    for (int q = 0; q < 4; ++q) mbar_init(bars.xbar[q], 64);
+    mbar_init(bars.v_tail, 1);
+    mbar_init(bars.drain, 1);
+    mbar_init(bars.drain2, 1);
+    mbar_init(bars.stall, 1);
+    fence_mbar_init();
+  }
+  if (warp == kSIssuer) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint64_t tmo = args.sync.timeout_ns;
+  Walk w;
+  w.b = plan->b;
+  w.h = plan->h;
+  w.qt = plan->qt;
+  w.at = plan->at;
+  w.left = hi - lo;
+  w.seq(args, tt);
+  w.piece(args, tt);
+  __syncthreads();  // the plan has been read: its place is the exchange area from here on
+
+  auto fail = [&](void) {
+    *abort_flag = 1;
+    record_error(args.sync.status, kStatusTimeout);
+  };
+  const uint32_t sQ = smem_u32(smem + L::kQOff);
+  const uint32_t sK = smem_u32(smem + L::kKOff);
+  const uint32_t sV = smem_u32(smem + L::kVOff);
+  const uint32_t sP = smem_u32(smem + L::kPOff);
+  const uint32_t sC = smem_u32(smem + L::kCOff);
+  const int n_box = kTile / box_rows;  // boxes of a key tile
+
+  if (warp >= kSoftmaxWarps) {
+    regs_dec<L::kRegsAux>();
+    // Page of this lane's box of key tile j (lane < n_box); num_pages, which lies outside
+    // the map and reads as zeros, behind the sequence and for a page that is none.
+    auto box_page = [&](int j) {
+      const int pos = j * kTile + lane * box_rows;
+      if (lane >= n_box || pos >= w.s.len) return args.c.num_pages;
+      const int p = paged_page(args.c, w.b, pos);
+      return p >= 0 ? p : args.c.num_pages;
+    };
+    auto load_tile = [&](uint32_t dst, const CUtensorMap* tm, int j, int page, uint32_t bar) {
+      if (lane == 0) mbar_expect_tx(bar, E4M3 ? L::kCodeBytes : L::kTileBytes);
+      __syncwarp();
+      if (lane < n_box) {
+        const int slot = (j * kTile + lane * box_rows) % args.c.page_size;
+        if constexpr (E4M3) {
+          tma_load_4d(dst + lane * box_rows * D, tm, 0, slot, w.h, page, bar);
+        } else {
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, slot, w.h, page, bar);
+        }
+      }
+      __syncwarp();
+    };
+    if (warp == kQkWarp || (!E4M3 && warp == kVWarp)) {
+      // ------------------------------------------------------------ producers
+      const bool is_k = warp == kQkWarp;
+      if (lane == 0) {
+        tma_prefetch_desc(is_k ? &tm_k : &tm_v);
+        if (is_k) tma_prefetch_desc(&tm_q);
+        if (E4M3) tma_prefetch_desc(&tm_v);
+      }
+      constexpr uint32_t kStages = E4M3 ? L::kCStages : L::kKStages;
+      static_assert(E4M3 || L::kKStages == L::kVStages, "one ring depth");
+      const BarRun full = E4M3 ? bars.c_full : (is_k ? bars.k_full : bars.v_full);
+      const BarRun empty = E4M3 ? bars.c_empty : (is_k ? bars.k_empty : bars.v_empty);
+      const uint32_t ring = E4M3 ? sC : (is_k ? sK : sV);
+      uint32_t it = 0, s = 0, ph = 1, q_armed = 0, tails = 0;
+      bool ok = true;
+      const uint32_t q_bytes = static_cast<uint32_t>(L::kChunks * G * tt * 128);
+      do {
+        if (is_k) {
+          if (q_armed > 0 && !mbar_wait_warp(bars.q_empty, (q_armed - 1) & 1, tmo, abort_flag)) {
+            fail();
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            mbar_expect_tx(bars.q_full, q_bytes);
+            for (int c = 0; c < L::kChunks; ++c)
+              tma_load_3d(sQ + c * 16384, &tm_q, c * 64, w.h * G, w.s.t0 + w.qt * tt, bars.q_full);
+          }
+          ++q_armed;
+        }
+        int page = w.nt > 0 ? box_page(w.j0) : 0;
+        for (int i = 0; i < w.nt && ok; ++i) {
+          const int j = w.j0 + i;
+          const int next_page = i + 1 < w.nt ? box_page(j + 1) : 0;  // ahead of the wait
+          for (int kv = 0; kv < (E4M3 ? 2 : 1); ++kv) {
+            if (!mbar_wait_warp(empty[s], ph, tmo, abort_flag)) {
+              fail();
+              ok = false;
+              break;
+            }
+            const uint32_t dst = ring + s * (E4M3 ? L::kCodeBytes : L::kTileBytes);
+            const int valid = w.s.len - j * kTile;
+            if (!E4M3 && !is_k && valid < kTile) {
+              // V's last tile: rows of its last page behind the sequence may hold anything
+              load_tile(dst, &tm_v, j, page, bars.v_tail);
+              ++tails;
+              if (!mbar_wait_warp(bars.v_tail, (tails - 1) & 1, tmo, abort_flag)) {
+                fail();  // the drain below waits for the load
+                ok = false;
+                break;
+              }
+              const int end = (valid + box_rows - 1) / box_rows * box_rows;
+              for (int x = valid * 8 + lane; x < end * 8; x += 32)
+                for (int c = 0; c < L::kChunks; ++c)
+                  st_shared_v4(dst + c * 16384 + x * 16, 0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(full[s]);
+            } else {
+              load_tile(dst, (E4M3 ? kv == 0 : is_k) ? &tm_k : &tm_v, j, page, full[s]);
+            }
+            ++it;
+            if (++s == kStages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          page = next_page;
+        }
+      } while (ok && w.next(args, tt));
+      // Drain: every load this warp issued must land before the CTA exits. Stage x was armed
+      // for ring positions x, x + kStages, ...; wait for the last one.
+      if (tails > 0) mbar_wait_warp(bars.v_tail, (tails - 1) & 1, tmo, nullptr);
+      for (uint32_t x = 0; x < kStages; ++x)
+        if (it > x) mbar_wait_warp(full[x], ((it - 1 - x) / kStages) & 1, tmo, nullptr);
+      if (q_armed) mbar_wait_warp(bars.q_full, (q_armed - 1) & 1, tmo, nullptr);
+    } else if (warp == kSIssuer) {
+      // ------------------------------------------------------------ S issuer
+      if (lane == 0) {
+        constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0, 0);  // S = Q K^T, both K-major
+        constexpr uint64_t kStep = static_cast<uint64_t>(L::kTileBytes >> 4);
+        const uint64_t dQ = sdesc_sw128(sQ, 16, 1024);
+        const uint64_t dK0 = sdesc_sw128(sK, 16, 1024);
+        uint32_t s = 0, ph = 0, sf0 = 0, sf1 = 0;
+        bool seen0 = false, seen1 = false;
+        bool ok = true;
+        // Test hook: this barrier is never completed, so the bounded wait runs out.
+        if (args.sync.inject_stall && !mbar_wait(bars.stall, 0, tmo, abort_flag)) {
+          fail();
+          ok = false;
+        }
+        int count = 0;
+        while (ok) {
+          // The tensor core runs products in issue order: the next piece's S products wait
+          // until this piece's last PV has been issued, so that they do not delay it.
+          bool ready = *pv_units >= count;
+          if (!ready) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!(ready = *pv_units >= count)) {
+              if (*abort_flag || globaltimer_ns() - t0 > tmo) break;
+              __nanosleep(64);
+            }
+          }
+          if (!ready || !mbar_wait(bars.q_full, count & 1, tmo, abort_flag)) {
+            fail();
+            break;
+          }
+          for (int p = 0; p < w.nt; ++p) {
+            const int g = p & 1;
+            if (!mbar_wait(bars.k_full[s], ph, tmo, abort_flag)) {
+              ok = false;
+              break;
+            }
+            // S_g is free once its warpgroup has read the previous S_g.
+            if (g == 0) {
+              if (seen0 && !mbar_wait(bars.s_free[0], sf0++ & 1, tmo, abort_flag)) {
+                ok = false;
+                break;
+              }
+              seen0 = true;
+            } else {
+              if (seen1 && !mbar_wait(bars.s_free[1], sf1++ & 1, tmo, abort_flag)) {
+                ok = false;
+                break;
+              }
+              seen1 = true;
+            }
+            tc_fence_after();
+            const uint64_t dk = dK0 + static_cast<uint64_t>(s) * kStep;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+              mma_ss(tmem + L::col_s(g), dQ + off, dk + off, kIdS, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(bars.s_full[g]);
+            mma_commit(bars.k_empty[s]);
+            if (++s == L::kKStages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          if (!ok) {
+            fail();
+            break;
+          }
+          mma_commit(bars.q_empty);  // Q may be replaced once these S products are done
+          ++count;
+          if (!w.next(args, tt)) break;
+        }
+        // Drain: all issued MMAs must finish before tensor memory is released.
+        mma_commit(bars.drain);
+        mbar_wait(bars.drain, 0, tmo, nullptr);
+      }
+      __syncwarp();
+    } else if (warp == kPvIssuer) {
+      // ------------------------------------------------------------ PV issuer
+      if (lane == 0) {
+        constexpr uint32_t kIdPV = idesc_bf16_f32(128, D, 0, 1);  // P K-major, V MN-major
+        constexpr uint64_t kStep = static_cast<uint64_t>(L::kTileBytes >> 4);
+        constexpr uint64_t kPStep = static_cast<uint64_t>(L::kPBytes >> 4);
+        const uint64_t dP0 = sdesc_sw128(sP, 16, 1024);
+        const uint64_t dV0 = sdesc_sw128(sV, 16384, 1024);
+        uint32_t s = 0, ph = 0, pc0 = 0, pc1 = 0;
+        bool ok = true;
+        int count = 0;
+        while (ok) {
+          // The first PV of a piece overwrites O_0 or O_1, which the previous piece's
+          // epilogue reads: it waits for that epilogue (o_free).
+          bool first_any = true, first0 = true, first1 = true;
+          for (int p = 0; p < w.nt; ++p) {
+            const int g = p & 1;
+            const uint32_t pc = g ? pc1 : pc0;
+            if (!mbar_wait(bars.v_full[s], ph, tmo, abort_flag) ||
+                !mbar_wait(bars.p_full[g], pc & 1, tmo, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (g) ++pc1; else ++pc0;
+            if (first_any) {
+              if (count > 0 && !mbar_wait(bars.o_free, (count - 1) & 1, tmo, abort_flag)) {
+                ok = false;
+                break;
+              }
+              mbar_arrive(bars.o_free);
+              first_any = false;
+            }
+            tc_fence_after();
+            const bool first = g ? first1 : first0;
+            const uint64_t dp = dP0 + static_cast<uint64_t>(g) * kPStep;
+            const uint64_t dv = dV0 + static_cast<uint64_t>(s) * kStep;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk) {
+              const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+              mma_ss(tmem + L::col_o(g), dp + off, dv + static_cast<uint64_t>((kk * 2048) >> 4),
+                     kIdPV, (first && kk == 0) ? 0u : 1u);
+            }
+            if (g) first1 = false; else first0 = false;
+            mma_commit(bars.pv_done[g]);
+            mma_commit(bars.v_empty[s]);
+            if (++s == L::kVStages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          // A piece without any PV still consumes the previous epilogue's handshake and
+          // adds its own arrival.
+          if (ok && first_any) {
+            if (count > 0 && !mbar_wait(bars.o_free, (count - 1) & 1, tmo, abort_flag))
+              ok = false;
+            else
+              mbar_arrive(bars.o_free);
+          }
+          if (!ok) {
+            fail();
+            break;
+          }
+          *pv_units = ++count;  // this piece's PVs are all issued
+          if (!w.next(args, tt)) break;
+        }
+        mma_commit(bars.drain2);
+        mbar_wait(bars.drain2, 0, tmo, nullptr);
+      }
+      __syncwarp();
+    } else if (E4M3 && warp >= kConvWarp) {
+      // ------------------------------------------------------------ converters
+      // Warp x takes rows 32 x .. 32 x + 31 of every tile. A lane reads 16 codes of a row in
+      // two 8-byte halves, in an order that keeps the lanes of a load, and then the 16-byte
+      // units of a store, on different banks.
+      const int r0 = (warp - kConvWarp) * 32;
+      constexpr int kLanes = D / 16;          // lanes per row
+      constexpr int kRowsPer = 32 / kLanes;   // rows per pass
+      const int u = lane % kLanes;
+      uint32_t cs = 0, cph = 0, ks = 0, kph = 1, vs = 0, vph = 1;
+      bool ok = true;
+      // scale bytes of this lane's row (row r0 + lane) of K and V in tile j; 0, for which a
+      // code of zero gives zero, where there is no row
+      auto scale_of = [&](int j, uint32_t& k_byte, uint32_t& v_byte) {
+        const int pos = j * kTile + r0 + lane;
+        k_byte = v_byte = 0u;
+        if (pos < w.s.len) {
+          const int page = paged_page(args.c, w.b, pos);
+          if (page >= 0) {
+            const long long at = (static_cast<long long>(page) * args.c.Hkv + w.h) * args.c.page_size +
+                                 pos % args.c.page_size;
+            k_byte = args.c.k_scale[at];
+            v_byte = args.c.v_scale[at];
+          }
+        }
+      };
+      do {
+        uint32_t kb = 0, vb = 0;
+        if (w.nt > 0) scale_of(w.j0, kb, vb);
+        for (int i = 0; i < w.nt && ok; ++i) {
+          const int j = w.j0 + i;
+          const int valid = w.s.len - j * kTile;  // rows of the tile that the cache holds
+          uint32_t nkb = 0, nvb = 0;
+          if (i + 1 < w.nt) scale_of(j + 1, nkb, nvb);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t factor = e4m3_factor(static_cast<int>(kv ? vb : kb));
+            if (!mbar_wait_warp(bars.c_full[cs], cph, tmo, abort_flag) ||
+                !mbar_wait_warp(kv ? bars.v_empty[vs] : bars.k_empty[ks], kv ? vph : kph, tmo,
+                                abort_flag)) {
+              fail();
+              ok = false;
+              break;
+            }
+            const uint32_t src = sC + cs * L::kCodeBytes;
+            const uint32_t dst = (kv ? sV + vs * L::kTileBytes : sK + ks * L::kTileBytes) +
+                                 (u >> 2) * 16384;
+#pragma unroll
+            for (int x = 0; x < kLanes; ++x) {
+              const int rr = x * kRowsPer + lane / kLanes;  // row within the warp's 32
+              const int row = r0 + rr;
+              const uint32_t f = __shfl_sync(0xffffffffu, factor, rr);
+              const uint32_t flip = D == 128 ? ((u >> 2) ^ (row & 1)) : ((row >> 1) & 1);
+              const uint32_t line = dst + row * 128;
+#pragma unroll
+              for (uint32_t y = 0; y < 2; ++y) {
+                const uint32_t half = y ^ flip;
+                uint32_t c0, c1;
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                             : "=r"(c0), "=r"(c1)
+                             : "r"(src + row * D + u * 16 + half * 8)
+                             : "memory");
+                // behind the sequence a page may hold any code
+                if (row >= valid) c0 = c1 = 0u;
+                const uint32_t v = (u & 3) * 2 + half;  // 16-byte unit of the 128-byte line
+                st_shared_v4(line + ((v ^ (row & 7)) << 4), e4m3_lo(c0, f), e4m3_hi(c0, f),
+                             e4m3_lo(c1, f), e4m3_hi(c1, f));
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bars.c_empty[cs]);
+              mbar_arrive(kv ? bars.v_full[vs] : bars.k_full[ks]);
+            }
+            if (++cs == L::kCStages) {
+              cs = 0;
+              cph ^= 1u;
+            }
+            if (kv) {
+              if (++vs == L::kVStages) {
+                vs = 0;
+                vph ^= 1u;
+              }
+            } else if (++ks == L::kKStages) {
+              ks = 0;
+              kph ^= 1u;
+            }
+          }
+          kb = nkb;
+          vb = nvb;
+        }
+      } while (ok && w.next(args, tt));
+    }
+  } else {
+    regs_inc<L::kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax
+    const int g = warp >> 2;                 // warpgroup: key tiles at positions p, p % 2 == g
+    const int quad = warp & 3;               // tensor-memory lane quadrant of this warp
+    const int t = quad * 32 + lane;          // row within the query tile
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_base + L::col_s(g);
+    const uint32_t tO = tmem + lane_base + L::col_o(g);
+    const uint32_t g_magic = (65536u + static_cast<uint32_t>(G) - 1u) / static_cast<uint32_t>(G);
+    // r / G for r < 128, G <= 128: the excess r / 65536 of the product stays below 1 / G
+    auto token_of = [&](int r) { return static_cast<int>((static_cast<uint32_t>(r) * g_magic) >> 16); };
+    // This row of P_g, with the row's swizzle phase (t mod 8) in address bits 4-6:
+    // 16-byte unit v of the row then sits at prow ^ (v << 4).
+    const uint32_t prow = sP + static_cast<uint32_t>(g * L::kPBytes + t * 128 + ((t & 7) << 4));
+    float2* xch = reinterpret_cast<float2*>(smem + L::kXchOff);
+    const float c_log2 = args.scale_log2;
+    uint32_t s_cnt = 0, pv_cnt = 0;
+    bool ok = true;
+    int count = 0;
+    PieceHeader left = {-1, 0, 1, 0};
+    do {
+      // keys [key_lo, key_hi) are visible to this row
+      int key_lo = 0, key_hi = w.s.len;
+      {
+        const int pos = w.s.len - w.s.nq + w.qt * tt + token_of(t);
+        if (args.causal && pos + 1 < key_hi) key_hi = pos + 1;
+        if (args.wl >= 0) key_lo = pos - args.wl;
+      }
+      float m_ref = -INFINITY;  // reference maximum, scaled log2 units
+      float l_sum = 0.f;        // running sum of exp2(s*c - m_ref)
+      int n_done = 0;           // key tiles of this warpgroup
+      for (int p = g; p < w.nt; p += 2) {
+        const int k0 = (w.j0 + p) * kTile;
+        if (!mbar_wait_warp(bars.s_full[g], s_cnt & 1, tmo, abort_flag)) {
+          fail();
+          ok = false;
+          break;
+        }
+        ++s_cnt;
+        tc_fence_after();
+        uint32_t sr[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, &sr[c * 32]);
+        tmem_ld_wait();
+        // S is in registers: the next S of this warpgroup may be written over it.
+        tc_fence_before();
+        mbar_arrive(bars.s_free[g]);
+        float s[128];
+#pragma unroll
+        for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(sr[k]);
+        if (k0 < key_lo || k0 + kTile > key_hi) mask_row(s, key_lo - k0, key_hi - k0);
+        // Row maximum: three-input max over eight independent accumulators.
+        float mx[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx[k] = fmaxf(s[2 * k], s[2 * k + 1]);
+#pragma unroll
+        for (int k = 16; k < 128; k += 16)
+#pragma unroll
+          for (int a = 0; a < 8; ++a) mx[a] = fmax3(mx[a], s[k + 2 * a], s[k + 2 * a + 1]);
+        const float mx_row =
+            fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+        const float m_new = fmaxf(m_ref, mx_row * c_log2);
+        const bool grow = m_new > m_ref + kRescale;
+        float alpha = 1.f;
+        if (grow) {
+          alpha = ex2_approx(m_ref - m_new);  // 0 when m_ref = -inf
+          l_sum *= alpha;
+          m_ref = m_new;
+        }
+        const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+        const uint64_t c2 = f2_pack(c_log2, c_log2);
+        const uint64_t nm2 = f2_pack(-m_use, -m_use);
+        uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // four packed partial sums
+        uint32_t pk[64];
+        bool pv_ok = true;
+        bool stored0 = false;  // first half already in P_g
+        // 128-byte swizzle: 16-byte unit v of the row's 64-key half h at v ^ (t & 7)
+        auto store_half = [&](int h) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            st_shared_v4((prow ^ static_cast<uint32_t>(v << 4)) + static_cast<uint32_t>(h * 16384),
+                         pk[h * 32 + 4 * v], pk[h * 32 + 4 * v + 1], pk[h * 32 + 4 * v + 2],
+                         pk[h * 32 + 4 * v + 3]);
+        };
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            const int k = half * 64 + e;
+            float y0, y1;
+            f2_unpack(f2_fma(f2_pack(s[k], s[k + 1]), c2, nm2), y0, y1);
+            const float p0 = ex2_approx(y0);
+            const float p1 = ex2_approx(y1);
+            rs2[(e >> 1) & 3] = f2_add(rs2[(e >> 1) & 3], f2_pack(p0, p1));
+            // P is rounded to bf16 for the product (at most 2^-8 of each weight); l keeps fp32
+            pk[half * 32 + (e >> 1)] = pack_bf16x2(p0, p1);
+          }
+          if (half == 0) {
+            // The first half goes out now if the previous PV (which reads P_g) has already
+            // completed; otherwise the second half's exponentials come first.
+            const bool ready =
+                n_done == 0 ||
+                __all_sync(0xffffffffu, mbar_test_wait(bars.pv_done[g], pv_cnt & 1));
+            if (ready) {
+              if (n_done > 0) {
+                ++pv_cnt;
+                tc_fence_after();
+              }
+              store_half(0);
+              stored0 = true;
+            }
+          } else {
+            if (!stored0) {
+              if (!mbar_wait_warp(bars.pv_done[g], pv_cnt & 1, tmo, abort_flag)) {
+                pv_ok = false;
+                break;
+              }
+              ++pv_cnt;
+              tc_fence_after();
+              store_half(0);
+            }
+            store_half(1);
+          }
+        }
+        if (!pv_ok) {
+          fail();
+          ok = false;
+          break;
+        }
+        {
+          const uint64_t t2 = f2_add(f2_add(rs2[0], rs2[1]), f2_add(rs2[2], rs2[3]));
+          float r0, r1;
+          f2_unpack(t2, r0, r1);
+          l_sum += r0 + r1;
+        }
+        // Rescale the O_g row in tensor memory (the previous PV has completed).
+        if (n_done > 0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(tO + c * 32, o);
+          }
+          tmem_st_wait();
+        }
+        // P_g's generic-proxy stores become visible to the tensor core's reads.
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bars.p_full[g]);
+        ++n_done;
+      }
+      if (!ok) break;
+      // ---- epilogue: merge the two warpgroups' partial softmaxes.
+      // This warpgroup's last PV has completed once its pv_done phase has.
+      if (n_done > 0) {
+        if (!mbar_wait_warp(bars.pv_done[g], pv_cnt & 1, tmo, abort_flag)) {
+          fail();
+          ok = false;
+          break;
+        }
+        ++pv_cnt;
+      }
+      // The exchange slots are reused once both warpgroups have finished the previous
+      // piece's epilogue (o_free completes after every read of them).
+      if (count > 0 && !mbar_wait_warp(bars.o_free, (count - 1) & 1, tmo, abort_flag)) {
+        fail();
+        ok = false;
+        break;
+      }
+      xch[g * kTile + t] = make_float2(m_ref, l_sum);
+      // The partner row (same lane quadrant, other warpgroup) arrives after its own last PV
+      // has completed, so both O_0 and O_1 are final past this wait.
+      mbar_arrive(bars.xbar[quad]);
+      if (!mbar_wait_warp(bars.xbar[quad], count & 1, tmo, abort_flag)) {
+        fail();
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float2 other = xch[(1 - g) * kTile + t];
+      const float m0 = g ? other.x : m_ref, l0 = g ? other.y : l_sum;
+      const float m1 = g ? m_ref : other.x, l1 = g ? l_sum : other.y;
+      const bool has0 = w.nt > 0, has1 = w.nt > 1;  // O_g was written
+      const float m = fmaxf(m0, m1);
+      const float a0 = (l0 > 0.f) ? ex2_approx(m0 - m) : 0.f;
+      const float a1 = (l1 > 0.f) ? ex2_approx(m1 - m) : 0.f;
+      const float l = a0 * l0 + a1 * l1;
+      const float inv = (l > 0.f) ? 1.f / l : 0.f;
+      const float w0 = a0 * inv, w1 = a1 * inv;
+      const float lse2 = (l > 0.f) ? m + __log2f(l) : -INFINITY;  // log2 units
+      const int tok0 = w.qt * tt;                                  // the tile's first token
+      const int rows = min(w.s.nq - tok0, tt) * G;                 // rows of the tile
+      const bool direct = w.from_start && w.ends;
+      // This warpgroup writes output columns [D/2 g, D/2 g + D/2) from both O_0 and O_1.
+      constexpr int kHalf = D / 2;
+      if (direct) {
+        // Each warp first puts its 32 rows x D bytes into shared memory (rows of P_g that it
+        // itself writes, free once its last PV has completed), then stores them so that
+        // neighbouring lanes cover whole rows.
+        constexpr int kUnits = kHalf / 8;  // 16-byte units of a row's half
+        const uint32_t stage = sP + static_cast<uint32_t>(g * L::kPBytes + quad * 4096);
+        const uint32_t srow = stage + static_cast<uint32_t>(lane * kHalf * 2);
+#pragma unroll
+        for (int c = 0; c < kHalf / 16; ++c) {  // 16 columns at a time (fewer live registers)
+          const uint32_t col = static_cast<uint32_t>(kHalf * g + 16 * c);
+          uint32_t o0[16], o1[16];
+          if (has0) tmem_ld16(tmem + lane_base + L::col_o(0) + col, o0);
+          if (has1) tmem_ld16(tmem + lane_base + L::col_o(1) + col, o1);
+          tmem_ld_wait();
+          uint32_t pk[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float v0 = 0.f, v1 = 0.f;
+            if (has0) {
+              v0 = __uint_as_float(o0[2 * k]) * w0;
+              v1 = __uint_as_float(o0[2 * k + 1]) * w0;
+            }
+            if (has1) {
+              v0 = fmaf(__uint_as_float(o1[2 * k]), w1, v0);
+              v1 = fmaf(__uint_as_float(o1[2 * k + 1]), w1, v1);
+            }
+            pk[k] = pack_bf16x2(v0, v1);
+          }
+          const uint32_t z = static_cast<uint32_t>(lane & (kUnits - 1));
+          st_shared_v4(srow + (((2 * c) ^ z) << 4), pk[0], pk[1], pk[2], pk[3]);
+          st_shared_v4(srow + (((2 * c + 1) ^ z) << 4), pk[4], pk[5], pk[6], pk[7]);
+        }
+        __syncwarp();
+        const int u = lane % kUnits;  // 16-byte unit of the row this lane stores
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+          const int r = i * (32 / kUnits) + lane / kUnits;  // row within the warp's 32
+          const uint4 val = ld_shared_v4(
+              stage + static_cast<uint32_t>(r * kHalf * 2 + ((u ^ (r & (kUnits - 1))) << 4)));
+          const int row = quad * 32 + r;
+          if (row < rows) {
+            const int tk = token_of(row);
+            const long long at = static_cast<long long>(w.s.t0 + tok0 + tk) * args.H + w.h * G +
+                                 (row - tk * G);
+            *reinterpret_cast<uint4*>(args.o + at * D + kHalf * g + 8 * u) = val;
+          }
+        }
+        if (t < rows && g == 0) {
+          const int tk = token_of(t);
+          args.lse[static_cast<long long>(w.s.t0 + tok0 + tk) * args.H + w.h * G + (t - tk * G)] =
+              lse2 * kLn2;
+        }
+      } else {
+        // a piece: normalised, fp32. Slot 0 continues what an earlier CTA began, slot 1 is
+        // continued by the next.
+        const long long at = (2ll * blockIdx.x + (w.from_start ? 1 : 0)) * kTile + t;
+#pragma unroll
+        for (int c = 0; c < kHalf / 16; ++c) {
+          const uint32_t col = static_cast<uint32_t>(kHalf * g + 16 * c);
+          uint32_t o0[16], o1[16];
+          if (has0) tmem_ld16(tmem + lane_base + L::col_o(0) + col, o0);
+          if (has1) tmem_ld16(tmem + lane_base + L::col_o(1) + col, o1);
+          tmem_ld_wait();
+          float y[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            y[k] = has0 ? __uint_as_float(o0[k]) * w0 : 0.f;
+            if (has1) y[k] = fmaf(__uint_as_float(o1[k]), w1, y[k]);
+          }
+          if (t < rows) {
+            float4* dst = reinterpret_cast<float4*>(args.o_part + at * D + col);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+          }
+        }
+        if (t < rows && g == 0) args.lse_part[at] = lse2;
+      }
+      if (!w.from_start) left.ended = w.ends;
+      if (w.from_start && !w.ends) {
+        left.b = w.b;
+        left.h = w.h;
+        left.qt = w.qt;
+      }
+      tc_fence_before();
+      mbar_arrive(bars.o_free);
+      ++count;
+    } while (w.next(args, tt));
+    if (tid == 0) headers[blockIdx.x] = left;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSIssuer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of the pieces of a query tile that runs' ends have cut, a warp per row: with lse_s
+// and the normalised O_s of piece s, O = sum_s 2^(lse_s - m) O_s / sum_s 2^(lse_s - m), m =
+// max_s lse_s, in the order of the pieces. Blocks (c, ..) take the tile that CTA c's run
+// began and did not end.
+constexpr int kMergeWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    fa_paged_chunk_merge_kernel(const PagedAttnArgs a, int ctas) {
+  constexpr int kPer = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x;
+  __shared__ int n_more;
+  pdl_wait();
+  const PieceHeader* headers = static_cast<const PieceHeader*>(a.headers);
+  const PieceHeader hd = headers[c];
+  if (hd.b < 0) return;
+  const PagedSeq s = paged_attn_seq(a.c, hd.b);
+  const int G = a.H / a.c.Hkv, tt = kTile / G;
+  const int tok0 = hd.qt * tt;
+  const int rows = min(s.nq - tok0, tt) * G;
+  const int r = blockIdx.y * kMergeWarps + warp;
+  if (static_cast<int>(blockIdx.y) * kMergeWarps >= rows) return;
+  const int n = 1 + pieces_after(headers, c, ctas, &n_more);  // slot 1 of c, slot 0 of the others
+  if (r >= rows) return;
+  auto row_of = [&](int i) { return (2ll * (c + i) + (i == 0 ? 1 : 0)) * kTile + r; };
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.lse_part[row_of(i)]);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  const float mu = m == -INFINITY ? 0.f : m;
+  float den = 0.f, acc[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const long long row = row_of(i);
+    const float x = ex2_approx(a.lse_part[row] - mu);
+    den += x;
+    const float* p = a.o_part + row * D + lane * kPer;
+    if constexpr (kPer == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      acc[0] += x * v.x;
+      acc[1] += x * v.y;
+      acc[2] += x * v.z;
+      acc[3] += x * v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(p);
+      acc[0] += x * v.x;
+      acc[1] += x * v.y;
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const int t = r / G;
+  const long long row = static_cast<long long>(s.t0 + tok0 + t) * a.H + hd.h * G + (r - t * G);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + row * D + lane * kPer);
+  dst[0] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if constexpr (kPer == 4) dst[1] = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+  if (lane == 0) a.lse[row] = den > 0.f ? (m + __log2f(den)) * kLn2 : -INFINITY;
+}
+
+namespace {
+
+template <int D, bool E4M3>
+cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                        const PagedAttnArgs& a, int box_rows, int ctas, cudaStream_t stream) {
+  using L = ChunkL<D, E4M3>;
+  auto kern = fa_paged_chunk_kernel<D, E4M3>;
+  // The in-kernel register reallocation assumes kRegsLaunch registers per thread at launch:
+  // with fewer, the softmax warpgroups' increase could never be granted and would wait
+  // forever, so such a kernel is refused.
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs < L::kRegsLaunch || attr.maxThreadsPerBlock < L::kThreads)
+    return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, L::kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, a, box_rows);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_merge(fa_paged_chunk_merge_kernel<D>, dim3(ctas, kTile / kMergeWarps),
+                      kMergeWarps * 32, stream, a, ctas);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const PagedAttnArgs& a, bool e4m3, int box_rows, int ctas,
+                               cudaStream_t stream) {
+  if (a.c.d == 64)
+    return e4m3 ? launch_impl<64, true>(tq, tk, tv, a, box_rows, ctas, stream)
+                : launch_impl<64, false>(tq, tk, tv, a, box_rows, ctas, stream);
+  return e4m3 ? launch_impl<128, true>(tq, tk, tv, a, box_rows, ctas, stream)
+              : launch_impl<128, false>(tq, tk, tv, a, box_rows, ctas, stream);
+}
+
+}  // namespace fa

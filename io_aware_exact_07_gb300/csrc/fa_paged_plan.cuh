@@ -1,0 +1,76 @@
+// How the kernels of paged attention divide a batch among their CTAs: the list of (work
+// unit, key block) places is cut into equal runs, by the lengths found on the device. A unit
+// cut by a run's end leaves pieces: slot 1 of the CTA where it began, slot 0 of those where
+// it went on.
+#pragma once
+#include "fa_paged.h"
+
+namespace fa {
+
+// Sum over the block's threads of x, and the sum of those before this one.
+template <int WARPS>
+__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums,
+                                                long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();  // earlier readers of warp_sums are done
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const long long y = warp_sums[w];
+    if (w < warp) before += y;
+    all += y;
+  }
+  *total = all;
+  return before + inc - x;
+}
+
+// What a CTA leaves for the merge: the unit that its run began and did not end (b < 0:
+// none), and whether a unit that it did not begin ended in its run (or there was none).
+struct PieceHeader {
+  int b, h, ended, qt;
+};
+
+// Number of CTAs after CTA c that hold further pieces of the unit begun there: up to the
+// first one in which it ended. Called by the whole block.
+__device__ __forceinline__ int pieces_after(const PieceHeader* headers, int c, int ctas, int* shared) {
+  if (threadIdx.x == 0) *shared = ctas - 1 - c;
+  __syncthreads();
+  for (int i = c + 1 + static_cast<int>(threadIdx.x); i < ctas; i += static_cast<int>(blockDim.x))
+    if (headers[i].ended != 0) {
+      atomicMin(shared, i - c);
+      break;
+    }
+  __syncthreads();
+  return *shared;
+}
+
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches the merge of a kernel just launched on `stream`. It may be scheduled while that
+// one runs; its blocks wait for its end (pdl_wait) before they read anything.
+template <typename... P, typename... A>
+cudaError_t launch_merge(void (*kern)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace fa

@@ -20,7 +20,7 @@
 //    the lengths found on the device. A head that falls into one run is written directly;
 //    one cut by a run's end leaves normalised pieces, merged by a second, small kernel with
 //    the two-block rule of the online softmax.
-#include "fa_paged.h"
+#include "fa_paged_plan.cuh"
 
 namespace fa {
 
@@ -162,29 +162,6 @@ struct Walk {
   }
 };
 
-// Sum over the block's threads, and the exclusive prefix of each.
-__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long inc = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  __syncthreads();  // earlier readers of warp_sums are done
-  if (lane == 31) warp_sums[warp] = inc;
-  __syncthreads();
-  long long before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const long long y = warp_sums[w];
-    if (w < warp) before += y;
-    all += y;
-  }
-  *total = all;
-  return before + inc - x;
-}
-
 }  // namespace
 
 template <int D, bool E4M3, int NT>
@@ -194,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, c4 = lane & 3;
   const int G = a.H / a.c.Hkv;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_launch_dependents();
 
   // ---- this CTA's run [lo, hi) of the list
   struct Plan {
@@ -213,15 +190,15 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
     const long long x = weight(b0 + tid);
     if (b0 == 0) x0 = x;
     long long sum;
-    block_scan(x, plan->warp_sums, &sum);
+    block_scan<kWarps>(x, plan->warp_sums, &sum);
     total += sum;
   }
   const long long per = (total + gridDim.x - 1) / gridDim.x;
   const long long lo = per * blockIdx.x;
   const long long hi = lo + per < total ? lo + per : total;
-  int4* headers = reinterpret_cast<int4*>(a.headers);
+  PieceHeader* headers = static_cast<PieceHeader*>(a.headers);
   if (lo >= hi) {
-    if (tid == 0) headers[blockIdx.x] = make_int4(-1, 0, 1, 0);
+    if (tid == 0) headers[blockIdx.x] = PieceHeader{-1, 0, 1, 0};
     return;
   }
   {
@@ -229,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
     for (int b0 = 0; b0 < a.c.B && base <= lo; b0 += kThreads) {
       const long long x = b0 == 0 ? x0 : weight(b0 + tid);
       long long sum;
-      const long long at = base + block_scan(x, plan->warp_sums, &sum);
+      const long long at = base + block_scan<kWarps>(x, plan->warp_sums, &sum);
       if (at <= lo && lo < at + x) {
         const long long n = x / a.c.Hkv;
         plan->b = b0 + tid;
@@ -589,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
     cw = nw;
   }
   cp_async_wait<0>();
-  if (tid == 0) headers[blockIdx.x] = make_int4(slot1_b, slot1_h, !starts_mid || ended0, 0);
+  if (tid == 0) headers[blockIdx.x] = PieceHeader{slot1_b, slot1_h, !starts_mid || ended0, 0};
 }
 
 // Merge of the pieces of a head that runs' ends have cut: with lse_s and the normalised O_s
@@ -605,22 +582,14 @@ __global__ void __launch_bounds__(kThreads) fa_paged_step_merge_kernel(const Pag
   __shared__ int n_more;
   __shared__ float mx[kWarps], dens[kWarps];
   __shared__ float acc_s[kWarps][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4* headers = reinterpret_cast<const int4*>(a.headers);
-  const int4 hd = headers[c];
-  if (hd.x < 0) return;
-  const PagedSeq s = paged_attn_seq(a.c, hd.x);
+  pdl_wait();
+  const PieceHeader* headers = static_cast<const PieceHeader*>(a.headers);
+  const PieceHeader hd = headers[c];
+  if (hd.b < 0) return;
+  const PagedSeq s = paged_attn_seq(a.c, hd.b);
   const int G = a.H / a.c.Hkv;
   if (r >= s.nq * G) return;
-  if (tid == 0) n_more = ctas - 1 - c;
-  __syncthreads();
-  for (int i = c + 1 + tid; i < ctas; i += kThreads)
-    if (headers[i].z != 0) {
-      atomicMin(&n_more, i - c);
-      break;
-    }
-  __syncthreads();
-  const int n = 1 + n_more;  // pieces: slot 1 of CTA c, slot 0 of the n - 1 after it
+  const int n = 1 + pieces_after(headers, c, ctas, &n_more);  // pieces: slot 1 of CTA c, slot 0 of the n - 1 after it
   auto row_of = [&](int i) { return (2ll * (c + i) + (i == 0 ? 1 : 0)) * rows + r; };
   float m = -INFINITY;
   for (int i = tid; i < n; i += kThreads) m = fmaxf(m, a.lse_part[row_of(i)]);
@@ -664,7 +633,7 @@ __global__ void __launch_bounds__(kThreads) fa_paged_step_merge_kernel(const Pag
       l += dens[w];
     }
     const int t = r / G;
-    const long long row = static_cast<long long>(s.t0 + t) * a.H + hd.y * G + (r - t * G);
+    const long long row = static_cast<long long>(s.t0 + t) * a.H + hd.h * G + (r - t * G);
     a.o[row * D + tid] = __float2bfloat16(l > 0.f ? y / l : 0.f);
     if (tid == 0) a.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
   }
@@ -681,18 +650,8 @@ cudaError_t launch_impl(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   kern<<<ctas, kThreads, L::kSmemBytes, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // The merge may be scheduled while the step runs; its blocks wait for the step's end
-  // before they read anything.
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (a.H / a.c.Hkv) * a.c.max_q);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_paged_step_merge_kernel<D>, a, ctas, L::kRows);
+  return launch_merge(fa_paged_step_merge_kernel<D>, dim3(ctas, (a.H / a.c.Hkv) * a.c.max_q),
+                      kThreads, stream, a, ctas, int(L::kRows));
 }
 
 template <int D, bool E4M3>
