@@ -795,7 +795,7 @@ struct PagedWorkspace {
 static PagedWorkspace paged_workspace(int G, int d, int max_q, int num_sms) {
   PagedWorkspace w;
   const long long rows = static_cast<long long>(G) * max_q;
-  w.ctas = num_sms;
+  w.ctas = num_sms < 256 ? num_sms : 256;  // the chunk kernel plans with a thread per CTA
   w.rows = rows <= 8 ? 8 : rows <= fa::kStepRows ? fa::kStepRows : fa::kTile;
   const size_t slots = 2 * static_cast<size_t>(w.ctas) * w.rows;
   w.lse_off = round256(static_cast<size_t>(w.ctas) * 16);
@@ -846,11 +846,15 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
   a.H = H;
+  a.G = H / H_kv;
+  a.tt = fa::kTile / a.G;
+  a.g_magic = (65536u + static_cast<unsigned>(a.G) - 1u) / static_cast<unsigned>(a.G);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   a.scale_log2 = scale * fa::kLog2e;
   a.causal = causal ? 1 : 0;
   a.wl = window_left;
+  a.sync = fa::SyncParams{};
   const bool e4m3 = type == FA_CACHE_E4M3;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -858,11 +862,10 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
     e = fa::launch_paged_step(a, e4m3, w.ctas, cs);
   } else {
     a.sync = make_sync(di, kStallForward);
-    const int G = H / H_kv;
     int box = 128;  // rows of a page that a key tile can take at once
     while (page_size % box != 0) box /= 2;
     CUtensorMap tq, tk, tv;
-    if (!encode_map_tokens(&tq, q, T, H, d, q_stride, G, fa::kTile / G) ||
+    if (!encode_map_tokens(&tq, q, T, H, d, q_stride, a.G, a.tt) ||
         !encode_map_pages(&tk, k_pages, a.c, e4m3, box) ||
         !encode_map_pages(&tv, v_pages, a.c, e4m3, box))
       return FA_ERR_CUDA;

@@ -126,6 +126,12 @@ __device__ __forceinline__ uint32_t e4m3_hi(uint32_t w, uint32_t factor) {
   return mul_bf16x2(e4m3_bits(prmt(w, 0u, 0x3424u)), factor);
 }
 
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t saddr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(saddr) : "memory");
+  return r;
+}
+
 struct PagedWriteArgs {
   PagedArgs c;
   const __nv_bfloat16* k_new;   // token t at t * k_stride, heads and d contiguous
@@ -143,6 +149,8 @@ struct PagedAttnArgs {
   const __nv_bfloat16* q;       // token t at t * q_stride, [H, d] contiguous
   long long q_stride;
   int H;
+  int G, tt;                    // H / Hkv; tokens of a 128-row query tile, 128 / G
+  unsigned g_magic;             // ceil(2^16 / G): r / G = r * g_magic >> 16 for r < 128
   __nv_bfloat16* o;             // [T, H, d]
   float* lse;                   // [T, H]
   float scale_log2;             // scale * log2(e)

@@ -5,10 +5,10 @@
 //
 // A query tile is 128 rows of one K/V head: TT = 128 / G tokens times the G = H / Hkv heads
 // that read it (row r = t * G + g), so that K and V are read once for all of them. The list
-// of (sequence, K/V head, query tile, 128-key tile) places is cut into equal runs, one per
-// CTA (one CTA per SM): chunks of any lengths keep all SMs equally busy, and few query tiles
-// over a long cache are split along the keys. A query tile cut by a run's end leaves
-// normalised pieces for the merge kernel.
+// of (sequence, K/V head, query tile, 128-key tile) places is divided equally among the CTAs
+// (one per SM) by the lengths found on the device: chunks of any lengths keep all SMs busy,
+// and few query tiles over a long cache are split along the keys. A query tile that is cut
+// leaves normalised pieces for the merge kernel.
 //
 // Roles of a CTA (the head-dimension-128 forward's shape, here for 64 too):
 //   warps 0-3, 4-7  softmax warpgroups g = 0, 1: key tiles at even and odd positions of a
@@ -48,8 +48,8 @@ struct ChunkL {
   static constexpr int kThreads = kWarps * 32;
   // Registers per thread at launch, and as the warpgroups share them out afterwards.
   static constexpr int kRegsLaunch = E4M3 ? 128 : 168;
-  static constexpr int kRegsSoftmax = E4M3 ? 184 : 200;
-  static constexpr int kRegsAux = E4M3 ? 72 : 96;
+  static constexpr int kRegsSoftmax = E4M3 ? 192 : 216;
+  static constexpr int kRegsAux = E4M3 ? 64 : 72;
   static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsAux <= kThreads * kRegsLaunch,
                 "register reallocation exceeds the block's launch allocation");
   static constexpr int kTileBytes = kTile * D * 2;   // a 128 x D bf16 tile
@@ -107,48 +107,103 @@ __device__ __forceinline__ Tiles tiles_of(const PagedAttnArgs& a, const PagedSeq
   return r;
 }
 
-// A CTA's run: units one after another, cut at its ends. Every role walks the same run.
-struct Walk {
+// A place in the list of units (sequence, K/V head, query tile).
+struct Unit {
   int b, h, qt, n_qt;
-  int at;            // place in the unit at which the piece begins
-  long long left;    // places left in the run
   PagedSeq s;
-  Tiles u;
+  __device__ __forceinline__ void seq(const PagedAttnArgs& a) {
+    s = paged_attn_seq(a.c, b);
+    n_qt = (s.nq + a.tt - 1) / a.tt;
+  }
+  // The first unit of the batch (b = B if it has none).
+  __device__ __forceinline__ void first(const PagedAttnArgs& a) {
+    h = qt = n_qt = 0;
+    for (b = 0; b < a.c.B; ++b) {
+      seq(a);
+      if (n_qt > 0) return;
+    }
+  }
+  // k units further on; b = B past the end.
+  __device__ __forceinline__ void advance(const PagedAttnArgs& a, int k) {
+    if (b >= a.c.B) return;
+    long long at = static_cast<long long>(h) * n_qt + qt + k;
+    while (at >= static_cast<long long>(n_qt) * a.c.Hkv) {
+      at -= static_cast<long long>(n_qt) * a.c.Hkv;
+      if (++b >= a.c.B) return;
+      seq(a);
+    }
+    h = static_cast<int>(at / n_qt);
+    qt = static_cast<int>(at - static_cast<long long>(h) * n_qt);
+  }
+};
+
+// A CTA's work, piece by piece; every role walks the same one. First `rounds` whole units,
+// gridDim.x apart in the list, so that neighbouring CTAs take neighbouring query tiles of a
+// head at the same time and share its K/V tiles in L2; then a run of the places behind
+// those, cut where it begins and ends. The run's first unit, if another CTA began it, comes
+// last: where runs are shorter than a unit, all CTAs then begin at a head's first key and
+// differ by one jump only, so that at any time they read a head at two places, not at as
+// many as there are CTAs. (16 query tiles of 512 key tiles each over 8 heads: with runs in
+// the list's order alone K and V, 268 MB, came from HBM once per query tile, at 7 TB/s.)
+struct Walk {
+  Unit u;
+  int rounds;                        // whole units left
+  bool in_round, in_run;
+  int run_b, run_h, run_qt, run_at;  // where the run begins: run_at places into that unit
+  int tail;                          // places of that unit kept for last
+  long long left;                    // places of the run left
   // the current piece
-  int j0, nt;        // its key tiles: j0, j0 + 1, ..., nt of them
+  int j0, nt;                        // its key tiles: j0, j0 + 1, ..., nt of them
   bool from_start, ends;
 
-  __device__ __forceinline__ void seq(const PagedAttnArgs& a, int tt) {
-    s = paged_attn_seq(a.c, b);
-    n_qt = (s.nq + tt - 1) / tt;
-  }
-  __device__ __forceinline__ void piece(const PagedAttnArgs& a, int tt) {
-    u = tiles_of(a, s, tt, qt);
-    const int take = left < u.n - at ? static_cast<int>(left) : u.n - at;
-    j0 = u.jf + at;
-    const int end = u.jf + u.nr;
-    nt = min(j0 + take, end) - j0;
-    if (nt < 0) nt = 0;
+  __device__ __forceinline__ int piece(const PagedAttnArgs& a, int at, long long most) {
+    const Tiles t = tiles_of(a, u.s, a.tt, u.qt);
+    const int take = most < t.n - at ? static_cast<int>(most) : t.n - at;
+    j0 = t.jf + at;
+    nt = max(0, min(j0 + take, t.jf + t.nr) - j0);
     from_start = at == 0;
-    ends = at + take == u.n;
-    left -= take;
+    ends = at + take == t.n;
+    return take;
   }
-  // Next piece; false at the end of the run.
-  __device__ __forceinline__ bool next(const PagedAttnArgs& a, int tt) {
-    if (left <= 0) return false;
-    at = 0;
-    if (++qt == n_qt) {
-      qt = 0;
-      if (++h == a.c.Hkv) {
-        h = 0;
-        do {
-          if (++b >= a.c.B) return false;
-          seq(a, tt);
-        } while (n_qt == 0);
+  __device__ __forceinline__ void to_run(const PagedAttnArgs& a) {
+    u.b = run_b;
+    u.h = run_h;
+    u.qt = run_qt;
+    u.seq(a);
+  }
+  // Next piece; false when there is none.
+  __device__ __forceinline__ bool next(const PagedAttnArgs& a) {
+    if (rounds > 0) {
+      if (in_round) u.advance(a, static_cast<int>(gridDim.x));
+      in_round = true;
+      --rounds;
+      piece(a, 0, 0x7FFFFFFF);
+      return true;
+    }
+    if (left > 0) {
+      if (in_run) {
+        u.advance(a, 1);
+      } else {
+        in_run = true;
+        to_run(a);
+        if (run_at > 0) {
+          tail = piece(a, run_at, left);
+          left -= tail;
+          if (left > 0) u.advance(a, 1);
+        }
+      }
+      if (left > 0) {
+        left -= piece(a, 0, left);
+        return true;
       }
     }
-    piece(a, tt);
-    return true;
+    if (tail > 0) {
+      to_run(a);
+      piece(a, run_at, tail);
+      tail = 0;
+      return true;
+    }
+    return false;
   }
 };
 
@@ -190,25 +245,26 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int G = args.H / args.c.Hkv;
-  const int tt = kTile / G;  // tokens of a query tile
 
   // ---- this CTA's run of the list
   struct Plan {
     long long warp_sums[L::kWarps];
-    long long rem;
-    int b, h, qt, at;
+    long long rem, lo, hi;
+    int b, h, qt, at;    // where the run begins
+    int b0, h0, qt0;     // the first whole unit
   };
   static_assert(sizeof(Plan) <= 2 * kTile * 8, "plan scratch");
   Plan* plan = reinterpret_cast<Plan*>(smem + L::kPlanOff);
   // Places of one K/V head of sequence b; long chunks are summed by the whole warp.
+  bool many = false;  // a sequence seen by this thread has several query tiles per head
   auto head_places = [&](int b) -> long long {
     PagedSeq s = {0, 0, 0};
     if (b < args.c.B) s = paged_attn_seq(args.c, b);
-    const int n_qt = (s.nq + tt - 1) / tt;
+    const int n_qt = (s.nq + args.tt - 1) / args.tt;
+    many |= n_qt > 1;
     long long sum = 0;
     if (n_qt <= 2)
-      for (int i = 0; i < n_qt; ++i) sum += tiles_of(args, s, tt, i).n;
+      for (int i = 0; i < n_qt; ++i) sum += tiles_of(args, s, args.tt, i).n;
     unsigned todo = __ballot_sync(0xffffffffu, n_qt > 2);
     while (todo != 0u) {
       const int src = __ffs(todo) - 1;
@@ -217,9 +273,9 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       z.t0 = 0;
       z.nq = __shfl_sync(0xffffffffu, s.nq, src);
       z.len = __shfl_sync(0xffffffffu, s.len, src);
-      const int n = (z.nq + tt - 1) / tt;
+      const int n = (z.nq + args.tt - 1) / args.tt;
       long long part = 0;
-      for (int i = lane; i < n; i += 32) part += tiles_of(args, z, tt, i).n;
+      for (int i = lane; i < n; i += 32) part += tiles_of(args, z, args.tt, i).n;
 #pragma unroll
       for (int k = 16; k > 0; k >>= 1) part += __shfl_xor_sync(0xffffffffu, part, k);
       if (lane == src) sum = part;
@@ -234,14 +290,54 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     block_scan<L::kWarps>(x, plan->warp_sums, &sum);
     total += sum;
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long lo = per * blockIdx.x;
-  const long long hi = lo + per < total ? lo + per : total;
-  if (lo >= hi) {
+  const bool shared = __syncthreads_or(many) != 0;  // some head has several query tiles
+  const int ctas = static_cast<int>(gridDim.x);
+  const long long per = (total + ctas - 1) / ctas;
+  // Whole units in rounds, as long as no CTA gets more than its share; thread c follows CTA
+  // c. Without several query tiles of a head there is nothing to share, and no round.
+  long long load = 0;
+  int rounds = 0;
+  if (shared) {
+    Unit v;
+    v.first(args);
+    if (tid < ctas) v.advance(args, tid);
+    if (tid == static_cast<int>(blockIdx.x) && v.b < args.c.B) {
+      plan->b0 = v.b;
+      plan->h0 = v.h;
+      plan->qt0 = v.qt;
+    }
+    while (true) {
+      const bool none = v.b >= args.c.B;
+      const int n = none ? 0 : tiles_of(args, v.s, args.tt, v.qt).n;
+      if (__syncthreads_or(tid < ctas && (none || load + n > per))) break;
+      load += n;
+      ++rounds;
+      v.advance(args, ctas);
+    }
+  }
+  // The places behind the rounds go to the CTAs in order, each up to its share. After rounds
+  // that is one place more, so that no run is empty before the last: the pieces of a unit
+  // then lie in consecutive CTAs.
+  long long lo, hi;
+  {
+    const bool mine = tid < ctas;
+    long long loads, room;
+    block_scan<L::kWarps>(mine ? load : 0, plan->warp_sums, &loads);
+    const long long share = per - load + (rounds > 0 ? 1 : 0);
+    const long long before = block_scan<L::kWarps>(mine ? share : 0, plan->warp_sums, &room);
+    if (tid == static_cast<int>(blockIdx.x)) {
+      plan->lo = min(total, loads + before);
+      plan->hi = min(total, loads + before + share);
+    }
+    __syncthreads();
+    lo = plan->lo;
+    hi = plan->hi;
+  }
+  if (lo >= hi && rounds == 0) {
     if (tid == 0) headers[blockIdx.x] = PieceHeader{-1, 0, 1, 0};
     return;
   }
-  {
+  if (lo < hi) {
     long long base = 0;
     for (int b0 = 0; b0 < args.c.B && base <= lo; b0 += L::kThreads) {
       const long long x = b0 == 0 ? x0 : head_places(b0 + tid) * args.c.Hkv;
@@ -257,13 +353,13 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     }
   }
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 0 && lo < hi) {
     // the query tile within the head: 32 at a time
     const PagedSeq s = paged_attn_seq(args.c, plan->b);
-    const int n_qt = (s.nq + tt - 1) / tt;
+    const int n_qt = (s.nq + args.tt - 1) / args.tt;
     long long rem = plan->rem;
     for (int i0 = 0; i0 < n_qt; i0 += 32) {
-      const int n = i0 + lane < n_qt ? tiles_of(args, s, tt, i0 + lane).n : 0;
+      const int n = i0 + lane < n_qt ? tiles_of(args, s, args.tt, i0 + lane).n : 0;
       long long inc = n;
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) {
@@ -355,13 +451,21 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint64_t tmo = args.sync.timeout_ns;
   Walk w;
-  w.b = plan->b;
-  w.h = plan->h;
-  w.qt = plan->qt;
-  w.at = plan->at;
-  w.left = hi - lo;
-  w.seq(args, tt);
-  w.piece(args, tt);
+  w.rounds = rounds;
+  w.in_round = w.in_run = false;
+  w.tail = 0;
+  w.left = lo < hi ? hi - lo : 0;
+  w.run_b = plan->b;
+  w.run_h = plan->h;
+  w.run_qt = plan->qt;
+  w.run_at = plan->at;
+  if (rounds > 0) {
+    w.u.b = plan->b0;
+    w.u.h = plan->h0;
+    w.u.qt = plan->qt0;
+    w.u.seq(args);
+  }
+  w.next(args);
   __syncthreads();  // the plan has been read: its place is the exchange area from here on
 
   auto fail = [&](void) {
@@ -381,8 +485,8 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     // the map and reads as zeros, behind the sequence and for a page that is none.
     auto box_page = [&](int j) {
       const int pos = j * kTile + lane * box_rows;
-      if (lane >= n_box || pos >= w.s.len) return args.c.num_pages;
-      const int p = paged_page(args.c, w.b, pos);
+      if (lane >= n_box || pos >= w.u.s.len) return args.c.num_pages;
+      const int p = paged_page(args.c, w.u.b, pos);
       return p >= 0 ? p : args.c.num_pages;
     };
     auto load_tile = [&](uint32_t dst, const CUtensorMap* tm, int j, int page, uint32_t bar) {
@@ -391,10 +495,10 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       if (lane < n_box) {
         const int slot = (j * kTile + lane * box_rows) % args.c.page_size;
         if constexpr (E4M3) {
-          tma_load_4d(dst + lane * box_rows * D, tm, 0, slot, w.h, page, bar);
+          tma_load_4d(dst + lane * box_rows * D, tm, 0, slot, w.u.h, page, bar);
         } else {
           for (int c = 0; c < L::kChunks; ++c)
-            tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, slot, w.h, page, bar);
+            tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, slot, w.u.h, page, bar);
         }
       }
       __syncwarp();
@@ -414,7 +518,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       const uint32_t ring = E4M3 ? sC : (is_k ? sK : sV);
       uint32_t it = 0, s = 0, ph = 1, q_armed = 0, tails = 0;
       bool ok = true;
-      const uint32_t q_bytes = static_cast<uint32_t>(L::kChunks * G * tt * 128);
+      const uint32_t q_bytes = static_cast<uint32_t>(L::kChunks * args.G * args.tt * 128);
       do {
         if (is_k) {
           if (q_armed > 0 && !mbar_wait_warp(bars.q_empty, (q_armed - 1) & 1, tmo, abort_flag)) {
@@ -425,7 +529,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           if (lane == 0) {
             mbar_expect_tx(bars.q_full, q_bytes);
             for (int c = 0; c < L::kChunks; ++c)
-              tma_load_3d(sQ + c * 16384, &tm_q, c * 64, w.h * G, w.s.t0 + w.qt * tt, bars.q_full);
+              tma_load_3d(sQ + c * 16384, &tm_q, c * 64, w.u.h * args.G, w.u.s.t0 + w.u.qt * args.tt, bars.q_full);
           }
           ++q_armed;
         }
@@ -440,7 +544,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
               break;
             }
             const uint32_t dst = ring + s * (E4M3 ? L::kCodeBytes : L::kTileBytes);
-            const int valid = w.s.len - j * kTile;
+            const int valid = w.u.s.len - j * kTile;
             if (!E4M3 && !is_k && valid < kTile) {
               // V's last tile: rows of its last page behind the sequence may hold anything
               load_tile(dst, &tm_v, j, page, bars.v_tail);
@@ -468,7 +572,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           }
           page = next_page;
         }
-      } while (ok && w.next(args, tt));
+      } while (ok && w.next(args));
       // Drain: every load this warp issued must land before the CTA exits. Stage x was armed
       // for ring positions x, x + kStages, ...; wait for the last one.
       if (tails > 0) mbar_wait_warp(bars.v_tail, (tails - 1) & 1, tmo, nullptr);
@@ -546,7 +650,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           }
           mma_commit(bars.q_empty);  // Q may be replaced once these S products are done
           ++count;
-          if (!w.next(args, tt)) break;
+          if (!w.next(args)) break;
         }
         // Drain: all issued MMAs must finish before tensor memory is released.
         mma_commit(bars.drain);
@@ -616,7 +720,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             break;
           }
           *pv_units = ++count;  // this piece's PVs are all issued
-          if (!w.next(args, tt)) break;
+          if (!w.next(args)) break;
         }
         mma_commit(bars.drain2);
         mbar_wait(bars.drain2, 0, tmo, nullptr);
@@ -638,10 +742,10 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       auto scale_of = [&](int j, uint32_t& k_byte, uint32_t& v_byte) {
         const int pos = j * kTile + r0 + lane;
         k_byte = v_byte = 0u;
-        if (pos < w.s.len) {
-          const int page = paged_page(args.c, w.b, pos);
+        if (pos < w.u.s.len) {
+          const int page = paged_page(args.c, w.u.b, pos);
           if (page >= 0) {
-            const long long at = (static_cast<long long>(page) * args.c.Hkv + w.h) * args.c.page_size +
+            const long long at = (static_cast<long long>(page) * args.c.Hkv + w.u.h) * args.c.page_size +
                                  pos % args.c.page_size;
             k_byte = args.c.k_scale[at];
             v_byte = args.c.v_scale[at];
@@ -653,7 +757,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         if (w.nt > 0) scale_of(w.j0, kb, vb);
         for (int i = 0; i < w.nt && ok; ++i) {
           const int j = w.j0 + i;
-          const int valid = w.s.len - j * kTile;  // rows of the tile that the cache holds
+          const int valid = w.u.s.len - j * kTile;  // rows of the tile that the cache holds
           uint32_t nkb = 0, nvb = 0;
           if (i + 1 < w.nt) scale_of(j + 1, nkb, nvb);
 #pragma unroll
@@ -669,26 +773,27 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             const uint32_t src = sC + cs * L::kCodeBytes;
             const uint32_t dst = (kv ? sV + vs * L::kTileBytes : sK + ks * L::kTileBytes) +
                                  (u >> 2) * 16384;
+            // four passes at a time: their loads are in flight together
 #pragma unroll
-            for (int x = 0; x < kLanes; ++x) {
-              const int rr = x * kRowsPer + lane / kLanes;  // row within the warp's 32
-              const int row = r0 + rr;
-              const uint32_t f = __shfl_sync(0xffffffffu, factor, rr);
-              const uint32_t flip = D == 128 ? ((u >> 2) ^ (row & 1)) : ((row >> 1) & 1);
-              const uint32_t line = dst + row * 128;
+            for (int x0 = 0; x0 < kLanes; x0 += 4) {
+              uint2 c[8];
 #pragma unroll
-              for (uint32_t y = 0; y < 2; ++y) {
-                const uint32_t half = y ^ flip;
-                uint32_t c0, c1;
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                             : "=r"(c0), "=r"(c1)
-                             : "r"(src + row * D + u * 16 + half * 8)
-                             : "memory");
+              for (int y = 0; y < 8; ++y) {
+                const int row = r0 + (x0 + (y >> 1)) * kRowsPer + lane / kLanes;
+                const uint32_t flip = D == 128 ? ((u >> 2) ^ (row & 1)) : ((row >> 1) & 1);
+                c[y] = ld_shared_v2(src + row * D + u * 16 + ((y & 1) ^ flip) * 8);
+              }
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const int rr = (x0 + (y >> 1)) * kRowsPer + lane / kLanes;  // within the warp's 32
+                const int row = r0 + rr;
+                const uint32_t flip = D == 128 ? ((u >> 2) ^ (row & 1)) : ((row >> 1) & 1);
+                const uint32_t f = __shfl_sync(0xffffffffu, factor, rr);
                 // behind the sequence a page may hold any code
-                if (row >= valid) c0 = c1 = 0u;
-                const uint32_t v = (u & 3) * 2 + half;  // 16-byte unit of the 128-byte line
-                st_shared_v4(line + ((v ^ (row & 7)) << 4), e4m3_lo(c0, f), e4m3_hi(c0, f),
-                             e4m3_lo(c1, f), e4m3_hi(c1, f));
+                if (row >= valid) c[y] = make_uint2(0u, 0u);
+                const uint32_t v = (u & 3) * 2 + ((y & 1) ^ flip);  // 16-byte unit of the line
+                st_shared_v4(dst + row * 128 + ((v ^ (row & 7)) << 4), e4m3_lo(c[y].x, f),
+                             e4m3_hi(c[y].x, f), e4m3_lo(c[y].y, f), e4m3_hi(c[y].y, f));
               }
             }
             fence_proxy_async_smem();
@@ -714,7 +819,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           kb = nkb;
           vb = nvb;
         }
-      } while (ok && w.next(args, tt));
+      } while (ok && w.next(args));
     }
   } else {
     regs_inc<L::kRegsSoftmax>();
@@ -725,9 +830,10 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + lane_base + L::col_s(g);
     const uint32_t tO = tmem + lane_base + L::col_o(g);
-    const uint32_t g_magic = (65536u + static_cast<uint32_t>(G) - 1u) / static_cast<uint32_t>(G);
     // r / G for r < 128, G <= 128: the excess r / 65536 of the product stays below 1 / G
-    auto token_of = [&](int r) { return static_cast<int>((static_cast<uint32_t>(r) * g_magic) >> 16); };
+    auto token_of = [&](int r) {
+      return static_cast<int>((static_cast<uint32_t>(r) * args.g_magic) >> 16);
+    };
     // This row of P_g, with the row's swizzle phase (t mod 8) in address bits 4-6:
     // 16-byte unit v of the row then sits at prow ^ (v << 4).
     const uint32_t prow = sP + static_cast<uint32_t>(g * L::kPBytes + t * 128 + ((t & 7) << 4));
@@ -736,20 +842,27 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     uint32_t s_cnt = 0, pv_cnt = 0;
     bool ok = true;
     int count = 0;
-    PieceHeader left = {-1, 0, 1, 0};
+    // The run's state is needed between pieces only: kept in local memory (the compiler
+    // cannot see through the pointer), it takes no registers from the row of scores.
+    Walk walk_mem = w;
+    Walk* wp = &walk_mem;
+    asm volatile("" : "+l"(wp)::"memory");
+    PieceHeader* left = &headers[blockIdx.x];
+    if (tid == 0) *left = PieceHeader{-1, 0, 1, 0};
     do {
+      const int nt = wp->nt, j0 = wp->j0;
       // keys [key_lo, key_hi) are visible to this row
-      int key_lo = 0, key_hi = w.s.len;
+      int key_lo = 0, key_hi = wp->u.s.len;
       {
-        const int pos = w.s.len - w.s.nq + w.qt * tt + token_of(t);
+        const int pos = wp->u.s.len - wp->u.s.nq + wp->u.qt * args.tt + token_of(t);
         if (args.causal && pos + 1 < key_hi) key_hi = pos + 1;
         if (args.wl >= 0) key_lo = pos - args.wl;
       }
       float m_ref = -INFINITY;  // reference maximum, scaled log2 units
       float l_sum = 0.f;        // running sum of exp2(s*c - m_ref)
       int n_done = 0;           // key tiles of this warpgroup
-      for (int p = g; p < w.nt; p += 2) {
-        const int k0 = (w.j0 + p) * kTile;
+      for (int p = g; p < nt; p += 2) {
+        const int k0 = (j0 + p) * kTile;
         if (!mbar_wait_warp(bars.s_full[g], s_cnt & 1, tmo, abort_flag)) {
           fail();
           ok = false;
@@ -902,7 +1015,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       const float2 other = xch[(1 - g) * kTile + t];
       const float m0 = g ? other.x : m_ref, l0 = g ? other.y : l_sum;
       const float m1 = g ? m_ref : other.x, l1 = g ? l_sum : other.y;
-      const bool has0 = w.nt > 0, has1 = w.nt > 1;  // O_g was written
+      const bool has0 = nt > 0, has1 = nt > 1;  // O_g was written
       const float m = fmaxf(m0, m1);
       const float a0 = (l0 > 0.f) ? ex2_approx(m0 - m) : 0.f;
       const float a1 = (l1 > 0.f) ? ex2_approx(m1 - m) : 0.f;
@@ -910,9 +1023,9 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       const float inv = (l > 0.f) ? 1.f / l : 0.f;
       const float w0 = a0 * inv, w1 = a1 * inv;
       const float lse2 = (l > 0.f) ? m + __log2f(l) : -INFINITY;  // log2 units
-      const int tok0 = w.qt * tt;                                  // the tile's first token
-      const int rows = min(w.s.nq - tok0, tt) * G;                 // rows of the tile
-      const bool direct = w.from_start && w.ends;
+      const int tok0 = wp->u.qt * args.tt;                                  // the tile's first token
+      const int rows = min(wp->u.s.nq - tok0, args.tt) * args.G;                 // rows of the tile
+      const bool direct = wp->from_start && wp->ends;
       // This warpgroup writes output columns [D/2 g, D/2 g + D/2) from both O_0 and O_1.
       constexpr int kHalf = D / 2;
       if (direct) {
@@ -957,20 +1070,20 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           const int row = quad * 32 + r;
           if (row < rows) {
             const int tk = token_of(row);
-            const long long at = static_cast<long long>(w.s.t0 + tok0 + tk) * args.H + w.h * G +
-                                 (row - tk * G);
+            const long long at = static_cast<long long>(wp->u.s.t0 + tok0 + tk) * args.H + wp->u.h * args.G +
+                                 (row - tk * args.G);
             *reinterpret_cast<uint4*>(args.o + at * D + kHalf * g + 8 * u) = val;
           }
         }
         if (t < rows && g == 0) {
           const int tk = token_of(t);
-          args.lse[static_cast<long long>(w.s.t0 + tok0 + tk) * args.H + w.h * G + (t - tk * G)] =
+          args.lse[static_cast<long long>(wp->u.s.t0 + tok0 + tk) * args.H + wp->u.h * args.G + (t - tk * args.G)] =
               lse2 * kLn2;
         }
       } else {
         // a piece: normalised, fp32. Slot 0 continues what an earlier CTA began, slot 1 is
         // continued by the next.
-        const long long at = (2ll * blockIdx.x + (w.from_start ? 1 : 0)) * kTile + t;
+        const long long at = (2ll * blockIdx.x + (wp->from_start ? 1 : 0)) * kTile + t;
 #pragma unroll
         for (int c = 0; c < kHalf / 16; ++c) {
           const uint32_t col = static_cast<uint32_t>(kHalf * g + 16 * c);
@@ -993,17 +1106,18 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         }
         if (t < rows && g == 0) args.lse_part[at] = lse2;
       }
-      if (!w.from_start) left.ended = w.ends;
-      if (w.from_start && !w.ends) {
-        left.b = w.b;
-        left.h = w.h;
-        left.qt = w.qt;
+      if (tid == 0) {
+        if (!wp->from_start) left->ended = wp->ends;
+        if (wp->from_start && !wp->ends) {
+          left->b = wp->u.b;
+          left->h = wp->u.h;
+          left->qt = wp->u.qt;
+        }
       }
       tc_fence_before();
       mbar_arrive(bars.o_free);
       ++count;
-    } while (w.next(args, tt));
-    if (tid == 0) headers[blockIdx.x] = left;
+    } while (wp->next(args));
   }
 
   tc_fence_before();
@@ -1031,7 +1145,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const PieceHeader hd = headers[c];
   if (hd.b < 0) return;
   const PagedSeq s = paged_attn_seq(a.c, hd.b);
-  const int G = a.H / a.c.Hkv, tt = kTile / G;
+  const int G = a.G, tt = a.tt;
   const int tok0 = hd.qt * tt;
   const int rows = min(s.nq - tok0, tt) * G;
   const int r = blockIdx.y * kMergeWarps + warp;

@@ -104,11 +104,6 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ uint2 ld_shared_v2(uint32_t saddr) {
-  uint2 r;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(saddr) : "memory");
-  return r;
-}
 __device__ __forceinline__ int ld_shared_u8(uint32_t saddr) {
   uint32_t r;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(saddr) : "memory");
