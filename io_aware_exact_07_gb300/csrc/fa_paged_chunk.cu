@@ -35,7 +35,7 @@ namespace fa {
 namespace {
 
 constexpr int kSoftmaxWarps = 8;
-constexpr int kQkWarp = 8;
+constexpr int kKWarp = 8;
 constexpr int kSIssuer = 9;
 constexpr int kPvIssuer = 10;
 constexpr int kVWarp = 11;
@@ -48,31 +48,42 @@ struct ChunkL {
   static constexpr int kThreads = kWarps * 32;
   // Registers per thread at launch, and as the warpgroups share them out afterwards.
   static constexpr int kRegsLaunch = E4M3 ? 128 : 168;
-  static constexpr int kRegsSoftmax = E4M3 ? 192 : 216;
-  static constexpr int kRegsAux = E4M3 ? 64 : 72;
-  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsAux <= kThreads * kRegsLaunch,
+  static constexpr int kRegsSoftmax = E4M3 ? 176 : 216;
+  static constexpr int kRegsAux = E4M3 ? 64 : 72;   // producers and issuers
+  static constexpr int kRegsConv = E4M3 ? 96 : 0;   // converters
+  static_assert(256 * kRegsSoftmax + 128 * (kRegsAux + kRegsConv) <= kThreads * kRegsLaunch,
                 "register reallocation exceeds the block's launch allocation");
-  static constexpr int kTileBytes = kTile * D * 2;   // a 128 x D bf16 tile
+  static constexpr int kTileBytes = kTile * D * 2;   // a 128 x D 16-bit tile
   static constexpr int kPBytes = kTile * kTile * 2;  // P_g
   static constexpr int kChunks = D / 64;             // 64-column (128-byte) swizzle chunks
-  static constexpr int kCodeBytes = kTile * D;       // a staged tile of codes
-  // At e4m3 and d = 128 one K tile suffices: a K tile is read by its S product while the
-  // next V tile is converted. That leaves room for two staged tiles.
-  static constexpr int kKStages = D == 64 ? (E4M3 ? 2 : 4) : (E4M3 ? 1 : 2);
-  static constexpr int kVStages = D == 64 ? (E4M3 ? 3 : 4) : 2;
-  static constexpr int kCStages = E4M3 ? (D == 64 ? 4 : 2) : 0;
+  // Ring depths. e4m3 at d = 128 has one K and one V tile: K is converted a tile ahead of V,
+  // so that only the PV product waits for a conversion after it, and the room goes to staged
+  // tiles of codes, which keep HBM busy.
+  static constexpr int kStages = D == 64 ? (E4M3 ? 2 : 4) : (E4M3 ? 1 : 2);
+  static constexpr int kCStages = E4M3 ? (D == 64 ? 8 : 3) : 0;  // staged tiles of codes
+  static constexpr int kCodeBytes = kTile * D;
   static constexpr int kMaxStages = 4;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kTileBytes;
-  static constexpr int kVOff = kKOff + kKStages * kTileBytes;
-  static constexpr int kPOff = kVOff + kVStages * kTileBytes;
+  static constexpr int kVOff = kKOff + kStages * kTileBytes;
+  static constexpr int kPOff = kVOff + kStages * kTileBytes;
   static constexpr int kCOff = kPOff + 2 * kPBytes;
   static constexpr int kBarOff = kCOff + kCStages * kCodeBytes;
-  // q_full, q_empty, K, V and staging rings (full, empty), s_full[2], s_free[2], p_full[2],
-  // pv_done[2], o_free, xbar[4], v_tail, drain, drain2, stall
-  static constexpr int kNumBars = 2 + 6 * kMaxStages + 8 + 1 + 4 + 4;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // abort flag, PV count, TMEM address
-  static constexpr int kXchOff = (kMiscOff + 16 + 15) / 16 * 16;  // (m, l) per warpgroup and row
+  // q_full, q_empty, q_ready, K and V rings (full, empty), staging ring (full, empty),
+  // s_full[2], s_free[2], p_full[2], pv_done[2], o_free, xbar[4], v_tail, drain, drain2, stall
+  static constexpr int kNumBars = 3 + 4 * kMaxStages + 2 * kCStages + 8 + 1 + 4 + 4;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;          // abort flag, TMEM address
+  // e4m3: the scale bytes of staged tiles (K's stage holds V's too); the scales of the latest
+  // tiles and Q's row exponents of the latest pieces, for the softmax. Tile n's slot is
+  // written when K's tile n is converted, after V's tile n - 2, which waited for the PV
+  // product of tile n - 2 - kStages: by then the softmax has read the slot of every tile up
+  // to that one, and n - kSlots is one of them. Pieces have a tile or more each.
+  static constexpr int kSlots = E4M3 ? 4 : 0;
+  static_assert(!E4M3 || kSlots >= 2 + kStages, "a slot is rewritten before it is read");
+  static constexpr int kBytesOff = (kMiscOff + 16 + 15) / 16 * 16;
+  static constexpr int kScaleOff = kBytesOff + 2 * kTile * kCStages;
+  static constexpr int kQExpOff = kScaleOff + 16 * kSlots;
+  static constexpr int kXchOff = kQExpOff + kTile * kSlots;  // (m, l) per warpgroup and row
   // the plan's scratch is used before the exchange area is
   static constexpr int kPlanOff = kXchOff;
   static constexpr int kSmemBytes = kXchOff + 2 * kTile * 8;
@@ -82,9 +93,9 @@ struct ChunkL {
 };
 
 struct Bars {
-  uint32_t q_full, q_empty;
+  uint32_t q_full, q_empty, q_ready;
   BarRun k_full, k_empty, v_full, v_empty, c_full, c_empty;  // ring stages
-  BarRun s_full, s_free, p_full, pv_done;                    // per softmax warpgroup
+  BarRun s_full, s_free, p_full, pv_done;   // per softmax warpgroup
   uint32_t o_free;
   BarRun xbar;
   uint32_t v_tail, drain, drain2, stall;
@@ -216,11 +227,33 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Copies `bytes` (a multiple of 16, both addresses aligned to 16) into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // Scores of keys outside [lo, hi) of a tile are masked.
+template <int N>
 __device__ __forceinline__ void mask_row(float* s, int lo, int hi) {
 #pragma unroll
-  for (int k = 0; k < 128; ++k)
+  for (int k = 0; k < N; ++k)
     if (k >= hi || k < lo) s[k] = -INFINITY;
+}
+
+// Maximum of N scores: three-input max over eight independent accumulators.
+template <int N>
+__device__ __forceinline__ float max_row(const float* s) {
+  float mx[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mx[k] = fmaxf(s[2 * k], s[2 * k + 1]);
+#pragma unroll
+  for (int k = 16; k < N; k += 16)
+#pragma unroll
+    for (int a = 0; a < 8; ++a) mx[a] = fmax3(mx[a], s[k + 2 * a], s[k + 2 * a + 1]);
+  return fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
 }
 
 }  // namespace
@@ -378,9 +411,6 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
 
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
-  // pieces whose PVs have all been issued: a count, not a barrier phase, since the PV issuer
-  // may run several pieces without key tiles ahead of the S issuer
-  volatile int* pv_units = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff + 8);
   Bars bars;
   {
@@ -393,12 +423,13 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     };
     bars.q_full = nb();
     bars.q_empty = nb();
+    bars.q_ready = nb();
     bars.k_full = run(L::kMaxStages);
     bars.k_empty = run(L::kMaxStages);
     bars.v_full = run(L::kMaxStages);
     bars.v_empty = run(L::kMaxStages);
-    bars.c_full = run(L::kMaxStages);
-    bars.c_empty = run(L::kMaxStages);
+    bars.c_full = run(L::kCStages);
+    bars.c_empty = run(L::kCStages);
     bars.s_full = run(2);
     bars.s_free = run(2);
     bars.p_full = run(2);
@@ -412,17 +443,19 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   }
   if (tid == 0) {
     *abort_flag = 0;
-    *pv_units = 0;
     mbar_init(bars.q_full, 1);
     mbar_init(bars.q_empty, 1);
+    mbar_init(bars.q_ready, 4);
     for (int s = 0; s < L::kMaxStages; ++s) {
       // e4m3: the four converter warps arrive; bf16: the producer, with the bytes expected
       mbar_init(bars.k_full[s], E4M3 ? 4 : 1);
       mbar_init(bars.v_full[s], E4M3 ? 4 : 1);
       mbar_init(bars.k_empty[s], 1);
       mbar_init(bars.v_empty[s], 1);
+    }
+    for (int s = 0; s < L::kCStages; ++s) {
       mbar_init(bars.c_full[s], 1);
-      mbar_init(bars.c_empty[s], 4);
+      mbar_init(bars.c_empty[s], 4);  // a lane of each converter warp
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(bars.s_full[g], 1);
@@ -476,139 +509,335 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   const uint32_t sK = smem_u32(smem + L::kKOff);
   const uint32_t sV = smem_u32(smem + L::kVOff);
   const uint32_t sP = smem_u32(smem + L::kPOff);
-  const uint32_t sC = smem_u32(smem + L::kCOff);
-  const int n_box = kTile / box_rows;  // boxes of a key tile
 
-  if (warp >= kSoftmaxWarps) {
+  if (E4M3 && warp >= kConvWarp) {
+    regs_dec<E4M3 ? L::kRegsConv : 24>();
+    // ------------------------------------------------------------ converters
+    // Warp x takes rows 32 x .. 32 x + 31 of every tile: staged codes, as f16 into the tiles
+    // that the products read. A row's scale 2^E is folded in relative to the tile's largest,
+    // 2^Et: code * 2^(E - Et) is exact in f16 down to E - Et = -15, and off by at most 2^-25
+    // below, 2^-33 of the largest value that the tile's codes can stand for. The softmax
+    // takes 2^Et into account. (Codes come by TMA, not by loads of these warps: a barrier
+    // arrival waits for a thread's loads in flight, so none could be ahead.)
+    // A pass covers 16 codes for each of 4 lanes of 8 rows, odd rows at the other half of the
+    // row (d = 128), so that 8 lanes load, and store, on different banks.
+    const int wx = warp - kConvWarp;
+    const int r0 = wx * 32;
+    const int row8 = lane >> 2, u = lane & 3;
+    const uint32_t sC = smem_u32(smem + L::kCOff);
+    const uint32_t sB = smem_u32(smem + L::kBytesOff);
+    uint32_t cs = 0, cph = 0, ks = 0, kph = 1, vs = 0, vph = 1, tile = 0, q_cnt = 0;
+    bool ok = true;
+    // Factors 2^(E - Et) of the lane's four rows 4 lane .. of key tile j as two f16 pairs, and
+    // Et + 127 (at least `least`): 0 for rows behind the sequence, a NaN for rows marked so.
+    auto factors = [&](uint32_t bytes, int j, int least, uint32_t(&f)[2]) -> int {
+      const int valid = w.u.s.len - (j * kTile + lane * 4);
+      int e[4], top = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        e[k] = static_cast<int>((bytes >> (8 * k)) & 255u);
+        if (e[k] != kScaleNaN) e[k] = min(e[k], kScaleMax + 127);
+        if (k < valid && e[k] != kScaleNaN) top = max(top, e[k]);
+      }
+      top = max(static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top))), least);
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = e[k] - top;  // <= 0 but for a NaN's mark
+        h[k] = x >= -14 ? static_cast<uint32_t>((x + 15) << 10) : (x >= -24 ? 1u << (x + 24) : 0u);
+        if (e[k] == kScaleNaN) h[k] = 0x7E00u;
+        if (k >= valid) h[k] = 0u;
+      }
+      f[0] = h[0] | h[1] << 16;
+      f[1] = h[2] | h[3] << 16;
+      return top;
+    };
+    auto convert_tile = [&](uint32_t dst, const uint32_t(&f)[2], int j) {
+      const int which = row8 & 3;
+      const int valid = w.u.s.len - j * kTile;
+      const uint32_t src = sC + cs * L::kCodeBytes;
+#pragma unroll
+      for (int rg = 0; rg < 4; ++rg) {
+        const int row = r0 + rg * 8 + row8;
+        const int from = wx * 8 + rg * 2 + (lane >> 4);  // the lane that has this row's factor
+        const uint32_t f0 = __shfl_sync(0xffffffffu, f[0], from);
+        const uint32_t f1 = __shfl_sync(0xffffffffu, f[1], from);
+        const uint32_t fx = prmt(which & 2 ? f1 : f0, 0u, which & 1 ? 0x3232u : 0x1010u);
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c) {
+          const int cc = L::kChunks == 2 ? (c ^ (row8 & 1)) : 0;
+          uint4 y = ld_shared_v4(src + row * D + cc * 64 + u * 16);
+          if (row >= valid) y = make_uint4(0u, 0u, 0u, 0u);  // a page may hold any code there
+          const uint32_t line = dst + cc * 16384 + row * 128;
+          uint32_t o[8];
+          e4m3_to_f16(y.x, o[0], o[1]);
+          e4m3_to_f16(y.y, o[2], o[3]);
+          e4m3_to_f16(y.z, o[4], o[5]);
+          e4m3_to_f16(y.w, o[6], o[7]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = mul_f16x2(o[k], fx);
+          st_shared_v4(line + (((2 * u) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+          st_shared_v4(line + (((2 * u + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+        }
+      }
+    };
+    // Q's rows 32 wx .. of the piece, bf16 -> f16 in place, each times 2^k that puts its
+    // largest magnitude into [2^14, 2^15): f16 then holds all that bf16 held but for elements
+    // below 2^-29 of it. (k is at most 60, which keeps the score's factor a normal number.)
+    auto do_q = [&]() -> bool {
+      if (!mbar_wait_warp(bars.q_full, q_cnt & 1, tmo, abort_flag)) return false;
+      int8_t* q_exp = reinterpret_cast<int8_t*>(smem + L::kQExpOff) + (q_cnt & (L::kSlots - 1)) * kTile;
+      const int r4 = lane >> 3, v = lane & 7;
+#pragma unroll 1
+      for (int pass = 0; pass < 8; ++pass) {
+        const int row = r0 + pass * 4 + r4;
+        const uint32_t at = sQ + row * 128 + ((v ^ (row & 7)) << 4);
+        uint4 x[L::kChunks];
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c) {
+          x[c] = ld_shared_v4(at + c * 16384);
+          constexpr uint32_t kAbs = 0x7FFF7FFFu;
+          const uint32_t m = __vmaxu2(__vmaxu2(x[c].x & kAbs, x[c].y & kAbs),
+                                      __vmaxu2(x[c].z & kAbs, x[c].w & kAbs));
+          top = max(top, max(m & 0xFFFFu, m >> 16));
+        }
+#pragma unroll
+        for (int k = 4; k > 0; k >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const int k2 = max(-114, min(60, 14 + 127 - static_cast<int>(top >> 7)));
+        const float m = pow2i(k2);
+        auto conv = [&](uint32_t y) {
+          return pack_f16x2(__uint_as_float(y << 16) * m, __uint_as_float(y & 0xFFFF0000u) * m);
+        };
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c)
+          st_shared_v4(at + c * 16384, conv(x[c].x), conv(x[c].y), conv(x[c].z), conv(x[c].w));
+        if (v == 0) q_exp[row] = static_cast<int8_t>(k2);
+      }
+      ++q_cnt;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.q_ready);
+      return true;
+    };
+    do {
+      // K_0, Q, K_1, V_0, K_2, V_1, ...: the order in which the producer stages them
+      uint32_t vb = 0, vb_next = 0;  // scale bytes of V's rows, in the next V tile and after it
+      for (int x = 0; ok && x < 2 * w.nt; ++x) {
+        const bool is_k = x == 0 || ((x & 1) != 0 && x != 2 * w.nt - 1);
+        const int j = w.j0 + (is_k ? (x + 1) >> 1 : (x - 1) >> 1);
+        const uint32_t empty = is_k ? bars.k_empty[ks] : bars.v_empty[vs];
+        if (!mbar_wait_warp(bars.c_full[cs], cph, tmo, abort_flag) ||
+            !mbar_wait_warp(empty, is_k ? kph : vph, tmo, abort_flag)) {
+          ok = false;
+          break;
+        }
+        // Et at least -40 and -60: the factors that the softmax makes of them stay normal
+        uint32_t f[2];
+        if (is_k) {
+          vb_next = ld_shared_u32(sB + cs * 2 * kTile + kTile + lane * 4);
+          if (x == 0) vb = vb_next;
+          const int ev = factors(vb_next, j, 127 - 60, f);
+          const int ek = factors(ld_shared_u32(sB + cs * 2 * kTile + lane * 4), j, 127 - 40, f);
+          if (wx == 0 && lane == 0)
+            reinterpret_cast<float4*>(smem + L::kScaleOff)[tile & (L::kSlots - 1)] = make_float4(
+                pow2i(ek - 127), static_cast<float>(ev - 127), pow2i(127 - ev), 0.f);
+          ++tile;
+        } else {
+          factors(vb, j, 127 - 60, f);
+          vb = vb_next;
+        }
+        convert_tile((is_k ? sK + ks * L::kTileBytes : sV + vs * L::kTileBytes), f, j);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {  // the codes have been read, the tile is complete
+          mbar_arrive(bars.c_empty[cs]);
+          mbar_arrive(is_k ? bars.k_full[ks] : bars.v_full[vs]);
+        }
+        if (++cs == L::kCStages) {
+          cs = 0;
+          cph ^= 1u;
+        }
+        uint32_t& at = is_k ? ks : vs;
+        uint32_t& phase = is_k ? kph : vph;
+        if (++at == L::kStages) {
+          at = 0;
+          phase ^= 1u;
+        }
+        if (x == 0) ok = do_q();
+      }
+    } while (ok && w.next(args));
+    if (!ok) fail();
+  } else if (warp >= kSoftmaxWarps) {
     regs_dec<L::kRegsAux>();
-    // Page of this lane's box of key tile j (lane < n_box); num_pages, which lies outside
-    // the map and reads as zeros, behind the sequence and for a page that is none.
-    auto box_page = [&](int j) {
-      const int pos = j * kTile + lane * box_rows;
-      if (lane >= n_box || pos >= w.u.s.len) return args.c.num_pages;
+    const int n_box = kTile / box_rows;  // boxes of a key tile
+    // Pages of 16-row groups: lane l has group l % 8 of key tile j + l / 8, so that one load
+    // serves four tiles. num_pages, which lies outside the maps and reads as zeros, behind
+    // the sequence and for a page that is none.
+    auto pages_of = [&](int j) {
+      const int pos = (j + (lane >> 3)) * kTile + (lane & 7) * 16;
+      if (pos >= w.u.s.len) return args.c.num_pages;
       const int p = paged_page(args.c, w.u.b, pos);
       return p >= 0 ? p : args.c.num_pages;
     };
-    auto load_tile = [&](uint32_t dst, const CUtensorMap* tm, int j, int page, uint32_t bar) {
-      if (lane == 0) mbar_expect_tx(bar, E4M3 ? L::kCodeBytes : L::kTileBytes);
-      __syncwarp();
-      if (lane < n_box) {
-        const int slot = (j * kTile + lane * box_rows) % args.c.page_size;
-        if constexpr (E4M3) {
-          tma_load_4d(dst + lane * box_rows * D, tm, 0, slot, w.u.h, page, bar);
-        } else {
-          for (int c = 0; c < L::kChunks; ++c)
-            tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, slot, w.u.h, page, bar);
-        }
-      }
-      __syncwarp();
-    };
-    if (warp == kQkWarp || (!E4M3 && warp == kVWarp)) {
-      // ------------------------------------------------------------ producers
-      const bool is_k = warp == kQkWarp;
-      if (lane == 0) {
-        tma_prefetch_desc(is_k ? &tm_k : &tm_v);
-        if (is_k) tma_prefetch_desc(&tm_q);
-        if (E4M3) tma_prefetch_desc(&tm_v);
-      }
-      constexpr uint32_t kStages = E4M3 ? L::kCStages : L::kKStages;
-      static_assert(E4M3 || L::kKStages == L::kVStages, "one ring depth");
-      const BarRun full = E4M3 ? bars.c_full : (is_k ? bars.k_full : bars.v_full);
-      const BarRun empty = E4M3 ? bars.c_empty : (is_k ? bars.k_empty : bars.v_empty);
-      const uint32_t ring = E4M3 ? sC : (is_k ? sK : sV);
-      uint32_t it = 0, s = 0, ph = 1, q_armed = 0, tails = 0;
+    const int groups = box_rows / 16;
+    if (!E4M3 && (warp == kKWarp || warp == kVWarp)) {
+      // ------------------------------------------------------------ producers, bf16
+      const bool is_k = warp == kKWarp;
+      const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+      if (lane == 0) tma_prefetch_desc(tm);
+      const BarRun full = is_k ? bars.k_full : bars.v_full;
+      const BarRun empty = is_k ? bars.k_empty : bars.v_empty;
+      const uint32_t ring = is_k ? sK : sV;
+      uint32_t it = 0, s = 0, ph = 1, tails = 0;
       bool ok = true;
-      const uint32_t q_bytes = static_cast<uint32_t>(L::kChunks * args.G * args.tt * 128);
       do {
-        if (is_k) {
-          if (q_armed > 0 && !mbar_wait_warp(bars.q_empty, (q_armed - 1) & 1, tmo, abort_flag)) {
+        int pages = 0;
+        for (int i = 0; i < w.nt; ++i) {
+          const int j = w.j0 + i;
+          if ((i & 3) == 0) pages = pages_of(j);
+          const int page = __shfl_sync(0xffffffffu, pages, (i & 3) * 8 + (lane * groups & 7));
+          if (!mbar_wait_warp(empty[s], ph, tmo, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          if (lane == 0) {
-            mbar_expect_tx(bars.q_full, q_bytes);
+          const uint32_t dst = ring + s * L::kTileBytes;
+          const int valid = w.u.s.len - j * kTile;
+          // V's last tile: rows of its last page behind the sequence may hold anything, so it
+          // comes on a barrier of its own and is handed on once they have been cleared
+          const bool tail = !is_k && valid < kTile;
+          const uint32_t bar = tail ? bars.v_tail : full[s];
+          if (lane == 0) mbar_expect_tx(bar, L::kTileBytes);
+          __syncwarp();
+          if (lane < n_box) {
+            const int slot = (j * kTile + lane * box_rows) % args.c.page_size;
             for (int c = 0; c < L::kChunks; ++c)
-              tma_load_3d(sQ + c * 16384, &tm_q, c * 64, w.u.h * args.G, w.u.s.t0 + w.u.qt * args.tt, bars.q_full);
+              tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, slot, w.u.h, page, bar);
           }
-          ++q_armed;
-        }
-        int page = w.nt > 0 ? box_page(w.j0) : 0;
-        for (int i = 0; i < w.nt && ok; ++i) {
-          const int j = w.j0 + i;
-          const int next_page = i + 1 < w.nt ? box_page(j + 1) : 0;  // ahead of the wait
-          for (int kv = 0; kv < (E4M3 ? 2 : 1); ++kv) {
-            if (!mbar_wait_warp(empty[s], ph, tmo, abort_flag)) {
-              fail();
+          __syncwarp();
+          if (tail) {
+            ++tails;
+            if (!mbar_wait_warp(bars.v_tail, (tails - 1) & 1, tmo, abort_flag)) {
+              fail();  // the drain below waits for the load
               ok = false;
               break;
             }
-            const uint32_t dst = ring + s * (E4M3 ? L::kCodeBytes : L::kTileBytes);
-            const int valid = w.u.s.len - j * kTile;
-            if (!E4M3 && !is_k && valid < kTile) {
-              // V's last tile: rows of its last page behind the sequence may hold anything
-              load_tile(dst, &tm_v, j, page, bars.v_tail);
-              ++tails;
-              if (!mbar_wait_warp(bars.v_tail, (tails - 1) & 1, tmo, abort_flag)) {
-                fail();  // the drain below waits for the load
-                ok = false;
-                break;
-              }
-              const int end = (valid + box_rows - 1) / box_rows * box_rows;
-              for (int x = valid * 8 + lane; x < end * 8; x += 32)
-                for (int c = 0; c < L::kChunks; ++c)
-                  st_shared_v4(dst + c * 16384 + x * 16, 0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(full[s]);
-            } else {
-              load_tile(dst, (E4M3 ? kv == 0 : is_k) ? &tm_k : &tm_v, j, page, full[s]);
-            }
-            ++it;
-            if (++s == kStages) {
-              s = 0;
-              ph ^= 1u;
-            }
+            const int end = (valid + box_rows - 1) / box_rows * box_rows;
+            for (int x = valid * 8 + lane; x < end * 8; x += 32)
+              for (int c = 0; c < L::kChunks; ++c)
+                st_shared_v4(dst + c * 16384 + x * 16, 0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full[s]);
           }
-          page = next_page;
+          ++it;
+          if (++s == L::kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
       } while (ok && w.next(args));
       // Drain: every load this warp issued must land before the CTA exits. Stage x was armed
       // for ring positions x, x + kStages, ...; wait for the last one.
       if (tails > 0) mbar_wait_warp(bars.v_tail, (tails - 1) & 1, tmo, nullptr);
-      for (uint32_t x = 0; x < kStages; ++x)
-        if (it > x) mbar_wait_warp(full[x], ((it - 1 - x) / kStages) & 1, tmo, nullptr);
-      if (q_armed) mbar_wait_warp(bars.q_full, (q_armed - 1) & 1, tmo, nullptr);
+      for (uint32_t x = 0; x < L::kStages; ++x)
+        if (it > x) mbar_wait_warp(full[x], ((it - 1 - x) / L::kStages) & 1, tmo, nullptr);
+    } else if (E4M3 && warp == kKWarp) {
+      // ------------------------------------------------------------ producer, e4m3
+      // Tiles of codes in the order K_0, K_1, V_0, K_2, V_1, ...; with K's tile come the
+      // scale bytes of K's and V's rows, 16 of a page at a time.
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+      const uint32_t sC = smem_u32(smem + L::kCOff);
+      const uint32_t sB = smem_u32(smem + L::kBytesOff);
+      uint32_t it = 0, s = 0, ph = 1;
+      auto stage = [&](int j, bool is_k, int pages, int i) -> bool {
+        const int box_page = __shfl_sync(0xffffffffu, pages, (i & 3) * 8 + (lane * groups & 7));
+        const int row_page = __shfl_sync(0xffffffffu, pages, (i & 3) * 8 + (lane & 7));
+        if (!mbar_wait_warp(bars.c_empty[s], ph, tmo, abort_flag)) return false;
+        const uint32_t bytes = sB + s * 2 * kTile + lane * 16;  // lanes 0-7: K's, 8-15: V's
+        const bool there = lane < 16 && is_k && row_page < args.c.num_pages;
+        // no page: its codes read as zeros, and so do its scales
+        if (lane < 16 && is_k && !there) st_shared_v4(bytes, 0u, 0u, 0u, 0u);
+        const int copies = __popc(__ballot_sync(0xffffffffu, there));
+        if (lane == 0) mbar_expect_tx(bars.c_full[s], L::kCodeBytes + copies * 16);
+        __syncwarp();
+        if (lane < n_box)
+          tma_load_4d(sC + s * L::kCodeBytes + lane * box_rows * D, is_k ? &tm_k : &tm_v, 0,
+                      (j * kTile + lane * box_rows) % args.c.page_size, w.u.h, box_page,
+                      bars.c_full[s]);
+        if (there) {
+          const long long at = (static_cast<long long>(row_page) * args.c.Hkv + w.u.h) *
+                                   args.c.page_size + (j * kTile + (lane & 7) * 16) % args.c.page_size;
+          bulk_load(bytes, (lane < 8 ? args.c.k_scale : args.c.v_scale) + at, 16, bars.c_full[s]);
+        }
+        __syncwarp();
+        ++it;
+        if (++s == L::kCStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+        return true;
+      };
+      bool ok = true;
+      do {
+        int pages = 0, ahead = 0;  // of tiles j0 + 4 n .. of V's, and of K's, a tile ahead
+        if (w.nt > 0) {
+          pages = ahead = pages_of(w.j0);
+          ok = stage(w.j0, true, ahead, 0);
+        }
+        for (int i = 0; ok && i < w.nt; ++i) {
+          if ((i & 3) == 0) pages = ahead;
+          if (i + 1 < w.nt) {
+            if (((i + 1) & 3) == 0) ahead = pages_of(w.j0 + i + 1);
+            ok = stage(w.j0 + i + 1, true, ahead, i + 1);
+          }
+          ok = ok && stage(w.j0 + i, false, pages, i);
+        }
+      } while (ok && w.next(args));
+      if (!ok) fail();
+      constexpr int kC = E4M3 ? L::kCStages : 1;
+      for (int x = 0; x < kC; ++x)
+        if (it > static_cast<uint32_t>(x))
+          mbar_wait_warp(bars.c_full[x], ((it - 1 - x) / kC) & 1, tmo, nullptr);
     } else if (warp == kSIssuer) {
       // ------------------------------------------------------------ S issuer
       if (lane == 0) {
-        constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0, 0);  // S = Q K^T, both K-major
+        // S = Q K^T, both K-major; bf16, or f16 for a quantised cache
+        constexpr uint32_t kIdS = E4M3 ? idesc_f16_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
         constexpr uint64_t kStep = static_cast<uint64_t>(L::kTileBytes >> 4);
         const uint64_t dQ = sdesc_sw128(sQ, 16, 1024);
         const uint64_t dK0 = sdesc_sw128(sK, 16, 1024);
+        const uint32_t q_bytes = static_cast<uint32_t>(L::kChunks * args.G * args.tt * 128);
         uint32_t s = 0, ph = 0, sf0 = 0, sf1 = 0;
+        uint32_t q_cnt = 0;  // pieces with key tiles so far: those that have loaded Q
         bool seen0 = false, seen1 = false;
         bool ok = true;
+        tma_prefetch_desc(&tm_q);
         // Test hook: this barrier is never completed, so the bounded wait runs out.
         if (args.sync.inject_stall && !mbar_wait(bars.stall, 0, tmo, abort_flag)) {
           fail();
           ok = false;
         }
-        int count = 0;
         while (ok) {
-          // The tensor core runs products in issue order: the next piece's S products wait
-          // until this piece's last PV has been issued, so that they do not delay it.
-          bool ready = *pv_units >= count;
-          if (!ready) {
-            const uint64_t t0 = globaltimer_ns();
-            while (!(ready = *pv_units >= count)) {
-              if (*abort_flag || globaltimer_ns() - t0 > tmo) break;
-              __nanosleep(64);
+          if (w.nt > 0) {
+            // Q is replaced once the last piece's S products have completed
+            if (q_cnt > 0 && !mbar_wait(bars.q_empty, (q_cnt - 1) & 1, tmo, abort_flag)) {
+              fail();
+              break;
             }
-          }
-          if (!ready || !mbar_wait(bars.q_full, count & 1, tmo, abort_flag)) {
-            fail();
-            break;
+            mbar_expect_tx(bars.q_full, q_bytes);
+            for (int c = 0; c < L::kChunks; ++c)
+              tma_load_3d(sQ + c * 16384, &tm_q, c * 64, w.u.h * args.G, w.u.s.t0 + w.u.qt * args.tt,
+                          bars.q_full);
+            ++q_cnt;
+            if (!mbar_wait(E4M3 ? bars.q_ready : bars.q_full, (q_cnt - 1) & 1, tmo, abort_flag)) {
+              fail();
+              break;
+            }
           }
           for (int p = 0; p < w.nt; ++p) {
             const int g = p & 1;
@@ -639,7 +868,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             }
             mma_commit(bars.s_full[g]);
             mma_commit(bars.k_empty[s]);
-            if (++s == L::kKStages) {
+            if (++s == L::kStages) {
               s = 0;
               ph ^= 1u;
             }
@@ -648,10 +877,10 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             fail();
             break;
           }
-          mma_commit(bars.q_empty);  // Q may be replaced once these S products are done
-          ++count;
+          if (w.nt > 0) mma_commit(bars.q_empty);
           if (!w.next(args)) break;
         }
+        if (q_cnt > 0) mbar_wait(bars.q_full, (q_cnt - 1) & 1, tmo, nullptr);
         // Drain: all issued MMAs must finish before tensor memory is released.
         mma_commit(bars.drain);
         mbar_wait(bars.drain, 0, tmo, nullptr);
@@ -660,7 +889,8 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     } else if (warp == kPvIssuer) {
       // ------------------------------------------------------------ PV issuer
       if (lane == 0) {
-        constexpr uint32_t kIdPV = idesc_bf16_f32(128, D, 0, 1);  // P K-major, V MN-major
+        // P K-major, V MN-major
+        constexpr uint32_t kIdPV = E4M3 ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
         constexpr uint64_t kStep = static_cast<uint64_t>(L::kTileBytes >> 4);
         constexpr uint64_t kPStep = static_cast<uint64_t>(L::kPBytes >> 4);
         const uint64_t dP0 = sdesc_sw128(sP, 16, 1024);
@@ -702,7 +932,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             if (g) first1 = false; else first0 = false;
             mma_commit(bars.pv_done[g]);
             mma_commit(bars.v_empty[s]);
-            if (++s == L::kVStages) {
+            if (++s == L::kStages) {
               s = 0;
               ph ^= 1u;
             }
@@ -719,107 +949,13 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             fail();
             break;
           }
-          *pv_units = ++count;  // this piece's PVs are all issued
+          ++count;
           if (!w.next(args)) break;
         }
         mma_commit(bars.drain2);
         mbar_wait(bars.drain2, 0, tmo, nullptr);
       }
       __syncwarp();
-    } else if (E4M3 && warp >= kConvWarp) {
-      // ------------------------------------------------------------ converters
-      // Warp x takes rows 32 x .. 32 x + 31 of every tile. A lane reads 16 codes of a row in
-      // two 8-byte halves, in an order that keeps the lanes of a load, and then the 16-byte
-      // units of a store, on different banks.
-      const int r0 = (warp - kConvWarp) * 32;
-      constexpr int kLanes = D / 16;          // lanes per row
-      constexpr int kRowsPer = 32 / kLanes;   // rows per pass
-      const int u = lane % kLanes;
-      uint32_t cs = 0, cph = 0, ks = 0, kph = 1, vs = 0, vph = 1;
-      bool ok = true;
-      // scale bytes of this lane's row (row r0 + lane) of K and V in tile j; 0, for which a
-      // code of zero gives zero, where there is no row
-      auto scale_of = [&](int j, uint32_t& k_byte, uint32_t& v_byte) {
-        const int pos = j * kTile + r0 + lane;
-        k_byte = v_byte = 0u;
-        if (pos < w.u.s.len) {
-          const int page = paged_page(args.c, w.u.b, pos);
-          if (page >= 0) {
-            const long long at = (static_cast<long long>(page) * args.c.Hkv + w.u.h) * args.c.page_size +
-                                 pos % args.c.page_size;
-            k_byte = args.c.k_scale[at];
-            v_byte = args.c.v_scale[at];
-          }
-        }
-      };
-      do {
-        uint32_t kb = 0, vb = 0;
-        if (w.nt > 0) scale_of(w.j0, kb, vb);
-        for (int i = 0; i < w.nt && ok; ++i) {
-          const int j = w.j0 + i;
-          const int valid = w.u.s.len - j * kTile;  // rows of the tile that the cache holds
-          uint32_t nkb = 0, nvb = 0;
-          if (i + 1 < w.nt) scale_of(j + 1, nkb, nvb);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t factor = e4m3_factor(static_cast<int>(kv ? vb : kb));
-            if (!mbar_wait_warp(bars.c_full[cs], cph, tmo, abort_flag) ||
-                !mbar_wait_warp(kv ? bars.v_empty[vs] : bars.k_empty[ks], kv ? vph : kph, tmo,
-                                abort_flag)) {
-              fail();
-              ok = false;
-              break;
-            }
-            const uint32_t src = sC + cs * L::kCodeBytes;
-            const uint32_t dst = (kv ? sV + vs * L::kTileBytes : sK + ks * L::kTileBytes) +
-                                 (u >> 2) * 16384;
-            // four passes at a time: their loads are in flight together
-#pragma unroll
-            for (int x0 = 0; x0 < kLanes; x0 += 4) {
-              uint2 c[8];
-#pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                const int row = r0 + (x0 + (y >> 1)) * kRowsPer + lane / kLanes;
-                const uint32_t flip = D == 128 ? ((u >> 2) ^ (row & 1)) : ((row >> 1) & 1);
-                c[y] = ld_shared_v2(src + row * D + u * 16 + ((y & 1) ^ flip) * 8);
-              }
-#pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                const int rr = (x0 + (y >> 1)) * kRowsPer + lane / kLanes;  // within the warp's 32
-                const int row = r0 + rr;
-                const uint32_t flip = D == 128 ? ((u >> 2) ^ (row & 1)) : ((row >> 1) & 1);
-                const uint32_t f = __shfl_sync(0xffffffffu, factor, rr);
-                // behind the sequence a page may hold any code
-                if (row >= valid) c[y] = make_uint2(0u, 0u);
-                const uint32_t v = (u & 3) * 2 + ((y & 1) ^ flip);  // 16-byte unit of the line
-                st_shared_v4(dst + row * 128 + ((v ^ (row & 7)) << 4), e4m3_lo(c[y].x, f),
-                             e4m3_hi(c[y].x, f), e4m3_lo(c[y].y, f), e4m3_hi(c[y].y, f));
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(bars.c_empty[cs]);
-              mbar_arrive(kv ? bars.v_full[vs] : bars.k_full[ks]);
-            }
-            if (++cs == L::kCStages) {
-              cs = 0;
-              cph ^= 1u;
-            }
-            if (kv) {
-              if (++vs == L::kVStages) {
-                vs = 0;
-                vph ^= 1u;
-              }
-            } else if (++ks == L::kKStages) {
-              ks = 0;
-              kph ^= 1u;
-            }
-          }
-          kb = nkb;
-          vb = nvb;
-        }
-      } while (ok && w.next(args));
     }
   } else {
     regs_inc<L::kRegsSoftmax>();
@@ -839,6 +975,11 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     const uint32_t prow = sP + static_cast<uint32_t>(g * L::kPBytes + t * 128 + ((t & 7) << 4));
     float2* xch = reinterpret_cast<float2*>(smem + L::kXchOff);
     const float c_log2 = args.scale_log2;
+    // e4m3: the tiles' scales and the row exponents of Q, as the converters leave them
+    const float4* tile_scale = reinterpret_cast<const float4*>(smem + L::kScaleOff);
+    const int8_t* q_exp = reinterpret_cast<const int8_t*>(smem + L::kQExpOff);
+    uint32_t tile_cnt = 0, q_cnt = 0;  // key tiles, and pieces with any, before this piece
+    float c_row = 0.f;
     uint32_t s_cnt = 0, pv_cnt = 0;
     bool ok = true;
     int count = 0;
@@ -870,28 +1011,45 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         }
         ++s_cnt;
         tc_fence_after();
-        uint32_t sr[128];
+        // A score's exponent is s * c_t + ev (log2 units): for a quantised cache with the scales
+        // that Q's row and K's tile were given, and V's tile's scale 2^ev, which P carries so
+        // that all tiles add to one O; l takes it out again.
+        float c_t = c_log2, ev = 0.f, ev_inv = 1.f;
+        if constexpr (E4M3) {
+          if (n_done == 0)
+            c_row = c_log2 * pow2i(-static_cast<int>(q_exp[(q_cnt & (L::kSlots - 1)) * kTile + t]));
+          const float4 z = tile_scale[(tile_cnt + p) & (L::kSlots - 1)];
+          c_t = c_row * z.x;
+          ev = z.y;
+          ev_inv = z.z;
+        }
+        // bf16: the whole row in registers at once. e4m3, where the converters need registers
+        // and instruction cache: half a row at a time, once for its maximum and once for P, in
+        // loops.
+        constexpr int kCols = E4M3 ? 64 : 128;
+        float s[kCols];
+        const bool edge = k0 < key_lo || k0 + kTile > key_hi;
+        auto load_scores = [&](int c0) {
+          uint32_t sr[kCols];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, &sr[c * 32]);
-        tmem_ld_wait();
-        // S is in registers: the next S of this warpgroup may be written over it.
-        tc_fence_before();
-        mbar_arrive(bars.s_free[g]);
-        float s[128];
+          for (int c = 0; c < kCols / 32; ++c) tmem_ld32(tS + c0 + c * 32, &sr[c * 32]);
+          tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(sr[k]);
-        if (k0 < key_lo || k0 + kTile > key_hi) mask_row(s, key_lo - k0, key_hi - k0);
-        // Row maximum: three-input max over eight independent accumulators.
-        float mx[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mx[k] = fmaxf(s[2 * k], s[2 * k + 1]);
-#pragma unroll
-        for (int k = 16; k < 128; k += 16)
-#pragma unroll
-          for (int a = 0; a < 8; ++a) mx[a] = fmax3(mx[a], s[k + 2 * a], s[k + 2 * a + 1]);
-        const float mx_row =
-            fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-        const float m_new = fmaxf(m_ref, mx_row * c_log2);
+          for (int k = 0; k < kCols; ++k) s[k] = __uint_as_float(sr[k]);
+        };
+        auto release_scores = [&]() {  // the next S of this warpgroup may be written over it
+          tc_fence_before();
+          mbar_arrive(bars.s_free[g]);
+        };
+        float mx_row = -INFINITY;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kTile; c0 += kCols) {
+          load_scores(c0);
+          if constexpr (!E4M3) release_scores();
+          if (edge) mask_row<kCols>(s, key_lo - k0 - c0, key_hi - k0 - c0);
+          mx_row = fmaxf(mx_row, max_row<kCols>(s));
+        }
+        const float m_new = fmaxf(m_ref, E4M3 ? fmaf(mx_row, c_t, ev) : mx_row * c_t);
         const bool grow = m_new > m_ref + kRescale;
         float alpha = 1.f;
         if (grow) {
@@ -900,59 +1058,74 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           m_ref = m_new;
         }
         const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-        const uint64_t c2 = f2_pack(c_log2, c_log2);
-        const uint64_t nm2 = f2_pack(-m_use, -m_use);
+        const uint64_t c2 = f2_pack(c_t, c_t);
+        const float nm = E4M3 ? ev - m_use : -m_use;
+        const uint64_t nm2 = f2_pack(nm, nm);
         uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // four packed partial sums
-        uint32_t pk[64];
+        constexpr int kPk = kCols / 2;
+        uint32_t pk[kPk];
         bool pv_ok = true;
-        bool stored0 = false;  // first half already in P_g
         // 128-byte swizzle: 16-byte unit v of the row's 64-key half h at v ^ (t & 7)
         auto store_half = [&](int h) {
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
+          for (int v = 0; v < 8; ++v) {
+            const int x = (E4M3 ? 0 : h * 32) + 4 * v;
             st_shared_v4((prow ^ static_cast<uint32_t>(v << 4)) + static_cast<uint32_t>(h * 16384),
-                         pk[h * 32 + 4 * v], pk[h * 32 + 4 * v + 1], pk[h * 32 + 4 * v + 2],
-                         pk[h * 32 + 4 * v + 3]);
+                         pk[x], pk[x + 1], pk[x + 2], pk[x + 3]);
+          }
         };
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        auto wait_pv = [&]() -> bool {  // the previous PV, which reads P_g, has completed
+          if (!mbar_wait_warp(bars.pv_done[g], pv_cnt & 1, tmo, abort_flag)) return false;
+          ++pv_cnt;
+          tc_fence_after();
+          return true;
+        };
+        // P = 2^(s * c_t + nm) of N scores, rounded to bf16 for the product (at most 2^-8 of each
+        // weight), or to f16 (2^-11, and 2^-25 where it is below 2^-14); l keeps fp32.
+        auto weights = [&](const float* x, uint32_t* to) {
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
-            const int k = half * 64 + e;
             float y0, y1;
-            f2_unpack(f2_fma(f2_pack(s[k], s[k + 1]), c2, nm2), y0, y1);
+            f2_unpack(f2_fma(f2_pack(x[e], x[e + 1]), c2, nm2), y0, y1);
             const float p0 = ex2_approx(y0);
             const float p1 = ex2_approx(y1);
             rs2[(e >> 1) & 3] = f2_add(rs2[(e >> 1) & 3], f2_pack(p0, p1));
-            // P is rounded to bf16 for the product (at most 2^-8 of each weight); l keeps fp32
-            pk[half * 32 + (e >> 1)] = pack_bf16x2(p0, p1);
+            to[e >> 1] = E4M3 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
           }
-          if (half == 0) {
-            // The first half goes out now if the previous PV (which reads P_g) has already
-            // completed; otherwise the second half's exponentials come first.
-            const bool ready =
-                n_done == 0 ||
-                __all_sync(0xffffffffu, mbar_test_wait(bars.pv_done[g], pv_cnt & 1));
-            if (ready) {
-              if (n_done > 0) {
-                ++pv_cnt;
-                tc_fence_after();
-              }
-              store_half(0);
-              stored0 = true;
+        };
+        if constexpr (E4M3) {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            load_scores(half * 64);
+            if (half == 1) release_scores();
+            if (edge) mask_row<kCols>(s, key_lo - k0 - half * 64, key_hi - k0 - half * 64);
+            weights(s, pk);
+            if (half == 0 && n_done > 0 && !wait_pv()) {
+              pv_ok = false;
+              break;
             }
-          } else {
-            if (!stored0) {
-              if (!mbar_wait_warp(bars.pv_done[g], pv_cnt & 1, tmo, abort_flag)) {
-                pv_ok = false;
-                break;
-              }
+            store_half(half);
+          }
+        } else {
+          weights(s, pk);
+          // The first half goes out now if the previous PV has already completed; otherwise the
+          // second half's exponentials come first.
+          const bool ready =
+              n_done == 0 ||
+              __all_sync(0xffffffffu, mbar_test_wait(bars.pv_done[g], pv_cnt & 1));
+          if (ready) {
+            if (n_done > 0) {
               ++pv_cnt;
               tc_fence_after();
-              store_half(0);
             }
-            store_half(1);
+            store_half(0);
           }
+          weights(s + kCols / 2, pk + kPk / 2);
+          if (!ready) {
+            pv_ok = wait_pv();
+            if (pv_ok) store_half(0);
+          }
+          if (pv_ok) store_half(1);
         }
         if (!pv_ok) {
           fail();
@@ -963,7 +1136,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           const uint64_t t2 = f2_add(f2_add(rs2[0], rs2[1]), f2_add(rs2[2], rs2[3]));
           float r0, r1;
           f2_unpack(t2, r0, r1);
-          l_sum += r0 + r1;
+          l_sum += E4M3 ? (r0 + r1) * ev_inv : r0 + r1;
         }
         // Rescale the O_g row in tensor memory (the previous PV has completed).
         if (n_done > 0 && __any_sync(0xffffffffu, grow)) {
@@ -1117,6 +1290,8 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       tc_fence_before();
       mbar_arrive(bars.o_free);
       ++count;
+      tile_cnt += nt;
+      q_cnt += nt > 0;
     } while (wp->next(args));
   }
 
