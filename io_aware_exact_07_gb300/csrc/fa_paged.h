@@ -138,6 +138,21 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t saddr) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t saddr) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(saddr) : "memory");
+  return r;
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t saddr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(saddr), "r"(a), "r"(b) : "memory");
+}
+// Copies 16 bytes into shared memory, or fills them with zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+
 // The four e4m3 codes of a word as f16 pairs, exactly (f16 holds every e4m3 value).
 __device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\t"

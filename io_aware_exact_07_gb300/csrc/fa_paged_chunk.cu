@@ -73,7 +73,7 @@ struct ChunkL {
   // s_full[2], s_free[2], p_full[2], pv_done[2], o_free, xbar[4], v_tail, drain, drain2, stall
   static constexpr int kNumBars = 3 + 4 * kMaxStages + 2 * kCStages + 8 + 1 + 4 + 4;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;          // abort flag, TMEM address
-  // e4m3: the scale bytes of staged tiles (K's stage holds V's too); the scales of the latest
+  // e4m3: the scale bytes of staged tiles (K's, then V's); the scales of the latest
   // tiles and Q's row exponents of the latest pieces, for the softmax. Tile n's slot is
   // written when K's tile n is converted, after V's tile n - 2, which waited for the PV
   // product of tile n - 2 - kStages: by then the softmax has read the slot of every tile up
@@ -83,7 +83,8 @@ struct ChunkL {
   static constexpr int kBytesOff = (kMiscOff + 16 + 15) / 16 * 16;
   static constexpr int kScaleOff = kBytesOff + 2 * kTile * kCStages;
   static constexpr int kQExpOff = kScaleOff + 16 * kSlots;
-  static constexpr int kXchOff = kQExpOff + kTile * kSlots;  // (m, l) per warpgroup and row
+  static constexpr int kFactorOff = kQExpOff + kTile * kSlots;  // 128 f16 factors
+  static constexpr int kXchOff = kFactorOff + (E4M3 ? 2 * kTile : 0);  // (m, l) per warpgroup and row
   // the plan's scratch is used before the exchange area is
   static constexpr int kPlanOff = kXchOff;
   static constexpr int kSmemBytes = kXchOff + 2 * kTile * 8;
@@ -227,12 +228,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Copies `bytes` (a multiple of 16, both addresses aligned to 16) into shared memory.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
+// Arrives on an mbarrier once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Scores of keys outside [lo, hi) of a tile are masked.
@@ -454,7 +452,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       mbar_init(bars.v_empty[s], 1);
     }
     for (int s = 0; s < L::kCStages; ++s) {
-      mbar_init(bars.c_full[s], 1);
+      mbar_init(bars.c_full[s], 17);  // the producer's lane 0, and 16 lanes for their scale bytes
       mbar_init(bars.c_empty[s], 4);  // a lane of each converter warp
     }
     for (int g = 0; g < 2; ++g) {
@@ -528,46 +526,66 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     const uint32_t sB = smem_u32(smem + L::kBytesOff);
     uint32_t cs = 0, cph = 0, ks = 0, kph = 1, vs = 0, vph = 1, tile = 0, q_cnt = 0;
     bool ok = true;
-    // Factors 2^(E - Et) of the lane's four rows 4 lane .. of key tile j as two f16 pairs, and
-    // Et + 127 (at least `least`): 0 for rows behind the sequence, a NaN for rows marked so.
-    auto factors = [&](uint32_t bytes, int j, int least, uint32_t(&f)[2]) -> int {
+    // The factors of the warp's 32 rows, f16, for its conversion.
+    const uint32_t sF = smem_u32(smem + L::kFactorOff) + wx * 64;
+    // Et + 127 of a tile from the lane's four scale bytes (rows 4 lane ..). 127 if all of the
+    // tile's rows are there with E of -14 .. 7, as those of a cache in use are: their factors
+    // 2^E are normal in f16 as they stand. Else the largest, at least `least`, so that the
+    // factors that the softmax makes of it stay normal.
+    auto top_of = [&](uint32_t bytes, int j, int least) -> int {
       const int valid = w.u.s.len - (j * kTile + lane * 4);
-      int e[4], top = 0;
-#pragma unroll
+      const bool usual = valid >= 4 && __vcmpgeu4(bytes, 0x71717171u) == 0xFFFFFFFFu &&
+                         __vcmpleu4(bytes, 0x86868686u) == 0xFFFFFFFFu;
+      if (__all_sync(0xffffffffu, usual)) return 127;
+      unsigned top = static_cast<unsigned>(least);
+#pragma unroll 1
       for (int k = 0; k < 4; ++k) {
-        e[k] = static_cast<int>((bytes >> (8 * k)) & 255u);
-        if (e[k] != kScaleNaN) e[k] = min(e[k], kScaleMax + 127);
-        if (k < valid && e[k] != kScaleNaN) top = max(top, e[k]);
+        const unsigned e = (bytes >> (8 * k)) & 255u;
+        if (k < valid && e != kScaleNaN) top = max(top, min(e, kScaleMax + 127u));
       }
-      top = max(static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top))), least);
-      uint32_t h[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int x = e[k] - top;  // <= 0 but for a NaN's mark
-        h[k] = x >= -14 ? static_cast<uint32_t>((x + 15) << 10) : (x >= -24 ? 1u << (x + 24) : 0u);
-        if (e[k] == kScaleNaN) h[k] = 0x7E00u;
-        if (k >= valid) h[k] = 0u;
-      }
-      f[0] = h[0] | h[1] << 16;
-      f[1] = h[2] | h[3] << 16;
-      return top;
+      // 128 in place of 127, whose factors are those above
+      const int t = static_cast<int>(__reduce_max_sync(0xffffffffu, top));
+      return t == 127 ? 128 : t;
     };
-    auto convert_tile = [&](uint32_t dst, const uint32_t(&f)[2], int j) {
-      const int which = row8 & 3;
+    // Writes the factors 2^(E - Et) of the warp's rows: 0 for rows behind the sequence, a NaN
+    // for rows marked so.
+    auto write_factors = [&](uint32_t bytes, int j, int top) {
+      if ((lane >> 3) == wx) {
+        uint32_t f[2];
+        if (top == 127) {  // bits (E + 15) << 10
+          f[0] = (prmt(bytes, 0u, 0x4140u) - 0x00700070u) << 10;
+          f[1] = (prmt(bytes, 0u, 0x4342u) - 0x00700070u) << 10;
+        } else {
+          const int valid = w.u.s.len - (j * kTile + lane * 4);
+          f[0] = f[1] = 0u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int e = static_cast<int>((bytes >> (8 * k)) & 255u);
+            const int x = min(e, kScaleMax + 127) - top;  // <= 0
+            uint32_t h = x >= -14 ? static_cast<uint32_t>((x + 15) << 10)
+                                  : (x >= -24 ? 1u << (x + 24) : 0u);
+            if (e == kScaleNaN) h = 0x7E00u;
+            if (k >= valid) h = 0u;
+            f[k >> 1] |= h << (16 * (k & 1));
+          }
+        }
+        st_shared_v2(sF + (lane & 7) * 8, f[0], f[1]);
+      }
+      __syncwarp();
+    };
+    auto convert_tile = [&](uint32_t dst, int j) {
       const int valid = w.u.s.len - j * kTile;
       const uint32_t src = sC + cs * L::kCodeBytes;
 #pragma unroll
       for (int rg = 0; rg < 4; ++rg) {
         const int row = r0 + rg * 8 + row8;
-        const int from = wx * 8 + rg * 2 + (lane >> 4);  // the lane that has this row's factor
-        const uint32_t f0 = __shfl_sync(0xffffffffu, f[0], from);
-        const uint32_t f1 = __shfl_sync(0xffffffffu, f[1], from);
-        const uint32_t fx = prmt(which & 2 ? f1 : f0, 0u, which & 1 ? 0x3232u : 0x1010u);
+        const uint32_t fx = prmt(ld_shared_u16(sF + (rg * 8 + row8) * 2), 0u, 0x1010u);
 #pragma unroll
         for (int c = 0; c < L::kChunks; ++c) {
           const int cc = L::kChunks == 2 ? (c ^ (row8 & 1)) : 0;
           uint4 y = ld_shared_v4(src + row * D + cc * 64 + u * 16);
-          if (row >= valid) y = make_uint4(0u, 0u, 0u, 0u);  // a page may hold any code there
+          // a page may hold any code behind the sequence (7F times 0 would be a NaN)
+          if (valid < kTile && row >= valid) y = make_uint4(0u, 0u, 0u, 0u);
           const uint32_t line = dst + cc * 16384 + row * 128;
           uint32_t o[8];
           e4m3_to_f16(y.x, o[0], o[1]);
@@ -622,7 +640,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     };
     do {
       // K_0, Q, K_1, V_0, K_2, V_1, ...: the order in which the producer stages them
-      uint32_t vb = 0, vb_next = 0;  // scale bytes of V's rows, in the next V tile and after it
+      int ev = 127, ev_next = 127;  // Et + 127 of the next V tile and of the one after it
       for (int x = 0; ok && x < 2 * w.nt; ++x) {
         const bool is_k = x == 0 || ((x & 1) != 0 && x != 2 * w.nt - 1);
         const int j = w.j0 + (is_k ? (x + 1) >> 1 : (x - 1) >> 1);
@@ -632,22 +650,23 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           ok = false;
           break;
         }
-        // Et at least -40 and -60: the factors that the softmax makes of them stay normal
-        uint32_t f[2];
+        const uint32_t sb = sB + cs * 2 * kTile + lane * 4;
+        const uint32_t v_bytes = ld_shared_u32(sb + kTile);
         if (is_k) {
-          vb_next = ld_shared_u32(sB + cs * 2 * kTile + kTile + lane * 4);
-          if (x == 0) vb = vb_next;
-          const int ev = factors(vb_next, j, 127 - 60, f);
-          const int ek = factors(ld_shared_u32(sB + cs * 2 * kTile + lane * 4), j, 127 - 40, f);
+          const uint32_t k_bytes = ld_shared_u32(sb);
+          const int ek = top_of(k_bytes, j, 127 - 40);
+          ev_next = top_of(v_bytes, j, 127 - 60);
+          if (x == 0) ev = ev_next;
           if (wx == 0 && lane == 0)
-            reinterpret_cast<float4*>(smem + L::kScaleOff)[tile & (L::kSlots - 1)] = make_float4(
-                pow2i(ek - 127), static_cast<float>(ev - 127), pow2i(127 - ev), 0.f);
+            reinterpret_cast<float4*>(smem + L::kScaleOff)[tile & (L::kSlots - 1)] =
+                make_float4(pow2i(ek - 127), static_cast<float>(ev_next - 127), pow2i(127 - ev_next), 0.f);
           ++tile;
+          write_factors(k_bytes, j, ek);
         } else {
-          factors(vb, j, 127 - 60, f);
-          vb = vb_next;
+          write_factors(v_bytes, j, ev);
+          ev = ev_next;
         }
-        convert_tile((is_k ? sK + ks * L::kTileBytes : sV + vs * L::kTileBytes), f, j);
+        convert_tile((is_k ? sK + ks * L::kTileBytes : sV + vs * L::kTileBytes), j);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {  // the codes have been read, the tile is complete
@@ -671,14 +690,29 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   } else if (warp >= kSoftmaxWarps) {
     regs_dec<L::kRegsAux>();
     const int n_box = kTile / box_rows;  // boxes of a key tile
-    // Pages of 16-row groups: lane l has group l % 8 of key tile j + l / 8, so that one load
-    // serves four tiles. num_pages, which lies outside the maps and reads as zeros, behind
-    // the sequence and for a page that is none.
-    auto pages_of = [&](int j) {
+    // Pages of 16-row groups, and the rows in them: lane l has group l % 8 of key tile j + l / 8,
+    // so that one load serves four tiles. num_pages, which lies outside the maps and reads
+    // as zeros, behind the sequence and for a page that is none.
+    struct Rows {
+      int page, slot;
+    };
+    auto rows_of = [&](int j) {
       const int pos = (j + (lane >> 3)) * kTile + (lane & 7) * 16;
-      if (pos >= w.u.s.len) return args.c.num_pages;
-      const int p = paged_page(args.c, w.u.b, pos);
-      return p >= 0 ? p : args.c.num_pages;
+      Rows r;
+      r.page = args.c.num_pages;
+      r.slot = pos % args.c.page_size;
+      if (pos < w.u.s.len) {
+        const int p = paged_page(args.c, w.u.b, pos);
+        if (p >= 0) r.page = p;
+      }
+      return r;
+    };
+    auto rows_at = [&](const Rows& r, int tile, int group) {
+      const int from = (tile & 3) * 8 + (group & 7);
+      Rows x;
+      x.page = __shfl_sync(0xffffffffu, r.page, from);
+      x.slot = __shfl_sync(0xffffffffu, r.slot, from);
+      return x;
     };
     const int groups = box_rows / 16;
     if (!E4M3 && (warp == kKWarp || warp == kVWarp)) {
@@ -692,11 +726,11 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       uint32_t it = 0, s = 0, ph = 1, tails = 0;
       bool ok = true;
       do {
-        int pages = 0;
+        Rows rows = {0, 0};
         for (int i = 0; i < w.nt; ++i) {
           const int j = w.j0 + i;
-          if ((i & 3) == 0) pages = pages_of(j);
-          const int page = __shfl_sync(0xffffffffu, pages, (i & 3) * 8 + (lane * groups & 7));
+          if ((i & 3) == 0) rows = rows_of(j);
+          const Rows box = rows_at(rows, i, lane * groups);
           if (!mbar_wait_warp(empty[s], ph, tmo, abort_flag)) {
             fail();
             ok = false;
@@ -711,9 +745,9 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           if (lane == 0) mbar_expect_tx(bar, L::kTileBytes);
           __syncwarp();
           if (lane < n_box) {
-            const int slot = (j * kTile + lane * box_rows) % args.c.page_size;
             for (int c = 0; c < L::kChunks; ++c)
-              tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, slot, w.u.h, page, bar);
+              tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, box.slot, w.u.h,
+                          box.page, bar);
           }
           __syncwarp();
           if (tail) {
@@ -745,57 +779,52 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         if (it > x) mbar_wait_warp(full[x], ((it - 1 - x) / L::kStages) & 1, tmo, nullptr);
     } else if (E4M3 && warp == kKWarp) {
       // ------------------------------------------------------------ producer, e4m3
-      // Tiles of codes in the order K_0, K_1, V_0, K_2, V_1, ...; with K's tile come the
-      // scale bytes of K's and V's rows, 16 of a page at a time.
+      // Tiles of codes in the order K_0, K_1, V_0, K_2, V_1, ..., with the rows' scale bytes, 16
+      // of a page at a time: K's and V's with K's tile (what a tile's scales come to is settled
+      // when K is converted), V's again with V's.
       if (lane == 0) {
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
       }
       const uint32_t sC = smem_u32(smem + L::kCOff);
       const uint32_t sB = smem_u32(smem + L::kBytesOff);
+      const uint8_t* scales = lane < 8 ? args.c.k_scale : args.c.v_scale;
       uint32_t it = 0, s = 0, ph = 1;
-      auto stage = [&](int j, bool is_k, int pages, int i) -> bool {
-        const int box_page = __shfl_sync(0xffffffffu, pages, (i & 3) * 8 + (lane * groups & 7));
-        const int row_page = __shfl_sync(0xffffffffu, pages, (i & 3) * 8 + (lane & 7));
-        if (!mbar_wait_warp(bars.c_empty[s], ph, tmo, abort_flag)) return false;
-        const uint32_t bytes = sB + s * 2 * kTile + lane * 16;  // lanes 0-7: K's, 8-15: V's
-        const bool there = lane < 16 && is_k && row_page < args.c.num_pages;
-        // no page: its codes read as zeros, and so do its scales
-        if (lane < 16 && is_k && !there) st_shared_v4(bytes, 0u, 0u, 0u, 0u);
-        const int copies = __popc(__ballot_sync(0xffffffffu, there));
-        if (lane == 0) mbar_expect_tx(bars.c_full[s], L::kCodeBytes + copies * 16);
-        __syncwarp();
-        if (lane < n_box)
-          tma_load_4d(sC + s * L::kCodeBytes + lane * box_rows * D, is_k ? &tm_k : &tm_v, 0,
-                      (j * kTile + lane * box_rows) % args.c.page_size, w.u.h, box_page,
-                      bars.c_full[s]);
-        if (there) {
-          const long long at = (static_cast<long long>(row_page) * args.c.Hkv + w.u.h) *
-                                   args.c.page_size + (j * kTile + (lane & 7) * 16) % args.c.page_size;
-          bulk_load(bytes, (lane < 8 ? args.c.k_scale : args.c.v_scale) + at, 16, bars.c_full[s]);
-        }
-        __syncwarp();
-        ++it;
-        if (++s == L::kCStages) {
-          s = 0;
-          ph ^= 1u;
-        }
-        return true;
-      };
       bool ok = true;
       do {
-        int pages = 0, ahead = 0;  // of tiles j0 + 4 n .. of V's, and of K's, a tile ahead
-        if (w.nt > 0) {
-          pages = ahead = pages_of(w.j0);
-          ok = stage(w.j0, true, ahead, 0);
-        }
-        for (int i = 0; ok && i < w.nt; ++i) {
-          if ((i & 3) == 0) pages = ahead;
-          if (i + 1 < w.nt) {
-            if (((i + 1) & 3) == 0) ahead = pages_of(w.j0 + i + 1);
-            ok = stage(w.j0 + i + 1, true, ahead, i + 1);
+        Rows k_rows = {0, 0}, v_rows = {0, 0};
+        for (int x = 0; ok && x < 2 * w.nt; ++x) {
+          const bool is_k = x == 0 || ((x & 1) != 0 && x != 2 * w.nt - 1);
+          const int i = is_k ? (x + 1) >> 1 : (x - 1) >> 1;
+          if (is_k && (i & 3) == 0) k_rows = rows_of(w.j0 + i);
+          if (!is_k && (i & 3) == 0) v_rows = x == 1 ? k_rows : rows_of(w.j0 + i);
+          const Rows& rows = is_k ? k_rows : v_rows;
+          const Rows box = rows_at(rows, i, lane * groups);
+          const Rows row = rows_at(rows, i, lane);
+          const bool there = row.page < args.c.num_pages;  // if not, zeros
+          const long long at =
+              there ? (static_cast<long long>(row.page) * args.c.Hkv + w.u.h) * args.c.page_size + row.slot
+                    : 0;
+          if (!mbar_wait_warp(bars.c_empty[s], ph, tmo, abort_flag)) {
+            ok = false;
+            break;
           }
-          ok = ok && stage(w.j0 + i, false, pages, i);
+          const uint32_t bar = bars.c_full[s];
+          if (lane < 16) {
+            if (is_k || lane >= 8) cp_async16(sB + s * 2 * kTile + lane * 16, scales + at, there);
+            cp_async_arrive(bar);
+          }
+          if (lane == 0) mbar_expect_tx(bar, L::kCodeBytes);
+          __syncwarp();
+          if (lane < n_box)
+            tma_load_4d(sC + s * L::kCodeBytes + lane * box_rows * D, is_k ? &tm_k : &tm_v, 0, box.slot,
+                        w.u.h, box.page, bar);
+          __syncwarp();
+          ++it;
+          if (++s == L::kCStages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
       } while (ok && w.next(args));
       if (!ok) fail();
