@@ -14,12 +14,11 @@
 //   warps 0-3, 4-7  softmax warpgroups g = 0, 1: key tiles at even and odd positions of a
 //                   piece (thread = query row), each with its own m, l, O in tensor memory;
 //                   the epilogue merges the two
-//   warp 8          Q, and K tiles (bf16: into the K ring; e4m3: code tiles of K and V into
-//                   the staging ring), one box per page (or 16 .. 128 rows of it)
-//   warp 9, 10      S issuer, PV issuer (one lane each)
-//   warp 11         V tiles (bf16)
-//   warps 12-15     e4m3 only: turn staged codes into the bf16 tiles that the products read,
-//                   exactly, with the rows' scales folded in; all else is as for bf16
+//   warps 8, 11     K and V tiles, one TMA box per page (or 16 .. 128 rows of it): into the K
+//                   and V rings, or codes into staging rings (e4m3)
+//   warps 9, 10     S issuer, which also loads Q, and PV issuer (one lane each)
+//   warps 12-19     e4m3 only: turn staged codes, and Q, into f16 tiles with the rows' scales
+//                   folded in; the products then run in f16, and P is f16 too
 // Keys behind a sequence are masked by their number; V's rows there are made zero, since a
 // weight of zero would not hide a NaN.
 //
@@ -39,52 +38,55 @@ constexpr int kKWarp = 8;
 constexpr int kSIssuer = 9;
 constexpr int kPvIssuer = 10;
 constexpr int kVWarp = 11;
-constexpr int kConvWarp = 12;  // first of four (e4m3)
+constexpr int kConvWarp = 12;  // first of the converters (e4m3)
+constexpr int kConvWarps = 8;
 constexpr float kRescale = 8.0f;  // log2 units: rescale O when m grows by > 2^8
 
 template <int D, bool E4M3>
 struct ChunkL {
-  static constexpr int kWarps = E4M3 ? 16 : 12;
+  static constexpr int kWarps = E4M3 ? kConvWarp + kConvWarps : 12;
   static constexpr int kThreads = kWarps * 32;
   // Registers per thread at launch, and as the warpgroups share them out afterwards.
-  static constexpr int kRegsLaunch = E4M3 ? 128 : 168;
-  static constexpr int kRegsSoftmax = E4M3 ? 176 : 216;
+  static constexpr int kRegsLaunch = E4M3 ? 96 : 168;
+  static constexpr int kRegsSoftmax = E4M3 ? 144 : 216;
   static constexpr int kRegsAux = E4M3 ? 64 : 72;   // producers and issuers
-  static constexpr int kRegsConv = E4M3 ? 96 : 0;   // converters
-  static_assert(256 * kRegsSoftmax + 128 * (kRegsAux + kRegsConv) <= kThreads * kRegsLaunch,
+  static constexpr int kRegsConv = E4M3 ? 64 : 0;   // converters
+  static_assert(256 * kRegsSoftmax + 128 * kRegsAux + (kThreads - 384) * kRegsConv <=
+                    kThreads * kRegsLaunch,
                 "register reallocation exceeds the block's launch allocation");
   static constexpr int kTileBytes = kTile * D * 2;   // a 128 x D 16-bit tile
   static constexpr int kPBytes = kTile * kTile * 2;  // P_g
   static constexpr int kChunks = D / 64;             // 64-column (128-byte) swizzle chunks
-  // Ring depths. e4m3 at d = 128 has one K and one V tile: K is converted a tile ahead of V,
-  // so that only the PV product waits for a conversion after it, and the room goes to staged
-  // tiles of codes, which keep HBM busy.
+  // Ring depths. e4m3 at d = 128 has one K and one V tile: K is free again once its S product
+  // has run, and the room goes to staged tiles of codes.
   static constexpr int kStages = D == 64 ? (E4M3 ? 2 : 4) : (E4M3 ? 1 : 2);
-  static constexpr int kCStages = E4M3 ? (D == 64 ? 8 : 3) : 0;  // staged tiles of codes
+  static constexpr int kCkStages = E4M3 ? (D == 64 ? 4 : 2) : 0;  // staged tiles of codes
+  static constexpr int kCvStages = E4M3 ? (D == 64 ? 4 : 1) : 0;
   static constexpr int kCodeBytes = kTile * D;
-  static constexpr int kMaxStages = 4;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kTileBytes;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
   static constexpr int kPOff = kVOff + kStages * kTileBytes;
   static constexpr int kCOff = kPOff + 2 * kPBytes;
-  static constexpr int kBarOff = kCOff + kCStages * kCodeBytes;
-  // q_full, q_empty, q_ready, K and V rings (full, empty), staging ring (full, empty),
+  static constexpr int kCvOff = kCOff + kCkStages * kCodeBytes;
+  static constexpr int kBarOff = kCvOff + kCvStages * kCodeBytes;
+  // q_full, q_empty, q_ready, K and V rings (full, empty), their staging rings (full, empty),
   // s_full[2], s_free[2], p_full[2], pv_done[2], o_free, xbar[4], v_tail, drain, drain2, stall
-  static constexpr int kNumBars = 3 + 4 * kMaxStages + 2 * kCStages + 8 + 1 + 4 + 4;
+  static constexpr int kNumBars = 3 + 4 * kStages + 2 * (kCkStages + kCvStages) + 8 + 1 + 4 + 4;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;          // abort flag, TMEM address
-  // e4m3: the scale bytes of staged tiles (K's, then V's); the scales of the latest
-  // tiles and Q's row exponents of the latest pieces, for the softmax. Tile n's slot is
-  // written when K's tile n is converted, after V's tile n - 2, which waited for the PV
-  // product of tile n - 2 - kStages: by then the softmax has read the slot of every tile up
-  // to that one, and n - kSlots is one of them. Pieces have a tile or more each.
+  // e4m3: the scale bytes of staged tiles (K's stages: K's and V's; V's stages: V's); the
+  // scales of the latest tiles and Q's row exponents of the latest pieces, for the softmax.
+  // Tile n's slot is written when K's tile n is converted, so after the S product of tile n -
+  // kStages; that one waited until the softmax had read S, and before it the slot, of tile n -
+  // kStages - 2 at least. A piece's exponents are written after all S products of the piece
+  // before, so when both warpgroups have left the piece before that one's predecessor.
   static constexpr int kSlots = E4M3 ? 4 : 0;
   static_assert(!E4M3 || kSlots >= 2 + kStages, "a slot is rewritten before it is read");
   static constexpr int kBytesOff = (kMiscOff + 16 + 15) / 16 * 16;
-  static constexpr int kScaleOff = kBytesOff + 2 * kTile * kCStages;
+  static constexpr int kScaleOff = kBytesOff + kTile * (2 * kCkStages + kCvStages);
   static constexpr int kQExpOff = kScaleOff + 16 * kSlots;
-  static constexpr int kFactorOff = kQExpOff + kTile * kSlots;  // 128 f16 factors
-  static constexpr int kXchOff = kFactorOff + (E4M3 ? 2 * kTile : 0);  // (m, l) per warpgroup and row
+  static constexpr int kFactorOff = kQExpOff + kTile * kSlots;  // f16 factors of K's and V's rows
+  static constexpr int kXchOff = kFactorOff + (E4M3 ? 4 * kTile : 0);  // (m, l) per warpgroup and row
   // the plan's scratch is used before the exchange area is
   static constexpr int kPlanOff = kXchOff;
   static constexpr int kSmemBytes = kXchOff + 2 * kTile * 8;
@@ -95,7 +97,8 @@ struct ChunkL {
 
 struct Bars {
   uint32_t q_full, q_empty, q_ready;
-  BarRun k_full, k_empty, v_full, v_empty, c_full, c_empty;  // ring stages
+  BarRun k_full, k_empty, v_full, v_empty;      // ring stages
+  BarRun ck_full, ck_empty, cv_full, cv_empty;  // staging rings (e4m3)
   BarRun s_full, s_free, p_full, pv_done;   // per softmax warpgroup
   uint32_t o_free;
   BarRun xbar;
@@ -422,12 +425,14 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     bars.q_full = nb();
     bars.q_empty = nb();
     bars.q_ready = nb();
-    bars.k_full = run(L::kMaxStages);
-    bars.k_empty = run(L::kMaxStages);
-    bars.v_full = run(L::kMaxStages);
-    bars.v_empty = run(L::kMaxStages);
-    bars.c_full = run(L::kCStages);
-    bars.c_empty = run(L::kCStages);
+    bars.k_full = run(L::kStages);
+    bars.k_empty = run(L::kStages);
+    bars.v_full = run(L::kStages);
+    bars.v_empty = run(L::kStages);
+    bars.ck_full = run(L::kCkStages);
+    bars.ck_empty = run(L::kCkStages);
+    bars.cv_full = run(L::kCvStages);
+    bars.cv_empty = run(L::kCvStages);
     bars.s_full = run(2);
     bars.s_free = run(2);
     bars.p_full = run(2);
@@ -444,16 +449,21 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     mbar_init(bars.q_full, 1);
     mbar_init(bars.q_empty, 1);
     mbar_init(bars.q_ready, 4);
-    for (int s = 0; s < L::kMaxStages; ++s) {
-      // e4m3: the four converter warps arrive; bf16: the producer, with the bytes expected
+    for (int s = 0; s < L::kStages; ++s) {
+      // e4m3: K's or V's four converter warps arrive; bf16: the producer, with the bytes expected
       mbar_init(bars.k_full[s], E4M3 ? 4 : 1);
       mbar_init(bars.v_full[s], E4M3 ? 4 : 1);
       mbar_init(bars.k_empty[s], 1);
       mbar_init(bars.v_empty[s], 1);
     }
-    for (int s = 0; s < L::kCStages; ++s) {
-      mbar_init(bars.c_full[s], 17);  // the producer's lane 0, and 16 lanes for their scale bytes
-      mbar_init(bars.c_empty[s], 4);  // a lane of each converter warp
+    // staged tiles: the producer's lane 0, and the lanes that copy scale bytes
+    for (int s = 0; s < L::kCkStages; ++s) {
+      mbar_init(bars.ck_full[s], 17);
+      mbar_init(bars.ck_empty[s], 4);
+    }
+    for (int s = 0; s < L::kCvStages; ++s) {
+      mbar_init(bars.cv_full[s], 9);
+      mbar_init(bars.cv_empty[s], 4);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(bars.s_full[g], 1);
@@ -511,23 +521,31 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   if (E4M3 && warp >= kConvWarp) {
     regs_dec<E4M3 ? L::kRegsConv : 24>();
     // ------------------------------------------------------------ converters
-    // Warp x takes rows 32 x .. 32 x + 31 of every tile: staged codes, as f16 into the tiles
-    // that the products read. A row's scale 2^E is folded in relative to the tile's largest,
+    // Four warps for K's tiles, four for V's (and for Q); warp x of them takes rows 32 x .. of
+    // every tile: staged codes, as f16 into the tiles that the products read. A row's scale 2^E is folded in relative to the tile's largest,
     // 2^Et: code * 2^(E - Et) is exact in f16 down to E - Et = -15, and off by at most 2^-25
     // below, 2^-33 of the largest value that the tile's codes can stand for. The softmax
     // takes 2^Et into account. (Codes come by TMA, not by loads of these warps: a barrier
     // arrival waits for a thread's loads in flight, so none could be ahead.)
     // A pass covers 16 codes for each of 4 lanes of 8 rows, odd rows at the other half of the
     // row (d = 128), so that 8 lanes load, and store, on different banks.
-    const int wx = warp - kConvWarp;
+    const bool is_k = warp < kConvWarp + 4;
+    const int wx = (warp - kConvWarp) & 3;
     const int r0 = wx * 32;
     const int row8 = lane >> 2, u = lane & 3;
-    const uint32_t sC = smem_u32(smem + L::kCOff);
-    const uint32_t sB = smem_u32(smem + L::kBytesOff);
-    uint32_t cs = 0, cph = 0, ks = 0, kph = 1, vs = 0, vph = 1, tile = 0, q_cnt = 0;
+    const uint32_t c_ring = smem_u32(smem + (is_k ? L::kCOff : L::kCvOff));
+    const uint32_t ring = is_k ? sK : sV;
+    // scale bytes: of K and V in K's stages, of V in V's
+    const uint32_t bytes = smem_u32(smem + L::kBytesOff) + (is_k ? 0 : 2 * kTile * L::kCkStages);
+    const BarRun c_full = is_k ? bars.ck_full : bars.cv_full;
+    const BarRun c_empty = is_k ? bars.ck_empty : bars.cv_empty;
+    const BarRun full = is_k ? bars.k_full : bars.v_full;
+    const BarRun empty = is_k ? bars.k_empty : bars.v_empty;
+    const uint32_t c_stages = is_k ? L::kCkStages : L::kCvStages;
+    uint32_t cs = 0, cph = 0, ts = 0, tph = 1, tile = 0, q_cnt = 0;
     bool ok = true;
-    // The factors of the warp's 32 rows, f16, for its conversion.
-    const uint32_t sF = smem_u32(smem + L::kFactorOff) + wx * 64;
+    // The factors of the warp's rows, f16, for its conversion.
+    const uint32_t sF = smem_u32(smem + L::kFactorOff) + (is_k ? 0 : 2 * kTile) + r0 * 2;
     // Et + 127 of a tile from the lane's four scale bytes (rows 4 lane ..). 127 if all of the
     // tile's rows are there with E of -14 .. 7, as those of a cache in use are: their factors
     // 2^E are normal in f16 as they stand. Else the largest, at least `least`, so that the
@@ -575,7 +593,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     };
     auto convert_tile = [&](uint32_t dst, int j) {
       const int valid = w.u.s.len - j * kTile;
-      const uint32_t src = sC + cs * L::kCodeBytes;
+      const uint32_t src = c_ring + cs * L::kCodeBytes;
 #pragma unroll
       for (int rg = 0; rg < 4; ++rg) {
         const int row = r0 + rg * 8 + row8;
@@ -599,7 +617,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         }
       }
     };
-    // Q's rows 32 wx .. of the piece, bf16 -> f16 in place, each times 2^k that puts its
+    // The warp's rows of Q, bf16 -> f16 in place, each times 2^k that puts its
     // largest magnitude into [2^14, 2^15): f16 then holds all that bf16 held but for elements
     // below 2^-29 of it. (k is at most 60, which keeps the score's factor a normal number.)
     auto do_q = [&]() -> bool {
@@ -639,51 +657,40 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       return true;
     };
     do {
-      // K_0, Q, K_1, V_0, K_2, V_1, ...: the order in which the producer stages them
-      int ev = 127, ev_next = 127;  // Et + 127 of the next V tile and of the one after it
-      for (int x = 0; ok && x < 2 * w.nt; ++x) {
-        const bool is_k = x == 0 || ((x & 1) != 0 && x != 2 * w.nt - 1);
-        const int j = w.j0 + (is_k ? (x + 1) >> 1 : (x - 1) >> 1);
-        const uint32_t empty = is_k ? bars.k_empty[ks] : bars.v_empty[vs];
-        if (!mbar_wait_warp(bars.c_full[cs], cph, tmo, abort_flag) ||
-            !mbar_wait_warp(empty, is_k ? kph : vph, tmo, abort_flag)) {
+      if (!is_k && w.nt > 0) ok = do_q();
+      for (int i = 0; ok && i < w.nt; ++i) {
+        const int j = w.j0 + i;
+        if (!mbar_wait_warp(c_full[cs], cph, tmo, abort_flag) ||
+            !mbar_wait_warp(empty[ts], tph, tmo, abort_flag)) {
           ok = false;
           break;
         }
-        const uint32_t sb = sB + cs * 2 * kTile + lane * 4;
-        const uint32_t v_bytes = ld_shared_u32(sb + kTile);
-        if (is_k) {
-          const uint32_t k_bytes = ld_shared_u32(sb);
-          const int ek = top_of(k_bytes, j, 127 - 40);
-          ev_next = top_of(v_bytes, j, 127 - 60);
-          if (x == 0) ev = ev_next;
-          if (wx == 0 && lane == 0)
+        const uint32_t sb = bytes + cs * (is_k ? 2 * kTile : kTile) + lane * 4;
+        const uint32_t mine = ld_shared_u32(sb);
+        const int top = top_of(mine, j, is_k ? 127 - 40 : 127 - 60);
+        write_factors(mine, j, top);
+        convert_tile(ring + ts * L::kTileBytes, j);
+        if (is_k && wx == 0) {
+          const int ev = top_of(ld_shared_u32(sb + kTile), j, 127 - 60) - 127;  // V's, as V's warps find it
+          if (lane == 0)
             reinterpret_cast<float4*>(smem + L::kScaleOff)[tile & (L::kSlots - 1)] =
-                make_float4(pow2i(ek - 127), static_cast<float>(ev_next - 127), pow2i(127 - ev_next), 0.f);
+                make_float4(pow2i(top - 127), static_cast<float>(ev), pow2i(-ev), 0.f);
           ++tile;
-          write_factors(k_bytes, j, ek);
-        } else {
-          write_factors(v_bytes, j, ev);
-          ev = ev_next;
         }
-        convert_tile((is_k ? sK + ks * L::kTileBytes : sV + vs * L::kTileBytes), j);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {  // the codes have been read, the tile is complete
-          mbar_arrive(bars.c_empty[cs]);
-          mbar_arrive(is_k ? bars.k_full[ks] : bars.v_full[vs]);
+          mbar_arrive(c_empty[cs]);
+          mbar_arrive(full[ts]);
         }
-        if (++cs == L::kCStages) {
+        if (++cs == c_stages) {
           cs = 0;
           cph ^= 1u;
         }
-        uint32_t& at = is_k ? ks : vs;
-        uint32_t& phase = is_k ? kph : vph;
-        if (++at == L::kStages) {
-          at = 0;
-          phase ^= 1u;
+        if (++ts == L::kStages) {
+          ts = 0;
+          tph ^= 1u;
         }
-        if (x == 0) ok = do_q();
       }
     } while (ok && w.next(args));
     if (!ok) fail();
@@ -715,14 +722,23 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       return x;
     };
     const int groups = box_rows / 16;
-    if (!E4M3 && (warp == kKWarp || warp == kVWarp)) {
-      // ------------------------------------------------------------ producers, bf16
+    if (warp == kKWarp || warp == kVWarp) {
+      // ------------------------------------------------------------ producers
+      // bf16: into the K or V ring. e4m3: codes into the staging ring, and the rows' scale
+      // bytes, 16 of a page at a time: K's and V's with K's tile (the softmax needs what a
+      // tile's scales come to before V is converted), V's again with V's.
       const bool is_k = warp == kKWarp;
       const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
       if (lane == 0) tma_prefetch_desc(tm);
-      const BarRun full = is_k ? bars.k_full : bars.v_full;
-      const BarRun empty = is_k ? bars.k_empty : bars.v_empty;
-      const uint32_t ring = is_k ? sK : sV;
+      const BarRun full = E4M3 ? (is_k ? bars.ck_full : bars.cv_full) : (is_k ? bars.k_full : bars.v_full);
+      const BarRun empty =
+          E4M3 ? (is_k ? bars.ck_empty : bars.cv_empty) : (is_k ? bars.k_empty : bars.v_empty);
+      const uint32_t ring = E4M3 ? smem_u32(smem + (is_k ? L::kCOff : L::kCvOff)) : (is_k ? sK : sV);
+      constexpr int kBytes = E4M3 ? L::kCodeBytes : L::kTileBytes;
+      const uint32_t stages = E4M3 ? (is_k ? L::kCkStages : L::kCvStages) : L::kStages;
+      const uint32_t scale_ring = smem_u32(smem + L::kBytesOff) + (is_k ? 0 : 2 * kTile * L::kCkStages);
+      const uint8_t* scales = is_k && lane < 8 ? args.c.k_scale : args.c.v_scale;
+      const int scale_lanes = is_k ? 16 : 8;
       uint32_t it = 0, s = 0, ph = 1, tails = 0;
       bool ok = true;
       do {
@@ -731,23 +747,41 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           const int j = w.j0 + i;
           if ((i & 3) == 0) rows = rows_of(j);
           const Rows box = rows_at(rows, i, lane * groups);
+          long long at = 0;
+          bool there = false;
+          if constexpr (E4M3) {
+            const Rows row = rows_at(rows, i, lane);
+            there = row.page < args.c.num_pages;  // if not, zeros
+            if (there)
+              at = (static_cast<long long>(row.page) * args.c.Hkv + w.u.h) * args.c.page_size + row.slot;
+          }
           if (!mbar_wait_warp(empty[s], ph, tmo, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          const uint32_t dst = ring + s * L::kTileBytes;
+          const uint32_t dst = ring + s * kBytes;
           const int valid = w.u.s.len - j * kTile;
           // V's last tile: rows of its last page behind the sequence may hold anything, so it
           // comes on a barrier of its own and is handed on once they have been cleared
-          const bool tail = !is_k && valid < kTile;
+          const bool tail = !E4M3 && !is_k && valid < kTile;
           const uint32_t bar = tail ? bars.v_tail : full[s];
-          if (lane == 0) mbar_expect_tx(bar, L::kTileBytes);
+          if constexpr (E4M3) {
+            if (lane < scale_lanes) {
+              cp_async16(scale_ring + s * scale_lanes * 16 + lane * 16, scales + at, there);
+              cp_async_arrive(bar);
+            }
+          }
+          if (lane == 0) mbar_expect_tx(bar, kBytes);
           __syncwarp();
           if (lane < n_box) {
-            for (int c = 0; c < L::kChunks; ++c)
-              tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, box.slot, w.u.h,
-                          box.page, bar);
+            if constexpr (E4M3) {
+              tma_load_4d(dst + lane * box_rows * D, tm, 0, box.slot, w.u.h, box.page, bar);
+            } else {
+              for (int c = 0; c < L::kChunks; ++c)
+                tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, box.slot, w.u.h,
+                            box.page, bar);
+            }
           }
           __syncwarp();
           if (tail) {
@@ -766,72 +800,17 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             if (lane == 0) mbar_arrive(full[s]);
           }
           ++it;
-          if (++s == L::kStages) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
         }
       } while (ok && w.next(args));
       // Drain: every load this warp issued must land before the CTA exits. Stage x was armed
-      // for ring positions x, x + kStages, ...; wait for the last one.
+      // for ring positions x, x + stages, ...; wait for the last one.
       if (tails > 0) mbar_wait_warp(bars.v_tail, (tails - 1) & 1, tmo, nullptr);
-      for (uint32_t x = 0; x < L::kStages; ++x)
-        if (it > x) mbar_wait_warp(full[x], ((it - 1 - x) / L::kStages) & 1, tmo, nullptr);
-    } else if (E4M3 && warp == kKWarp) {
-      // ------------------------------------------------------------ producer, e4m3
-      // Tiles of codes in the order K_0, K_1, V_0, K_2, V_1, ..., with the rows' scale bytes, 16
-      // of a page at a time: K's and V's with K's tile (what a tile's scales come to is settled
-      // when K is converted), V's again with V's.
-      if (lane == 0) {
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
-      }
-      const uint32_t sC = smem_u32(smem + L::kCOff);
-      const uint32_t sB = smem_u32(smem + L::kBytesOff);
-      const uint8_t* scales = lane < 8 ? args.c.k_scale : args.c.v_scale;
-      uint32_t it = 0, s = 0, ph = 1;
-      bool ok = true;
-      do {
-        Rows k_rows = {0, 0}, v_rows = {0, 0};
-        for (int x = 0; ok && x < 2 * w.nt; ++x) {
-          const bool is_k = x == 0 || ((x & 1) != 0 && x != 2 * w.nt - 1);
-          const int i = is_k ? (x + 1) >> 1 : (x - 1) >> 1;
-          if (is_k && (i & 3) == 0) k_rows = rows_of(w.j0 + i);
-          if (!is_k && (i & 3) == 0) v_rows = x == 1 ? k_rows : rows_of(w.j0 + i);
-          const Rows& rows = is_k ? k_rows : v_rows;
-          const Rows box = rows_at(rows, i, lane * groups);
-          const Rows row = rows_at(rows, i, lane);
-          const bool there = row.page < args.c.num_pages;  // if not, zeros
-          const long long at =
-              there ? (static_cast<long long>(row.page) * args.c.Hkv + w.u.h) * args.c.page_size + row.slot
-                    : 0;
-          if (!mbar_wait_warp(bars.c_empty[s], ph, tmo, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = bars.c_full[s];
-          if (lane < 16) {
-            if (is_k || lane >= 8) cp_async16(sB + s * 2 * kTile + lane * 16, scales + at, there);
-            cp_async_arrive(bar);
-          }
-          if (lane == 0) mbar_expect_tx(bar, L::kCodeBytes);
-          __syncwarp();
-          if (lane < n_box)
-            tma_load_4d(sC + s * L::kCodeBytes + lane * box_rows * D, is_k ? &tm_k : &tm_v, 0, box.slot,
-                        w.u.h, box.page, bar);
-          __syncwarp();
-          ++it;
-          if (++s == L::kCStages) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-      } while (ok && w.next(args));
-      if (!ok) fail();
-      constexpr int kC = E4M3 ? L::kCStages : 1;
-      for (int x = 0; x < kC; ++x)
-        if (it > static_cast<uint32_t>(x))
-          mbar_wait_warp(bars.c_full[x], ((it - 1 - x) / kC) & 1, tmo, nullptr);
+      for (uint32_t x = 0; x < stages; ++x)
+        if (it > x) mbar_wait_warp(full[x], ((it - 1 - x) / stages) & 1, tmo, nullptr);
     } else if (warp == kSIssuer) {
       // ------------------------------------------------------------ S issuer
       if (lane == 0) {
