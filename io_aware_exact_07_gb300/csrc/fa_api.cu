@@ -718,6 +718,13 @@ static fa_status paged_args(const void* k, const void* v, const uint8_t* ks, con
   a->v_scale = const_cast<uint8_t*>(vs);
   a->num_pages = num_pages;
   a->page_size = page_size;
+  // 2^(s - 1) < page_size <= 2^s: m = ceil(2^(31 + s) / page_size) has 32 bits, and the excess
+  // pos * (m * page_size - 2^(31 + s)) < 2^31 * page_size <= 2^(31 + s) of the product does
+  // not reach the next whole quotient.
+  int s = 0;
+  while ((1ll << s) < page_size) ++s;
+  a->page_mul = static_cast<unsigned>(((1ull << (31 + s)) + page_size - 1) / page_size);
+  a->page_shift = s - 1;
   a->Hkv = Hkv;
   a->d = d;
   a->stride_page = sp;

@@ -27,6 +27,8 @@ struct PagedArgs {
   uint8_t* k_scale;             // [num_pages, Hkv, page_size] scale bytes (e4m3), else null
   uint8_t* v_scale;
   int num_pages, page_size, Hkv, d;
+  unsigned page_mul;            // pos / page_size = pos * page_mul >> 32 + page_shift,
+  int page_shift;               // 0 <= pos < 2^31
   long long stride_page, stride_head, stride_row;  // in elements
   const int32_t* table;         // [B, max_pages], row b at b * table_stride
   long long table_stride;
@@ -78,10 +80,18 @@ __device__ __forceinline__ PagedSeq paged_attn_seq(const PagedArgs& a, int b) {
   return s;
 }
 
+__device__ __forceinline__ int page_index(const PagedArgs& a, int pos) {
+  return static_cast<int>(__umulhi(static_cast<unsigned>(pos), a.page_mul) >> a.page_shift);
+}
+// Row of position pos >= 0 in its page.
+__device__ __forceinline__ int page_row(const PagedArgs& a, int pos) {
+  return pos - page_index(a, pos) * a.page_size;
+}
+
 // Page that holds position pos of sequence b, or -1 (recorded) where the table
 // names none of the pool's pages.
 __device__ __forceinline__ int paged_page(const PagedArgs& a, int b, int pos) {
-  const int p = a.table[b * a.table_stride + pos / a.page_size];
+  const int p = a.table[b * a.table_stride + page_index(a, pos)];
   if (p >= 0 && p < a.num_pages) return p;
   record_error(a.status, kStatusInvalid);
   return -1;

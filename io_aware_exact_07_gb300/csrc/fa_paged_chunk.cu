@@ -57,31 +57,32 @@ struct ChunkL {
   static constexpr int kTileBytes = kTile * D * 2;   // a 128 x D 16-bit tile
   static constexpr int kPBytes = kTile * kTile * 2;  // P_g
   static constexpr int kChunks = D / 64;             // 64-column (128-byte) swizzle chunks
-  // Ring depths. e4m3 at d = 128 has one K and one V tile: K is free again once its S product
-  // has run, and the room goes to staged tiles of codes.
-  static constexpr int kStages = D == 64 ? (E4M3 ? 2 : 4) : (E4M3 ? 1 : 2);
+  // Ring depths. e4m3 at d = 128 has room for one K and one V tile (K's is free again once its
+  // S product has run) and three staged tiles of codes.
+  static constexpr int kKStages = D == 64 ? (E4M3 ? 2 : 4) : (E4M3 ? 1 : 2);
+  static constexpr int kVStages = kKStages;
   static constexpr int kCkStages = E4M3 ? (D == 64 ? 4 : 2) : 0;  // staged tiles of codes
   static constexpr int kCvStages = E4M3 ? (D == 64 ? 4 : 1) : 0;
   static constexpr int kCodeBytes = kTile * D;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kTileBytes;
-  static constexpr int kVOff = kKOff + kStages * kTileBytes;
-  static constexpr int kPOff = kVOff + kStages * kTileBytes;
+  static constexpr int kVOff = kKOff + kKStages * kTileBytes;
+  static constexpr int kPOff = kVOff + kVStages * kTileBytes;
   static constexpr int kCOff = kPOff + 2 * kPBytes;
   static constexpr int kCvOff = kCOff + kCkStages * kCodeBytes;
   static constexpr int kBarOff = kCvOff + kCvStages * kCodeBytes;
   // q_full, q_empty, q_ready, K and V rings (full, empty), their staging rings (full, empty),
   // s_full[2], s_free[2], p_full[2], pv_done[2], o_free, xbar[4], v_tail, drain, drain2, stall
-  static constexpr int kNumBars = 3 + 4 * kStages + 2 * (kCkStages + kCvStages) + 8 + 1 + 4 + 4;
+  static constexpr int kNumBars = 3 + 2 * (kKStages + kVStages) + 2 * (kCkStages + kCvStages) + 8 + 1 + 4 + 4;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;          // abort flag, TMEM address
   // e4m3: the scale bytes of staged tiles (K's stages: K's and V's; V's stages: V's); the
   // scales of the latest tiles and Q's row exponents of the latest pieces, for the softmax.
   // Tile n's slot is written when K's tile n is converted, so after the S product of tile n -
-  // kStages; that one waited until the softmax had read S, and before it the slot, of tile n -
-  // kStages - 2 at least. A piece's exponents are written after all S products of the piece
+  // kKStages; that one waited until the softmax had read S, and before it the slot, of tile n -
+  // kKStages - 2 at least. A piece's exponents are written after all S products of the piece
   // before, so when both warpgroups have left the piece before that one's predecessor.
   static constexpr int kSlots = E4M3 ? 4 : 0;
-  static_assert(!E4M3 || kSlots >= 2 + kStages, "a slot is rewritten before it is read");
+  static_assert(!E4M3 || kSlots >= 2 + kKStages, "a slot is rewritten before it is read");
   static constexpr int kBytesOff = (kMiscOff + 16 + 15) / 16 * 16;
   static constexpr int kScaleOff = kBytesOff + kTile * (2 * kCkStages + kCvStages);
   static constexpr int kQExpOff = kScaleOff + 16 * kSlots;
@@ -425,10 +426,10 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     bars.q_full = nb();
     bars.q_empty = nb();
     bars.q_ready = nb();
-    bars.k_full = run(L::kStages);
-    bars.k_empty = run(L::kStages);
-    bars.v_full = run(L::kStages);
-    bars.v_empty = run(L::kStages);
+    bars.k_full = run(L::kKStages);
+    bars.k_empty = run(L::kKStages);
+    bars.v_full = run(L::kVStages);
+    bars.v_empty = run(L::kVStages);
     bars.ck_full = run(L::kCkStages);
     bars.ck_empty = run(L::kCkStages);
     bars.cv_full = run(L::kCvStages);
@@ -449,11 +450,13 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     mbar_init(bars.q_full, 1);
     mbar_init(bars.q_empty, 1);
     mbar_init(bars.q_ready, 4);
-    for (int s = 0; s < L::kStages; ++s) {
-      // e4m3: K's or V's four converter warps arrive; bf16: the producer, with the bytes expected
+    // e4m3: K's or V's four converter warps arrive; bf16: the producer, with the bytes expected
+    for (int s = 0; s < L::kKStages; ++s) {
       mbar_init(bars.k_full[s], E4M3 ? 4 : 1);
-      mbar_init(bars.v_full[s], E4M3 ? 4 : 1);
       mbar_init(bars.k_empty[s], 1);
+    }
+    for (int s = 0; s < L::kVStages; ++s) {
+      mbar_init(bars.v_full[s], E4M3 ? 4 : 1);
       mbar_init(bars.v_empty[s], 1);
     }
     // staged tiles: the producer's lane 0, and the lanes that copy scale bytes
@@ -622,7 +625,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     // below 2^-29 of it. (k is at most 60, which keeps the score's factor a normal number.)
     auto do_q = [&]() -> bool {
       if (!mbar_wait_warp(bars.q_full, q_cnt & 1, tmo, abort_flag)) return false;
-      int8_t* q_exp = reinterpret_cast<int8_t*>(smem + L::kQExpOff) + (q_cnt & (L::kSlots - 1)) * kTile;
+      int8_t* q_exp = reinterpret_cast<int8_t*>(smem + L::kQExpOff) + (q_cnt & (L::kSlots - 1u)) * kTile;
       const int r4 = lane >> 3, v = lane & 7;
 #pragma unroll 1
       for (int pass = 0; pass < 8; ++pass) {
@@ -673,7 +676,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         if (is_k && wx == 0) {
           const int ev = top_of(ld_shared_u32(sb + kTile), j, 127 - 60) - 127;  // V's, as V's warps find it
           if (lane == 0)
-            reinterpret_cast<float4*>(smem + L::kScaleOff)[tile & (L::kSlots - 1)] =
+            reinterpret_cast<float4*>(smem + L::kScaleOff)[tile & (L::kSlots - 1u)] =
                 make_float4(pow2i(top - 127), static_cast<float>(ev), pow2i(-ev), 0.f);
           ++tile;
         }
@@ -687,7 +690,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           cs = 0;
           cph ^= 1u;
         }
-        if (++ts == L::kStages) {
+        if (++ts == (is_k ? L::kKStages : L::kVStages)) {
           ts = 0;
           tph ^= 1u;
         }
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       const int pos = (j + (lane >> 3)) * kTile + (lane & 7) * 16;
       Rows r;
       r.page = args.c.num_pages;
-      r.slot = pos % args.c.page_size;
+      r.slot = page_row(args.c, pos);
       if (pos < w.u.s.len) {
         const int p = paged_page(args.c, w.u.b, pos);
         if (p >= 0) r.page = p;
@@ -735,7 +738,8 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           E4M3 ? (is_k ? bars.ck_empty : bars.cv_empty) : (is_k ? bars.k_empty : bars.v_empty);
       const uint32_t ring = E4M3 ? smem_u32(smem + (is_k ? L::kCOff : L::kCvOff)) : (is_k ? sK : sV);
       constexpr int kBytes = E4M3 ? L::kCodeBytes : L::kTileBytes;
-      const uint32_t stages = E4M3 ? (is_k ? L::kCkStages : L::kCvStages) : L::kStages;
+      const uint32_t stages =
+          E4M3 ? (is_k ? L::kCkStages : L::kCvStages) : (is_k ? L::kKStages : L::kVStages);
       const uint32_t scale_ring = smem_u32(smem + L::kBytesOff) + (is_k ? 0 : 2 * kTile * L::kCkStages);
       const uint8_t* scales = is_k && lane < 8 ? args.c.k_scale : args.c.v_scale;
       const int scale_lanes = is_k ? 16 : 8;
@@ -876,7 +880,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             }
             mma_commit(bars.s_full[g]);
             mma_commit(bars.k_empty[s]);
-            if (++s == L::kStages) {
+            if (++s == L::kKStages) {
               s = 0;
               ph ^= 1u;
             }
@@ -940,7 +944,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             if (g) first1 = false; else first0 = false;
             mma_commit(bars.pv_done[g]);
             mma_commit(bars.v_empty[s]);
-            if (++s == L::kStages) {
+            if (++s == L::kVStages) {
               s = 0;
               ph ^= 1u;
             }
@@ -1025,15 +1029,17 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         float c_t = c_log2, ev = 0.f, ev_inv = 1.f;
         if constexpr (E4M3) {
           if (n_done == 0)
-            c_row = c_log2 * pow2i(-static_cast<int>(q_exp[(q_cnt & (L::kSlots - 1)) * kTile + t]));
-          const float4 z = tile_scale[(tile_cnt + p) & (L::kSlots - 1)];
+            c_row = c_log2 * pow2i(-static_cast<int>(q_exp[(q_cnt & (L::kSlots - 1u)) * kTile + t]));
+          const float4 z = tile_scale[(tile_cnt + p) & (L::kSlots - 1u)];
           c_t = c_row * z.x;
           ev = z.y;
           ev_inv = z.z;
         }
         // bf16: the whole row in registers at once. e4m3, where the converters need registers
-        // and instruction cache: half a row at a time, once for its maximum and once for P, in
-        // loops.
+        // and instruction cache: half a row at a time, once for its maximum and once for P (in
+        // loops at d = 128, where straight code took 2.2 us a tile instead of 1.8 and where the
+        // converters' code is twice as long; straight at d = 64, 1.2 us instead of 1.5).
+        constexpr int kUnroll = D == 64 ? 2 : 1;
         constexpr int kCols = E4M3 ? 64 : 128;
         float s[kCols];
         const bool edge = k0 < key_lo || k0 + kTile > key_hi;
@@ -1050,7 +1056,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           mbar_arrive(bars.s_free[g]);
         };
         float mx_row = -INFINITY;
-#pragma unroll 1
+#pragma unroll kUnroll
         for (int c0 = 0; c0 < kTile; c0 += kCols) {
           load_scores(c0);
           if constexpr (!E4M3) release_scores();
@@ -1102,7 +1108,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           }
         };
         if constexpr (E4M3) {
-#pragma unroll 1
+#pragma unroll kUnroll
           for (int half = 0; half < 2; ++half) {
             load_scores(half * 64);
             if (half == 1) release_scores();

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kIoWarps * 32) fa_paged_write_kernel(const Pag
   if (t < s.t0 || t >= s.t0 + s.nq || pos < 0) return;
   const int page = paged_page(a.c, b, pos);
   if (page < 0) return;
-  const int slot = pos % a.c.page_size;
+  const int slot = page_row(a.c, pos);
   const int u = lane % kLanes;  // 16-byte unit of the row
   for (int r0 = sub * kRows; r0 < 2 * a.c.Hkv; r0 += warps_per_token * kRows) {
     const int r = r0 + lane / kLanes;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kIoWarps * 32) fa_paged_read_kernel(const Page
   const int j0 = g * kReadRows;
   const int len = paged_seq(a.c, b).len;
   const int page = j0 < len ? paged_page(a.c, b, j0) : -1;
-  const int slot = j0 % a.c.page_size;
+  const int slot = page_row(a.c, j0);
   // rows of this group that the cache holds; the others are written as zeros
   const int have = page < 0 ? 0 : min(kReadRows, len - j0);
   const int rows = min(kReadRows, a.N - j0);

@@ -14,8 +14,12 @@
 //    at least 112 empty rows); keeping S and P in registers saves the handshakes that a
 //    short sequence cannot hide.
 //  - The order of the columns d within a product is free as long as both operands share
-//    it: a thread takes the 16 bytes of a row that it can load at once. e4m3 rows are
-//    turned into bf16 (exactly) between shared memory and the product, in registers.
+//    it: a thread takes the 16 bytes of a row that it can load at once.
+//  - e4m3 codes become f16 between shared memory and the product, which the hardware converts
+//    exactly; the products run in f16, with Q scaled by a power of two per row to fit. A key's
+//    K scale goes to its score, its V scale to its weight: P carries it (and the running
+//    maximum counts it), the softmax's sum takes it out again. Turning the codes into bf16
+//    with their scales, by integer operations, takes 2.5 instructions a code instead of 0.6.
 //  - The (sequence, K/V head, 128-key block) list is cut into equal runs, one per CTA, by
 //    the lengths found on the device. A head that falls into one run is written directly;
 //    one cut by a run's end leaves normalised pieces, merged by a second, small kernel with
@@ -80,13 +84,21 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+template <bool F16>
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   uint32_t r;
@@ -232,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
   auto issue = [&](int stage) {
     const int j = chunk_of(lw);
     const int have = lpage >= 0 ? lw.s.len - j : 0;  // rows of the chunk that the cache holds
-    const int slot = j % a.c.page_size;
+    const int slot = page_row(a.c, j);
     const int page = lpage >= 0 ? lpage : 0;
     const long long at = (page * a.c.stride_page + lw.h * a.c.stride_head +
                           (slot + lrow) * a.c.stride_row) * kEs + lunit * 16;
@@ -277,8 +289,36 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
       }
     }
   };
+  // What a row's scores are multiplied with: rows 2 c4, 2 c4 + 1 of each group of eight.
+  float c_row[NT][2];
+  // e4m3: Q's rows as f16, each times 2^k that puts its largest magnitude into [2^14, 2^15):
+  // f16 then holds all that bf16 held but for elements below 2^-29 of it.
+  auto ready_q = [&](uint32_t(&q)[NT][D / 8]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      c_row[n][0] = c_row[n][1] = a.scale_log2;
+      if constexpr (E4M3) {
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) m2 = __vmaxu2(m2, q[n][i] & 0x7FFF7FFFu);
+        uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int k = max(-114, min(60, 14 + 127 - static_cast<int>(top >> 7)));
+        const float f = pow2i(k);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          q[n][i] = pack_f16x2(__uint_as_float(q[n][i] << 16) * f,
+                               __uint_as_float(q[n][i] & 0xFFFF0000u) * f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          c_row[n][e] *= pow2i(-__shfl_sync(0xffffffffu, k, (2 * c4 + e) * 4));
+      }
+    }
+  };
   uint32_t q[NT][D / 8];
   load_q(cw, q);
+  ready_q(q);
 
   const long long steps = hi - lo;
 #pragma unroll
@@ -326,11 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
     const int key_min = a.wl >= 0 ? pos0 - a.wl : 0;
     if (j0 < cw.s.len && j0 + kChunk > key_min) {
       const uint32_t sk = ring + stage * L::kStageBytes, sv = sk + L::kTileBytes;
-      // factor of key k of the chunk (e4m3); behind the sequence, where the codes are filled
-      // with zeros and the scale byte may be anything, 0
-      auto factor = [&](uint32_t scales, int k) {
-        return j0 + k < cw.s.len ? e4m3_factor(ld_shared_u8(scales + k)) : 0u;
-      };
       // ---- S^T = K Q^T: keys g8 and g8 + 8, query rows 2 c4 and 2 c4 + 1
       float s[NT][4], s2[NT][4];  // two chains of products
 #pragma unroll
@@ -344,13 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
           const uint4 k1 = ld_shared_v4(sk + k_unit<D, E4M3>(g8 + 8, 4 * x + c4) * 16);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma16816(s[n], k0.x, k1.x, k0.y, k1.y, q[n][4 * x], q[n][4 * x + 1]);
-            mma16816(s2[n], k0.z, k1.z, k0.w, k1.w, q[n][4 * x + 2], q[n][4 * x + 3]);
+            mma16816<E4M3>(s[n], k0.x, k1.x, k0.y, k1.y, q[n][4 * x], q[n][4 * x + 1]);
+            mma16816<E4M3>(s2[n], k0.z, k1.z, k0.w, k1.w, q[n][4 * x + 2], q[n][4 * x + 3]);
           }
         }
       } else {
-        const uint32_t ss = scale_ring + stage * L::kScaleBytes;
-        const uint32_t f0 = factor(ss, g8), f1 = factor(ss, g8 + 8);
 #pragma unroll
         for (int x = 0; x < D / 64; ++x) {
           const uint4 k0 = ld_shared_v4(sk + k_unit<D, E4M3>(g8, 4 * x + c4) * 16);
@@ -358,21 +391,39 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
           const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const uint32_t a0 = e4m3_lo(w0[w], f0), a2 = e4m3_hi(w0[w], f0);
-            const uint32_t a1 = e4m3_lo(w1[w], f1), a3 = e4m3_hi(w1[w], f1);
+            uint32_t a0, a1, a2, a3;
+            e4m3_to_f16(w0[w], a0, a2);
+            e4m3_to_f16(w1[w], a1, a3);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-              mma16816(w & 1 ? s2[n] : s[n], a0, a1, a2, a3, q[n][8 * x + 2 * w],
+              mma16816<E4M3>(w & 1 ? s2[n] : s[n], a0, a1, a2, a3, q[n][8 * x + 2 * w],
                        q[n][8 * x + 2 * w + 1]);
           }
         }
       }
-      // ---- masks, running maximum, P
+      // ---- scores in log2 units, masks, running maximum, P. e4m3: keys g8 and g8 + 8 have K's
+      // scale, V's exponent, and what takes V's scale out of the sum (times 2^-64, so that the
+      // sum stays in range for the smallest scales; a scale byte of 0, which only a page that
+      // is none has, counts as 127).
+      float k_scale[2] = {1.f, 1.f}, v_exp[2] = {0.f, 0.f}, v_inv[2] = {1.f, 1.f};
+      if constexpr (E4M3) {
+        const uint32_t ss = scale_ring + stage * L::kScaleBytes + g8;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int kb = ld_shared_u8(ss + 8 * e);
+          int vb = ld_shared_u8(ss + 16 + 8 * e);
+          vb = vb == 0 ? 127 : min(vb, kScaleMax + 127);
+          k_scale[e] = kb == kScaleNaN ? __uint_as_float(0x7FC00000u) : pow2i(min(kb, kScaleMax + 127) - 127);
+          v_exp[e] = static_cast<float>(vb - 127);
+          v_inv[e] = pow2i(127 - 64 - vb);
+        }
+      }
       bool grow = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + s2[n][e]) * a.scale_log2;
+        for (int e = 0; e < 4; ++e)
+          s[n][e] = (s[n][e] + s2[n][e]) * (c_row[n][e & 1] * k_scale[e >> 1]) + v_exp[e >> 1];
       }
       const int last_lo = a.wl >= 0 ? cw.s.len - 1 - a.wl : 0;  // first key of the last token
       const int first_hi = a.causal ? pos0 + 1 : cw.s.len;      // end of the first token's keys
@@ -422,11 +473,17 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
           const float m = m_ref[n][e & 1];
           p[e] = ex2_approx(s[n][e] - (m == -INFINITY ? 0.f : m));
         }
-        l_sum[n][0] += p[0] + p[2];
-        l_sum[n][1] += p[1] + p[3];
-        // P is rounded to bf16 for the product (at most 2^-8 of each weight); the sum keeps fp32
-        p0[n] = movmatrix_t(pack_bf16x2(p[0], p[1]));
-        p1[n] = movmatrix_t(pack_bf16x2(p[2], p[3]));
+        if constexpr (E4M3) {
+          l_sum[n][0] = fmaf(p[0], v_inv[0], fmaf(p[2], v_inv[1], l_sum[n][0]));
+          l_sum[n][1] = fmaf(p[1], v_inv[0], fmaf(p[3], v_inv[1], l_sum[n][1]));
+        } else {
+          l_sum[n][0] += p[0] + p[2];
+          l_sum[n][1] += p[1] + p[3];
+        }
+        // P is rounded to bf16 for the product (at most 2^-8 of each weight), or to f16 (2^-11,
+        // and 2^-25 where it is below 2^-14); the sum keeps fp32
+        p0[n] = movmatrix_t(E4M3 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
+        p1[n] = movmatrix_t(E4M3 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
       }
       // ---- O^T += V^T P^T
       if constexpr (!E4M3) {
@@ -436,14 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
           uint32_t v[4];
           ldmatrix4_t(sv + v_unit<D, E4M3>(key, 2 * x + ((lane >> 3) & 1)) * 16, v);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(o[n][x], v[0], v[1], v[2], v[3], p0[n], p1[n]);
+          for (int n = 0; n < NT; ++n) mma16816<E4M3>(o[n][x], v[0], v[1], v[2], v[3], p0[n], p1[n]);
         }
       } else {
-        const uint32_t ss = scale_ring + stage * L::kScaleBytes + 16;
-        uint32_t f[2];  // factors of keys 2 c4, 2 c4 + 1 and of 2 c4 + 8, 2 c4 + 9
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          f[e] = prmt(factor(ss, 2 * c4 + 8 * e), factor(ss, 2 * c4 + 8 * e + 1), 0x5410u);
         constexpr int kWords = D / 32;  // words of a thread's columns, D / 8 of them, per key
         uint32_t v[4][kWords];          // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
 #pragma unroll
@@ -463,16 +515,13 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
         }
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {  // columns (D / 8) g8 + 2 x and + 1
+          // both columns' codes of two keys in one word, then as f16 pairs of keys
+          constexpr uint32_t kSel[2] = {0x5140u, 0x7362u};
           uint32_t r[4];
+          e4m3_to_f16(prmt(v[0][x >> 1], v[1][x >> 1], kSel[x & 1]), r[0], r[1]);
+          e4m3_to_f16(prmt(v[2][x >> 1], v[3][x >> 1], kSel[x & 1]), r[2], r[3]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int byte = 2 * (x & 1) + (e & 1);
-            const uint32_t sel = 0x4000u + 0x1010u * static_cast<uint32_t>(byte);
-            r[e] = mul_bf16x2(
-                e4m3_bits(prmt(v[e >> 1 << 1][x >> 1], v[(e >> 1 << 1) + 1][x >> 1], sel)), f[e >> 1]);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(o[n][x], r[0], r[1], r[2], r[3], p0[n], p1[n]);
+          for (int n = 0; n < NT; ++n) mma16816<E4M3>(o[n][x], r[0], r[1], r[2], r[3], p0[n], p1[n]);
         }
       }
     }
@@ -523,8 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
           y[2] += k * v.z;
           y[3] += k * v.w;
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;  // log2 units
+        // e4m3: l is 2^-64 of the sum
+        const float inv = l > 0.f ? (E4M3 ? 1.f / l * pow2i(-64) : 1.f / l) : 0.f;
+        const float lse2 = l > 0.f ? m + __log2f(l) + (E4M3 ? 64.f : 0.f) : -INFINITY;  // log2
         if (direct) {
           const int t = r / G;
           const long long row = static_cast<long long>(cw.s.t0 + t) * a.H + cw.h * G + (r - t * G);
@@ -551,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < D / 8; ++e) q[n][e] = qn[n][e];
+        ready_q(q);
       }
     }
     cw = nw;
