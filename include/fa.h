@@ -299,14 +299,15 @@ fa_status fa_paged_read(const void* k_pages, const void* v_pages, const uint8_t*
  * finite (a NaN or an infinity there may reach every new token of the sequence); what lies
  * behind the length, in the same page too, does not matter.
  *   max_q: the largest number of new tokens of one sequence (a bound on it is enough).
- *   workspace: fa_paged_workspace_size(H, H_kv, d, max_q) bytes, 16-byte aligned; its
- *   contents on entry do not matter.
+ *   workspace: fa_paged_workspace_size(H, H_kv, d, max_q, max_pages * page_size) bytes,
+ *   16-byte aligned (NULL where that is 0); its contents on entry do not matter. Calls that
+ *   may overlap need one each.
  * The work of a call is divided among the SMs by the lengths found on the device, so a
  * captured call may be replayed with other lengths. Results do not depend on atomics.
  * Errors: FA_ERR_INVALID_ARG (as above, H not a multiple of H_kv, scale not positive and
  * finite, window_left < -1, max_q < 1, T * H >= 2^31), FA_ERR_UNSUPPORTED (H / H_kv >
  * 128, and as above), FA_ERR_WORKSPACE, FA_ERR_CUDA. */
-size_t fa_paged_workspace_size(int H, int H_kv, int d, int max_q);
+size_t fa_paged_workspace_size(int H, int H_kv, int d, int max_q, int max_keys);
 fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
                         const uint8_t* k_scale, const uint8_t* v_scale, void* o, float* lse,
                         int type, int num_pages, int page_size, int H, int H_kv, int d,

@@ -115,7 +115,7 @@ def load(build_if_missing: bool = False):
         lib.fa_paged_write.restype = i
         lib.fa_paged_read.argtypes = [vp] * 4 + cache + [i, i, vp, vp, vp]
         lib.fa_paged_read.restype = i
-        lib.fa_paged_workspace_size.argtypes = [i, i, i, i]
+        lib.fa_paged_workspace_size.argtypes = [i, i, i, i, i]
         lib.fa_paged_workspace_size.restype = sz
         lib.fa_paged_attn.argtypes = ([vp] * 7 + [i, i, i, i, i, i, i64, i64, i64, vp, i64, i, vp]
                                       + [vp, i, i, i, i64, f, i, i, vp, sz, vp])
@@ -348,8 +348,8 @@ def fa_paged_read(k_pages, v_pages, k_scale, v_scale, type, num_pages, page_size
                                 _ptr(kv_lens), B, N, _ptr(k_out), _ptr(v_out), _stream(stream))
 
 
-def fa_paged_workspace_size(H, H_kv, d, max_q) -> int:
-    return int(load().fa_paged_workspace_size(H, H_kv, d, max_q))
+def fa_paged_workspace_size(H, H_kv, d, max_q, max_keys) -> int:
+    return int(load().fa_paged_workspace_size(H, H_kv, d, max_q, max_keys))
 
 
 def fa_paged_attn(q, k_pages, v_pages, k_scale, v_scale, o, lse, type, num_pages, page_size, H,
@@ -674,10 +674,10 @@ def _used_on(stream, *tensors):
             t.record_stream(stream)
 
 
-@functools.lru_cache(maxsize=None)
-def _paged_workspace_bytes(H, H_kv, d, max_q, dev):
+@functools.lru_cache(maxsize=4096)
+def _paged_workspace_bytes(H, H_kv, d, max_q, max_keys, dev):
     with torch.cuda.device(dev):  # depends on the device's number of SMs
-        return fa_paged_workspace_size(H, H_kv, d, max_q)
+        return fa_paged_workspace_size(H, H_kv, d, max_q, max_keys)
 
 
 def paged_write(k_new, v_new, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None,
@@ -737,9 +737,8 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
             raise ValueError(f"out must be contiguous: bf16 [{T}, {H}, {d}] and fp32 [{T}, {H}]")
     if T == 0:
         return o, lse
-    ws, ws_bytes = None, _paged_workspace_bytes(H, Hkv, d, n, dev)
-    if ws_bytes:
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    ws_bytes = _paged_workspace_bytes(H, Hkv, d, n, head[2] * batch[7], dev)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
     _call("fa_paged_attn", dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
           _data(k_scale), _data(v_scale), o.data_ptr(), lse.data_ptr(), *head, H, *batch, cu, B, T,
           n, qs, 1.0 / math.sqrt(d) if scale is None else float(scale), bool(causal),

@@ -797,26 +797,28 @@ fa_status fa_paged_read(const void* k_pages, const void* v_pages, const uint8_t*
 // Workspace of fa_paged_attn: one header per CTA, then the pieces' lse and outputs.
 struct PagedWorkspace {
   int ctas, rows;
+  bool whole;  // a step over few keys: no head is cut, nothing is left behind
   size_t lse_off, o_off, bytes;
 };
-static PagedWorkspace paged_workspace(int G, int d, int max_q, int num_sms) {
+static PagedWorkspace paged_workspace(int G, int d, int max_q, long long max_keys, int num_sms) {
   PagedWorkspace w;
   const long long rows = static_cast<long long>(G) * max_q;
+  w.whole = rows <= fa::kStepRows && max_keys <= fa::kWholeKeys;
   w.ctas = num_sms < 256 ? num_sms : 256;  // the chunk kernel plans with a thread per CTA
   w.rows = rows <= 8 ? 8 : rows <= fa::kStepRows ? fa::kStepRows : fa::kTile;
   const size_t slots = 2 * static_cast<size_t>(w.ctas) * w.rows;
   w.lse_off = round256(static_cast<size_t>(w.ctas) * 16);
   w.o_off = w.lse_off + round256(slots * sizeof(float));
-  w.bytes = w.o_off + round256(slots * d * sizeof(float));
+  w.bytes = w.whole ? 0 : w.o_off + round256(slots * d * sizeof(float));
   return w;
 }
 
-size_t fa_paged_workspace_size(int H, int H_kv, int d, int max_q) {
+size_t fa_paged_workspace_size(int H, int H_kv, int d, int max_q, int max_keys) {
   DeviceInfo* di = nullptr;
   if (H < 1 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128) || max_q < 1 ||
-      device_info(&di) != FA_OK)
+      max_keys < 1 || device_info(&di) != FA_OK)
     return 0;
-  return paged_workspace(H / H_kv, d, max_q, di->num_sms).bytes;
+  return paged_workspace(H / H_kv, d, max_q, max_keys, di->num_sms).bytes;
 }
 
 fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
@@ -842,13 +844,14 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_INVALID_ARG;
   DeviceInfo* di = nullptr;
   if ((st = device_info(&di)) != FA_OK) return st;
-  const PagedWorkspace w = paged_workspace(H / H_kv, d, max_q, di->num_sms);
-  if (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace))
+  const PagedWorkspace w = paged_workspace(
+      H / H_kv, d, max_q, static_cast<long long>(max_pages) * page_size, di->num_sms);
+  if (w.bytes > 0 && (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace)))
     return FA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.headers = ws;
-  a.lse_part = reinterpret_cast<float*>(ws + w.lse_off);
-  a.o_part = reinterpret_cast<float*>(ws + w.o_off);
+  a.lse_part = w.whole ? nullptr : reinterpret_cast<float*>(ws + w.lse_off);
+  a.o_part = w.whole ? nullptr : reinterpret_cast<float*>(ws + w.o_off);
   a.c.status = di->status;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
@@ -861,6 +864,7 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   a.scale_log2 = scale * fa::kLog2e;
   a.causal = causal ? 1 : 0;
   a.wl = window_left;
+  a.whole = w.whole;
   a.sync = fa::SyncParams{};
   const bool e4m3 = type == FA_CACHE_E4M3;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);

@@ -206,6 +206,7 @@ struct PagedAttnArgs {
   float scale_log2;             // scale * log2(e)
   int causal;
   int wl;                       // sliding window (-1: none)
+  int whole;                    // step kernel: no head is cut between CTAs
   // Workspace of calls whose work is cut between CTAs: a header per CTA and two pieces,
   // each of `rows` query rows: o_part [ctas, 2, rows, d], lse_part [ctas, 2, rows] (log2).
   void* headers;                // [ctas] int4
@@ -214,6 +215,7 @@ struct PagedAttnArgs {
   SyncParams sync;
 };
 constexpr int kStepRows = 16;   // most query rows per K/V head of the step kernel
+constexpr int kWholeKeys = 512; // page tables with room for so many keys: heads are not cut
 
 cudaError_t launch_paged_write(const PagedWriteArgs& a, bool e4m3, cudaStream_t stream);
 cudaError_t launch_paged_read(const PagedReadArgs& a, bool e4m3, cudaStream_t stream);

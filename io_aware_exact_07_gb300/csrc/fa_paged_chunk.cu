@@ -1387,12 +1387,9 @@ cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   // The in-kernel register reallocation assumes kRegsLaunch registers per thread at launch:
   // with fewer, the softmax warpgroups' increase could never be granted and would wait
   // forever, so such a kernel is refused.
-  cudaFuncAttributes attr;
-  cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-  if (e != cudaSuccess) return e;
-  if (attr.numRegs < L::kRegsLaunch || attr.maxThreadsPerBlock < L::kThreads)
-    return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e =
+      allow_smem(reinterpret_cast<const void*>(kern), L::kSmemBytes, L::kRegsLaunch, ready);
   if (e != cudaSuccess) return e;
   kern<<<ctas, L::kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, a, box_rows);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

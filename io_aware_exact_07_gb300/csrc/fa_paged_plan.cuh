@@ -3,6 +3,8 @@
 // cut by a run's end leaves pieces: slot 1 of the CTA where it began, slot 0 of those where
 // it went on.
 #pragma once
+#include <atomic>
+
 #include "fa_paged.h"
 
 namespace fa {
@@ -56,6 +58,23 @@ __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device, and checks that
+// it has at least `regs` registers a thread; once per device (a bit each of `ready`).
+inline cudaError_t allow_smem(const void* kern, int bytes, int regs,
+                              std::atomic<unsigned long long>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes attr;
+  if ((e = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return e;
+  if (attr.numRegs < regs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Launches the merge of a kernel just launched on `stream`. It may be scheduled while that
 // one runs; its blocks wait for its end (pdl_wait) before they read anything.

@@ -23,22 +23,28 @@
 //  - The (sequence, K/V head, 128-key block) list is cut into equal runs, one per CTA, by
 //    the lengths found on the device. A head that falls into one run is written directly;
 //    one cut by a run's end leaves normalised pieces, merged by a second, small kernel with
-//    the two-block rule of the online softmax.
+//    the two-block rule of the online softmax. Where the page table has room for few keys,
+//    runs are of whole heads and there is nothing to merge.
 #include "fa_paged_plan.cuh"
 
 namespace fa {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 16;                  // keys of a warp's step
-constexpr int kBlock = kWarps * kChunk;     // keys of a block
+constexpr int kMergeWarps = 8;
 constexpr float kRescale = 8.0f;            // log2 units: rescale O when m grows by > 2^8
 constexpr int kSmemMax = 232448;
 
 template <int D, bool E4M3, int NT>
 struct StepL {
+  // More warps hide the latency of a warp's chain of steps where its keys are few bytes, as
+  // far as the merge buffer leaves room for two stages. 16 sequences of 16384 keys, 8 K/V heads,
+  // with 8, 12, 16 warps: e4m3 d = 128 112, 96, 97 us; e4m3 d = 64 97, 75, 71; bf16 d = 64 91,
+  // 91, 87; bf16 d = 128 with 8: 164.
+  static constexpr int kWarps = NT == 2 ? 8 : D == 64 ? 16 : E4M3 ? 12 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kBlock = kWarps * kChunk;          // keys of a block
   static constexpr int kRows = 8 * NT;                    // query rows
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kUnits = kRowBytes / 16;           // 16-byte units of a row
@@ -123,6 +129,7 @@ __device__ __forceinline__ int ld_shared_u8(uint32_t saddr) {
 struct Span {
   int first, n;
 };
+template <int kBlock>
 __device__ __forceinline__ Span span_of(const PagedAttnArgs& a, const PagedSeq& s) {
   Span r;
   const int lo = a.wl >= 0 ? s.len - s.nq - a.wl : 0;
@@ -134,6 +141,7 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& a, const PagedSeq& 
 }
 
 // A place in the list of (sequence, K/V head, key block).
+template <int kBlock>
 struct Walk {
   int b, h;          // sequence (B past the end), K/V head
   int blk, end;      // key block, end of the sequence's blocks
@@ -141,7 +149,7 @@ struct Walk {
   PagedSeq s;
   __device__ __forceinline__ void load(const PagedAttnArgs& a) {
     s = paged_attn_seq(a.c, b);
-    const Span sp = span_of(a, s);
+    const Span sp = span_of<kBlock>(a, s);
     first = sp.first;
     end = first + sp.n;
   }
@@ -167,15 +175,17 @@ struct Walk {
 }  // namespace
 
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step_kernel(const PagedAttnArgs a) {
   using L = StepL<D, E4M3, NT>;
+  using Walk = Walk<L::kBlock>;
+  constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kBlock = L::kBlock;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, c4 = lane & 3;
-  const int G = a.H / a.c.Hkv;
+  const int G = a.G;
   pdl_launch_dependents();
 
-  // ---- this CTA's run [lo, hi) of the list
+  // ---- this CTA's run [lo, hi) of the list: of key blocks, or (whole) of K/V heads
   struct Plan {
     long long warp_sums[kWarps];
     int b;
@@ -185,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
   static_assert(sizeof(Plan) <= 256, "plan area");
   auto weight = [&](int b) -> long long {
     if (b >= a.c.B) return 0;
-    return static_cast<long long>(span_of(a, paged_attn_seq(a.c, b)).n) * a.c.Hkv;
+    const int n = span_of<kBlock>(a, paged_attn_seq(a.c, b)).n;
+    return static_cast<long long>(a.whole ? min(n, 1) : n) * a.c.Hkv;
   };
   long long total = 0, x0 = 0;
   for (int b0 = 0; b0 < a.c.B; b0 += kThreads) {
@@ -200,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
   const long long hi = lo + per < total ? lo + per : total;
   PieceHeader* headers = static_cast<PieceHeader*>(a.headers);
   if (lo >= hi) {
-    if (tid == 0) headers[blockIdx.x] = PieceHeader{-1, 0, 1, 0};
+    if (tid == 0 && !a.whole) headers[blockIdx.x] = PieceHeader{-1, 0, 1, 0};
     return;
   }
   {
@@ -210,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
       long long sum;
       const long long at = base + block_scan<kWarps>(x, plan->warp_sums, &sum);
       if (at <= lo && lo < at + x) {
-        const long long n = x / a.c.Hkv;
+        const long long n = x / a.c.Hkv;  // blocks (1 if whole) of a head
         plan->b = b0 + tid;
         plan->rem_h = static_cast<int>((lo - at) / n);
         plan->rem_blk = static_cast<int>((lo - at) % n);
@@ -320,7 +331,16 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
   load_q(cw, q);
   ready_q(q);
 
-  const long long steps = hi - lo;
+  long long steps = hi - lo;  // blocks
+  if (a.whole) {
+    Walk t = cw;
+    steps = 0;
+    for (long long u = lo; u < hi; ++u) {
+      steps += t.end - t.first;
+      t.blk = t.end - 1;
+      t.next(a);
+    }
+  }
 #pragma unroll
   for (int s = 0; s < L::kStages - 1; ++s) {
     if (s < steps) issue(s);
@@ -607,7 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
     cw = nw;
   }
   cp_async_wait<0>();
-  if (tid == 0) headers[blockIdx.x] = PieceHeader{slot1_b, slot1_h, !starts_mid || ended0, 0};
+  if (tid == 0 && !a.whole)
+    headers[blockIdx.x] = PieceHeader{slot1_b, slot1_h, !starts_mid || ended0, 0};
 }
 
 // Merge of the pieces of a head that runs' ends have cut: with lse_s and the normalised O_s
@@ -615,37 +636,37 @@ __global__ void __launch_bounds__(kThreads, 1) fa_paged_step_kernel(const PagedA
 // takes query row r of the head that CTA c's run began and did not end; the next CTAs'
 // pieces follow until one ends it. In the order of the pieces, so always the same result.
 template <int D>
-__global__ void __launch_bounds__(kThreads) fa_paged_step_merge_kernel(const PagedAttnArgs a, int ctas,
+__global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_step_merge_kernel(const PagedAttnArgs a, int ctas,
                                                                        int rows) {
   constexpr int kPer = D / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, r = blockIdx.y;
   __shared__ int n_more;
-  __shared__ float mx[kWarps], dens[kWarps];
-  __shared__ float acc_s[kWarps][D];
+  __shared__ float mx[kMergeWarps], dens[kMergeWarps];
+  __shared__ float acc_s[kMergeWarps][D];
   pdl_wait();
   const PieceHeader* headers = static_cast<const PieceHeader*>(a.headers);
   const PieceHeader hd = headers[c];
   if (hd.b < 0) return;
   const PagedSeq s = paged_attn_seq(a.c, hd.b);
-  const int G = a.H / a.c.Hkv;
+  const int G = a.G;
   if (r >= s.nq * G) return;
   const int n = 1 + pieces_after(headers, c, ctas, &n_more);  // pieces: slot 1 of CTA c, slot 0 of the n - 1 after it
   auto row_of = [&](int i) { return (2ll * (c + i) + (i == 0 ? 1 : 0)) * rows + r; };
   float m = -INFINITY;
-  for (int i = tid; i < n; i += kThreads) m = fmaxf(m, a.lse_part[row_of(i)]);
+  for (int i = tid; i < n; i += kMergeWarps * 32) m = fmaxf(m, a.lse_part[row_of(i)]);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   if (lane == 0) mx[warp] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, mx[w]);
+  for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, mx[w]);
   const float mu = m == -INFINITY ? 0.f : m;
   float den = 0.f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
 #pragma unroll 4
-  for (int i = warp; i < n; i += kWarps) {
+  for (int i = warp; i < n; i += kMergeWarps) {
     const long long row = row_of(i);
     const float w = ex2_approx(a.lse_part[row] - mu);
     den += w;
@@ -669,7 +690,7 @@ __global__ void __launch_bounds__(kThreads) fa_paged_step_merge_kernel(const Pag
   if (tid < D) {
     float y = 0.f, l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kMergeWarps; ++w) {
       y += acc_s[w][tid];
       l += dens[w];
     }
@@ -686,20 +707,19 @@ template <int D, bool E4M3, int NT>
 cudaError_t launch_impl(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   using L = StepL<D, E4M3, NT>;
   auto kern = fa_paged_step_kernel<D, E4M3, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       L::kSmemBytes);
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), L::kSmemBytes, 0, ready);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kThreads, L::kSmemBytes, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_merge(fa_paged_step_merge_kernel<D>, dim3(ctas, (a.H / a.c.Hkv) * a.c.max_q),
-                      kThreads, stream, a, ctas, int(L::kRows));
+  kern<<<ctas, L::kThreads, L::kSmemBytes, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess || a.whole) return e;
+  return launch_merge(fa_paged_step_merge_kernel<D>, dim3(ctas, a.G * a.c.max_q),
+                      kMergeWarps * 32, stream, a, ctas, int(L::kRows));
 }
 
 template <int D, bool E4M3>
 cudaError_t launch_rows(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
-  const int rows = (a.H / a.c.Hkv) * a.c.max_q;
-  return rows <= 8 ? launch_impl<D, E4M3, 1>(a, ctas, stream)
-                   : launch_impl<D, E4M3, 2>(a, ctas, stream);
+  return a.G * a.c.max_q <= 8 ? launch_impl<D, E4M3, 1>(a, ctas, stream)
+                              : launch_impl<D, E4M3, 2>(a, ctas, stream);
 }
 
 }  // namespace

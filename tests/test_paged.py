@@ -333,7 +333,7 @@ def test_two_graphs_and_an_eager_call_share_a_workspace():
     b = Batch([1, 2], [3000, 100], 16, 2, 64, G=4, seed=17)
     c = Batch([60, 5], [2000, 70], 16, 2, 64, G=4, seed=18)
     xs = [y.fill().on(DEV) for y in (b, c)]
-    need = max(fa.fa_paged_workspace_size(8, 2, 64, n) for n in (2, 60))
+    need = max(fa.fa_paged_workspace_size(8, 2, 64, n, 1 << 20) for n in (2, 60))
     ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
     outs = [(torch.empty_like(x.q), torch.empty(x.q.shape[:2], device=DEV)) for x in xs]
 
@@ -436,12 +436,12 @@ def test_prefill_then_steps_then_read_back(e4m3):
 
 def test_workspace_is_checked():
     lib = fa.load()
-    b = Batch([1, 1], [300, 40], 16, 2, 64, G=2, seed=24)
+    b = Batch([1, 1], [3000, 40], 16, 2, 64, G=2, seed=24)
     x = b.fill().on(DEV)
     o, lse = torch.empty_like(x.q), torch.empty((2, 4), device=DEV)
     P, Hkv, page, d = x.k.shape
-    need = fa.fa_paged_workspace_size(4, 2, 64, 1)
-    assert need > 0 and fa.fa_paged_workspace_size(4, 3, 64, 1) == 0
+    need = fa.fa_paged_workspace_size(4, 2, 64, 1, x.table.shape[1] * page)
+    assert need > 0 and fa.fa_paged_workspace_size(4, 3, 64, 1, 100) == 0
     ws = torch.empty(need + 16, dtype=torch.uint8, device=DEV)
     for at, size, status in ((None, need, 4), (ws.data_ptr(), need - 1, 4),
                              (ws.data_ptr() + 8, need, 4), (ws.data_ptr(), need, 0)):
