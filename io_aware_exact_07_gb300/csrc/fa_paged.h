@@ -153,6 +153,9 @@ __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t saddr) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(saddr) : "memory");
   return r;
 }
+__device__ __forceinline__ void st_shared_u32(uint32_t saddr, uint32_t a) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(saddr), "r"(a) : "memory");
+}
 __device__ __forceinline__ void st_shared_v2(uint32_t saddr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(saddr), "r"(a), "r"(b) : "memory");
 }
@@ -214,7 +217,7 @@ struct PagedAttnArgs {
   float* lse_part;
   SyncParams sync;
 };
-constexpr int kStepRows = 16;   // most query rows per K/V head of the step kernel
+constexpr int kStepRows = 32;   // most query rows per K/V head of the step kernel
 constexpr int kWholeKeys = 512; // page tables with room for so many keys: heads are not cut
 
 cudaError_t launch_paged_write(const PagedWriteArgs& a, bool e4m3, cudaStream_t stream);

@@ -142,14 +142,15 @@ struct Unit {
   // k units further on; b = B past the end.
   __device__ __forceinline__ void advance(const PagedAttnArgs& a, int k) {
     if (b >= a.c.B) return;
-    long long at = static_cast<long long>(h) * n_qt + qt + k;
-    while (at >= static_cast<long long>(n_qt) * a.c.Hkv) {
-      at -= static_cast<long long>(n_qt) * a.c.Hkv;
+    // (units of a sequence: at most T * Hkv, which fits an int)
+    unsigned at = static_cast<unsigned>(h * n_qt + qt + k), all;
+    while (at >= (all = static_cast<unsigned>(n_qt * a.c.Hkv))) {
+      at -= all;
       if (++b >= a.c.B) return;
       seq(a);
     }
-    h = static_cast<int>(at / n_qt);
-    qt = static_cast<int>(at - static_cast<long long>(h) * n_qt);
+    h = static_cast<int>(at / static_cast<unsigned>(n_qt));
+    qt = static_cast<int>(at) - h * n_qt;
   }
 };
 
@@ -1172,6 +1173,21 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         ++n_done;
       }
       if (!ok) break;
+      // The next piece is worked out while this one's last PV runs.
+      const int head = wp->u.h * args.G;                           // the tile's first query head
+      const int tok0 = wp->u.qt * args.tt;                         // its first token
+      const int rows = min(wp->u.s.nq - tok0, args.tt) * args.G;   // its rows
+      const int row0 = wp->u.s.t0 + tok0;
+      const bool from_start = wp->from_start, ends = wp->ends;
+      if (tid == 0) {
+        if (!from_start) left->ended = ends;
+        if (from_start && !ends) {
+          left->b = wp->u.b;
+          left->h = wp->u.h;
+          left->qt = wp->u.qt;
+        }
+      }
+      const bool more = wp->next(args);
       // ---- epilogue: merge the two warpgroups' partial softmaxes.
       // This warpgroup's last PV has completed once its pv_done phase has.
       if (n_done > 0) {
@@ -1210,9 +1226,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       const float inv = (l > 0.f) ? 1.f / l : 0.f;
       const float w0 = a0 * inv, w1 = a1 * inv;
       const float lse2 = (l > 0.f) ? m + __log2f(l) : -INFINITY;  // log2 units
-      const int tok0 = wp->u.qt * args.tt;                                  // the tile's first token
-      const int rows = min(wp->u.s.nq - tok0, args.tt) * args.G;                 // rows of the tile
-      const bool direct = wp->from_start && wp->ends;
+      const bool direct = from_start && ends;
       // This warpgroup writes output columns [D/2 g, D/2 g + D/2) from both O_0 and O_1.
       constexpr int kHalf = D / 2;
       if (direct) {
@@ -1257,20 +1271,18 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           const int row = quad * 32 + r;
           if (row < rows) {
             const int tk = token_of(row);
-            const long long at = static_cast<long long>(wp->u.s.t0 + tok0 + tk) * args.H + wp->u.h * args.G +
-                                 (row - tk * args.G);
+            const long long at = static_cast<long long>(row0 + tk) * args.H + head + (row - tk * args.G);
             *reinterpret_cast<uint4*>(args.o + at * D + kHalf * g + 8 * u) = val;
           }
         }
         if (t < rows && g == 0) {
           const int tk = token_of(t);
-          args.lse[static_cast<long long>(wp->u.s.t0 + tok0 + tk) * args.H + wp->u.h * args.G + (t - tk * args.G)] =
-              lse2 * kLn2;
+          args.lse[static_cast<long long>(row0 + tk) * args.H + head + (t - tk * args.G)] = lse2 * kLn2;
         }
       } else {
         // a piece: normalised, fp32. Slot 0 continues what an earlier CTA began, slot 1 is
         // continued by the next.
-        const long long at = (2ll * blockIdx.x + (wp->from_start ? 1 : 0)) * kTile + t;
+        const long long at = (2ll * blockIdx.x + (from_start ? 1 : 0)) * kTile + t;
 #pragma unroll
         for (int c = 0; c < kHalf / 16; ++c) {
           const uint32_t col = static_cast<uint32_t>(kHalf * g + 16 * c);
@@ -1293,20 +1305,13 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         }
         if (t < rows && g == 0) args.lse_part[at] = lse2;
       }
-      if (tid == 0) {
-        if (!wp->from_start) left->ended = wp->ends;
-        if (wp->from_start && !wp->ends) {
-          left->b = wp->u.b;
-          left->h = wp->u.h;
-          left->qt = wp->u.qt;
-        }
-      }
       tc_fence_before();
       mbar_arrive(bars.o_free);
       ++count;
       tile_cnt += nt;
       q_cnt += nt > 0;
-    } while (wp->next(args));
+      if (!more) break;
+    } while (true);
   }
 
   tc_fence_before();

@@ -1,5 +1,5 @@
 // Attention of few new tokens per sequence over a paged cache (a decode step: one new
-// token, or a handful of drafted ones): at most 16 query rows per K/V head, G = H / Hkv
+// token, or a handful of drafted ones): at most 32 query rows per K/V head, G = H / Hkv
 // heads times nq tokens. The page "FlashAttention — L3 Cross-Paper Synthesis" (section 3)
 // names this case, bound by reading K and V, as left unoptimised. HBM is the bound, so the
 // kernel is a stream of K and V through shared memory, each byte read once per K/V head:
@@ -9,10 +9,13 @@
 //    that the main loop has no block barrier and loads run ahead across heads and sequences.
 //    16 keys lie in one page (its size is a multiple of 16), so one table entry serves them.
 //  - S^T = K Q^T and O^T += V^T P^T with m16n8k16 products: the keys (then the columns of V)
-//    are the 16 rows, the query rows the 8 columns. With at most 8 (or 16) query rows the
-//    products are far below what bounds the kernel (128-row tensor-memory tiles would hold
-//    at least 112 empty rows); keeping S and P in registers saves the handshakes that a
-//    short sequence cannot hide.
+//    are the 16 rows, the query rows the 8 columns (1, 2 or 4 times). With so few query rows
+//    the products are below what bounds the kernel (a 128-row tensor-memory tile would be
+//    three quarters empty, and its softmax walks all of it); keeping S and P in registers
+//    saves the handshakes that a short sequence cannot hide. From 17 rows on it is these
+//    products that bound it, at some 7 cycles each and SM. 24 sequences, 8 K/V heads, 32 rows,
+//    d = 128, here and with 128-row tiles: 8192 bf16 keys 156 and 140 us, 1024 keys 44 and 47,
+//    8192 quantised keys 161 and 201; 128 sequences of 200 keys 60 and 74.
 //  - The order of the columns d within a product is free as long as both operands share
 //    it: a thread takes the 16 bytes of a row that it can load at once.
 //  - e4m3 codes become f16 between shared memory and the product, which the hardware converts
@@ -39,10 +42,10 @@ constexpr int kSmemMax = 232448;
 template <int D, bool E4M3, int NT>
 struct StepL {
   // More warps hide the latency of a warp's chain of steps where its keys are few bytes, as
-  // far as the merge buffer leaves room for two stages. 16 sequences of 16384 keys, 8 K/V heads,
-  // with 8, 12, 16 warps: e4m3 d = 128 112, 96, 97 us; e4m3 d = 64 97, 75, 71; bf16 d = 64 91,
-  // 91, 87; bf16 d = 128 with 8: 164.
-  static constexpr int kWarps = NT == 2 ? 8 : D == 64 ? 16 : E4M3 ? 12 : 8;
+  // far as registers and the merge buffer leave room. 16 sequences of 16384 keys, 8 K/V heads,
+  // 4 rows with 8, 12, 16 warps: e4m3 d = 128 112, 96, 97 us; e4m3 d = 64 97, 75, 71; bf16 d =
+  // 64 91, 91, 87; bf16 d = 128 with 8: 164. 24 of 8192 keys, 20 rows, d = 64: 95, 89, 152.
+  static constexpr int kWarps = NT >= 2 ? (D == 64 ? 12 : 8) : D == 64 ? 16 : E4M3 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kBlock = kWarps * kChunk;          // keys of a block
   static constexpr int kRows = 8 * NT;                    // query rows
@@ -52,9 +55,15 @@ struct StepL {
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kScaleBytes = E4M3 ? 32 : 0;       // K's and V's 16 scale bytes
   static constexpr int kPitch = D + 4;                    // merge buffer row, in floats
-  static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
+  // 32 rows: Q lies in shared memory, one copy for all warps, and two warps join their states
+  // in registers before the merge, whose buffer then takes half the room.
+  static constexpr bool kQShared = NT == 4;
+  static constexpr int kFold = NT == 4 ? 2 : 1;
+  static constexpr int kStates = kWarps / kFold;
+  static constexpr int kQBytes = kQShared ? kRows * (D * 2 + 4) : 0;  // rows, and their exponents
+  static constexpr int kMergeBytes = kStates * kRows * kPitch * 4;
   static constexpr int kMlBytes = kWarps * kRows * 8;
-  static constexpr int kFixed = kMergeBytes + kMlBytes + 256;
+  static constexpr int kFixed = kMergeBytes + kMlBytes + kQBytes + 256;
   static constexpr int kFit = (kSmemMax - kFixed) / (kWarps * (kStageBytes + kScaleBytes));
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static_assert(kStages >= 2, "the ring needs two stages");
@@ -62,7 +71,8 @@ struct StepL {
   static constexpr int kScaleOff = kWarps * kStages * kStageBytes;
   static constexpr int kMergeOff = kScaleOff + kWarps * kStages * kScaleBytes;
   static constexpr int kMlOff = kMergeOff + kMergeBytes;
-  static constexpr int kPlanOff = kMlOff + kMlBytes;
+  static constexpr int kQOff = kMlOff + kMlBytes;
+  static constexpr int kPlanOff = kQOff + kQBytes;
   static constexpr int kSmemBytes = kPlanOff + 256;
   static_assert(kSmemBytes <= kSmemMax, "more shared memory than one CTA may hold");
 };
@@ -280,56 +290,118 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
     lpage = page_of(lw);
   };
   // ---- query rows of a K/V head: row r = t * G + g; the rows' columns in the order of the
-  // products, two registers per 16 columns
-  auto load_q = [&](const Walk& w, uint32_t(&q)[NT][D / 8]) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = n * 8 + g8;
-      const bool real = r < w.s.nq * G;
-      const int t = r / G;
-      const __nv_bfloat16* p = a.q + (w.s.t0 + t) * a.q_stride + (w.h * G + (r - t * G)) * D;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        // bf16: columns 32 i + 8 c4 ..; e4m3: 64 (i / 2) + 16 c4 + 8 (i % 2) ..
-        const int col = E4M3 ? (i >> 1) * 64 + c4 * 16 + (i & 1) * 8 : i * 32 + c4 * 8;
-        const uint4 x = real ? *reinterpret_cast<const uint4*>(p + col) : make_uint4(0u, 0u, 0u, 0u);
-        q[n][4 * i] = x.x;
-        q[n][4 * i + 1] = x.y;
-        q[n][4 * i + 2] = x.z;
-        q[n][4 * i + 3] = x.w;
-      }
-    }
+  // products, two registers per 16 columns. Column from which 16 bytes of a thread's row serve
+  // products 2 i and 2 i + 1.
+  auto q_col = [&](int i) {
+    return E4M3 ? (i >> 1) * 64 + c4 * 16 + (i & 1) * 8 : i * 32 + c4 * 8;
   };
-  // What a row's scores are multiplied with: rows 2 c4, 2 c4 + 1 of each group of eight.
-  float c_row[NT][2];
-  // e4m3: Q's rows as f16, each times 2^k that puts its largest magnitude into [2^14, 2^15):
-  // f16 then holds all that bf16 held but for elements below 2^-29 of it.
-  auto ready_q = [&](uint32_t(&q)[NT][D / 8]) {
+  auto q_load = [&](const Walk& w, int r, int col) {
+    const int t = r / G;
+    const __nv_bfloat16* p = a.q + (w.s.t0 + t) * a.q_stride + (w.h * G + (r - t * G)) * D;
+    return r < w.s.nq * G ? *reinterpret_cast<const uint4*>(p + col) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  // e4m3: Q's rows as f16, each times 2^k that puts its largest magnitude (bf16 bits `top`)
+  // into [2^14, 2^15): f16 then holds all that bf16 held but for elements below 2^-29 of it.
+  auto q_exponent = [](uint32_t top) {
+    return max(-114, min(60, 14 + 127 - static_cast<int>(top >> 7)));
+  };
+  auto top_of = [](const uint4& x) {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    const uint32_t m =
+        __vmaxu2(__vmaxu2(x.x & kAbs, x.y & kAbs), __vmaxu2(x.z & kAbs, x.w & kAbs));
+    return max(m & 0xFFFFu, m >> 16);
+  };
+  auto to_f16 = [](uint4 x, float f) {
+    auto one = [&](uint32_t y) {
+      return pack_f16x2(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f);
+    };
+    return make_uint4(one(x.x), one(x.y), one(x.z), one(x.w));
+  };
+  float c_row[NT][2];  // what a row's scores are multiplied with, rows 2 c4, 2 c4 + 1 of each eight
+  // Q in registers ...
+  constexpr int kQRegs = L::kQShared ? 1 : D / 32;
+  uint4 q[NT][kQRegs] = {}, qn[NT][kQRegs];
+  auto load_q = [&](const Walk& w, uint4(&x)[NT][kQRegs]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < kQRegs; ++i) x[n][i] = q_load(w, n * 8 + g8, q_col(i));
+  };
+  auto ready_q = [&]() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       c_row[n][0] = c_row[n][1] = a.scale_log2;
       if constexpr (E4M3) {
-        uint32_t m2 = 0;
+        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) m2 = __vmaxu2(m2, q[n][i] & 0x7FFF7FFFu);
-        uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
+        for (int i = 0; i < kQRegs; ++i) top = max(top, top_of(q[n][i]));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int k = max(-114, min(60, 14 + 127 - static_cast<int>(top >> 7)));
-        const float f = pow2i(k);
+        const int k = q_exponent(top);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          q[n][i] = pack_f16x2(__uint_as_float(q[n][i] << 16) * f,
-                               __uint_as_float(q[n][i] & 0xFFFF0000u) * f);
+        for (int i = 0; i < kQRegs; ++i) q[n][i] = to_f16(q[n][i], pow2i(k));
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           c_row[n][e] *= pow2i(-__shfl_sync(0xffffffffu, k, (2 * c4 + e) * 4));
       }
     }
   };
-  uint32_t q[NT][D / 8];
-  load_q(cw, q);
-  ready_q(q);
+  // ... or in shared memory: the block's threads bring 16-byte units of it, spread over the
+  // banks for the eight lanes (two rows, four units) that read at once.
+  const uint32_t sQ = smem_u32(smem + L::kQOff), sQExp = sQ + L::kRows * D * 2;
+  auto q_unit = [](int r, int u) {
+    return r * (D / 8) + (u ^ (E4M3 ? (r & 1) : ((r & 1) << 2)));
+  };
+  constexpr int kQAll = L::kRows * (D / 8);
+  constexpr int kQUnits = L::kQShared ? (kQAll + kThreads - 1) / kThreads : 1;
+  uint4 qs[kQUnits];
+  auto load_q_shared = [&](const Walk& w) {
+#pragma unroll
+    for (int i = 0; i < kQUnits; ++i) {
+      const int x = tid + i * kThreads;
+      if (x < kQAll) qs[i] = q_load(w, x / (D / 8), x % (D / 8) * 8);
+    }
+  };
+  auto store_q_shared = [&]() {
+#pragma unroll
+    for (int i = 0; i < kQUnits; ++i) {
+      const int x = tid + i * kThreads, r = x / (D / 8), u = x % (D / 8);
+      if (x >= kQAll) break;
+      uint4 y = qs[i];
+      if constexpr (E4M3) {
+        uint32_t top = top_of(y);
+#pragma unroll
+        for (int k = D / 16; k > 0; k >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const int k = q_exponent(top);
+        y = to_f16(y, pow2i(k));
+        if (u == 0) st_shared_u32(sQExp + r * 4, __float_as_uint(a.scale_log2 * pow2i(-k)));
+      }
+      st_shared_v4(sQ + q_unit(r, u) * 16, y.x, y.y, y.z, y.w);
+    }
+  };
+  auto ready_q_shared = [&]() {  // after a barrier
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        c_row[n][e] = E4M3 ? __uint_as_float(ld_shared_u32(sQExp + (n * 8 + 2 * c4 + e) * 4))
+                           : a.scale_log2;
+  };
+  auto get_q = [&](int n, int i) {  // the registers of products 2 i and 2 i + 1
+    if constexpr (L::kQShared)
+      return ld_shared_v4(sQ + q_unit(n * 8 + g8, q_col(i) >> 3) * 16);
+    else
+      return q[n][i];
+  };
+  if constexpr (L::kQShared) {
+    load_q_shared(cw);
+    store_q_shared();
+    __syncthreads();
+    ready_q_shared();
+  } else {
+    load_q(cw, q);
+    ready_q();
+  }
 
   long long steps = hi - lo;  // blocks
   if (a.whole) {
@@ -378,8 +450,9 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
     Walk nw = cw;
     nw.next(a);
     const bool ends = nw.b != cw.b || nw.h != cw.h;  // the unit's last block
-    uint32_t qn[NT][D / 8];
-    if (ends && i + 1 < steps) load_q(nw, qn);
+    if constexpr (!L::kQShared) {
+      if (ends && i + 1 < steps) load_q(nw, qn);
+    }
 
     const int j0 = chunk_of(cw);
     const int pos0 = cw.s.len - cw.s.nq;  // position of the first new token
@@ -387,7 +460,8 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
     if (j0 < cw.s.len && j0 + kChunk > key_min) {
       const uint32_t sk = ring + stage * L::kStageBytes, sv = sk + L::kTileBytes;
       // ---- S^T = K Q^T: keys g8 and g8 + 8, query rows 2 c4 and 2 c4 + 1
-      float s[NT][4], s2[NT][4];  // two chains of products
+      constexpr bool kTwo = NT <= 2;  // two chains of products each, where there are few
+      float s[NT][4], s2[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -399,8 +473,9 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
           const uint4 k1 = ld_shared_v4(sk + k_unit<D, E4M3>(g8 + 8, 4 * x + c4) * 16);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma16816<E4M3>(s[n], k0.x, k1.x, k0.y, k1.y, q[n][4 * x], q[n][4 * x + 1]);
-            mma16816<E4M3>(s2[n], k0.z, k1.z, k0.w, k1.w, q[n][4 * x + 2], q[n][4 * x + 3]);
+            const uint4 y = get_q(n, x);
+            mma16816<E4M3>(s[n], k0.x, k1.x, k0.y, k1.y, y.x, y.y);
+            mma16816<E4M3>(kTwo ? s2[n] : s[n], k0.z, k1.z, k0.w, k1.w, y.z, y.w);
           }
         }
       } else {
@@ -410,14 +485,18 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
           const uint4 k1 = ld_shared_v4(sk + k_unit<D, E4M3>(g8 + 8, 4 * x + c4) * 16);
           const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t a0, a1, a2, a3;
-            e4m3_to_f16(w0[w], a0, a2);
-            e4m3_to_f16(w1[w], a1, a3);
+          for (int w = 0; w < 4; w += 2) {
+            uint32_t a0[4], a1[4];
+            e4m3_to_f16(w0[w], a0[0], a0[2]);
+            e4m3_to_f16(w1[w], a0[1], a0[3]);
+            e4m3_to_f16(w0[w + 1], a1[0], a1[2]);
+            e4m3_to_f16(w1[w + 1], a1[1], a1[3]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma16816<E4M3>(w & 1 ? s2[n] : s[n], a0, a1, a2, a3, q[n][8 * x + 2 * w],
-                       q[n][8 * x + 2 * w + 1]);
+            for (int n = 0; n < NT; ++n) {
+              const uint4 y = get_q(n, 2 * x + (w >> 1));
+              mma16816<E4M3>(s[n], a0[0], a0[1], a0[2], a0[3], y.x, y.y);
+              mma16816<E4M3>(kTwo ? s2[n] : s[n], a1[0], a1[1], a1[2], a1[3], y.z, y.w);
+            }
           }
         }
       }
@@ -550,7 +629,10 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
     if (ends || i + 1 == steps) {
       // ---- merge the warps' states of this piece
       const int M = cw.s.nq * G;
-      __syncthreads();  // the last merge's readers are done
+      const bool more = ends && i + 1 < steps;
+      if constexpr (L::kQShared) {
+        if (more) load_q_shared(nw);
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -558,17 +640,61 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
           float l = l_sum[n][e];
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-          const int r = n * 8 + 2 * c4 + e;
-          if (r < M) {
-            if (g8 == 0) ml[warp * L::kRows + r] = make_float2(m_ref[n][e], l);
-            float* dst = merge + (warp * L::kRows + r) * L::kPitch;
+          l_sum[n][e] = l;
+        }
+      // State `to` of the merge buffer: (m, l) and O of every row.
+      auto put_state = [&](int to) {
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-              dst[E4M3 ? (D / 8) * g8 + 2 * x : 16 * x + g8] = o[n][x][e];
-              dst[E4M3 ? (D / 8) * g8 + 2 * x + 1 : 16 * x + g8 + 8] = o[n][x][e + 2];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = n * 8 + 2 * c4 + e;
+            if (r < M) {
+              if (g8 == 0) ml[to * L::kRows + r] = make_float2(m_ref[n][e], l_sum[n][e]);
+              float* dst = merge + (to * L::kRows + r) * L::kPitch;
+#pragma unroll
+              for (int x = 0; x < D / 16; ++x) {
+                dst[E4M3 ? (D / 8) * g8 + 2 * x : 16 * x + g8] = o[n][x][e];
+                dst[E4M3 ? (D / 8) * g8 + 2 * x + 1 : 16 * x + g8 + 8] = o[n][x][e + 2];
+              }
             }
           }
+      };
+      __syncthreads();  // the last merge's readers are done, and every warp is with Q
+      if constexpr (L::kQShared) {
+        if (more) store_q_shared();
+      }
+      if constexpr (L::kFold == 2) {
+        if (warp >= L::kStates) put_state(warp - L::kStates);
+        __syncthreads();
+        if (warp < L::kStates) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = n * 8 + 2 * c4 + e;
+              if (r < M) {
+                const float2 z = ml[warp * L::kRows + r];
+                const float m = fmaxf(m_ref[n][e], z.x), mu = m == -INFINITY ? 0.f : m;
+                const float k0 = ex2_approx(m_ref[n][e] - mu), k1 = ex2_approx(z.x - mu);
+                m_ref[n][e] = m;
+                l_sum[n][e] = k0 * l_sum[n][e] + k1 * z.y;
+                const float* src = merge + (warp * L::kRows + r) * L::kPitch;
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                  const float y0 = src[E4M3 ? (D / 8) * g8 + 2 * x : 16 * x + g8];
+                  const float y1 = src[E4M3 ? (D / 8) * g8 + 2 * x + 1 : 16 * x + g8 + 8];
+                  o[n][x][e] = k0 * o[n][x][e] + k1 * y0;
+                  o[n][x][e + 2] = k0 * o[n][x][e + 2] + k1 * y1;
+                }
+              }
+            }
+          __syncwarp();  // this state has been read by every lane
+          put_state(warp);
         }
+      } else {
+        put_state(warp);
+      }
       __syncthreads();
       const bool from_start = piece_blk == cw.first;
       const bool direct = from_start && ends;
@@ -578,11 +704,11 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
         const int r = it / (D / 4), d0 = (it % (D / 4)) * 4;
         float m = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * L::kRows + r].x);
+        for (int w = 0; w < L::kStates; ++w) m = fmaxf(m, ml[w * L::kRows + r].x);
         const float mu = m == -INFINITY ? 0.f : m;
         float l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < L::kStates; ++w) {
           const float2 z = ml[w * L::kRows + r];
           const float k = ex2_approx(z.x - mu);
           l += k * z.y;
@@ -616,12 +742,16 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
       first_piece = false;
       clear();
       piece_blk = nw.blk;
-      if (ends) {
+      if (more) {
+        if constexpr (L::kQShared) {
+          ready_q_shared();
+        } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < D / 8; ++e) q[n][e] = qn[n][e];
-        ready_q(q);
+            for (int x = 0; x < kQRegs; ++x) q[n][x] = qn[n][x];
+          ready_q();
+        }
       }
     }
     cw = nw;
@@ -718,8 +848,10 @@ cudaError_t launch_impl(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
 
 template <int D, bool E4M3>
 cudaError_t launch_rows(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
-  return a.G * a.c.max_q <= 8 ? launch_impl<D, E4M3, 1>(a, ctas, stream)
-                              : launch_impl<D, E4M3, 2>(a, ctas, stream);
+  const int rows = a.G * a.c.max_q;
+  return rows <= 8    ? launch_impl<D, E4M3, 1>(a, ctas, stream)
+         : rows <= 16 ? launch_impl<D, E4M3, 2>(a, ctas, stream)
+                      : launch_impl<D, E4M3, 4>(a, ctas, stream);
 }
 
 }  // namespace
