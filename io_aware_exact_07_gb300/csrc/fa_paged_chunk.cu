@@ -17,6 +17,9 @@
 //   warps 8, 11     K and V tiles, one TMA box per page (or 16 .. 128 rows of it): into the K
 //                   and V rings, or codes into staging rings (e4m3)
 //   warps 9, 10     S issuer, which also loads Q, and PV issuer (one lane each)
+//   warp 11         also works out the CTA's pieces, ahead of the others, who take them from a
+//                   ring in shared memory (the divisions and loads behind a piece took each
+//                   role 3000 cycles, half of what a piece of 4 key tiles takes)
 //   warps 12-19     e4m3 only: turn staged codes, and Q, into f16 tiles with the rows' scales
 //                   folded in; the products then run in f16, and P is f16 too
 // Keys behind a sequence are masked by their number; V's rows there are made zero, since a
@@ -64,6 +67,7 @@ struct ChunkL {
   static constexpr int kCkStages = E4M3 ? (D == 64 ? 4 : 2) : 0;  // staged tiles of codes
   static constexpr int kCvStages = E4M3 ? (D == 64 ? 4 : 1) : 0;
   static constexpr int kCodeBytes = kTile * D;
+  static constexpr int kPieces = 4;                  // ring of pieces
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kTileBytes;
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;
@@ -72,8 +76,9 @@ struct ChunkL {
   static constexpr int kCvOff = kCOff + kCkStages * kCodeBytes;
   static constexpr int kBarOff = kCvOff + kCvStages * kCodeBytes;
   // q_full, q_empty, q_ready, K and V rings (full, empty), their staging rings (full, empty),
-  // s_full[2], s_free[2], p_full[2], pv_done[2], o_free, xbar[4], v_tail, drain, drain2, stall
-  static constexpr int kNumBars = 3 + 2 * (kKStages + kVStages) + 2 * (kCkStages + kCvStages) + 8 + 1 + 4 + 4;
+  // piece ring (full, empty), s_full[2], s_free[2], p_full[2], pv_done[2], o_free, xbar[4],
+  // v_tail, drain, drain2, stall
+  static constexpr int kNumBars = 3 + 2 * (kKStages + kVStages) + 2 * (kCkStages + kCvStages) + 2 * kPieces + 8 + 1 + 4 + 4;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;          // abort flag, TMEM address
   // e4m3: the scale bytes of staged tiles (K's stages: K's and V's; V's stages: V's); the
   // scales of the latest tiles and Q's row exponents of the latest pieces, for the softmax.
@@ -83,7 +88,8 @@ struct ChunkL {
   // before, so when both warpgroups have left the piece before that one's predecessor.
   static constexpr int kSlots = E4M3 ? 4 : 0;
   static_assert(!E4M3 || kSlots >= 2 + kKStages, "a slot is rewritten before it is read");
-  static constexpr int kBytesOff = (kMiscOff + 16 + 15) / 16 * 16;
+  static constexpr int kPieceOff = (kMiscOff + 16 + 15) / 16 * 16;
+  static constexpr int kBytesOff = kPieceOff + 48 * kPieces;
   static constexpr int kScaleOff = kBytesOff + kTile * (2 * kCkStages + kCvStages);
   static constexpr int kQExpOff = kScaleOff + 16 * kSlots;
   static constexpr int kFactorOff = kQExpOff + kTile * kSlots;  // f16 factors of K's and V's rows
@@ -100,6 +106,7 @@ struct Bars {
   uint32_t q_full, q_empty, q_ready;
   BarRun k_full, k_empty, v_full, v_empty;      // ring stages
   BarRun ck_full, ck_empty, cv_full, cv_empty;  // staging rings (e4m3)
+  BarRun pc_full, pc_empty;                     // pieces
   BarRun s_full, s_free, p_full, pv_done;   // per softmax warpgroup
   uint32_t o_free;
   BarRun xbar;
@@ -154,7 +161,15 @@ struct Unit {
   }
 };
 
-// A CTA's work, piece by piece; every role walks the same one. First `rounds` whole units,
+// A piece as the roles need it: key tiles [j0, j0 + nt) (nt < 0: no piece is left) of the query
+// tile whose first token is tok0 of its sequence, token row row0 of q and o, position pos0.
+struct Piece {
+  int b, h, qt, nt;
+  int j0, len, pos0, row0;
+  int rows, from_start, ends, pad;
+};
+
+// A CTA's work, piece by piece. First `rounds` whole units,
 // gridDim.x apart in the list, so that neighbouring CTAs take neighbouring query tiles of a
 // head at the same time and share its K/V tiles in L2; then a run of the places behind
 // those, cut where it begins and ends. The run's first unit, if another CTA began it, comes
@@ -435,6 +450,8 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     bars.ck_empty = run(L::kCkStages);
     bars.cv_full = run(L::kCvStages);
     bars.cv_empty = run(L::kCvStages);
+    bars.pc_full = run(L::kPieces);
+    bars.pc_empty = run(L::kPieces);
     bars.s_full = run(2);
     bars.s_free = run(2);
     bars.p_full = run(2);
@@ -469,6 +486,11 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       mbar_init(bars.cv_full[s], 9);
       mbar_init(bars.cv_empty[s], 4);
     }
+    for (int s = 0; s < L::kPieces; ++s) {
+      mbar_init(bars.pc_full[s], 1);
+      // a lane of each softmax and converter warp, of the K producer and of the two issuers
+      mbar_init(bars.pc_empty[s], kSoftmaxWarps + 3 + (E4M3 ? kConvWarps : 0));
+    }
     for (int g = 0; g < 2; ++g) {
       mbar_init(bars.s_full[g], 1);
       mbar_init(bars.s_free[g], 128);
@@ -496,21 +518,22 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint64_t tmo = args.sync.timeout_ns;
   Walk w;
-  w.rounds = rounds;
-  w.in_round = w.in_run = false;
-  w.tail = 0;
-  w.left = lo < hi ? hi - lo : 0;
-  w.run_b = plan->b;
-  w.run_h = plan->h;
-  w.run_qt = plan->qt;
-  w.run_at = plan->at;
-  if (rounds > 0) {
-    w.u.b = plan->b0;
-    w.u.h = plan->h0;
-    w.u.qt = plan->qt0;
-    w.u.seq(args);
+  if (warp == kVWarp) {
+    w.rounds = rounds;
+    w.in_round = w.in_run = false;
+    w.tail = 0;
+    w.left = lo < hi ? hi - lo : 0;
+    w.run_b = plan->b;
+    w.run_h = plan->h;
+    w.run_qt = plan->qt;
+    w.run_at = plan->at;
+    if (rounds > 0) {
+      w.u.b = plan->b0;
+      w.u.h = plan->h0;
+      w.u.qt = plan->qt0;
+      w.u.seq(args);
+    }
   }
-  w.next(args);
   __syncthreads();  // the plan has been read: its place is the exchange area from here on
 
   auto fail = [&](void) {
@@ -522,8 +545,39 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   const uint32_t sV = smem_u32(smem + L::kVOff);
   const uint32_t sP = smem_u32(smem + L::kPOff);
 
+  // Piece n, from the ring; false if the wait for it ran out.
+  const uint32_t sPc = smem_u32(smem + L::kPieceOff);
+  auto read_piece = [&](int n) {
+    const uint32_t at = sPc + (n % L::kPieces) * 48;
+    const uint4 x = ld_shared_v4(at), y = ld_shared_v4(at + 16), z = ld_shared_v4(at + 32);
+    Piece p;
+    p.b = static_cast<int>(x.x);
+    p.h = static_cast<int>(x.y);
+    p.qt = static_cast<int>(x.z);
+    p.nt = static_cast<int>(x.w);
+    p.j0 = static_cast<int>(y.x);
+    p.len = static_cast<int>(y.y);
+    p.pos0 = static_cast<int>(y.z);
+    p.row0 = static_cast<int>(y.w);
+    p.rows = static_cast<int>(z.x);
+    p.from_start = static_cast<int>(z.y);
+    p.ends = static_cast<int>(z.z);
+    p.pad = 0;
+    return p;
+  };
+  auto wait_piece = [&](int n) {
+    return mbar_wait_warp(bars.pc_full[n % L::kPieces], (n / L::kPieces) & 1, tmo, abort_flag);
+  };
+  auto wait_piece_lane = [&](int n) {
+    return mbar_wait(bars.pc_full[n % L::kPieces], (n / L::kPieces) & 1, tmo, abort_flag);
+  };
+  auto leave_piece = [&](int n) {  // by one lane
+    mbar_arrive(bars.pc_empty[n % L::kPieces]);
+  };
+
   if (E4M3 && warp >= kConvWarp) {
     regs_dec<E4M3 ? L::kRegsConv : 24>();
+    Piece pc = {};
     // ------------------------------------------------------------ converters
     // Four warps for K's tiles, four for V's (and for Q); warp x of them takes rows 32 x .. of
     // every tile: staged codes, as f16 into the tiles that the products read. A row's scale 2^E is folded in relative to the tile's largest,
@@ -555,7 +609,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     // 2^E are normal in f16 as they stand. Else the largest, at least `least`, so that the
     // factors that the softmax makes of it stay normal.
     auto top_of = [&](uint32_t bytes, int j, int least) -> int {
-      const int valid = w.u.s.len - (j * kTile + lane * 4);
+      const int valid = pc.len - (j * kTile + lane * 4);
       const bool usual = valid >= 4 && __vcmpgeu4(bytes, 0x71717171u) == 0xFFFFFFFFu &&
                          __vcmpleu4(bytes, 0x86868686u) == 0xFFFFFFFFu;
       if (__all_sync(0xffffffffu, usual)) return 127;
@@ -578,7 +632,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           f[0] = (prmt(bytes, 0u, 0x4140u) - 0x00700070u) << 10;
           f[1] = (prmt(bytes, 0u, 0x4342u) - 0x00700070u) << 10;
         } else {
-          const int valid = w.u.s.len - (j * kTile + lane * 4);
+          const int valid = pc.len - (j * kTile + lane * 4);
           f[0] = f[1] = 0u;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -596,7 +650,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       __syncwarp();
     };
     auto convert_tile = [&](uint32_t dst, int j) {
-      const int valid = w.u.s.len - j * kTile;
+      const int valid = pc.len - j * kTile;
       const uint32_t src = c_ring + cs * L::kCodeBytes;
 #pragma unroll
       for (int rg = 0; rg < 4; ++rg) {
@@ -660,10 +714,18 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       if (lane == 0) mbar_arrive(bars.q_ready);
       return true;
     };
-    do {
-      if (!is_k && w.nt > 0) ok = do_q();
-      for (int i = 0; ok && i < w.nt; ++i) {
-        const int j = w.j0 + i;
+    for (int n = 0;; ++n) {
+      if (!wait_piece(n)) {
+        ok = false;
+        break;
+      }
+      pc = read_piece(n);
+      if (pc.nt < 0) break;
+      __syncwarp();
+      if (lane == 0) leave_piece(n);
+      if (!is_k && pc.nt > 0) ok = do_q();
+      for (int i = 0; ok && i < pc.nt; ++i) {
+        const int j = pc.j0 + i;
         if (!mbar_wait_warp(c_full[cs], cph, tmo, abort_flag) ||
             !mbar_wait_warp(empty[ts], tph, tmo, abort_flag)) {
           ok = false;
@@ -696,10 +758,12 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           tph ^= 1u;
         }
       }
-    } while (ok && w.next(args));
+      if (!ok) break;
+    }
     if (!ok) fail();
   } else if (warp >= kSoftmaxWarps) {
     regs_dec<L::kRegsAux>();
+    Piece pc = {};
     const int n_box = kTile / box_rows;  // boxes of a key tile
     // Pages of 16-row groups, and the rows in them: lane l has group l % 8 of key tile j + l / 8,
     // so that one load serves four tiles. num_pages, which lies outside the maps and reads
@@ -712,8 +776,8 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       Rows r;
       r.page = args.c.num_pages;
       r.slot = page_row(args.c, pos);
-      if (pos < w.u.s.len) {
-        const int p = paged_page(args.c, w.u.b, pos);
+      if (pos < pc.len) {
+        const int p = paged_page(args.c, pc.b, pos);
         if (p >= 0) r.page = p;
       }
       return r;
@@ -746,10 +810,57 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       const int scale_lanes = is_k ? 16 : 8;
       uint32_t it = 0, s = 0, ph = 1, tails = 0;
       bool ok = true;
-      do {
+      Piece ahead = {};
+      for (int n = is_k ? 0 : -1; ok; ++n) {
+        if (is_k) {
+          if (!wait_piece(n)) {
+            fail();
+            ok = false;
+            break;
+          }
+          pc = read_piece(n);
+          __syncwarp();
+          if (pc.nt >= 0 && lane == 0) leave_piece(n);
+        } else {
+          // this warp works out the pieces: the next one before it loads V of this one
+          pc = ahead;
+          if (n < 0 || pc.nt >= 0) {
+            ahead.nt = -1;
+            if (w.next(args)) {
+              const int tok0 = w.u.qt * args.tt;
+              ahead.b = w.u.b;
+              ahead.h = w.u.h;
+              ahead.qt = w.u.qt;
+              ahead.nt = w.nt;
+              ahead.j0 = w.j0;
+              ahead.len = w.u.s.len;
+              ahead.pos0 = w.u.s.len - w.u.s.nq + tok0;
+              ahead.row0 = w.u.s.t0 + tok0;
+              ahead.rows = min(w.u.s.nq - tok0, args.tt) * args.G;
+              ahead.from_start = w.from_start;
+              ahead.ends = w.ends;
+            }
+            const int x = (n + 1) % L::kPieces;
+            if (!mbar_wait_warp(bars.pc_empty[x], (((n + 1) / L::kPieces) & 1) ^ 1, tmo, abort_flag)) {
+              fail();
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              const uint32_t at = sPc + x * 48;
+              st_shared_v4(at, ahead.b, ahead.h, ahead.qt, ahead.nt);
+              st_shared_v4(at + 16, ahead.j0, ahead.len, ahead.pos0, ahead.row0);
+              st_shared_v4(at + 32, ahead.rows, ahead.from_start, ahead.ends, 0);
+              mbar_arrive(bars.pc_full[x]);
+            }
+            __syncwarp();
+            if (n < 0) continue;
+          }
+        }
+        if (pc.nt < 0) break;
         Rows rows = {0, 0};
-        for (int i = 0; i < w.nt; ++i) {
-          const int j = w.j0 + i;
+        for (int i = 0; i < pc.nt; ++i) {
+          const int j = pc.j0 + i;
           if ((i & 3) == 0) rows = rows_of(j);
           const Rows box = rows_at(rows, i, lane * groups);
           long long at = 0;
@@ -758,7 +869,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             const Rows row = rows_at(rows, i, lane);
             there = row.page < args.c.num_pages;  // if not, zeros
             if (there)
-              at = (static_cast<long long>(row.page) * args.c.Hkv + w.u.h) * args.c.page_size + row.slot;
+              at = (static_cast<long long>(row.page) * args.c.Hkv + pc.h) * args.c.page_size + row.slot;
           }
           if (!mbar_wait_warp(empty[s], ph, tmo, abort_flag)) {
             fail();
@@ -766,7 +877,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             break;
           }
           const uint32_t dst = ring + s * kBytes;
-          const int valid = w.u.s.len - j * kTile;
+          const int valid = pc.len - j * kTile;
           // V's last tile: rows of its last page behind the sequence may hold anything, so it
           // comes on a barrier of its own and is handed on once they have been cleared
           const bool tail = !E4M3 && !is_k && valid < kTile;
@@ -781,10 +892,10 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           __syncwarp();
           if (lane < n_box) {
             if constexpr (E4M3) {
-              tma_load_4d(dst + lane * box_rows * D, tm, 0, box.slot, w.u.h, box.page, bar);
+              tma_load_4d(dst + lane * box_rows * D, tm, 0, box.slot, pc.h, box.page, bar);
             } else {
               for (int c = 0; c < L::kChunks; ++c)
-                tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, box.slot, w.u.h,
+                tma_load_4d(dst + c * 16384 + lane * box_rows * 128, tm, c * 64, box.slot, pc.h,
                             box.page, bar);
             }
           }
@@ -810,7 +921,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             ph ^= 1u;
           }
         }
-      } while (ok && w.next(args));
+      }
       // Drain: every load this warp issued must land before the CTA exits. Stage x was armed
       // for ring positions x, x + stages, ...; wait for the last one.
       if (tails > 0) mbar_wait_warp(bars.v_tail, (tails - 1) & 1, tmo, nullptr);
@@ -835,8 +946,15 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           fail();
           ok = false;
         }
-        while (ok) {
-          if (w.nt > 0) {
+        for (int n = 0; ok; ++n) {
+          if (!wait_piece_lane(n)) {
+            fail();
+            break;
+          }
+          pc = read_piece(n);
+          if (pc.nt < 0) break;
+          leave_piece(n);
+          if (pc.nt > 0) {
             // Q is replaced once the last piece's S products have completed
             if (q_cnt > 0 && !mbar_wait(bars.q_empty, (q_cnt - 1) & 1, tmo, abort_flag)) {
               fail();
@@ -844,7 +962,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             }
             mbar_expect_tx(bars.q_full, q_bytes);
             for (int c = 0; c < L::kChunks; ++c)
-              tma_load_3d(sQ + c * 16384, &tm_q, c * 64, w.u.h * args.G, w.u.s.t0 + w.u.qt * args.tt,
+              tma_load_3d(sQ + c * 16384, &tm_q, c * 64, pc.h * args.G, pc.row0,
                           bars.q_full);
             ++q_cnt;
             if (!mbar_wait(E4M3 ? bars.q_ready : bars.q_full, (q_cnt - 1) & 1, tmo, abort_flag)) {
@@ -852,7 +970,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
               break;
             }
           }
-          for (int p = 0; p < w.nt; ++p) {
+          for (int p = 0; p < pc.nt; ++p) {
             const int g = p & 1;
             if (!mbar_wait(bars.k_full[s], ph, tmo, abort_flag)) {
               ok = false;
@@ -890,8 +1008,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             fail();
             break;
           }
-          if (w.nt > 0) mma_commit(bars.q_empty);
-          if (!w.next(args)) break;
+          if (pc.nt > 0) mma_commit(bars.q_empty);
         }
         if (q_cnt > 0) mbar_wait(bars.q_full, (q_cnt - 1) & 1, tmo, nullptr);
         // Drain: all issued MMAs must finish before tensor memory is released.
@@ -910,12 +1027,18 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         const uint64_t dV0 = sdesc_sw128(sV, 16384, 1024);
         uint32_t s = 0, ph = 0, pc0 = 0, pc1 = 0;
         bool ok = true;
-        int count = 0;
-        while (ok) {
+        for (int count = 0; ok; ++count) {  // piece
+          if (!wait_piece_lane(count)) {
+            fail();
+            break;
+          }
+          pc = read_piece(count);
+          if (pc.nt < 0) break;
+          leave_piece(count);
           // The first PV of a piece overwrites O_0 or O_1, which the previous piece's
           // epilogue reads: it waits for that epilogue (o_free).
           bool first_any = true, first0 = true, first1 = true;
-          for (int p = 0; p < w.nt; ++p) {
+          for (int p = 0; p < pc.nt; ++p) {
             const int g = p & 1;
             const uint32_t pc = g ? pc1 : pc0;
             if (!mbar_wait(bars.v_full[s], ph, tmo, abort_flag) ||
@@ -962,8 +1085,6 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             fail();
             break;
           }
-          ++count;
-          if (!w.next(args)) break;
         }
         mma_commit(bars.drain2);
         mbar_wait(bars.drain2, 0, tmo, nullptr);
@@ -996,22 +1117,27 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     uint32_t s_cnt = 0, pv_cnt = 0;
     bool ok = true;
     int count = 0;
-    // The run's state is needed between pieces only: kept in local memory (the compiler
-    // cannot see through the pointer), it takes no registers from the row of scores.
-    Walk walk_mem = w;
-    Walk* wp = &walk_mem;
-    asm volatile("" : "+l"(wp)::"memory");
     PieceHeader* left = &headers[blockIdx.x];
     if (tid == 0) *left = PieceHeader{-1, 0, 1, 0};
-    do {
-      const int nt = wp->nt, j0 = wp->j0;
+    while (true) {
+      if (!wait_piece(count)) {
+        fail();
+        ok = false;
+        break;
+      }
+      int nt, j0;
       // keys [key_lo, key_hi) are visible to this row
-      int key_lo = 0, key_hi = wp->u.s.len;
+      int key_lo = 0, key_hi;
       {
-        const int pos = wp->u.s.len - wp->u.s.nq + wp->u.qt * args.tt + token_of(t);
+        const Piece pc = read_piece(count);
+        nt = pc.nt;
+        j0 = pc.j0;
+        key_hi = pc.len;
+        const int pos = pc.pos0 + token_of(t);
         if (args.causal && pos + 1 < key_hi) key_hi = pos + 1;
         if (args.wl >= 0) key_lo = pos - args.wl;
       }
+      if (nt < 0) break;
       float m_ref = -INFINITY;  // reference maximum, scaled log2 units
       float l_sum = 0.f;        // running sum of exp2(s*c - m_ref)
       int n_done = 0;           // key tiles of this warpgroup
@@ -1173,21 +1299,6 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         ++n_done;
       }
       if (!ok) break;
-      // The next piece is worked out while this one's last PV runs.
-      const int head = wp->u.h * args.G;                           // the tile's first query head
-      const int tok0 = wp->u.qt * args.tt;                         // its first token
-      const int rows = min(wp->u.s.nq - tok0, args.tt) * args.G;   // its rows
-      const int row0 = wp->u.s.t0 + tok0;
-      const bool from_start = wp->from_start, ends = wp->ends;
-      if (tid == 0) {
-        if (!from_start) left->ended = ends;
-        if (from_start && !ends) {
-          left->b = wp->u.b;
-          left->h = wp->u.h;
-          left->qt = wp->u.qt;
-        }
-      }
-      const bool more = wp->next(args);
       // ---- epilogue: merge the two warpgroups' partial softmaxes.
       // This warpgroup's last PV has completed once its pv_done phase has.
       if (n_done > 0) {
@@ -1226,7 +1337,9 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       const float inv = (l > 0.f) ? 1.f / l : 0.f;
       const float w0 = a0 * inv, w1 = a1 * inv;
       const float lse2 = (l > 0.f) ? m + __log2f(l) : -INFINITY;  // log2 units
-      const bool direct = from_start && ends;
+      const Piece pc = read_piece(count);
+      const int head = pc.h * args.G;  // the tile's first query head
+      const bool direct = pc.from_start && pc.ends;
       // This warpgroup writes output columns [D/2 g, D/2 g + D/2) from both O_0 and O_1.
       constexpr int kHalf = D / 2;
       if (direct) {
@@ -1269,20 +1382,20 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           const uint4 val = ld_shared_v4(
               stage + static_cast<uint32_t>(r * kHalf * 2 + ((u ^ (r & (kUnits - 1))) << 4)));
           const int row = quad * 32 + r;
-          if (row < rows) {
+          if (row < pc.rows) {
             const int tk = token_of(row);
-            const long long at = static_cast<long long>(row0 + tk) * args.H + head + (row - tk * args.G);
+            const long long at = static_cast<long long>(pc.row0 + tk) * args.H + head + (row - tk * args.G);
             *reinterpret_cast<uint4*>(args.o + at * D + kHalf * g + 8 * u) = val;
           }
         }
-        if (t < rows && g == 0) {
+        if (t < pc.rows && g == 0) {
           const int tk = token_of(t);
-          args.lse[static_cast<long long>(row0 + tk) * args.H + head + (t - tk * args.G)] = lse2 * kLn2;
+          args.lse[static_cast<long long>(pc.row0 + tk) * args.H + head + (t - tk * args.G)] = lse2 * kLn2;
         }
       } else {
         // a piece: normalised, fp32. Slot 0 continues what an earlier CTA began, slot 1 is
         // continued by the next.
-        const long long at = (2ll * blockIdx.x + (from_start ? 1 : 0)) * kTile + t;
+        const long long at = (2ll * blockIdx.x + (pc.from_start ? 1 : 0)) * kTile + t;
 #pragma unroll
         for (int c = 0; c < kHalf / 16; ++c) {
           const uint32_t col = static_cast<uint32_t>(kHalf * g + 16 * c);
@@ -1296,22 +1409,31 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
             y[k] = has0 ? __uint_as_float(o0[k]) * w0 : 0.f;
             if (has1) y[k] = fmaf(__uint_as_float(o1[k]), w1, y[k]);
           }
-          if (t < rows) {
+          if (t < pc.rows) {
             float4* dst = reinterpret_cast<float4*>(args.o_part + at * D + col);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
           }
         }
-        if (t < rows && g == 0) args.lse_part[at] = lse2;
+        if (t < pc.rows && g == 0) args.lse_part[at] = lse2;
+      }
+      if (tid == 0) {
+        if (!pc.from_start) left->ended = pc.ends;
+        if (pc.from_start && !pc.ends) {
+          left->b = pc.b;
+          left->h = pc.h;
+          left->qt = pc.qt;
+        }
       }
       tc_fence_before();
       mbar_arrive(bars.o_free);
+      __syncwarp();
+      if (lane == 0) leave_piece(count);
       ++count;
       tile_cnt += nt;
       q_cnt += nt > 0;
-      if (!more) break;
-    } while (true);
+    }
   }
 
   tc_fence_before();
