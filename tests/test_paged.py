@@ -22,14 +22,14 @@ def attn(b, x, **kw):
     return fa.paged_attn(x.q, x.k, x.v, x.table, x.kv, cu_seqlens_q=x.cu, **x.sc, **kw)
 
 
-def run(b, causal=True, window_left=-1, max_q=None, rows=None):
+def run(b, causal=True, window_left=-1, max_q=None):
     x = b.fill().on(DEV)
+    rows = int(b.cu[-1])  # those of the sequences: the others are not written
     o, lse = attn(b, x, causal=causal, window_left=window_left, max_q=max_q or max(b.nq))
     sync()
     check_attn(o, lse, b.oracle(causal, window_left), rows)
     o2, lse2 = attn(b, x, causal=causal, window_left=window_left, max_q=max_q or max(b.nq))
     sync()
-    rows = int(b.cu[-1])
     assert torch.equal(o[:rows], o2[:rows]) and torch.equal(lse[:rows], lse2[:rows])
     return x, o, lse
 
@@ -479,3 +479,132 @@ def test_binding_refusals_on_the_gpu():
         with pytest.raises((fa.FAError, ValueError)):
             fa.paged_attn(**dict(base, **bad))
     sync()
+
+
+# ------------------------------------------------------------------ more shapes and values
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,G,Hkv,kv,page", [
+    ([5, 8, 1], 4, 2, [1000, 8, 300], 32),     # 17 to 32 rows per K/V head
+    ([1, 1], 17, 2, [700, 129], 48),
+    ([2, 3], 10, 1, [260, 2], 16),
+    ([1, 1, 1], 32, 1, [4000, 15, 16], 128),
+    ([8, 1, 4], 4, 1, [3000, 1, 200], 64),     # 32 rows, cut between CTAs
+])
+def test_up_to_32_rows(nq, G, Hkv, kv, page, d, e4m3):
+    run(Batch(nq, kv, page, Hkv, d, e4m3, G=G, seed=sum(kv) + G))
+
+
+@pytest.mark.parametrize("d,e4m3", [(64, False), (64, True), (128, False), (128, True)])
+def test_chunks_of_many_query_tiles(d, e4m3):
+    # more query tiles than CTAs: whole tiles in rounds, then runs that are cut
+    run(Batch([1300], [1500], 64, 8, d, e4m3, G=2, seed=31))
+    run(Batch([700, 1, 0, 333], [705, 2000, 40, 333], 16, 4, d, e4m3, G=3, seed=32), True, 200)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_fewer_query_tiles_than_ctas(e4m3):
+    # one or two heads' query tiles over a long cache: every tile is cut, each CTA's run ends
+    # inside the next
+    run(Batch([200], [8111], 128, 2, 64, e4m3, G=4, seed=33))
+    run(Batch([64, 40], [3000, 9000], 16, 1, 128, e4m3, G=8, seed=34), False)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(seed):
+    g = np.random.RandomState(1000 + seed)
+    B = int(g.choice([1, 2, 5, 30]))
+    top = int(g.choice([40, 300, 1500]))
+    kv = [int(n) for n in g.randint(0, top + 1, B)]
+    most = int(g.choice([1, 3, 9, 70]))
+    nq = [int(min(g.randint(0, most + 1), n + 2)) for n in kv]
+    nq[int(g.randint(B))] = most
+    b = Batch(nq, kv, int(g.choice([16, 32, 80, 256])), int(g.choice([1, 2, 3])),
+              int(g.choice([64, 128])), bool(g.randint(2)), G=int(g.choice([1, 2, 5, 8])),
+              seed=seed, layout=str(g.choice(["head", "row", "pair"])),
+              extra_rows=int(g.randint(3)), table_pad=int(g.randint(3)))
+    run(b, bool(g.randint(2)), int(g.choice([-1, -1, 0, 17, 130])))
+
+
+def test_batches_without_new_tokens():
+    b = Batch([0, 0, 0], [40, 0, 7], 16, 2, 64, G=2, seed=35, extra_rows=9)
+    x = b.fill().on(DEV)
+    before = x.k.clone()
+    for n in (1, 8, 100):   # each of the kernels
+        out = (torch.full_like(x.q, 5.0), torch.full(x.q.shape[:2], 5.0, device=DEV))
+        attn(b, x, causal=True, max_q=n, out=out)
+        assert all((t == 5).all() for t in out)
+    fa.paged_write(x.k_new, x.v_new, x.k, x.v, x.table, x.kv, cu_seqlens_q=x.cu)
+    sync()
+    assert torch.equal(x.k, before)
+
+
+@pytest.mark.parametrize("nq", [[1, 1], [4, 6], [60, 33]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_quantised_rows_of_very_different_magnitude(nq, d):
+    # scales of neighbouring keys differ by up to 2^45; an absolute error of 2^-25 of the
+    # largest scale 2^E per key is what the tile conversion may add, and 2^-25 times 448 of it
+    # what the rounding of P to f16 may
+    g = torch.Generator().manual_seed(d)
+    b = Batch(nq, [700, 300], 16, 2, d, True, G=4, seed=36)
+    for i in range(2):
+        n = b.rows["k"][i].shape[0]
+        e = torch.randint(-24, 1, (n, 2, 1), generator=g)
+        b.rows["k"][i] = (b.rows["k"][i].float() * torch.exp2(e.float())).to(torch.bfloat16)
+        e = torch.randint(-40, 6, (n, 2, 1), generator=g)
+        b.rows["v"][i] = (b.rows["v"][i].float() * torch.exp2(e.float())).to(torch.bfloat16)
+    x = b.fill().on(DEV)
+    o, lse = attn(b, x, causal=True, max_q=max(nq))
+    sync()
+    o_ref, lse_ref, o_abs = b.oracle(True)
+    top = 2.0 ** max(int(s.max()) - 127 for s in [b.scale["v"][b.scale["v"] != 133]])
+    tol = 1.05 * 2.0 ** -8 * (o_abs + np.abs(o_ref)) + 700 * 449 * 2.0 ** -25 * top
+    assert np.all(np.abs(o.double().cpu().numpy() - o_ref) <= tol)
+    assert np.abs(lse.double().cpu().numpy() - lse_ref).max() <= 2e-4
+
+
+@pytest.mark.parametrize("nq", [[1, 1], [60, 33]])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("q_exp,k_exp,v_exp", [(20, -20, 0), (-60, 0, 0), (0, 0, -30), (-15, 12, 4),
+                                               (0, -40, 0)])
+def test_magnitudes_of_queries_keys_and_values(q_exp, k_exp, v_exp, nq, e4m3):
+    b = Batch(nq, [300, 170], 16, 2, 128, e4m3, G=2, seed=37)
+    by = lambda t, e: (t.float() * 2.0 ** e).to(torch.bfloat16)
+    b.q = by(b.q, q_exp)
+    for n, e in (("k", k_exp), ("v", v_exp)):
+        b.rows[n] = [by(t, e) for t in b.rows[n]]
+    run(b)
+
+
+@pytest.mark.parametrize("nq", [[1, 1], [60, 33]])
+def test_rows_that_hold_a_nan(nq):
+    # a NaN among a quantised sequence's keys or values reaches that sequence's rows alone
+    for n in "kv":
+        b = Batch(nq, [300, 170], 16, 1, 64, True, G=2, seed=38)
+        b.rows[n][0][5, 0, 3] = float("nan")
+        x = b.fill().on(DEV)
+        o, lse = attn(b, x, causal=True, max_q=max(nq))
+        sync()
+        assert torch.isnan(o[:nq[0]]).all()
+        b.rows[n][0][5, 0, 3] = 1.0
+        ref = b.oracle(True)
+        check_attn(o[nq[0]:], lse[nq[0]:], tuple(r[nq[0]:] for r in ref))
+
+
+@pytest.mark.parametrize("d,e4m3", [(64, False), (128, False), (64, True), (128, True)])
+def test_stalled_chunk_times_out_and_the_next_call_is_right(d, e4m3):
+    b = Batch([90, 3], [700, 300], 16, 2, d, e4m3, G=2, seed=39)
+    x = b.fill().on(DEV)
+    sync()
+    fa.fa_set_wait_timeout_ns(200_000_000)
+    try:
+        fa.fa_test_inject_stall(1)
+        attn(b, x, causal=True, max_q=90)
+        assert reported() == fa.FA_ERR_TIMEOUT
+    finally:
+        fa.fa_test_inject_stall(0)
+        fa.fa_set_wait_timeout_ns(4_000_000_000)
+    o, lse = attn(b, x, causal=True, max_q=90)
+    sync()
+    check_attn(o, lse, b.oracle(True))
