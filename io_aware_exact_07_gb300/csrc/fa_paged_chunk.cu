@@ -51,9 +51,11 @@ struct ChunkL {
   static constexpr int kThreads = kWarps * 32;
   // Registers per thread at launch, and as the warpgroups share them out afterwards.
   static constexpr int kRegsLaunch = E4M3 ? 96 : 168;
-  static constexpr int kRegsSoftmax = E4M3 ? 144 : 216;
+  // (e4m3, measured us per 128 x 128 tile and SM for softmax, aux, converters: d = 128 144, 64, 64
+  // 1.71, 160, 64, 48 1.79, 128, 64, 80 1.71; d = 64 160, 64, 48 1.11, 144, 64, 64 2.40.)
+  static constexpr int kRegsSoftmax = E4M3 ? (D == 64 ? 160 : 144) : 216;
   static constexpr int kRegsAux = E4M3 ? 64 : 72;   // producers and issuers
-  static constexpr int kRegsConv = E4M3 ? 64 : 0;   // converters
+  static constexpr int kRegsConv = E4M3 ? (D == 64 ? 48 : 64) : 0;  // converters
   static_assert(256 * kRegsSoftmax + 128 * kRegsAux + (kThreads - 384) * kRegsConv <=
                     kThreads * kRegsLaunch,
                 "register reallocation exceeds the block's launch allocation");
@@ -1163,10 +1165,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           ev_inv = z.z;
         }
         // bf16: the whole row in registers at once. e4m3, where the converters need registers
-        // and instruction cache: half a row at a time, once for its maximum and once for P (in
-        // loops at d = 128, where straight code took 2.2 us a tile instead of 1.8 and where the
-        // converters' code is twice as long; straight at d = 64, 1.2 us instead of 1.5).
-        constexpr int kUnroll = D == 64 ? 2 : 1;
+        // and instruction cache: half a row at a time, in one loop.
         constexpr int kCols = E4M3 ? 64 : 128;
         float s[kCols];
         const bool edge = k0 < key_lo || k0 + kTile > key_hi;
@@ -1182,26 +1181,27 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           tc_fence_before();
           mbar_arrive(bars.s_free[g]);
         };
-        float mx_row = -INFINITY;
-#pragma unroll kUnroll
-        for (int c0 = 0; c0 < kTile; c0 += kCols) {
-          load_scores(c0);
-          if constexpr (!E4M3) release_scores();
-          if (edge) mask_row<kCols>(s, key_lo - k0 - c0, key_hi - k0 - c0);
-          mx_row = fmaxf(mx_row, max_row<kCols>(s));
-        }
-        const float m_new = fmaxf(m_ref, E4M3 ? fmaf(mx_row, c_t, ev) : mx_row * c_t);
-        const bool grow = m_new > m_ref + kRescale;
+        bool grow = false;
         float alpha = 1.f;
-        if (grow) {
-          alpha = ex2_approx(m_ref - m_new);  // 0 when m_ref = -inf
-          l_sum *= alpha;
-          m_ref = m_new;
-        }
-        const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+        uint64_t nm2 = 0;  // what a score's exponent adds, twice
+        // Takes the largest score of a row, or of a half of it, into the reference maximum, which
+        // moves when it would be exceeded by more than 2^8; whether it has.
+        auto refer_to = [&](float mx) -> bool {
+          const float m_new = fmaxf(m_ref, E4M3 ? fmaf(mx, c_t, ev) : mx * c_t);
+          const bool grows = m_new > m_ref + kRescale;
+          if (grows) {
+            const float x = ex2_approx(m_ref - m_new);  // 0 when m_ref = -inf
+            alpha *= x;
+            l_sum *= x;
+            m_ref = m_new;
+          }
+          const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+          const float nm = E4M3 ? ev - m_use : -m_use;
+          nm2 = f2_pack(nm, nm);
+          grow |= grows;
+          return grows;
+        };
         const uint64_t c2 = f2_pack(c_t, c_t);
-        const float nm = E4M3 ? ev - m_use : -m_use;
-        const uint64_t nm2 = f2_pack(nm, nm);
         uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // four packed partial sums
         constexpr int kPk = kCols / 2;
         uint32_t pk[kPk];
@@ -1235,19 +1235,42 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           }
         };
         if constexpr (E4M3) {
-#pragma unroll kUnroll
-          for (int half = 0; half < 2; ++half) {
+          // The first half's weights are stored before the second half's maximum is known: on
+          // the rare tile where that moves the reference, both halves are done over.
+          bool settled = false, stored = n_done == 0;
+#pragma unroll 1
+          for (int half = 0; half < 2;) {
             load_scores(half * 64);
-            if (half == 1) release_scores();
             if (edge) mask_row<kCols>(s, key_lo - k0 - half * 64, key_hi - k0 - half * 64);
+            if (!settled) {
+              const bool grows = refer_to(max_row<kCols>(s));
+              if (half == 1) {
+                settled = true;
+                if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) rs2[x] = 0ull;
+                  half = 0;
+                  continue;
+                }
+              }
+            }
+            if (half == 1) release_scores();
             weights(s, pk);
-            if (half == 0 && n_done > 0 && !wait_pv()) {
-              pv_ok = false;
-              break;
+            if (!stored) {
+              if (!wait_pv()) {
+                pv_ok = false;
+                break;
+              }
+              stored = true;
             }
             store_half(half);
+            ++half;
           }
         } else {
+          load_scores(0);
+          release_scores();
+          if (edge) mask_row<kCols>(s, key_lo - k0, key_hi - k0);
+          refer_to(max_row<kCols>(s));
           weights(s, pk);
           // The first half goes out now if the previous PV has already completed; otherwise the
           // second half's exponentials come first.
