@@ -34,10 +34,14 @@ __device__ __forceinline__ int scale_exponent(uint32_t top) {
   return e < kScaleMin ? kScaleMin : (e > kScaleMax ? kScaleMax : e);
 }
 
-__device__ __forceinline__ uint32_t codes2(uint32_t pair, float f) {
-  const float lo = __uint_as_float(pair << 16) * f;
-  const float hi = __uint_as_float(pair & 0xFFFF0000u) * f;
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+// The codes of four bf16 values times f, f.
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, uint64_t ff) {
+  float x0, x1, x2, x3;
+  f2_unpack(f2_mul(f2_pack(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u)), ff), x0, x1);
+  f2_unpack(f2_mul(f2_pack(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u)), ff), x2, x3);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x2, x3), __NV_SATFINITE, __NV_E4M3);
+  return prmt(lo, hi, 0x5410u);
 }
 
 }  // namespace
@@ -76,13 +80,15 @@ __global__ void __launch_bounds__(kIoWarps * 32) fa_paged_write_kernel(const Pag
   const int page = paged_page(a.c, b, pos);
   if (page < 0) return;
   const int slot = page_row(a.c, pos);
+  const long long at0 = page * a.c.stride_page + slot * a.c.stride_row + u * 8;
+  const long long scale0 = static_cast<long long>(page) * a.c.Hkv * a.c.page_size + slot;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int r = r0 + i * kRows;
     const bool real = r < 2 * a.c.Hkv;
     const bool is_v = r >= a.c.Hkv;
     const int h = is_v ? r - a.c.Hkv : r;
-    const long long at = page * a.c.stride_page + h * a.c.stride_head + slot * a.c.stride_row + u * 8;
+    const long long at = at0 + h * a.c.stride_head;
     uint8_t* base = is_v ? a.c.v : a.c.k;
     if constexpr (!E4M3) {
       if (real) *reinterpret_cast<uint4*>(base + at * 2) = x[i];
@@ -95,16 +101,13 @@ __global__ void __launch_bounds__(kIoWarps * 32) fa_paged_write_kernel(const Pag
       for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const bool finite = top < 0x7F80u;
       const int e = finite ? scale_exponent(top) : 0;
-      const float f = pow2i(-e);
-      uint2 w;
-      w.x = codes2(x[i].x, f) | codes2(x[i].y, f) << 16;
-      w.y = codes2(x[i].z, f) | codes2(x[i].w, f) << 16;
+      const uint64_t ff = f2_pack(pow2i(-e), pow2i(-e));
+      uint2 w = make_uint2(codes4(x[i].x, x[i].y, ff), codes4(x[i].z, x[i].w, ff));
       if (!finite) w = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
       if (real) {
         *reinterpret_cast<uint2*>(base + at) = w;
         if (u == 0)
-          (is_v ? a.c.v_scale : a.c.k_scale)[(static_cast<long long>(page) * a.c.Hkv + h) *
-                                                 a.c.page_size + slot] =
+          (is_v ? a.c.v_scale : a.c.k_scale)[scale0 + h * a.c.page_size] =
               static_cast<uint8_t>(finite ? e + 127 : kScaleNaN);
       }
     }

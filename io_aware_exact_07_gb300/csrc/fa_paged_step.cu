@@ -203,20 +203,44 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   };
   Plan* plan = reinterpret_cast<Plan*>(smem + L::kPlanOff);
   static_assert(sizeof(Plan) <= 256, "plan area");
+  bool whole = a.whole != 0;
+  int most = 0, heads = 0;  // blocks of this thread's longest sequence, its K/V heads
   auto weight = [&](int b) -> long long {
     if (b >= a.c.B) return 0;
     const int n = span_of<kBlock>(a, paged_attn_seq(a.c, b)).n;
-    return static_cast<long long>(a.whole ? min(n, 1) : n) * a.c.Hkv;
+    most = max(most, n);
+    if (n > 0) heads += a.c.Hkv;
+    return static_cast<long long>(whole ? min(n, 1) : n) * a.c.Hkv;
   };
   long long total = 0, x0 = 0;
-  for (int b0 = 0; b0 < a.c.B; b0 += kThreads) {
-    const long long x = weight(b0 + tid);
-    if (b0 == 0) x0 = x;
-    long long sum;
-    block_scan<kWarps>(x, plan->warp_sums, &sum);
-    total += sum;
+  auto add_up = [&]() {
+    total = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += kThreads) {
+      const long long x = weight(b0 + tid);
+      if (b0 == 0) x0 = x;
+      long long sum;
+      block_scan<kWarps>(x, plan->warp_sums, &sum);
+      total += sum;
+    }
+  };
+  add_up();
+  long long per = (total + gridDim.x - 1) / gridDim.x;
+  // About as many heads as CTAs, of about the same length: a head each, since five sixths of
+  // the SMs can draw all that HBM gives where a warp's work per byte is least, and cutting
+  // costs pieces and their merge. 128 heads (152 CTAs), cut and whole: 16384 bf16 keys of 128
+  // 161 and 156 us, 4096 keys 48 and 44, 1000 keys 15.6 and 13.9. Where the warps' work counts
+  // it is the cut that pays: 16384 quantised keys 95 and 107, 32 rows 193 and 214 (d = 64:
+  // 1000 keys 10.7 and 12.0, 4096 keys 29.5 and 27.6).
+  if constexpr (!E4M3 && D == 128 && NT <= 2) {
+    long long all;
+    block_scan<kWarps>(heads, plan->warp_sums, &all);
+    const bool uneven = 5ll * most > 6 * per;
+    if (!whole && all <= gridDim.x && !__syncthreads_or(uneven)) {
+      whole = true;
+      add_up();
+      per = 1;
+    }
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
   const long long lo = per * blockIdx.x;
   const long long hi = lo + per < total ? lo + per : total;
   PieceHeader* headers = static_cast<PieceHeader*>(a.headers);
@@ -404,7 +428,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   }
 
   long long steps = hi - lo;  // blocks
-  if (a.whole) {
+  if (whole) {
     Walk t = cw;
     steps = 0;
     for (long long u = lo; u < hi; ++u) {

@@ -608,3 +608,11 @@ def test_stalled_chunk_times_out_and_the_next_call_is_right(d, e4m3):
     o, lse = attn(b, x, causal=True, max_q=90)
     sync()
     check_attn(o, lse, b.oracle(True))
+
+
+@pytest.mark.parametrize("kv", [[700] * 17, [700] * 16 + [840], [700] * 16 + [900], [700] * 15,
+                                [700] * 16 + [0], [700] * 19, [700] * 20])
+def test_about_one_head_per_cta(kv):
+    # the choice between a head per CTA and heads cut into equal runs, on both sides
+    run(Batch([1] * len(kv), kv, 32, 8, 128, G=2, seed=41, table_pad=2))
+    run(Batch([3] * len(kv), kv, 32, 8, 128, G=4, seed=42, table_pad=2), True, 600)
