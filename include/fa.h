@@ -238,13 +238,13 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
  *     16 bytes, below 2^40 bytes.
  *   type: FA_CACHE_BF16 (bf16 values) or FA_CACHE_E4M3 (one e4m3 code per value and
  *     one scale byte per row, k_scale and v_scale: uint8 [num_pages, H_kv,
- *     page_size], contiguous, 16-byte aligned; not used for bf16). A quantised value is code * 2^E with
- *     scale byte E + 127, E the smallest exponent in [-117, 7] that keeps the row's
- *     largest magnitude within 448 * 2^E (0 for a row of zeros); codes are rounded
- *     to nearest even and saturate (magnitudes above 57344 = 448 * 2^7). A row that
- *     holds a NaN or an infinity gets scale byte 255 and code 0x7F throughout and
- *     counts as NaN. Both products and read-back use code * 2^E, which is exact in
- *     bf16. Scale bytes 135 to 254 are never written; they count as 134.
+ *     page_size], contiguous, 16-byte aligned; not used for bf16). A quantised value is
+ *     code * 2^E with scale byte E + 127, E the smallest exponent in [-117, 7] that
+ *     keeps the row's largest magnitude within 448 * 2^E (0 for a row of zeros); codes
+ *     are rounded to nearest even and saturate (magnitudes above 57344 = 448 * 2^7). A
+ *     row that holds a NaN or an infinity gets scale byte 255 and code 0x7F throughout
+ *     and counts as NaN. code * 2^E is exact in bf16, and read-back gives it so. Scale
+ *     bytes 135 to 254 are never written; they count as 134.
  *   page_size: a multiple of 16; d: 64 or 128.
  * The batch, B sequences (device pointers):
  *   page_table: int32, row b at b * table_stride; its entry i < max_pages names the
@@ -304,6 +304,16 @@ fa_status fa_paged_read(const void* k_pages, const void* v_pages, const uint8_t*
  *   may overlap need one each.
  * The work of a call is divided among the SMs by the lengths found on the device, so a
  * captured call may be replayed with other lengths. Results do not depend on atomics.
+ * Accuracy, against exact attention of the cached values: scores, sums and O's accumulators
+ * are fp32; the weights P are rounded to bf16 (by at most 2^-8 of each), from a quantised
+ * cache to f16 (2^-11 of each, or 2^-32 of the row's largest weight times value scale where
+ * that is more); O is rounded to bf16. From a quantised cache q enters the product in f16,
+ * each row times the power of two that brings its largest magnitude into [2^14, 2^15), 2^60 at
+ * most: an element below 2^-29 of that magnitude is off by at most 2^-40 of it. With more than
+ * 32 query rows per K/V head ((H / H_kv) * max_q) the keys and values are f16 too, relative to
+ * the largest scale 2^E among the 128 keys around them: exact where their own is at least 2^-15
+ * of it, off by at most 2^-25 of it otherwise; that largest scale counts as at least 2^-40 for
+ * keys and 2^-60 for values.
  * Errors: FA_ERR_INVALID_ARG (as above, H not a multiple of H_kv, scale not positive and
  * finite, window_left < -1, max_q < 1, T * H >= 2^31), FA_ERR_UNSUPPORTED (H / H_kv >
  * 128, and as above), FA_ERR_WORKSPACE, FA_ERR_CUDA. */
@@ -397,8 +407,8 @@ fa_status fa_butterfly_mask(uint8_t* mask_host, int nb);
 /* Reads the status word of the current device after synchronising `stream`;
  * returns FA_OK or the first device-side error recorded since the last clear:
  * FA_ERR_TIMEOUT (a bounded wait ran out), FA_ERR_INVALID_ARG when a paged call
- * met a length, offset or page number out of range (see there), or FA_ERR_CUDA when a kernel found
- * its launch unusable and returned without work (the d = 128 forward and the
+ * met a length, offset or page number out of range (see there), or FA_ERR_CUDA
+ * when a kernel found its launch unusable and returned without work (the d = 128 forward and the
  * d = 128 key-tile backward kernel use nearly all 227 KB of shared memory with
  * no alignment slack and check that their dynamic shared memory starts on a
  * 1024-byte boundary).
@@ -421,7 +431,8 @@ void fa_set_wait_timeout_ns(uint64_t ns);
  * FA_ERR_TIMEOUT recorded; the hook is consumed by that launch and later
  * launches run normally. mode selects the launch:
  *   1: the next forward-type kernel (fa_fwd and its _gqa / _window forms,
- *      fa_decode, fa_fwd_fp8, fa_fwd_fp8_gqa);
+ *      fa_decode, fa_fwd_fp8, fa_fwd_fp8_gqa, fa_paged_attn with more than 32
+ *      query rows per K/V head: with fewer its kernel waits for nothing);
  *   2: the next dK/dV kernel (fa_bwd and its _gqa / _window / _noalloc forms,
  *      fa_bwd_dkdv);
  *   3: the next dQ kernel (the same backward calls, fa_bwd_dq).

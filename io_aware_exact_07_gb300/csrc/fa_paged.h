@@ -219,8 +219,8 @@ struct PagedAttnArgs {
 };
 constexpr int kStepRows = 32;   // most query rows per K/V head of the step kernel
 // Page tables with room for so many keys: heads are not cut, and neither the merge nor its
-// workspace is needed (8 sequences of up to 512 keys, 4 K/V heads, d = 64: 9.3 us cut, 7.8
-// whole; from some 1000 keys on the longest head of a ragged batch costs more than that).
+// workspace is needed (8 sequences, 4 K/V heads, d = 64, cut and whole: up to 512 keys 9.3 and
+// 7.8 us, up to 1000 9.0 and 9.6, 2000 10.4 and 13.9).
 constexpr int kWholeKeys = 512;
 
 cudaError_t launch_paged_write(const PagedWriteArgs& a, bool e4m3, cudaStream_t stream);

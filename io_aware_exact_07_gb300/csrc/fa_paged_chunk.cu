@@ -43,7 +43,6 @@ constexpr int kPvIssuer = 10;
 constexpr int kVWarp = 11;
 constexpr int kConvWarp = 12;  // first of the converters (e4m3)
 constexpr int kConvWarps = 8;
-constexpr float kRescale = 8.0f;  // log2 units: rescale O when m grows by > 2^8
 
 template <int D, bool E4M3>
 struct ChunkL {
@@ -582,9 +581,10 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     Piece pc = {};
     // ------------------------------------------------------------ converters
     // Four warps for K's tiles, four for V's (and for Q); warp x of them takes rows 32 x .. of
-    // every tile: staged codes, as f16 into the tiles that the products read. A row's scale 2^E is folded in relative to the tile's largest,
-    // 2^Et: code * 2^(E - Et) is exact in f16 down to E - Et = -15, and off by at most 2^-25
-    // below, 2^-33 of the largest value that the tile's codes can stand for. The softmax
+    // every tile: staged codes, as f16 into the tiles that the products read. A row's scale 2^E
+    // is folded in relative to the tile's largest, 2^Et: code * 2^(E - Et) is exact in f16 down
+    // to E - Et = -15, and off by at most 2^-25 below, 2^-33 of the largest value that the
+    // tile's codes can stand for. The softmax
     // takes 2^Et into account. (Codes come by TMA, not by loads of these warps: a barrier
     // arrival waits for a thread's loads in flight, so none could be ahead.)
     // A pass covers 16 codes for each of 4 lanes of 8 rows, odd rows at the other half of the
@@ -1185,9 +1185,9 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         float alpha = 1.f;
         uint64_t nm2 = 0;  // what a score's exponent adds, twice
         // Takes the largest score of a row, or of a half of it, into the reference maximum, which
-        // moves when it would be exceeded by more than 2^8; whether it has.
+        // moves when it would be exceeded by more than 2^kRescale; whether it has.
         auto refer_to = [&](float mx) -> bool {
-          const float m_new = fmaxf(m_ref, E4M3 ? fmaf(mx, c_t, ev) : mx * c_t);
+          const float m_new = fmaxf(m_ref, E4M3 ? fmaf(mx, c_t, ev - kF16Lift) : mx * c_t);
           const bool grows = m_new > m_ref + kRescale;
           if (grows) {
             const float x = ex2_approx(m_ref - m_new);  // 0 when m_ref = -inf
@@ -1222,7 +1222,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           return true;
         };
         // P = 2^(s * c_t + nm) of N scores, rounded to bf16 for the product (at most 2^-8 of each
-        // weight), or to f16 (2^-11, and 2^-25 where it is below 2^-14); l keeps fp32.
+        // weight), or to f16 (2^-11, or 2^-32 of the largest where that is more); l keeps fp32.
         auto weights = [&](const float* x, uint32_t* to) {
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {

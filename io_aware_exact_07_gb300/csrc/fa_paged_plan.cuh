@@ -9,6 +9,12 @@
 
 namespace fa {
 
+// The reference maximum of a running softmax moves when a score exceeds it by more than 2^8
+// (scores are in log2 units). With f16 weights it lies 2^7 below the largest score: weights
+// reach 2^15, which f16 holds, and the smallest ones keep 7 bits more.
+constexpr float kRescale = 8.0f;
+constexpr float kF16Lift = 7.0f;
+
 // Sum over the block's threads of x, and the sum of those before this one.
 template <int WARPS>
 __device__ __forceinline__ long long block_scan(long long x, long long* warp_sums,

@@ -36,7 +36,6 @@ namespace {
 
 constexpr int kChunk = 16;                  // keys of a warp's step
 constexpr int kMergeWarps = 8;
-constexpr float kRescale = 8.0f;            // log2 units: rescale O when m grows by > 2^8
 constexpr int kSmemMax = 232448;
 
 template <int D, bool E4M3, int NT>
@@ -541,6 +540,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
           v_inv[e] = pow2i(127 - 64 - vb);
         }
       }
+      constexpr float kLift = E4M3 ? kF16Lift : 0.f;
       bool grow = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -565,9 +565,9 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          grow |= fmaxf(s[n][e], s[n][e + 2]) > m_ref[n][e] + kRescale;
-      // The reference maximum moves only when a score exceeds it by more than 2^8 (so P
-      // stays below 2^8): most steps need one vote instead of the row maxima.
+          grow |= fmaxf(s[n][e], s[n][e + 2]) > m_ref[n][e] + (kRescale + kLift);
+      // The reference maximum moves rarely, so most steps need one vote instead of the row
+      // maxima.
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
             float mx = fmaxf(s[n][e], s[n][e + 2]);
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-            const float m_new = fmaxf(m_ref[n][e], mx);
+            const float m_new = fmaxf(m_ref[n][e], mx - kLift);
             const float alpha = m_new == -INFINITY ? 1.f : ex2_approx(m_ref[n][e] - m_new);
             m_ref[n][e] = m_new;
             l_sum[n][e] *= alpha;
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
           l_sum[n][1] += p[1] + p[3];
         }
         // P is rounded to bf16 for the product (at most 2^-8 of each weight), or to f16 (2^-11,
-        // and 2^-25 where it is below 2^-14); the sum keeps fp32
+        // or 2^-32 of the largest weight where that is more); the sum keeps fp32
         p0[n] = movmatrix_t(E4M3 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
         p1[n] = movmatrix_t(E4M3 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
       }

@@ -616,3 +616,27 @@ def test_about_one_head_per_cta(kv):
     # the choice between a head per CTA and heads cut into equal runs, on both sides
     run(Batch([1] * len(kv), kv, 32, 8, 128, G=2, seed=41, table_pad=2))
     run(Batch([3] * len(kv), kv, 32, 8, 128, G=4, seed=42, table_pad=2), True, 600)
+
+
+@pytest.mark.parametrize("nq", [1, 640])
+def test_many_small_weights_beside_a_large_one(nq):
+    # one key with a score of 18 above the other 65535, whose values are 1 and its own 0 (but one): O =
+    # w / (1 + w) with w = 65535 e^-18, about 2^-10. Each weight may be off by 2^-32 of the
+    # largest (and P and O by bf16's half step, as elsewhere).
+    n, page, G = 65536, 256, 32
+    k = torch.zeros(n, 1, 64)
+    k[0] = 2.25
+    v = torch.ones(n, 1, 64)
+    v[0, 0, 1:] = 0.0   # (the row's scale is that of the others)
+    c = fa.paged_cache(n // page, page, 1, 64, e4m3=True, device=DEV)
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV).reshape(1, -1)
+    kv = torch.tensor([n], dtype=torch.int32, device=DEV)
+    fa.paged_write(k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV), page_table=table,
+                   kv_lens=kv, **c)
+    q = torch.ones(nq, G, 64, dtype=torch.bfloat16, device=DEV)
+    o, lse = fa.paged_attn(q, page_table=table, kv_lens=kv, max_q=nq, causal=False, **c)
+    sync()
+    w = (n - 1) * np.exp(-18.0)
+    ref = w / (1 + w)
+    assert (o[..., 1:].double() - ref).abs().max().item() <= 1.05 * 2.0 ** -7 * ref + n * 2.0 ** -32
+    assert (lse.double() - 18 - np.log1p(w)).abs().max().item() <= 2e-4
