@@ -25,8 +25,13 @@
 // Keys behind a sequence are masked by their number; V's rows there are made zero, since a
 // weight of zero would not hide a NaN.
 //
-// Bounds: for chunks the exponentials (one per score, 16 a cycle and SM) and the tensor core
-// (512 cycles of products per 128 x 128 tile at d = 128); for few rows HBM.
+// Bounds: for chunks the tensor core (1024 cycles of products per 128 x 128 tile at d = 128, of
+// 1540 measured with a bf16 cache: 0.80 us a tile; each warpgroup's chain of scores, maximum,
+// exponentials and the handshakes with the products is the rest); with few rows HBM; from an
+// e4m3 cache (1.47 us a tile) the conversion, which takes registers, issue slots and bandwidth
+// of shared memory from the softmax (without it 1.21 us), and the chain that goes from a PV
+// product over the S that takes its place to the next P (with neither conversion nor
+// exponentials still 0.95 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -51,7 +56,7 @@ struct ChunkL {
   // Registers per thread at launch, and as the warpgroups share them out afterwards.
   static constexpr int kRegsLaunch = E4M3 ? 96 : 168;
   // (e4m3, measured us per 128 x 128 tile and SM for softmax, aux, converters: d = 128 144, 64, 64
-  // 1.71, 160, 64, 48 1.79, 128, 64, 80 1.71; d = 64 160, 64, 48 1.11, 144, 64, 64 2.40.)
+  // 1.47, 160, 64, 48 1.49, 128, 64, 80 1.50; d = 64 160, 64, 48 1.05, 144, 64, 64 1.25.)
   static constexpr int kRegsSoftmax = E4M3 ? (D == 64 ? 160 : 144) : 216;
   static constexpr int kRegsAux = E4M3 ? 64 : 72;   // producers and issuers
   static constexpr int kRegsConv = E4M3 ? (D == 64 ? 48 : 64) : 0;  // converters
@@ -59,14 +64,18 @@ struct ChunkL {
                     kThreads * kRegsLaunch,
                 "register reallocation exceeds the block's launch allocation");
   static constexpr int kTileBytes = kTile * D * 2;   // a 128 x D 16-bit tile
-  static constexpr int kPBytes = kTile * kTile * 2;  // P_g
+  // P_g: in shared memory (bf16), or in tensor memory (f16, e4m3): there the converters need the
+  // room and the bandwidth of shared memory (us per tile with P in shared memory and in tensor
+  // memory: e4m3 d = 128 1.71 and 1.47, d = 64 1.11 and 1.05).
+  static constexpr int kPBytes = E4M3 ? 0 : kTile * kTile * 2;
   static constexpr int kChunks = D / 64;             // 64-column (128-byte) swizzle chunks
-  // Ring depths. e4m3 at d = 128 has room for one K and one V tile (K's is free again once its
-  // S product has run) and three staged tiles of codes.
-  static constexpr int kKStages = D == 64 ? (E4M3 ? 2 : 4) : (E4M3 ? 1 : 2);
-  static constexpr int kVStages = kKStages;
-  static constexpr int kCkStages = E4M3 ? (D == 64 ? 4 : 2) : 0;  // staged tiles of codes
-  static constexpr int kCvStages = E4M3 ? (D == 64 ? 4 : 1) : 0;
+  // Ring depths; e4m3: of tiles ready for the products, and of staged codes (us per tile at d =
+  // 128 with 2, 1, 3, 2 tiles of K, V, K's codes, V's codes 1.47; 2, 2, 2, 1 1.67; 1, 1, 4, 3
+  // 1.49; 1, 2, 2, 3 1.50).
+  static constexpr int kKStages = D == 64 && !E4M3 ? 4 : 2;
+  static constexpr int kVStages = D == 128 && E4M3 ? 1 : kKStages;
+  static constexpr int kCkStages = E4M3 ? (D == 64 ? 4 : 3) : 0;
+  static constexpr int kCvStages = E4M3 ? (D == 64 ? 4 : 2) : 0;
   static constexpr int kCodeBytes = kTile * D;
   static constexpr int kPieces = 4;                  // ring of pieces
   static constexpr int kQOff = 0;
@@ -101,6 +110,9 @@ struct ChunkL {
   static_assert(kSmemBytes <= 232448, "shared memory exceeds the per-block limit");
   __device__ static constexpr uint32_t col_s(int g) { return 128u * static_cast<uint32_t>(g); }
   __device__ static constexpr uint32_t col_o(int g) { return 256u + 128u * static_cast<uint32_t>(g); }
+  // e4m3: P_g's 64 columns, beside O_g where it leaves them, else in the second half of S_g
+  __device__ static constexpr uint32_t col_p(int g) { return (D == 64 ? col_o(g) : col_s(g)) + 64u; }
+  static constexpr bool kPInS = E4M3 && D == 128;
 };
 
 struct Bars {
@@ -978,15 +990,17 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
               ok = false;
               break;
             }
-            // S_g is free once its warpgroup has read the previous S_g.
+            // S_g is free once its warpgroup has read the previous S_g, or, with P_g in it, once
+            // the previous PV_g has run.
+            const BarRun s_free = L::kPInS ? bars.pv_done : bars.s_free;
             if (g == 0) {
-              if (seen0 && !mbar_wait(bars.s_free[0], sf0++ & 1, tmo, abort_flag)) {
+              if (seen0 && !mbar_wait(s_free[0], sf0++ & 1, tmo, abort_flag)) {
                 ok = false;
                 break;
               }
               seen0 = true;
             } else {
-              if (seen1 && !mbar_wait(bars.s_free[1], sf1++ & 1, tmo, abort_flag)) {
+              if (seen1 && !mbar_wait(s_free[1], sf1++ & 1, tmo, abort_flag)) {
                 ok = false;
                 break;
               }
@@ -1064,8 +1078,12 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk) {
               const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-              mma_ss(tmem + L::col_o(g), dp + off, dv + static_cast<uint64_t>((kk * 2048) >> 4),
-                     kIdPV, (first && kk == 0) ? 0u : 1u);
+              const uint64_t v_at = dv + static_cast<uint64_t>((kk * 2048) >> 4);
+              const uint32_t acc = (first && kk == 0) ? 0u : 1u;
+              if constexpr (E4M3)
+                mma_ts(tmem + L::col_o(g), tmem + L::col_p(g) + 8 * kk, v_at, kIdPV, acc);
+              else
+                mma_ss(tmem + L::col_o(g), dp + off, v_at, kIdPV, acc);
             }
             if (g) first1 = false; else first0 = false;
             mma_commit(bars.pv_done[g]);
@@ -1102,6 +1120,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + lane_base + L::col_s(g);
     const uint32_t tO = tmem + lane_base + L::col_o(g);
+    const uint32_t tP = tmem + lane_base + L::col_p(g);  // e4m3
     // r / G for r < 128, G <= 128: the excess r / 65536 of the product stays below 1 / G
     auto token_of = [&](int r) {
       return static_cast<int>((static_cast<uint32_t>(r) * args.g_magic) >> 16);
@@ -1184,22 +1203,19 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         bool grow = false;
         float alpha = 1.f;
         uint64_t nm2 = 0;  // what a score's exponent adds, twice
-        // Takes the largest score of a row, or of a half of it, into the reference maximum, which
-        // moves when it would be exceeded by more than 2^kRescale; whether it has.
-        auto refer_to = [&](float mx) -> bool {
+        // Takes the largest score of a row into the reference maximum, which moves when it would
+        // be exceeded by more than 2^kRescale.
+        auto refer_to = [&](float mx) {
           const float m_new = fmaxf(m_ref, E4M3 ? fmaf(mx, c_t, ev - kF16Lift) : mx * c_t);
-          const bool grows = m_new > m_ref + kRescale;
-          if (grows) {
-            const float x = ex2_approx(m_ref - m_new);  // 0 when m_ref = -inf
-            alpha *= x;
-            l_sum *= x;
+          grow = m_new > m_ref + kRescale;
+          if (grow) {
+            alpha = ex2_approx(m_ref - m_new);  // 0 when m_ref = -inf
+            l_sum *= alpha;
             m_ref = m_new;
           }
           const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
           const float nm = E4M3 ? ev - m_use : -m_use;
           nm2 = f2_pack(nm, nm);
-          grow |= grows;
-          return grows;
         };
         const uint64_t c2 = f2_pack(c_t, c_t);
         uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // four packed partial sums
@@ -1210,7 +1226,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         auto store_half = [&](int h) {
 #pragma unroll
           for (int v = 0; v < 8; ++v) {
-            const int x = (E4M3 ? 0 : h * 32) + 4 * v;
+            const int x = h * 32 + 4 * v;
             st_shared_v4((prow ^ static_cast<uint32_t>(v << 4)) + static_cast<uint32_t>(h * 16384),
                          pk[x], pk[x + 1], pk[x + 2], pk[x + 3]);
           }
@@ -1235,37 +1251,28 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           }
         };
         if constexpr (E4M3) {
-          // The first half's weights are stored before the second half's maximum is known: on
-          // the rare tile where that moves the reference, both halves are done over.
-          bool settled = false, stored = n_done == 0;
+          // The halves are loaded as 0, 1 (for the maximum; then 1's weights) and 0 again: P_g,
+          // where it lies in S_g, takes the columns of half 1.
+          float mx = -INFINITY;
 #pragma unroll 1
-          for (int half = 0; half < 2;) {
+          for (int step = 0; step < 3; ++step) {
+            const int half = step & 1;
             load_scores(half * 64);
+            if (step == 2 && !L::kPInS) release_scores();
             if (edge) mask_row<kCols>(s, key_lo - k0 - half * 64, key_hi - k0 - half * 64);
-            if (!settled) {
-              const bool grows = refer_to(max_row<kCols>(s));
-              if (half == 1) {
-                settled = true;
-                if (__any_sync(0xffffffffu, grows)) {
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) rs2[x] = 0ull;
-                  half = 0;
-                  continue;
-                }
-              }
-            }
-            if (half == 1) release_scores();
-            weights(s, pk);
-            if (!stored) {
-              if (!wait_pv()) {
+            if (step < 2) mx = fmaxf(mx, max_row<kCols>(s));
+            if (step == 0) continue;
+            if (step == 1) {
+              refer_to(mx);
+              if (n_done > 0 && !wait_pv()) {
                 pv_ok = false;
                 break;
               }
-              stored = true;
             }
-            store_half(half);
-            ++half;
+            weights(s, pk);
+            tmem_st32(tP + half * 32, pk);
           }
+          tmem_st_wait();
         } else {
           load_scores(0);
           release_scores();
@@ -1316,7 +1323,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           tmem_st_wait();
         }
         // P_g's generic-proxy stores become visible to the tensor core's reads.
-        fence_proxy_async_smem();
+        if constexpr (!E4M3) fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(bars.p_full[g]);
         ++n_done;
@@ -1365,7 +1372,40 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       const bool direct = pc.from_start && pc.ends;
       // This warpgroup writes output columns [D/2 g, D/2 g + D/2) from both O_0 and O_1.
       constexpr int kHalf = D / 2;
-      if (direct) {
+      if (direct && E4M3) {
+        // P_g takes no shared memory here that rows could be gathered in: 32 bytes of a row, a
+        // whole sector, at a time
+        const int tk = token_of(t);
+        const long long at = static_cast<long long>(pc.row0 + tk) * args.H + head + (t - tk * args.G);
+#pragma unroll 1
+        for (int c = 0; c < kHalf / 16; ++c) {
+          const uint32_t col = static_cast<uint32_t>(kHalf * g + 16 * c);
+          uint32_t o0[16], o1[16];
+          if (has0) tmem_ld16(tmem + lane_base + L::col_o(0) + col, o0);
+          if (has1) tmem_ld16(tmem + lane_base + L::col_o(1) + col, o1);
+          tmem_ld_wait();
+          uint32_t pk[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float v0 = 0.f, v1 = 0.f;
+            if (has0) {
+              v0 = __uint_as_float(o0[2 * k]) * w0;
+              v1 = __uint_as_float(o0[2 * k + 1]) * w0;
+            }
+            if (has1) {
+              v0 = fmaf(__uint_as_float(o1[2 * k]), w1, v0);
+              v1 = fmaf(__uint_as_float(o1[2 * k + 1]), w1, v1);
+            }
+            pk[k] = pack_bf16x2(v0, v1);
+          }
+          if (t < pc.rows) {
+            uint4* dst = reinterpret_cast<uint4*>(args.o + at * D + col);
+            dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          }
+        }
+        if (t < pc.rows && g == 0) args.lse[at] = lse2 * kLn2;
+      } else if (direct) {
         // Each warp first puts its 32 rows x D bytes into shared memory (rows of P_g that it
         // itself writes, free once its last PV has completed), then stores them so that
         // neighbouring lanes cover whole rows.
