@@ -310,7 +310,7 @@ fa_status fa_paged_read(const void* k_pages, const void* v_pages, const uint8_t*
  * that is more); O is rounded to bf16. From a quantised cache q enters the product in f16,
  * each row times the power of two that brings its largest magnitude into [2^14, 2^15), 2^60 at
  * most: an element below 2^-29 of that magnitude is off by at most 2^-40 of it. With more than
- * 32 query rows per K/V head ((H / H_kv) * max_q) the keys and values are f16 too, relative to
+ * 24 query rows per K/V head ((H / H_kv) * max_q) the keys and values are f16 too, relative to
  * the largest scale 2^E among the 128 keys around them: exact where their own is at least 2^-15
  * of it, off by at most 2^-25 of it otherwise; that largest scale counts as at least 2^-40 for
  * keys and 2^-60 for values.
@@ -431,7 +431,7 @@ void fa_set_wait_timeout_ns(uint64_t ns);
  * FA_ERR_TIMEOUT recorded; the hook is consumed by that launch and later
  * launches run normally. mode selects the launch:
  *   1: the next forward-type kernel (fa_fwd and its _gqa / _window forms,
- *      fa_decode, fa_fwd_fp8, fa_fwd_fp8_gqa, fa_paged_attn with more than 32
+ *      fa_decode, fa_fwd_fp8, fa_fwd_fp8_gqa, fa_paged_attn with more than 24
  *      query rows per K/V head: with fewer its kernel waits for nothing);
  *   2: the next dK/dV kernel (fa_bwd and its _gqa / _window / _noalloc forms,
  *      fa_bwd_dkdv);

@@ -805,7 +805,7 @@ static PagedWorkspace paged_workspace(int G, int d, int max_q, long long max_key
   const long long rows = static_cast<long long>(G) * max_q;
   w.whole = rows <= fa::kStepRows && max_keys <= fa::kWholeKeys;
   w.ctas = num_sms < 256 ? num_sms : 256;  // the chunk kernel plans with a thread per CTA
-  w.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= fa::kStepRows ? fa::kStepRows : fa::kTile;
+  w.rows = rows <= fa::kStepRows ? static_cast<int>((rows + 7) / 8 * 8) : fa::kTile;
   const size_t slots = 2 * static_cast<size_t>(w.ctas) * w.rows;
   w.lse_off = round256(static_cast<size_t>(w.ctas) * 16);
   w.o_off = w.lse_off + round256(slots * sizeof(float));

@@ -217,7 +217,7 @@ struct PagedAttnArgs {
   float* lse_part;
   SyncParams sync;
 };
-constexpr int kStepRows = 32;   // most query rows per K/V head of the step kernel
+constexpr int kStepRows = 24;   // most query rows per K/V head of the step kernel
 // Page tables with room for so many keys: heads are not cut, and neither the merge nor its
 // workspace is needed (8 sequences, 4 K/V heads, d = 64, cut and whole: up to 512 keys 9.3 and
 // 7.8 us, up to 1000 9.0 and 9.6, 2000 10.4 and 13.9).

@@ -1,5 +1,5 @@
 // Attention of few new tokens per sequence over a paged cache (a decode step: one new
-// token, or a handful of drafted ones): at most 32 query rows per K/V head, G = H / Hkv
+// token, or a handful of drafted ones): at most 24 query rows per K/V head, G = H / Hkv
 // heads times nq tokens. The page "FlashAttention — L3 Cross-Paper Synthesis" (section 3)
 // names this case, bound by reading K and V, as left unoptimised. HBM is the bound, so the
 // kernel is a stream of K and V through shared memory, each byte read once per K/V head:
@@ -9,13 +9,15 @@
 //    that the main loop has no block barrier and loads run ahead across heads and sequences.
 //    16 keys lie in one page (its size is a multiple of 16), so one table entry serves them.
 //  - S^T = K Q^T and O^T += V^T P^T with m16n8k16 products: the keys (then the columns of V)
-//    are the 16 rows, the query rows the 8 columns (1, 2 or 4 times). With so few query rows
+//    are the 16 rows, the query rows the 8 columns (1 to 3 times). With so few query rows
 //    the products are below what bounds the kernel (a 128-row tensor-memory tile would be
 //    three quarters empty, and its softmax walks all of it); keeping S and P in registers
 //    saves the handshakes that a short sequence cannot hide. From 17 rows on it is these
-//    products that bound it, at some 7 cycles each and SM. 24 sequences, 8 K/V heads, 32 rows,
-//    d = 128, here and with 128-row tiles: 8192 bf16 keys 156 and 140 us, 1024 keys 44 and 47,
-//    8192 quantised keys 161 and 201; 128 sequences of 200 keys 60 and 74.
+//    products that bound it, at some 7 cycles each and SM. Here and with 128-row tiles, us, 24
+//    sequences, 8 K/V heads, 24 rows: d = 128, 8192 bf16 keys 138 and 132, 1024 keys 35 and 38,
+//    e4m3 122 and 147, 34 and 50; d = 64 79 and 82, 22 and 31, e4m3 86 and 107; 128 sequences
+//    of 200 keys 48 and 55, 4 of 3000 13 and 17. 32 rows: 8192 keys 156 and 133, 1024 44 and 38,
+//    e4m3 160 and 148, d = 64 94 and 82, 128 of 200 keys 60 and 55.
 //  - The order of the columns d within a product is free as long as both operands share
 //    it: a thread takes the 16 bytes of a row that it can load at once.
 //  - e4m3 codes become f16 between shared memory and the product, which the hardware converts
@@ -54,10 +56,11 @@ struct StepL {
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kScaleBytes = E4M3 ? 32 : 0;       // K's and V's 16 scale bytes
   static constexpr int kPitch = D + 4;                    // merge buffer row, in floats
-  // 32 rows: Q lies in shared memory, one copy for all warps, and two warps join their states
-  // in registers before the merge, whose buffer then takes half the room.
-  static constexpr bool kQShared = NT == 4;
-  static constexpr int kFold = NT == 4 ? 2 : 1;
+  // From 17 rows on Q lies in shared memory, one copy for all warps. Where the merge's buffer
+  // would leave no room for the ring, two warps first join their states in registers, and it
+  // takes half (20 rows, d = 64, where it fits without: 58.6 us, with 62.4).
+  static constexpr bool kQShared = NT == 3;
+  static constexpr int kFold = NT == 3 && kRowBytes == 256 ? 2 : 1;
   static constexpr int kStates = kWarps / kFold;
   static constexpr int kQBytes = kQShared ? kRows * (D * 2 + 4) : 0;  // rows, and their exponents
   static constexpr int kMergeBytes = kStates * kRows * kPitch * 4;
@@ -227,10 +230,10 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   // About as many heads as CTAs, of about the same length: a head each, since five sixths of
   // the SMs can draw all that HBM gives where a warp's work per byte is least, and cutting
   // costs pieces and their merge. 128 heads (152 CTAs), cut and whole: 16384 bf16 keys of 128
-  // 161 and 156 us, 4096 keys 48 and 44, 1000 keys 15.6 and 13.9. Where the warps' work counts
-  // it is the cut that pays: 16384 quantised keys 95 and 107, 32 rows 193 and 214 (d = 64:
-  // 1000 keys 10.7 and 12.0, 4096 keys 29.5 and 27.6).
-  if constexpr (!E4M3 && D == 128 && NT <= 2) {
+  // 161 and 156 us, 4096 keys 48 and 44, 1000 keys 15.6 and 13.9, with 20 rows 56 and 51 for 4096.
+  // Where the warps' work counts it is the cut that pays: 16384 quantised keys 95 and 107 (d =
+  // 64: 1000 keys 10.7 and 12.0, 4096 keys 29.5 and 27.6).
+  if constexpr (!E4M3 && D == 128) {
     long long all;
     block_scan<kWarps>(heads, plan->warp_sums, &all);
     const bool uneven = 5ll * most > 6 * per;
@@ -875,7 +878,7 @@ cudaError_t launch_rows(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   const int rows = a.G * a.c.max_q;
   return rows <= 8    ? launch_impl<D, E4M3, 1>(a, ctas, stream)
          : rows <= 16 ? launch_impl<D, E4M3, 2>(a, ctas, stream)
-                      : launch_impl<D, E4M3, 4>(a, ctas, stream);
+                      : launch_impl<D, E4M3, 3>(a, ctas, stream);
 }
 
 }  // namespace
