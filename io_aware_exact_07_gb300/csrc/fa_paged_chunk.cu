@@ -151,26 +151,54 @@ struct Unit {
     s = paged_attn_seq(a.c, b);
     n_qt = (s.nq + a.tt - 1) / a.tt;
   }
-  // The first unit of the batch (b = B if it has none).
-  __device__ __forceinline__ void first(const PagedAttnArgs& a) {
+  __device__ __forceinline__ void at(unsigned x) {  // its unit x
+    h = static_cast<int>(x / static_cast<unsigned>(n_qt));
+    qt = static_cast<int>(x) - h * n_qt;
+  }
+  // Unit x of those from sequence b0 on, by the whole warp (b0 is the same for all lanes, x need
+  // not be); b = B past the end. 32 sequences at a time: one by one, each a load from L2, 1023
+  // sequences of one token beside a chunk took 400 us of planning.
+  __device__ __forceinline__ void find(const PagedAttnArgs& a, int b0, unsigned x) {
+    const int lane = threadIdx.x & 31;
+    bool found = false;
+    b = a.c.B;
     h = qt = n_qt = 0;
-    for (b = 0; b < a.c.B; ++b) {
+    for (; b0 < a.c.B; b0 += 32) {
+      unsigned n = 0;  // units of sequence b0 + lane (those of the batch fit an int)
+      if (b0 + lane < a.c.B)
+        n = static_cast<unsigned>((paged_attn_seq(a.c, b0 + lane).nq + a.tt - 1) / a.tt * a.c.Hkv);
+      unsigned inc = n;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, inc, k);
+        if (lane >= k) inc += y;
+      }
+      const unsigned all = __shfl_sync(0xffffffffu, inc, 31);
+      int i = 0;  // sequences that end at or before x
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1)
+        if (__shfl_sync(0xffffffffu, inc, i + k - 1) <= x) i += k;
+      const unsigned before = __shfl_sync(0xffffffffu, inc - n, i);
+      if (!found) {
+        found = x < all;
+        x -= found ? before : all;
+        if (found) b = b0 + i;
+      }
+      if (__all_sync(0xffffffffu, found)) break;
+    }
+    if (found) {
       seq(a);
-      if (n_qt > 0) return;
+      at(x);
     }
   }
-  // k units further on; b = B past the end.
+  // k units further on, by a warp whose lanes all hold the same unit.
   __device__ __forceinline__ void advance(const PagedAttnArgs& a, int k) {
     if (b >= a.c.B) return;
-    // (units of a sequence: at most T * Hkv, which fits an int)
-    unsigned at = static_cast<unsigned>(h * n_qt + qt + k), all;
-    while (at >= (all = static_cast<unsigned>(n_qt * a.c.Hkv))) {
-      at -= all;
-      if (++b >= a.c.B) return;
-      seq(a);
-    }
-    h = static_cast<int>(at / static_cast<unsigned>(n_qt));
-    qt = static_cast<int>(at) - h * n_qt;
+    const unsigned x = static_cast<unsigned>(h * n_qt + qt + k);
+    if (x < static_cast<unsigned>(n_qt * a.c.Hkv))
+      at(x);
+    else
+      find(a, b, x);
   }
 };
 
@@ -316,16 +344,17 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     long long rem, lo, hi;
     int b, h, qt, at;    // where the run begins
     int b0, h0, qt0;     // the first whole unit
+    int last;
   };
   static_assert(sizeof(Plan) <= 2 * kTile * 8, "plan scratch");
   Plan* plan = reinterpret_cast<Plan*>(smem + L::kPlanOff);
   // Places of one K/V head of sequence b; long chunks are summed by the whole warp.
-  bool many = false;  // a sequence seen by this thread has several query tiles per head
+  int last = -1;  // the last sequence seen by this thread with several query tiles per head
   auto head_places = [&](int b) -> long long {
     PagedSeq s = {0, 0, 0};
     if (b < args.c.B) s = paged_attn_seq(args.c, b);
     const int n_qt = (s.nq + args.tt - 1) / args.tt;
-    many |= n_qt > 1;
+    if (n_qt > 1) last = b;
     long long sum = 0;
     if (n_qt <= 2)
       for (int i = 0; i < n_qt; ++i) sum += tiles_of(args, s, args.tt, i).n;
@@ -354,17 +383,21 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     block_scan<L::kWarps>(x, plan->warp_sums, &sum);
     total += sum;
   }
-  const bool shared = __syncthreads_or(many) != 0;  // some head has several query tiles
+  if (tid == 0) plan->last = -1;
+  __syncthreads();
+  if (last >= 0) atomicMax(&plan->last, last);
+  __syncthreads();
+  last = plan->last;
   const int ctas = static_cast<int>(gridDim.x);
   const long long per = (total + ctas - 1) / ctas;
   // Whole units in rounds, as long as no CTA gets more than its share; thread c follows CTA
-  // c. Without several query tiles of a head there is nothing to share, and no round.
+  // c. Behind the last sequence with several query tiles per head there is nothing to share,
+  // and no round.
   long long load = 0;
   int rounds = 0;
-  if (shared) {
+  if (last >= 0) {
     Unit v;
-    v.first(args);
-    if (tid < ctas) v.advance(args, tid);
+    v.find(args, 0, static_cast<unsigned>(tid));
     if (tid == static_cast<int>(blockIdx.x) && v.b < args.c.B) {
       plan->b0 = v.b;
       plan->h0 = v.h;
@@ -373,10 +406,12 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     while (true) {
       const bool none = v.b >= args.c.B;
       const int n = none ? 0 : tiles_of(args, v.s, args.tt, v.qt).n;
-      if (__syncthreads_or(tid < ctas && (none || load + n > per))) break;
+      if (__syncthreads_or((tid < ctas && (none || load + n > per)) || (tid == 0 && v.b > last))) break;
       load += n;
       ++rounds;
-      v.advance(args, ctas);
+      // lane l is l units behind lane 0 (which is not past the end while a round begins)
+      const unsigned x = static_cast<unsigned>(v.h * v.n_qt + v.qt + ctas);
+      v.find(args, __shfl_sync(0xffffffffu, v.b, 0), __shfl_sync(0xffffffffu, x, 0) + lane);
     }
   }
   // The places behind the rounds go to the CTAs in order, each up to its share. After rounds

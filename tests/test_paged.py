@@ -640,3 +640,15 @@ def test_many_small_weights_beside_a_large_one(nq):
     ref = w / (1 + w)
     assert (o[..., 1:].double() - ref).abs().max().item() <= 1.05 * 2.0 ** -7 * ref + n * 2.0 ** -32
     assert (lse.double() - 18 - np.log1p(w)).abs().max().item() <= 2e-4
+
+
+@pytest.mark.parametrize("order", ["first", "last", "between", "two"])
+def test_chunks_among_many_single_tokens(order):
+    # units of more than 32 sequences lie between those of a chunk
+    g = np.random.RandomState(len(order))
+    one = [1] * 150
+    nq = {"first": [300] + one, "last": one + [300], "between": one[:70] + [150, 0, 0] + one[70:],
+          "two": [130] + one[:90] + [200] + one[:3]}[order]
+    kv = [int(n) + int(g.randint(1, 200)) for n in nq]
+    run(Batch(nq, kv, 16, 2, 64, G=4, seed=43, extra_rows=2))
+    run(Batch(nq, kv, 32, 1, 128, True, G=8, seed=44), True, 60)
