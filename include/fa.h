@@ -315,8 +315,9 @@ fa_status fa_paged_read(const void* k_pages, const void* v_pages, const uint8_t*
  * of it, off by at most 2^-25 of it otherwise; that largest scale counts as at least 2^-40 for
  * keys and 2^-60 for values.
  * Errors: FA_ERR_INVALID_ARG (as above, H not a multiple of H_kv, scale not positive and
- * finite, window_left < -1, max_q < 1, T * H >= 2^31), FA_ERR_UNSUPPORTED (H / H_kv >
- * 128, and as above), FA_ERR_WORKSPACE, FA_ERR_CUDA. */
+ * finite, window_left < -1, max_q < 1, T * H >= 2^31, max_pages * page_size + max_q >=
+ * 2^31 - 256), FA_ERR_UNSUPPORTED (H / H_kv > 128, and as above), FA_ERR_WORKSPACE,
+ * FA_ERR_CUDA. */
 size_t fa_paged_workspace_size(int H, int H_kv, int d, int max_q, int max_keys);
 fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
                         const uint8_t* k_scale, const uint8_t* v_scale, void* o, float* lse,

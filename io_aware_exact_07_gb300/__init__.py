@@ -604,6 +604,8 @@ def _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale):
     if page_table.dtype != torch.int32 or len(table) != 2 or page_table.get_device() != dev:
         raise ValueError("page_table must be int32 [B, max_pages], on the pages' device")
     B, width = table
+    if B < 1 or width < 1:
+        raise ValueError("page_table must have a row and a page")
     ts, tc = page_table.stride()
     if tc != 1 and width > 1:
         raise ValueError("the rows of page_table must be contiguous")
@@ -715,8 +717,8 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
                causal=False, window_left=-1, k_scale=None, v_scale=None, out=None, stream=None):
     """Attention of the new tokens q [T, H, d] over the cache (fa_paged_attn). The tokens of
     sequence b are rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] (T / B each without
-    cu_seqlens_q); max_q bounds their number (T where it is not given: pass it for single
-    tokens, whose kernel is another). Returns (o [T, H, d] bf16, lse [T, H] fp32); rows that
+    cu_seqlens_q); max_q bounds their number (T where it is not given: pass it, since up to 24
+    rows H / H_kv * max_q run on a kernel of their own). Returns (o [T, H, d] bf16, lse [T, H] fp32); rows that
     belong to no sequence are not written. out = (o, lse) gives the buffers."""
     head, batch, B, dev = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
     Hkv, d = batch[0], batch[1]
@@ -742,7 +744,7 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
     _call("fa_paged_attn", dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
           _data(k_scale), _data(v_scale), o.data_ptr(), lse.data_ptr(), *head, H, *batch, cu, B, T,
           n, qs, 1.0 / math.sqrt(d) if scale is None else float(scale), bool(causal),
-          window_left, _data(ws), ws_bytes)
+          min(window_left, 0x7FFFFFFF), _data(ws), ws_bytes)
     if stream is not None:
         _used_on(stream, *((o, lse, ws) if out is None else (ws,)))
     return o, lse

@@ -838,14 +838,17 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
   if (q_stride < static_cast<int64_t>(H) * d || q_stride % 8 != 0) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(T) * H >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+  // positions reach from -max_q (more new tokens than positions) to the tables' room
+  const long long max_keys = static_cast<long long>(max_pages) * page_size;
+  if (max_keys + max_q >= (1ll << 31) - 256) return FA_ERR_INVALID_ARG;
+  if (window_left >= max_keys) window_left = -1;  // hides nothing
   if (H / H_kv > 128) return FA_ERR_UNSUPPORTED;
   if (T == 0) return FA_OK;
   if (!q || !o || !lse || !aligned16(q) || !aligned16(o)) return FA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_INVALID_ARG;
   DeviceInfo* di = nullptr;
   if ((st = device_info(&di)) != FA_OK) return st;
-  const PagedWorkspace w = paged_workspace(
-      H / H_kv, d, max_q, static_cast<long long>(max_pages) * page_size, di->num_sms);
+  const PagedWorkspace w = paged_workspace(H / H_kv, d, max_q, max_keys, di->num_sms);
   if (w.bytes > 0 && (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace)))
     return FA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

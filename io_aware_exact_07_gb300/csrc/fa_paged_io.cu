@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kIoWarps * 32) fa_paged_write_kernel(const Pag
       if (real) {
         *reinterpret_cast<uint2*>(base + at) = w;
         if (u == 0)
-          (is_v ? a.c.v_scale : a.c.k_scale)[scale0 + h * a.c.page_size] =
+          (is_v ? a.c.v_scale : a.c.k_scale)[scale0 + static_cast<long long>(h) * a.c.page_size] =
               static_cast<uint8_t>(finite ? e + 127 : kScaleNaN);
       }
     }

@@ -652,3 +652,25 @@ def test_chunks_among_many_single_tokens(order):
     kv = [int(n) + int(g.randint(1, 200)) for n in nq]
     run(Batch(nq, kv, 16, 2, 64, G=4, seed=43, extra_rows=2))
     run(Batch(nq, kv, 32, 1, 128, True, G=8, seed=44), True, 60)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("nq", [[5, 2], [60, 40]])
+def test_windows_wider_than_any_sequence(nq, causal):
+    # more new tokens than positions too: some stand at negative ones
+    b = Batch(nq, [3, 40], 16, 2, 64, G=2, seed=45)
+    x = b.fill().on(DEV)
+    ref = b.oracle(causal)
+    for wl in (48, 2 ** 31 - 1, 2 ** 32):
+        o, lse = attn(b, x, causal=causal, window_left=wl, max_q=max(nq))
+        sync()
+        check_attn(o, lse, ref)
+
+
+def test_batches_without_sequences_or_pages_are_refused():
+    c = fa.paged_cache(2, 16, 1, 64, device=DEV)
+    for B, width in ((0, 3), (2, 0)):
+        with pytest.raises(ValueError):
+            fa.paged_attn(torch.zeros(B, 1, 64, dtype=torch.bfloat16, device=DEV),
+                          page_table=torch.zeros(B, width, dtype=torch.int32, device=DEV),
+                          kv_lens=torch.zeros(B, dtype=torch.int32, device=DEV), **c)

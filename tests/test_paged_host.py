@@ -138,3 +138,18 @@ def test_attention_check_sees_a_wrong_key():
     with pytest.raises(AssertionError):
         check_attn(torch.from_numpy(off[0]), torch.from_numpy(off[1]), ref)
     check_attn(torch.from_numpy(ref[0]).to(torch.bfloat16), torch.from_numpy(ref[1]).float(), ref)
+
+
+def test_positions_stay_within_32_bits(lib):
+    # tables with room for 2^31 - 272 positions, and new tokens that would reach back past -2^31
+    room = dict(max_pages=(1 << 27) - 17, ts=1 << 27)
+    assert attn(lib, **room, max_q=16) == 1
+    assert attn(lib, **room, max_q=15, wsb=0) != 1  # refused for its workspace, or no device
+
+
+@pytest.mark.parametrize("rows", [[], [[]]])
+def test_empty_batches_are_refused(rows):
+    kp = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        fa.paged_read(kp, kp, torch.zeros(len(rows), 0, dtype=torch.int32),
+                      torch.zeros(len(rows), dtype=torch.int32), 5)
