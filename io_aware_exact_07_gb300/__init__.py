@@ -737,6 +737,8 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
                 or lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()
                 or o.get_device() != dev or lse.get_device() != dev):
             raise ValueError(f"out must be contiguous: bf16 [{T}, {H}, {d}] and fp32 [{T}, {H}]")
+        if o.data_ptr() == q.data_ptr() and T > 0:
+            raise ValueError("out may not be q: rows of q are read after others of o are written")
     if T == 0:
         return o, lse
     ws_bytes = _paged_workspace_bytes(H, Hkv, d, n, head[2] * batch[7], dev)

@@ -674,3 +674,10 @@ def test_batches_without_sequences_or_pages_are_refused():
             fa.paged_attn(torch.zeros(B, 1, 64, dtype=torch.bfloat16, device=DEV),
                           page_table=torch.zeros(B, width, dtype=torch.int32, device=DEV),
                           kv_lens=torch.zeros(B, dtype=torch.int32, device=DEV), **c)
+
+
+def test_output_in_place_of_q_is_refused():
+    b = Batch([1, 2], [20, 5], 16, 2, 64, G=2, seed=46)
+    x = b.fill().on(DEV)
+    with pytest.raises(ValueError):
+        attn(b, x, causal=True, max_q=2, out=(x.q, torch.empty(x.q.shape[:2], device=DEV)))
