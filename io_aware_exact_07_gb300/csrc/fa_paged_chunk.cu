@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (threadIdx.x == 0) {
       record_error(args.sync.status, kStatusCuda);
-      headers[blockIdx.x] = PieceHeader{-1, 0, 1, 0};
+      headers[blockIdx.x] = PieceHeader{-1, 0, 0, 1};
     }
     return;
   }
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     hi = plan->hi;
   }
   if (lo >= hi && rounds == 0) {
-    if (tid == 0) headers[blockIdx.x] = PieceHeader{-1, 0, 1, 0};
+    if (tid == 0) headers[blockIdx.x] = PieceHeader{-1, 0, 0, 1};
     return;
   }
   if (lo < hi) {
@@ -1174,7 +1174,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     bool ok = true;
     int count = 0;
     PieceHeader* left = &headers[blockIdx.x];
-    if (tid == 0) *left = PieceHeader{-1, 0, 1, 0};
+    if (tid == 0) *left = PieceHeader{-1, 0, 0, 1};
     while (true) {
       if (!wait_piece(count)) {
         fail();
@@ -1519,9 +1519,9 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       if (tid == 0) {
         if (!pc.from_start) left->ended = pc.ends;
         if (pc.from_start && !pc.ends) {
-          left->b = pc.b;
+          left->row0 = pc.row0;
           left->h = pc.h;
-          left->qt = pc.qt;
+          left->rows = pc.rows;
         }
       }
       tc_fence_before();
@@ -1556,46 +1556,42 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   __shared__ int n_more;
   pdl_wait();
   const PieceHeader* headers = static_cast<const PieceHeader*>(a.headers);
-  const PieceHeader hd = headers[c];
-  if (hd.b < 0) return;
-  const PagedSeq s = paged_attn_seq(a.c, hd.b);
-  const int G = a.G, tt = a.tt;
-  const int tok0 = hd.qt * tt;
-  const int rows = min(s.nq - tok0, tt) * G;
+  PieceHeader hd;
+  const int n = 1 + pieces_after(headers, c, ctas, &n_more, &hd);  // slot 1 of c, slot 0 of the others
+  const int G = a.G;
   const int r = blockIdx.y * kMergeWarps + warp;
-  if (static_cast<int>(blockIdx.y) * kMergeWarps >= rows) return;
-  const int n = 1 + pieces_after(headers, c, ctas, &n_more);  // slot 1 of c, slot 0 of the others
-  if (r >= rows) return;
+  if (hd.row0 < 0 || r >= hd.rows) return;
   auto row_of = [&](int i) { return (2ll * (c + i) + (i == 0 ? 1 : 0)) * kTile + r; };
-  float m = -INFINITY;
+  // the first pieces are under way while the maximum is found
+  float m = -INFINITY, den = 0.f, acc[kPer] = {}, lse0[2] = {-INFINITY, -INFINITY}, part0[2][kPer] = {};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i < n) {
+      lse0[i] = a.lse_part[row_of(i)];
+      load_part<kPer>(a.o_part + row_of(i) * D + lane * kPer, part0[i]);
+    }
+  }
   for (int i = lane; i < n; i += 32) m = fmaxf(m, a.lse_part[row_of(i)]);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   const float mu = m == -INFINITY ? 0.f : m;
-  float den = 0.f, acc[kPer];
+  auto add = [&](float lse, const float* part) {
+    const float w = ex2_approx(lse - mu);
+    den += w;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+    for (int k = 0; k < kPer; ++k) acc[k] += w * part[k];
+  };
+  add(lse0[0], part0[0]);
+  add(lse0[1], part0[1]);
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const long long row = row_of(i);
-    const float x = ex2_approx(a.lse_part[row] - mu);
-    den += x;
-    const float* p = a.o_part + row * D + lane * kPer;
-    if constexpr (kPer == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p);
-      acc[0] += x * v.x;
-      acc[1] += x * v.y;
-      acc[2] += x * v.z;
-      acc[3] += x * v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(p);
-      acc[0] += x * v.x;
-      acc[1] += x * v.y;
-    }
+  for (int i = 2; i < n; ++i) {
+    float part[kPer];
+    load_part<kPer>(a.o_part + row_of(i) * D + lane * kPer, part);
+    add(a.lse_part[row_of(i)], part);
   }
   const float inv = den > 0.f ? 1.f / den : 0.f;
   const int t = r / G;
-  const long long row = static_cast<long long>(s.t0 + tok0 + t) * a.H + hd.h * G + (r - t * G);
+  const long long row = static_cast<long long>(hd.row0 + t) * a.H + hd.h * G + (r - t * G);
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + row * D + lane * kPer);
   dst[0] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
   if constexpr (kPer == 4) dst[1] = pack_bf16x2(acc[2] * inv, acc[3] * inv);

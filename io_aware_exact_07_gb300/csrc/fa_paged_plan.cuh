@@ -40,24 +40,43 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
   return before + inc - x;
 }
 
-// What a CTA leaves for the merge: the unit that its run began and did not end (b < 0:
-// none), and whether a unit that it did not begin ended in its run (or there was none).
-struct PieceHeader {
-  int b, h, ended, qt;
+// What a CTA leaves for the merge: the unit that its run began and did not end (row0 < 0:
+// none), its first token's row, K/V head and query rows; and whether a unit that it did not
+// begin ended in its run (or there was none).
+struct alignas(16) PieceHeader {
+  int row0, h, rows, ended;
 };
 
-// Number of CTAs after CTA c that hold further pieces of the unit begun there: up to the
-// first one in which it ended. Called by the whole block.
-__device__ __forceinline__ int pieces_after(const PieceHeader* headers, int c, int ctas, int* shared) {
+// The header of CTA c, and the number of CTAs after it that hold further pieces of the unit
+// begun there: up to the first one in which it ended (0 if it began none). Called by the whole
+// block, which has a thread for every CTA.
+__device__ __forceinline__ int pieces_after(const PieceHeader* headers, int c, int ctas, int* shared,
+                                            PieceHeader* of_c) {
+  const int i = c + 1 + static_cast<int>(threadIdx.x);
+  const int ended = i < ctas ? headers[i].ended : 0;
+  *of_c = headers[c];
+  if (of_c->row0 < 0) return 0;
   if (threadIdx.x == 0) *shared = ctas - 1 - c;
   __syncthreads();
-  for (int i = c + 1 + static_cast<int>(threadIdx.x); i < ctas; i += static_cast<int>(blockDim.x))
-    if (headers[i].ended != 0) {
-      atomicMin(shared, i - c);
-      break;
-    }
+  if (ended != 0) atomicMin(shared, i - c);
   __syncthreads();
   return *shared;
+}
+
+// N values of a piece's row, fp32, from p on.
+template <int N>
+__device__ __forceinline__ void load_part(const float* p, float* v) {
+  if constexpr (N == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = x.x;
+    v[1] = x.y;
+    v[2] = x.z;
+    v[3] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    v[0] = x.x;
+    v[1] = x.y;
+  }
 }
 
 __device__ __forceinline__ void pdl_launch_dependents() {

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   const long long hi = lo + per < total ? lo + per : total;
   PieceHeader* headers = static_cast<PieceHeader*>(a.headers);
   if (lo >= hi) {
-    if (tid == 0 && !a.whole) headers[blockIdx.x] = PieceHeader{-1, 0, 1, 0};
+    if (tid == 0 && !a.whole) headers[blockIdx.x] = PieceHeader{-1, 0, 0, 1};
     return;
   }
   {
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   };
   clear();
   bool first_piece = true, ended0 = false;
-  int slot1_b = -1, slot1_h = 0;
+  int slot1_row = -1, slot1_h = 0, slot1_rows = 0;
   float* merge = reinterpret_cast<float*>(smem + L::kMergeOff);
   float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
   int stage = 0;
@@ -763,8 +763,9 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
       }
       if (first_piece && starts_mid) ended0 = ends;
       if (!ends && from_start) {
-        slot1_b = cw.b;
+        slot1_row = cw.s.t0;
         slot1_h = cw.h;
+        slot1_rows = M;
       }
       first_piece = false;
       clear();
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   }
   cp_async_wait<0>();
   if (tid == 0 && !a.whole)
-    headers[blockIdx.x] = PieceHeader{slot1_b, slot1_h, !starts_mid || ended0, 0};
+    headers[blockIdx.x] = PieceHeader{slot1_row, slot1_h, slot1_rows, !starts_mid || ended0};
 }
 
 // Merge of the pieces of a head that runs' ends have cut: with lse_s and the normalised O_s
@@ -803,14 +804,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_step_merge_kernel(c
   __shared__ float acc_s[kMergeWarps][D];
   pdl_wait();
   const PieceHeader* headers = static_cast<const PieceHeader*>(a.headers);
-  const PieceHeader hd = headers[c];
-  if (hd.b < 0) return;
-  const PagedSeq s = paged_attn_seq(a.c, hd.b);
+  PieceHeader hd;
+  // pieces: slot 1 of CTA c, slot 0 of the n - 1 after it
+  const int n = 1 + pieces_after(headers, c, ctas, &n_more, &hd);
+  if (hd.row0 < 0 || r >= hd.rows) return;
   const int G = a.G;
-  if (r >= s.nq * G) return;
-  const int n = 1 + pieces_after(headers, c, ctas, &n_more);  // pieces: slot 1 of CTA c, slot 0 of the n - 1 after it
   auto row_of = [&](int i) { return (2ll * (c + i) + (i == 0 ? 1 : 0)) * rows + r; };
-  float m = -INFINITY;
+  // the warp's first piece is under way while the maximum is found
+  float m = -INFINITY, den = 0.f, acc[kPer] = {}, lse0 = -INFINITY, part0[kPer] = {};
+  if (warp < n) {
+    lse0 = a.lse_part[row_of(warp)];
+    load_part<kPer>(a.o_part + row_of(warp) * D + lane * kPer, part0);
+  }
   for (int i = tid; i < n; i += kMergeWarps * 32) m = fmaxf(m, a.lse_part[row_of(i)]);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
@@ -819,26 +824,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_step_merge_kernel(c
 #pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, mx[w]);
   const float mu = m == -INFINITY ? 0.f : m;
-  float den = 0.f, acc[kPer];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += kMergeWarps) {
-    const long long row = row_of(i);
-    const float w = ex2_approx(a.lse_part[row] - mu);
+  auto add = [&](float lse, const float* part) {
+    const float w = ex2_approx(lse - mu);
     den += w;
-    const float* p = a.o_part + row * D + lane * kPer;
-    if constexpr (kPer == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p);
-      acc[0] += w * v.x;
-      acc[1] += w * v.y;
-      acc[2] += w * v.z;
-      acc[3] += w * v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(p);
-      acc[0] += w * v.x;
-      acc[1] += w * v.y;
-    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] += w * part[k];
+  };
+  add(lse0, part0);
+#pragma unroll 4
+  for (int i = warp + kMergeWarps; i < n; i += kMergeWarps) {
+    float part[kPer];
+    load_part<kPer>(a.o_part + row_of(i) * D + lane * kPer, part);
+    add(a.lse_part[row_of(i)], part);
   }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc_s[warp][lane * kPer + k] = acc[k];
@@ -852,7 +849,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_step_merge_kernel(c
       l += dens[w];
     }
     const int t = r / G;
-    const long long row = static_cast<long long>(s.t0 + t) * a.H + hd.h * G + (r - t * G);
+    const long long row = static_cast<long long>(hd.row0 + t) * a.H + hd.h * G + (r - t * G);
     a.o[row * D + tid] = __float2bfloat16(l > 0.f ? y / l : 0.f);
     if (tid == 0) a.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
   }
