@@ -155,23 +155,93 @@ struct Unit {
     h = static_cast<int>(x / static_cast<unsigned>(n_qt));
     qt = static_cast<int>(x) - h * n_qt;
   }
-  // Unit x of those from sequence b0 on, by the whole warp (b0 is the same for all lanes, x need
-  // not be); b = B past the end. 32 sequences at a time: one by one, each a load from L2, 1023
-  // sequences of one token beside a chunk took 400 us of planning.
-  __device__ __forceinline__ void find(const PagedAttnArgs& a, int b0, unsigned x) {
+  // k units further on, by a warp whose lanes all hold the same unit.
+  template <bool E4M3>
+  __device__ __forceinline__ void advance(const PagedAttnArgs& a, int k);
+};
+
+// The units of 32 sequences, one a lane, and which they are in the list of all. Of use to a
+// whole warp that looks for units further and further on: taking sequences one by one, each a
+// load from L2, 1023 single tokens beside a chunk took 400 us of planning.
+struct Window {
+  int b0;
+  unsigned from, all, inc;  // units before the window; in it; up to the lane's sequence
+  PagedSeq s;
+  int n_qt;
+  // The window at sequence x, with `before` units in front of it.
+  __device__ __forceinline__ void load(const PagedAttnArgs& a, int x, unsigned before) {
     const int lane = threadIdx.x & 31;
+    b0 = x;
+    from = before;
+    s = PagedSeq{0, 0, 0};
+    if (b0 + lane < a.c.B) s = paged_attn_seq(a.c, b0 + lane);
+    n_qt = (s.nq + a.tt - 1) / a.tt;
+    inc = static_cast<unsigned>(n_qt * a.c.Hkv);  // (the units of a batch fit an int)
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, inc, k);
+      if (lane >= k) inc += y;
+    }
+    all = __shfl_sync(0xffffffffu, inc, 31);
+  }
+  // Unit x, which may differ from lane to lane, but for every lane lies behind the window's
+  // first sequence; b = B past the end. Moves the window on as far as that takes.
+  __device__ __forceinline__ Unit find(const PagedAttnArgs& a, unsigned x) {
+    Unit u;
+    u.b = a.c.B;
+    u.h = u.qt = u.n_qt = 0;
+    u.s = PagedSeq{0, 0, 0};
+    while (true) {
+      const bool here = x >= from && x - from < all;
+      const unsigned y = x - from;
+      int i = 0;  // sequences that end at or before it
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1)
+        if (__shfl_sync(0xffffffffu, inc, i + k - 1) <= y) i += k;
+      const int n = __shfl_sync(0xffffffffu, n_qt, i);
+      const unsigned before = __shfl_sync(0xffffffffu, inc - static_cast<unsigned>(n_qt * a.c.Hkv), i);
+      const PagedSeq z = {__shfl_sync(0xffffffffu, s.t0, i), __shfl_sync(0xffffffffu, s.nq, i),
+                          __shfl_sync(0xffffffffu, s.len, i)};
+      if (here) {
+        u.b = b0 + i;
+        u.n_qt = n;
+        u.s = z;
+        u.at(y - before);
+      }
+      if (__all_sync(0xffffffffu, here || x < from) || b0 + 32 >= a.c.B) return u;
+      load(a, b0 + 32, from + all);
+    }
+  }
+};
+
+// (Two forms of one search, chosen by what the compiler makes of the whole kernel, whose softmax
+// this warp shares registers and instruction cache with: chunks of 512 tokens over 5000 keys on
+// average, with the window and with loads of its own: bf16 148 and 142 us, e4m3 232 and 249.)
+template <bool E4M3>
+__device__ __forceinline__ void Unit::advance(const PagedAttnArgs& a, int k) {
+  if (b >= a.c.B) return;
+  unsigned x = static_cast<unsigned>(h * n_qt + qt + k);
+  if (x < static_cast<unsigned>(n_qt * a.c.Hkv)) {
+    at(x);
+  } else if constexpr (E4M3) {
+    Window w;
+    w.load(a, b, 0u);
+    *this = w.find(a, x);
+  } else {
+    const int lane = threadIdx.x & 31;
+    int b0 = b;
     bool found = false;
     b = a.c.B;
     h = qt = n_qt = 0;
     for (; b0 < a.c.B; b0 += 32) {
-      unsigned n = 0;  // units of sequence b0 + lane (those of the batch fit an int)
+      unsigned n = 0;
       if (b0 + lane < a.c.B)
         n = static_cast<unsigned>((paged_attn_seq(a.c, b0 + lane).nq + a.tt - 1) / a.tt * a.c.Hkv);
       unsigned inc = n;
 #pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const unsigned y = __shfl_up_sync(0xffffffffu, inc, k);
-        if (lane >= k) inc += y;
+      for (int j = 1; j < 32; j <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, inc, j);
+        if (lane >= j) inc += y;
       }
       const unsigned all = __shfl_sync(0xffffffffu, inc, 31);
       int i = 0;  // sequences that end at or before x
@@ -179,28 +249,19 @@ struct Unit {
       for (int k = 16; k > 0; k >>= 1)
         if (__shfl_sync(0xffffffffu, inc, i + k - 1) <= x) i += k;
       const unsigned before = __shfl_sync(0xffffffffu, inc - n, i);
-      if (!found) {
-        found = x < all;
-        x -= found ? before : all;
-        if (found) b = b0 + i;
+      found = x < all;
+      x -= found ? before : all;
+      if (found) {
+        b = b0 + i;
+        break;
       }
-      if (__all_sync(0xffffffffu, found)) break;
     }
     if (found) {
       seq(a);
       at(x);
     }
   }
-  // k units further on, by a warp whose lanes all hold the same unit.
-  __device__ __forceinline__ void advance(const PagedAttnArgs& a, int k) {
-    if (b >= a.c.B) return;
-    const unsigned x = static_cast<unsigned>(h * n_qt + qt + k);
-    if (x < static_cast<unsigned>(n_qt * a.c.Hkv))
-      at(x);
-    else
-      find(a, b, x);
-  }
-};
+}
 
 // A piece as the roles need it: key tiles [j0, j0 + nt) (nt < 0: no piece is left) of the query
 // tile whose first token is tok0 of its sequence, token row row0 of q and o, position pos0.
@@ -218,6 +279,7 @@ struct Piece {
 // differ by one jump only, so that at any time they read a head at two places, not at as
 // many as there are CTAs. (16 query tiles of 512 key tiles each over 8 heads: with runs in
 // the list's order alone K and V, 268 MB, came from HBM once per query tile, at 7 TB/s.)
+template <bool E4M3>
 struct Walk {
   Unit u;
   int rounds;                        // whole units left
@@ -247,7 +309,7 @@ struct Walk {
   // Next piece; false when there is none.
   __device__ __forceinline__ bool next(const PagedAttnArgs& a) {
     if (rounds > 0) {
-      if (in_round) u.advance(a, static_cast<int>(gridDim.x));
+      if (in_round) u.template advance<E4M3>(a, static_cast<int>(gridDim.x));
       in_round = true;
       --rounds;
       piece(a, 0, 0x7FFFFFFF);
@@ -255,14 +317,14 @@ struct Walk {
     }
     if (left > 0) {
       if (in_run) {
-        u.advance(a, 1);
+        u.template advance<E4M3>(a, 1);
       } else {
         in_run = true;
         to_run(a);
         if (run_at > 0) {
           tail = piece(a, run_at, left);
           left -= tail;
-          if (left > 0) u.advance(a, 1);
+          if (left > 0) u.template advance<E4M3>(a, 1);
         }
       }
       if (left > 0) {
@@ -338,143 +400,6 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   const int warp = tid >> 5;
   const int lane = tid & 31;
 
-  // ---- this CTA's run of the list
-  struct Plan {
-    long long warp_sums[L::kWarps];
-    long long rem, lo, hi;
-    int b, h, qt, at;    // where the run begins
-    int b0, h0, qt0;     // the first whole unit
-    int last;
-  };
-  static_assert(sizeof(Plan) <= 2 * kTile * 8, "plan scratch");
-  Plan* plan = reinterpret_cast<Plan*>(smem + L::kPlanOff);
-  // Places of one K/V head of sequence b; long chunks are summed by the whole warp.
-  int last = -1;  // the last sequence seen by this thread with several query tiles per head
-  auto head_places = [&](int b) -> long long {
-    PagedSeq s = {0, 0, 0};
-    if (b < args.c.B) s = paged_attn_seq(args.c, b);
-    const int n_qt = (s.nq + args.tt - 1) / args.tt;
-    if (n_qt > 1) last = b;
-    long long sum = 0;
-    if (n_qt <= 2)
-      for (int i = 0; i < n_qt; ++i) sum += tiles_of(args, s, args.tt, i).n;
-    unsigned todo = __ballot_sync(0xffffffffu, n_qt > 2);
-    while (todo != 0u) {
-      const int src = __ffs(todo) - 1;
-      todo &= todo - 1;
-      PagedSeq z;
-      z.t0 = 0;
-      z.nq = __shfl_sync(0xffffffffu, s.nq, src);
-      z.len = __shfl_sync(0xffffffffu, s.len, src);
-      const int n = (z.nq + args.tt - 1) / args.tt;
-      long long part = 0;
-      for (int i = lane; i < n; i += 32) part += tiles_of(args, z, args.tt, i).n;
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) part += __shfl_xor_sync(0xffffffffu, part, k);
-      if (lane == src) sum = part;
-    }
-    return sum;
-  };
-  long long total = 0, x0 = 0;
-  for (int b0 = 0; b0 < args.c.B; b0 += L::kThreads) {
-    const long long x = head_places(b0 + tid) * args.c.Hkv;
-    if (b0 == 0) x0 = x;
-    long long sum;
-    block_scan<L::kWarps>(x, plan->warp_sums, &sum);
-    total += sum;
-  }
-  if (tid == 0) plan->last = -1;
-  __syncthreads();
-  if (last >= 0) atomicMax(&plan->last, last);
-  __syncthreads();
-  last = plan->last;
-  const int ctas = static_cast<int>(gridDim.x);
-  const long long per = (total + ctas - 1) / ctas;
-  // Whole units in rounds, as long as no CTA gets more than its share; thread c follows CTA
-  // c. Behind the last sequence with several query tiles per head there is nothing to share,
-  // and no round.
-  long long load = 0;
-  int rounds = 0;
-  if (last >= 0) {
-    Unit v;
-    v.find(args, 0, static_cast<unsigned>(tid));
-    if (tid == static_cast<int>(blockIdx.x) && v.b < args.c.B) {
-      plan->b0 = v.b;
-      plan->h0 = v.h;
-      plan->qt0 = v.qt;
-    }
-    while (true) {
-      const bool none = v.b >= args.c.B;
-      const int n = none ? 0 : tiles_of(args, v.s, args.tt, v.qt).n;
-      if (__syncthreads_or((tid < ctas && (none || load + n > per)) || (tid == 0 && v.b > last))) break;
-      load += n;
-      ++rounds;
-      // lane l is l units behind lane 0 (which is not past the end while a round begins)
-      const unsigned x = static_cast<unsigned>(v.h * v.n_qt + v.qt + ctas);
-      v.find(args, __shfl_sync(0xffffffffu, v.b, 0), __shfl_sync(0xffffffffu, x, 0) + lane);
-    }
-  }
-  // The places behind the rounds go to the CTAs in order, each up to its share. After rounds
-  // that is one place more, so that no run is empty before the last: the pieces of a unit
-  // then lie in consecutive CTAs.
-  long long lo, hi;
-  {
-    const bool mine = tid < ctas;
-    long long loads, room;
-    block_scan<L::kWarps>(mine ? load : 0, plan->warp_sums, &loads);
-    const long long share = per - load + (rounds > 0 ? 1 : 0);
-    const long long before = block_scan<L::kWarps>(mine ? share : 0, plan->warp_sums, &room);
-    if (tid == static_cast<int>(blockIdx.x)) {
-      plan->lo = min(total, loads + before);
-      plan->hi = min(total, loads + before + share);
-    }
-    __syncthreads();
-    lo = plan->lo;
-    hi = plan->hi;
-  }
-  if (lo >= hi && rounds == 0) {
-    if (tid == 0) headers[blockIdx.x] = PieceHeader{-1, 0, 0, 1};
-    return;
-  }
-  if (lo < hi) {
-    long long base = 0;
-    for (int b0 = 0; b0 < args.c.B && base <= lo; b0 += L::kThreads) {
-      const long long x = b0 == 0 ? x0 : head_places(b0 + tid) * args.c.Hkv;
-      long long sum;
-      const long long at = base + block_scan<L::kWarps>(x, plan->warp_sums, &sum);
-      if (at <= lo && lo < at + x) {
-        const long long one = x / args.c.Hkv;  // places of one head
-        plan->b = b0 + tid;
-        plan->h = static_cast<int>((lo - at) / one);
-        plan->rem = (lo - at) % one;
-      }
-      base += sum;
-    }
-  }
-  __syncthreads();
-  if (warp == 0 && lo < hi) {
-    // the query tile within the head: 32 at a time
-    const PagedSeq s = paged_attn_seq(args.c, plan->b);
-    const int n_qt = (s.nq + args.tt - 1) / args.tt;
-    long long rem = plan->rem;
-    for (int i0 = 0; i0 < n_qt; i0 += 32) {
-      const int n = i0 + lane < n_qt ? tiles_of(args, s, args.tt, i0 + lane).n : 0;
-      long long inc = n;
-#pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, k);
-        if (lane >= k) inc += y;
-      }
-      if (inc - n <= rem && rem < inc) {
-        plan->qt = i0 + lane;
-        plan->at = static_cast<int>(rem - (inc - n));
-      }
-      const long long all = __shfl_sync(0xffffffffu, inc, 31);
-      if (rem < all) break;
-      rem -= all;
-    }
-  }
-
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff + 8);
@@ -511,7 +436,11 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     bars.drain2 = nb();
     bars.stall = nb();
   }
-  if (tid == 0) {
+  // (by a thread that has little to do for the plan, while the plan waits for its first loads)
+  if (tid == kSIssuer * 32) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
     *abort_flag = 0;
     mbar_init(bars.q_full, 1);
     mbar_init(bars.q_empty, 1);
@@ -556,6 +485,151 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     mbar_init(bars.stall, 1);
     fence_mbar_init();
   }
+  // ---- this CTA's run of the list
+  struct Plan {
+    long long warp_sums[L::kWarps];
+    long long rem, lo, hi;
+    int b, h, qt, at;    // where the run begins
+    int b0, h0, qt0;     // the first whole unit
+    int last;
+  };
+  static_assert(sizeof(Plan) <= 2 * kTile * 8, "plan scratch");
+  Plan* plan = reinterpret_cast<Plan*>(smem + L::kPlanOff);
+  // Places of one K/V head of sequence b; long chunks are summed by the whole warp.
+  int last = -1;  // the last sequence seen by this thread with several query tiles per head
+  auto head_places = [&](int b) -> long long {
+    PagedSeq s = {0, 0, 0};
+    if (b < args.c.B) s = paged_attn_seq(args.c, b);
+    const int n_qt = (s.nq + args.tt - 1) / args.tt;
+    if (n_qt > 1) last = b;
+    long long sum = 0;
+    if (n_qt <= 2)
+      for (int i = 0; i < n_qt; ++i) sum += tiles_of(args, s, args.tt, i).n;
+    unsigned todo = __ballot_sync(0xffffffffu, n_qt > 2);
+    while (todo != 0u) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      PagedSeq z;
+      z.t0 = 0;
+      z.nq = __shfl_sync(0xffffffffu, s.nq, src);
+      z.len = __shfl_sync(0xffffffffu, s.len, src);
+      const int n = (z.nq + args.tt - 1) / args.tt;
+      long long part = 0;
+      for (int i = lane; i < n; i += 32) part += tiles_of(args, z, args.tt, i).n;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) part += __shfl_xor_sync(0xffffffffu, part, k);
+      if (lane == src) sum = part;
+    }
+    return sum;
+  };
+  long long total = 0, x0 = 0, at0 = 0, sum0 = 0;
+  for (int b0 = 0; b0 < args.c.B; b0 += L::kThreads) {
+    const long long x = head_places(b0 + tid) * args.c.Hkv;
+    long long sum;
+    const long long at = block_scan<L::kWarps>(x, plan->warp_sums, &sum);
+    if (b0 == 0) {
+      x0 = x;
+      at0 = at;
+      sum0 = sum;
+    }
+    total += sum;
+  }
+  if (tid == 0) plan->last = -1;
+  __syncthreads();
+  if (last >= 0) atomicMax(&plan->last, last);
+  __syncthreads();
+  last = plan->last;
+  const int ctas = static_cast<int>(gridDim.x);
+  const long long per = (total + ctas - 1) / ctas;
+  // Whole units in rounds, as long as no CTA gets more than its share; thread c follows CTA
+  // c. Behind the last sequence with several query tiles per head there is nothing to share,
+  // and no round.
+  long long load = 0;
+  int rounds = 0;
+  if (last >= 0) {
+    Window w;
+    Unit v;
+    // (threads behind the last CTA's look up that one's units)
+    unsigned x = static_cast<unsigned>(min(tid, ctas - 1));
+    w.load(args, 0, 0u);
+    v = w.find(args, x);
+    if (tid == static_cast<int>(blockIdx.x) && v.b < args.c.B) {
+      plan->b0 = v.b;
+      plan->h0 = v.h;
+      plan->qt0 = v.qt;
+    }
+    while (true) {
+      const bool none = v.b >= args.c.B;
+      const int n = none ? 0 : tiles_of(args, v.s, args.tt, v.qt).n;
+      if (__syncthreads_or(none || load + n > per || (tid == 0 && v.b > last))) break;
+      load += n;
+      ++rounds;
+      x += static_cast<unsigned>(ctas);
+      v = w.find(args, x);
+    }
+  }
+  // The places behind the rounds go to the CTAs in order, each up to its share. After rounds
+  // that is one place more, so that no run is empty before the last: the pieces of a unit
+  // then lie in consecutive CTAs.
+  long long lo, hi;
+  {
+    const long long each = per + (rounds > 0 ? 1 : 0);
+    long long loads;
+    const long long before = block_scan<L::kWarps>(tid < ctas ? load : 0, plan->warp_sums, &loads);
+    if (tid == static_cast<int>(blockIdx.x)) {
+      const long long from = loads + tid * each - before;
+      plan->lo = min(total, from);
+      plan->hi = min(total, from + each - load);
+    }
+    __syncthreads();
+    lo = plan->lo;
+    hi = plan->hi;
+  }
+  if (lo >= hi && rounds == 0) {
+    if (tid == 0) headers[blockIdx.x] = PieceHeader{-1, 0, 0, 1};
+    return;
+  }
+  if (lo < hi) {
+    long long base = 0;
+    for (int b0 = 0; b0 < args.c.B && base <= lo; b0 += L::kThreads) {
+      long long x = x0, sum = sum0, at = at0;
+      if (b0 > 0) {
+        x = head_places(b0 + tid) * args.c.Hkv;
+        at = base + block_scan<L::kWarps>(x, plan->warp_sums, &sum);
+      }
+      if (at <= lo && lo < at + x) {
+        const long long one = x / args.c.Hkv;  // places of one head
+        plan->b = b0 + tid;
+        plan->h = static_cast<int>((lo - at) / one);
+        plan->rem = (lo - at) % one;
+      }
+      base += sum;
+    }
+  }
+  __syncthreads();
+  if (warp == 0 && lo < hi) {
+    // the query tile within the head: 32 at a time
+    const PagedSeq s = paged_attn_seq(args.c, plan->b);
+    const int n_qt = (s.nq + args.tt - 1) / args.tt;
+    long long rem = plan->rem;
+    for (int i0 = 0; i0 < n_qt; i0 += 32) {
+      const int n = i0 + lane < n_qt ? tiles_of(args, s, args.tt, i0 + lane).n : 0;
+      long long inc = n;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, k);
+        if (lane >= k) inc += y;
+      }
+      if (inc - n <= rem && rem < inc) {
+        plan->qt = i0 + lane;
+        plan->at = static_cast<int>(rem - (inc - n));
+      }
+      const long long all = __shfl_sync(0xffffffffu, inc, 31);
+      if (rem < all) break;
+      rem -= all;
+    }
+  }
+
   if (warp == kSIssuer) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -565,7 +639,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint64_t tmo = args.sync.timeout_ns;
-  Walk w;
+  Walk<E4M3> w;
   if (warp == kVWarp) {
     w.rounds = rounds;
     w.in_round = w.in_run = false;
@@ -846,7 +920,6 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       // tile's scales come to before V is converted), V's again with V's.
       const bool is_k = warp == kKWarp;
       const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-      if (lane == 0) tma_prefetch_desc(tm);
       const BarRun full = E4M3 ? (is_k ? bars.ck_full : bars.cv_full) : (is_k ? bars.k_full : bars.v_full);
       const BarRun empty =
           E4M3 ? (is_k ? bars.ck_empty : bars.cv_empty) : (is_k ? bars.k_empty : bars.v_empty);
@@ -989,7 +1062,6 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         uint32_t q_cnt = 0;  // pieces with key tiles so far: those that have loaded Q
         bool seen0 = false, seen1 = false;
         bool ok = true;
-        tma_prefetch_desc(&tm_q);
         // Test hook: this barrier is never completed, so the bounded wait runs out.
         if (args.sync.inject_stall && !mbar_wait(bars.stall, 0, tmo, abort_flag)) {
           fail();
