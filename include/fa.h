@@ -328,6 +328,14 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
                         int max_q, int64_t q_stride, float scale, int causal, int window_left,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* The three calls with their arguments in a block, 8 bytes each in the order above but for the
+ * stream: pointers and integers as int64_t, scale as a double. For bindings that spend time on
+ * every argument of a call (through Python's ctypes the 30 of fa_paged_attn cost as much as its
+ * launch). An integer outside its parameter's range is refused with FA_ERR_INVALID_ARG. */
+fa_status fa_paged_write_block(const int64_t* args, void* stream);
+fa_status fa_paged_read_block(const int64_t* args, void* stream);
+fa_status fa_paged_attn_block(const int64_t* args, void* stream);
+
 /* FP8 forward with incoherent processing (FA-3's FP8 path, which the
  * cross-paper synthesis page on FlashAttention names in its section 2), head
  * dimension 128, forward only.

@@ -19,6 +19,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -42,6 +43,7 @@ EXPORTS = (
     "fa_bwd_workspace_size", "fa_bwd_preprocess",
     "fa_bwd_dkdv", "fa_bwd_dq", "fa_decode", "fa_decode_workspace_size",
     "fa_paged_write", "fa_paged_read", "fa_paged_attn", "fa_paged_workspace_size",
+    "fa_paged_write_block", "fa_paged_read_block", "fa_paged_attn_block",
     "fa_fp8_workspace_size", "fa_fp8_vt_stride", "fa_fp8_quantize", "fa_fwd_fp8",
     "fa_fp8_quantize_gqa", "fa_fwd_fp8_gqa",
     "fa_bwd_noalloc", "fa_dropout_p8", "fa_debug_dropout_keep",
@@ -115,6 +117,9 @@ def load(build_if_missing: bool = False):
         lib.fa_paged_write.restype = i
         lib.fa_paged_read.argtypes = [vp] * 4 + cache + [i, i, vp, vp, vp]
         lib.fa_paged_read.restype = i
+        for f_block in (lib.fa_paged_write_block, lib.fa_paged_read_block, lib.fa_paged_attn_block):
+            f_block.argtypes = [ctypes.c_char_p, vp]
+            f_block.restype = i
         lib.fa_paged_workspace_size.argtypes = [i, i, i, i, i]
         lib.fa_paged_workspace_size.restype = sz
         lib.fa_paged_attn.argtypes = ([vp] * 7 + [i, i, i, i, i, i, i64, i64, i64, vp, i64, i, vp]
@@ -637,7 +642,7 @@ def _offsets(cu, B, T, max_q, dev):
     if cu is None:
         if T % B != 0 or (max_q is not None and max_q * B != T):
             raise ValueError("without cu_seqlens_q the rows must be B times max_q")
-        return None, T // B
+        return 0, T // B
     if (cu.dtype != torch.int32 or cu.shape != (B + 1,) or cu.get_device() != dev
             or not cu.is_contiguous()):
         raise ValueError(f"cu_seqlens_q must be contiguous int32 [{B + 1}], on the pages' device")
@@ -645,11 +650,18 @@ def _offsets(cu, B, T, max_q, dev):
 
 
 def _data(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-def _call(name, dev, stream, *args):
-    """Call a C entry point on device `dev` and a stream of it (the current one if None)."""
+# The arguments of the paged entry points as their _block forms take them.
+_WRITE_BLOCK = struct.Struct("=24q").pack
+_READ_BLOCK = struct.Struct("=20q").pack
+_ATTN_BLOCK = struct.Struct("=25qd4q").pack
+
+
+def _call(name, dev, stream, block):
+    """Call a C entry point, its arguments packed into `block`, on device `dev` and a stream of
+    it (the current one if None)."""
     if stream is None:
         # the raw handle of the current stream, without a Stream object around it: a
         # decode step makes this call in microseconds
@@ -657,11 +669,11 @@ def _call(name, dev, stream, *args):
     else:
         handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
     f = getattr(load() if _lib is None else _lib, name)
-    if torch.cuda.current_device() == dev:
-        status = f(*args, handle)
+    if torch._C._cuda_getDevice() == dev:
+        status = f(block, handle)
     else:
         with torch.cuda.device(dev):
-            status = f(*args, handle)
+            status = f(block, handle)
     if status != FA_OK:
         raise FAError(status, name)
 
@@ -694,8 +706,9 @@ def paged_write(k_new, v_new, k_pages, v_pages, page_table, kv_lens, cu_seqlens_
     if v_new.shape[0] != T:
         raise ValueError("k_new and v_new must have the same number of rows")
     cu, n = _offsets(cu_seqlens_q, B, T, None, dev)
-    _call("fa_paged_write", dev, stream, k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
-          v_pages.data_ptr(), _data(k_scale), _data(v_scale), *head, *batch, cu, B, T, n, ks, vs)
+    _call("fa_paged_write_block", dev, stream,
+          _WRITE_BLOCK(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                       _data(k_scale), _data(v_scale), *head, *batch, cu, B, T, n, ks, vs))
 
 
 def paged_read(k_pages, v_pages, page_table, kv_lens, N, k_scale=None, v_scale=None, stream=None):
@@ -703,11 +716,12 @@ def paged_read(k_pages, v_pages, page_table, kv_lens, N, k_scale=None, v_scale=N
     bf16 [B, H_kv, N, d], zeros behind each sequence. fwd and decode take them with
     seqlens_k=kv_lens."""
     head, batch, B, dev = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
-    shape, device = (B, batch[0], N, batch[1]), k_pages.device
-    k = torch.empty(shape, dtype=torch.bfloat16, device=device)
-    v = torch.empty(shape, dtype=torch.bfloat16, device=device)
-    _call("fa_paged_read", dev, stream, k_pages.data_ptr(), v_pages.data_ptr(), _data(k_scale),
-          _data(v_scale), *head, *batch, B, N, k.data_ptr(), v.data_ptr())
+    shape = (B, batch[0], N, batch[1])
+    k = k_pages.new_empty(shape, dtype=torch.bfloat16)
+    v = k_pages.new_empty(shape, dtype=torch.bfloat16)
+    _call("fa_paged_read_block", dev, stream,
+          _READ_BLOCK(k_pages.data_ptr(), v_pages.data_ptr(), _data(k_scale), _data(v_scale),
+                      *head, *batch, B, N, k.data_ptr(), v.data_ptr()))
     if stream is not None:
         _used_on(stream, k, v)
     return k, v
@@ -727,10 +741,9 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
     T, H = q.shape[0], q.shape[1]
     qs = _new_rows("q", q, H, d, dev)
     cu, n = _offsets(cu_seqlens_q, B, T, max_q, dev)
-    device = k_pages.device
     if out is None:
-        o = torch.empty((T, H, d), dtype=torch.bfloat16, device=device)
-        lse = torch.empty((T, H), dtype=torch.float32, device=device)
+        o = q.new_empty((T, H, d))
+        lse = q.new_empty((T, H), dtype=torch.float32)
     else:
         o, lse = out
         if (o.dtype != torch.bfloat16 or o.shape != (T, H, d) or not o.is_contiguous()
@@ -742,11 +755,12 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
     if T == 0:
         return o, lse
     ws_bytes = _paged_workspace_bytes(H, Hkv, d, n, head[2] * batch[7], dev)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
-    _call("fa_paged_attn", dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-          _data(k_scale), _data(v_scale), o.data_ptr(), lse.data_ptr(), *head, H, *batch, cu, B, T,
-          n, qs, 1.0 / math.sqrt(d) if scale is None else float(scale), bool(causal),
-          min(window_left, 0x7FFFFFFF), _data(ws), ws_bytes)
+    ws = q.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
+    _call("fa_paged_attn_block", dev, stream,
+          _ATTN_BLOCK(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _data(k_scale),
+                      _data(v_scale), o.data_ptr(), lse.data_ptr(), *head, H, *batch, cu, B, T, n,
+                      qs, 1.0 / math.sqrt(d) if scale is None else scale, bool(causal),
+                      min(window_left, 0x7FFFFFFF), _data(ws), ws_bytes))
     if stream is not None:
         _used_on(stream, *((o, lse, ws) if out is None else (ws,)))
     return o, lse

@@ -888,6 +888,41 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// The calls above from blocks of arguments; x[i] for i in `ints` are ints.
+#define FA_BLOCK_INTS(...)                                                    \
+  if (x == nullptr) return FA_ERR_INVALID_ARG;                                \
+  for (const int i : {__VA_ARGS__})                                           \
+    if (x[i] != static_cast<int32_t>(x[i])) return FA_ERR_INVALID_ARG;        \
+  auto p = [&](int i) { return reinterpret_cast<void*>(x[i]); };              \
+  auto u8 = [&](int i) { return reinterpret_cast<uint8_t*>(x[i]); };          \
+  auto i32 = [&](int i) { return reinterpret_cast<const int32_t*>(x[i]); };   \
+  auto n = [&](int i) { return static_cast<int>(x[i]); };
+
+fa_status fa_paged_write_block(const int64_t* x, void* stream) {
+  FA_BLOCK_INTS(6, 7, 8, 9, 10, 16, 19, 20, 21)
+  return fa_paged_write(p(0), p(1), p(2), p(3), u8(4), u8(5), n(6), n(7), n(8), n(9), n(10), x[11],
+                        x[12], x[13], i32(14), x[15], n(16), i32(17), i32(18), n(19), n(20), n(21),
+                        x[22], x[23], stream);
+}
+
+fa_status fa_paged_read_block(const int64_t* x, void* stream) {
+  FA_BLOCK_INTS(4, 5, 6, 7, 8, 14, 16, 17)
+  return fa_paged_read(p(0), p(1), u8(2), u8(3), n(4), n(5), n(6), n(7), n(8), x[9], x[10], x[11],
+                       i32(12), x[13], n(14), i32(15), n(16), n(17), p(18), p(19), stream);
+}
+
+fa_status fa_paged_attn_block(const int64_t* x, void* stream) {
+  FA_BLOCK_INTS(7, 8, 9, 10, 11, 12, 18, 21, 22, 23, 26, 27)
+  double scale;
+  memcpy(&scale, x + 25, sizeof(scale));
+  if (x[29] < 0) return FA_ERR_INVALID_ARG;
+  return fa_paged_attn(p(0), p(1), p(2), u8(3), u8(4), p(5), static_cast<float*>(p(6)), n(7), n(8),
+                       n(9), n(10), n(11), n(12), x[13], x[14], x[15], i32(16), x[17], n(18),
+                       i32(19), i32(20), n(21), n(22), n(23), x[24], static_cast<float>(scale),
+                       n(26), n(27), p(28), static_cast<size_t>(x[29]), stream);
+}
+#undef FA_BLOCK_INTS
+
 int fa_dropout_p8(float dropout_p) { return p8_of(dropout_p); }
 
 fa_status fa_debug_dropout_keep(uint8_t* keep, int B, int H, int N, float dropout_p,

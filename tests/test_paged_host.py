@@ -1,6 +1,7 @@
 """The paged-cache calls on the host: what they refuse before any device work, and the
 oracle's quantised rows against values worked out by hand."""
 import ctypes
+import struct
 
 import numpy as np
 import pytest
@@ -153,3 +154,32 @@ def test_empty_batches_are_refused(rows):
     with pytest.raises(ValueError):
         fa.paged_read(kp, kp, torch.zeros(len(rows), 0, dtype=torch.int32),
                       torch.zeros(len(rows), dtype=torch.int32), 5)
+
+
+class Captured:
+    """Stands for the library: a call gives back its arguments."""
+    def __getattr__(self, name):
+        return lambda *args: args
+
+
+@pytest.mark.parametrize("call,name,fmt", [(write, "write", "=24q"), (read, "read", "=20q"),
+                                           (attn, "attn", "=25qd4q")])
+def test_calls_from_blocks_check_as_the_others_do(lib, call, name, fmt):
+    block = getattr(lib, f"fa_paged_{name}_block")
+    pack = lambda **kw: struct.pack(fmt, *(0 if v is None else v
+                                           for v in call(Captured(), **kw)[:-1]))
+    for bad in (dict(k=0), dict(k=A + 8), dict(table=A + 2), dict(kv=0), dict(page_size=24),
+                dict(d=96), dict(type=2), dict(type=1), dict(sp=1 << 40), dict(sh=-64),
+                dict(max_pages=0), dict(ts=2), dict(B=0), dict(k=A, H_kv=0)):
+        assert block(pack(**bad), None) == call(lib, **bad) != 0, bad
+    for wide in (dict(B=2 + (1 << 32)), dict(d=64 + (1 << 32)), dict(max_pages=1 << 31)):
+        assert block(pack(**wide), None) == 1
+    assert block(None, None) == 1
+
+
+def test_attention_from_a_block_checks_its_own_arguments(lib):
+    pack = lambda **kw: struct.pack("=25qd4q", *(0 if v is None else v
+                                                 for v in attn(Captured(), **kw)[:-1]))
+    for bad in (dict(scale=0.0), dict(scale=float("nan")), dict(scale=1e300), dict(wl=-2),
+                dict(H=3), dict(qs=8), dict(max_q=0), dict(q=A + 2), dict(o=0), dict(wsb=-1)):
+        assert lib.fa_paged_attn_block(pack(**bad), None) == 1, bad
