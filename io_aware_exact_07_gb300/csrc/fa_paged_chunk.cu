@@ -28,7 +28,7 @@
 // Bounds: for chunks the tensor core (1024 cycles of products per 128 x 128 tile at d = 128, of
 // 1540 measured with a bf16 cache: 0.80 us a tile; each warpgroup's chain of scores, maximum,
 // exponentials and the handshakes with the products is the rest); with few rows HBM; from an
-// e4m3 cache (1.47 us a tile) the conversion, which takes registers, issue slots and bandwidth
+// e4m3 cache (1.44 us a tile) the conversion, which takes registers, issue slots and bandwidth
 // of shared memory from the softmax (without it 1.21 us), and the chain that goes from a PV
 // product over the S that takes its place to the next P (with neither conversion nor
 // exponentials still 0.95 us).
@@ -268,7 +268,7 @@ __device__ __forceinline__ void Unit::advance(const PagedAttnArgs& a, int k) {
 struct Piece {
   int b, h, qt, nt;
   int j0, len, pos0, row0;
-  int rows, from_start, ends, pad;
+  int rows, from_start, ends;
 };
 
 // A CTA's work, piece by piece. First `rounds` whole units,
@@ -684,7 +684,6 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     p.rows = static_cast<int>(z.x);
     p.from_start = static_cast<int>(z.y);
     p.ends = static_cast<int>(z.z);
-    p.pad = 0;
     return p;
   };
   auto wait_piece = [&](int n) {

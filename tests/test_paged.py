@@ -681,3 +681,33 @@ def test_output_in_place_of_q_is_refused():
     x = b.fill().on(DEV)
     with pytest.raises(ValueError):
         attn(b, x, causal=True, max_q=2, out=(x.q, torch.empty(x.q.shape[:2], device=DEV)))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_captured_chunk_is_replayed_with_other_lengths_and_offsets(e4m3):
+    # one capture for 64 packed rows of up to 60 per sequence; rows and lengths move between
+    # the sequences, some get none
+    pool = Batch([64, 64, 64], [900, 700, 500], 16, 2, 64, e4m3, G=2, seed=47)
+    x = pool.fill().on(DEV)
+    q = x.q[:64].clone()
+    kv, cu = x.kv.clone(), torch.tensor([0, 30, 60, 64], dtype=torch.int32, device=DEV)
+    out = (torch.empty_like(q), torch.empty(q.shape[:2], device=DEV))
+
+    def call():
+        fa.paged_attn(q, x.k, x.v, x.table, kv, cu, max_q=60, causal=True, out=out, **x.sc)
+    call()
+    sync()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for nq, lens in (([30, 30, 4], [900, 700, 500]), ([0, 60, 4], [900, 61, 5]),
+                     ([1, 2, 60], [640, 128, 127]), ([7, 0, 0], [7, 0, 300])):
+        c = Batch(nq, lens, 16, 2, 64, e4m3, G=2, seed=47)
+        c.q = pool.q[:64]
+        for n in "kv":
+            c.rows[n] = [r[:L] for r, L in zip(pool.rows[n], lens)]
+        kv.copy_(torch.tensor(lens, dtype=torch.int32))
+        cu.copy_(torch.tensor(np.concatenate([[0], np.cumsum(nq)]), dtype=torch.int32))
+        g.replay()
+        sync()
+        check_attn(*out, c.oracle(True), rows=sum(nq))
