@@ -848,8 +848,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       if (!is_k && pc.nt > 0) ok = do_q();
       for (int i = 0; ok && i < pc.nt; ++i) {
         const int j = pc.j0 + i;
-        if (!mbar_wait_warp(c_full[cs], cph, tmo, abort_flag) ||
-            !mbar_wait_warp(empty[ts], tph, tmo, abort_flag)) {
+        if (!mbar_wait_warp(c_full[cs], cph, tmo, abort_flag)) {
           ok = false;
           break;
         }
@@ -857,6 +856,12 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         const uint32_t mine = ld_shared_u32(sb);
         const int top = top_of(mine, j, is_k ? 127 - 40 : 127 - 60);
         write_factors(mine, j, top);
+        // (the wait comes as late as it can: for V the last PV product, this and the next one
+        // are a chain)
+        if (!mbar_wait_warp(empty[ts], tph, tmo, abort_flag)) {
+          ok = false;
+          break;
+        }
         convert_tile(ring + ts * L::kTileBytes, j);
         if (is_k && wx == 0) {
           const int ev = top_of(ld_shared_u32(sb + kTile), j, 127 - 60) - 127;  // V's, as V's warps find it
