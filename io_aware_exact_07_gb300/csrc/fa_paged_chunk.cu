@@ -26,9 +26,9 @@
 // weight of zero would not hide a NaN.
 //
 // Bounds: for chunks the tensor core (1024 cycles of products per 128 x 128 tile at d = 128, of
-// 1540 measured with a bf16 cache: 0.80 us a tile; each warpgroup's chain of scores, maximum,
+// 1500 measured with a bf16 cache: 0.78 us a tile; each warpgroup's chain of scores, maximum,
 // exponentials and the handshakes with the products is the rest); with few rows HBM; from an
-// e4m3 cache (1.44 us a tile) the conversion, which takes registers, issue slots and bandwidth
+// e4m3 cache (1.39 us a tile) the conversion, which takes registers, issue slots and bandwidth
 // of shared memory from the softmax (without it 1.21 us), and the chain that goes from a PV
 // product over the S that takes its place to the next P (with neither conversion nor
 // exponentials still 0.95 us).
