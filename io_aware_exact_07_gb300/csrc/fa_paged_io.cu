@@ -24,14 +24,12 @@ namespace {
 constexpr int kIoWarps = 8;
 constexpr int kReadRows = 16;  // rows per warp; a page holds a multiple of it
 
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-
 // Exponent of the scale of a row whose largest magnitude has the bf16 bits `top`
-// (finite): with top = 1.m * 2^x, 448 = 1.75 * 2^8 is reached from m = 96 / 128 on.
+// (finite): with top = 1.m * 2^x, 448 = 1.75 * 2^8 is exceeded from m = 97 / 128 on, where
+// adding 31 carries into the exponent.
 __device__ __forceinline__ int scale_exponent(uint32_t top) {
-  if (top == 0u) return 0;
-  const int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0);
-  return e < kScaleMin ? kScaleMin : (e > kScaleMax ? kScaleMax : e);
+  const int e = static_cast<int>((top + 31u) >> 7) - 127 - 8;
+  return top == 0u ? 0 : max(kScaleMin, min(kScaleMax, e));
 }
 
 // The codes of four bf16 values times f, f.
@@ -94,11 +92,17 @@ __global__ void __launch_bounds__(kIoWarps * 32) fa_paged_write_kernel(const Pag
       if (real) *reinterpret_cast<uint4*>(base + at * 2) = x[i];
     } else {
       constexpr uint32_t kAbs = 0x7FFF7FFFu;
-      const uint32_t m2 =
-          max2(max2(x[i].x & kAbs, x[i].y & kAbs), max2(x[i].z & kAbs, x[i].w & kAbs));
+      uint32_t m2 = __vimax3_u16x2(x[i].x & kAbs, x[i].y & kAbs, x[i].z & kAbs);
+      m2 = __vmaxu2(m2, x[i].w & kAbs);
       uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
+      if constexpr (kLanes == 16) {  // a row each for the halves of the warp
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, lane < 16 ? top : 0u);
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : top);
+        top = lane < 16 ? lo : hi;
+      } else {
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
       const bool finite = top < 0x7F80u;
       const int e = finite ? scale_exponent(top) : 0;
       const uint64_t ff = f2_pack(pow2i(-e), pow2i(-e));
@@ -197,8 +201,9 @@ cudaError_t launch_write(const PagedWriteArgs& a, cudaStream_t stream) {
 
 // A warp takes 16 rows of 128 values or 64 at once where that leaves some ten warps for each
 // SM, and as few as it can where the rows have to spread over the SMs. 18300 tokens of 8 heads
-// to e4m3 with 1, 2, 4, 8, 16 passes, d = 128: 47, 29, 25, 25, 43 us (of 17 that the bytes
-// take); with 1 and 8 passes 2400 tokens take 6.6 and 5.3 us, 1200 tokens 4.2 and 4.3.
+// to e4m3 with 1, 2, 4, 8, 16 passes, d = 128: 47, 29, 25, 25, 43 us (23 now, of 17 that the bytes
+// take: the quantising instructions and a chain of loads per warp bound it; bf16 23 of 22); with 1
+// and 8 passes 2400 tokens take 6.6 and 5.3 us, 1200 tokens 4.2 and 4.3.
 template <int D, bool E4M3>
 cudaError_t launch_write(const PagedWriteArgs& a, cudaStream_t stream) {
   const long long rows = 2ll * a.c.T * a.c.Hkv;

@@ -711,3 +711,26 @@ def test_a_captured_chunk_is_replayed_with_other_lengths_and_offsets(e4m3):
         g.replay()
         sync()
         check_attn(*out, c.oracle(True), rows=sum(nq))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_every_finite_magnitude_as_a_rows_largest(d):
+    # exponent and codes are exact: compared with the oracle's bit by bit
+    g = torch.Generator().manual_seed(d)
+    top = torch.arange(0x7F80, dtype=torch.int32)  # bf16 bits
+    n = top.numel()
+    bits = torch.minimum((torch.rand(n, d, generator=g) * (top[:, None] + 1)).to(torch.int32),
+                         top[:, None])
+    bits += torch.randint(0, 2, (n, d), generator=g).to(torch.int32) * -32768
+    bits[torch.arange(n), torch.randint(0, d, (n,), generator=g)] = top
+    x = bits.to(torch.int16).view(torch.bfloat16).reshape(n, 1, d)
+    P = -(-n // 256)
+    c = fa.paged_cache(P, 256, 1, d, e4m3=True, device=DEV)
+    fa.paged_write(x.to(DEV), x.to(DEV), kv_lens=torch.tensor([n], dtype=torch.int32, device=DEV),
+                   page_table=torch.arange(P, dtype=torch.int32, device=DEV).reshape(1, P), **c)
+    sync()
+    codes, scale = oracle.quantize_rows(x.double().numpy())
+    for name in "kv":
+        got = c[name + "_pages"].cpu().numpy().reshape(P * 256, 1, d)[:n]
+        assert np.array_equal(got, codes)
+        assert np.array_equal(c[name + "_scale"].cpu().numpy().reshape(-1, 1)[:n], scale)
