@@ -4,8 +4,8 @@
 // names this case, bound by reading K and V, as left unoptimised. HBM is the bound, so the
 // kernel is a stream of K and V through shared memory, each byte read once per K/V head:
 //
-//  - Every warp is on its own: it takes 16 keys of each 128-key block, brings their K and V
-//    rows into its own ring of stages with cp.async, and keeps its own softmax state, so
+//  - Every warp is on its own: it takes 16 or 32 keys of each block of keys, brings their K and
+//    V rows into its own ring of stages with cp.async, and keeps its own softmax state, so
 //    that the main loop has no block barrier and loads run ahead across heads and sequences.
 //    16 keys lie in one page (its size is a multiple of 16), so one table entry serves them.
 //  - S^T = K Q^T and O^T += V^T P^T with m16n8k16 products: the keys (then the columns of V)
@@ -16,7 +16,7 @@
 //    products that bound it, at some 7 cycles each and SM. Here and with 128-row tiles, us, 24
 //    sequences, 8 K/V heads, 24 rows: d = 128, 8192 bf16 keys 138 and 132, 1024 keys 35 and 38,
 //    e4m3 122 and 147, 34 and 50; d = 64 79 and 82, 22 and 31, e4m3 86 and 107; 128 sequences
-//    of 200 keys 48 and 55, 4 of 3000 13 and 17. 32 rows: 8192 keys 156 and 133, 1024 44 and 38,
+//    of 200 keys 48 and 55, 4 of 3000 13 and 17 (e4m3 here since then 10 to 20 % less). 32 rows: 8192 keys 156 and 133, 1024 44 and 38,
 //    e4m3 160 and 148, d = 64 94 and 82, 128 of 200 keys 60 and 55.
 //  - The order of the columns d within a product is free as long as both operands share
 //    it: a thread takes the 16 bytes of a row that it can load at once.
@@ -36,7 +36,7 @@ namespace fa {
 
 namespace {
 
-constexpr int kChunk = 16;                  // keys of a warp's step
+constexpr int kGroup = 16;                  // keys of a product, which lie in one page
 constexpr int kMergeWarps = 8;
 constexpr int kSmemMax = 232448;
 
@@ -44,23 +44,32 @@ template <int D, bool E4M3, int NT>
 struct StepL {
   // More warps hide the latency of a warp's chain of steps where its keys are few bytes, as
   // far as registers and the merge buffer leave room. 16 sequences of 16384 keys, 8 K/V heads,
-  // 4 rows with 8, 12, 16 warps: e4m3 d = 128 112, 96, 97 us; e4m3 d = 64 97, 75, 71; bf16 d =
-  // 64 91, 91, 87; bf16 d = 128 with 8: 164. 24 of 8192 keys, 20 rows, d = 64: 95, 89, 152.
-  static constexpr int kWarps = NT >= 2 ? (D == 64 ? 12 : 8) : D == 64 ? 16 : E4M3 ? 12 : 8;
+  // 4 rows with 8, 12, 16 warps: e4m3 d = 128 112, 96, 97 us; bf16 d = 64 91, 91, 87; bf16 d =
+  // 128 with 8: 160; e4m3 d = 64 (kU = 2) with 12, 16: 59, 58, and 128 of 200 keys 21, 23.5. 24
+  // of 8192 keys, 20 rows, d = 64: 95, 89, 152.
+  static constexpr int kWarps = NT >= 2 ? (D == 64 ? 12 : 8) : E4M3 ? 12 : D == 64 ? 16 : 8;
   static constexpr int kThreads = kWarps * 32;
+  // Groups of a warp's step. From codes to O a group is a long chain, of which a scheduler's
+  // three warps hide too little: two at once overlap, and share the vote, the walk and the
+  // waits. e4m3, 16 sequences of 16384 keys, 8 K/V heads, one and two groups: 4 rows, d = 128 94
+  // and 88 us, d = 64 71 and 59; 16 rows 135 and 112, 89 and 74; 24 rows 149 and 134, 105 and 87.
+  // (bf16, d = 64, whose bytes bound it, gains nothing; at d = 128 there is no room.)
+  static constexpr int kU = E4M3 ? 2 : 1;
+  static constexpr int kChunk = kU * kGroup;
   static constexpr int kBlock = kWarps * kChunk;          // keys of a block
   static constexpr int kRows = 8 * NT;                    // query rows
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kUnits = kRowBytes / 16;           // 16-byte units of a row
-  static constexpr int kTileBytes = kChunk * kRowBytes;   // 16 K rows, or V rows
+  static constexpr int kGroupBytes = kGroup * kRowBytes;  // 16 K rows, or V rows
+  static constexpr int kTileBytes = kU * kGroupBytes;     // those of a step
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kScaleBytes = E4M3 ? 32 : 0;       // K's and V's 16 scale bytes
+  static constexpr int kScaleBytes = E4M3 ? 32 * kU : 0;  // K's and V's scale bytes, 16 each a group
   static constexpr int kPitch = D + 4;                    // merge buffer row, in floats
   // From 17 rows on Q lies in shared memory, one copy for all warps. Where the merge's buffer
   // would leave no room for the ring, two warps first join their states in registers, and it
   // takes half (20 rows, d = 64, where it fits without: 58.6 us, with 62.4).
   static constexpr bool kQShared = NT == 3;
-  static constexpr int kFold = NT == 3 && kRowBytes == 256 ? 2 : 1;
+  static constexpr int kFold = kU == 2 || (NT == 3 && kRowBytes == 256) ? 2 : 1;
   static constexpr int kStates = kWarps / kFold;
   static constexpr int kQBytes = kQShared ? kRows * (D * 2 + 4) : 0;  // rows, and their exponents
   static constexpr int kMergeBytes = kStates * kRows * kPitch * 4;
@@ -191,6 +200,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   using L = StepL<D, E4M3, NT>;
   using Walk = Walk<L::kBlock>;
   constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kBlock = L::kBlock;
+  constexpr int kU = L::kU, kChunk = L::kChunk;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, c4 = lane & 3;
@@ -277,43 +287,50 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   const uint32_t ring = smem_u32(smem + L::kRingOff) + warp * L::kStages * L::kStageBytes;
   const uint32_t scale_ring = smem_u32(smem + L::kScaleOff) + warp * L::kStages * L::kScaleBytes;
   constexpr int kRowsPer = 32 / L::kUnits;        // rows that the lanes cover at once
-  constexpr int kLoads = kChunk / kRowsPer;
+  constexpr int kLoads = kGroup / kRowsPer;
   const int lrow = lane / L::kUnits, lunit = lane % L::kUnits;
   constexpr int kEs = E4M3 ? 1 : 2;
   const long long row_bytes = a.c.stride_row * kEs;
   Walk lw = cw;  // the block to load next
   auto chunk_of = [&](const Walk& w) { return w.blk * kBlock + warp * kChunk; };
-  auto page_of = [&](const Walk& w) {
-    const int j = chunk_of(w);
-    return j < w.s.len ? paged_page(a.c, w.b, j) : -1;
-  };
-  int lpage = page_of(lw);
-  auto issue = [&](int stage) {
-    const int j = chunk_of(lw);
-    const int have = lpage >= 0 ? lw.s.len - j : 0;  // rows of the chunk that the cache holds
-    const int slot = page_row(a.c, j);
-    const int page = lpage >= 0 ? lpage : 0;
-    const long long at = (page * a.c.stride_page + lw.h * a.c.stride_head +
-                          (slot + lrow) * a.c.stride_row) * kEs + lunit * 16;
-    const uint32_t dk = ring + stage * L::kStageBytes, dv = dk + L::kTileBytes;
+  int lpage[kU];  // pages of its groups
+  auto find_pages = [&]() {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r = lrow + i * kRowsPer;
-      const bool real = r < have;
-      const long long off = real ? at + i * kRowsPer * row_bytes : 0;
-      cp_async16(dk + k_unit<D, E4M3>(r, lunit) * 16, a.c.k + off, real);
-      cp_async16(dv + v_unit<D, E4M3>(r, lunit) * 16, a.c.v + off, real);
+    for (int g = 0; g < kU; ++g) {
+      const int j = chunk_of(lw) + g * kGroup;
+      lpage[g] = j < lw.s.len ? paged_page(a.c, lw.b, j) : -1;
     }
-    if constexpr (E4M3) {
-      if (lane < 2) {  // the 16 rows' scale bytes lie next to each other
-        const long long so =
-            (static_cast<long long>(page) * a.c.Hkv + lw.h) * a.c.page_size + slot;
-        cp_async16(scale_ring + stage * L::kScaleBytes + lane * 16,
-                   (lane ? a.c.v_scale : a.c.k_scale) + so, have > 0);
+  };
+  find_pages();
+  auto issue = [&](int stage) {
+#pragma unroll
+    for (int g = 0; g < kU; ++g) {
+      const int j = chunk_of(lw) + g * kGroup;
+      const int have = lpage[g] >= 0 ? lw.s.len - j : 0;  // rows of the group that the cache holds
+      const int slot = page_row(a.c, j);
+      const int page = lpage[g] >= 0 ? lpage[g] : 0;
+      const long long at = (page * a.c.stride_page + lw.h * a.c.stride_head +
+                            (slot + lrow) * a.c.stride_row) * kEs + lunit * 16;
+      const uint32_t dk = ring + stage * L::kStageBytes + g * L::kGroupBytes, dv = dk + L::kTileBytes;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = lrow + i * kRowsPer;
+        const bool real = r < have;
+        const long long off = real ? at + i * kRowsPer * row_bytes : 0;
+        cp_async16(dk + k_unit<D, E4M3>(r, lunit) * 16, a.c.k + off, real);
+        cp_async16(dv + v_unit<D, E4M3>(r, lunit) * 16, a.c.v + off, real);
+      }
+      if constexpr (E4M3) {
+        if (lane < 2) {  // the 16 rows' scale bytes lie next to each other
+          const long long so =
+              (static_cast<long long>(page) * a.c.Hkv + lw.h) * a.c.page_size + slot;
+          cp_async16(scale_ring + stage * L::kScaleBytes + g * 32 + lane * 16,
+                     (lane ? a.c.v_scale : a.c.k_scale) + so, have > 0);
+        }
       }
     }
     lw.next(a);
-    lpage = page_of(lw);
+    find_pages();
   };
   // ---- query rows of a K/V head: row r = t * G + g; the rows' columns in the order of the
   // products, two registers per 16 columns. Column from which 16 bytes of a thread's row serve
@@ -487,41 +504,44 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
       const uint32_t sk = ring + stage * L::kStageBytes, sv = sk + L::kTileBytes;
       // ---- S^T = K Q^T: keys g8 and g8 + 8, query rows 2 c4 and 2 c4 + 1
       constexpr bool kTwo = NT <= 2;  // two chains of products each, where there are few
-      float s[NT][4], s2[NT][4];
+      float s[kU][NT][4], s2[kU][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int g = 0; g < kU; ++g) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
-      if constexpr (!E4M3) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          const uint4 k0 = ld_shared_v4(sk + k_unit<D, E4M3>(g8, 4 * x + c4) * 16);
-          const uint4 k1 = ld_shared_v4(sk + k_unit<D, E4M3>(g8 + 8, 4 * x + c4) * 16);
+          for (int e = 0; e < 4; ++e) s[g][n][e] = s2[g][n][e] = 0.f;
+        if constexpr (!E4M3) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 y = get_q(n, x);
-            mma16816<E4M3>(s[n], k0.x, k1.x, k0.y, k1.y, y.x, y.y);
-            mma16816<E4M3>(kTwo ? s2[n] : s[n], k0.z, k1.z, k0.w, k1.w, y.z, y.w);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          const uint4 k0 = ld_shared_v4(sk + k_unit<D, E4M3>(g8, 4 * x + c4) * 16);
-          const uint4 k1 = ld_shared_v4(sk + k_unit<D, E4M3>(g8 + 8, 4 * x + c4) * 16);
-          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-          for (int w = 0; w < 4; w += 2) {
-            uint32_t a0[4], a1[4];
-            e4m3_to_f16(w0[w], a0[0], a0[2]);
-            e4m3_to_f16(w1[w], a0[1], a0[3]);
-            e4m3_to_f16(w0[w + 1], a1[0], a1[2]);
-            e4m3_to_f16(w1[w + 1], a1[1], a1[3]);
+          for (int x = 0; x < D / 32; ++x) {
+            const uint4 k0 = ld_shared_v4(sk + g * L::kGroupBytes + k_unit<D, E4M3>(g8, 4 * x + c4) * 16);
+            const uint4 k1 = ld_shared_v4(sk + g * L::kGroupBytes + k_unit<D, E4M3>(g8 + 8, 4 * x + c4) * 16);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              const uint4 y = get_q(n, 2 * x + (w >> 1));
-              mma16816<E4M3>(s[n], a0[0], a0[1], a0[2], a0[3], y.x, y.y);
-              mma16816<E4M3>(kTwo ? s2[n] : s[n], a1[0], a1[1], a1[2], a1[3], y.z, y.w);
+              const uint4 y = get_q(n, x);
+              mma16816<E4M3>(s[g][n], k0.x, k1.x, k0.y, k1.y, y.x, y.y);
+              mma16816<E4M3>(kTwo ? s2[g][n] : s[g][n], k0.z, k1.z, k0.w, k1.w, y.z, y.w);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) {
+            const uint4 k0 = ld_shared_v4(sk + g * L::kGroupBytes + k_unit<D, E4M3>(g8, 4 * x + c4) * 16);
+            const uint4 k1 = ld_shared_v4(sk + g * L::kGroupBytes + k_unit<D, E4M3>(g8 + 8, 4 * x + c4) * 16);
+            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+            for (int w = 0; w < 4; w += 2) {
+              uint32_t a0[4], a1[4];
+              e4m3_to_f16(w0[w], a0[0], a0[2]);
+              e4m3_to_f16(w1[w], a0[1], a0[3]);
+              e4m3_to_f16(w0[w + 1], a1[0], a1[2]);
+              e4m3_to_f16(w1[w + 1], a1[1], a1[3]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint4 y = get_q(n, 2 * x + (w >> 1));
+                mma16816<E4M3>(s[g][n], a0[0], a0[1], a0[2], a0[3], y.x, y.y);
+                mma16816<E4M3>(kTwo ? s2[g][n] : s[g][n], a1[0], a1[1], a1[2], a1[3], y.z, y.w);
+              }
             }
           }
         }
@@ -530,45 +550,56 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
       // scale, V's exponent, and what takes V's scale out of the sum (times 2^-64, so that the
       // sum stays in range for the smallest scales; a scale byte of 0, which only a page that
       // is none has, counts as 127).
-      float k_scale[2] = {1.f, 1.f}, v_exp[2] = {0.f, 0.f}, v_inv[2] = {1.f, 1.f};
-      if constexpr (E4M3) {
-        const uint32_t ss = scale_ring + stage * L::kScaleBytes + g8;
+      float v_inv[kU][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int kb = ld_shared_u8(ss + 8 * e);
-          int vb = ld_shared_u8(ss + 16 + 8 * e);
-          vb = vb == 0 ? 127 : min(vb, kScaleMax + 127);
-          k_scale[e] = kb == kScaleNaN ? __uint_as_float(0x7FC00000u) : pow2i(min(kb, kScaleMax + 127) - 127);
-          v_exp[e] = static_cast<float>(vb - 127);
-          v_inv[e] = pow2i(127 - 64 - vb);
+      for (int g = 0; g < kU; ++g) {
+        float k_scale[2] = {1.f, 1.f}, v_exp[2] = {0.f, 0.f};
+        if constexpr (E4M3) {
+          const uint32_t ss = scale_ring + stage * L::kScaleBytes + g * 32 + g8;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int kb = ld_shared_u8(ss + 8 * e);
+            int vb = ld_shared_u8(ss + 16 + 8 * e);
+            vb = vb == 0 ? 127 : min(vb, kScaleMax + 127);
+            k_scale[e] = kb == kScaleNaN ? __uint_as_float(0x7FC00000u) : pow2i(min(kb, kScaleMax + 127) - 127);
+            v_exp[e] = static_cast<float>(vb - 127);
+            v_inv[g][e] = pow2i(127 - 64 - vb);
+          }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[g][n][e] = (s[g][n][e] + s2[g][n][e]) * (c_row[n][e & 1] * k_scale[e >> 1]) + v_exp[e >> 1];
       }
       constexpr float kLift = E4M3 ? kF16Lift : 0.f;
-      bool grow = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[n][e] = (s[n][e] + s2[n][e]) * (c_row[n][e & 1] * k_scale[e >> 1]) + v_exp[e >> 1];
-      }
       const int last_lo = a.wl >= 0 ? cw.s.len - 1 - a.wl : 0;  // first key of the last token
       const int first_hi = a.causal ? pos0 + 1 : cw.s.len;      // end of the first token's keys
       if (j0 < last_lo || j0 + kChunk > first_hi) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int g = 0; g < kU; ++g)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = j0 + g8 + (e >> 1) * 8;
-            const int pos = pos0 + (n * 8 + 2 * c4 + (e & 1)) / G;
-            if (key >= cw.s.len || (a.causal && key > pos) || (a.wl >= 0 && key < pos - a.wl))
-              s[n][e] = -INFINITY;
-          }
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = j0 + g * kGroup + g8 + (e >> 1) * 8;
+              const int pos = pos0 + (n * 8 + 2 * c4 + (e & 1)) / G;
+              if (key >= cw.s.len || (a.causal && key > pos) || (a.wl >= 0 && key < pos - a.wl))
+                s[g][n][e] = -INFINITY;
+            }
       }
+      // largest of the thread's scores of rows 2 c4 + e
+      auto largest = [&](int n, int e) {
+        float mx = fmaxf(s[0][n][e], s[0][n][e + 2]);
+#pragma unroll
+        for (int g = 1; g < kU; ++g) mx = fmaxf(mx, fmaxf(s[g][n][e], s[g][n][e + 2]));
+        return mx;
+      };
+      bool grow = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          grow |= fmaxf(s[n][e], s[n][e + 2]) > m_ref[n][e] + (kRescale + kLift);
+        for (int e = 0; e < 2; ++e) grow |= largest(n, e) > m_ref[n][e] + (kRescale + kLift);
       // The reference maximum moves rarely, so most steps need one vote instead of the row
       // maxima.
       if (__any_sync(0xffffffffu, grow)) {
@@ -576,7 +607,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(s[n][e], s[n][e + 2]);
+            float mx = largest(n, e);
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
             const float m_new = fmaxf(m_ref[n][e], mx - kLift);
@@ -590,64 +621,69 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
             }
           }
       }
-      uint32_t p0[NT], p1[NT];  // P^T as the second operand: keys 2 c4 (+ 8) .., query row g8
+      uint32_t p0[kU][NT], p1[kU][NT];  // P^T as the second operand: keys 2 c4 (+ 8) .., query row g8
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float p[4];
+      for (int g = 0; g < kU; ++g)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float m = m_ref[n][e & 1];
-          p[e] = ex2_approx(s[n][e] - (m == -INFINITY ? 0.f : m));
-        }
-        if constexpr (E4M3) {
-          l_sum[n][0] = fmaf(p[0], v_inv[0], fmaf(p[2], v_inv[1], l_sum[n][0]));
-          l_sum[n][1] = fmaf(p[1], v_inv[0], fmaf(p[3], v_inv[1], l_sum[n][1]));
-        } else {
-          l_sum[n][0] += p[0] + p[2];
-          l_sum[n][1] += p[1] + p[3];
-        }
-        // P is rounded to bf16 for the product (at most 2^-8 of each weight), or to f16 (2^-11,
-        // or 2^-32 of the largest weight where that is more); the sum keeps fp32
-        p0[n] = movmatrix_t(E4M3 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
-        p1[n] = movmatrix_t(E4M3 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
-      }
-      // ---- O^T += V^T P^T
-      if constexpr (!E4M3) {
-        const int key = (lane & 7) + ((lane >> 4) << 3);
+        for (int n = 0; n < NT; ++n) {
+          float p[4];
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          uint32_t v[4];
-          ldmatrix4_t(sv + v_unit<D, E4M3>(key, 2 * x + ((lane >> 3) & 1)) * 16, v);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816<E4M3>(o[n][x], v[0], v[1], v[2], v[3], p0[n], p1[n]);
-        }
-      } else {
-        constexpr int kWords = D / 32;  // words of a thread's columns, D / 8 of them, per key
-        uint32_t v[4][kWords];          // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = 2 * c4 + (e & 1) + (e >> 1) * 8;
-          if constexpr (D == 128) {
-            const uint4 y = ld_shared_v4(sv + v_unit<D, E4M3>(key, g8) * 16);
-            v[e][0] = y.x;
-            v[e][1] = y.y;
-            v[e][kWords - 2] = y.z;
-            v[e][kWords - 1] = y.w;
-          } else {
-            const uint2 y = ld_shared_v2(sv + v_unit<D, E4M3>(key, g8 >> 1) * 16 + (g8 & 1) * 8);
-            v[e][0] = y.x;
-            v[e][1] = y.y;
+          for (int e = 0; e < 4; ++e) {
+            const float m = m_ref[n][e & 1];
+            p[e] = ex2_approx(s[g][n][e] - (m == -INFINITY ? 0.f : m));
           }
+          if constexpr (E4M3) {
+            l_sum[n][0] = fmaf(p[0], v_inv[g][0], fmaf(p[2], v_inv[g][1], l_sum[n][0]));
+            l_sum[n][1] = fmaf(p[1], v_inv[g][0], fmaf(p[3], v_inv[g][1], l_sum[n][1]));
+          } else {
+            l_sum[n][0] += p[0] + p[2];
+            l_sum[n][1] += p[1] + p[3];
+          }
+          // P is rounded to bf16 for the product (at most 2^-8 of each weight), or to f16 (2^-11,
+          // or 2^-32 of the largest weight where that is more); the sum keeps fp32
+          p0[g][n] = movmatrix_t(E4M3 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
+          p1[g][n] = movmatrix_t(E4M3 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
         }
+      // ---- O^T += V^T P^T
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {  // columns (D / 8) g8 + 2 x and + 1
-          // both columns' codes of two keys in one word, then as f16 pairs of keys
-          constexpr uint32_t kSel[2] = {0x5140u, 0x7362u};
-          uint32_t r[4];
-          e4m3_to_f16(prmt(v[0][x >> 1], v[1][x >> 1], kSel[x & 1]), r[0], r[1]);
-          e4m3_to_f16(prmt(v[2][x >> 1], v[3][x >> 1], kSel[x & 1]), r[2], r[3]);
+      for (int g = 0; g < kU; ++g) {
+        if constexpr (!E4M3) {
+          const int key = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816<E4M3>(o[n][x], r[0], r[1], r[2], r[3], p0[n], p1[n]);
+          for (int x = 0; x < D / 16; ++x) {
+            uint32_t v[4];
+            ldmatrix4_t(sv + g * L::kGroupBytes + v_unit<D, E4M3>(key, 2 * x + ((lane >> 3) & 1)) * 16, v);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<E4M3>(o[n][x], v[0], v[1], v[2], v[3], p0[g][n], p1[g][n]);
+          }
+        } else {
+          constexpr int kWords = D / 32;  // words of a thread's columns, D / 8 of them, per key
+          uint32_t v[4][kWords];          // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = 2 * c4 + (e & 1) + (e >> 1) * 8;
+            if constexpr (D == 128) {
+              const uint4 y = ld_shared_v4(sv + g * L::kGroupBytes + v_unit<D, E4M3>(key, g8) * 16);
+              v[e][0] = y.x;
+              v[e][1] = y.y;
+              v[e][kWords - 2] = y.z;
+              v[e][kWords - 1] = y.w;
+            } else {
+              const uint2 y = ld_shared_v2(sv + g * L::kGroupBytes + v_unit<D, E4M3>(key, g8 >> 1) * 16 + (g8 & 1) * 8);
+              v[e][0] = y.x;
+              v[e][1] = y.y;
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {  // columns (D / 8) g8 + 2 x and + 1
+            // both columns' codes of two keys in one word, then as f16 pairs of keys
+            constexpr uint32_t kSel[2] = {0x5140u, 0x7362u};
+            uint32_t r[4];
+            e4m3_to_f16(prmt(v[0][x >> 1], v[1][x >> 1], kSel[x & 1]), r[0], r[1]);
+            e4m3_to_f16(prmt(v[2][x >> 1], v[3][x >> 1], kSel[x & 1]), r[2], r[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<E4M3>(o[n][x], r[0], r[1], r[2], r[3], p0[g][n], p1[g][n]);
+          }
         }
       }
     }
