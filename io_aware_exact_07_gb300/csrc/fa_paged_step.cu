@@ -25,7 +25,7 @@
 //    K scale goes to its score, its V scale to its weight: P carries it (and the running
 //    maximum counts it), the softmax's sum takes it out again. Turning the codes into bf16
 //    with their scales, by integer operations, takes 2.5 instructions a code instead of 0.6.
-//  - The (sequence, K/V head, 128-key block) list is cut into equal runs, one per CTA, by
+//  - The (sequence, K/V head, key block) list is cut into equal runs, one per CTA, by
 //    the lengths found on the device. A head that falls into one run is written directly;
 //    one cut by a run's end leaves normalised pieces, merged by a second, small kernel with
 //    the two-block rule of the online softmax. Where the page table has room for few keys,
@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   // the SMs can draw all that HBM gives where a warp's work per byte is least, and cutting
   // costs pieces and their merge. 128 heads (152 CTAs), cut and whole: 16384 bf16 keys of 128
   // 161 and 156 us, 4096 keys 48 and 44, 1000 keys 15.6 and 13.9, with 20 rows 56 and 51 for 4096.
-  // Where the warps' work counts it is the cut that pays: 16384 quantised keys 95 and 107 (d =
-  // 64: 1000 keys 10.7 and 12.0, 4096 keys 29.5 and 27.6).
+  // Where the warps' work counts there is nothing to gain: e4m3 16384 keys 88.5 and 88.0, 4096
+  // 31.4 and 30.2, 1000 12.8 and 13.7; d = 64 1000 bf16 keys 10.7 and 12.0, 4096 29.5 and 27.6.
   if constexpr (!E4M3 && D == 128) {
     long long all;
     block_scan<kWarps>(heads, plan->warp_sums, &all);
