@@ -93,16 +93,21 @@ struct ChunkL {
   // e4m3: the scale bytes of staged tiles (K's stages: K's and V's; V's stages: V's); the
   // scales of the latest tiles and Q's row exponents of the latest pieces, for the softmax.
   // Tile n's slot is written when K's tile n is converted, so after the S product of tile n -
-  // kKStages; that one waited until the softmax had read S, and before it the slot, of tile n -
-  // kKStages - 2 at least. A piece's exponents are written after all S products of the piece
-  // before, so when both warpgroups have left the piece before that one's predecessor.
-  static constexpr int kSlots = E4M3 ? 4 : 0;
-  static_assert(!E4M3 || kSlots >= 2 + kKStages, "a slot is rewritten before it is read");
+  // kKStages; that one waited until its warpgroup had read the tile before (S, and before it the
+  // slot). The other warpgroup has then read all but its latest tile in front of it: where a
+  // piece of an odd number of tiles ends, the next one begins with the same warpgroup, which
+  // leaves tile n - kKStages - 2 unread, and none before that (a warpgroup enters a piece once
+  // both have read all of the piece before). A piece's exponents are written after all S products
+  // of the piece before, so when both warpgroups have left the piece before that one's
+  // predecessor.
+  static constexpr int kScaleSlots = E4M3 ? 8 : 0;
+  static constexpr int kQExpSlots = E4M3 ? 4 : 0;
+  static_assert(!E4M3 || kScaleSlots >= kKStages + 3, "a slot is rewritten before it is read");
   static constexpr int kPieceOff = (kMiscOff + 16 + 15) / 16 * 16;
   static constexpr int kBytesOff = kPieceOff + 48 * kPieces;
   static constexpr int kScaleOff = kBytesOff + kTile * (2 * kCkStages + kCvStages);
-  static constexpr int kQExpOff = kScaleOff + 16 * kSlots;
-  static constexpr int kFactorOff = kQExpOff + kTile * kSlots;  // f16 factors of K's and V's rows
+  static constexpr int kQExpOff = kScaleOff + 16 * kScaleSlots;
+  static constexpr int kFactorOff = kQExpOff + kTile * kQExpSlots;  // f16 factors of K's and V's rows
   static constexpr int kXchOff = kFactorOff + (E4M3 ? 4 * kTile : 0);  // (m, l) per warpgroup and row
   // the plan's scratch is used before the exchange area is
   static constexpr int kPlanOff = kXchOff;
@@ -802,7 +807,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
     // below 2^-29 of it. (k is at most 60, which keeps the score's factor a normal number.)
     auto do_q = [&]() -> bool {
       if (!mbar_wait_warp(bars.q_full, q_cnt & 1, tmo, abort_flag)) return false;
-      int8_t* q_exp = reinterpret_cast<int8_t*>(smem + L::kQExpOff) + (q_cnt & (L::kSlots - 1u)) * kTile;
+      int8_t* q_exp = reinterpret_cast<int8_t*>(smem + L::kQExpOff) + (q_cnt & (L::kQExpSlots - 1u)) * kTile;
       const int r4 = lane >> 3, v = lane & 7;
 #pragma unroll 1
       for (int pass = 0; pass < 8; ++pass) {
@@ -866,7 +871,7 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         if (is_k && wx == 0) {
           const int ev = top_of(ld_shared_u32(sb + kTile), j, 127 - 60) - 127;  // V's, as V's warps find it
           if (lane == 0)
-            reinterpret_cast<float4*>(smem + L::kScaleOff)[tile & (L::kSlots - 1u)] =
+            reinterpret_cast<float4*>(smem + L::kScaleOff)[tile & (L::kScaleSlots - 1u)] =
                 make_float4(pow2i(top - 127), static_cast<float>(ev), pow2i(-ev), 0.f);
           ++tile;
         }
@@ -1288,8 +1293,8 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
         float c_t = c_log2, ev = 0.f, ev_inv = 1.f;
         if constexpr (E4M3) {
           if (n_done == 0)
-            c_row = c_log2 * pow2i(-static_cast<int>(q_exp[(q_cnt & (L::kSlots - 1u)) * kTile + t]));
-          const float4 z = tile_scale[(tile_cnt + p) & (L::kSlots - 1u)];
+            c_row = c_log2 * pow2i(-static_cast<int>(q_exp[(q_cnt & (L::kQExpSlots - 1u)) * kTile + t]));
+          const float4 z = tile_scale[(tile_cnt + p) & (L::kScaleSlots - 1u)];
           c_t = c_row * z.x;
           ev = z.y;
           ev_inv = z.z;
