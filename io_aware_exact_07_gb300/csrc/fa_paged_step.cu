@@ -39,6 +39,9 @@ namespace {
 constexpr int kGroup = 16;                  // keys of a product, which lie in one page
 constexpr int kMergeWarps = 8;
 constexpr int kSmemMax = 232448;
+// A multiple of 16 that no length reaches (they stay below 2^31 - 256), and from which a warp's
+// keys of a block can be counted on in 32 bits.
+constexpr unsigned kFarKey = 0x7FFFFF00u;
 
 template <int D, bool E4M3, int NT>
 struct StepL {
@@ -86,6 +89,7 @@ struct StepL {
   static constexpr int kPlanOff = kQOff + kQBytes;
   static constexpr int kSmemBytes = kPlanOff + 256;
   static_assert(kSmemBytes <= kSmemMax, "more shared memory than one CTA may hold");
+  static_assert(kChunk <= 0x7FFFFFFF - kFarKey, "keys of a step beyond 31 bits");
 };
 
 // Where unit `u` (16 bytes) of row `row` lies in a tile. The exclusive-or spreads the rows
@@ -155,7 +159,7 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& a, const PagedSeq& 
   Span r;
   const int lo = a.wl >= 0 ? s.len - s.nq - a.wl : 0;
   r.first = lo > 0 ? lo / kBlock : 0;
-  r.n = (s.len + kBlock - 1) / kBlock - r.first;
+  r.n = (s.len - 1) / kBlock + 1 - r.first;  // (len + kBlock - 1 may have 33 bits)
   if (r.n < 1) r.n = 1;
   if (s.nq <= 0) r.n = 0;
   return r;
@@ -292,7 +296,11 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   constexpr int kEs = E4M3 ? 1 : 2;
   const long long row_bytes = a.c.stride_row * kEs;
   Walk lw = cw;  // the block to load next
-  auto chunk_of = [&](const Walk& w) { return w.blk * kBlock + warp * kChunk; };
+  // First of the warp's keys of a block; those of the last one may begin beyond 31 bits.
+  auto chunk_of = [&](const Walk& w) {
+    const unsigned j = static_cast<unsigned>(w.blk) * kBlock + static_cast<unsigned>(warp * kChunk);
+    return static_cast<int>(min(j, kFarKey));
+  };
   int lpage[kU];  // pages of its groups
   auto find_pages = [&]() {
 #pragma unroll

@@ -48,3 +48,66 @@ def test_scales_that_differ_from_tile_to_tile(nq, kv, d):
         sync()
         assert np.all(np.abs(o.double().cpu().numpy() - o_ref) <= tol)
         assert np.abs(lse.double().cpu().numpy() - lse_ref).max() <= 2e-4
+
+
+# ------------------------------------------------------------------ the longest sequences
+
+class Longest:
+    """One sequence of 2^31 - 272 positions, the most that a table of whole pages can hold, over
+    four pages named many times: its first three pages hold values of -1, all others of +1. The
+    exact result follows from how often each page is named."""
+    page, entries = 144, 14913079
+
+    def __init__(self, d, e4m3, G, seed):
+        g = torch.Generator().manual_seed(seed)
+        self.L = self.page * self.entries
+        assert self.L == 2 ** 31 - 272
+        self.table = torch.randint(1, 4, (1, self.entries), generator=g, dtype=torch.int32)
+        self.table[0, :3] = 0
+        self.q = torch.randn((1, G, d), generator=g).to(torch.bfloat16)
+        rows = torch.randn((4 * self.page, 1, d), generator=g).to(torch.bfloat16)
+        vals = torch.ones((4, self.page, 1, d), dtype=torch.bfloat16)
+        vals[0] = -1
+        self.cache = fa.paged_cache(4, self.page, 1, d, e4m3=e4m3, device=DEV)
+        fill = torch.arange(4, dtype=torch.int32, device=DEV)[None]
+        n = torch.tensor([4 * self.page], dtype=torch.int32, device=DEV)
+        fa.paged_write(rows.to(DEV), vals.reshape(rows.shape).to(DEV), page_table=fill, kv_lens=n,
+                       **self.cache)
+        k, _ = fa.paged_read(page_table=fill, kv_lens=n, N=4 * self.page, **self.cache)
+        self.kv = torch.tensor([self.L], dtype=torch.int32, device=DEV)
+        s = self.q[0].double() @ k[0, 0].double().cpu().T / np.sqrt(d)       # [G, 4 pages' rows]
+        times = torch.bincount(self.table[0].long(), minlength=4).double().repeat_interleave(self.page)
+        w = times * s.exp()
+        sign = torch.ones(4 * self.page, dtype=torch.float64)
+        sign[:self.page] = -1
+        self.lse, self.o = w.sum(1).log(), (w * sign).sum(1) / w.sum(1)
+
+    def check(self, steps):
+        """Sums of `steps` terms in fp32, each addition off by at most 2^-23 of the sum (the tensor
+        cores may cut where others round): O, of values of magnitude 1, and lse."""
+        o, lse = fa.paged_attn(self.q.to(DEV), page_table=self.table.to(DEV), kv_lens=self.kv, max_q=1,
+                               causal=True, **self.cache)
+        sync()
+        tol = steps * 2.0 ** -23 + 2 * U
+        assert (o[0].double().cpu() - self.o[:, None]).abs().max().item() <= 2 * tol < 0.5
+        assert (lse[0].double().cpu() - self.lse).abs().max().item() <= tol
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G", [4, 16, 24])
+def test_longest_sequence_with_few_rows(G, d, e4m3):
+    # each warp of a CTA (8 of them at least) adds 16 keys at a time
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    Longest(d, e4m3, G, 61).check(2 ** 31 // 16 // 8 // sms + 1)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_new_row_at_the_last_position(e4m3):
+    z = Longest(64, e4m3, 1, 62)
+    new = torch.full((1, 1, 64), 0.5, dtype=torch.bfloat16, device=DEV)
+    fa.paged_write(new, -new, page_table=z.table.to(DEV), kv_lens=z.kv, **z.cache)
+    k, v = fa.paged_read(page_table=z.table[:, -1:].to(DEV), N=z.page,
+                         kv_lens=torch.tensor([z.page], dtype=torch.int32, device=DEV), **z.cache)
+    sync()
+    assert (k[0, 0, -1] == 0.5).all() and (v[0, 0, -1] == -0.5).all() and (v[0, 0, :-1] == 1).all()
