@@ -904,11 +904,14 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       int page, slot;
     };
     auto rows_of = [&](int j) {
-      const int pos = (j + (lane >> 3)) * kTile + (lane & 7) * 16;
+      // (unsigned: up to three tiles behind the sequence's last, which may lie beyond 31 bits)
+      const unsigned at = static_cast<unsigned>(j + (lane >> 3)) * kTile + (lane & 7) * 16;
       Rows r;
       r.page = args.c.num_pages;
-      r.slot = page_row(args.c, pos);
-      if (pos < pc.len) {
+      r.slot = 0;
+      if (at < static_cast<unsigned>(pc.len)) {
+        const int pos = static_cast<int>(at);
+        r.slot = page_row(args.c, pos);
         const int p = paged_page(args.c, pc.b, pos);
         if (p >= 0) r.page = p;
       }

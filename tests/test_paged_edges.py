@@ -111,3 +111,11 @@ def test_new_row_at_the_last_position(e4m3):
                          kv_lens=torch.tensor([z.page], dtype=torch.int32, device=DEV), **z.cache)
     sync()
     assert (k[0, 0, -1] == 0.5).all() and (v[0, 0, -1] == -0.5).all() and (v[0, 0, :-1] == 1).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_longest_sequence_with_many_rows(d, e4m3):
+    # a CTA's two warpgroups take key tiles of 128 in turn, in 8 products of 16 keys each
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    Longest(d, e4m3, 32, 63).check(2 ** 31 // 16 // 2 // sms + 8)
