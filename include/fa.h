@@ -295,9 +295,10 @@ fa_status fa_paged_read(const void* k_pages, const void* v_pages, const uint8_t*
  * position p of a sequence of length L sees keys j < L, with causal j <= p, and with
  * window_left >= 0 only j >= p - window_left. Writes o (bf16 [T, H, d], contiguous,
  * 16-byte aligned; not overlapping q) and lse (fp32 [T, H], natural log); a row that sees no
- * key gets O = 0 and lse = -inf. Cached rows of positions below a sequence's length are
- * expected to be finite (a NaN or an infinity there may reach every new token of the sequence);
- * what lies behind the length, in the same page too, does not matter.
+ * key gets O = 0 and lse = -inf; a NaN in a row of q makes that row's O and lse NaN. Cached rows
+ * of positions below a sequence's length are expected to be finite (a NaN or an infinity there may
+ * reach every new token of the sequence; a NaN in a key makes O and lse NaN for the rows that see
+ * it); what lies behind the length, in the same page too, does not matter.
  *   max_q: the largest number of new tokens of one sequence (a bound on it is enough).
  *   workspace: fa_paged_workspace_size(H, H_kv, d, max_q, max_pages * page_size) bytes,
  *   16-byte aligned (NULL where that is 0); its contents on entry do not matter. Calls that

@@ -1480,12 +1480,13 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
       const float m1 = g ? m_ref : other.x, l1 = g ? l_sum : other.y;
       const bool has0 = nt > 0, has1 = nt > 1;  // O_g was written
       const float m = fmaxf(m0, m1);
-      const float a0 = (l0 > 0.f) ? ex2_approx(m0 - m) : 0.f;
-      const float a1 = (l1 > 0.f) ? ex2_approx(m1 - m) : 0.f;
+      // l is 0 where no key was seen, and a NaN stays one
+      const float a0 = (l0 == 0.f) ? 0.f : ex2_approx(m0 - m);
+      const float a1 = (l1 == 0.f) ? 0.f : ex2_approx(m1 - m);
       const float l = a0 * l0 + a1 * l1;
-      const float inv = (l > 0.f) ? 1.f / l : 0.f;
+      const float inv = (l == 0.f) ? 0.f : 1.f / l;
       const float w0 = a0 * inv, w1 = a1 * inv;
-      const float lse2 = (l > 0.f) ? m + __log2f(l) : -INFINITY;  // log2 units
+      const float lse2 = (l == 0.f) ? -INFINITY : m + __log2f(l);  // log2 units
       const Piece pc = read_piece(count);
       const int head = pc.h * args.G;  // the tile's first query head
       const bool direct = pc.from_start && pc.ends;
@@ -1629,7 +1630,8 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
 // Merge of the pieces of a query tile that runs' ends have cut, a warp per row: with lse_s
 // and the normalised O_s of piece s, O = sum_s 2^(lse_s - m) O_s / sum_s 2^(lse_s - m), m =
 // max_s lse_s, in the order of the pieces. Blocks (c, ..) take the tile that CTA c's run
-// began and did not end.
+// began and did not end. A piece whose lse is a NaN takes no part in the maximum, and makes
+// the sums NaN.
 constexpr int kMergeWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
@@ -1673,13 +1675,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     load_part<kPer>(a.o_part + row_of(i) * D + lane * kPer, part);
     add(a.lse_part[row_of(i)], part);
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = den == 0.f ? 0.f : 1.f / den;
   const int t = r / G;
   const long long row = static_cast<long long>(hd.row0 + t) * a.H + hd.h * G + (r - t * G);
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + row * D + lane * kPer);
   dst[0] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
   if constexpr (kPer == 4) dst[1] = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-  if (lane == 0) a.lse[row] = den > 0.f ? (m + __log2f(den)) * kLn2 : -INFINITY;
+  if (lane == 0) a.lse[row] = den == 0.f ? -INFINITY : (m + __log2f(den)) * kLn2;
 }
 
 namespace {

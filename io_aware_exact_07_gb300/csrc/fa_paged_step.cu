@@ -789,9 +789,9 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
           y[2] += k * v.z;
           y[3] += k * v.w;
         }
-        // e4m3: l is 2^-64 of the sum
-        const float inv = l > 0.f ? (E4M3 ? 1.f / l * pow2i(-64) : 1.f / l) : 0.f;
-        const float lse2 = l > 0.f ? m + __log2f(l) + (E4M3 ? 64.f : 0.f) : -INFINITY;  // log2
+        // l is 0 for a row that sees no key, and a NaN stays one. e4m3: l is 2^-64 of the sum
+        const float inv = l == 0.f ? 0.f : (E4M3 ? 1.f / l * pow2i(-64) : 1.f / l);
+        const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l) + (E4M3 ? 64.f : 0.f);  // log2
         if (direct) {
           const int t = r / G;
           const long long row = static_cast<long long>(cw.s.t0 + t) * a.H + cw.h * G + (r - t * G);
@@ -836,7 +836,8 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
 // Merge of the pieces of a head that runs' ends have cut: with lse_s and the normalised O_s
 // of piece s, O = sum_s 2^(lse_s - m) O_s / sum_s 2^(lse_s - m), m = max_s lse_s. Block (c, r)
 // takes query row r of the head that CTA c's run began and did not end; the next CTAs'
-// pieces follow until one ends it. In the order of the pieces, so always the same result.
+// pieces follow until one ends it. In the order of the pieces, so always the same result. A
+// piece whose lse is a NaN takes no part in the maximum, and makes the sums NaN.
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_step_merge_kernel(const PagedAttnArgs a, int ctas,
                                                                        int rows) {
@@ -894,8 +895,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_step_merge_kernel(c
     }
     const int t = r / G;
     const long long row = static_cast<long long>(hd.row0 + t) * a.H + hd.h * G + (r - t * G);
-    a.o[row * D + tid] = __float2bfloat16(l > 0.f ? y / l : 0.f);
-    if (tid == 0) a.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    a.o[row * D + tid] = __float2bfloat16(l == 0.f ? 0.f : y / l);
+    if (tid == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
   }
 }
 

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import io_aware_exact_07_gb300 as fa
-from _paged import Batch
+from _paged import Batch, check_attn
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -119,3 +119,43 @@ def test_longest_sequence_with_many_rows(d, e4m3):
     # a CTA's two warpgroups take key tiles of 128 in turn, in 8 products of 16 keys each
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     Longest(d, e4m3, 32, 63).check(2 ** 31 // 16 // 2 // sms + 8)
+
+
+# ------------------------------------------------------------------ NaN
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("nq,kv,Hkv", [
+    ([1, 1], [300, 170], 2),         # whole heads
+    ([3, 1], [9000, 12345], 2),      # heads cut between CTAs
+    ([60, 33], [300, 170], 2),       # whole query tiles
+    ([300], [9001], 1),              # cut ones
+])
+def test_a_nan_in_a_query_is_a_nan_in_its_row(nq, kv, Hkv, d, e4m3):
+    b = Batch(nq, kv, 32, Hkv, d, e4m3, G=2, seed=71)
+    ref = b.oracle(True)
+    hit = torch.zeros(b.q.shape[:2], dtype=torch.bool)
+    for t, h, c in ((0, 1, 5), (b.T - 1, 0, d - 1), (b.T // 2, b.H - 1, 0)):
+        b.q[t, h, c] = float("nan")
+        hit[t, h] = True
+    x = b.fill().on(DEV)
+    o, lse = attn(b, x, causal=True, max_q=max(nq))
+    sync()
+    o, lse = o.cpu(), lse.cpu()
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    keep = ~hit.numpy()
+    check_attn(o[~hit], lse[~hit], tuple(r[keep] for r in ref))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("nq,kv", [([1, 1], [300, 170]), ([1, 1], [20001, 170]),
+                                   ([60, 33], [300, 170]), ([60, 33], [9001, 170])])
+def test_a_nan_in_a_key_is_a_nan_in_the_rows_that_see_it(nq, kv, e4m3):
+    b = Batch(nq, kv, 16, 1, 64, e4m3, G=2, seed=72)
+    ref = b.oracle(True)
+    b.rows["k"][0][5, 0, 3] = float("nan")
+    x = b.fill().on(DEV)
+    o, lse = attn(b, x, causal=True, max_q=max(nq))
+    sync()
+    assert torch.isnan(o[:nq[0]]).all() and torch.isnan(lse[:nq[0]]).all()
+    check_attn(o[nq[0]:], lse[nq[0]:], tuple(r[nq[0]:] for r in ref))
