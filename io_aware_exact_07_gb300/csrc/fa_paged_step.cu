@@ -148,6 +148,19 @@ __device__ __forceinline__ int ld_shared_u8(uint32_t saddr) {
   return static_cast<int>(r);
 }
 
+// The factor 2^x, x <= 0, of a softmax sum, and of the products with V that go with it. The
+// maxima of a quantised cache count V's scales, its sums do not: 2^x may be below 2^-126 and
+// still leave something of a sum, so there it is applied in two halves.
+template <bool HALVES>
+struct Factor {
+  float part;
+  __device__ __forceinline__ explicit Factor(float x) : part(ex2_approx(HALVES ? 0.5f * x : x)) {}
+  __device__ __forceinline__ float all() const { return HALVES ? part * part : part; }
+  __device__ __forceinline__ float of(float sum) const {
+    return HALVES ? sum * part * part : sum * part;
+  }
+};
+
 // Key blocks [first, first + n) of a sequence that hold a key some new token sees: with a
 // sliding window the first token sees the lowest. A sequence with new tokens has at least
 // one block (its rows have to be written), one without has none.
@@ -557,8 +570,12 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
       // ---- scores in log2 units, masks, running maximum, P. e4m3: keys g8 and g8 + 8 have K's
       // scale, V's exponent, and what takes V's scale out of the sum (times 2^-64, so that the
       // sum stays in range for the smallest scales; a scale byte of 0, which only a page that
-      // is none has, counts as 127).
+      // is none has, counts as 127). A weight that falls below 2^-126 because of its V scale is
+      // lost to O, where it does not count, but would be lost to the sum as well. With V scales of
+      // 2^-57 at least that is 2^-69 of the sum at most, which is 2^-64 or more; with smaller ones
+      // among the step's (`wide`) the sum has exponentials of its own.
       float v_inv[kU][2];
+      bool wide = false;
 #pragma unroll
       for (int g = 0; g < kU; ++g) {
         float k_scale[2] = {1.f, 1.f}, v_exp[2] = {0.f, 0.f};
@@ -572,6 +589,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
             k_scale[e] = kb == kScaleNaN ? __uint_as_float(0x7FC00000u) : pow2i(min(kb, kScaleMax + 127) - 127);
             v_exp[e] = static_cast<float>(vb - 127);
             v_inv[g][e] = pow2i(127 - 64 - vb);
+            wide |= vb < 127 - 57;
           }
         }
 #pragma unroll
@@ -580,6 +598,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
           for (int e = 0; e < 4; ++e)
             s[g][n][e] = (s[g][n][e] + s2[g][n][e]) * (c_row[n][e & 1] * k_scale[e >> 1]) + v_exp[e >> 1];
       }
+      if constexpr (E4M3) wide = __any_sync(0xffffffffu, wide);
       constexpr float kLift = E4M3 ? kF16Lift : 0.f;
       const int last_lo = a.wl >= 0 ? cw.s.len - 1 - a.wl : 0;  // first key of the last token
       const int first_hi = a.causal ? pos0 + 1 : cw.s.len;      // end of the first token's keys
@@ -619,9 +638,10 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
             const float m_new = fmaxf(m_ref[n][e], mx - kLift);
-            const float alpha = m_new == -INFINITY ? 1.f : ex2_approx(m_ref[n][e] - m_new);
+            const Factor<E4M3> f(m_new == -INFINITY ? 0.f : m_ref[n][e] - m_new);
+            const float alpha = f.all();
             m_ref[n][e] = m_new;
-            l_sum[n][e] *= alpha;
+            l_sum[n][e] = f.of(l_sum[n][e]);
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
               o[n][x][e] *= alpha;
@@ -641,8 +661,19 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
             p[e] = ex2_approx(s[g][n][e] - (m == -INFINITY ? 0.f : m));
           }
           if constexpr (E4M3) {
-            l_sum[n][0] = fmaf(p[0], v_inv[g][0], fmaf(p[2], v_inv[g][1], l_sum[n][0]));
-            l_sum[n][1] = fmaf(p[1], v_inv[g][0], fmaf(p[3], v_inv[g][1], l_sum[n][1]));
+            if (!wide) {
+              l_sum[n][0] = fmaf(p[0], v_inv[g][0], fmaf(p[2], v_inv[g][1], l_sum[n][0]));
+              l_sum[n][1] = fmaf(p[1], v_inv[g][0], fmaf(p[3], v_inv[g][1], l_sum[n][1]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float m = m_ref[n][e & 1];
+                const float x = s[g][n][e] - (m == -INFINITY ? 0.f : m);
+                // -log2 of v_inv is V's exponent and 64
+                const int k = 127 - static_cast<int>(__float_as_uint(v_inv[g][e >> 1]) >> 23);
+                l_sum[n][e & 1] += ex2_approx(x - static_cast<float>(k));
+              }
+            }
           } else {
             l_sum[n][0] += p[0] + p[2];
             l_sum[n][1] += p[1] + p[3];
@@ -747,9 +778,10 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
               if (r < M) {
                 const float2 z = ml[warp * L::kRows + r];
                 const float m = fmaxf(m_ref[n][e], z.x), mu = m == -INFINITY ? 0.f : m;
-                const float k0 = ex2_approx(m_ref[n][e] - mu), k1 = ex2_approx(z.x - mu);
+                const Factor<E4M3> f0(m_ref[n][e] - mu), f1(z.x - mu);
+                const float k0 = f0.all(), k1 = f1.all();
                 m_ref[n][e] = m;
-                l_sum[n][e] = k0 * l_sum[n][e] + k1 * z.y;
+                l_sum[n][e] = f0.of(l_sum[n][e]) + f1.of(z.y);
                 const float* src = merge + (warp * L::kRows + r) * L::kPitch;
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
@@ -781,8 +813,9 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
 #pragma unroll
         for (int w = 0; w < L::kStates; ++w) {
           const float2 z = ml[w * L::kRows + r];
-          const float k = ex2_approx(z.x - mu);
-          l += k * z.y;
+          const Factor<E4M3> f(z.x - mu);
+          const float k = f.all();
+          l += f.of(z.y);
           const float4 v = *reinterpret_cast<const float4*>(merge + (w * L::kRows + r) * L::kPitch + d0);
           y[0] += k * v.x;
           y[1] += k * v.y;

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import io_aware_exact_07_gb300 as fa
+import oracle
 from _paged import Batch, check_attn
 
 pytestmark = pytest.mark.gpu
@@ -159,3 +160,39 @@ def test_a_nan_in_a_key_is_a_nan_in_the_rows_that_see_it(nq, kv, e4m3):
     sync()
     assert torch.isnan(o[:nq[0]]).all() and torch.isnan(lse[:nq[0]]).all()
     check_attn(o[nq[0]:], lse[nq[0]:], tuple(r[nq[0]:] for r in ref))
+
+
+# ------------------------------------------------------------------ the ends of the range of scales
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("order", ["small first", "large first", "mixed"])
+@pytest.mark.parametrize("nq,kv", [([1, 1], [600, 90]), ([4, 3], [600, 90]), ([8, 5], [600, 90]),
+                                   ([2, 1], [20001, 90]), ([60, 33], [600, 90])])
+def test_values_of_both_ends_of_the_range_of_scales(nq, kv, order, d):
+    # V's rows have the smallest scale, 2^-117, and the largest, 2^6 (or any between): the softmax
+    # sum counts all keys alike, also those whose weight times value scale is 2^-126 of the largest
+    # or less, as scores of up to 4 sqrt(d) make it. P's rounding to f16 adds 2^-32 of the row's
+    # largest weight times value scale, once a key, and f16 tiles 2^-25 of the scale. Scores are
+    # four times those of check_attn, and their fp32 errors: 8e-4, 20 % of 2^-8.
+    b = Batch(nq, kv, 16, 2, d, True, G=2, seed=81)
+    g = torch.Generator().manual_seed(81)
+    for i, L in enumerate(kv):
+        b.rows["k"][i] *= 4
+        e = torch.full((L, 1, 1), -116.0)
+        if order == "mixed":
+            e = torch.randint(-116, 14, (L, 1, 1), generator=g).float()
+        elif order == "small first":
+            e[L * 3 // 4::37] = 13
+        else:
+            e[:L // 4:37] = 13
+        v = b.rows["v"][i].double().clamp(-3.4, 3.4) * torch.exp2(e.double())
+        b.rows["v"][i] = v.to(torch.bfloat16)
+    x = b.fill().on(DEV)
+    scales = oracle.quantize_rows(b.rows["v"][0].double().numpy())[1].astype(int) - 127
+    assert scales.min() == -117 and scales.max() >= 5
+    o, lse = attn(b, x, causal=True, max_q=max(nq))
+    sync()
+    o_ref, lse_ref, o_abs = b.oracle(True)
+    tol = 1.2 * U * (o_abs + np.abs(o_ref)) + 448 * 2.0 ** 7 * (max(kv) * 2.0 ** -32 + 2.0 ** -25)
+    assert np.abs(lse.double().cpu().numpy() - lse_ref).max() <= 8e-4
+    assert np.all(np.abs(o.double().cpu().numpy() - o_ref) <= tol)
