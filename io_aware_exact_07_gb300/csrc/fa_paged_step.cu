@@ -822,19 +822,22 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
           y[2] += k * v.z;
           y[3] += k * v.w;
         }
-        // l is 0 for a row that sees no key, and a NaN stays one. e4m3: l is 2^-64 of the sum
-        const float inv = l == 0.f ? 0.f : (E4M3 ? 1.f / l * pow2i(-64) : 1.f / l);
+        // l is 0 for a row that sees no key, and a NaN stays one. e4m3: l is 2^-64 of the sum,
+        // which 1 / l makes good last: it may be 2^-92 alone, with values of 2^-117
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = E4M3 ? y[k] * inv * pow2i(-64) : y[k] * inv;
         const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l) + (E4M3 ? 64.f : 0.f);  // log2
         if (direct) {
           const int t = r / G;
           const long long row = static_cast<long long>(cw.s.t0 + t) * a.H + cw.h * G + (r - t * G);
           *reinterpret_cast<uint2*>(a.o + row * D + d0) = make_uint2(
-              pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv));
+              pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
           if (d0 == 0) a.lse[row] = lse2 * kLn2;
         } else {
           const long long row = (2ll * blockIdx.x + slot) * L::kRows + r;
           *reinterpret_cast<float4*>(a.o_part + row * D + d0) =
-              make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+              make_float4(y[0], y[1], y[2], y[3]);
           if (d0 == 0) a.lse_part[row] = lse2;
         }
       }

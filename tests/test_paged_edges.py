@@ -196,3 +196,28 @@ def test_values_of_both_ends_of_the_range_of_scales(nq, kv, order, d):
     tol = 1.2 * U * (o_abs + np.abs(o_ref)) + 448 * 2.0 ** 7 * (max(kv) * 2.0 ** -32 + 2.0 ** -25)
     assert np.abs(lse.double().cpu().numpy() - lse_ref).max() <= 8e-4
     assert np.all(np.abs(o.double().cpu().numpy() - o_ref) <= tol)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,B", [(1, 200), (16, 200), (24, 200), (4, 3)])
+def test_smallest_values_under_large_sums(G, B, d):
+    # a head's first 384 keys have a score of 0, the others one of 5.5 (7.9 in log2 units, just less
+    # than moves the maximum); all its values are 1.5 * 2^-112, so O is that
+    n, page = 30000, 16
+    c = fa.paged_cache(n // page, page, 1, d, e4m3=True, device=DEV)
+    k = torch.full((n, 1, d), 0.6875 * 64 / d)
+    k[:384] = 0
+    v = torch.full((n, 1, d), 1.5 * 2.0 ** -112)
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV).expand(B, -1).contiguous()
+    kv = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    fa.paged_write(k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV), page_table=table[:1],
+                   kv_lens=kv[:1], **c)
+    q = torch.ones(B, G, d, dtype=torch.bfloat16, device=DEV)
+    o, lse = fa.paged_attn(q, page_table=table, kv_lens=kv, max_q=1, scale=0.125, **c)
+    sync()
+    exact = float(v[0, 0, 0])
+    # O is off by its rounding, 2^-8 of it, P's weights by 2^-11, and 30000 additions in fp32 by less
+    # than 2^-9
+    assert (o.double() / exact - 1).abs().max().item() <= 2.0 ** -8 + 2.0 ** -9 + 2.0 ** -10
+    lse_ref = np.log(384 + (n - 384) * np.exp(5.5))
+    assert (lse.double() - lse_ref).abs().max().item() <= 2e-4 + 2.0 ** -9
