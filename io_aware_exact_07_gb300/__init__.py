@@ -15,6 +15,7 @@ quantised to e4m3 (``paged_cache`` allocates one).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -173,6 +174,29 @@ def _stream(stream=None):
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _memory_on(stream, dev):
+    """Context in which tensors are made for a call on `stream` of device `dev` (None: the current
+    one). Memory that torch hands out is free in the order of the stream that is current then:
+    work queued earlier on another one may still use it."""
+    if stream is None:
+        return _HERE
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
+def _given_out(stream, dev, *tensors):
+    """Results made by _memory_on(stream, dev) will be used on the current stream too: once the
+    caller drops them, their memory waits for the work queued there as well."""
+    if stream is not None:
+        here = torch.cuda.current_stream(dev)
+        for t in tensors:
+            t.record_stream(here)
 
 
 def _ptr(t):
@@ -678,16 +702,6 @@ def _call(name, dev, stream, block):
         raise FAError(status, name)
 
 
-def _used_on(stream, *tensors):
-    """Tell the allocator that tensors made here are used on a stream other than the
-    current one, so that their memory is not handed out again before that work is done."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
-
-
 @functools.lru_cache(maxsize=4096)
 def _paged_workspace_bytes(H, H_kv, d, max_q, max_keys, dev):
     with torch.cuda.device(dev):  # depends on the device's number of SMs
@@ -717,13 +731,13 @@ def paged_read(k_pages, v_pages, page_table, kv_lens, N, k_scale=None, v_scale=N
     seqlens_k=kv_lens."""
     head, batch, B, dev = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
     shape = (B, batch[0], N, batch[1])
-    k = k_pages.new_empty(shape, dtype=torch.bfloat16)
-    v = k_pages.new_empty(shape, dtype=torch.bfloat16)
+    with _memory_on(stream, dev):
+        k = k_pages.new_empty(shape, dtype=torch.bfloat16)
+        v = k_pages.new_empty(shape, dtype=torch.bfloat16)
     _call("fa_paged_read_block", dev, stream,
           _READ_BLOCK(k_pages.data_ptr(), v_pages.data_ptr(), _data(k_scale), _data(v_scale),
                       *head, *batch, B, N, k.data_ptr(), v.data_ptr()))
-    if stream is not None:
-        _used_on(stream, k, v)
+    _given_out(stream, dev, k, v)
     return k, v
 
 
@@ -742,8 +756,9 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
     qs = _new_rows("q", q, H, d, dev)
     cu, n = _offsets(cu_seqlens_q, B, T, max_q, dev)
     if out is None:
-        o = q.new_empty((T, H, d))
-        lse = q.new_empty((T, H), dtype=torch.float32)
+        with _memory_on(stream, dev):
+            o = q.new_empty((T, H, d))
+            lse = q.new_empty((T, H), dtype=torch.float32)
     else:
         o, lse = out
         if (o.dtype != torch.bfloat16 or o.shape != (T, H, d) or not o.is_contiguous()
@@ -755,12 +770,13 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
     if T == 0:
         return o, lse
     ws_bytes = _paged_workspace_bytes(H, Hkv, d, n, head[2] * batch[7], dev)
-    ws = q.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
+    with _memory_on(stream, dev):
+        ws = q.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
     _call("fa_paged_attn_block", dev, stream,
           _ATTN_BLOCK(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _data(k_scale),
                       _data(v_scale), o.data_ptr(), lse.data_ptr(), *head, H, *batch, cu, B, T, n,
                       qs, 1.0 / math.sqrt(d) if scale is None else scale, bool(causal),
                       min(window_left, 0x7FFFFFFF), _data(ws), ws_bytes))
-    if stream is not None:
-        _used_on(stream, *((o, lse, ws) if out is None else (ws,)))
+    if out is None:
+        _given_out(stream, dev, o, lse)
     return o, lse

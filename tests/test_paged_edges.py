@@ -221,3 +221,52 @@ def test_smallest_values_under_large_sums(G, B, d):
     assert (o.double() / exact - 1).abs().max().item() <= 2.0 ** -8 + 2.0 ** -9 + 2.0 ** -10
     lse_ref = np.log(384 + (n - 384) * np.exp(5.5))
     assert (lse.double() - lse_ref).abs().max().item() <= 2e-4 + 2.0 ** -9
+
+
+# ------------------------------------------------------------------ memory on another stream
+
+def handles(stream):
+    return stream, stream.cuda_stream
+
+
+@pytest.mark.parametrize("as_handle", [0, 1])
+def test_memory_that_the_current_stream_still_uses_is_not_taken(as_handle):
+    # a tensor of the results' size is dropped while a write to it waits behind a long kernel
+    b = Batch([1, 30], [700, 300], 16, 2, 64, G=2, seed=91)
+    x = b.fill().on(DEV)
+    side = torch.cuda.Stream()
+    call = dict(stream=handles(side)[as_handle])
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for _ in range(2):
+        torch.cuda._sleep(200_000_000)
+        late = [torch.empty(t.shape, dtype=t.dtype, device=DEV).fill_(9) for t in
+                (x.q, torch.empty(x.q.shape[:2]), torch.empty(2, 2, 700, 64, dtype=torch.bfloat16),
+                 torch.empty(2, 2, 700, 64, dtype=torch.bfloat16),
+                 torch.empty(fa.fa_paged_workspace_size(4, 2, 64, 30, 704), dtype=torch.uint8))]
+        del late
+        o, lse = attn(b, x, causal=True, max_q=30, **call)
+        k, v = fa.paged_read(x.k, x.v, x.table, x.kv, 700, **call)
+        sync()
+        check_attn(o, lse, b.oracle(True))
+        for n, got in (("k", k), ("v", v)):
+            assert np.array_equal(got[0].double().cpu().numpy(), np.moveaxis(b.stored(n, 0), 0, 1))
+
+
+@pytest.mark.parametrize("as_handle", [0, 1])
+def test_results_dropped_while_the_current_stream_reads_them(as_handle):
+    b = Batch([1, 30], [700, 300], 16, 2, 64, G=2, seed=92)
+    x = b.fill().on(DEV)
+    side = torch.cuda.Stream()
+    call = dict(stream=handles(side)[as_handle])
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    o, lse = attn(b, x, causal=True, max_q=30, **call)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(200_000_000)
+    got = o.clone(), lse.clone()
+    del o, lse
+    for _ in range(3):  # would write over them, had their memory been handed out again
+        fa.paged_attn(-x.q, x.k, x.v, x.table, x.kv, cu_seqlens_q=x.cu, max_q=30, **call)
+    sync()
+    check_attn(*got, b.oracle(True))
