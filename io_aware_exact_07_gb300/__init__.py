@@ -186,7 +186,9 @@ def _memory_on(stream, dev):
     if stream is None:
         return _HERE
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        # (torch knows CUDA's handle 1, cudaStreamLegacy, as stream 0 only)
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=dev)
     return torch.cuda.stream(stream)
 
 
@@ -478,8 +480,9 @@ def fwd(q, k, v, scale=None, causal=False, dropout_p=0.0, seed=0, offset=0, bloc
     Hkv = _kv_heads(q, k, v)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    with _memory_on(stream, q.device):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     if tuple(window) != (-1, -1):
         st = fa_fwd_window(q, k, v, o, lse, B, H, Hkv, N, d, scale, causal, window[0], window[1],
                            dropout_p, seed, offset, block_mask, seqlens_k, stream)
@@ -490,6 +493,7 @@ def fwd(q, k, v, scale=None, causal=False, dropout_p=0.0, seed=0, offset=0, bloc
         st = fa_fwd_gqa(q, k, v, o, lse, B, H, Hkv, N, d, scale, causal, dropout_p, seed, offset,
                         block_mask, seqlens_k, stream)
     _check(st, "fa_fwd")
+    _given_out(stream, q.device, o, lse)
     return o, lse
 
 
@@ -503,10 +507,11 @@ def bwd(q, k, v, o, dout, lse, scale=None, causal=False, dropout_p=0.0, seed=0, 
     Hkv = _kv_heads(q, k, v)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ws_bytes = fa_bwd_workspace_size(B, H, N, d)
-    if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    with _memory_on(stream, q.device):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        if workspace is None:
+            workspace = torch.empty(fa_bwd_workspace_size(B, H, N, d), dtype=torch.uint8,
+                                    device=q.device)
     if tuple(window) != (-1, -1):
         st = fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, B, H, Hkv, N, d, scale, causal,
                            window[0], window[1], dropout_p, seed, offset, block_mask, seqlens_k,
@@ -519,6 +524,7 @@ def bwd(q, k, v, o, dout, lse, scale=None, causal=False, dropout_p=0.0, seed=0, 
                         dropout_p, seed, offset, block_mask, seqlens_k, workspace,
                         workspace.numel(), stream)
     _check(st, "fa_bwd")
+    _given_out(stream, q.device, dq, dk, dv)
     return dq, dk, dv
 
 
@@ -535,12 +541,14 @@ def decode(q, k_cache, v_cache, scale=None, causal=False, seqlens_k=None, num_ct
         raise ValueError("k_cache and v_cache must be [B, H_kv, Nk, d] like q's B and d")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     ws_bytes = fa_decode_workspace_size(B, H, Hkv, Nq, Nk, d, num_ctas)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
+    with _memory_on(stream, q.device):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
     _check(fa_decode(q, k_cache, v_cache, o, lse, B, H, Hkv, Nq, Nk, d, scale, causal, seqlens_k,
                      num_ctas, ws, ws_bytes, stream, window_left), "fa_decode")
+    _given_out(stream, q.device, o, lse)
     return o, lse
 
 
@@ -553,14 +561,15 @@ def fp8_quantize(q, k, v, signs=None, stream=None):
     B, H, N, d = q.shape
     dev = q.device
     Np = fa_fp8_vt_stride(N)
-    out = dict(q8=torch.empty((B, H, N, d), dtype=torch.uint8, device=dev),
-               k8=torch.empty((B, Hkv, N, d), dtype=torch.uint8, device=dev),
-               vt8=torch.empty((B, Hkv, d, Np), dtype=torch.uint8, device=dev),
-               s_q=torch.empty((B, H), dtype=torch.float32, device=dev),
-               s_k=torch.empty((B, Hkv), dtype=torch.float32, device=dev),
-               s_v=torch.empty((B, Hkv, d), dtype=torch.float32, device=dev))
     wsb = fa_fp8_workspace_size(B, H, d)
-    ws = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
+    with _memory_on(stream, dev):
+        out = dict(q8=torch.empty((B, H, N, d), dtype=torch.uint8, device=dev),
+                   k8=torch.empty((B, Hkv, N, d), dtype=torch.uint8, device=dev),
+                   vt8=torch.empty((B, Hkv, d, Np), dtype=torch.uint8, device=dev),
+                   s_q=torch.empty((B, H), dtype=torch.float32, device=dev),
+                   s_k=torch.empty((B, Hkv), dtype=torch.float32, device=dev),
+                   s_v=torch.empty((B, Hkv, d), dtype=torch.float32, device=dev))
+        ws = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
     if Hkv == H:
         st = fa_fp8_quantize(q, k, v, signs, B, H, N, d, out["q8"], out["k8"], out["vt8"],
                              out["s_q"], out["s_k"], out["s_v"], ws, wsb, stream)
@@ -568,6 +577,7 @@ def fp8_quantize(q, k, v, signs=None, stream=None):
         st = fa_fp8_quantize_gqa(q, k, v, signs, B, H, Hkv, N, d, out["q8"], out["k8"],
                                  out["vt8"], out["s_q"], out["s_k"], out["s_v"], ws, wsb, stream)
     _check(st, "fa_fp8_quantize")
+    _given_out(stream, dev, *out.values())
     return out
 
 
@@ -576,14 +586,17 @@ def fwd_fp8(qz, scale, causal=False, seqlens_k=None, stream=None):
     fp8_quantize; returns (o bf16, lse)."""
     B, H, N, d = qz["q8"].shape
     Hkv = qz["k8"].shape[1]
-    o = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=qz["q8"].device)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=qz["q8"].device)
+    dev = qz["q8"].device
+    with _memory_on(stream, dev):
+        o = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
     args = (qz["q8"], qz["k8"], qz["vt8"], qz["s_q"], qz["s_k"], qz["s_v"], o, lse)
     if Hkv == H:
         st = fa_fwd_fp8(*args, B, H, N, d, scale, causal, seqlens_k, stream)
     else:
         st = fa_fwd_fp8_gqa(*args, B, H, Hkv, N, d, scale, causal, seqlens_k, stream)
     _check(st, "fa_fwd_fp8")
+    _given_out(stream, dev, o, lse)
     return o, lse
 
 

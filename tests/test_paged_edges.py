@@ -270,3 +270,15 @@ def test_results_dropped_while_the_current_stream_reads_them(as_handle):
         fa.paged_attn(-x.q, x.k, x.v, x.table, x.kv, cu_seqlens_q=x.cu, max_q=30, **call)
     sync()
     check_attn(*got, b.oracle(True))
+
+
+@pytest.mark.parametrize("handle", [0, 1, 2])  # the default stream, and CUDA's two handles for it
+def test_default_streams_by_their_handles(handle):
+    b = Batch([1, 30], [700, 300], 16, 2, 64, G=2, seed=93)
+    x = b.fill().on(DEV)
+    torch.cuda.synchronize()
+    o, lse = attn(b, x, causal=True, max_q=30, stream=handle)
+    k, _ = fa.paged_read(x.k, x.v, x.table, x.kv, 700, stream=handle)
+    sync()
+    check_attn(o, lse, b.oracle(True))
+    assert np.array_equal(k[0].double().cpu().numpy(), np.moveaxis(b.stored("k", 0), 0, 1))
