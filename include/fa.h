@@ -256,11 +256,13 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
  *     sequence: token i of n sits at position kv_lens[b] - n + i. Rows from cu[B] on
  *     are neither read nor written. NULL: max_q rows each, T = B * max_q.
  * What lies on the device is checked there, before any access: offsets out of order
- * or beyond T, a length outside [0, max_pages * page_size], a page number outside
- * [0, num_pages) and, for fa_paged_attn, a sequence with more than max_q new tokens.
- * Each is reported as FA_ERR_INVALID_ARG by fa_device_status; such a page reads as
- * zeros and is not written, such a length counts as 0 and such a sequence has no
- * new tokens. Pages that two sequences share are fine to read; where a write's
+ * or beyond T, a length outside [0, max_pages * page_size], the number of a page that
+ * the call reads or writes outside [0, num_pages) and, for fa_paged_attn, a sequence
+ * with more than max_q new tokens. Each is reported as FA_ERR_INVALID_ARG by
+ * fa_device_status (a call with T = 0 looks at nothing); such a page reads as zeros and
+ * is not written, such a length counts as 0 and such a sequence has no new tokens. Where
+ * offsets out of order give a token to several sequences, it may be taken for any of
+ * them or for none. Pages that two sequences share are fine to read; where a write's
  * positions lead to the same row of a page twice, one of the two stays. */
 typedef enum { FA_CACHE_BF16 = 0, FA_CACHE_E4M3 = 1 } fa_cache_type;
 

@@ -47,13 +47,20 @@ __device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, uint64_t ff) 
 // One warp takes rows of one token: D / 8 lanes hold a row (16 bytes each), so a pass covers
 // 2 (d = 128) or 4 (d = 64) of the token's 2 Hkv rows (K's heads, then V's). The rows of all
 // PASSES passes are loaded first, so that they and the chain of loads that finds their place
-// (offsets, length, page table) are in flight together.
+// (offsets, length, page table) are in flight together. The blocks from `blocks` on take no
+// rows: their threads look over a sequence each, since offsets and lengths out of range are to be
+// reported where no token leads to them too.
 template <int D, bool E4M3, int PASSES>
-__global__ void __launch_bounds__(kIoWarps * 32) fa_paged_write_kernel(const PagedWriteArgs a,
-                                                                       int warps_per_token) {
+__global__ void __launch_bounds__(kIoWarps * 32)
+    fa_paged_write_kernel(const PagedWriteArgs a, int warps_per_token, unsigned blocks) {
   constexpr int kLanes = D / 8;
   constexpr int kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31;
+  if (blockIdx.x >= blocks) {
+    const unsigned b = (blockIdx.x - blocks) * (kIoWarps * 32) + threadIdx.x;
+    if (b < static_cast<unsigned>(a.c.B)) paged_seq(a.c, static_cast<int>(b));
+    return;
+  }
   const long long task = static_cast<long long>(blockIdx.x) * kIoWarps + (threadIdx.x >> 5);
   const int t = static_cast<int>(task / warps_per_token);
   const int sub = static_cast<int>(task - static_cast<long long>(t) * warps_per_token);
@@ -193,9 +200,11 @@ cudaError_t launch_write(const PagedWriteArgs& a, cudaStream_t stream) {
   constexpr int kRows = PASSES * 256 / D;  // rows of a warp
   const int warps_per_token = (2 * a.c.Hkv + kRows - 1) / kRows;
   const long long blocks = (static_cast<long long>(a.c.T) * warps_per_token + kIoWarps - 1) / kIoWarps;
-  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  const long long checks = (a.c.B + kIoWarps * 32ll - 1) / (kIoWarps * 32);
+  if (blocks + checks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   fa_paged_write_kernel<D, E4M3, PASSES>
-      <<<static_cast<unsigned>(blocks), kIoWarps * 32, 0, stream>>>(a, warps_per_token);
+      <<<static_cast<unsigned>(blocks + checks), kIoWarps * 32, 0, stream>>>(
+          a, warps_per_token, static_cast<unsigned>(blocks));
   return cudaGetLastError();
 }
 

@@ -282,3 +282,51 @@ def test_default_streams_by_their_handles(handle):
     sync()
     check_attn(o, lse, b.oracle(True))
     assert np.array_equal(k[0].double().cpu().numpy(), np.moveaxis(b.stored("k", 0), 0, 1))
+
+
+# ------------------------------------------------------------------ reported from the device
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("cu,kv,stored", [
+    # offsets, lengths; the new tokens (of 6) of each sequence that enter its last positions
+    ([0, 3, 6], [200, 130], ((0, 3), (3, 6))),      # nothing wrong
+    ([0, 3, 1000], [200, 130], ((0, 3), None)),
+    ([0, 3, 7], [200, 130], ((0, 3), None)),
+    ([0, -2, 6], [200, 130], (None, None)),
+    ([-1, 3, 6], [200, 130], (None, (3, 6))),
+    ([0, 6, 1000], [200, 130], ((0, 6), None)),     # no token leads to the second sequence ...
+    ([0, 6, 5], [200, 130], ((0, 5), None)),
+    ([0, 6, 6], [200, -1], ((0, 6), None)),
+    ([0, 0, 6], [10 ** 6, 130], (None, (0, 6))),    # ... or to the first
+    ([0, 3, 6], [200, 10 ** 6], ((0, 3), None)),
+    ([0, 3, 6], [-5, 130], (None, (3, 6))),
+])
+def test_what_a_write_reports_and_stores(cu, kv, stored, e4m3):
+    b = Batch([3, 3], [200, 130], 16, 2, 64, e4m3, G=2, seed=101)
+    old = {n: b.fill().pages[n].clone() for n in "kv"}
+    old_scale = {n: b.scale[n].clone() if e4m3 else None for n in "kv"}
+    x = b.on(DEV)
+    new = {n: (b.new[n].float() * 0.25 + 8).to(torch.bfloat16) for n in "kv"}
+    for i, rows in enumerate(stored):
+        if rows is None:
+            continue
+        n_seq = cu[i + 1] - cu[i] if cu[i + 1] > cu[i] else 0
+        for t in range(*rows):
+            pos = kv[i] - n_seq + t - cu[i]
+            at, row = oracle.paged_positions(b.table.numpy(), 16, i, np.array([pos]))
+            for n in "kv":
+                y = new[n][t]
+                if e4m3:
+                    codes, sc = oracle.quantize_rows(y.double().numpy())
+                    old_scale[n][at, :, row] = torch.from_numpy(sc)[None]
+                    y = torch.from_numpy(codes)
+                old[n][at, :, row] = y[None]
+    as_int = lambda z: torch.tensor(z, dtype=torch.int32, device=DEV)
+    fa.paged_write(new["k"].to(DEV), new["v"].to(DEV), x.k, x.v, x.table, as_int(kv),
+                   cu_seqlens_q=as_int(cu), **x.sc)
+    torch.cuda.synchronize()
+    wrong = (cu, kv) != ([0, 3, 6], [200, 130])
+    assert fa.fa_device_status(clear=True) == (fa.FA_ERR_INVALID_ARG if wrong else fa.FA_OK)
+    for n, got in (("k", x.k), ("v", x.v)):
+        assert torch.equal(got.cpu(), old[n])
+        assert not e4m3 or torch.equal(x.sc[n + "_scale"].cpu(), old_scale[n])
