@@ -262,14 +262,16 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
  * fa_device_status (a call with T = 0 looks at nothing); such a page reads as zeros and
  * is not written, such a length counts as 0 and such a sequence has no new tokens. Where
  * offsets out of order give a token to several sequences, it may be taken for any of
- * them or for none. Pages that two sequences share are fine to read; where a write's
- * positions lead to the same row of a page twice, one of the two stays. */
+ * them or for none. Pages that two sequences share are fine to read. Where a
+ * write's positions lead to the same row of a page several times, the row ends up as a
+ * mixture: each 16 bytes of a bf16 row, each 8 codes and the scale byte of a quantised one,
+ * come from any of the tokens. */
 typedef enum { FA_CACHE_BF16 = 0, FA_CACHE_E4M3 = 1 } fa_cache_type;
 
 /* Stores k_new and v_new into the pages at their positions. k_new, v_new: bf16 [T,
  * H_kv, d], token t at t * k_stride and t * v_stride (elements, multiples of 8), heads
  * and d contiguous, 16-byte aligned. Tokens at negative positions (a length below the
- * number of new tokens) are not stored. Deterministic.
+ * number of new tokens) are not stored. Deterministic, but for rows written several times.
  * Errors: FA_ERR_INVALID_ARG (null or unaligned pointers, sizes, strides),
  * FA_ERR_UNSUPPORTED (d, type, page_size not a multiple of 16), FA_ERR_CUDA.
  * Asynchronous on `stream`; nothing is allocated. T = 0 is allowed and does nothing. */

@@ -330,3 +330,30 @@ def test_what_a_write_reports_and_stores(cu, kv, stored, e4m3):
     for n, got in (("k", x.k), ("v", x.v)):
         assert torch.equal(got.cpu(), old[n])
         assert not e4m3 or torch.equal(x.sc[n + "_scale"].cpu(), old_scale[n])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_rows_that_two_sequences_write(e4m3):
+    # the second half of every sequence's page is shared by pairs: what each unit of such a row
+    # holds comes from one of the two, all other rows are as written
+    B, Hkv, d, page, n = 64, 4, 128, 16, 16
+    g = torch.Generator().manual_seed(111)
+    new = torch.randn((B * n, Hkv, d), generator=g).to(torch.bfloat16)
+    table = torch.stack([torch.arange(B, dtype=torch.int32), torch.arange(B, dtype=torch.int32) // 2 + B], 1)
+    c = fa.paged_cache(B + B // 2, page, Hkv, d, e4m3=e4m3, device=DEV)
+    kv = torch.full((B,), 24, dtype=torch.int32, device=DEV)  # positions 8 .. 23
+    fa.paged_write(new.to(DEV), -new.to(DEV), page_table=table.to(DEV), kv_lens=kv, **c)
+    sync()
+    for name, x in (("k", new), ("v", -new)):
+        got = c[name + "_pages"].cpu()
+        want = x.reshape(B, n, Hkv, d).transpose(1, 2)  # [B, Hkv, tokens, d]
+        if e4m3:
+            want, sc = (torch.from_numpy(t) for t in oracle.quantize_rows(want.double().numpy()))
+            got_sc = c[name + "_scale"].cpu()
+            assert torch.equal(got_sc[:B, :, 8:], sc[:, :, :8])
+            pair = sc[:, :, 8:].reshape(B // 2, 2, Hkv, 8)
+            assert ((got_sc[B:, :, :8] == pair[:, 0]) | (got_sc[B:, :, :8] == pair[:, 1])).all()
+        assert torch.equal(got[:B, :, 8:], want[:, :, :8])
+        pair = want[:, :, 8:].reshape(B // 2, 2, Hkv, 8, d // 8, 8)
+        units = got[B:, :, :8].reshape(B // 2, Hkv, 8, d // 8, 8)
+        assert ((units == pair[:, 0]).all(-1) | (units == pair[:, 1]).all(-1)).all()
