@@ -357,3 +357,30 @@ def test_rows_that_two_sequences_write(e4m3):
         pair = want[:, :, 8:].reshape(B // 2, 2, Hkv, 8, d // 8, 8)
         units = got[B:, :, :8].reshape(B // 2, Hkv, 8, d // 8, 8)
         assert ((units == pair[:, 0]).all(-1) | (units == pair[:, 1]).all(-1)).all()
+
+
+# ------------------------------------------------------------------ the C mirrors
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("nq", [[1, 2], [40, 9]])
+def test_calls_with_caller_owned_buffers(nq, e4m3):
+    # fa_paged_write, _attn and _read as the C entry points take their arguments
+    b = Batch(nq, [700, 130], 16, 2, 64, e4m3, G=2, seed=121)
+    x = b.fill(upto=[L - n for L, n in zip(b.kv, nq)]).on(DEV)
+    P, Hkv, page, d = x.k.shape
+    scales = (x.sc["k_scale"], x.sc["v_scale"])
+    cache = (int(e4m3), P, page)
+    rest = (Hkv, d, *x.k.stride()[:3], x.table, x.table.stride(0), x.table.shape[1], x.kv)
+    assert fa.fa_paged_write(x.k_new, x.v_new, x.k, x.v, *scales, *cache, *rest, x.cu, 2, b.T,
+                             max(nq), Hkv * d, Hkv * d) == fa.FA_OK
+    o, lse = torch.empty_like(x.q), torch.empty(x.q.shape[:2], device=DEV)
+    size = fa.fa_paged_workspace_size(b.H, Hkv, d, max(nq), x.table.shape[1] * page)
+    ws = torch.empty(max(size, 1), dtype=torch.uint8, device=DEV)
+    assert fa.fa_paged_attn(x.q, x.k, x.v, *scales, o, lse, *cache, b.H, *rest, x.cu, 2, b.T,
+                            max(nq), b.H * d, d ** -0.5, True, -1, ws, size) == fa.FA_OK
+    k, v = (torch.empty((2, Hkv, 700, d), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    assert fa.fa_paged_read(x.k, x.v, *scales, *cache, *rest, 2, 700, k, v) == fa.FA_OK
+    sync()
+    check_attn(o, lse, b.oracle(True))
+    for n, got in (("k", k), ("v", v)):
+        assert np.array_equal(got[0].double().cpu().numpy(), np.moveaxis(b.stored(n, 0), 0, 1))
