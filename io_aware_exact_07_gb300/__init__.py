@@ -760,7 +760,7 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
     sequence b are rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] (T / B each without
     cu_seqlens_q); max_q bounds their number (T where it is not given: pass it, since up to 24
     rows H / H_kv * max_q run on a kernel of their own). Returns (o [T, H, d] bf16, lse [T, H] fp32); rows that
-    belong to no sequence are not written. out = (o, lse) gives the buffers."""
+    belong to no sequence are not written. out = (o, lse) gives the buffers (not over q)."""
     head, batch, B, dev = _paged_batch(k_pages, v_pages, page_table, kv_lens, k_scale, v_scale)
     Hkv, d = batch[0], batch[1]
     if q.dim() != 3:
@@ -778,8 +778,10 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
                 or lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()
                 or o.get_device() != dev or lse.get_device() != dev):
             raise ValueError(f"out must be contiguous: bf16 [{T}, {H}, {d}] and fp32 [{T}, {H}]")
-        if o.data_ptr() == q.data_ptr() and T > 0:
-            raise ValueError("out may not be q: rows of q are read after others of o are written")
+        qp, op, lp = q.data_ptr(), o.data_ptr(), lse.data_ptr()
+        q_end = qp + 2 * ((T - 1) * qs + H * d)
+        if T > 0 and (qp < op + 2 * T * H * d and op < q_end or qp < lp + 4 * T * H and lp < q_end):
+            raise ValueError("out may not overlap q: rows of q are read after others are written")
     if T == 0:
         return o, lse
     ws_bytes = _paged_workspace_bytes(H, Hkv, d, n, head[2] * batch[7], dev)

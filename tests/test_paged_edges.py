@@ -359,6 +359,29 @@ def test_rows_that_two_sequences_write(e4m3):
         assert ((units == pair[:, 0]).all(-1) | (units == pair[:, 1]).all(-1)).all()
 
 
+# ------------------------------------------------------------------ outputs over q
+
+def test_outputs_over_a_part_of_q_are_refused():
+    b = Batch([1, 2], [20, 5], 16, 2, 64, G=2, seed=131)
+    x = b.fill().on(DEV)
+    n = x.q.numel()
+    flat = torch.empty(4 * n, dtype=torch.bfloat16, device=DEV)
+    q = flat[n:2 * n].view(x.q.shape).copy_(x.q)
+    lse = torch.empty(x.q.shape[:2], device=DEV)
+    call = dict(page_table=x.table, kv_lens=x.kv, cu_seqlens_q=x.cu, max_q=2, causal=True)
+    for at in (n // 2, n - 8, n, n + 8, 2 * n - 8):
+        with pytest.raises(ValueError):
+            fa.paged_attn(q, x.k, x.v, out=(flat[at:at + n].view(q.shape), lse), **call)
+    with pytest.raises(ValueError):
+        over = flat[n:n + 2 * lse.numel()].view(torch.float32).view(lse.shape)
+        fa.paged_attn(q, x.k, x.v, out=(torch.empty_like(q), over), **call)
+    for at in (0, 2 * n):   # next to it
+        out = flat[at:at + n].view(q.shape), lse
+        fa.paged_attn(q, x.k, x.v, out=out, **call)
+        sync()
+        check_attn(*out, b.oracle(True))
+
+
 # ------------------------------------------------------------------ the C mirrors
 
 @pytest.mark.parametrize("e4m3", [False, True])
