@@ -42,6 +42,14 @@ constexpr int kSmemMax = 232448;
 // A multiple of 16 that no length reaches (they stay below 2^31 - 256), and from which a warp's
 // keys of a block can be counted on in 32 bits.
 constexpr unsigned kFarKey = 0x7FFFFF00u;
+// A quantised cache's maxima count V's scales (2^-117 .. 2^7), its sums do not: a weight may be
+// 2^-133 of the largest and still count for 2^-9 of the sum. So weights are computed times 2^kUp,
+// which fp32 has room for above the 2^15 of f16; only what is below 2^-49 of the sum then falls
+// below 2^-126. (Exponentials of their own for keys with small scales, behind a test in every
+// step, cost 2 to 4 % with 9 rows and more, this 1 %.) The sum is held times 2^-kDown: its terms
+// are 2^132 at most (a weight of 2^15 with a scale of 2^-117), a row's largest is 1 at least, and
+// 2^31 of them stay in range.
+constexpr int kUp = 40, kDown = 40;
 
 template <int D, bool E4M3, int NT>
 struct StepL {
@@ -568,14 +576,9 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
         }
       }
       // ---- scores in log2 units, masks, running maximum, P. e4m3: keys g8 and g8 + 8 have K's
-      // scale, V's exponent, and what takes V's scale out of the sum (times 2^-64, so that the
-      // sum stays in range for the smallest scales; a scale byte of 0, which only a page that
-      // is none has, counts as 127). A weight that falls below 2^-126 because of its V scale is
-      // lost to O, where it does not count, but would be lost to the sum as well. With V scales of
-      // 2^-57 at least that is 2^-69 of the sum at most, which is 2^-64 or more; with smaller ones
-      // among the step's (`wide`) the sum has exponentials of its own.
+      // scale, V's exponent, and what takes V's scale out of the sum (a scale byte of 0, which
+      // only a page that is none has, counts as 127).
       float v_inv[kU][2];
-      bool wide = false;
 #pragma unroll
       for (int g = 0; g < kU; ++g) {
         float k_scale[2] = {1.f, 1.f}, v_exp[2] = {0.f, 0.f};
@@ -588,8 +591,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
             vb = vb == 0 ? 127 : min(vb, kScaleMax + 127);
             k_scale[e] = kb == kScaleNaN ? __uint_as_float(0x7FC00000u) : pow2i(min(kb, kScaleMax + 127) - 127);
             v_exp[e] = static_cast<float>(vb - 127);
-            v_inv[g][e] = pow2i(127 - 64 - vb);
-            wide |= vb < 127 - 57;
+            v_inv[g][e] = pow2i(127 - kUp - kDown - vb);
           }
         }
 #pragma unroll
@@ -598,7 +600,6 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
           for (int e = 0; e < 4; ++e)
             s[g][n][e] = (s[g][n][e] + s2[g][n][e]) * (c_row[n][e & 1] * k_scale[e >> 1]) + v_exp[e >> 1];
       }
-      if constexpr (E4M3) wide = __any_sync(0xffffffffu, wide);
       constexpr float kLift = E4M3 ? kF16Lift : 0.f;
       const int last_lo = a.wl >= 0 ? cw.s.len - 1 - a.wl : 0;  // first key of the last token
       const int first_hi = a.causal ? pos0 + 1 : cw.s.len;      // end of the first token's keys
@@ -658,22 +659,14 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float m = m_ref[n][e & 1];
-            p[e] = ex2_approx(s[g][n][e] - (m == -INFINITY ? 0.f : m));
+            p[e] = ex2_approx(s[g][n][e] - (m == -INFINITY ? 0.f : E4M3 ? m - kUp : m));
           }
           if constexpr (E4M3) {
-            if (!wide) {
-              l_sum[n][0] = fmaf(p[0], v_inv[g][0], fmaf(p[2], v_inv[g][1], l_sum[n][0]));
-              l_sum[n][1] = fmaf(p[1], v_inv[g][0], fmaf(p[3], v_inv[g][1], l_sum[n][1]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float m = m_ref[n][e & 1];
-                const float x = s[g][n][e] - (m == -INFINITY ? 0.f : m);
-                // -log2 of v_inv is V's exponent and 64
-                const int k = 127 - static_cast<int>(__float_as_uint(v_inv[g][e >> 1]) >> 23);
-                l_sum[n][e & 1] += ex2_approx(x - static_cast<float>(k));
-              }
-            }
+            l_sum[n][0] = fmaf(p[0], v_inv[g][0], fmaf(p[2], v_inv[g][1], l_sum[n][0]));
+            l_sum[n][1] = fmaf(p[1], v_inv[g][0], fmaf(p[3], v_inv[g][1], l_sum[n][1]));
+            const uint64_t down = f2_pack(pow2i(-kUp), pow2i(-kUp));
+            f2_unpack(f2_mul(f2_pack(p[0], p[1]), down), p[0], p[1]);
+            f2_unpack(f2_mul(f2_pack(p[2], p[3]), down), p[2], p[3]);
           } else {
             l_sum[n][0] += p[0] + p[2];
             l_sum[n][1] += p[1] + p[3];
@@ -822,12 +815,12 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
           y[2] += k * v.z;
           y[3] += k * v.w;
         }
-        // l is 0 for a row that sees no key, and a NaN stays one. e4m3: l is 2^-64 of the sum,
-        // which 1 / l makes good last: it may be 2^-92 alone, with values of 2^-117
+        // l is 0 for a row that sees no key, and a NaN stays one. e4m3: l is 2^-kDown of the sum,
+        // which is made good last (1 / l alone may be as small as 2^-123)
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = E4M3 ? y[k] * inv * pow2i(-64) : y[k] * inv;
-        const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l) + (E4M3 ? 64.f : 0.f);  // log2
+        for (int k = 0; k < 4; ++k) y[k] = E4M3 ? y[k] * inv * pow2i(-kDown) : y[k] * inv;
+        const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l) + (E4M3 ? kDown : 0);  // log2
         if (direct) {
           const int t = r / G;
           const long long row = static_cast<long long>(cw.s.t0 + t) * a.H + cw.h * G + (r - t * G);
