@@ -750,7 +750,8 @@ def paged_read(k_pages, v_pages, page_table, kv_lens, N, k_scale=None, v_scale=N
     _call("fa_paged_read_block", dev, stream,
           _READ_BLOCK(k_pages.data_ptr(), v_pages.data_ptr(), _data(k_scale), _data(v_scale),
                       *head, *batch, B, N, k.data_ptr(), v.data_ptr()))
-    _given_out(stream, dev, k, v)
+    if stream is not None:
+        _given_out(stream, dev, k, v)
     return k, v
 
 
@@ -768,11 +769,13 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
     T, H = q.shape[0], q.shape[1]
     qs = _new_rows("q", q, H, d, dev)
     cu, n = _offsets(cu_seqlens_q, B, T, max_q, dev)
-    if out is None:
-        with _memory_on(stream, dev):
+    ws_bytes = _paged_workspace_bytes(H, Hkv, d, n, head[2] * batch[7], dev) if T > 0 else 0
+    with _memory_on(stream, dev):
+        if out is None:
             o = q.new_empty((T, H, d))
             lse = q.new_empty((T, H), dtype=torch.float32)
-    else:
+        ws = q.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
+    if out is not None:
         o, lse = out
         if (o.dtype != torch.bfloat16 or o.shape != (T, H, d) or not o.is_contiguous()
                 or lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()
@@ -784,14 +787,11 @@ def paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q=None, max_
             raise ValueError("out may not overlap q: rows of q are read after others are written")
     if T == 0:
         return o, lse
-    ws_bytes = _paged_workspace_bytes(H, Hkv, d, n, head[2] * batch[7], dev)
-    with _memory_on(stream, dev):
-        ws = q.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
     _call("fa_paged_attn_block", dev, stream,
           _ATTN_BLOCK(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _data(k_scale),
                       _data(v_scale), o.data_ptr(), lse.data_ptr(), *head, H, *batch, cu, B, T, n,
                       qs, 1.0 / math.sqrt(d) if scale is None else scale, bool(causal),
                       min(window_left, 0x7FFFFFFF), _data(ws), ws_bytes))
-    if out is None:
+    if stream is not None and out is None:
         _given_out(stream, dev, o, lse)
     return o, lse
