@@ -407,3 +407,29 @@ def test_calls_with_caller_owned_buffers(nq, e4m3):
     check_attn(o, lse, b.oracle(True))
     for n, got in (("k", k), ("v", v)):
         assert np.array_equal(got[0].double().cpu().numpy(), np.moveaxis(b.stored(n, 0), 0, 1))
+
+
+@pytest.mark.parametrize("as_handle", [0, 1])
+def test_a_forked_stream_inside_a_capture(as_handle):
+    # outputs and workspace come from the graph's memory, also on a stream that joined its capture
+    b = Batch([1, 30], [700, 300], 16, 2, 64, G=2, seed=94)
+    x = b.fill().on(DEV)
+    side = torch.cuda.Stream()
+    call = dict(stream=handles(side)[as_handle])
+    attn(b, x, causal=True, max_q=30)
+    torch.cuda.synchronize()
+    q = x.q.clone()
+    x.q.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        o, lse = attn(b, x, causal=True, max_q=30, **call)
+        k, _ = fa.paged_read(x.k, x.v, x.table, x.kv, 700, **call)
+        torch.cuda.current_stream().wait_stream(side)
+    x.q.copy_(q)
+    for _ in range(3):
+        fa.paged_attn(-q, x.k, x.v, x.table, x.kv, cu_seqlens_q=x.cu, max_q=30)
+        g.replay()
+        sync()
+        check_attn(o, lse, b.oracle(True))
+        assert np.array_equal(k[0].double().cpu().numpy(), np.moveaxis(b.stored("k", 0), 0, 1))
