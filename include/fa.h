@@ -247,9 +247,9 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
  *     bytes 135 to 254 are never written; they count as 134.
  *   page_size: a multiple of 16; d: 64 or 128.
  * The batch, B sequences (device pointers):
- *   page_table: int32, row b at b * table_stride; its entry i < max_pages names the
- *     page of positions i * page_size .. of sequence b. Entries past a sequence's
- *     length are not read. max_pages * page_size < 2^31 - 256.
+ *   page_table: int32, row b at b * table_stride (at least max_pages); its entry i <
+ *     max_pages names the page of positions i * page_size .. of sequence b. Entries past a
+ *     sequence's length are not read. max_pages * page_size < 2^31 - 256.
  *   kv_lens: int32 [B], the length of each sequence, its new tokens included.
  *   cu_seqlens_q: int32 [B + 1], new tokens of sequence b are rows cu[b] .. cu[b+1]
  *     of the T packed token rows (none is possible), the last positions of the

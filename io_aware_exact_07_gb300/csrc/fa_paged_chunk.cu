@@ -26,12 +26,13 @@
 // weight of zero would not hide a NaN.
 //
 // Bounds: for chunks the tensor core (1024 cycles of products per 128 x 128 tile at d = 128, of
-// 1500 measured with a bf16 cache: 0.78 us a tile; each warpgroup's chain of scores, maximum,
-// exponentials and the handshakes with the products is the rest); with few rows HBM; from an
-// e4m3 cache (1.39 us a tile) the conversion, which takes registers, issue slots and bandwidth
-// of shared memory from the softmax (without it 1.21 us), and the chain that goes from a PV
-// product over the S that takes its place to the next P (with neither conversion nor
-// exponentials still 0.95 us).
+// 1500 measured with a bf16 cache; each warpgroup's chain of scores, maximum, exponentials and
+// the handshakes with the products is the rest); with few rows HBM; from an e4m3 cache the
+// conversion, which takes registers, issue slots and bandwidth of shared memory from the softmax,
+// and the chain that goes from a PV product over the S that takes its place to the next P. us a
+// tile and SM (8 K/V heads, 16 query tiles of 512 key tiles each): d = 128 bf16 0.83, e4m3 1.42
+// (when it took 1.39, without the conversion 1.21, without the exponentials too 0.95); d = 64
+// bf16 0.75, e4m3 1.05.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -56,7 +57,9 @@ struct ChunkL {
   // Registers per thread at launch, and as the warpgroups share them out afterwards.
   static constexpr int kRegsLaunch = E4M3 ? 96 : 168;
   // (e4m3, measured us per 128 x 128 tile and SM for softmax, aux, converters: d = 128 144, 64, 64
-  // 1.47, 160, 64, 48 1.49, 128, 64, 80 1.50; d = 64 160, 64, 48 1.05, 144, 64, 64 1.25.)
+  // 1.47, 160, 64, 48 1.49, 128, 64, 80 1.50; d = 64 160, 64, 48 1.05, 144, 64, 64 1.25. These and
+  // the comparisons below are from before later steps, which took 1.47 to 1.4.) At 96 registers the
+  // e4m3 kernels spill: 368 bytes of stores and 404 of loads at d = 128, 100 and 136 at d = 64.
   static constexpr int kRegsSoftmax = E4M3 ? (D == 64 ? 160 : 144) : 216;
   static constexpr int kRegsAux = E4M3 ? 64 : 72;   // producers and issuers
   static constexpr int kRegsConv = E4M3 ? (D == 64 ? 48 : 64) : 0;  // converters
@@ -1357,7 +1360,9 @@ __global__ void __launch_bounds__(ChunkL<D, E4M3>::kThreads, 1)
           return true;
         };
         // P = 2^(s * c_t + nm) of N scores, rounded to bf16 for the product (at most 2^-8 of each
-        // weight), or to f16 (2^-11, or 2^-32 of the largest where that is more); l keeps fp32.
+        // weight: its operands have one type, which is V's; a second product for what the rounding
+        // leaves would cost half as many again as there are), or to f16 (2^-11, or 2^-32 of the
+        // largest where that is more); l keeps fp32.
         auto weights = [&](const float* x, uint32_t* to) {
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {

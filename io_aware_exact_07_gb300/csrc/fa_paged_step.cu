@@ -12,12 +12,15 @@
 //    are the 16 rows, the query rows the 8 columns (1 to 3 times). With so few query rows
 //    the products are below what bounds the kernel (a 128-row tensor-memory tile would be
 //    three quarters empty, and its softmax walks all of it); keeping S and P in registers
-//    saves the handshakes that a short sequence cannot hide. From 17 rows on it is these
-//    products that bound it, at some 7 cycles each and SM. Here and with 128-row tiles, us, 24
-//    sequences, 8 K/V heads, 24 rows: d = 128, 8192 bf16 keys 138 and 132, 1024 keys 35 and 38,
-//    e4m3 122 and 147, 34 and 50; d = 64 79 and 82, 22 and 31, e4m3 86 and 107; 128 sequences
-//    of 200 keys 48 and 55, 4 of 3000 13 and 17 (e4m3 here since then 10 to 20 % less). 32 rows: 8192 keys 156 and 133, 1024 44 and 38,
-//    e4m3 160 and 148, d = 64 94 and 82, 128 of 200 keys 60 and 55.
+//    saves the handshakes that a short sequence cannot hide. With more rows the products, some
+//    7 cycles each and SM, come near what the bytes take, and e4m3 is bound by them and the
+//    conversion. us, and those of the bytes, 24 sequences of 8192 keys, 8 K/V heads, 16 and 24
+//    rows: d = 128 bf16 129 and 136 of 119, e4m3 92 and 112 of 60; d = 64 71 and 77 of 60, 61 and
+//    73 of 30. The border of 24 rows was measured when e4m3 took 10 to 20 % more than now; here and
+//    with 128-row tiles, 24 rows: d = 128, 8192 bf16 keys 138 and 132, 1024 keys 35 and 38, e4m3
+//    122 and 147, 34 and 50; d = 64 79 and 82, 22 and 31, e4m3 86 and 107; 128 sequences of 200
+//    keys 48 and 55, 4 of 3000 13 and 17. 32 rows: 8192 keys 156 and 133, 1024 44 and 38, e4m3 160
+//    and 148, d = 64 94 and 82, 128 of 200 keys 60 and 55.
 //  - The order of the columns d within a product is free as long as both operands share
 //    it: a thread takes the 16 bytes of a row that it can load at once.
 //  - e4m3 codes become f16 between shared memory and the product, which the hardware converts
@@ -63,7 +66,7 @@ struct StepL {
   // Groups of a warp's step. From codes to O a group is a long chain, of which a scheduler's
   // three warps hide too little: two at once overlap, and share the vote, the walk and the
   // waits. e4m3, 16 sequences of 16384 keys, 8 K/V heads, one and two groups: 4 rows, d = 128 94
-  // and 88 us, d = 64 71 and 59; 16 rows 135 and 112, 89 and 74; 24 rows 149 and 134, 105 and 87.
+  // and 88 us, d = 64 71 and 60; 16 rows 135 and 112, 89 and 74; 24 rows 149 and 134, 105 and 87.
   // (bf16, d = 64, whose bytes bound it, gains nothing; at d = 128 there is no room.)
   static constexpr int kU = E4M3 ? 2 : 1;
   static constexpr int kChunk = kU * kGroup;
@@ -671,8 +674,9 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
             l_sum[n][0] += p[0] + p[2];
             l_sum[n][1] += p[1] + p[3];
           }
-          // P is rounded to bf16 for the product (at most 2^-8 of each weight), or to f16 (2^-11,
-          // or 2^-32 of the largest weight where that is more); the sum keeps fp32
+          // P is rounded to bf16 for the product (at most 2^-8 of each weight: its operands have one
+          // type, which is V's), or to f16 (2^-11, or 2^-32 of the largest weight where that is
+          // more); the sum keeps fp32
           p0[g][n] = movmatrix_t(E4M3 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
           p1[g][n] = movmatrix_t(E4M3 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
         }
