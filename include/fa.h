@@ -139,6 +139,80 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
                         const uint8_t* block_mask, const int32_t* seqlens_k, void* workspace,
                         size_t workspace_bytes, void* stream);
 
+/* Attention of queries over keys of another length (cross attention to an encoder's states, or to
+ * a memory in front of the queries), with or without a learned bias by relative position, and
+ * its backward pass. (The cross-paper synthesis page on FlashAttention lists cross attention
+ * among the variants an IO-aware kernel should cover, section 5.)
+ *   q, o, dout, dq: bf16 [B, H, Nq, d]; k, v, dk, dv: bf16 [B, H_kv, Nk, d]; lse: fp32
+ *   [B, H, Nq]; contiguous, 16-byte aligned. Query head h attends with K/V head h / (H / H_kv).
+ *   Query i sits at position p = i + q_offset of the key axis (0: at key i; Nk - Nq: at the last
+ *   Nq positions). Key j is visible to it if j < seqlens_k[b] (Nk if null; clamped to [0, Nk]),
+ *   with causal j <= p, and p - window_left <= j <= p + window_right (-1: unbounded). A row that
+ *   sees no key gets O = 0, lse = -inf and no gradient. What K and V hold at and behind
+ *   seqlens_k[b], NaN and infinities too, does not matter; dK and dV are 0 there.
+ *   Dropout as in fa_fwd, with row index (b*H + h)*Nq + i.
+ *   rel_lines: null, or the bias of the scores as fa_rel_bias laid it out for H heads and these
+ *   rel_left and rel_right: key j gets the bias of distance j - p.
+ *   dtable: null, or fp32 [num_buckets, H], the gradient of the bias table: entry (n, h) is the
+ *   sum of dS of head h over the pairs whose distance maps to n (rel_map: as given to
+ *   fa_rel_bias; entries outside [0, num_buckets) take part in no sum). Written whole. Its sums
+ *   are fp32 within a tile pair's row or place and fp64 across them, and are taken with the D of
+ *   the unrounded O.
+ * Every output is deterministic. fa_bwd_cross runs the kernels of fa_bwd, and for dtable three
+ * more: row sums, the tiles near the diagonal, the sums by bucket. workspace:
+ * fa_bwd_cross_workspace_size(...) bytes (rel_grad: whether dtable is wanted), 16-byte aligned;
+ * its contents on entry do not matter; calls that may overlap need one each.
+ * Errors: FA_ERR_INVALID_ARG (as for fa_fwd and fa_bwd; Nq or Nk above 2^28, |q_offset| above
+ * 2^28, B*H_kv*Nk >= 2^31, a window bound below -1, a dtable without lines or map),
+ * FA_ERR_UNSUPPORTED (d, more than 65536 distances or buckets or 65535 heads with a bias),
+ * FA_ERR_WORKSPACE, FA_ERR_CUDA. Asynchronous on `stream`; nothing is allocated. */
+fa_status fa_fwd_cross(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                       int H, int H_kv, int Nq, int Nk, int d, float scale, int causal,
+                       int q_offset, int window_left, int window_right, float dropout_p,
+                       uint64_t seed, uint64_t offset, const int32_t* seqlens_k,
+                       const float* rel_lines, int rel_left, int rel_right, void* stream);
+size_t fa_bwd_cross_workspace_size(int B, int H, int Nq, int Nk, int d, int causal, int q_offset,
+                                   int rel_grad, int rel_left, int rel_right);
+fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* o,
+                       const void* dout, const float* lse, void* dq, void* dk, void* dv, int B,
+                       int H, int H_kv, int Nq, int Nk, int d, float scale, int causal,
+                       int q_offset, int window_left, int window_right, float dropout_p,
+                       uint64_t seed, uint64_t offset, const int32_t* seqlens_k,
+                       const float* rel_lines, int rel_left, int rel_right,
+                       const int32_t* rel_map, int num_buckets, float* dtable, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* A learned bias of the scores by relative position, in buckets of distances: key j gets
+ * table[map[clamp(j - p, -left, right) + left], h] from the query at position p in head h.
+ * fa_rel_bias lays it out for the attention calls, a line of fa_rel_line_length(left, right)
+ * floats per head, in log2 units (0 where left or right is out of range):
+ *   table: [num_buckets, H], fp32 (FA_TABLE_F32) or bf16 (FA_TABLE_BF16), contiguous, device;
+ *          finite or -inf (which hides the bucket's keys)
+ *   map:   int32 [left + right + 1], device: the bucket of distances -left .. right. An entry
+ *          outside [0, num_buckets) gives a bias of 0 and is reported as FA_ERR_INVALID_ARG by
+ *          fa_device_status.
+ *   lines: fp32 [H, fa_rel_line_length(left, right)], device
+ * A line holds the table's values as they were: lay it out again after the table changes.
+ * Errors: FA_ERR_INVALID_ARG (null or unaligned pointers, sizes below 1, left or right below 0),
+ * FA_ERR_UNSUPPORTED (left + right + 1 or num_buckets above 65536, H above 65535, type),
+ * FA_ERR_CUDA. Asynchronous on `stream`; nothing is allocated. */
+typedef enum { FA_TABLE_F32 = 0, FA_TABLE_BF16 = 1 } fa_table_type;
+int fa_rel_line_length(int left, int right);
+fa_status fa_rel_bias(const void* table, int table_type, const int32_t* map, int left, int right,
+                      int num_buckets, int H, float* lines, void* stream);
+
+/* Host helper: the usual map of distances to num_buckets buckets. Of half = num_buckets buckets
+ * (num_buckets / 2 if bidirectional: keys behind the query's position take the second half), the
+ * first half / 2 hold one distance each, the others share the distances up to max_distance by
+ * their logarithm: n >= e = half / 2 falls into min(half - 1, e + floor(log(n / e) /
+ * log(max_distance / e) * (half - e))), with the borders computed in whole numbers. Without
+ * bidirectional, keys behind the position count as distance 0. Writes the map of distances -left ..
+ * right to host memory (nothing if map_host is null) and left, and returns left + right + 1; 0
+ * if an argument is out of range (num_buckets odd with bidirectional or above 1024, half < 2,
+ * max_distance <= half / 2 or above 32767) or the map does not fit in `capacity` entries. */
+int fa_rel_buckets(int32_t* map_host, int capacity, int num_buckets, int max_distance,
+                   int bidirectional, int* left);
+
 /* The three stages fa_bwd runs, for callers that schedule or time them
  * separately. They must run in this order on one stream with the same
  * workspace (it carries D from the first stage to the other two); dK/dV and
@@ -220,6 +294,23 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
                     int B, int H, int H_kv, int Nq, int Nk, int d, float scale, int causal,
                     int window_left, const int32_t* seqlens_k, int num_ctas, void* workspace,
                     size_t workspace_bytes, void* stream);
+
+/* fa_decode with a bias by relative position: rel_lines as for fa_fwd_cross, row i of batch b at
+ * position L_b - Nq + i. What the caches hold at and behind L_b, NaN and infinities too, does not
+ * matter. Workspace and errors as fa_decode, plus FA_ERR_INVALID_ARG when rel_lines is null or Nk
+ * is above 2^28. */
+fa_status fa_decode_rel(const void* q, const void* k_cache, const void* v_cache, void* o,
+                        float* lse, int B, int H, int H_kv, int Nq, int Nk, int d, float scale,
+                        int causal, int window_left, const int32_t* seqlens_k,
+                        const float* rel_lines, int rel_left, int rel_right, int num_ctas,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* These calls with their arguments in a block, 8 bytes each in the order above but for the
+ * stream: pointers and integers as int64_t, scale and dropout_p as doubles (see
+ * fa_paged_attn_block). */
+fa_status fa_fwd_cross_block(const int64_t* args, void* stream);
+fa_status fa_bwd_cross_block(const int64_t* args, void* stream);
+fa_status fa_decode_rel_block(const int64_t* args, void* stream);
 
 /* Attention over a paged key/value cache. The page "FlashAttention — L3
  * Cross-Paper Synthesis" (section 3) names short-query attention over a cache,

@@ -9,7 +9,9 @@ the library is missing or fails to load, calls raise.
 
 ``fwd`` / ``bwd`` are conveniences that allocate the outputs (and the backward
 workspace) with torch and call ``fa_fwd`` / ``fa_bwd``; ``decode`` does the
-same for ``fa_decode`` (short query blocks over a K/V cache). ``paged_write``,
+same for ``fa_decode`` (short query blocks over a K/V cache). ``fwd`` and ``bwd``
+also take keys of another length than the queries (cross attention), and all three
+a learned bias by relative position (``rel_buckets``, ``rel_bias``). ``paged_write``,
 ``paged_read`` and ``paged_attn`` work on a cache held in pages, in bf16 or
 quantised to e4m3 (``paged_cache`` allocates one).
 """
@@ -22,6 +24,7 @@ import math
 import os
 import struct
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -38,11 +41,17 @@ FA_ERR_TIMEOUT = 5
 FA_CACHE_BF16 = 0
 FA_CACHE_E4M3 = 1
 
+FA_TABLE_F32 = 0
+FA_TABLE_BF16 = 1
+
 # Symbols declared in include/fa.h.
 EXPORTS = (
     "fa_fwd", "fa_bwd", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_window", "fa_bwd_window",
     "fa_bwd_workspace_size", "fa_bwd_preprocess",
     "fa_bwd_dkdv", "fa_bwd_dq", "fa_decode", "fa_decode_workspace_size",
+    "fa_fwd_cross", "fa_bwd_cross", "fa_bwd_cross_workspace_size", "fa_decode_rel",
+    "fa_fwd_cross_block", "fa_bwd_cross_block", "fa_decode_rel_block",
+    "fa_rel_line_length", "fa_rel_bias", "fa_rel_buckets",
     "fa_paged_write", "fa_paged_read", "fa_paged_attn", "fa_paged_workspace_size",
     "fa_paged_write_block", "fa_paged_read_block", "fa_paged_attn_block",
     "fa_fp8_workspace_size", "fa_fp8_vt_stride", "fa_fp8_quantize", "fa_fwd_fp8",
@@ -112,13 +121,30 @@ def load(build_if_missing: bool = False):
         lib.fa_decode_workspace_size.restype = sz
         lib.fa_decode.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp, i, vp, sz, vp]
         lib.fa_decode.restype = i
+        lib.fa_fwd_cross.argtypes = ([vp] * 5 + [i] * 6 + [f, i, i, i, i, f, u64, u64, vp, vp, i, i,
+                                                           vp])
+        lib.fa_fwd_cross.restype = i
+        lib.fa_bwd_cross_workspace_size.argtypes = [i] * 10
+        lib.fa_bwd_cross_workspace_size.restype = sz
+        lib.fa_bwd_cross.argtypes = ([vp] * 9 + [i] * 6 + [f, i, i, i, i, f, u64, u64, vp, vp, i, i,
+                                                           vp, i, vp, vp, sz, vp])
+        lib.fa_bwd_cross.restype = i
+        lib.fa_decode_rel.argtypes = ([vp] * 5 + [i] * 6 + [f, i, i, vp, vp, i, i, i, vp, sz, vp])
+        lib.fa_decode_rel.restype = i
+        lib.fa_rel_line_length.argtypes = [i, i]
+        lib.fa_rel_line_length.restype = i
+        lib.fa_rel_bias.argtypes = [vp, i, vp, i, i, i, i, vp, vp]
+        lib.fa_rel_bias.restype = i
+        lib.fa_rel_buckets.argtypes = [vp, i, i, i, i, ctypes.POINTER(i)]
+        lib.fa_rel_buckets.restype = i
         i64 = ctypes.c_int64
         cache = [i, i, i, i, i, i64, i64, i64, vp, i64, i, vp]  # type .. d, strides, table, lengths
         lib.fa_paged_write.argtypes = [vp] * 6 + cache + [vp, i, i, i, i64, i64, vp]
         lib.fa_paged_write.restype = i
         lib.fa_paged_read.argtypes = [vp] * 4 + cache + [i, i, vp, vp, vp]
         lib.fa_paged_read.restype = i
-        for f_block in (lib.fa_paged_write_block, lib.fa_paged_read_block, lib.fa_paged_attn_block):
+        for f_block in (lib.fa_paged_write_block, lib.fa_paged_read_block, lib.fa_paged_attn_block,
+                        lib.fa_fwd_cross_block, lib.fa_bwd_cross_block, lib.fa_decode_rel_block):
             f_block.argtypes = [ctypes.c_char_p, vp]
             f_block.restype = i
         lib.fa_paged_workspace_size.argtypes = [i, i, i, i, i]
@@ -177,6 +203,7 @@ def _stream(stream=None):
 
 
 _HERE = contextlib.nullcontext()
+_U64 = (1 << 64) - 1
 
 
 def _memory_on(stream, dev):
@@ -359,6 +386,76 @@ def fa_decode(q, k_cache, v_cache, o, lse, B, H, H_kv, Nq, Nk, d, scale, causal=
                             _stream(stream))
 
 
+def _seqlens_ptr(seqlens_k, B):
+    if seqlens_k is not None and (seqlens_k.dtype != torch.int32 or not seqlens_k.is_cuda
+                                  or not seqlens_k.is_contiguous()
+                                  or tuple(seqlens_k.shape) != (int(B),)):
+        raise ValueError(f"seqlens_k must be a contiguous int32 CUDA tensor [{int(B)}]")
+    return _ptr(seqlens_k)
+
+
+def fa_fwd_cross(q, k, v, o, lse, B, H, H_kv, Nq, Nk, d, scale, causal=False, q_offset=0,
+                 window_left=-1, window_right=-1, dropout_p=0.0, seed=0, offset=0, seqlens_k=None,
+                 rel_lines=None, rel_left=0, rel_right=0, stream=None) -> int:
+    return load().fa_fwd_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, H_kv, Nq, Nk,
+                               d, float(scale), int(bool(causal)), int(q_offset), int(window_left),
+                               int(window_right), float(dropout_p), int(seed), int(offset),
+                               _seqlens_ptr(seqlens_k, B), _ptr(rel_lines), int(rel_left),
+                               int(rel_right), _stream(stream))
+
+
+def fa_bwd_cross_workspace_size(B, H, Nq, Nk, d, causal=False, q_offset=0, rel_grad=False,
+                                rel_left=0, rel_right=0) -> int:
+    return int(load().fa_bwd_cross_workspace_size(B, H, Nq, Nk, d, int(bool(causal)), q_offset,
+                                                  int(bool(rel_grad)), rel_left, rel_right))
+
+
+def fa_bwd_cross(q, k, v, o, dout, lse, dq, dk, dv, B, H, H_kv, Nq, Nk, d, scale, causal=False,
+                 q_offset=0, window_left=-1, window_right=-1, dropout_p=0.0, seed=0, offset=0,
+                 seqlens_k=None, rel_lines=None, rel_left=0, rel_right=0, rel_map=None,
+                 num_buckets=0, dtable=None, workspace=None, workspace_bytes=0,
+                 stream=None) -> int:
+    return load().fa_bwd_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
+                               _ptr(dk), _ptr(dv), B, H, H_kv, Nq, Nk, d, float(scale),
+                               int(bool(causal)), int(q_offset), int(window_left),
+                               int(window_right), float(dropout_p), int(seed), int(offset),
+                               _seqlens_ptr(seqlens_k, B), _ptr(rel_lines), int(rel_left),
+                               int(rel_right), _ptr(rel_map), int(num_buckets), _ptr(dtable),
+                               _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def fa_decode_rel(q, k_cache, v_cache, o, lse, B, H, H_kv, Nq, Nk, d, scale, rel_lines, rel_left,
+                  rel_right, causal=False, window_left=-1, seqlens_k=None, num_ctas=0,
+                  workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load().fa_decode_rel(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(lse), B, H,
+                                H_kv, Nq, Nk, d, float(scale), int(bool(causal)),
+                                int(window_left), _seqlens_ptr(seqlens_k, B), _ptr(rel_lines),
+                                int(rel_left), int(rel_right), int(num_ctas), _ptr(workspace),
+                                int(workspace_bytes), _stream(stream))
+
+
+def fa_rel_line_length(left, right) -> int:
+    return int(load().fa_rel_line_length(int(left), int(right)))
+
+
+def fa_rel_bias(table, table_type, map, left, right, num_buckets, H, lines, stream=None) -> int:
+    return load().fa_rel_bias(_ptr(table), int(table_type), _ptr(map), int(left), int(right),
+                              int(num_buckets), H, _ptr(lines), _stream(stream))
+
+
+def fa_rel_buckets(num_buckets, max_distance, bidirectional=True):
+    """Host int32 map of distances -left .. right to buckets, and left."""
+    left = ctypes.c_int(0)
+    call = lambda t, n: load().fa_rel_buckets(t, n, int(num_buckets), int(max_distance),
+                                              int(bool(bidirectional)), ctypes.byref(left))
+    n = call(None, 0)
+    if n <= 0:
+        raise FAError(FA_ERR_INVALID_ARG, "fa_rel_buckets")
+    m = torch.empty(n, dtype=torch.int32)
+    call(ctypes.c_void_p(m.data_ptr()), n)
+    return m, left.value
+
+
 def fa_paged_write(k_new, v_new, k_pages, v_pages, k_scale, v_scale, type, num_pages, page_size,
                    H_kv, d, stride_page, stride_head, stride_row, page_table, table_stride,
                    max_pages, kv_lens, cu_seqlens_q, B, T, max_q, k_stride, v_stride,
@@ -471,11 +568,16 @@ def fa_test_inject_stall(mode: int) -> None:
 # ----------------------------------------------------------- conveniences
 
 def fwd(q, k, v, scale=None, causal=False, dropout_p=0.0, seed=0, offset=0, block_mask=None,
-        seqlens_k=None, stream=None, window=(-1, -1)):
+        seqlens_k=None, stream=None, window=(-1, -1), q_offset=0, rel_bias=None):
     """Allocate O and lse with torch and run fa_fwd (fa_fwd_gqa when k and v
     have fewer heads than q, fa_fwd_window when window = (left, right) is
-    set). Returns (o, lse)."""
+    set; fa_fwd_cross when k and v have another length, q_offset is the position of
+    the first query on the key axis, or rel_bias is a bias from rel_bias()).
+    Returns (o, lse)."""
     _check_qkv(q, k, v)
+    if rel_bias is not None or q_offset != 0 or k.shape[2] != q.shape[2]:
+        return _fwd_cross(q, k, v, scale, causal, dropout_p, seed, offset, block_mask, seqlens_k,
+                          stream, window, q_offset, rel_bias)
     B, H, N, d = q.shape
     Hkv = _kv_heads(q, k, v)
     if scale is None:
@@ -498,11 +600,17 @@ def fwd(q, k, v, scale=None, causal=False, dropout_p=0.0, seed=0, offset=0, bloc
 
 
 def bwd(q, k, v, o, dout, lse, scale=None, causal=False, dropout_p=0.0, seed=0, offset=0,
-        block_mask=None, seqlens_k=None, workspace=None, stream=None, window=(-1, -1)):
+        block_mask=None, seqlens_k=None, workspace=None, stream=None, window=(-1, -1), q_offset=0,
+        rel_bias=None, rel_grad=True):
     """Allocate dQ, dK, dV (and the workspace if not given) and run fa_bwd
     (fa_bwd_gqa when k and v have fewer heads than q, fa_bwd_window when
-    window = (left, right) is set)."""
+    window = (left, right) is set, fa_bwd_cross as fwd). With a rel_bias and rel_grad the
+    gradient of its table follows, fp32 [num_buckets, H]: (dq, dk, dv, dtable)."""
     _check_qkv(q, k, v, o, dout)
+    if rel_bias is not None or q_offset != 0 or k.shape[2] != q.shape[2]:
+        return _bwd_cross(q, k, v, o, dout, lse, scale, causal, dropout_p, seed, offset,
+                          block_mask, seqlens_k, workspace, stream, window, q_offset, rel_bias,
+                          rel_grad)
     B, H, N, d = q.shape
     Hkv = _kv_heads(q, k, v)
     if scale is None:
@@ -529,10 +637,10 @@ def bwd(q, k, v, o, dout, lse, scale=None, causal=False, dropout_p=0.0, seed=0, 
 
 
 def decode(q, k_cache, v_cache, scale=None, causal=False, seqlens_k=None, num_ctas=0,
-           stream=None, window_left=-1):
+           stream=None, window_left=-1, rel_bias=None):
     """Allocate O, lse (and the workspace, if the split needs one) with torch and
-    run fa_decode: q [B, H, Nq, d] over k_cache, v_cache [B, H_kv, Nk, d].
-    Returns (o, lse)."""
+    run fa_decode: q [B, H, Nq, d] over k_cache, v_cache [B, H_kv, Nk, d]
+    (fa_decode_rel with a bias from rel_bias()). Returns (o, lse)."""
     _check_qkv(q, k_cache, v_cache)
     B, H, Nq, d = q.shape
     _, Hkv, Nk, _ = k_cache.shape
@@ -541,6 +649,9 @@ def decode(q, k_cache, v_cache, scale=None, causal=False, seqlens_k=None, num_ct
         raise ValueError("k_cache and v_cache must be [B, H_kv, Nk, d] like q's B and d")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
+    if rel_bias is not None:
+        return _decode_rel(q, k_cache, v_cache, scale, causal, seqlens_k, num_ctas, stream,
+                           window_left, rel_bias)
     ws_bytes = fa_decode_workspace_size(B, H, Hkv, Nq, Nk, d, num_ctas)
     with _memory_on(stream, q.device):
         o = torch.empty_like(q)
@@ -597,6 +708,172 @@ def fwd_fp8(qz, scale, causal=False, seqlens_k=None, stream=None):
         st = fa_fwd_fp8_gqa(*args, B, H, Hkv, N, d, scale, causal, seqlens_k, stream)
     _check(st, "fa_fwd_fp8")
     _given_out(stream, dev, o, lse)
+    return o, lse
+
+
+# ------------------------------------------- other key lengths, relative position bias
+
+class RelBuckets(NamedTuple):
+    """A map of distances (key position minus query position) to rows of a bias table:
+    map, int32 on the GPU, holds the rows of distances -left, -left + 1, ..; what lies beyond
+    its ends counts as these."""
+    map: torch.Tensor
+    left: int
+    num_buckets: int
+
+    @property
+    def right(self) -> int:
+        return self.map.numel() - 1 - self.left
+
+
+class RelBias(NamedTuple):
+    """A bias table laid out for fwd, bwd and decode by rel_bias(). It holds the table's values
+    as they were then."""
+    lines: torch.Tensor
+    buckets: RelBuckets
+
+
+def rel_buckets(num_buckets=32, max_distance=128, bidirectional=True, device="cuda"):
+    """The usual buckets (fa_rel_buckets): near distances one each, farther ones up to
+    max_distance by their logarithm; with bidirectional, keys behind the query's position have
+    the second half of the buckets, without it they count as distance 0."""
+    m, left = fa_rel_buckets(num_buckets, max_distance, bidirectional)
+    return RelBuckets(m.to(device), left, int(num_buckets))
+
+
+def rel_bias(table, buckets, stream=None):
+    """Lay out a bias table [num_buckets, H] (fp32 or bf16, one learned bias per bucket and query
+    head) for fwd, bwd and decode (fa_rel_bias). Do so again after the table changes."""
+    dev = table.get_device()
+    m, left = buckets.map, buckets.left
+    if (table.dim() != 2 or table.shape[0] != buckets.num_buckets or dev < 0
+            or table.dtype not in (torch.float32, torch.bfloat16) or not table.is_contiguous()):
+        raise ValueError("table must be a contiguous fp32 or bf16 CUDA tensor "
+                         f"[{buckets.num_buckets}, H]")
+    if (m.dtype != torch.int32 or m.dim() != 1 or not m.is_contiguous() or m.get_device() != dev
+            or not 0 <= left < m.numel()):
+        raise ValueError("the map must be contiguous int32 on the table's device, and hold "
+                         "distance 0")
+    H = table.shape[1]
+    length = fa_rel_line_length(left, buckets.right)
+    with _memory_on(stream, dev):
+        lines = table.new_empty((H, length), dtype=torch.float32)
+    kind = FA_TABLE_F32 if table.dtype == torch.float32 else FA_TABLE_BF16
+    with torch.cuda.device(dev):
+        st = fa_rel_bias(table, kind, m, left, buckets.right, buckets.num_buckets, H, lines,
+                         stream)
+    _check(st, "fa_rel_bias")
+    _given_out(stream, dev, lines)
+    return RelBias(lines, buckets)
+
+
+_FWD_CROSS_BLOCK = struct.Struct("=11qd4qdQQ4q").pack
+_BWD_CROSS_BLOCK = struct.Struct("=15qd4qdQQ9q").pack
+_DECODE_REL_BLOCK = struct.Struct("=11qd9q").pack
+
+
+def _cross_args(q, k, v, scale, seqlens_k, rel):
+    """Checked sizes, scale and pointers of a call with keys of their own length: (B, H, H_kv, Nq,
+    Nk, d), scale, seqlens_k's pointer, (lines' pointer, left, right), and the device's index."""
+    B, H, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    dev = q.get_device()
+    if (k.shape[0] != B or k.shape[3] != d or v.shape != k.shape or Hkv < 1 or H % Hkv != 0
+            or k.get_device() != dev or v.get_device() != dev):
+        raise ValueError("k and v must be [B, H_kv, Nk, d] with H a multiple of H_kv, on q's "
+                         "device")
+    if seqlens_k is not None and (seqlens_k.dtype != torch.int32 or seqlens_k.shape != (B,)
+                                  or seqlens_k.get_device() != dev
+                                  or not seqlens_k.is_contiguous()):
+        raise ValueError(f"seqlens_k must be contiguous int32 [{B}], on q's device")
+    bias = (0, 0, 0)
+    if rel is not None:
+        left, right = rel.buckets.left, rel.buckets.right
+        if (rel.lines.shape != (H, left + right + 513) or rel.lines.dtype != torch.float32
+                or rel.lines.get_device() != dev or not rel.lines.is_contiguous()):
+            raise ValueError(f"rel_bias must come from rel_bias() with a table of {H} heads, on "
+                             "q's device")
+        bias = (rel.lines.data_ptr(), left, right)
+    return ((B, H, Hkv, Nq, Nk, d), 1.0 / math.sqrt(d) if scale is None else float(scale),
+            _data(seqlens_k), bias, dev)
+
+
+def _fwd_cross(q, k, v, scale, causal, dropout_p, seed, offset, block_mask, seqlens_k, stream,
+               window, q_offset, rel):
+    if block_mask is not None:
+        raise ValueError("a block mask needs k and v of q's length, q_offset 0 and no rel_bias")
+    sizes, scale, sl, bias, dev = _cross_args(q, k, v, scale, seqlens_k, rel)
+    with _memory_on(stream, dev):
+        o = torch.empty_like(q)
+        lse = q.new_empty(q.shape[:3], dtype=torch.float32)
+    _call("fa_fwd_cross_block", dev, stream,
+          _FWD_CROSS_BLOCK(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                           *sizes, scale, bool(causal), q_offset, *window, dropout_p,
+                           seed & _U64, offset & _U64, sl, *bias))
+    if stream is not None:
+        _given_out(stream, dev, o, lse)
+    return o, lse
+
+
+def _bwd_cross(q, k, v, o, dout, lse, scale, causal, dropout_p, seed, offset, block_mask,
+               seqlens_k, workspace, stream, window, q_offset, rel, rel_grad):
+    if block_mask is not None:
+        raise ValueError("a block mask needs k and v of q's length, q_offset 0 and no rel_bias")
+    sizes, scale, sl, bias, dev = _cross_args(q, k, v, scale, seqlens_k, rel)
+    B, H, Hkv, Nq, Nk, d = sizes
+    if (o.shape != q.shape or dout.shape != q.shape or o.get_device() != dev
+            or dout.get_device() != dev):
+        raise ValueError("o and dout must be like q")
+    if (lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or lse.get_device() != dev
+            or not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous fp32 [{B}, {H}, {Nq}], on q's device")
+    rel_grad = bool(rel_grad) and rel is not None
+    grad_args = (0, 0, 0)
+    if rel_grad:
+        m = rel.buckets.map
+        if m.dtype != torch.int32 or m.get_device() != dev or not m.is_contiguous():
+            raise ValueError("the map must be contiguous int32, on q's device")
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous, on q's device")
+    with _memory_on(stream, dev):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        if workspace is None:
+            size = fa_bwd_cross_workspace_size(B, H, Nq, Nk, d, causal, q_offset, rel_grad,
+                                               bias[1], bias[2])
+            workspace = q.new_empty(size, dtype=torch.uint8)
+        if rel_grad:
+            dtable = q.new_empty((rel.buckets.num_buckets, H), dtype=torch.float32)
+            grad_args = (m.data_ptr(), rel.buckets.num_buckets, dtable.data_ptr())
+    _call("fa_bwd_cross_block", dev, stream,
+          _BWD_CROSS_BLOCK(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
+                           lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes,
+                           scale, bool(causal), q_offset, *window, dropout_p, seed & _U64,
+                           offset & _U64, sl, *bias, *grad_args, workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size()))
+    out = (dq, dk, dv, dtable) if rel_grad else (dq, dk, dv)
+    if stream is not None:
+        _given_out(stream, dev, *out)
+    return out
+
+
+_decode_workspace_bytes = functools.lru_cache(maxsize=4096)(
+    lambda dev, *sizes: fa_decode_workspace_size(*sizes))
+
+
+def _decode_rel(q, k_cache, v_cache, scale, causal, seqlens_k, num_ctas, stream, window_left, rel):
+    sizes, scale, sl, bias, dev = _cross_args(q, k_cache, v_cache, scale, seqlens_k, rel)
+    with torch.cuda.device(dev):  # the split depends on the device's number of SMs
+        ws_bytes = _decode_workspace_bytes(dev, *sizes, num_ctas)
+    with _memory_on(stream, dev):
+        o = torch.empty_like(q)
+        lse = q.new_empty(q.shape[:3], dtype=torch.float32)
+        ws = q.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
+    _call("fa_decode_rel_block", dev, stream,
+          _DECODE_REL_BLOCK(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
+                            lse.data_ptr(), *sizes, scale, bool(causal), window_left, sl, *bias,
+                            num_ctas, _data(ws), ws_bytes))
+    if stream is not None:
+        _given_out(stream, dev, o, lse)
     return o, lse
 
 

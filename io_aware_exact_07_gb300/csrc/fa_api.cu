@@ -8,7 +8,10 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <cstdlib>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include "../../include/fa.h"
 #include "fa_decode.h"
@@ -182,6 +185,8 @@ fa::MaskParams make_mask(int B, int H, int Hkv, int N, int causal, const uint8_t
   m.wr = wr;
   m.block_mask = bm;
   m.seqlens_k = sl;
+  m.Nk = N;
+  m.q_off = 0;
   return m;
 }
 
@@ -219,6 +224,11 @@ fa::SyncParams make_sync(const DeviceInfo* di, StallTarget target) {
   s.inject_stall = take_stall(target);
   return s;
 }
+
+// Limits of the calls with positions on a key axis: sums of two positions, an offset and a window
+// stay within 32 bits.
+constexpr int kMaxAxis = 1 << 28;
+constexpr int kMaxDistances = 1 << 16;  // distances of a bias, left + right + 1
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -259,6 +269,8 @@ static fa_status fwd_impl(const void* q, const void* k, const void* v, void* o, 
   a.scale_log2 = scale * fa::kLog2e;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
+  a.mode = wl >= 0 || wr >= 0 ? fa::kWindow : fa::kPlain;
+  a.rel = fa::RelParams{};
   cudaError_t e = fa::launch_fwd(tq, tk, tv, a, d, a.drop.p8 > 0, di->num_sms,
                                  static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
@@ -338,6 +350,9 @@ static fa_status bwd_prepare(const void* q, const void* k, const void* v, const 
   a->dq = static_cast<__nv_bfloat16*>(dq);
   a->dk = static_cast<__nv_bfloat16*>(dk);
   a->dv = static_cast<__nv_bfloat16*>(dv);
+  a->mode = wl >= 0 || wr >= 0 ? fa::kWindow : fa::kPlain;
+  a->rel = fa::RelParams{};
+  a->row_sums = nullptr;
   return FA_OK;
 }
 
@@ -539,10 +554,13 @@ size_t fa_decode_workspace_size(int B, int H, int H_kv, int Nq, int Nk, int d, i
   return decode_ws_bytes(B, H, Nq, d, p);
 }
 
-fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
-                    int B, int H, int H_kv, int Nq, int Nk, int d, float scale, int causal,
-                    int window_left, const int32_t* seqlens_k, int num_ctas, void* workspace,
-                    size_t workspace_bytes, void* stream) {
+static fa_status check_lines(const float* lines, int left, int right);
+
+static fa_status decode_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
+                             float* lse, int B, int H, int H_kv, int Nq, int Nk, int d,
+                             float scale, int causal, int window_left, const int32_t* seqlens_k,
+                             int num_ctas, const fa::RelParams& rel, void* workspace,
+                             size_t workspace_bytes, void* stream) {
   DecodePlan p;
   fa_status st = decode_plan(B, H, H_kv, Nq, Nk, d, num_ctas, &p);
   if (st != FA_OK) return st;
@@ -578,6 +596,7 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
   a.sync = make_sync(di, kStallForward);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
+  a.rel = rel;
   const size_t slots = static_cast<size_t>(B) * H * Nq * p.seg_max;
   a.o_part = ws > 0 ? static_cast<float*>(workspace) : nullptr;
   a.lse_part = ws > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
@@ -586,6 +605,302 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = fa::launch_decode(tq, tk, tv, a, d, p.grid, s);
   if (e == cudaSuccess && p.seg_max > 1) e = fa::launch_decode_combine(a, d, s);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                    int B, int H, int H_kv, int Nq, int Nk, int d, float scale, int causal,
+                    int window_left, const int32_t* seqlens_k, int num_ctas, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  return decode_impl(q, k_cache, v_cache, o, lse, B, H, H_kv, Nq, Nk, d, scale, causal,
+                     window_left, seqlens_k, num_ctas, fa::RelParams{}, workspace,
+                     workspace_bytes, stream);
+}
+
+fa_status fa_decode_rel(const void* q, const void* k_cache, const void* v_cache, void* o,
+                        float* lse, int B, int H, int H_kv, int Nq, int Nk, int d, float scale,
+                        int causal, int window_left, const int32_t* seqlens_k,
+                        const float* rel_lines, int rel_left, int rel_right, int num_ctas,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  fa_status st = check_lines(rel_lines, rel_left, rel_right);
+  if (st != FA_OK) return st;
+  if (Nk > kMaxAxis) return FA_ERR_INVALID_ARG;
+  return decode_impl(q, k_cache, v_cache, o, lse, B, H, H_kv, Nq, Nk, d, scale, causal,
+                     window_left, seqlens_k, num_ctas, fa::RelParams{rel_lines, rel_left, rel_right},
+                     workspace, workspace_bytes, stream);
+}
+
+static fa_status check_lines(const float* lines, int left, int right) {
+  if (lines == nullptr || (reinterpret_cast<uintptr_t>(lines) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  if (left < 0 || right < 0 || left >= kMaxDistances || right >= kMaxDistances)
+    return FA_ERR_INVALID_ARG;
+  return left + right + 1 <= kMaxDistances ? FA_OK : FA_ERR_UNSUPPORTED;
+}
+
+int fa_rel_line_length(int left, int right) {
+  if (left < 0 || right < 0 || left >= kMaxDistances || right >= kMaxDistances ||
+      left + right + 1 > kMaxDistances)
+    return 0;
+  return fa::RelParams{nullptr, left, right}.stride();
+}
+
+// n^a >= b^c * m^d in whole numbers of any size.
+static bool power_at_least(uint32_t n, int a, uint32_t b, int c, uint32_t m, int d) {
+  typedef std::vector<uint32_t> Big;  // little-endian
+  auto times = [](Big& x, uint32_t y) {
+    uint64_t carry = 0;
+    for (uint32_t& w : x) {
+      carry += static_cast<uint64_t>(w) * y;
+      w = static_cast<uint32_t>(carry);
+      carry >>= 32;
+    }
+    if (carry != 0) x.push_back(static_cast<uint32_t>(carry));
+  };
+  Big l(1, 1u), r(1, 1u);
+  for (int i = 0; i < a; ++i) times(l, n);
+  for (int i = 0; i < d; ++i) times(r, m);
+  for (int i = 0; i < c; ++i) times(r, b);
+  if (l.size() != r.size()) return l.size() > r.size();
+  for (size_t i = l.size(); i-- > 0;)
+    if (l[i] != r[i]) return l[i] > r[i];
+  return true;
+}
+
+int fa_rel_buckets(int32_t* map_host, int capacity, int num_buckets, int max_distance,
+                   int bidirectional, int* left) {
+  const int half = bidirectional ? num_buckets / 2 : num_buckets;
+  const int exact = half / 2, steps = half - exact;
+  if (left == nullptr || num_buckets > 1024 || half < 2 || (bidirectional && num_buckets % 2) ||
+      max_distance <= exact || max_distance >= kMaxDistances / 2)
+    return 0;
+  // Bucket exact + t begins at the smallest n with (n / exact)^steps >= (max_distance / exact)^t,
+  // that is n^steps >= max_distance^t exact^(steps - t): a comparison of whole numbers, so that no
+  // logarithm's rounding decides where a bucket begins. (Doubles say where to look first.)
+  std::vector<int32_t> side;  // buckets of distances 0, 1, ... up to where the last one begins
+  try {
+    for (int n = 0; n < exact; ++n) side.push_back(n);
+    for (int t = 1; t < steps; ++t) {
+      int n = static_cast<int>(exact * std::pow(static_cast<double>(max_distance) / exact,
+                                                static_cast<double>(t) / steps)) - 1;
+      if (n < exact) n = exact;
+      while (!power_at_least(n, steps, exact, steps - t, max_distance, t)) ++n;
+      while (static_cast<int>(side.size()) < n) side.push_back(exact + t - 1);
+    }
+    side.push_back(half - 1);
+  } catch (const std::bad_alloc&) {
+    return 0;
+  }
+  const int reach = static_cast<int>(side.size()) - 1;
+  const int total = bidirectional ? 2 * reach + 1 : reach + 1;
+  *left = reach;
+  if (map_host != nullptr) {
+    if (capacity < total) return 0;
+    for (int i = 0; i <= reach; ++i) map_host[reach - i] = side[i];
+    if (bidirectional)
+      for (int i = 1; i <= reach; ++i) map_host[reach + i] = half + side[i];
+  }
+  return total;
+}
+
+fa_status fa_rel_bias(const void* table, int table_type, const int32_t* map, int left, int right,
+                      int num_buckets, int H, float* lines, void* stream) {
+  fa_status st = check_lines(lines, left, right);
+  if (st != FA_OK) return st;
+  if (H < 1 || num_buckets < 1 || !table || !map) return FA_ERR_INVALID_ARG;
+  if (table_type != FA_TABLE_F32 && table_type != FA_TABLE_BF16) return FA_ERR_UNSUPPORTED;
+  if (num_buckets > kMaxDistances || H > 65535) return FA_ERR_UNSUPPORTED;
+  const uintptr_t unit = table_type == FA_TABLE_F32 ? 3u : 1u;
+  if ((reinterpret_cast<uintptr_t>(table) & unit) != 0 ||
+      (reinterpret_cast<uintptr_t>(map) & 3u) != 0)
+    return FA_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  if ((st = device_info(&di)) != FA_OK) return st;
+  fa::RelLinesArgs a;
+  a.table = table;
+  a.bf16 = table_type == FA_TABLE_BF16;
+  a.map = map;
+  a.left = left;
+  a.right = right;
+  a.num_buckets = num_buckets;
+  a.H = H;
+  a.lines = lines;
+  a.status = di->status;
+  return fa::launch_rel_lines(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                   : FA_ERR_CUDA;
+}
+
+// Checks that the calls with positions share; fills the mask and the bias.
+static fa_status cross_args(int B, int H, int Hkv, int Nq, int Nk, int d, float scale, int causal,
+                            int q_offset, int wl, int wr, float dropout_p,
+                            const int32_t* seqlens_k, const float* lines, int left, int right,
+                            fa::MaskParams* m, fa::RelParams* rel, int* mode) {
+  fa_status st = check_common(B, H, Nq, d, scale, dropout_p, Hkv);
+  if (st != FA_OK) return st;
+  if (Nk < 1 || static_cast<long long>(B) * Hkv * Nk >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+  if (Nq > kMaxAxis || Nk > kMaxAxis || q_offset > kMaxAxis || q_offset < -kMaxAxis)
+    return FA_ERR_INVALID_ARG;
+  if (wl < -1 || wr < -1) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(seqlens_k) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  // a window as wide as all positions hides nothing
+  const int widest = Nq + Nk + std::abs(q_offset);
+  *m = make_mask(B, H, Hkv, Nq, causal, nullptr, seqlens_k, wl >= widest ? -1 : wl,
+                 wr >= widest ? -1 : wr);
+  m->Nk = Nk;
+  m->q_off = q_offset;
+  *mode = fa::kCross;
+  *rel = fa::RelParams{};
+  if (lines != nullptr) {
+    if ((st = check_lines(lines, left, right)) != FA_OK) return st;
+    if (H > 65535) return FA_ERR_UNSUPPORTED;
+    *rel = fa::RelParams{lines, left, right};
+    *mode = fa::kRel;
+  }
+  return FA_OK;
+}
+
+fa_status fa_fwd_cross(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                       int H, int H_kv, int Nq, int Nk, int d, float scale, int causal,
+                       int q_offset, int window_left, int window_right, float dropout_p,
+                       uint64_t seed, uint64_t offset, const int32_t* seqlens_k,
+                       const float* rel_lines, int rel_left, int rel_right, void* stream) {
+  fa::FwdArgs a;
+  fa_status st = cross_args(B, H, H_kv, Nq, Nk, d, scale, causal, q_offset, window_left,
+                            window_right, dropout_p, seqlens_k, rel_lines, rel_left, rel_right,
+                            &a.mask, &a.rel, &a.mode);
+  if (st != FA_OK) return st;
+  for (const void* p : {q, k, v, static_cast<const void*>(o)})
+    if (!p || !aligned16(p)) return FA_ERR_INVALID_ARG;
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  if ((st = device_info(&di)) != FA_OK) return st;
+  CUtensorMap tq, tk, tv;
+  if (!encode_map(&tq, q, B * H, Nq, d) || !encode_map(&tk, k, B * H_kv, Nk, d) ||
+      !encode_map(&tv, v, B * H_kv, Nk, d))
+    return FA_ERR_CUDA;
+  a.drop = make_drop(dropout_p, seed, offset);
+  a.sync = make_sync(di, kStallForward);
+  a.scale_log2 = scale * fa::kLog2e;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  cudaError_t e = fa::launch_fwd(tq, tk, tv, a, d, a.drop.p8 > 0, di->num_sms,
+                                 static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Workspace of fa_bwd_cross: D, and for the gradient of a bias table what the dQ kernel leaves of
+// each query row, the near tiles' diagonal sums and the far fields' sums.
+struct CrossWorkspace {
+  int first, n_diag;  // near tile pairs: kt - qt = first .. first + n_diag - 1
+  size_t rows_off, diag_off, far_off, bytes;
+};
+static CrossWorkspace cross_workspace(int B, int H, int Nq, int Nk, int causal, int q_offset,
+                                      bool grad, int left, int right) {
+  CrossWorkspace w = {0, 0, 0, 0, 0, 0};
+  const size_t rows = static_cast<size_t>(B) * H * Nq;
+  w.bytes = round256(rows * sizeof(float));
+  if (!grad) return w;
+  w.rows_off = w.bytes;
+  w.diag_off = w.rows_off + round256(rows * 4 * fa::kRelRowSums * sizeof(float));
+  // near: -left - 127 < 128 (kt - qt) - q_offset < right + 127, between the first and last tiles,
+  // and under a causal mask not wholly to the right of the queries
+  constexpr long long T = fa::kTile;
+  auto floor_div = [](long long x) { return x >= 0 ? x / T : -((-x + T - 1) / T); };
+  const long long n_q = (Nq + T - 1) / T, n_k = (Nk + T - 1) / T;
+  long long lo = floor_div(static_cast<long long>(q_offset) - left - (T - 1)) + 1;
+  long long hi = -floor_div(-(static_cast<long long>(q_offset) + right + (T - 1))) - 1;
+  if (causal && hi > floor_div(static_cast<long long>(q_offset) + T - 1))
+    hi = floor_div(static_cast<long long>(q_offset) + T - 1);
+  if (lo < 1 - n_q) lo = 1 - n_q;
+  if (hi > n_k - 1) hi = n_k - 1;
+  w.first = static_cast<int>(lo);
+  w.n_diag = hi < lo ? 0 : static_cast<int>(hi - lo + 1);
+  w.far_off = w.diag_off + round256((static_cast<size_t>(H) * w.n_diag + fa::kRelMaxCtas) *
+                                    fa::kRelDiagFloats * sizeof(float));
+  const size_t chunks = (static_cast<size_t>(Nq) + fa::kRelRows - 1) / fa::kRelRows;
+  w.bytes = w.far_off + round256(static_cast<size_t>(B) * H * chunks * 2 * sizeof(double));
+  return w;
+}
+
+size_t fa_bwd_cross_workspace_size(int B, int H, int Nq, int Nk, int d, int causal, int q_offset,
+                                   int rel_grad, int rel_left, int rel_right) {
+  if (B < 1 || H < 1 || Nq < 1 || Nk < 1 || (d != 64 && d != 128) || Nq > kMaxAxis ||
+      Nk > kMaxAxis || q_offset > kMaxAxis || q_offset < -kMaxAxis ||
+      static_cast<long long>(B) * H * Nq >= (1ll << 31))
+    return 0;
+  if (rel_grad && fa_rel_line_length(rel_left, rel_right) == 0) return 0;
+  return cross_workspace(B, H, Nq, Nk, causal, q_offset, rel_grad != 0, rel_left, rel_right).bytes;
+}
+
+fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* o,
+                       const void* dout, const float* lse, void* dq, void* dk, void* dv, int B,
+                       int H, int H_kv, int Nq, int Nk, int d, float scale, int causal,
+                       int q_offset, int window_left, int window_right, float dropout_p,
+                       uint64_t seed, uint64_t offset, const int32_t* seqlens_k,
+                       const float* rel_lines, int rel_left, int rel_right,
+                       const int32_t* rel_map, int num_buckets, float* dtable, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  fa::RelGradArgs g;
+  fa::BwdArgs& a = g.b;
+  fa_status st = cross_args(B, H, H_kv, Nq, Nk, d, scale, causal, q_offset, window_left,
+                            window_right, dropout_p, seqlens_k, rel_lines, rel_left, rel_right,
+                            &a.mask, &a.rel, &a.mode);
+  if (st != FA_OK) return st;
+  for (const void* p : {q, k, v, o, dout, static_cast<const void*>(dq),
+                        static_cast<const void*>(dk), static_cast<const void*>(dv)})
+    if (!p || !aligned16(p)) return FA_ERR_INVALID_ARG;
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  const bool grad = dtable != nullptr;
+  if (grad) {
+    if (!rel_lines || !rel_map || num_buckets < 1) return FA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(rel_map) | reinterpret_cast<uintptr_t>(dtable)) & 3u) != 0)
+      return FA_ERR_INVALID_ARG;
+    if (num_buckets > kMaxDistances) return FA_ERR_UNSUPPORTED;
+  }
+  const CrossWorkspace w = cross_workspace(B, H, Nq, Nk, a.mask.causal, q_offset, grad, rel_left,
+                                           rel_right);
+  if (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace))
+    return FA_ERR_WORKSPACE;
+  DeviceInfo* di = nullptr;
+  if ((st = device_info(&di)) != FA_OK) return st;
+  CUtensorMap m[4];
+  if (!encode_map(&m[0], q, B * H, Nq, d) || !encode_map(&m[1], k, B * H_kv, Nk, d) ||
+      !encode_map(&m[2], v, B * H_kv, Nk, d) || !encode_map(&m[3], dout, B * H, Nq, d))
+    return FA_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.drop = make_drop(dropout_p, seed, offset);
+  a.sync = make_sync(di, kStallNone);
+  a.scale = scale;
+  a.scale_log2 = scale * fa::kLog2e;
+  a.o = static_cast<const __nv_bfloat16*>(o);
+  a.dout = static_cast<const __nv_bfloat16*>(dout);
+  a.lse = lse;
+  a.dsum = reinterpret_cast<float*>(ws);
+  a.dq = static_cast<__nv_bfloat16*>(dq);
+  a.dk = static_cast<__nv_bfloat16*>(dk);
+  a.dv = static_cast<__nv_bfloat16*>(dv);
+  a.row_sums = grad ? reinterpret_cast<float*>(ws + w.rows_off) : nullptr;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool drop = a.drop.p8 > 0;
+  cudaError_t e = fa::launch_bwd_preprocess(a, d, di->num_sms, s);
+  if (e == cudaSuccess) {
+    a.sync.inject_stall = take_stall(kStallDkdv);
+    e = fa::launch_bwd_dkdv(m[0], m[1], m[2], m[3], a, d, drop, di->num_sms, s);
+  }
+  if (e == cudaSuccess) {
+    a.sync.inject_stall = take_stall(kStallDq);
+    e = fa::launch_bwd_dq(m[0], m[1], m[2], m[3], a, d, drop, di->num_sms, s);
+  }
+  if (e == cudaSuccess && grad) {
+    a.sync.inject_stall = 0;
+    g.map = rel_map;
+    g.num_buckets = num_buckets;
+    g.dtable = dtable;
+    g.first = w.first;
+    g.n_diag = w.n_diag;
+    g.diag_sums = reinterpret_cast<float*>(ws + w.diag_off);
+    g.far_sums = reinterpret_cast<double*>(ws + w.far_off);
+    e = fa::launch_rel_grad(m[0], m[1], m[2], m[3], g, d, drop, di->num_sms, s);
+  }
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -896,7 +1211,9 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   auto p = [&](int i) { return reinterpret_cast<void*>(x[i]); };              \
   auto u8 = [&](int i) { return reinterpret_cast<uint8_t*>(x[i]); };          \
   auto i32 = [&](int i) { return reinterpret_cast<const int32_t*>(x[i]); };   \
-  auto n = [&](int i) { return static_cast<int>(x[i]); };
+  auto n = [&](int i) { return static_cast<int>(x[i]); };                     \
+  (void)u8;                                                                   \
+  (void)i32;
 
 fa_status fa_paged_write_block(const int64_t* x, void* stream) {
   FA_BLOCK_INTS(6, 7, 8, 9, 10, 16, 19, 20, 21)
@@ -920,6 +1237,43 @@ fa_status fa_paged_attn_block(const int64_t* x, void* stream) {
                        n(9), n(10), n(11), n(12), x[13], x[14], x[15], i32(16), x[17], n(18),
                        i32(19), i32(20), n(21), n(22), n(23), x[24], static_cast<float>(scale),
                        n(26), n(27), p(28), static_cast<size_t>(x[29]), stream);
+}
+
+fa_status fa_fwd_cross_block(const int64_t* x, void* stream) {
+  FA_BLOCK_INTS(5, 6, 7, 8, 9, 10, 12, 13, 14, 15, 21, 22)
+  double scale, drop;
+  memcpy(&scale, x + 11, sizeof(scale));
+  memcpy(&drop, x + 16, sizeof(drop));
+  return fa_fwd_cross(p(0), p(1), p(2), p(3), static_cast<float*>(p(4)), n(5), n(6), n(7), n(8),
+                      n(9), n(10), static_cast<float>(scale), n(12), n(13), n(14), n(15),
+                      static_cast<float>(drop), static_cast<uint64_t>(x[17]),
+                      static_cast<uint64_t>(x[18]), i32(19), static_cast<float*>(p(20)), n(21),
+                      n(22), stream);
+}
+
+fa_status fa_bwd_cross_block(const int64_t* x, void* stream) {
+  FA_BLOCK_INTS(9, 10, 11, 12, 13, 14, 16, 17, 18, 19, 25, 26, 28)
+  double scale, drop;
+  memcpy(&scale, x + 15, sizeof(scale));
+  memcpy(&drop, x + 20, sizeof(drop));
+  if (x[31] < 0) return FA_ERR_INVALID_ARG;
+  return fa_bwd_cross(p(0), p(1), p(2), p(3), p(4), static_cast<float*>(p(5)), p(6), p(7), p(8),
+                      n(9), n(10), n(11), n(12), n(13), n(14), static_cast<float>(scale), n(16),
+                      n(17), n(18), n(19), static_cast<float>(drop), static_cast<uint64_t>(x[21]),
+                      static_cast<uint64_t>(x[22]), i32(23), static_cast<float*>(p(24)), n(25),
+                      n(26), i32(27), n(28), static_cast<float*>(p(29)), p(30),
+                      static_cast<size_t>(x[31]), stream);
+}
+
+fa_status fa_decode_rel_block(const int64_t* x, void* stream) {
+  FA_BLOCK_INTS(5, 6, 7, 8, 9, 10, 12, 13, 16, 17, 18)
+  double scale;
+  memcpy(&scale, x + 11, sizeof(scale));
+  if (x[20] < 0) return FA_ERR_INVALID_ARG;
+  return fa_decode_rel(p(0), p(1), p(2), p(3), static_cast<float*>(p(4)), n(5), n(6), n(7), n(8),
+                       n(9), n(10), static_cast<float>(scale), n(12), n(13), i32(14),
+                       static_cast<float*>(p(15)), n(16), n(17), n(18), p(19),
+                       static_cast<size_t>(x[20]), stream);
 }
 #undef FA_BLOCK_INTS
 

@@ -17,6 +17,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "fa_common.cuh"
 #include "fa_kernels.h"
 
@@ -113,13 +115,14 @@ struct DkdvLayout {
   __device__ static constexpr uint32_t col_dpt() { return static_cast<uint32_t>(2 * D + 128); }
 };
 
-template <int D, bool DROPOUT, bool GQA, bool WIN>
+template <int D, bool DROPOUT, bool GQA, int MODE>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_do, const BwdArgs args) {
   using L = DkdvLayout<D, DROPOUT>;
+  constexpr bool WIN = MODE == kWindow, CROSS = MODE >= kCross, REL = MODE == kRel;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0u) {  // uniform over the block: nothing has started yet
     if (threadIdx.x == 0) record_error(args.sync.status, kStatusCuda);
@@ -130,7 +133,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int lane = tid & 31;
   const MaskParams& mk = args.mask;
   const int N = mk.N;
-  const int n_t = (N + kTile - 1) / kTile;  // query tiles == key tiles
+  const int Nk = CROSS ? mk.Nk : N;         // keys
+  const int n_q = (N + kTile - 1) / kTile;  // query tiles
+  const int n_t = CROSS ? (Nk + kTile - 1) / kTile : n_q;  // key tiles
   const int n_units = mk.B * mk.Hkv * n_t;
   const int G = GQA ? mk.H / mk.Hkv : 1;  // query heads per K/V head
 
@@ -246,8 +251,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
            ++bh) {  // the query heads sharing this K/V head
-        for (int chunk = 0; chunk * 32 < n_t && ok; ++chunk) {
-          uint32_t bits = warp_valid_bits_t<WIN>(mk, kt, chunk, n_t, n_kv);
+        for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
+          uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
           while (bits != 0u) {
             const int qt = chunk * 32 + (__ffs(bits) - 1);
             bits &= bits - 1;
@@ -269,6 +274,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               const bool in = row < N;
               const long long idx = static_cast<long long>(bh) * N + row;
               vp[r] = q_side ? -lse2_of(args.lse, idx, in) : (in ? -args.dsum[idx] : 0.f);
+              // a tile whose bias is one number: added here
+              if constexpr (REL)
+                if (q_side)
+                  vp[r] += rel_far_bias(args.rel, rel_line(args.rel, bh % mk.H),
+                                        kt * kTile - tile_pos(mk, qt));
             }
             reinterpret_cast<float4*>(rowvals + s * 128)[lane] = v4;
             if (lane == 0) {
@@ -338,8 +348,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int prev_s = -1;
       for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
              ++bh) {  // the query heads sharing this K/V head
-        for (int chunk = 0; chunk * 32 < n_t && ok; ++chunk) {
-          uint32_t bits = warp_valid_bits_t<WIN>(mk, kt, chunk, n_t, n_kv);
+        for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
+          uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
           while (bits != 0u) {
             bits &= bits - 1;
             const int sq = it % L::kQStages, sd = it % L::kDOStages;
@@ -455,8 +465,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int n_done = 0;
       for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
              ++bh) {  // the query heads sharing this K/V head
-        for (int chunk = 0; chunk * 32 < n_t && ok; ++chunk) {
-          uint32_t bits = warp_valid_bits_t<WIN>(mk, kt, chunk, n_t, n_kv);
+        for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
+          uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
           while (bits != 0u) {
             const int qt = chunk * 32 + (__ffs(bits) - 1);
             bits &= bits - 1;
@@ -503,7 +513,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               tmem_ld32(tSt, &sr[0]);
               tmem_ld32(tSt + 32, &sr[32]);
               tmem_ld_wait();
-              const uint64_t c2 = f2_pack(c_log2, c_log2);
+              float cs = c_log2;
+              if constexpr (REL) {  // each element's own bias; scores to log2 units
+                const int d0 = kt * kTile - tile_pos(mk, qt);
+                if (!rel_far_left(args.rel, d0) && !rel_far_right(args.rel, d0)) {
+                  const float* lp = rel_line(args.rel, bh % mk.H) + (d0 + r - 64 * wg);
+  #pragma unroll
+                  for (int c = 0; c < 64; ++c)
+                    sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), c_log2, __ldg(lp - c)));
+                  cs = 1.f;
+                }
+              }
+              const uint64_t c2 = f2_pack(cs, cs);
   #pragma unroll
               for (int c4 = 0; c4 < 16; ++c4) {
                 const ulonglong2 nl = reinterpret_cast<const ulonglong2*>(lse_t)[c4];  // -lse2 pairs
@@ -519,12 +540,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 }
               }
             }
-            if (tile_needs_element_mask<WIN>(mk, qt, kt, kv_len)) {
+            if (tile_needs_element_mask<MODE>(mk, qt, kt, kv_len)) {
               const bool key_ok = key < kv_len;
   #pragma unroll
               for (int c = 0; c < 64; ++c) {
-                const bool allowed = key_ok && (!mk.causal || key <= q0 + c) &&
-                                     (!WIN || in_window(mk, q0 + c, key));
+                const int pos = CROSS ? q0 + c + mk.q_off : q0 + c;
+                const bool allowed = key_ok && (!mk.causal || key <= pos) &&
+                                     (!(WIN || CROSS) || in_window(mk, pos, key));
                 p[c] = allowed ? p[c] : 0.f;
               }
             }
@@ -561,6 +583,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 uint32_t dr[32];
                 tmem_ld32(tDPt + 32 * h, dr);
                 tmem_ld_wait();
+                if constexpr (CROSS) {  // a key behind the length, whatever its V holds
+                  if (key >= kv_len)
+  #pragma unroll
+                    for (int c = 0; c < 32; ++c) dr[c] = 0u;
+                }
   #pragma unroll
                 for (int c4 = 0; c4 < 8; ++c4) {
                   const ulonglong2 nd = reinterpret_cast<const ulonglong2*>(dsum_t)[8 * h + c4];  // -D
@@ -609,8 +636,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint32_t tAcc = tmem + lane_base + (wg == 0 ? L::col_dv() : L::col_dk());
       const float mult = (wg == 0) ? args.drop.keep_scale : args.scale;
       __nv_bfloat16* dst_base = (wg == 0) ? args.dv : args.dk;
-      __nv_bfloat16* dst = dst_base + (static_cast<size_t>(bhk) * N + static_cast<size_t>(key)) * D;
-      const bool row_ok = key < N;
+      __nv_bfloat16* dst = dst_base + (static_cast<size_t>(bhk) * Nk + static_cast<size_t>(key)) * D;
+      const bool row_ok = key < Nk;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
@@ -667,11 +694,14 @@ template <int D, bool DROP>
 static cudaError_t launch_dkdv_impl(const CUtensorMap& tq, const CUtensorMap& tk,
                                     const CUtensorMap& tv, const CUtensorMap& tdo,
                                     const BwdArgs& a, int grid, cudaStream_t stream) {
-  const bool gqa = a.mask.Hkv != a.mask.H, win = a.mask.wl >= 0 || a.mask.wr >= 0;
-  auto kern = gqa ? (win ? fa_bwd_dkdv_kernel<D, DROP, true, true>
-                         : fa_bwd_dkdv_kernel<D, DROP, true, false>)
-                  : (win ? fa_bwd_dkdv_kernel<D, DROP, false, true>
-                         : fa_bwd_dkdv_kernel<D, DROP, false, false>);
+  auto pick = [&](auto gqa) {
+    constexpr bool G = decltype(gqa)::value;
+    return a.mode == kRel      ? fa_bwd_dkdv_kernel<D, DROP, G, kRel>
+           : a.mode == kCross  ? fa_bwd_dkdv_kernel<D, DROP, G, kCross>
+           : a.mode == kWindow ? fa_bwd_dkdv_kernel<D, DROP, G, kWindow>
+                               : fa_bwd_dkdv_kernel<D, DROP, G, kPlain>;
+  };
+  auto kern = a.mask.Hkv != a.mask.H ? pick(std::true_type{}) : pick(std::false_type{});
   constexpr int kSmem = DkdvLayout<D, DROP>::kSmemBytes;
   cudaError_t e = set_smem(kern, kSmem);
   if (e != cudaSuccess) return e;
@@ -682,7 +712,7 @@ static cudaError_t launch_dkdv_impl(const CUtensorMap& tq, const CUtensorMap& tk
 cudaError_t launch_bwd_dkdv(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& tdo, const BwdArgs& a, int d, bool dropout,
                             int num_sms, cudaStream_t stream) {
-  const int n_t = (a.mask.N + kTile - 1) / kTile;
+  const int n_t = (a.mask.Nk + kTile - 1) / kTile;
   const long long units = static_cast<long long>(a.mask.B) * a.mask.Hkv * n_t;  // (K/V head, key tile)
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
   if (grid <= 0) return cudaSuccess;

@@ -126,13 +126,14 @@ struct DkdvBars {
   uint32_t stall;  // test hook: never completed
 };
 
-template <int D, bool DROPOUT, bool GQA, bool WIN>
+template <int D, bool DROPOUT, bool GQA, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_bwd_dkdv_split_kernel(const __grid_constant__ CUtensorMap tm_q,
                              const __grid_constant__ CUtensorMap tm_k,
                              const __grid_constant__ CUtensorMap tm_v,
                              const __grid_constant__ CUtensorMap tm_do, const BwdArgs args) {
   using L = DkdvL<D>;
+  constexpr bool WIN = MODE == kWindow, CROSS = MODE >= kCross, REL = MODE == kRel;
   constexpr int T = L::T;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -142,7 +143,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = tid & 31;
   const MaskParams& mk = args.mask;
   const int N = mk.N;
-  const int n_t = (N + kTile - 1) / kTile;
+  const int Nk = CROSS ? mk.Nk : N;                        // keys
+  const int n_q = (N + kTile - 1) / kTile;                 // query tiles
+  const int n_t = CROSS ? (Nk + kTile - 1) / kTile : n_q;  // key tiles
   const int n_units = mk.B * mk.Hkv * n_t;
   const int G = GQA ? mk.H / mk.Hkv : 1;  // query heads per K/V head
   const bool rot = mk.seqlens_k != nullptr;  // rotated schedule under key padding
@@ -250,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++kv_arms[kb];
         for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
                ++bh) {  // the query heads sharing this K/V head
-          for (int chunk = 0; chunk * 32 < n_t && ok; ++chunk) {
-            uint32_t bits = warp_valid_bits_t<WIN>(mk, kt, chunk, n_t, n_kv);
+          for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
+            uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
             while (bits != 0u) {
               const int qt = chunk * 32 + (__ffs(bits) - 1);
               bits &= bits - 1;
@@ -271,6 +274,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool in = row < N;
                 const long long idx = static_cast<long long>(bh) * N + row;
                 lp[r] = -lse2_at(args.lse, idx, in);
+                // a tile whose bias is one number: added here
+                if constexpr (REL)
+                  lp[r] += rel_far_bias(args.rel, rel_line(args.rel, bh % mk.H),
+                                        kt * kTile - tile_pos(mk, qt));
                 dp[r] = in ? -args.dsum[idx] : 0.f;
               }
               // staged negated: the compute warps add them as packed pairs
@@ -329,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dV = sdesc_sw128(sKV + (2 * kb + 1) * T, 16, 1024);
         for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
                ++bh) {  // the query heads sharing this K/V head
-          for (int chunk = 0; chunk * 32 < n_t && ok; ++chunk) {
-            const uint32_t vbits = warp_valid_bits_t<WIN>(mk, kt, chunk, n_t, n_kv);
+          for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
+            const uint32_t vbits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
             if (leader) {
               for (uint32_t bits = vbits; bits != 0u && ok; bits &= bits - 1) {
                 const int s = it % L::kStages;
@@ -379,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool first = true;
         for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
                ++bh) {  // the query heads sharing this K/V head
-          for (int chunk = 0; chunk * 32 < n_t && ok; ++chunk) {
-            const uint32_t vbits = warp_valid_bits_t<WIN>(mk, kt, chunk, n_t, n_kv);
+          for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
+            const uint32_t vbits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
             if (leader) {
               for (uint32_t bits = vbits; bits != 0u && ok; bits &= bits - 1) {
                 const int s = it % L::kStages;
@@ -455,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n_done = 0;
       for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
              ++bh) {  // the query heads sharing this K/V head
-        for (int chunk = 0; chunk * 32 < n_t && ok; ++chunk) {
-          uint32_t bits = warp_valid_bits_t<WIN>(mk, kt, chunk, n_t, n_kv);
+        for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
+          uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
           while (bits != 0u && ok) {
             const int qt = chunk * 32 + (__ffs(bits) - 1);
             bits &= bits - 1;
@@ -511,7 +518,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(bars.st_free);
               }
-              const uint64_t c2 = f2_pack(c_log2, c_log2);
+              float cs = c_log2;
+              if constexpr (REL) {  // each element's own bias; scores to log2 units
+                const int d0 = kt * kTile - tile_pos(mk, qt);
+                if (!rel_far_left(args.rel, d0) && !rel_far_right(args.rel, d0)) {
+                  const float* lp = rel_line(args.rel, bh % mk.H) + (d0 + r - 32 * wg);
+  #pragma unroll
+                  for (int c = 0; c < 32; ++c)
+                    sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), c_log2, __ldg(lp - c)));
+                  cs = 1.f;
+                }
+              }
+              const uint64_t c2 = f2_pack(cs, cs);
   #pragma unroll
               for (int c4 = 0; c4 < 8; ++c4) {
                 const ulonglong2 nl = reinterpret_cast<const ulonglong2*>(lse_t)[c4];  // -lse2 pairs
@@ -527,14 +545,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            if (tile_needs_element_mask<WIN>(mk, qt, kt, kv_len)) {
+            if (tile_needs_element_mask<MODE>(mk, qt, kt, kv_len)) {
               const bool key_ok = key < kv_len;
   #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                p[c] = (key_ok && (!mk.causal || key <= q0 + c) &&
-                        (!WIN || in_window(mk, q0 + c, key)))
+              for (int c = 0; c < 32; ++c) {
+                const int pos = CROSS ? q0 + c + mk.q_off : q0 + c;
+                p[c] = (key_ok && (!mk.causal || key <= pos) &&
+                        (!(WIN || CROSS) || in_window(mk, pos, key)))
                            ? p[c]
                            : 0.f;
+              }
             }
             {
               uint32_t pk[16];  // dropped copy for dV
@@ -573,6 +593,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               if constexpr (L::kSepBuf) {
                 tc_fence_before();
                 mbar_arrive(bars.dpt_free);
+              }
+              if constexpr (CROSS) {  // a key behind the length, whatever its V holds
+                if (key >= kv_len)
+  #pragma unroll
+                  for (int c = 0; c < 32; ++c) dr[c] = 0u;
               }
               uint32_t pk[16];
   #pragma unroll
@@ -630,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem + lane_base + (is_dv ? L::kColDV : L::kColDK) + kHalf * (wg & 1);
       const float mult = is_dv ? args.drop.keep_scale : args.scale;
       __nv_bfloat16* dst = (is_dv ? args.dv : args.dk) +
-                           (static_cast<size_t>(bhk) * N + static_cast<size_t>(key)) * D +
+                           (static_cast<size_t>(bhk) * Nk + static_cast<size_t>(key)) * D +
                            kHalf * (wg & 1);
 #pragma unroll
       for (int c = 0; c < kHalf / 32; ++c) {
@@ -647,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 16; ++k)
           pk[k] = pack_bf16x2(__uint_as_float(v[2 * k]) * mult,
                               __uint_as_float(v[2 * k + 1]) * mult);
-        if (key < N) {
+        if (key < Nk) {
           uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -701,22 +726,23 @@ struct DqBars {
   uint32_t stall;  // test hook: never completed
 };
 
-template <int D, bool DROPOUT>
+template <int D, bool DROPOUT, int MODE>
 struct DqRealloc {
-  static constexpr bool value = (D == 128) || DROPOUT;
+  static constexpr bool value = (D == 128) || DROPOUT || MODE == kRel;
 };
 
-template <int D, bool DROPOUT, bool WIN>
+template <int D, bool DROPOUT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_bwd_dq_split_kernel(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ CUtensorMap tm_do, const BwdArgs args) {
   using L = DqL<D>;
+  constexpr bool WIN = MODE == kWindow, CROSS = MODE >= kCross, REL = MODE == kRel;
   // Register reallocation pays at d = 128 and with dropout (both keep more values
   // live per compute thread); at d = 64 without dropout the compute warps need no
   // more than the launch allocation and the kernel runs faster without it.
-  constexpr bool kRealloc = DqRealloc<D, DROPOUT>::value;
+  constexpr bool kRealloc = DqRealloc<D, DROPOUT, MODE>::value;
   constexpr int T = L::T;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -809,11 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     qt = u % n_q;
     if (mk.causal) qt = n_q - 1 - qt;
   };
-  auto kv_limit = [&](int qt, int n_kv) {
-    int jmax = n_kv;
-    if (mk.causal && qt + 1 < jmax) jmax = qt + 1;
-    return jmax;
-  };
+  auto kv_limit = [&](int qt, int n_kv) { return key_tiles_upto<MODE>(mk, qt + 1, n_kv); };
 
   if (warp >= kComputeWarps) {
     // producer, issuers and the idle warp: one warpgroup, which hands most of its
@@ -844,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++qd_arms[qb];
         for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-          uint32_t bits = warp_valid_bits<WIN>(mk, qt, chunk, n_q, n_kv);
+          uint32_t bits = warp_valid_bits<MODE>(mk, qt, chunk, n_q, n_kv);
           while (bits != 0u) {
             const int j = chunk * 32 + (__ffs(bits) - 1);
             bits &= bits - 1;
@@ -913,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dQ = sdesc_sw128(sQD + (2 * qb) * T, 16, 1024);
         const uint64_t dDO = sdesc_sw128(sQD + (2 * qb + 1) * T, 16, 1024);
         for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-          const uint32_t vbits = warp_valid_bits<WIN>(mk, qt, chunk, n_q, n_kv);
+          const uint32_t vbits = warp_valid_bits<MODE>(mk, qt, chunk, n_q, n_kv);
           if (leader) {
             for (uint32_t bits = vbits; bits != 0u && ok; bits &= bits - 1) {
               const int ks = it % L::kKStages, vs = it % L::kVStages;
@@ -962,9 +984,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int jmax = kv_limit(qt, n_kv);
         bool first = true;
         for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-          const uint32_t vbits = warp_valid_bits<WIN>(mk, qt, chunk, n_q, n_kv);
-          if (leader) {
-            for (uint32_t bits = vbits; bits != 0u && ok; bits &= bits - 1) {
+          const uint32_t vbits = warp_valid_bits<MODE>(mk, qt, chunk, n_q, n_kv);
+          auto issue = [&](uint32_t bits) {
+            for (; bits != 0u && ok; bits &= bits - 1) {
               const int ks = it % L::kKStages;
               if (!mbar_wait(bars.ds_ready, dsc++ & 1, tmo, abort_flag) ||
                   !mbar_wait(bars.k_full[ks], (it / L::kKStages) & 1u, tmo, abort_flag) ||
@@ -982,6 +1004,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++it;
             }
             if (!ok) fail();
+          };
+          uint32_t cut = 0u;  // the tile that the length cuts: the last of the unit
+          if constexpr (CROSS) {
+            const int jc = cut_tile(mk, kv_len);
+            if (jc >= 0 && jc / 32 == chunk) cut = vbits & (1u << (jc & 31));
+          }
+          if (leader) issue(vbits & ~cut);
+          if constexpr (CROSS) {
+            if (cut != 0u) {
+              // (the S product may still read these rows of K: its scores there are masked)
+              const uint32_t n = __shfl_sync(0xffffffffu, it, 0);
+              const int ks = n % L::kKStages;
+              if (mbar_wait_warp(bars.k_full[ks], (n / L::kKStages) & 1u, tmo, abort_flag))
+                zero_tile_rows<TileT<D>::kChunks>(sK + ks * T, kv_len % kTile, lane, 32);
+              __syncwarp();
+              if (leader) issue(cut);
+            }
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
@@ -1048,8 +1087,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mk.wl >= 0) key_lo = row - mk.wl;
       }
       int n_done = 0;
+      // sums over this thread's keys: dS; dS and P left and right of the range of distances
+      float sum_ds = 0.f, left_ds = 0.f, right_ds = 0.f, left_p = 0.f, right_p = 0.f;
       for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-        uint32_t bits = warp_valid_bits<WIN>(mk, qt, chunk, n_q, n_kv);
+        uint32_t bits = warp_valid_bits<MODE>(mk, qt, chunk, n_q, n_kv);
         while (bits != 0u && ok) {
           const int j = chunk * 32 + (__ffs(bits) - 1);
           bits &= bits - 1;
@@ -1069,7 +1110,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // WIN: whether this row's visible-key edge falls in the warpgroup's 32 columns
           const bool masked = WIN ? (j * kTile + 32 * wg < key_lo || j * kTile + 32 * wg + 32 > key_hi)
-                                  : tile_needs_element_mask<WIN>(mk, qt, j, kv_len);
+                                  : tile_needs_element_mask<MODE>(mk, qt, j, kv_len);
+          // the bias of a tile beyond the range of distances is one number
+          bool far_l = false, far_r = false;
+          uint64_t x2 = nl2, cs2 = c2;
+          if constexpr (REL) {
+            const int d0 = j * kTile - tile_pos(mk, qt);
+            far_l = rel_far_left(args.rel, d0);
+            far_r = rel_far_right(args.rel, d0);
+            const float nl = rel_far_bias(args.rel, rel_line(args.rel, bh % mk.H), d0) - lse2;
+            x2 = f2_pack(nl, nl);
+          }
           // ---- P = exp2(S c - lse2), kept as bf16 pairs
           if (!mbar_wait_warp(bars.s_full, sc++ & 1, tmo, abort_flag)) {
             fail();
@@ -1090,11 +1141,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
             tc_fence_before();
             mbar_arrive(bars.s_free);
+            if constexpr (REL) {
+              if (!far_l && !far_r) {  // each element's own bias; scores to log2 units
+                const float* lp = rel_line(args.rel, bh % mk.H) +
+                                  (j * kTile - tile_pos(mk, qt) - t + 32 * wg);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), c_log2, __ldg(lp + c)));
+                cs2 = f2_pack(1.f, 1.f);
+              }
+            }
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
               float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2,
-                               nl2),
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), cs2,
+                               x2),
                         x0, x1);
               p[c] = ex2_approx(x0);
               p[c + 1] = ex2_approx(x1);
@@ -1105,6 +1166,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int lim_local = key_hi - base, lo_local = key_lo - base;
 #pragma unroll
                 for (int c = 0; c < 32; ++c) p[c] = (c >= lo_local && c < lim_local) ? p[c] : 0.f;
+              }
+            } else if constexpr (CROSS) {
+              if (masked) {
+                int lo, lim;
+                visible_keys(mk, row + mk.q_off, j, kv_len, lo, lim);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  p[c] = (c >= lo - 32 * wg && c < lim - 32 * wg) ? p[c] : 0.f;
               }
             } else if (masked) {  // keys [0, lim) of this tile are allowed for this row
               int lim = kv_len - j * kTile;
@@ -1126,11 +1195,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           uint32_t pk[16];
           {
+            uint64_t s2[2] = {0ull, 0ull};  // packed sums of dS
             uint32_t dr[32];
             tmem_ld32(tDP, dr);
             tmem_ld_wait();
             tc_fence_before();
             mbar_arrive(bars.dp_free);
+            if constexpr (CROSS) {  // keys behind the length, whatever their V holds
+              const int lim = kv_len - j * kTile - 32 * wg;
+              if (lim < 32)
+#pragma unroll
+                for (int c = 0; c < 32; ++c) dr[c] = c < lim ? dr[c] : 0u;
+            }
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               uint32_t dp0 = dr[2 * c], dp1 = dr[2 * c + 1];
@@ -1144,8 +1220,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t t =
                   f2_fma(ks2, f2_pack(__uint_as_float(dp0), __uint_as_float(dp1)), nd2);
               float d0, d1;
-              f2_unpack(f2_mul(f2_pack(p[2 * c], p[2 * c + 1]), t), d0, d1);
+              const uint64_t ds = f2_mul(f2_pack(p[2 * c], p[2 * c + 1]), t);
+              if constexpr (REL) s2[c & 1] = f2_add(s2[c & 1], ds);
+              f2_unpack(ds, d0, d1);
               pk[c] = pack_bf16x2(d0, d1);
+            }
+            if constexpr (REL) {
+              float s0, s1;
+              f2_unpack(f2_add(s2[0], s2[1]), s0, s1);
+              sum_ds += s0 + s1;
+              if (far_l || far_r) {
+                uint64_t p2[2] = {0ull, 0ull};
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  p2[c & 1] = f2_add(p2[c & 1], f2_pack(p[2 * c], p[2 * c + 1]));
+                float p0, p1;
+                f2_unpack(f2_add(p2[0], p2[1]), p0, p1);
+                left_ds += far_l ? s0 + s1 : 0.f;
+                left_p += far_l ? p0 + p1 : 0.f;
+                right_ds += far_l ? 0.f : s0 + s1;
+                right_p += far_l ? 0.f : p0 + p1;
+              }
             }
           }
           if (gt > 0) {  // the previous dQ MMA has finished reading the dS buffer
@@ -1174,6 +1269,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(bars.ds_ready);
         ds_pending = false;
+      }
+      if constexpr (REL) {
+        if (args.row_sums != nullptr && row_in) {
+          const size_t rows = static_cast<size_t>(mk.B) * mk.H * N;
+          float* out = args.row_sums + static_cast<size_t>(wg) * rows + static_cast<size_t>(ridx);
+          const float sums[kRelRowSums] = {sum_ds, left_ds, right_ds, left_p, right_p};
+#pragma unroll
+          for (int k = 0; k < kRelRowSums; ++k) out[4 * rows * k] = sums[k];
+        }
       }
       // ---- epilogue: dQ = scale * acc, D/4 columns per warpgroup
       if (!mbar_wait_warp(bars.dq_full, unit_count & 1, tmo, abort_flag)) {
@@ -1258,15 +1362,17 @@ template <int D>
 cudaError_t launch_dkdv_split_d(const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, const CUtensorMap& tdo, const BwdArgs& a,
                                 bool dropout, int grid, cudaStream_t stream) {
-  const bool gqa = a.mask.Hkv != a.mask.H, win = a.mask.wl >= 0 || a.mask.wr >= 0;
-  auto pick = [&](auto drop) {
-    constexpr bool DR = decltype(drop)::value;
-    return gqa ? (win ? fa_bwd_dkdv_split_kernel<D, DR, true, true>
-                      : fa_bwd_dkdv_split_kernel<D, DR, true, false>)
-               : (win ? fa_bwd_dkdv_split_kernel<D, DR, false, true>
-                      : fa_bwd_dkdv_split_kernel<D, DR, false, false>);
+  auto pick = [&](auto drop, auto gqa) {
+    constexpr bool DR = decltype(drop)::value, G = decltype(gqa)::value;
+    return a.mode == kRel      ? fa_bwd_dkdv_split_kernel<D, DR, G, kRel>
+           : a.mode == kCross  ? fa_bwd_dkdv_split_kernel<D, DR, G, kCross>
+           : a.mode == kWindow ? fa_bwd_dkdv_split_kernel<D, DR, G, kWindow>
+                               : fa_bwd_dkdv_split_kernel<D, DR, G, kPlain>;
   };
-  auto kern = dropout ? pick(std::true_type{}) : pick(std::false_type{});
+  const std::true_type yes;
+  const std::false_type no;
+  auto kern = a.mask.Hkv != a.mask.H ? (dropout ? pick(yes, yes) : pick(no, yes))
+                                     : (dropout ? pick(yes, no) : pick(no, no));
   cudaError_t e = set_smem_split(kern, DkdvL<D>::kSmemBytes, true);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, DkdvL<D>::kSmemBytes, stream>>>(tq, tk, tv, tdo, a);
@@ -1277,12 +1383,17 @@ template <int D>
 cudaError_t launch_dq_split_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& tdo, const BwdArgs& a, bool dropout, int grid,
                               cudaStream_t stream) {
-  const bool win = a.mask.wl >= 0 || a.mask.wr >= 0;
-  auto kern = dropout ? (win ? fa_bwd_dq_split_kernel<D, true, true>
-                             : fa_bwd_dq_split_kernel<D, true, false>)
-                      : (win ? fa_bwd_dq_split_kernel<D, false, true>
-                             : fa_bwd_dq_split_kernel<D, false, false>);
-  const bool realloc = dropout ? DqRealloc<D, true>::value : DqRealloc<D, false>::value;
+  auto pick = [&](auto drop) {
+    constexpr bool DR = decltype(drop)::value;
+    return a.mode == kRel      ? fa_bwd_dq_split_kernel<D, DR, kRel>
+           : a.mode == kCross  ? fa_bwd_dq_split_kernel<D, DR, kCross>
+           : a.mode == kWindow ? fa_bwd_dq_split_kernel<D, DR, kWindow>
+                               : fa_bwd_dq_split_kernel<D, DR, kPlain>;
+  };
+  auto kern = dropout ? pick(std::true_type{}) : pick(std::false_type{});
+  const bool realloc = dropout ? DqRealloc<D, true, kPlain>::value
+                       : a.mode == kRel ? DqRealloc<D, false, kRel>::value
+                                        : DqRealloc<D, false, kPlain>::value;
   cudaError_t e = set_smem_split(kern, DqL<D>::kSmemBytes, realloc);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, DqL<D>::kSmemBytes, stream>>>(tq, tk, tv, tdo, a);
@@ -1294,7 +1405,7 @@ cudaError_t launch_dq_split_d(const CUtensorMap& tq, const CUtensorMap& tk, cons
 cudaError_t launch_bwd_dkdv_split(const CUtensorMap& tq, const CUtensorMap& tk,
                                   const CUtensorMap& tv, const CUtensorMap& tdo, const BwdArgs& a,
                                   int d, bool dropout, int num_sms, cudaStream_t stream) {
-  const int n_t = (a.mask.N + kTile - 1) / kTile;
+  const int n_t = (a.mask.Nk + kTile - 1) / kTile;
   const long long units = static_cast<long long>(a.mask.B) * a.mask.Hkv * n_t;  // (K/V head, key tile)
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
   if (grid <= 0) return cudaSuccess;

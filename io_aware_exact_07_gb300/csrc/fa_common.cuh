@@ -28,15 +28,54 @@ struct BarRun {
   }
 };
 
+// Instances of the bf16 forward and backward kernels. kPlain and kWindow have as many queries as
+// keys. kCross has Nq queries at positions q_off .. of an axis of Nk keys, with every mask but the
+// block mask; kRel adds a bias by relative position to it.
+enum Mode : int { kPlain = 0, kWindow = 1, kCross = 2, kRel = 3 };
+
 struct MaskParams {
-  int B, H, N;
+  int B, H, N;                  // N: query rows (and keys, but for kCross and kRel)
   int Hkv;                      // K/V heads (H for per-head attention; H / Hkv query heads share one)
   int nb;                       // ceil(N / 128): tiles per side, block-mask row length
   int causal;
   int wl, wr;                   // sliding window: keys i - wl .. i + wr visible (-1: unbounded)
   const uint8_t* block_mask;    // [nb, nb] or null
   const int32_t* seqlens_k;     // [B] or null
+  int Nk;                       // keys
+  int q_off;                    // kCross, kRel: query i sits at position i + q_off of the key axis
 };
+
+// The bias of the scores by relative position (kRel): the distance of key j from the query at
+// position p is j - p, and what lies beyond -left and right counts as these. Each head has a line
+// of its biases in log2 units, by distance from -left - kRelPad to right + kRelPad, so that the
+// distances of a tile that is not wholly beyond an end (at most 253 past it) need no clamp.
+constexpr int kRelPad = 256;
+struct RelParams {
+  const float* lines;           // [H, stride]
+  int left, right;
+  __host__ __device__ int stride() const { return left + right + 1 + 2 * kRelPad; }
+};
+
+// Where tile pair (qt, kt) lies: d0 is the distance of its first key from its first query, so its
+// distances are d0 - 127 .. d0 + 127. Left or right of the line's range the bias is one number.
+__device__ __forceinline__ bool rel_far_left(const RelParams& r, int d0) {
+  return d0 + (kTile - 1) <= -r.left;
+}
+__device__ __forceinline__ bool rel_far_right(const RelParams& r, int d0) {
+  return d0 - (kTile - 1) >= r.right;
+}
+
+// Line of head h, indexed by distance.
+__device__ __forceinline__ const float* rel_line(const RelParams& r, int h) {
+  return r.lines + static_cast<size_t>(h) * r.stride() + r.left + kRelPad;
+}
+
+// Bias of a tile pair that lies beyond an end of the range (0 for other pairs, whose elements
+// have their own).
+__device__ __forceinline__ float rel_far_bias(const RelParams& r, const float* line, int d0) {
+  return rel_far_left(r, d0) ? __ldg(line - r.left)
+                             : (rel_far_right(r, d0) ? __ldg(line + r.right) : 0.f);
+}
 
 struct DropParams {
   int p8;                       // drop iff Philox byte < p8
@@ -74,11 +113,33 @@ __device__ __forceinline__ int group_first_head(const MaskParams& m, int bhk) {
   return (bhk / m.Hkv) * m.H + (bhk % m.Hkv) * (m.H / m.Hkv);
 }
 
-// Number of valid keys of batch b (key padding clamps to [0, N]).
+// Number of valid keys of batch b (key padding clamps to [0, Nk]).
 __device__ __forceinline__ int kv_len_of(const MaskParams& m, int b) {
-  if (m.seqlens_k == nullptr) return m.N;
+  if (m.seqlens_k == nullptr) return m.Nk;
   int L = m.seqlens_k[b];
-  return L < 0 ? 0 : (L > m.N ? m.N : L);
+  return L < 0 ? 0 : (L > m.Nk ? m.Nk : L);
+}
+
+// kCross, kRel: position of the first row of query tile qt on the key axis.
+__device__ __forceinline__ int tile_pos(const MaskParams& m, int qt) {
+  return qt * kTile + m.q_off;
+}
+
+// Key tiles [0, bound) hold every tile that is valid for query tiles .. qt_end - 1: n_kv, or with
+// a causal mask those up to the last row's position.
+template <int MODE>
+__device__ __forceinline__ int key_tiles_upto(const MaskParams& m, int qt_end, int n_kv) {
+  int bound = n_kv;
+  if constexpr (MODE >= kCross) {
+    if (m.causal) {
+      const int end = tile_pos(m, qt_end);  // positions below it are reached
+      const int c = end > 0 ? (end - 1) / kTile + 1 : 0;
+      if (c < bound) bound = c;
+    }
+  } else {
+    if (m.causal && qt_end < bound) bound = qt_end;
+  }
+  return bound;
 }
 
 // Static schedule of the persistent kernels: in round k the CTAs take the
@@ -102,15 +163,22 @@ __device__ __forceinline__ int sched_unit(int k, bool rotate = false) {
 }
 
 // Whether the (query tile qt, key tile kt) pair has any allowed element.
-// n_kv = ceil(kv_len / 128), n_q = ceil(N / 128). With a sliding window (WIN:
-// a separate kernel instance, so that kernels without one keep their code)
+// n_kv = ceil(kv_len / 128), n_q = ceil(N / 128). With a sliding window (a
+// separate kernel instance, so that kernels without one keep their code)
 // the pair is skipped when the band i - wl <= j <= i + wr misses the tile.
-template <bool WIN = false>
+template <int MODE = kPlain>
 __device__ __forceinline__ bool tile_valid(const MaskParams& m, int qt, int kt, int n_q,
                                            int n_kv) {
   if (qt >= n_q || kt >= n_kv) return false;
+  if constexpr (MODE >= kCross) {
+    const int p0 = tile_pos(m, qt), k0 = kt * kTile;
+    if (m.causal && k0 > p0 + (kTile - 1)) return false;
+    if (m.wl >= 0 && k0 + (kTile - 1) + m.wl < p0) return false;
+    if (m.wr >= 0 && k0 > p0 + (kTile - 1) + m.wr) return false;
+    return true;
+  }
   if (m.causal && kt > qt) return false;
-  if constexpr (WIN) {
+  if constexpr (MODE == kWindow) {
     if (m.wl >= 0 && kt * kTile + (kTile - 1) + m.wl < qt * kTile) return false;
     if (m.wr >= 0 && kt * kTile > qt * kTile + (kTile - 1) + m.wr) return false;
   }
@@ -121,14 +189,49 @@ __device__ __forceinline__ bool tile_valid(const MaskParams& m, int qt, int kt, 
 // Whether the pair needs a per-element mask (causal diagonal, key tile
 // crossing kv_len, or a sliding-window edge inside the tile). Query rows
 // beyond N are never written, so the query tail needs none.
-template <bool WIN = false>
+template <int MODE = kPlain>
 __device__ __forceinline__ bool tile_needs_element_mask(const MaskParams& m, int qt, int kt,
                                                         int kv_len) {
-  if constexpr (WIN) {
+  if constexpr (MODE >= kCross) {
+    const int p0 = tile_pos(m, qt), k0 = kt * kTile;
+    return (m.causal && k0 + (kTile - 1) > p0) || (m.wl >= 0 && k0 < p0 + (kTile - 1) - m.wl) ||
+           (m.wr >= 0 && k0 + (kTile - 1) > p0 + m.wr) || k0 + kTile > kv_len;
+  }
+  if constexpr (MODE == kWindow) {
     if (m.wl >= 0 && kt * kTile < qt * kTile + (kTile - 1) - m.wl) return true;
     if (m.wr >= 0 && kt * kTile + (kTile - 1) > qt * kTile + m.wr) return true;
   }
   return (m.causal && kt == qt) || ((kt + 1) * kTile > kv_len);
+}
+
+// kCross, kRel: keys [lo, lim) of key tile kt, counted from its first, are visible to the query at
+// position pos.
+__device__ __forceinline__ void visible_keys(const MaskParams& m, int pos, int kt, int kv_len,
+                                             int& lo, int& lim) {
+  const int k0 = kt * kTile;
+  lim = kv_len - k0;
+  lo = 0;
+  if (m.causal) lim = min(lim, pos + 1 - k0);
+  if (m.wr >= 0) lim = min(lim, pos + m.wr + 1 - k0);
+  if (m.wl >= 0) lo = pos - m.wl - k0;
+}
+
+// kCross, kRel: the key tile that a length below Nk cuts (-1: none) has rows behind it, which may
+// hold anything; a weight of zero does not keep a NaN or an infinity there out of a product.
+// (Rows from Nk on arrive as zeros.)
+__device__ __forceinline__ int cut_tile(const MaskParams& m, int kv_len) {
+  return kv_len < m.Nk && kv_len % kTile != 0 ? kv_len / kTile : -1;
+}
+
+// Zeroes rows [first, 128) of a 128 x (64 CHUNKS) bf16 tile in shared memory, with `n` threads of
+// which this is thread i, and makes that visible to the tensor core's reads.
+template <int CHUNKS>
+__device__ __forceinline__ void zero_tile_rows(uint32_t tile, int first, int i, int n) {
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c)  // (a row's 128 bytes are permuted within themselves)
+    for (int u = first * 8 + i; u < kTile * 8; u += n)
+      st_shared_v4(tile + static_cast<uint32_t>(c * 16384 + u * 16), 0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
 }
 
 // Whether key j is inside query i's sliding window.
@@ -138,20 +241,20 @@ __device__ __forceinline__ bool in_window(const MaskParams& m, int i, int j) {
 
 // Bits j in [32*c, 32*c + 32) that are valid for query tile qt, computed by a
 // whole warp (one candidate per lane).
-template <bool WIN = false>
+template <int MODE = kPlain>
 __device__ __forceinline__ uint32_t warp_valid_bits(const MaskParams& m, int qt, int chunk,
                                                     int n_q, int n_kv) {
   const int lane = threadIdx.x & 31;
-  const bool v = tile_valid<WIN>(m, qt, chunk * 32 + lane, n_q, n_kv);
+  const bool v = tile_valid<MODE>(m, qt, chunk * 32 + lane, n_q, n_kv);
   return __ballot_sync(0xffffffffu, v);
 }
 
 // Same, transposed: query tiles qt in [32*c, 32*c + 32) valid for key tile kt.
-template <bool WIN = false>
+template <int MODE = kPlain>
 __device__ __forceinline__ uint32_t warp_valid_bits_t(const MaskParams& m, int kt, int chunk,
                                                       int n_q, int n_kv) {
   const int lane = threadIdx.x & 31;
-  const bool v = tile_valid<WIN>(m, chunk * 32 + lane, kt, n_q, n_kv);
+  const bool v = tile_valid<MODE>(m, chunk * 32 + lane, kt, n_q, n_kv);
   return __ballot_sync(0xffffffffu, v);
 }
 

@@ -114,7 +114,7 @@ __device__ __forceinline__ long long make_piece(const DecodeArgs& a, int cta, lo
 
 }  // namespace
 
-template <int D>
+template <int D, bool REL>
 __global__ void __launch_bounds__(kDecThreads, 1)
     fa_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k,
@@ -378,6 +378,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         vis = lc < vis ? lc : vis;
       }
       const int key_lo = args.wl >= 0 ? Lb - args.Nq + i - args.wl : 0;
+      // REL: this row's position, and the line of biases of its head
+      const int pos_q = Lb - args.Nq + i;
+      const float* line = nullptr;
+      if constexpr (REL)
+        line = rel_line(args.rel, (pc.bkv % args.Hkv) * G + (real ? r / args.Nq : 0));
       float m_ref = -INFINITY;  // reference maximum, scaled log2 units
       float l_sum = 0.f;        // running sum of exp2(s*c - m_ref)
       for (int j = pc.j0; j < pc.j1; ++j) {
@@ -403,6 +408,39 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           for (int k = 0; k < 128; ++k)
             if (k >= lim || k < lo) s[k] = -INFINITY;
         }
+        // The bias: one number for keys far from the row, else each element's own, which brings
+        // the scores to log2 units. Rows of a warp differ in both, so the warp decides together.
+        float cs = c_log2, far = 0.f;
+        if constexpr (REL) {
+          const int d0 = j * kTile - pos_q;  // distance of the tile's first key
+          const bool far_l = d0 + (kTile - 1) <= -args.rel.left, far_r = d0 >= args.rel.right;
+          if (__all_sync(0xffffffffu, far_l || far_r)) {
+            far = __ldg(line + (far_l ? -args.rel.left : args.rel.right));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              s[k] = fmaf(s[k], c_log2,
+                          __ldg(line + max(-args.rel.left, min(d0 + k, args.rel.right))));
+            cs = 1.f;
+          }
+          // Rows of V behind the length may hold anything (a weight of zero does not keep a NaN
+          // out of the product): zero them before the tile's PV.
+          if (Lb < args.Nk && Lb - j * kTile < kTile) {
+            const int stage = it % L::kStages;
+            if (!mbar_wait_warp(bars.v_full[stage], (it / L::kStages) & 1u, tmo, abort_flag)) {
+              fail();
+              ok = false;
+              break;
+            }
+            const uint32_t tile = sV + static_cast<uint32_t>(stage * L::kTileBytes);
+            const int first = Lb - j * kTile;
+#pragma unroll
+            for (int c = 0; c < L::kChunks; ++c)
+              for (int u = first * 8 + r; u < kTile * 8; u += 32 * n_sw)
+                st_shared_v4(tile + static_cast<uint32_t>(c * 16384 + u * 16), 0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+          }
+        }
         float mx[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx[k] = fmaxf(s[2 * k], s[2 * k + 1]);
@@ -410,9 +448,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         for (int k = 16; k < 128; k += 16)
 #pragma unroll
           for (int a = 0; a < 8; ++a) mx[a] = fmax3(mx[a], s[k + 2 * a], s[k + 2 * a + 1]);
-        const float m_tile = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                   fmaxf(mx[6], mx[7])) *
-                             c_log2;
+        const float mx_row = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
+                                   fmaxf(mx[6], mx[7]));
+        const float m_tile = REL ? fmaf(mx_row, cs, far) : mx_row * c_log2;
         const float m_new = fmaxf(m_ref, m_tile);
         const bool grow = m_new > m_ref + kDecRescale;
         float alpha = 1.f;
@@ -443,8 +481,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           }
         }
         const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-        const uint64_t c2 = f2_pack(c_log2, c_log2);
-        const uint64_t nm2 = f2_pack(-m_use, -m_use);
+        const uint64_t c2 = f2_pack(cs, cs);
+        const float nm = REL ? far - m_use : -m_use;
+        const uint64_t nm2 = f2_pack(nm, nm);
         uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -594,23 +633,26 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   if (lane == 0) a.lse[row] = den > 0.f ? m + __logf(den) : -INFINITY;
 }
 
+template <int D, bool REL>
+static cudaError_t launch_decode_d(const CUtensorMap& tq, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, const DecodeArgs& a, int grid,
+                                   cudaStream_t stream) {
+  auto kern = fa_decode_kernel<D, REL>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       DecL<D>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kDecThreads, DecL<D>::kSmemBytes, stream>>>(tq, tk, tv, a);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_decode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const DecodeArgs& a, int d, int grid, cudaStream_t stream) {
   if (grid <= 0) return cudaSuccess;
-  if (d == 64) {
-    auto kern = fa_decode_kernel<64>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         DecL<64>::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    kern<<<grid, kDecThreads, DecL<64>::kSmemBytes, stream>>>(tq, tk, tv, a);
-  } else {
-    auto kern = fa_decode_kernel<128>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         DecL<128>::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    kern<<<grid, kDecThreads, DecL<128>::kSmemBytes, stream>>>(tq, tk, tv, a);
-  }
-  return cudaGetLastError();
+  const bool rel = a.rel.lines != nullptr;
+  return d == 64 ? (rel ? launch_decode_d<64, true>(tq, tk, tv, a, grid, stream)
+                        : launch_decode_d<64, false>(tq, tk, tv, a, grid, stream))
+                 : (rel ? launch_decode_d<128, true>(tq, tk, tv, a, grid, stream)
+                        : launch_decode_d<128, false>(tq, tk, tv, a, grid, stream));
 }
 
 cudaError_t launch_decode_combine(const DecodeArgs& a, int d, cudaStream_t stream) {

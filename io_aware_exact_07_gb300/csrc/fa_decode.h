@@ -28,6 +28,7 @@ struct DecodeArgs {
   float* lse;                   // [B, H, Nq]
   float* o_part;                // [B*H*Nq, seg_max, d] fp32 (heads cut by CTA boundaries)
   float* lse_part;              // [B*H*Nq, seg_max]
+  RelParams rel;                // bias by relative position; lines null: none
 };
 
 cudaError_t launch_decode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -111,11 +111,12 @@ __device__ __forceinline__ UnitCoord decode_unit(int u, int BH, int H, int n_qbl
 
 }  // namespace
 
-template <int D, bool DROPOUT, bool WIN>
+template <int D, bool DROPOUT, int MODE>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const FwdArgs args) {
   using L = FwdLayout<D>;
+  constexpr bool WIN = MODE == kWindow, CROSS = MODE >= kCross, REL = MODE == kRel;
   // Without dropout each half of P is stored as soon as it is formed; with
   // dropout (more live registers) both halves are stored at the end, which keeps
   // that instance free of spills.
@@ -231,8 +232,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int kvh = kv_head(mk, uc.bh);  // K/V head of this query head
         const int kv_len = kv_len_of(mk, uc.b);
         const int n_kv = (kv_len + kTile - 1) / kTile;
-        int jmax = n_kv;
-        if (mk.causal && uc.qt0 + 2 < jmax) jmax = uc.qt0 + 2;
+        const int jmax = key_tiles_upto<MODE>(mk, uc.qt0 + 2, n_kv);
         if (unit_count > 0) {
           if (!mbar_wait_warp(bars.q_empty, (unit_count - 1) & 1, tmo, abort_flag)) {
             fail();
@@ -250,8 +250,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         ++q_armed;
         for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-          uint32_t bits = warp_valid_bits<WIN>(mk, uc.qt0, chunk, n_q, n_kv) |
-                          warp_valid_bits<WIN>(mk, uc.qt0 + 1, chunk, n_q, n_kv);
+          uint32_t bits = warp_valid_bits<MODE>(mk, uc.qt0, chunk, n_q, n_kv) |
+                          warp_valid_bits<MODE>(mk, uc.qt0 + 1, chunk, n_q, n_kv);
           while (bits != 0u) {
             const int j = chunk * 32 + (__ffs(bits) - 1);
             bits &= bits - 1;
@@ -337,8 +337,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const UnitCoord uc = decode_unit(u, BH, mk.H, n_qblk, mk.causal);
         const int kv_len = kv_len_of(mk, uc.b);
         const int n_kv = (kv_len + kTile - 1) / kTile;
-        int jmax = n_kv;
-        if (mk.causal && uc.qt0 + 2 < jmax) jmax = uc.qt0 + 2;
+        const int jmax = key_tiles_upto<MODE>(mk, uc.qt0 + 2, n_kv);
         const uint32_t uph = unit_count & 1;
         if (leader) {
           ok = mbar_wait(bars.q_full[0], uph, tmo, abort_flag) &&
@@ -347,8 +346,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-          const uint32_t va = warp_valid_bits<WIN>(mk, uc.qt0, chunk, n_q, n_kv);
-          const uint32_t vb = warp_valid_bits<WIN>(mk, uc.qt0 + 1, chunk, n_q, n_kv);
+          const uint32_t va = warp_valid_bits<MODE>(mk, uc.qt0, chunk, n_q, n_kv);
+          const uint32_t vb = warp_valid_bits<MODE>(mk, uc.qt0 + 1, chunk, n_q, n_kv);
           if (leader) {
             uint32_t bits = va | vb;
             while (bits != 0u && ok) {
@@ -415,8 +414,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const UnitCoord uc = decode_unit(u, BH, mk.H, n_qblk, mk.causal);
         const int kv_len = kv_len_of(mk, uc.b);
         const int n_kv = (kv_len + kTile - 1) / kTile;
-        int jmax = n_kv;
-        if (mk.causal && uc.qt0 + 2 < jmax) jmax = uc.qt0 + 2;
+        const int jmax = key_tiles_upto<MODE>(mk, uc.qt0 + 2, n_kv);
         bool first0 = true, first1 = true;
         // The first PV of query tile x in a unit overwrites O_x, which the
         // previous unit's epilogue reads: it waits for that epilogue (o_free[x])
@@ -445,10 +443,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           return true;
         };
         for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-          const uint32_t va = warp_valid_bits<WIN>(mk, uc.qt0, chunk, n_q, n_kv);
-          const uint32_t vb = warp_valid_bits<WIN>(mk, uc.qt0 + 1, chunk, n_q, n_kv);
-          if (leader) {
-            uint32_t bits = va | vb;
+          const uint32_t va = warp_valid_bits<MODE>(mk, uc.qt0, chunk, n_q, n_kv);
+          const uint32_t vb = warp_valid_bits<MODE>(mk, uc.qt0 + 1, chunk, n_q, n_kv);
+          auto issue = [&](uint32_t bits) {
             while (bits != 0u && ok) {
               const int bit = __ffs(bits) - 1;
               bits &= bits - 1;
@@ -466,6 +463,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               ++it;
             }
             if (!ok) fail();
+          };
+          uint32_t cut = 0u;  // the tile that the length cuts: the last of the unit
+          if constexpr (CROSS) {
+            const int jc = cut_tile(mk, kv_len);
+            if (jc >= 0 && jc / 32 == chunk) cut = (va | vb) & (1u << (jc & 31));
+          }
+          if (leader) issue((va | vb) & ~cut);
+          if constexpr (CROSS) {
+            if (cut != 0u) {
+              const uint32_t n = __shfl_sync(0xffffffffu, it, 0);
+              const int s = n % L::kStages;
+              if (mbar_wait_warp(bars.v_full[s], (n / L::kStages) & 1u, tmo, abort_flag))
+                zero_tile_rows<L::kChunks>(sV + s * L::kTileBytes, kv_len % kTile, lane, 32);
+              __syncwarp();
+              if (leader) issue(cut);
+            }
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
@@ -504,8 +517,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int row = qt * kTile + t;
       const int kv_len = kv_len_of(mk, uc.b);
       const int n_kv = (kv_len + kTile - 1) / kTile;
-      int jmax = n_kv;
-      if (mk.causal && qt + 1 < jmax) jmax = qt + 1;
+      const int jmax = key_tiles_upto<MODE>(mk, qt + 1, n_kv);
       // sliding window: keys [key_lo, key_hi) are visible to this row
       int key_lo = 0, key_hi = kv_len;
       if constexpr (WIN) {
@@ -519,7 +531,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const uint32_t row_global = static_cast<uint32_t>(uc.bh) * static_cast<uint32_t>(N) +
                                   static_cast<uint32_t>(row);
       for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-        uint32_t bits = warp_valid_bits<WIN>(mk, qt, chunk, n_q, n_kv);
+        uint32_t bits = warp_valid_bits<MODE>(mk, qt, chunk, n_q, n_kv);
         while (bits != 0u) {
           const int j = chunk * 32 + (__ffs(bits) - 1);
           bits &= bits - 1;
@@ -547,7 +559,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               for (int k = 0; k < 128; ++k)
                 if (k >= lim || k < lo) s[k] = -INFINITY;
             }
-          } else if (tile_needs_element_mask<WIN>(mk, qt, j, kv_len)) {
+          } else if constexpr (CROSS) {
+            if (tile_needs_element_mask<MODE>(mk, qt, j, kv_len)) {
+              int lo, lim;
+              visible_keys(mk, row + mk.q_off, j, kv_len, lo, lim);
+#pragma unroll
+              for (int k = 0; k < 128; ++k)
+                if (k >= lim || k < lo) s[k] = -INFINITY;
+            }
+          } else if (tile_needs_element_mask<MODE>(mk, qt, j, kv_len)) {
             int lim = kv_len - j * kTile;                 // keys [0, lim) of this tile are valid
             if (mk.causal) {
               const int lc = row - j * kTile + 1;       // causal: key <= row
@@ -556,6 +576,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
             for (int k = 0; k < 128; ++k)
               if (k >= lim) s[k] = -INFINITY;
+          }
+          // The bias: one number far from the diagonal, else each element's own, which brings
+          // the scores to log2 units.
+          float cs = c_log2, far = 0.f;
+          if constexpr (REL) {
+            const int d0 = j * kTile - tile_pos(mk, qt);
+            const float* line = rel_line(args.rel, uc.h);
+            if (rel_far_left(args.rel, d0) || rel_far_right(args.rel, d0)) {
+              far = rel_far_bias(args.rel, line, d0);
+            } else {
+              const float* lp = line + (d0 - t);
+#pragma unroll
+              for (int k = 0; k < 128; ++k) s[k] = fmaf(s[k], c_log2, __ldg(lp + k));
+              cs = 1.f;
+            }
           }
           // Row maximum: three-input max over eight independent accumulators.
           float mx[8];
@@ -567,7 +602,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int a = 0; a < 8; ++a) mx[a] = fmax3(mx[a], s[k + 2 * a], s[k + 2 * a + 1]);
           const float mx_row = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
                                      fmaxf(mx[6], mx[7]));
-          const float m_tile = mx_row * c_log2;
+          const float m_tile = REL ? fmaf(mx_row, cs, far) : mx_row * c_log2;
           const float m_new = fmaxf(m_ref, m_tile);
           const bool grow = m_new > m_ref + kRescaleThreshold;
           float alpha = 1.f;
@@ -580,8 +615,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           // P = exp2(s*c - m_ref), summed (undropped) into l, dropout applied,
           // packed to bf16 and stored over S, 64 columns at a time. The scale
           // and subtract and the row sum run on packed pairs of lanes.
-          const uint64_t c2 = f2_pack(c_log2, c_log2);
-          const uint64_t nm2 = f2_pack(-m_use, -m_use);
+          const uint64_t c2 = f2_pack(cs, cs);
+          const float nm = REL ? far - m_use : -m_use;
+          const uint64_t nm2 = f2_pack(nm, nm);
           uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // four packed partial sums
           uint32_t pk[64];
           bool pv_ok = true;
@@ -745,8 +781,10 @@ static cudaError_t launch_fwd_impl(const CUtensorMap& tq, const CUtensorMap& tk,
                                    const CUtensorMap& tv, const FwdArgs& a, int grid,
                                    cudaStream_t stream) {
   using L = FwdLayout<D>;
-  const bool win = a.mask.wl >= 0 || a.mask.wr >= 0;
-  auto kern = win ? fa_fwd_kernel<D, DROPOUT, true> : fa_fwd_kernel<D, DROPOUT, false>;
+  auto kern = a.mode == kRel     ? fa_fwd_kernel<D, DROPOUT, kRel>
+              : a.mode == kCross ? fa_fwd_kernel<D, DROPOUT, kCross>
+              : a.mode == kWindow ? fa_fwd_kernel<D, DROPOUT, kWindow>
+                                  : fa_fwd_kernel<D, DROPOUT, kPlain>;
   // The in-kernel register reallocation assumes kRegsLaunch registers per thread
   // at launch: with fewer, the softmax warpgroups' increase could never be
   // granted and would wait forever, so such a kernel is refused.

@@ -104,20 +104,14 @@ __device__ __forceinline__ Unit decode_unit(int u, int H, int n_q, int causal) {
   return c;
 }
 
-// Key tiles [0, jmax) can hold valid tiles of query tile qt.
-__device__ __forceinline__ int key_tile_bound(const MaskParams& mk, int qt, int n_kv) {
-  int jmax = n_kv;
-  if (mk.causal && qt + 1 < jmax) jmax = qt + 1;
-  return jmax;
-}
-
 }  // namespace
 
-template <bool DROPOUT, bool WIN>
+template <bool DROPOUT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_fwd128_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const FwdArgs args) {
   using L = Layout;
+  constexpr bool WIN = MODE == kWindow, CROSS = MODE >= kCross, REL = MODE == kRel;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (threadIdx.x == 0) record_error(args.sync.status, kStatusCuda);
@@ -234,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit uc = decode_unit(u, mk.H, n_q, mk.causal);
         const int kvh = kv_head(mk, uc.bh);
         const int n_kv = (kv_len_of(mk, uc.b) + kTile - 1) / kTile;
-        const int jmax = key_tile_bound(mk, uc.qt, n_kv);
+        const int jmax = key_tiles_upto<MODE>(mk, uc.qt + 1, n_kv);
         if (is_k) {
           if (unit_count > 0 &&
               !mbar_wait_warp(bars.q_empty, (unit_count - 1) & 1, tmo, abort_flag)) {
@@ -250,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++q_armed;
         }
         for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-          uint32_t bits = warp_valid_bits<WIN>(mk, uc.qt, chunk, n_q, n_kv);
+          uint32_t bits = warp_valid_bits<MODE>(mk, uc.qt, chunk, n_q, n_kv);
           while (bits != 0u) {
             const int j = chunk * 32 + (__ffs(bits) - 1);
             bits &= bits - 1;
@@ -303,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
         const Unit uc = decode_unit(u, mk.H, n_q, mk.causal);
         const int n_kv = (kv_len_of(mk, uc.b) + kTile - 1) / kTile;
-        const int jmax = key_tile_bound(mk, uc.qt, n_kv);
+        const int jmax = key_tiles_upto<MODE>(mk, uc.qt + 1, n_kv);
         // The tensor core runs products in issue order: the next unit's S products
         // wait until the PV issuer has issued this unit's last PV, so that they
         // do not delay it (the softmax warpgroups' epilogue waits for that PV; they
@@ -325,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         int pos = 0;  // position in the unit's tile list
         for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-          const uint32_t bits = warp_valid_bits<WIN>(mk, uc.qt, chunk, n_q, n_kv);
+          const uint32_t bits = warp_valid_bits<MODE>(mk, uc.qt, chunk, n_q, n_kv);
           if (leader) {
             uint32_t b = bits;
             int p = pos;
@@ -391,17 +385,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       int unit_count = 0;
       for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
         const Unit uc = decode_unit(u, mk.H, n_q, mk.causal);
-        const int n_kv = (kv_len_of(mk, uc.b) + kTile - 1) / kTile;
-        const int jmax = key_tile_bound(mk, uc.qt, n_kv);
+        const int kv_len = kv_len_of(mk, uc.b);
+        const int n_kv = (kv_len + kTile - 1) / kTile;
+        const int jmax = key_tiles_upto<MODE>(mk, uc.qt + 1, n_kv);
         // The first PV of a unit overwrites O_0 or O_1, which the previous unit's
         // epilogue reads: it waits for that epilogue (o_free).
         bool first_any = true, first0 = true, first1 = true;
         int pos = 0;
         for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-          const uint32_t bits = warp_valid_bits<WIN>(mk, uc.qt, chunk, n_q, n_kv);
-          if (leader) {
-            uint32_t b = bits;
-            int p = pos;
+          const uint32_t bits = warp_valid_bits<MODE>(mk, uc.qt, chunk, n_q, n_kv);
+          int p = pos;
+          auto issue = [&](uint32_t b) {
             while (b != 0u && ok) {
               b &= b - 1;
               const int g = p & 1;
@@ -442,6 +436,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++p;
             }
             if (!ok) fail();
+          };
+          uint32_t cut = 0u;  // the tile that the length cuts: the last of the unit
+          if constexpr (CROSS) {
+            const int jc = cut_tile(mk, kv_len);
+            if (jc >= 0 && jc / 32 == chunk) cut = bits & (1u << (jc & 31));
+          }
+          if (leader) issue(bits & ~cut);
+          if constexpr (CROSS) {
+            if (cut != 0u) {
+              const uint32_t n = __shfl_sync(0xffffffffu, it, 0);
+              const int s = n & 1;
+              if (mbar_wait_warp(bars.v_full[s], (n >> 1) & 1u, tmo, abort_flag))
+                zero_tile_rows<2>(sV + s * L::kTileBytes, kv_len % kTile, lane, 32);
+              __syncwarp();
+              if (leader) issue(cut);
+            }
           }
           pos += __popc(bits);
           ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -487,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = uc.qt * kTile + t;
       const int kv_len = kv_len_of(mk, uc.b);
       const int n_kv = (kv_len + kTile - 1) / kTile;
-      const int jmax = key_tile_bound(mk, uc.qt, n_kv);
+      const int jmax = key_tiles_upto<MODE>(mk, uc.qt + 1, n_kv);
       // sliding window: keys [key_lo, key_hi) are visible to this row
       int key_lo = 0, key_hi = kv_len;
       if constexpr (WIN) {
@@ -502,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t row_global = static_cast<uint32_t>(uc.bh) * static_cast<uint32_t>(N) +
                                   static_cast<uint32_t>(row);
       for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
-        uint32_t bits = warp_valid_bits<WIN>(mk, uc.qt, chunk, n_q, n_kv);
+        uint32_t bits = warp_valid_bits<MODE>(mk, uc.qt, chunk, n_q, n_kv);
         while (bits != 0u) {
           const int j = chunk * 32 + (__ffs(bits) - 1);
           bits &= bits - 1;
@@ -531,7 +541,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 128; ++k)
                 if (k >= lim || k < lo) s[k] = -INFINITY;
             }
-          } else if (tile_needs_element_mask<WIN>(mk, uc.qt, j, kv_len)) {
+          } else if constexpr (CROSS) {
+            if (tile_needs_element_mask<MODE>(mk, uc.qt, j, kv_len)) {
+              int lo, lim;
+              visible_keys(mk, row + mk.q_off, j, kv_len, lo, lim);
+#pragma unroll
+              for (int k = 0; k < 128; ++k)
+                if (k >= lim || k < lo) s[k] = -INFINITY;
+            }
+          } else if (tile_needs_element_mask<MODE>(mk, uc.qt, j, kv_len)) {
             int lim = kv_len - j * kTile;                 // keys [0, lim) of this tile are valid
             if (mk.causal) {
               const int lc = row - j * kTile + 1;       // causal: key <= row
@@ -540,6 +558,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 128; ++k)
               if (k >= lim) s[k] = -INFINITY;
+          }
+          // The bias: one number far from the diagonal, else each element's own, which brings
+          // the scores to log2 units.
+          float cs = c_log2, far = 0.f;
+          if constexpr (REL) {
+            const int d0 = j * kTile - tile_pos(mk, uc.qt);
+            const float* line = rel_line(args.rel, uc.bh - uc.b * mk.H);
+            if (rel_far_left(args.rel, d0) || rel_far_right(args.rel, d0)) {
+              far = rel_far_bias(args.rel, line, d0);
+            } else {
+              const float* lp = line + (d0 - t);
+#pragma unroll
+              for (int k = 0; k < 128; ++k) s[k] = fmaf(s[k], c_log2, __ldg(lp + k));
+              cs = 1.f;
+            }
           }
           // Row maximum: three-input max over eight independent accumulators.
           float mx[8];
@@ -551,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int a = 0; a < 8; ++a) mx[a] = fmax3(mx[a], s[k + 2 * a], s[k + 2 * a + 1]);
           const float mx_row = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
                                      fmaxf(mx[6], mx[7]));
-          const float m_new = fmaxf(m_ref, mx_row * c_log2);
+          const float m_new = fmaxf(m_ref, REL ? fmaf(mx_row, cs, far) : mx_row * c_log2);
           const bool grow = m_new > m_ref + kRescaleThreshold;
           float alpha = 1.f;
           if (grow) {
@@ -562,8 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
           // P = exp2(s*c - m_ref), summed (undropped) into l, dropout applied,
           // packed to bf16 and stored into P_g, which the previous PV reads.
-          const uint64_t c2 = f2_pack(c_log2, c_log2);
-          const uint64_t nm2 = f2_pack(-m_use, -m_use);
+          const uint64_t c2 = f2_pack(cs, cs);
+          const float nm = REL ? far - m_use : -m_use;
+          const uint64_t nm2 = f2_pack(nm, nm);
           uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // four packed partial sums
           uint32_t pk[64];
           bool pv_ok = true;
@@ -793,8 +827,10 @@ template <bool DROPOUT>
 static cudaError_t launch_fwd128_impl(const CUtensorMap& tq, const CUtensorMap& tk,
                                       const CUtensorMap& tv, const FwdArgs& a, int grid,
                                       cudaStream_t stream) {
-  const bool win = a.mask.wl >= 0 || a.mask.wr >= 0;
-  auto kern = win ? fa_fwd128_kernel<DROPOUT, true> : fa_fwd128_kernel<DROPOUT, false>;
+  auto kern = a.mode == kRel     ? fa_fwd128_kernel<DROPOUT, kRel>
+              : a.mode == kCross ? fa_fwd128_kernel<DROPOUT, kCross>
+              : a.mode == kWindow ? fa_fwd128_kernel<DROPOUT, kWindow>
+                                  : fa_fwd128_kernel<DROPOUT, kPlain>;
   // The in-kernel register reallocation assumes kRegsLaunch registers per thread
   // at launch: with fewer, the softmax warpgroups' increase could never be
   // granted and would wait forever, so such a kernel is refused.

@@ -16,6 +16,8 @@ struct FwdArgs {
   float scale_log2;  // scale * log2(e)
   __nv_bfloat16* o;  // [B, H, N, d]
   float* lse;        // [B, H, N]
+  int mode;          // Mode
+  RelParams rel;     // kRel
 };
 
 struct BwdArgs {
@@ -31,7 +33,16 @@ struct BwdArgs {
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
+  int mode;          // Mode
+  RelParams rel;     // kRel
+  // kRel, for the gradient of the bias (null: not wanted): what each of the dQ kernel's four
+  // warpgroups saw of a query row, [kRelRowSums][4][B*H*N] fp32
+  float* row_sums;
 };
+
+// Sums over the keys of a query row: dS, dS left of the range of distances, dS right of it, P
+// left of it, P right of it.
+constexpr int kRelRowSums = 5;
 
 // Tensor maps of a [B*H, N, d] bf16 tensor with 128 x 64 boxes, 128-byte swizzle.
 cudaError_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -59,6 +70,33 @@ cudaError_t launch_bwd_dkdv_split(const CUtensorMap& tq, const CUtensorMap& tk,
 cudaError_t launch_bwd_dq_split(const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, const CUtensorMap& tdo, const BwdArgs& a,
                                 int d, bool dropout, int num_sms, cudaStream_t stream);
+
+// Relative position bias (fa_rel.cu).
+struct RelLinesArgs {
+  const void* table;   // [num_buckets, H], fp32 or bf16
+  bool bf16;
+  const int32_t* map;  // [left + right + 1]
+  int left, right, num_buckets, H;
+  float* lines;
+  unsigned int* status;
+};
+cudaError_t launch_rel_lines(const RelLinesArgs& a, cudaStream_t stream);
+
+struct RelGradArgs {
+  BwdArgs b;             // dsum becomes the D of the unrounded O
+  const int32_t* map;
+  int num_buckets;
+  float* dtable;         // [num_buckets, H]
+  int first, n_diag;     // near tile pairs: kt - qt = first .. first + n_diag - 1
+  float* diag_sums;      // [H * n_diag + kRelMaxCtas][4][160]
+  double* far_sums;      // [B * H, ceil(N / kRelRows)][2]
+};
+constexpr int kRelMaxCtas = 512;
+constexpr int kRelRows = 1024;      // query rows whose far sums a block forms
+constexpr int kRelDiagFloats = 640; // 4 column chunks x 160 diagonals
+cudaError_t launch_rel_grad(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                            const CUtensorMap& tdo, const RelGradArgs& a, int d, bool dropout,
+                            int num_sms, cudaStream_t stream);
 
 cudaError_t launch_debug_dropout(uint8_t* keep, int B, int H, int N, const DropParams& d,
                                  cudaStream_t stream);

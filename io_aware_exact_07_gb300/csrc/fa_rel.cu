@@ -1,0 +1,533 @@
+// Learned relative position bias: the lines of biases that the attention kernels read, and the
+// gradient of the table they come from.
+//
+// The score of key j for the query at position p gets table[map[clamp(j - p, -left, right) + left],
+// h]. A head's biases by distance form one line, which is a few KB for the usual rules, so the
+// attention kernels read it from L1 or add one number to a whole tile that lies beyond an end of
+// the range. The gradient of a table entry is the sum of dS over the pairs whose distance maps to
+// it:
+//   dS_ij = P_ij (Z_ij/(1-p) dO_i.v_j - D_i),  D_i = sum_j P_ij Z_ij/(1-p) dO_i.v_j.
+// The backward kernels take D_i from the rounded O. That is off by up to 2^-9 |dO_i||O_i|, and a
+// sum over many pairs of one row collects it: R_i = sum_j dS_ij would be zero with the exact D_i
+// (the weights of a row sum to one), so D_i + R_i is the D of the unrounded O, and the sum of dS
+// over a set of keys of the row is corrected by -R_i times their weights' sum. The dQ kernel
+// leaves R_i and the sums of dS and P over the tiles beyond either end of the range:
+//   rel_rows    adds R to D and sums up the two far fields;
+//   rel_near    recomputes dS on the tiles near the diagonal. For a fixed kt - qt every tile has
+//               the same distance at the same place, so a CTA adds tiles of a head and kt - qt,
+//               over batch rows and query tiles, element by element in registers and forms the
+//               sums along the diagonals once, when it moves on;
+//   rel_table   adds the diagonals' and far fields' sums up by bucket, in fp64.
+// No atomics: the order of every sum is fixed.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fa_common.cuh"
+#include "fa_kernels.h"
+
+namespace fa {
+
+namespace {
+
+constexpr unsigned kStatusInvalid = 1u;
+
+__device__ __forceinline__ int clamp_distance(int x, int left, int right) {
+  return x < -left ? -left : (x > right ? right : x);
+}
+
+// ------------------------------------------------------------------ lines
+__global__ void __launch_bounds__(256) rel_lines_kernel(const RelLinesArgs a) {
+  const RelParams r{nullptr, a.left, a.right};
+  const int e = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y;
+  if (e >= r.stride()) return;
+  const int n = __ldg(a.map + clamp_distance(e - a.left - kRelPad, a.left, a.right) + a.left);
+  float x = 0.f;
+  if (n < 0 || n >= a.num_buckets) {
+    record_error(a.status, kStatusInvalid);
+  } else {
+    const size_t at = static_cast<size_t>(n) * a.H + h;
+    x = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.table)[at])
+               : static_cast<const float*>(a.table)[at];
+  }
+  a.lines[static_cast<size_t>(h) * r.stride() + e] = x * kLog2e;
+}
+
+// ------------------------------------------------------------------ rows
+// One block takes kRelRows query rows of a head (b, h).
+__global__ void __launch_bounds__(256) rel_rows_kernel(const RelGradArgs a, int chunks) {
+  const int bh = blockIdx.x / chunks, chunk = blockIdx.x % chunks, N = a.b.mask.N;
+  const size_t rows = static_cast<size_t>(a.b.mask.B) * a.b.mask.H * N;
+  double left = 0.0, right = 0.0;
+  for (int i = threadIdx.x; i < kRelRows; i += 256) {
+    const int row = chunk * kRelRows + i;
+    if (row >= N) break;
+    const size_t idx = static_cast<size_t>(bh) * N + row;
+    float s[kRelRowSums];
+#pragma unroll
+    for (int k = 0; k < kRelRowSums; ++k) {
+      const float* p = a.b.row_sums + 4 * rows * k + idx;
+      s[k] = (p[0] + p[rows]) + (p[2 * rows] + p[3 * rows]);
+    }
+    a.b.dsum[idx] += s[0];
+    left += static_cast<double>(s[1]) - static_cast<double>(s[0]) * s[3];
+    right += static_cast<double>(s[2]) - static_cast<double>(s[0]) * s[4];
+  }
+  __shared__ double part[2][8];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    left += __shfl_xor_sync(0xffffffffu, left, o);
+    right += __shfl_xor_sync(0xffffffffu, right, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    part[0][threadIdx.x >> 5] = left;
+    part[1][threadIdx.x >> 5] = right;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    double x = 0.0;
+    for (int w = 0; w < 8; ++w) x += part[threadIdx.x][w];
+    a.far_sums[static_cast<size_t>(blockIdx.x) * 2 + threadIdx.x] = x;
+  }
+}
+
+// ------------------------------------------------------------------ near tiles
+// The list of near tile pairs: by head, then kt - qt (a group of pairs has one of each), then
+// batch row, then query tile. CTA c takes per_cta of them from c * per_cta on.
+struct NearList {
+  int n_q, n_k, B, first, n_diag;
+  __device__ int begin(int g) const { return max(0, -(first + g)); }  // query tiles of kt - qt
+  __device__ int count(int g) const { return max(0, min(n_q, n_k - (first + g)) - begin(g)); }
+  __device__ long long head_total() const {
+    long long n = 0;
+    for (int g = 0; g < n_diag; ++g) n += count(g);
+    return n * B;
+  }
+};
+
+__device__ __forceinline__ NearList near_list(const RelGradArgs& a) {
+  NearList l;
+  l.n_q = (a.b.mask.N + kTile - 1) / kTile;
+  l.n_k = (a.b.mask.Nk + kTile - 1) / kTile;
+  l.B = a.b.mask.B;
+  l.first = a.first;
+  l.n_diag = a.n_diag;
+  return l;
+}
+
+__device__ __forceinline__ long long near_per_cta(long long total, int ctas) {
+  return (total + ctas - 1) / ctas;
+}
+
+// A walk over the pairs of one CTA.
+struct NearWalk {
+  NearList l;
+  long long left;  // pairs from here on, this one included
+  int h, g, b, i;  // head, group of the head, batch row, query tile counted from the group's first
+  int n;           // query tiles of the group
+
+  __device__ NearWalk(const NearList& list, int H, int ctas, int cta) : l(list) {
+    const long long per_head = l.head_total(), total = per_head * H;
+    const long long per = near_per_cta(total, ctas), at = per * cta;
+    left = max(0ll, min(per, total - at));
+    h = g = b = i = n = 0;
+    if (left == 0) return;
+    h = static_cast<int>(at / per_head);
+    long long rest = at % per_head;
+    while (rest >= static_cast<long long>(l.count(g)) * l.B) {
+      rest -= static_cast<long long>(l.count(g)) * l.B;
+      ++g;
+    }
+    n = l.count(g);
+    b = static_cast<int>(rest / n);
+    i = static_cast<int>(rest % n);
+  }
+  __device__ int qt() const { return l.begin(g) + i; }
+  __device__ int kt() const { return qt() + l.first + g; }
+  __device__ int group() const { return h * l.n_diag + g; }
+  __device__ void next() {
+    --left;
+    if (++i < n) return;
+    i = 0;
+    if (++b < l.B) return;
+    b = 0;
+    do {
+      if (++g == l.n_diag) {
+        g = 0;
+        ++h;
+      }
+      n = l.count(g);
+    } while (n == 0 && left > 0);
+  }
+};
+
+constexpr int kNearThreads = 10 * 32;
+constexpr int kNearProducerWarp = 8;
+constexpr int kNearMmaWarp = 9;
+constexpr int kDiagPitch = 33;
+
+template <int D>
+struct NearL {
+  static constexpr int T = kTile * D * 2;
+  static constexpr int kChunks = D / 64;
+  static constexpr int kStages = D == 64 ? 6 : 3;  // ring of tile pairs: (Q, K), (dO, V), ...
+  static constexpr int kDiagOff = kStages * 2 * T;
+  static constexpr int kLineOff = kDiagOff + 2 * kTile * kDiagPitch * 4;
+  static constexpr int kBarOff = kLineOff + 2 * 192 * 4;
+  static constexpr int kNumBars = 2 * kStages + 4 + 1;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  // no slack for rounding the base up: the kernel checks its alignment
+  static constexpr int kSmemBytes = kMiscOff + 16;
+  static_assert(kSmemBytes <= 232448, "shared memory exceeds the per-block limit");
+};
+
+template <int D, bool DROPOUT>
+__global__ void __launch_bounds__(kNearThreads, 1)
+    rel_near_kernel(const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_do, const RelGradArgs args) {
+  using L = NearL<D>;
+  constexpr int T = L::T;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0u) {  // uniform over the block: nothing has started yet
+    if (threadIdx.x == 0) record_error(args.b.sync.status, kStatusCuda);
+    return;
+  }
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const MaskParams& mk = args.b.mask;
+  const int N = mk.N;
+
+  uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff + 8);
+  const BarRun full{smem_u32(bar_mem)};                          // ring stages
+  const BarRun empty{full.base + 8u * L::kStages};
+  const BarRun s_full{empty.base + 8u * L::kStages};             // S and dP buffers
+  const BarRun s_free{s_full.base + 16u};
+  const uint32_t drain = s_free.base + 16u;
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(full[s], 1);
+      mbar_init(empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full[x], 1);
+      mbar_init(s_free[x], 256);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kNearMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint64_t tmo = args.b.sync.timeout_ns;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    record_error(args.b.sync.status, kStatusTimeout);
+  };
+  const uint32_t sRing = smem_u32(smem);
+  const NearList list = near_list(args);
+  NearWalk w(list, mk.H, gridDim.x, blockIdx.x);
+  auto valid = [&](const NearWalk& w) {
+    const int n_kv = (kv_len_of(mk, w.b) + kTile - 1) / kTile;
+    return tile_valid<kRel>(mk, w.qt(), w.kt(), list.n_q, n_kv);
+  };
+
+  if (warp == kNearProducerWarp) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (; w.left > 0 && ok; w.next()) {
+        if (!valid(w)) continue;
+        const int bh = w.b * mk.H + w.h, kvh = kv_head(mk, bh);
+        for (int half = 0; half < 2; ++half, ++it) {
+          const int s = it % L::kStages;
+          if (!mbar_wait(empty[s], ((it / L::kStages) & 1u) ^ 1u, tmo, abort_flag)) {
+            fail();
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(full[s], 2 * T);
+          for (int c = 0; c < L::kChunks; ++c) {
+            tma_load_3d(sRing + (2 * s) * T + c * 16384, half ? &tm_do : &tm_q, c * 64,
+                        w.qt() * kTile, bh, full[s]);
+            tma_load_3d(sRing + (2 * s + 1) * T + c * 16384, half ? &tm_v : &tm_k, c * 64,
+                        w.kt() * kTile, kvh, full[s]);
+          }
+        }
+      }
+      // every load issued here must land before the CTA exits
+      for (int s = 0; s < L::kStages; ++s)
+        if (it > static_cast<uint32_t>(s))
+          mbar_wait(full[s], ((it - 1 - s) / L::kStages) & 1, tmo, nullptr);
+    }
+    __syncwarp();
+  } else if (warp == kNearMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t kId = idesc_bf16_f32(128, 128, 0, 0);
+      uint32_t it = 0;
+      bool ok = true;
+      for (; w.left > 0 && ok; w.next()) {
+        if (!valid(w)) continue;
+        const uint32_t n = it >> 1, x = n & 1u;  // pairs so far; S and dP buffer
+        if (n >= 2 && !mbar_wait(s_free[x], ((n >> 1) - 1) & 1u, tmo, abort_flag)) {
+          fail();
+          break;
+        }
+        for (uint32_t half = 0; half < 2; ++half, ++it) {
+          const int s = it % L::kStages;
+          if (!mbar_wait(full[s], (it / L::kStages) & 1u, tmo, abort_flag)) {
+            fail();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = sdesc_sw128(sRing + (2 * s) * T, 16, 1024);
+          const uint64_t db = sdesc_sw128(sRing + (2 * s + 1) * T, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+            mma_ss(tmem + 256u * x + 128u * half, da + off, db + off, kId, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(empty[s]);
+        }
+        if (ok) mma_commit(s_full[x]);
+      }
+      mma_commit(drain);
+      mbar_wait(drain, 0, tmo, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // Warpgroup wg owns key columns [64 wg, 64 wg + 64) of every tile; the thread owns a query row.
+    const int wg = warp >> 2, quad = warp & 3;
+    const int t = quad * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    float* diag = reinterpret_cast<float*>(smem + L::kDiagOff) + wg * kTile * kDiagPitch;
+    float* line_s = reinterpret_cast<float*>(smem + L::kLineOff) + wg * 192;
+    const float c_log2 = args.b.scale_log2;
+    const uint64_t c2 = f2_pack(c_log2, c_log2);
+    const uint64_t ks2 = f2_pack(args.b.drop.keep_scale, args.b.drop.keep_scale);
+    auto sync_wg = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
+    float acc[64];
+#pragma unroll
+    for (int c = 0; c < 64; ++c) acc[c] = 0.f;
+    // Sums of the accumulated tile along its diagonals, per 32 columns: entry e of column chunk
+    // k is the sum of the elements with key column - query row = 32 k + e - 127.
+    auto flush = [&](int group) {
+      float* out = args.diag_sums +
+                   (static_cast<size_t>(group) + blockIdx.x) * kRelDiagFloats + 2 * wg * 160;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) diag[t * kDiagPitch + c] = acc[32 * k + c];
+        sync_wg();
+        for (int e = t; e < 159; e += 128) {
+          float x = 0.f;
+          for (int c = max(0, e - 127); c <= min(31, e); ++c) x += diag[(c + 127 - e) * kDiagPitch + c];
+          out[160 * k + e] = x;
+        }
+        sync_wg();
+      }
+#pragma unroll
+      for (int c = 0; c < 64; ++c) acc[c] = 0.f;
+    };
+    uint32_t n = 0;
+    int group = -1;
+    bool ok = true;
+    for (; w.left > 0 && ok; w.next()) {
+      const int d0 = w.kt() * kTile - tile_pos(mk, w.qt());
+      if (w.group() != group) {
+        if (group >= 0) flush(group);
+        group = w.group();
+        sync_wg();  // the previous group's line is no longer read
+        const float* line = rel_line(args.b.rel, w.h) + (d0 - 127 + 64 * wg);
+        line_s[t] = __ldg(line + t);
+        if (t < 63) line_s[128 + t] = __ldg(line + 128 + t);
+        sync_wg();
+      }
+      if (!valid(w)) continue;
+      const int bh = w.b * mk.H + w.h, kt = w.kt();
+      const int row = w.qt() * kTile + t;
+      const size_t ridx = static_cast<size_t>(bh) * N + row;
+      float nl = -INFINITY, nd = 0.f;  // -lse in log2 units, -D
+      if (row < N) {
+        const float lse = args.b.lse[ridx];
+        nl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+        nd = -args.b.dsum[ridx];
+      }
+      const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+      const int kv_len = kv_len_of(mk, w.b);
+      int lo = 0, lim = kTile;
+      const bool masked = tile_needs_element_mask<kRel>(mk, w.qt(), kt, kv_len);
+      if (masked) visible_keys(mk, row + mk.q_off, kt, kv_len, lo, lim);
+      const uint32_t x = n & 1u;
+      if (!mbar_wait_warp(s_full[x], (n >> 1) & 1u, tmo, abort_flag)) {
+        fail();
+        ok = false;
+        break;
+      }
+      ++n;
+      tc_fence_after();
+      const uint32_t tS = tmem + lane_base + 256u * x + 64u * wg;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t sr[32], dr[32];
+        tmem_ld32(tS + 32 * half, sr);
+        tmem_ld32(tS + 128 + 32 * half, dr);
+        uint4 kw[2];
+        if constexpr (DROPOUT) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            kw[g] = dropout_keep16(args.b.drop, static_cast<uint32_t>(ridx),
+                                   static_cast<uint32_t>(kt * 8 + 4 * wg + 2 * half + g));
+        }
+        tmem_ld_wait();
+        if (half == 1) {
+          tc_fence_before();
+          mbar_arrive(s_free[x]);
+        }
+        const int c0 = 64 * wg + 32 * half;
+        const float* lp = line_s + (127 + 32 * half - t);
+        if (masked) {
+          // (a key behind the length may hold anything in V)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const bool see = c0 + c >= lo && c0 + c < lim;
+            sr[c] = see ? sr[c] : 0xFF800000u;  // -inf
+            dr[c] = see ? dr[c] : 0u;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float x0, x1, a0, a1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2,
+                           f2_add(f2_pack(lp[c], lp[c + 1]), nl2)),
+                    x0, x1);
+          if constexpr (DROPOUT) {
+            const uint4 k4 = kw[c >> 4];
+            const uint32_t wd = (c & 15) < 4 ? k4.x : (c & 15) < 8 ? k4.y : (c & 15) < 12 ? k4.z : k4.w;
+            dr[c] &= prmt(wd, 0u, (8u | (c & 3)) * 0x1111u);
+            dr[c + 1] &= prmt(wd, 0u, (8u | ((c + 1) & 3)) * 0x1111u);
+          }
+          const uint64_t t2 =
+              f2_fma(ks2, f2_pack(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd2);
+          f2_unpack(f2_fma(f2_pack(ex2_approx(x0), ex2_approx(x1)), t2,
+                           f2_pack(acc[32 * half + c], acc[32 * half + c + 1])),
+                    a0, a1);
+          acc[32 * half + c] = a0;
+          acc[32 * half + c + 1] = a1;
+        }
+      }
+    }
+    if (group >= 0 && ok) flush(group);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kNearMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ table
+// One warp per table entry (bucket n of head h): it goes over all distances a near tile can hold
+// and adds those that map to the bucket, then the far fields.
+constexpr int kMaxDiags = 640;
+
+__global__ void __launch_bounds__(256) rel_table_kernel(const RelGradArgs a, int ctas, int chunks) {
+  __shared__ long long start[kMaxDiags + 1];  // first pair of each group, within a head
+  const NearList l = near_list(a);
+  for (int g = threadIdx.x; g <= l.n_diag; g += 256) {
+    long long n = 0;
+    for (int i = 0; i < g; ++i) n += l.count(i);
+    start[g] = n * l.B;
+  }
+  __syncthreads();
+  const int n = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, h = blockIdx.y;
+  if (n >= a.num_buckets) return;
+  const long long per_head = start[l.n_diag];
+  const long long per = max(1ll, near_per_cta(per_head * a.b.mask.H, ctas));
+  const int left = a.b.rel.left, right = a.b.rel.right, off = a.b.mask.q_off;
+  constexpr int kOver = 2 * (kTile - 1);  // a near tile reaches that far past either end
+  double sum = 0.0;
+  for (int x = lane; l.n_diag > 0 && x < left + right + 1 + 2 * kOver; x += 32) {
+    const int dist = x - left - kOver;
+    if (__ldg(a.map + clamp_distance(dist, left, right) + left) != n) continue;
+    const int e = dist + off + (kTile - 1);
+    const int diag = (e >= 0 ? e / kTile : -((-e + kTile - 1) / kTile)) - l.first;  // the last
+    for (int g = max(diag - 1, 0); g <= min(diag, l.n_diag - 1); ++g) {
+      const int at = dist - ((l.first + g) * kTile - off) + (kTile - 1);
+      if (at > 2 * (kTile - 1) || start[g + 1] == start[g]) continue;
+      const long long p0 = h * per_head + start[g], p1 = h * per_head + start[g + 1] - 1;
+      for (int c = static_cast<int>(p0 / per); c <= static_cast<int>(p1 / per); ++c) {
+        const float* s = a.diag_sums +
+                         (static_cast<size_t>(h) * l.n_diag + g + c) * kRelDiagFloats;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (at >= 32 * k && at < 32 * k + 159) sum += s[160 * k + at - 32 * k];
+      }
+    }
+  }
+  for (int side = 0; side < 2; ++side) {
+    if (__ldg(a.map + (side ? left + right : 0)) != n) continue;
+    for (int i = lane; i < a.b.mask.B * chunks; i += 32) {
+      const size_t bh = static_cast<size_t>(i / chunks) * a.b.mask.H + h;
+      sum += a.far_sums[(bh * chunks + i % chunks) * 2 + side];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) a.dtable[static_cast<size_t>(n) * a.b.mask.H + h] = static_cast<float>(sum);
+}
+
+template <int D, bool DROPOUT>
+cudaError_t launch_near(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                        const CUtensorMap& tdo, const RelGradArgs& a, int ctas,
+                        cudaStream_t stream) {
+  auto kern = rel_near_kernel<D, DROPOUT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       NearL<D>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, kNearThreads, NearL<D>::kSmemBytes, stream>>>(tq, tk, tv, tdo, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rel_lines(const RelLinesArgs& a, cudaStream_t stream) {
+  const int stride = a.left + a.right + 1 + 2 * kRelPad;
+  rel_lines_kernel<<<dim3((stride + 255) / 256, a.H), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rel_grad(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                            const CUtensorMap& tdo, const RelGradArgs& a, int d, bool dropout,
+                            int num_sms, cudaStream_t stream) {
+  if (a.n_diag > kMaxDiags) return cudaErrorInvalidValue;
+  const MaskParams& m = a.b.mask;
+  const int chunks = (m.N + kRelRows - 1) / kRelRows;
+  rel_rows_kernel<<<chunks * m.B * m.H, 256, 0, stream>>>(a, chunks);
+  cudaError_t e = cudaGetLastError();
+  const int ctas = num_sms < kRelMaxCtas ? num_sms : kRelMaxCtas;
+  if (e == cudaSuccess && a.n_diag > 0) {
+    if (d == 64)
+      e = dropout ? launch_near<64, true>(tq, tk, tv, tdo, a, ctas, stream)
+                  : launch_near<64, false>(tq, tk, tv, tdo, a, ctas, stream);
+    else
+      e = dropout ? launch_near<128, true>(tq, tk, tv, tdo, a, ctas, stream)
+                  : launch_near<128, false>(tq, tk, tv, tdo, a, ctas, stream);
+  }
+  if (e != cudaSuccess) return e;
+  rel_table_kernel<<<dim3((a.num_buckets + 7) / 8, m.H), 256, 0, stream>>>(a, ctas, chunks);
+  return cudaGetLastError();
+}
+
+}  // namespace fa
