@@ -353,6 +353,7 @@ static fa_status bwd_prepare(const void* q, const void* k, const void* v, const 
   a->mode = wl >= 0 || wr >= 0 ? fa::kWindow : fa::kPlain;
   a->rel = fa::RelParams{};
   a->row_sums = nullptr;
+  a->key_tiles = nullptr;
   return FA_OK;
 }
 
@@ -787,17 +788,20 @@ fa_status fa_fwd_cross(const void* q, const void* k, const void* v, void* o, flo
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// Workspace of fa_bwd_cross: D, and for the gradient of a bias table what the dQ kernel leaves of
+// Workspace of fa_bwd_cross: D, the list of key tiles, and for the gradient of a bias table what the dQ kernel leaves of
 // each query row, the near tiles' diagonal sums and the far fields' sums.
 struct CrossWorkspace {
   int first, n_diag;  // near tile pairs: kt - qt = first .. first + n_diag - 1
-  size_t rows_off, diag_off, far_off, bytes;
+  size_t tiles_off, rows_off, diag_off, line_off, far_off, bytes;
 };
 static CrossWorkspace cross_workspace(int B, int H, int Nq, int Nk, int causal, int q_offset,
                                       bool grad, int left, int right) {
-  CrossWorkspace w = {0, 0, 0, 0, 0, 0};
+  CrossWorkspace w = {};
   const size_t rows = static_cast<size_t>(B) * H * Nq;
-  w.bytes = round256(rows * sizeof(float));
+  w.tiles_off = round256(rows * sizeof(float));
+  // (room for a K/V head per query head)
+  const size_t tiles = static_cast<size_t>(B) * H * ((static_cast<size_t>(Nk) + fa::kTile - 1) / fa::kTile);
+  w.bytes = w.tiles_off + round256((tiles + 1) * sizeof(int32_t));
   if (!grad) return w;
   w.rows_off = w.bytes;
   w.diag_off = w.rows_off + round256(rows * 4 * fa::kRelRowSums * sizeof(float));
@@ -814,10 +818,12 @@ static CrossWorkspace cross_workspace(int B, int H, int Nq, int Nk, int causal, 
   if (hi > n_k - 1) hi = n_k - 1;
   w.first = static_cast<int>(lo);
   w.n_diag = hi < lo ? 0 : static_cast<int>(hi - lo + 1);
-  w.far_off = w.diag_off + round256((static_cast<size_t>(H) * w.n_diag + fa::kRelMaxCtas) *
+  w.line_off = w.diag_off + round256((static_cast<size_t>(H) * w.n_diag + fa::kRelMaxCtas) *
                                     fa::kRelDiagFloats * sizeof(float));
+  w.far_off = w.line_off + round256(static_cast<size_t>(H) * (left + right + 1 + 4 * (T - 1)) *
+                                    sizeof(float));
   const size_t chunks = (static_cast<size_t>(Nq) + fa::kRelRows - 1) / fa::kRelRows;
-  w.bytes = w.far_off + round256(static_cast<size_t>(B) * H * chunks * 2 * sizeof(double));
+  w.bytes = w.far_off + round256(static_cast<size_t>(B) * H * chunks * 2 * sizeof(float));
   return w;
 }
 
@@ -879,6 +885,7 @@ fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* 
   a.dk = static_cast<__nv_bfloat16*>(dk);
   a.dv = static_cast<__nv_bfloat16*>(dv);
   a.row_sums = grad ? reinterpret_cast<float*>(ws + w.rows_off) : nullptr;
+  a.key_tiles = seqlens_k != nullptr ? reinterpret_cast<int32_t*>(ws + w.tiles_off) : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool drop = a.drop.p8 > 0;
   cudaError_t e = fa::launch_bwd_preprocess(a, d, di->num_sms, s);
@@ -898,7 +905,8 @@ fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* 
     g.first = w.first;
     g.n_diag = w.n_diag;
     g.diag_sums = reinterpret_cast<float*>(ws + w.diag_off);
-    g.far_sums = reinterpret_cast<double*>(ws + w.far_off);
+    g.line_sums = reinterpret_cast<float*>(ws + w.line_off);
+    g.far_sums = reinterpret_cast<float*>(ws + w.far_off);
     e = fa::launch_rel_grad(m[0], m[1], m[2], m[3], g, d, drop, di->num_sms, s);
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
@@ -1209,11 +1217,9 @@ fa_status fa_paged_attn(const void* q, const void* k_pages, const void* v_pages,
   for (const int i : {__VA_ARGS__})                                           \
     if (x[i] != static_cast<int32_t>(x[i])) return FA_ERR_INVALID_ARG;        \
   auto p = [&](int i) { return reinterpret_cast<void*>(x[i]); };              \
-  auto u8 = [&](int i) { return reinterpret_cast<uint8_t*>(x[i]); };          \
+  [[maybe_unused]] auto u8 = [&](int i) { return reinterpret_cast<uint8_t*>(x[i]); };  \
   auto i32 = [&](int i) { return reinterpret_cast<const int32_t*>(x[i]); };   \
-  auto n = [&](int i) { return static_cast<int>(x[i]); };                     \
-  (void)u8;                                                                   \
-  (void)i32;
+  auto n = [&](int i) { return static_cast<int>(x[i]); };
 
 fa_status fa_paged_write_block(const int64_t* x, void* stream) {
   FA_BLOCK_INTS(6, 7, 8, 9, 10, 16, 19, 20, 21)

@@ -37,7 +37,32 @@ template <int D>
 __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __nv_bfloat16* __restrict__ o,
                                                              const __nv_bfloat16* __restrict__ dout,
                                                              float* __restrict__ dsum,
-                                                             long long rows) {
+                                                             long long rows, const MaskParams mk,
+                                                             int32_t* key_tiles, __nv_bfloat16* dk,
+                                                             __nv_bfloat16* dv) {
+  if (key_tiles != nullptr) {
+    const int lane = threadIdx.x & 31, n_t = (mk.Nk + kTile - 1) / kTile;
+    for (int bhk = blockIdx.x; bhk < mk.B * mk.Hkv; bhk += gridDim.x) {
+      const int b = bhk / mk.Hkv;
+      const int tiles = (kv_len_of(mk, b) + kTile - 1) / kTile;
+      if (threadIdx.x < 32) {
+        int before = 0;  // key tiles within the lengths of the batch rows in front
+        for (int i = lane; i < b; i += 32) before += (kv_len_of(mk, i) + kTile - 1) / kTile;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+        const int at = before * mk.Hkv + (bhk - b * mk.Hkv) * tiles;
+        for (int i = lane; i < tiles; i += 32) key_tiles[1 + at + i] = bhk * n_t + i;
+        if (bhk == mk.B * mk.Hkv - 1 && lane == 0) key_tiles[0] = at + tiles;
+      }
+      const long long begin =
+          (static_cast<long long>(bhk) * mk.Nk + static_cast<long long>(tiles) * kTile) * (D / 8);
+      const long long end = (static_cast<long long>(bhk) + 1) * mk.Nk * (D / 8);
+      for (long long i = begin + threadIdx.x; i < end; i += blockDim.x) {
+        reinterpret_cast<uint4*>(dk)[i] = make_uint4(0u, 0u, 0u, 0u);
+        reinterpret_cast<uint4*>(dv)[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
   const int sub = threadIdx.x & 7;
   const unsigned gmask = 0xFFu << (threadIdx.x & 24);
   const long long groups_per_grid = (static_cast<long long>(gridDim.x) * blockDim.x) >> 3;
@@ -136,7 +161,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int Nk = CROSS ? mk.Nk : N;         // keys
   const int n_q = (N + kTile - 1) / kTile;  // query tiles
   const int n_t = CROSS ? (Nk + kTile - 1) / kTile : n_q;  // key tiles
-  const int n_units = mk.B * mk.Hkv * n_t;
+  const int n_units = CROSS ? key_tile_count(args, n_t) : mk.B * mk.Hkv * n_t;
   const int G = GQA ? mk.H / mk.Hkv : 1;  // query heads per K/V head
 
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -229,7 +254,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int unit_count = 0;
     for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-      const int bhk = u / n_t, kt = u % n_t;  // K/V head, key tile
+      const int e = CROSS ? key_tile_at(args, u) : u;
+      const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
       const int b = bhk / mk.Hkv;
       const int kv_len = kv_len_of(mk, b);
       const int n_kv = (kv_len + kTile - 1) / kTile;
@@ -251,6 +277,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
            ++bh) {  // the query heads sharing this K/V head
+        RelHead head{};
+        if constexpr (REL) head = rel_head(args.rel, bh % mk.H);
         for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
           uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
           while (bits != 0u) {
@@ -277,8 +305,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               // a tile whose bias is one number: added here
               if constexpr (REL)
                 if (q_side)
-                  vp[r] += rel_far_bias(args.rel, rel_line(args.rel, bh % mk.H),
-                                        kt * kTile - tile_pos(mk, qt));
+                  vp[r] += rel_far_bias(args.rel, head, kt * kTile - tile_pos(mk, qt));
             }
             reinterpret_cast<float4*>(rowvals + s * 128)[lane] = v4;
             if (lane == 0) {
@@ -335,7 +362,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     };
     for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-      const int bhk = u / n_t, kt = u % n_t;  // K/V head, key tile
+      const int e = CROSS ? key_tile_at(args, u) : u;
+      const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
       const int b = bhk / mk.Hkv;
       const int kv_len = kv_len_of(mk, b);
       const int n_kv = (kv_len + kTile - 1) / kTile;
@@ -457,12 +485,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int unit_count = 0;
     for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-      const int bhk = u / n_t, kt = u % n_t;  // K/V head, key tile
+      const int e = CROSS ? key_tile_at(args, u) : u;
+      const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
       const int b = bhk / mk.Hkv;
       const int kv_len = kv_len_of(mk, b);
       const int n_kv = (kv_len + kTile - 1) / kTile;
       const int key = kt * kTile + r;
       int n_done = 0;
+      TileRun plain{}, near{};  // query tiles without a mask per element, with a bias per element
+      if constexpr (CROSS) plain = free_query_tiles(mk, kt, kv_len);
+      if constexpr (REL) near = near_query_tiles(args.rel, mk, kt);
       for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
              ++bh) {  // the query heads sharing this K/V head
         for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
@@ -514,13 +546,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               tmem_ld32(tSt + 32, &sr[32]);
               tmem_ld_wait();
               float cs = c_log2;
-              if constexpr (REL) {  // each element's own bias; scores to log2 units
-                const int d0 = kt * kTile - tile_pos(mk, qt);
-                if (!rel_far_left(args.rel, d0) && !rel_far_right(args.rel, d0)) {
-                  const float* lp = rel_line(args.rel, bh % mk.H) + (d0 + r - 64 * wg);
-  #pragma unroll
-                  for (int c = 0; c < 64; ++c)
-                    sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), c_log2, __ldg(lp - c)));
+              if constexpr (REL) {  // each element's own bias
+                if (near.has(qt)) {
+                  const int d0 = kt * kTile - tile_pos(mk, qt);
+                  rel_add<64, -1>(rel_line(args.rel, bh % mk.H) + (d0 + r - 64 * wg), c_log2, sr);
                   cs = 1.f;
                 }
               }
@@ -540,14 +569,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 }
               }
             }
-            if (tile_needs_element_mask<MODE>(mk, qt, kt, kv_len)) {
-              const bool key_ok = key < kv_len;
+            if (CROSS ? !plain.has(qt) : tile_needs_element_mask<MODE>(mk, qt, kt, kv_len)) {
+              if constexpr (CROSS) {
+                int lo, hi;
+                seeing_queries(mk, key, q0 + mk.q_off, kv_len, lo, hi);
   #pragma unroll
-              for (int c = 0; c < 64; ++c) {
-                const int pos = CROSS ? q0 + c + mk.q_off : q0 + c;
-                const bool allowed = key_ok && (!mk.causal || key <= pos) &&
-                                     (!(WIN || CROSS) || in_window(mk, pos, key));
-                p[c] = allowed ? p[c] : 0.f;
+                for (int c = 0; c < 64; ++c) p[c] = (c >= lo && c < hi) ? p[c] : 0.f;
+              } else {
+                const bool key_ok = key < kv_len;
+  #pragma unroll
+                for (int c = 0; c < 64; ++c) {
+                  const bool allowed = key_ok && (!mk.causal || key <= q0 + c) &&
+                                       (!WIN || in_window(mk, q0 + c, key));
+                  p[c] = allowed ? p[c] : 0.f;
+                }
               }
             }
             {
@@ -584,7 +619,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tmem_ld32(tDPt + 32 * h, dr);
                 tmem_ld_wait();
                 if constexpr (CROSS) {  // a key behind the length, whatever its V holds
-                  if (key >= kv_len)
+                  if (plain.hi == 0 && key >= kv_len)
   #pragma unroll
                     for (int c = 0; c < 32; ++c) dr[c] = 0u;
                 }
@@ -681,12 +716,16 @@ cudaError_t set_smem(K kern, int bytes) {
 cudaError_t launch_bwd_preprocess(const BwdArgs& a, int d, int num_sms, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.mask.B) * a.mask.H * a.mask.N;
   const long long want = (rows * 8 + 255) / 256;
-  const int grid = static_cast<int>(want < num_sms * 8LL ? want : num_sms * 8LL);
+  const bool zero = a.key_tiles != nullptr;
+  const long long blocks = zero ? max(want, static_cast<long long>(a.mask.B) * a.mask.Hkv) : want;
+  const int grid = static_cast<int>(blocks < num_sms * 8LL ? blocks : num_sms * 8LL);
   if (grid <= 0) return cudaSuccess;
   if (d == 64)
-    bwd_preprocess_kernel<64><<<grid, 256, 0, stream>>>(a.o, a.dout, a.dsum, rows);
+    bwd_preprocess_kernel<64><<<grid, 256, 0, stream>>>(a.o, a.dout, a.dsum, rows, a.mask,
+                                                      a.key_tiles, a.dk, a.dv);
   else
-    bwd_preprocess_kernel<128><<<grid, 256, 0, stream>>>(a.o, a.dout, a.dsum, rows);
+    bwd_preprocess_kernel<128><<<grid, 256, 0, stream>>>(a.o, a.dout, a.dsum, rows, a.mask,
+                                                      a.key_tiles, a.dk, a.dv);
   return cudaGetLastError();
 }
 

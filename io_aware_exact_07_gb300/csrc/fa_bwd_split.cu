@@ -146,9 +146,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int Nk = CROSS ? mk.Nk : N;                        // keys
   const int n_q = (N + kTile - 1) / kTile;                 // query tiles
   const int n_t = CROSS ? (Nk + kTile - 1) / kTile : n_q;  // key tiles
-  const int n_units = mk.B * mk.Hkv * n_t;
+  const int n_units = CROSS ? key_tile_count(args, n_t) : mk.B * mk.Hkv * n_t;
   const int G = GQA ? mk.H / mk.Hkv : 1;  // query heads per K/V head
-  const bool rot = mk.seqlens_k != nullptr;  // rotated schedule under key padding
+  // rotated schedule under key padding (where the list has its empty units too)
+  const bool rot = mk.seqlens_k != nullptr && !CROSS;
 
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
@@ -235,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int unit_count = 0;
       for (int u = sched_unit(0, rot); u < n_units && ok; u = sched_unit(++unit_count, rot)) {
-        const int bhk = u / n_t, kt = u % n_t;  // K/V head, key tile
+        const int e = CROSS ? key_tile_at(args, u) : u;
+        const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
         const int kv_len = kv_len_of(mk, bhk / mk.Hkv);
         const int n_kv = (kv_len + kTile - 1) / kTile;
         const int kb = unit_count % L::kKVBufs;
@@ -253,6 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++kv_arms[kb];
         for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
                ++bh) {  // the query heads sharing this K/V head
+          RelHead head{};
+          if constexpr (REL) head = rel_head(args.rel, bh % mk.H);
           for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
             uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
             while (bits != 0u) {
@@ -276,8 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lp[r] = -lse2_at(args.lse, idx, in);
                 // a tile whose bias is one number: added here
                 if constexpr (REL)
-                  lp[r] += rel_far_bias(args.rel, rel_line(args.rel, bh % mk.H),
-                                        kt * kTile - tile_pos(mk, qt));
+                  lp[r] += rel_far_bias(args.rel, head, kt * kTile - tile_pos(mk, qt));
                 dp[r] = in ? -args.dsum[idx] : 0.f;
               }
               // staged negated: the compute warps add them as packed pairs
@@ -322,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
       int unit_count = 0;
       for (int u = sched_unit(0, rot); u < n_units && ok; u = sched_unit(++unit_count, rot)) {
-        const int bhk = u / n_t, kt = u % n_t;  // K/V head, key tile
+        const int e = CROSS ? key_tile_at(args, u) : u;
+        const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
         const int kv_len = kv_len_of(mk, bhk / mk.Hkv);
         const int n_kv = (kv_len + kTile - 1) / kTile;
         const int kb = unit_count % L::kKVBufs;
@@ -380,7 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int unit_count = 0;
       for (int u = sched_unit(0, rot); u < n_units && ok; u = sched_unit(++unit_count, rot)) {
-        const int bhk = u / n_t, kt = u % n_t;  // K/V head, key tile
+        const int e = CROSS ? key_tile_at(args, u) : u;
+        const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
         const int kv_len = kv_len_of(mk, bhk / mk.Hkv);
         const int n_kv = (kv_len + kTile - 1) / kTile;
         bool first = true;
@@ -455,11 +460,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int unit_count = 0;
     for (int u = sched_unit(0, rot); u < n_units && ok; u = sched_unit(++unit_count, rot)) {
-      const int bhk = u / n_t, kt = u % n_t;  // K/V head, key tile
+      const int e = CROSS ? key_tile_at(args, u) : u;
+        const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
       const int kv_len = kv_len_of(mk, bhk / mk.Hkv);
       const int n_kv = (kv_len + kTile - 1) / kTile;
       const int key = kt * kTile + r;
       int n_done = 0;
+      // Query tiles without a mask per element, as a run known per unit. (The kRel instance tests
+      // each tile: two more values kept per thread cost it more, 2.13 ms against 2.04 at
+      // H = 16, N = 16384; the kCross instance gains, 1.93 against 1.97.)
+      constexpr bool kRun = MODE == kCross;
+      TileRun plain{};
+      if constexpr (kRun) plain = free_query_tiles(mk, kt, kv_len);
       for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
              ++bh) {  // the query heads sharing this K/V head
         for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
@@ -519,13 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bars.st_free);
               }
               float cs = c_log2;
-              if constexpr (REL) {  // each element's own bias; scores to log2 units
+              if constexpr (REL) {  // each element's own bias
                 const int d0 = kt * kTile - tile_pos(mk, qt);
-                if (!rel_far_left(args.rel, d0) && !rel_far_right(args.rel, d0)) {
-                  const float* lp = rel_line(args.rel, bh % mk.H) + (d0 + r - 32 * wg);
-  #pragma unroll
-                  for (int c = 0; c < 32; ++c)
-                    sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), c_log2, __ldg(lp - c)));
+                if (!rel_far(args.rel, d0)) {
+                  rel_add<32, -1>(rel_line(args.rel, bh % mk.H) + (d0 + r - 32 * wg), c_log2, sr);
                   cs = 1.f;
                 }
               }
@@ -545,15 +554,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            if (tile_needs_element_mask<MODE>(mk, qt, kt, kv_len)) {
-              const bool key_ok = key < kv_len;
+            if (kRun ? !plain.has(qt) : tile_needs_element_mask<MODE>(mk, qt, kt, kv_len)) {
+              if constexpr (CROSS) {
+                int lo, hi;
+                seeing_queries(mk, key, q0 + mk.q_off, kv_len, lo, hi);
   #pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const int pos = CROSS ? q0 + c + mk.q_off : q0 + c;
-                p[c] = (key_ok && (!mk.causal || key <= pos) &&
-                        (!(WIN || CROSS) || in_window(mk, pos, key)))
-                           ? p[c]
-                           : 0.f;
+                for (int c = 0; c < 32; ++c) p[c] = (c >= lo && c < hi) ? p[c] : 0.f;
+              } else {
+                const bool key_ok = key < kv_len;
+  #pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  p[c] = (key_ok && (!mk.causal || key <= q0 + c) &&
+                          (!WIN || in_window(mk, q0 + c, key)))
+                             ? p[c]
+                             : 0.f;
               }
             }
             {
@@ -595,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bars.dpt_free);
               }
               if constexpr (CROSS) {  // a key behind the length, whatever its V holds
-                if (key >= kv_len)
+                if ((!kRun || plain.hi == 0) && key >= kv_len)
   #pragma unroll
                   for (int c = 0; c < 32; ++c) dr[c] = 0u;
               }
@@ -655,13 +669,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem + lane_base + (is_dv ? L::kColDV : L::kColDK) + kHalf * (wg & 1);
       const float mult = is_dv ? args.drop.keep_scale : args.scale;
       __nv_bfloat16* dst = (is_dv ? args.dv : args.dk) +
-                           (static_cast<size_t>(bhk) * Nk + static_cast<size_t>(key)) * D +
+                           (static_cast<size_t>(bhk) * Nk + static_cast<size_t>(kt * kTile)) * D +
                            kHalf * (wg & 1);
-#pragma unroll
-      for (int c = 0; c < kHalf / 32; ++c) {
+      static_assert(kHalf == 32, "one warp's share of a row is staged at once");
+      {
         uint32_t v[32];
         if (n_done > 0) {
-          tmem_ld32(tAcc + 32 * c, v);
+          tmem_ld32(tAcc, v);
           tmem_ld_wait();
         } else {
 #pragma unroll
@@ -672,15 +686,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 16; ++k)
           pk[k] = pack_bf16x2(__uint_as_float(v[2 * k]) * mult,
                               __uint_as_float(v[2 * k + 1]) * mult);
-        if (key < Nk) {
-          uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
+        tc_fence_before();
+        mbar_arrive(bars.acc_free);  // dV and dK are in registers
+        // 16 rows x 64 bytes at a time go through shared memory, so that a store instruction
+        // writes 8 rows' whole segments instead of a quarter of 32.
+        const uint32_t stage = smem_u32(drop_scratch);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            d4[k] = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+        for (int half = 0; half < 2; ++half) {
+          if ((lane >> 4) == half) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              st_shared_v4(stage + static_cast<uint32_t>((lane & 15) * 64 +
+                                                         ((k ^ ((lane >> 1) & 3)) << 4)),
+                           pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = 8 * i + (lane >> 2), u4 = lane & 3;
+            const uint4 val = ld_shared_v4(
+                stage + static_cast<uint32_t>(rr * 64 + ((u4 ^ ((rr >> 1) & 3)) << 4)));
+            const int row = quad * 32 + 16 * half + rr;
+            if (kt * kTile + row < Nk)
+              *reinterpret_cast<uint4*>(dst + static_cast<size_t>(row) * D + 8 * u4) = val;
+          }
+          __syncwarp();
         }
       }
-      tc_fence_before();
-      mbar_arrive(bars.acc_free);
     }
   }
   tc_fence_before();
@@ -712,7 +744,8 @@ struct DqL {
   // d = 64: the epilogue stages each compute warp's 32 rows of dQ (1 KB) before
   // storing them coalesced; at d = 128 shared memory has no room for it.
   static constexpr bool kStageDq = (D == 64);
-  static constexpr int kStageOff = (kMiscOff + 64 + 127) / 128 * 128;
+  static constexpr int kOrderOff = kMiscOff + 64;
+  static constexpr int kStageOff = (kOrderOff + kMaxOrdered + 127) / 128 * 128;
   static constexpr int kSmemBytes = kStageOff + (kStageDq ? kComputeWarps * 1024 : 0) + 1024;
   static_assert(kSmemBytes <= 232448, "dQ layout exceeds 227 KB of shared memory");
   static constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256, kColDS = 256 + D;
@@ -728,7 +761,7 @@ struct DqBars {
 
 template <int D, bool DROPOUT, int MODE>
 struct DqRealloc {
-  static constexpr bool value = (D == 128) || DROPOUT || MODE == kRel;
+  static constexpr bool value = (D == 128) || DROPOUT || MODE == kRel;  // REALLOC_REL
 };
 
 template <int D, bool DROPOUT, int MODE>
@@ -758,6 +791,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff + 8);
+
+  uint8_t* order = smem + L::kOrderOff;
+  if constexpr (CROSS) order_by_length(mk, order, tid, kThreads);
 
   DqBars bars;
   {
@@ -834,6 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bh = u / n_q;
     qt = u % n_q;
     if (mk.causal) qt = n_q - 1 - qt;
+    if constexpr (CROSS) bh = ordered_head(mk, order, bh);
   };
   auto kv_limit = [&](int qt, int n_kv) { return key_tiles_upto<MODE>(mk, qt + 1, n_kv); };
 
@@ -1087,8 +1124,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mk.wl >= 0) key_lo = row - mk.wl;
       }
       int n_done = 0;
-      // sums over this thread's keys: dS; dS and P left and right of the range of distances
-      float sum_ds = 0.f, left_ds = 0.f, right_ds = 0.f, left_p = 0.f, right_p = 0.f;
+      // Sums of dS and P over this thread's keys. The tiles come left of the range of distances
+      // (phase 0), near (1), then right of it (2); dS is summed up over all of them with its
+      // values at the changes kept, P from the first near one on (a row's weights sum to one).
+      uint64_t ds2 = 0ull, p2 = 0ull;
+      float left_ds = 0.f, upto_ds = 0.f, near_p = 0.f;
+      int phase = 0, change = 0;
+      uint64_t x2 = nl2;       // what the exponents get: the bias of a far block, less lse
+      bool own_bias = false;   // each element has its own bias
+      TileRun plain{}, near{};
+      RelHead head{};
+      // (at d = 128 a test per tile is faster: 181 us against 209 at H = 16, N = 4096, B = 2)
+      constexpr bool kRun = CROSS && D == 64;
+      if constexpr (kRun) plain = free_key_tiles(mk, tile_pos(mk, qt), kv_len);
+      if constexpr (REL) {
+        near = near_tiles(args.rel, -tile_pos(mk, qt));
+        head = rel_head(args.rel, bh % mk.H);
+      }
       for (int chunk = 0; chunk * 32 < jmax && ok; ++chunk) {
         uint32_t bits = warp_valid_bits<MODE>(mk, qt, chunk, n_q, n_kv);
         while (bits != 0u && ok) {
@@ -1110,16 +1162,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // WIN: whether this row's visible-key edge falls in the warpgroup's 32 columns
           const bool masked = WIN ? (j * kTile + 32 * wg < key_lo || j * kTile + 32 * wg + 32 > key_hi)
-                                  : tile_needs_element_mask<MODE>(mk, qt, j, kv_len);
-          // the bias of a tile beyond the range of distances is one number
-          bool far_l = false, far_r = false;
-          uint64_t x2 = nl2, cs2 = c2;
+                              : kRun ? !plain.has(j)
+                                      : tile_needs_element_mask<MODE>(mk, qt, j, kv_len);
           if constexpr (REL) {
-            const int d0 = j * kTile - tile_pos(mk, qt);
-            far_l = rel_far_left(args.rel, d0);
-            far_r = rel_far_right(args.rel, d0);
-            const float nl = rel_far_bias(args.rel, rel_line(args.rel, bh % mk.H), d0) - lse2;
-            x2 = f2_pack(nl, nl);
+            if (j >= change) {  // the bias or the sums change with this tile
+              const int now = j < near.lo ? 0 : (j < near.hi ? 1 : 2);
+              if (now != phase) {
+                if (phase == 0) left_ds = f2_sum(ds2);
+                if (now == 2) {
+                  upto_ds = f2_sum(ds2);
+                  near_p = f2_sum(p2);
+                }
+                phase = now;
+              }
+              // (a warp's 32 x 32 block may lie beyond the range of distances in a near tile)
+              const int ds = j * kTile - tile_pos(mk, qt) + 32 * wg - 32 * quad;
+              const bool far_l = rel_far_left(args.rel, ds, 32);
+              own_bias = !far_l && !rel_far_right(args.rel, ds, 32);
+              const float nl = (own_bias ? 0.f : (far_l ? head.left : head.right)) - lse2;
+              x2 = f2_pack(nl, nl);
+              change = now == 0 ? near.lo : (now == 1 ? j + 1 : INT_MAX);
+            }
           }
           // ---- P = exp2(S c - lse2), kept as bf16 pairs
           if (!mbar_wait_warp(bars.s_full, sc++ & 1, tmo, abort_flag)) {
@@ -1141,21 +1204,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
             tc_fence_before();
             mbar_arrive(bars.s_free);
+            uint64_t cs2 = c2;
             if constexpr (REL) {
-              if (!far_l && !far_r) {  // each element's own bias; scores to log2 units
-                const float* lp = rel_line(args.rel, bh % mk.H) +
-                                  (j * kTile - tile_pos(mk, qt) - t + 32 * wg);
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), c_log2, __ldg(lp + c)));
+              if (own_bias) {
+                rel_add<32, 1>(head.line + (j * kTile - tile_pos(mk, qt) + 32 * wg - t), c_log2, sr);
                 cs2 = f2_pack(1.f, 1.f);
               }
             }
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
               float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), cs2,
-                               x2),
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), cs2, x2),
                         x0, x1);
               p[c] = ex2_approx(x0);
               p[c + 1] = ex2_approx(x1);
@@ -1195,7 +1254,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           uint32_t pk[16];
           {
-            uint64_t s2[2] = {0ull, 0ull};  // packed sums of dS
             uint32_t dr[32];
             tmem_ld32(tDP, dr);
             tmem_ld_wait();
@@ -1203,7 +1261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(bars.dp_free);
             if constexpr (CROSS) {  // keys behind the length, whatever their V holds
               const int lim = kv_len - j * kTile - 32 * wg;
-              if (lim < 32)
+              if (masked && lim < 32)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) dr[c] = c < lim ? dr[c] : 0u;
             }
@@ -1221,25 +1279,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                   f2_fma(ks2, f2_pack(__uint_as_float(dp0), __uint_as_float(dp1)), nd2);
               float d0, d1;
               const uint64_t ds = f2_mul(f2_pack(p[2 * c], p[2 * c + 1]), t);
-              if constexpr (REL) s2[c & 1] = f2_add(s2[c & 1], ds);
+              if constexpr (REL) ds2 = f2_add(ds2, ds);
               f2_unpack(ds, d0, d1);
               pk[c] = pack_bf16x2(d0, d1);
             }
             if constexpr (REL) {
-              float s0, s1;
-              f2_unpack(f2_add(s2[0], s2[1]), s0, s1);
-              sum_ds += s0 + s1;
-              if (far_l || far_r) {
-                uint64_t p2[2] = {0ull, 0ull};
+              if (phase > 0) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                  p2[c & 1] = f2_add(p2[c & 1], f2_pack(p[2 * c], p[2 * c + 1]));
-                float p0, p1;
-                f2_unpack(f2_add(p2[0], p2[1]), p0, p1);
-                left_ds += far_l ? s0 + s1 : 0.f;
-                left_p += far_l ? p0 + p1 : 0.f;
-                right_ds += far_l ? 0.f : s0 + s1;
-                right_p += far_l ? 0.f : p0 + p1;
+                for (int c = 0; c < 16; ++c) p2 = f2_add(p2, f2_pack(p[2 * c], p[2 * c + 1]));
               }
             }
           }
@@ -1274,9 +1321,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (args.row_sums != nullptr && row_in) {
           const size_t rows = static_cast<size_t>(mk.B) * mk.H * N;
           float* out = args.row_sums + static_cast<size_t>(wg) * rows + static_cast<size_t>(ridx);
-          const float sums[kRelRowSums] = {sum_ds, left_ds, right_ds, left_p, right_p};
-#pragma unroll
-          for (int k = 0; k < kRelRowSums; ++k) out[4 * rows * k] = sums[k];
+          const float all_ds = f2_sum(ds2), all_p = f2_sum(p2);
+          if (phase == 0) left_ds = all_ds;
+          out[0] = all_ds;
+          out[4 * rows] = left_ds;
+          out[8 * rows] = phase == 2 ? all_ds - upto_ds : 0.f;
+          out[12 * rows] = all_p;
+          out[16 * rows] = phase == 2 ? all_p - near_p : 0.f;
         }
       }
       // ---- epilogue: dQ = scale * acc, D/4 columns per warpgroup

@@ -2,6 +2,7 @@
 // tile validity (causal / key padding / block-sparse), the Philox dropout
 // generator and the device status word.
 #pragma once
+#include <climits>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -56,25 +57,56 @@ struct RelParams {
   __host__ __device__ int stride() const { return left + right + 1 + 2 * kRelPad; }
 };
 
-// Where tile pair (qt, kt) lies: d0 is the distance of its first key from its first query, so its
-// distances are d0 - 127 .. d0 + 127. Left or right of the line's range the bias is one number.
-__device__ __forceinline__ bool rel_far_left(const RelParams& r, int d0) {
-  return d0 + (kTile - 1) <= -r.left;
+// Where a block of n queries x n keys lies whose first key is d0 behind its first query: its
+// distances are d0 - (n - 1) .. d0 + (n - 1). Beyond an end of the range the bias is one number.
+__device__ __forceinline__ bool rel_far_left(const RelParams& r, int d0, int n = kTile) {
+  return d0 + (n - 1) <= -r.left;
 }
-__device__ __forceinline__ bool rel_far_right(const RelParams& r, int d0) {
-  return d0 - (kTile - 1) >= r.right;
+__device__ __forceinline__ bool rel_far_right(const RelParams& r, int d0, int n = kTile) {
+  return d0 - (n - 1) >= r.right;
 }
 
-// Line of head h, indexed by distance.
+__device__ __forceinline__ bool rel_far(const RelParams& r, int d0) {
+  return rel_far_left(r, d0) || rel_far_right(r, d0);
+}
+
+// The line of head h, indexed by distance.
 __device__ __forceinline__ const float* rel_line(const RelParams& r, int h) {
   return r.lines + static_cast<size_t>(h) * r.stride() + r.left + kRelPad;
 }
 
-// Bias of a tile pair that lies beyond an end of the range (0 for other pairs, whose elements
-// have their own).
-__device__ __forceinline__ float rel_far_bias(const RelParams& r, const float* line, int d0) {
-  return rel_far_left(r, d0) ? __ldg(line - r.left)
-                             : (rel_far_right(r, d0) ? __ldg(line + r.right) : 0.f);
+// The bias of a head: its line, and the biases beyond the ends.
+struct RelHead {
+  const float* line;
+  float left, right;
+};
+__device__ __forceinline__ RelHead rel_head(const RelParams& r, int h) {
+  RelHead x;
+  x.line = rel_line(r, h);
+  x.left = __ldg(x.line - r.left);
+  x.right = __ldg(x.line + r.right);
+  return x;
+}
+
+// Bias of a block beyond an end of the range (0 for others, whose elements have their own).
+__device__ __forceinline__ float rel_far_bias(const RelParams& r, const RelHead& x, int d0,
+                                              int n = kTile) {
+  return rel_far_left(r, d0, n) ? x.left : (rel_far_right(r, d0, n) ? x.right : 0.f);
+}
+
+// Adds to N scores of this thread their own biases, STEP apart in distance from lp on, and brings
+// them to log2 units.
+template <int N, int STEP>
+__device__ __forceinline__ void rel_add(const float* lp, float c_log2, uint32_t* s) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {  // (more loads at once cost the kernels registers elsewhere)
+    float b[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) b[c] = __ldg(lp + STEP * (i + c));
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      s[i + c] = __float_as_uint(fmaf(__uint_as_float(s[i + c]), c_log2, b[c]));
+  }
 }
 
 struct DropParams {
@@ -142,6 +174,33 @@ __device__ __forceinline__ int key_tiles_upto(const MaskParams& m, int qt_end, i
   return bound;
 }
 
+// kCross, kRel with key lengths: batch rows in falling order of their number of key tiles, so that
+// the alternation of sched_unit gives every CTA long units and short ones, the short ones last.
+// (Rows of a batch that is not ordered come as they are: more than kMaxOrdered make units enough.)
+constexpr int kMaxOrdered = 256;
+__device__ __forceinline__ bool is_ordered(const MaskParams& m) {
+  return m.seqlens_k != nullptr && m.B > 1 && m.B <= kMaxOrdered;
+}
+__device__ __forceinline__ void order_by_length(const MaskParams& m, uint8_t* order, int tid,
+                                                int threads) {
+  if (!is_ordered(m)) return;
+  for (int b = tid; b < m.B; b += threads) {
+    const int n = (kv_len_of(m, b) + kTile - 1) / kTile;
+    int rank = 0;
+    for (int i = 0; i < m.B; ++i) {
+      const int x = (kv_len_of(m, i) + kTile - 1) / kTile;
+      rank += (x > n || (x == n && i < b)) ? 1 : 0;
+    }
+    order[rank] = static_cast<uint8_t>(b);
+  }
+}
+// Head b*H + h at position x of the heads in that order.
+__device__ __forceinline__ int ordered_head(const MaskParams& m, const uint8_t* order, int x) {
+  if (!is_ordered(m)) return x;
+  const int s = x / m.H;
+  return order[s] * m.H + (x - s * m.H);
+}
+
 // Static schedule of the persistent kernels: in round k the CTAs take the
 // positions [k G, k G + G) of the work list, G = gridDim.x, in forward order
 // on even rounds and in reverse order on odd rounds. Every role of a CTA walks
@@ -204,6 +263,48 @@ __device__ __forceinline__ bool tile_needs_element_mask(const MaskParams& m, int
   return (m.causal && kt == qt) || ((kt + 1) * kTile > kv_len);
 }
 
+// A run of tiles [lo, hi).
+struct TileRun {
+  int lo, hi;
+  __device__ __forceinline__ bool has(int i) const { return i >= lo && i < hi; }
+};
+__device__ __forceinline__ int floor_tiles(int x) { return x >> 7; }         // x / 128 rounded down
+__device__ __forceinline__ int ceil_tiles(int x) { return (x + 127) >> 7; }  // and up
+static_assert(kTile == 128, "shifts by 7");
+
+// kCross, kRel: the key tiles of a query tile whose first row is at position p0 (the query tiles of
+// key tile kt) that need no mask per element.
+__device__ __forceinline__ TileRun free_key_tiles(const MaskParams& m, int p0, int kv_len) {
+  TileRun r{0, floor_tiles(kv_len)};
+  if (m.causal) r.hi = min(r.hi, floor_tiles(p0 + 1));
+  if (m.wr >= 0) r.hi = min(r.hi, floor_tiles(p0 + m.wr + 1));
+  if (m.wl >= 0) r.lo = ceil_tiles(p0 + (kTile - 1) - m.wl);
+  return r;
+}
+__device__ __forceinline__ TileRun free_query_tiles(const MaskParams& m, int kt, int kv_len) {
+  const int k0 = kt * kTile - m.q_off;
+  TileRun r{0, INT_MAX};
+  if (m.causal) r.lo = ceil_tiles(k0 + kTile - 1);
+  if (m.wr >= 0) r.lo = max(r.lo, ceil_tiles(k0 + kTile - 1 - m.wr));
+  if (m.wl >= 0) r.hi = floor_tiles(k0 - (kTile - 1) + m.wl) + 1;
+  if ((kt + 1) * kTile > kv_len) r.hi = 0;
+  return r;
+}
+
+// kRel: the tiles along one axis whose block of n queries x n keys lies within reach of the
+// diagonal, at distance d0 + 128 i for key tile i: before them it is far to the left, behind them
+// far to the right.
+__device__ __forceinline__ TileRun near_tiles(const RelParams& r, int d0, int n = kTile) {
+  // not d0 + 128 i + n - 1 <= -left, and not d0 + 128 i - (n - 1) >= right
+  return TileRun{floor_tiles(-r.left - (n - 1) - d0) + 1, ceil_tiles(r.right + (n - 1) - d0)};
+}
+
+// The same for the query tiles of key tile kt: distance kt * 128 - q_off - 128 i for query tile i.
+__device__ __forceinline__ TileRun near_query_tiles(const RelParams& r, const MaskParams& m, int kt) {
+  const int d0 = kt * kTile - m.q_off;
+  return TileRun{floor_tiles(d0 - (kTile - 1) - r.right) + 1, ceil_tiles(d0 + (kTile - 1) + r.left)};
+}
+
 // kCross, kRel: keys [lo, lim) of key tile kt, counted from its first, are visible to the query at
 // position pos.
 __device__ __forceinline__ void visible_keys(const MaskParams& m, int pos, int kt, int kv_len,
@@ -214,6 +315,17 @@ __device__ __forceinline__ void visible_keys(const MaskParams& m, int pos, int k
   if (m.causal) lim = min(lim, pos + 1 - k0);
   if (m.wr >= 0) lim = min(lim, pos + m.wr + 1 - k0);
   if (m.wl >= 0) lo = pos - m.wl - k0;
+}
+
+// kCross, kRel: of the queries at positions pos0, pos0 + 1, .. those from lo to hi - 1 see key `key`.
+__device__ __forceinline__ void seeing_queries(const MaskParams& m, int key, int pos0, int kv_len,
+                                               int& lo, int& hi) {
+  lo = 0;
+  hi = kTile;
+  if (m.causal) lo = key - pos0;
+  if (m.wr >= 0) lo = max(lo, key - m.wr - pos0);
+  if (m.wl >= 0) hi = min(hi, key + m.wl - pos0 + 1);
+  if (key >= kv_len) hi = 0;
 }
 
 // kCross, kRel: the key tile that a length below Nk cuts (-1: none) has rows behind it, which may

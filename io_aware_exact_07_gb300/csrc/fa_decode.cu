@@ -380,9 +380,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int key_lo = args.wl >= 0 ? Lb - args.Nq + i - args.wl : 0;
       // REL: this row's position, and the line of biases of its head
       const int pos_q = Lb - args.Nq + i;
-      const float* line = nullptr;
+      RelHead head{};
       if constexpr (REL)
-        line = rel_line(args.rel, (pc.bkv % args.Hkv) * G + (real ? r / args.Nq : 0));
+        head = rel_head(args.rel, (pc.bkv % args.Hkv) * G + (real ? r / args.Nq : 0));
       float m_ref = -INFINITY;  // reference maximum, scaled log2 units
       float l_sum = 0.f;        // running sum of exp2(s*c - m_ref)
       for (int j = pc.j0; j < pc.j1; ++j) {
@@ -415,12 +415,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           const int d0 = j * kTile - pos_q;  // distance of the tile's first key
           const bool far_l = d0 + (kTile - 1) <= -args.rel.left, far_r = d0 >= args.rel.right;
           if (__all_sync(0xffffffffu, far_l || far_r)) {
-            far = __ldg(line + (far_l ? -args.rel.left : args.rel.right));
+            far = far_l ? head.left : head.right;
           } else {
 #pragma unroll
             for (int k = 0; k < 128; ++k)
               s[k] = fmaf(s[k], c_log2,
-                          __ldg(line + max(-args.rel.left, min(d0 + k, args.rel.right))));
+                          __ldg(head.line + max(-args.rel.left, min(d0 + k, args.rel.right))));
             cs = 1.f;
           }
           // Rows of V behind the length may hold anything (a weight of zero does not keep a NaN

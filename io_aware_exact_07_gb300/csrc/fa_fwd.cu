@@ -70,7 +70,8 @@ struct FwdLayout {
   static constexpr int kNumBars = 2 + 1 + 4 * kStages + 10 + 3;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   // epilogue staging: 4 KB per softmax warp (its 32 rows of O, 128 bytes each)
-  static constexpr int kStageOff = (kMiscOff + 64 + 127) / 128 * 128;
+  static constexpr int kOrderOff = kMiscOff + 64;
+  static constexpr int kStageOff = (kOrderOff + kMaxOrdered + 127) / 128 * 128;
   static constexpr int kSmemBytes = kStageOff + 8 * 4096 + 1024;  // + slack for 1024-byte alignment
   // Tensor memory has room for a separate P buffer per query tile
   // (2 x (128 S + 64 P + 64 O) = 512 columns), so the next S can be computed
@@ -93,19 +94,21 @@ struct UnitCoord {
   int bh, b, h, qt0;  // qt0 = index of query tile a (tile b is qt0 + 1)
 };
 
-__device__ __forceinline__ UnitCoord decode_unit(int u, int BH, int H, int n_qblk, int causal) {
+template <int MODE>
+__device__ __forceinline__ UnitCoord decode_unit(int u, const MaskParams& mk, int n_qblk,
+                                                 const uint8_t* order) {
   UnitCoord c;
   // Heads are processed one after another so that concurrently running CTAs
   // share K/V tiles in L2; with a causal mask the longest query blocks of a
   // head come first.
-  const int bh = u / n_qblk;
+  int bh = u / n_qblk;
   int qb = u % n_qblk;
-  if (causal) qb = n_qblk - 1 - qb;
+  if (mk.causal) qb = n_qblk - 1 - qb;
+  if constexpr (MODE >= kCross) bh = ordered_head(mk, order, bh);
   c.bh = bh;
-  c.b = bh / H;
-  c.h = bh % H;
+  c.b = bh / mk.H;
+  c.h = bh % mk.H;
   c.qt0 = 2 * qb;
-  (void)BH;
   return c;
 }
 
@@ -138,6 +141,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff + 8);
+  uint8_t* order = smem + L::kOrderOff;
 
   Bars bars;
   {
@@ -192,6 +196,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     mbar_init(bars.stall, 1);
     fence_mbar_init();
   }
+  if constexpr (CROSS) order_by_length(mk, order, tid, kFwdThreads);
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       int unit_count = 0;
       for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-        const UnitCoord uc = decode_unit(u, BH, mk.H, n_qblk, mk.causal);
+        const UnitCoord uc = decode_unit<MODE>(u, mk, n_qblk, order);
         const int kvh = kv_head(mk, uc.bh);  // K/V head of this query head
         const int kv_len = kv_len_of(mk, uc.b);
         const int n_kv = (kv_len + kTile - 1) / kTile;
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       };
       int unit_count = 0;
       for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-        const UnitCoord uc = decode_unit(u, BH, mk.H, n_qblk, mk.causal);
+        const UnitCoord uc = decode_unit<MODE>(u, mk, n_qblk, order);
         const int kv_len = kv_len_of(mk, uc.b);
         const int n_kv = (kv_len + kTile - 1) / kTile;
         const int jmax = key_tiles_upto<MODE>(mk, uc.qt0 + 2, n_kv);
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       bool ok = true;
       int unit_count = 0;
       for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-        const UnitCoord uc = decode_unit(u, BH, mk.H, n_qblk, mk.causal);
+        const UnitCoord uc = decode_unit<MODE>(u, mk, n_qblk, order);
         const int kv_len = kv_len_of(mk, uc.b);
         const int n_kv = (kv_len + kTile - 1) / kTile;
         const int jmax = key_tiles_upto<MODE>(mk, uc.qt0 + 2, n_kv);
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     bool ok = true;
     int unit_count = 0;
     for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-      const UnitCoord uc = decode_unit(u, BH, mk.H, n_qblk, mk.causal);
+      const UnitCoord uc = decode_unit<MODE>(u, mk, n_qblk, order);
       const int qt = uc.qt0 + x;
       const int row = qt * kTile + t;
       const int kv_len = kv_len_of(mk, uc.b);
@@ -525,6 +530,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (mk.wr >= 0 && row + mk.wr + 1 < key_hi) key_hi = row + mk.wr + 1;
         if (mk.wl >= 0) key_lo = row - mk.wl;
       }
+      TileRun plain{}, near{};  // key tiles without a mask per element, with a bias per element
+      if constexpr (CROSS) plain = free_key_tiles(mk, tile_pos(mk, qt), kv_len);
+      if constexpr (REL) near = near_tiles(args.rel, -tile_pos(mk, qt));
+      RelHead head{};
+      if constexpr (REL) head = rel_head(args.rel, uc.h);
       float m_ref = -INFINITY;  // reference maximum, scaled log2 units
       float l_sum = 0.f;        // running sum of exp2(s*c - m_ref), undropped
       int n_done = 0;
@@ -560,7 +570,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (k >= lim || k < lo) s[k] = -INFINITY;
             }
           } else if constexpr (CROSS) {
-            if (tile_needs_element_mask<MODE>(mk, qt, j, kv_len)) {
+            if (!plain.has(j)) {
               int lo, lim;
               visible_keys(mk, row + mk.q_off, j, kv_len, lo, lim);
 #pragma unroll
@@ -581,14 +591,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           // the scores to log2 units.
           float cs = c_log2, far = 0.f;
           if constexpr (REL) {
-            const int d0 = j * kTile - tile_pos(mk, qt);
-            const float* line = rel_line(args.rel, uc.h);
-            if (rel_far_left(args.rel, d0) || rel_far_right(args.rel, d0)) {
-              far = rel_far_bias(args.rel, line, d0);
+            if (!near.has(j)) {
+              far = j < near.lo ? head.left : head.right;
             } else {
-              const float* lp = line + (d0 - t);
+              const int d0 = j * kTile - tile_pos(mk, qt);
+              const float* lp = head.line + (d0 - t);
+              const uint64_t cl2 = f2_pack(c_log2, c_log2);
 #pragma unroll
-              for (int k = 0; k < 128; ++k) s[k] = fmaf(s[k], c_log2, __ldg(lp + k));
+              for (int c = 0; c < 128; c += 32) {
+                float b[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) b[k] = __ldg(lp + c + k);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2)
+                  f2_unpack(f2_fma(f2_pack(s[c + k], s[c + k + 1]), cl2, f2_pack(b[k], b[k + 1])),
+                            s[c + k], s[c + k + 1]);
+              }
               cs = 1.f;
             }
           }

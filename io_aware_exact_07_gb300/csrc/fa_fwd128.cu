@@ -71,7 +71,8 @@ struct Layout {
   static constexpr int kXchOff = kMiscOff + 16;            // (m, l) per warpgroup and row
   // No alignment slack: the kernel checks that the dynamic shared memory starts
   // on a 1024-byte boundary, which the swizzled tiles need.
-  static constexpr int kSmemBytes = kXchOff + 2 * kTile * 8;
+  static constexpr int kOrderOff = kXchOff + 2 * kTile * 8;
+  static constexpr int kSmemBytes = kOrderOff + kMaxOrdered;
   static_assert(kSmemBytes <= 232448, "shared memory exceeds the per-block limit");
   // tensor-memory columns
   __device__ static constexpr uint32_t col_s(int g) { return 128u * static_cast<uint32_t>(g); }
@@ -93,14 +94,17 @@ struct Unit {
   int bh, b, qt;
 };
 
-__device__ __forceinline__ Unit decode_unit(int u, int H, int n_q, int causal) {
+template <int MODE>
+__device__ __forceinline__ Unit decode_unit(int u, const MaskParams& mk, int n_q,
+                                            const uint8_t* order) {
   // Heads one after another, so that concurrently running CTAs share K/V tiles
   // in L2; with a causal mask the longest query tiles of a head come first.
   Unit c;
   c.bh = u / n_q;
   c.qt = u - c.bh * n_q;
-  if (causal) c.qt = n_q - 1 - c.qt;
-  c.b = c.bh / H;
+  if (mk.causal) c.qt = n_q - 1 - c.qt;
+  if constexpr (MODE >= kCross) c.bh = ordered_head(mk, order, c.bh);
+  c.b = c.bh / mk.H;
   return c;
 }
 
@@ -129,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff + 8);
+  uint8_t* order = smem + L::kOrderOff;
   // units (in this CTA's order) whose PVs have all been issued: a count, not a
   // barrier phase, since the PV issuer may run several units without key tiles
   // ahead of the S issuer
@@ -186,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bars.stall, 1);
     fence_mbar_init();
   }
+  if constexpr (CROSS) order_by_length(mk, order, tid, kThreads);
   if (warp == kSIssuerWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -225,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       int unit_count = 0;
       for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-        const Unit uc = decode_unit(u, mk.H, n_q, mk.causal);
+        const Unit uc = decode_unit<MODE>(u, mk, n_q, order);
         const int kvh = kv_head(mk, uc.bh);
         const int n_kv = (kv_len_of(mk, uc.b) + kTile - 1) / kTile;
         const int jmax = key_tiles_upto<MODE>(mk, uc.qt + 1, n_kv);
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
       int unit_count = 0;
       for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-        const Unit uc = decode_unit(u, mk.H, n_q, mk.causal);
+        const Unit uc = decode_unit<MODE>(u, mk, n_q, order);
         const int n_kv = (kv_len_of(mk, uc.b) + kTile - 1) / kTile;
         const int jmax = key_tiles_upto<MODE>(mk, uc.qt + 1, n_kv);
         // The tensor core runs products in issue order: the next unit's S products
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int unit_count = 0;
       for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-        const Unit uc = decode_unit(u, mk.H, n_q, mk.causal);
+        const Unit uc = decode_unit<MODE>(u, mk, n_q, order);
         const int kv_len = kv_len_of(mk, uc.b);
         const int n_kv = (kv_len + kTile - 1) / kTile;
         const int jmax = key_tiles_upto<MODE>(mk, uc.qt + 1, n_kv);
@@ -493,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int unit_count = 0;
     for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-      const Unit uc = decode_unit(u, mk.H, n_q, mk.causal);
+      const Unit uc = decode_unit<MODE>(u, mk, n_q, order);
       const int row = uc.qt * kTile + t;
       const int kv_len = kv_len_of(mk, uc.b);
       const int n_kv = (kv_len + kTile - 1) / kTile;
@@ -505,6 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mk.wr >= 0 && row + mk.wr + 1 < key_hi) key_hi = row + mk.wr + 1;
         if (mk.wl >= 0) key_lo = row - mk.wl;
       }
+      TileRun plain{}, near{};  // key tiles without a mask per element, with a bias per element
+      if constexpr (CROSS) plain = free_key_tiles(mk, tile_pos(mk, uc.qt), kv_len);
+      if constexpr (REL) near = near_tiles(args.rel, -tile_pos(mk, uc.qt));
+      RelHead head{};
+      if constexpr (REL) head = rel_head(args.rel, uc.bh - uc.b * mk.H);
       float m_ref = -INFINITY;  // reference maximum, scaled log2 units
       float l_sum = 0.f;        // running sum of exp2(s*c - m_ref), undropped
       int n_done = 0;           // key tiles of this warpgroup
@@ -542,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (k >= lim || k < lo) s[k] = -INFINITY;
             }
           } else if constexpr (CROSS) {
-            if (tile_needs_element_mask<MODE>(mk, uc.qt, j, kv_len)) {
+            if (!plain.has(j)) {
               int lo, lim;
               visible_keys(mk, row + mk.q_off, j, kv_len, lo, lim);
 #pragma unroll
@@ -563,14 +574,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the scores to log2 units.
           float cs = c_log2, far = 0.f;
           if constexpr (REL) {
-            const int d0 = j * kTile - tile_pos(mk, uc.qt);
-            const float* line = rel_line(args.rel, uc.bh - uc.b * mk.H);
-            if (rel_far_left(args.rel, d0) || rel_far_right(args.rel, d0)) {
-              far = rel_far_bias(args.rel, line, d0);
+            if (!near.has(j)) {
+              far = j < near.lo ? head.left : head.right;
             } else {
-              const float* lp = line + (d0 - t);
+              const int d0 = j * kTile - tile_pos(mk, uc.qt);
+              const float* lp = head.line + (d0 - t);
+              const uint64_t cl2 = f2_pack(c_log2, c_log2);
 #pragma unroll
-              for (int k = 0; k < 128; ++k) s[k] = fmaf(s[k], c_log2, __ldg(lp + k));
+              for (int c = 0; c < 128; c += 32) {
+                float b[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) b[k] = __ldg(lp + c + k);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2)
+                  f2_unpack(f2_fma(f2_pack(s[c + k], s[c + k + 1]), cl2, f2_pack(b[k], b[k + 1])),
+                            s[c + k], s[c + k + 1]);
+              }
               cs = 1.f;
             }
           }

@@ -38,10 +38,21 @@ struct BwdArgs {
   // kRel, for the gradient of the bias (null: not wanted): what each of the dQ kernel's four
   // warpgroups saw of a query row, [kRelRowSums][4][B*H*N] fp32
   float* row_sums;
+  // kCross, kRel with key lengths: the (K/V head, key tile) pairs within them (bhk * tiles + kt, as
+  // many as the first entry says), so that the CTAs of the key-tile kernel get even shares. The
+  // preprocess kernel lists them, and zeroes the gradients of whole tiles behind the lengths.
+  int32_t* key_tiles;
 };
 
+__device__ __forceinline__ int key_tile_count(const BwdArgs& a, int tiles) {
+  return a.key_tiles != nullptr ? a.key_tiles[0] : a.mask.B * a.mask.Hkv * tiles;
+}
+__device__ __forceinline__ int key_tile_at(const BwdArgs& a, int u) {
+  return a.key_tiles != nullptr ? a.key_tiles[1 + u] : u;
+}
+
 // Sums over the keys of a query row: dS, dS left of the range of distances, dS right of it, P
-// left of it, P right of it.
+// not left of it, P right of it.
 constexpr int kRelRowSums = 5;
 
 // Tensor maps of a [B*H, N, d] bf16 tensor with 128 x 64 boxes, 128-byte swizzle.
@@ -89,11 +100,12 @@ struct RelGradArgs {
   float* dtable;         // [num_buckets, H]
   int first, n_diag;     // near tile pairs: kt - qt = first .. first + n_diag - 1
   float* diag_sums;      // [H * n_diag + kRelMaxCtas][4][160]
-  double* far_sums;      // [B * H, ceil(N / kRelRows)][2]
+  float* line_sums;      // [H, left + right + 1 + 508], by distance from -left - 254 on
+  float* far_sums;       // [B * H, ceil(N / kRelRows)][2]
 };
 constexpr int kRelMaxCtas = 512;
-constexpr int kRelRows = 1024;      // query rows whose far sums a block forms
-constexpr int kRelDiagFloats = 640; // 4 column chunks x 160 diagonals
+constexpr int kRelRows = 256;       // query rows whose far sums a block forms
+constexpr int kRelDiagFloats = 640; // 4 warpgroups x 160 diagonals
 cudaError_t launch_rel_grad(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& tdo, const RelGradArgs& a, int d, bool dropout,
                             int num_sms, cudaStream_t stream);

@@ -17,7 +17,10 @@
 //               the same distance at the same place, so a CTA adds tiles of a head and kt - qt,
 //               over batch rows and query tiles, element by element in registers and forms the
 //               sums along the diagonals once, when it moves on;
-//   rel_table   adds the diagonals' and far fields' sums up by bucket, in fp64.
+//   rel_line    adds the diagonals' sums up by distance;
+//   rel_table   adds the distances and the far fields up by bucket.
+// Sums are fp32, over few values each; the long ones at the end keep what each addition rounds off
+// (Knuth's two-sum): this GPU adds fp64 at a 64th of the rate.
 // No atomics: the order of every sum is fixed.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -34,6 +37,30 @@ constexpr unsigned kStatusInvalid = 1u;
 __device__ __forceinline__ int clamp_distance(int x, int left, int right) {
   return x < -left ? -left : (x > right ? right : x);
 }
+
+// A sum with its rounding errors.
+struct Sum {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Sum& x) {
+    add(x.hi);
+    lo = __fadd_rn(lo, x.lo);
+  }
+  // over the warp; the same on every lane
+  __device__ __forceinline__ void add_lanes() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Sum x;
+      x.hi = __shfl_xor_sync(0xffffffffu, hi, o);
+      x.lo = __shfl_xor_sync(0xffffffffu, lo, o);
+      add(x);
+    }
+  }
+};
 
 // ------------------------------------------------------------------ lines
 __global__ void __launch_bounds__(256) rel_lines_kernel(const RelLinesArgs a) {
@@ -57,10 +84,10 @@ __global__ void __launch_bounds__(256) rel_lines_kernel(const RelLinesArgs a) {
 __global__ void __launch_bounds__(256) rel_rows_kernel(const RelGradArgs a, int chunks) {
   const int bh = blockIdx.x / chunks, chunk = blockIdx.x % chunks, N = a.b.mask.N;
   const size_t rows = static_cast<size_t>(a.b.mask.B) * a.b.mask.H * N;
-  double left = 0.0, right = 0.0;
-  for (int i = threadIdx.x; i < kRelRows; i += 256) {
-    const int row = chunk * kRelRows + i;
-    if (row >= N) break;
+  float left = 0.f, right = 0.f;
+  static_assert(kRelRows == 256, "a thread per row");
+  const int row = chunk * kRelRows + static_cast<int>(threadIdx.x);
+  if (row < N) {
     const size_t idx = static_cast<size_t>(bh) * N + row;
     float s[kRelRowSums];
 #pragma unroll
@@ -69,10 +96,11 @@ __global__ void __launch_bounds__(256) rel_rows_kernel(const RelGradArgs a, int 
       s[k] = (p[0] + p[rows]) + (p[2 * rows] + p[3 * rows]);
     }
     a.b.dsum[idx] += s[0];
-    left += static_cast<double>(s[1]) - static_cast<double>(s[0]) * s[3];
-    right += static_cast<double>(s[2]) - static_cast<double>(s[0]) * s[4];
+    // (a row that sees no key has sums of zero)
+    left = fmaf(-s[0], 1.f - s[3], s[1]);
+    right = fmaf(-s[0], s[4], s[2]);
   }
-  __shared__ double part[2][8];
+  __shared__ float part[2][8];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     left += __shfl_xor_sync(0xffffffffu, left, o);
@@ -84,9 +112,9 @@ __global__ void __launch_bounds__(256) rel_rows_kernel(const RelGradArgs a, int 
   }
   __syncthreads();
   if (threadIdx.x < 2) {
-    double x = 0.0;
-    for (int w = 0; w < 8; ++w) x += part[threadIdx.x][w];
-    a.far_sums[static_cast<size_t>(blockIdx.x) * 2 + threadIdx.x] = x;
+    const float* x = part[threadIdx.x];
+    a.far_sums[static_cast<size_t>(blockIdx.x) * 2 + threadIdx.x] =
+        ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
   }
 }
 
@@ -160,10 +188,18 @@ struct NearWalk {
   }
 };
 
-constexpr int kNearThreads = 10 * 32;
-constexpr int kNearProducerWarp = 8;
-constexpr int kNearMmaWarp = 9;
+constexpr int kNearComputeWarps = 16;
+constexpr int kNearCompute = kNearComputeWarps * 32;
+constexpr int kNearProducerWarp = 16;
+constexpr int kNearMmaWarp = 17;
+constexpr int kNearThreads = 18 * 32;
 constexpr int kDiagPitch = 33;
+// The producer walks the list and hands each pair on in shared memory: head b*H + h (-1: no more),
+// query tile, key tile, group; key length and the CTA's first group. Pair n's slot is taken again
+// for pair n + 8, whose ring stage pair n + 5 or a later one has left: its products waited until
+// the compute warps had read the S of pair n + 3, and they read the slot of a pair before the S of
+// the one in front of it.
+constexpr int kPairSlots = 8;
 
 template <int D>
 struct NearL {
@@ -172,9 +208,10 @@ struct NearL {
   static constexpr int kStages = D == 64 ? 6 : 3;  // ring of tile pairs: (Q, K), (dO, V), ...
   static constexpr int kDiagOff = kStages * 2 * T;
   static constexpr int kLineOff = kDiagOff + 2 * kTile * kDiagPitch * 4;
-  static constexpr int kBarOff = kLineOff + 2 * 192 * 4;
-  static constexpr int kNumBars = 2 * kStages + 4 + 1;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr int kBarOff = kLineOff + 256 * 4;
+  static constexpr int kNumBars = 2 * kStages + 4 + kPairSlots + 1;
+  static constexpr int kPairOff = kBarOff + (kNumBars + 1) / 2 * 16;
+  static constexpr int kMiscOff = kPairOff + kPairSlots * 32;
   // no slack for rounding the base up: the kernel checks its alignment
   static constexpr int kSmemBytes = kMiscOff + 16;
   static_assert(kSmemBytes <= 232448, "shared memory exceeds the per-block limit");
@@ -206,7 +243,9 @@ __global__ void __launch_bounds__(kNearThreads, 1)
   const BarRun empty{full.base + 8u * L::kStages};
   const BarRun s_full{empty.base + 8u * L::kStages};             // S and dP buffers
   const BarRun s_free{s_full.base + 16u};
-  const uint32_t drain = s_free.base + 16u;
+  const BarRun pair_full{s_free.base + 16u};
+  const uint32_t drain = pair_full.base + 8u * kPairSlots;
+  int4* pairs = reinterpret_cast<int4*>(smem + L::kPairOff);
   if (tid == 0) {
     *abort_flag = 0;
     for (int s = 0; s < L::kStages; ++s) {
@@ -215,8 +254,9 @@ __global__ void __launch_bounds__(kNearThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(s_full[x], 1);
-      mbar_init(s_free[x], 256);
+      mbar_init(s_free[x], kNearCompute);
     }
+    for (int s = 0; s < kPairSlots; ++s) mbar_init(pair_full[s], 1);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -234,36 +274,47 @@ __global__ void __launch_bounds__(kNearThreads, 1)
     record_error(args.b.sync.status, kStatusTimeout);
   };
   const uint32_t sRing = smem_u32(smem);
-  const NearList list = near_list(args);
-  NearWalk w(list, mk.H, gridDim.x, blockIdx.x);
-  auto valid = [&](const NearWalk& w) {
-    const int n_kv = (kv_len_of(mk, w.b) + kTile - 1) / kTile;
-    return tile_valid<kRel>(mk, w.qt(), w.kt(), list.n_q, n_kv);
-  };
 
   if (warp == kNearProducerWarp) {
     if (lane == 0) {
+      const NearList list = near_list(args);
+      NearWalk w(list, mk.H, gridDim.x, blockIdx.x);
+      const int first_group = w.left > 0 ? w.group() : -1;
       uint32_t it = 0;
       bool ok = true;
+      int group = -1;
+      // the ring's next stage, and the slot of the pair that it begins
+      auto hand_on = [&](int bh, int qt, int kt, int kv_len) -> bool {
+        const int s = it % L::kStages;
+        if (!mbar_wait(empty[s], ((it / L::kStages) & 1u) ^ 1u, tmo, abort_flag)) return false;
+        const uint32_t slot = (it >> 1) % kPairSlots;
+        pairs[2 * slot] = make_int4(bh, qt, kt, group);
+        pairs[2 * slot + 1] = make_int4(kv_len, first_group, 0, 0);
+        mbar_arrive(pair_full[slot]);
+        return true;
+      };
       for (; w.left > 0 && ok; w.next()) {
-        if (!valid(w)) continue;
+        group = w.group();
+        const int kv_len = kv_len_of(mk, w.b), qt = w.qt(), kt = w.kt();
+        if (!tile_valid<kRel>(mk, qt, kt, list.n_q, (kv_len + kTile - 1) / kTile)) continue;
         const int bh = w.b * mk.H + w.h, kvh = kv_head(mk, bh);
         for (int half = 0; half < 2; ++half, ++it) {
           const int s = it % L::kStages;
-          if (!mbar_wait(empty[s], ((it / L::kStages) & 1u) ^ 1u, tmo, abort_flag)) {
-            fail();
+          if (half == 0 ? !hand_on(bh, qt, kt, kv_len)
+                        : !mbar_wait(empty[s], ((it / L::kStages) & 1u) ^ 1u, tmo, abort_flag)) {
             ok = false;
             break;
           }
           mbar_expect_tx(full[s], 2 * T);
           for (int c = 0; c < L::kChunks; ++c) {
-            tma_load_3d(sRing + (2 * s) * T + c * 16384, half ? &tm_do : &tm_q, c * 64,
-                        w.qt() * kTile, bh, full[s]);
+            tma_load_3d(sRing + (2 * s) * T + c * 16384, half ? &tm_do : &tm_q, c * 64, qt * kTile,
+                        bh, full[s]);
             tma_load_3d(sRing + (2 * s + 1) * T + c * 16384, half ? &tm_v : &tm_k, c * 64,
-                        w.kt() * kTile, kvh, full[s]);
+                        kt * kTile, kvh, full[s]);
           }
         }
       }
+      if (!ok || !hand_on(-1, 0, 0, 0)) fail();
       // every load issued here must land before the CTA exits
       for (int s = 0; s < L::kStages; ++s)
         if (it > static_cast<uint32_t>(s))
@@ -275,17 +326,20 @@ __global__ void __launch_bounds__(kNearThreads, 1)
       constexpr uint32_t kId = idesc_bf16_f32(128, 128, 0, 0);
       uint32_t it = 0;
       bool ok = true;
-      for (; w.left > 0 && ok; w.next()) {
-        if (!valid(w)) continue;
+      while (ok) {
         const uint32_t n = it >> 1, x = n & 1u;  // pairs so far; S and dP buffer
+        if (!mbar_wait(pair_full[n % kPairSlots], (n / kPairSlots) & 1u, tmo, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (pairs[2 * (n % kPairSlots)].x < 0) break;
         if (n >= 2 && !mbar_wait(s_free[x], ((n >> 1) - 1) & 1u, tmo, abort_flag)) {
-          fail();
+          ok = false;
           break;
         }
         for (uint32_t half = 0; half < 2; ++half, ++it) {
           const int s = it % L::kStages;
           if (!mbar_wait(full[s], (it / L::kStages) & 1u, tmo, abort_flag)) {
-            fail();
             ok = false;
             break;
           }
@@ -301,72 +355,103 @@ __global__ void __launch_bounds__(kNearThreads, 1)
         }
         if (ok) mma_commit(s_full[x]);
       }
+      if (!ok) fail();
       mma_commit(drain);
       mbar_wait(drain, 0, tmo, nullptr);
     }
     __syncwarp();
   } else {
-    // Warpgroup wg owns key columns [64 wg, 64 wg + 64) of every tile; the thread owns a query row.
+    // Warpgroup wg owns key columns [32 wg, 32 wg + 32) of every tile; the thread owns a query row.
     const int wg = warp >> 2, quad = warp & 3;
     const int t = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    float* diag = reinterpret_cast<float*>(smem + L::kDiagOff) + wg * kTile * kDiagPitch;
-    float* line_s = reinterpret_cast<float*>(smem + L::kLineOff) + wg * 192;
+    float* diag = reinterpret_cast<float*>(smem + L::kDiagOff) + (wg & 1) * kTile * kDiagPitch;
+    float* line_s = reinterpret_cast<float*>(smem + L::kLineOff);
     const float c_log2 = args.b.scale_log2;
     const uint64_t c2 = f2_pack(c_log2, c_log2);
     const uint64_t ks2 = f2_pack(args.b.drop.keep_scale, args.b.drop.keep_scale);
-    auto sync_wg = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
-    float acc[64];
+    auto sync_wg = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory"); };
+    auto sync_all = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kNearCompute) : "memory"); };
+    float acc[32];
 #pragma unroll
-    for (int c = 0; c < 64; ++c) acc[c] = 0.f;
-    // Sums of the accumulated tile along its diagonals, per 32 columns: entry e of column chunk
-    // k is the sum of the elements with key column - query row = 32 k + e - 127.
+    for (int c = 0; c < 32; ++c) acc[c] = 0.f;
+    // Sums of the accumulated tile along its diagonals, per warpgroup: entry e is the sum of the
+    // elements with key column - query row = 32 wg + e - 127. Two warpgroups at a time.
     auto flush = [&](int group) {
       float* out = args.diag_sums +
-                   (static_cast<size_t>(group) + blockIdx.x) * kRelDiagFloats + 2 * wg * 160;
+                   (static_cast<size_t>(group) + blockIdx.x) * kRelDiagFloats + wg * 160;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int round = 0; round < 2; ++round) {
+        if ((wg >> 1) == round) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) diag[t * kDiagPitch + c] = acc[32 * k + c];
-        sync_wg();
-        for (int e = t; e < 159; e += 128) {
-          float x = 0.f;
-          for (int c = max(0, e - 127); c <= min(31, e); ++c) x += diag[(c + 127 - e) * kDiagPitch + c];
-          out[160 * k + e] = x;
+          for (int c = 0; c < 32; ++c) diag[t * kDiagPitch + c] = acc[c];
+          sync_wg();
+          for (int e = t; e < 159; e += 128) {
+            float x = 0.f;
+            for (int c = max(0, e - 127); c <= min(31, e); ++c)
+              x += diag[(c + 127 - e) * kDiagPitch + c];
+            out[e] = x;
+          }
         }
-        sync_wg();
+        sync_all();
       }
 #pragma unroll
-      for (int c = 0; c < 64; ++c) acc[c] = 0.f;
+      for (int c = 0; c < 32; ++c) acc[c] = 0.f;
     };
-    uint32_t n = 0;
-    int group = -1;
+    int4 p = make_int4(-1, 0, 0, -1), p_next;  // the pair, and the one after it
+    int kv_len = 0, kv_next = 0;
+    float lse_next = 0.f, d_next = 0.f;        // lse and D of the next pair's row
     bool ok = true;
-    for (; w.left > 0 && ok; w.next()) {
-      const int d0 = w.kt() * kTile - tile_pos(mk, w.qt());
-      if (w.group() != group) {
-        if (group >= 0) flush(group);
-        group = w.group();
-        sync_wg();  // the previous group's line is no longer read
-        const float* line = rel_line(args.b.rel, w.h) + (d0 - 127 + 64 * wg);
-        line_s[t] = __ldg(line + t);
-        if (t < 63) line_s[128 + t] = __ldg(line + 128 + t);
-        sync_wg();
+    auto look_ahead = [&](uint32_t n) {
+      const uint32_t slot = n % kPairSlots;
+      if (!mbar_wait_warp(pair_full[slot], (n / kPairSlots) & 1u, tmo, abort_flag)) {
+        fail();
+        ok = false;
+        return;
       }
-      if (!valid(w)) continue;
-      const int bh = w.b * mk.H + w.h, kt = w.kt();
-      const int row = w.qt() * kTile + t;
-      const size_t ridx = static_cast<size_t>(bh) * N + row;
-      float nl = -INFINITY, nd = 0.f;  // -lse in log2 units, -D
-      if (row < N) {
-        const float lse = args.b.lse[ridx];
-        nl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-        nd = -args.b.dsum[ridx];
+      p_next = pairs[2 * slot];
+      kv_next = pairs[2 * slot + 1].x;
+      const int row = p_next.y * kTile + t;
+      lse_next = -INFINITY;
+      d_next = 0.f;
+      if (p_next.x >= 0 && row < N) {
+        const size_t i = static_cast<size_t>(p_next.x) * N + row;
+        lse_next = args.b.lse[i];
+        d_next = args.b.dsum[i];
       }
+    };
+    look_ahead(0);
+    const int first_group = ok ? pairs[1].y : -1;
+    // the sums of the groups that this CTA's pairs begin and end with, and of those between, are
+    // written once each, be there valid pairs or none
+    int group = first_group, line_group = -1;
+    for (uint32_t n = 0; ok; ++n) {
+      p = p_next;
+      kv_len = kv_next;
+      if (p.w != group) {
+        // (the sums of a group without a valid pair here are zeros)
+        if (group >= 0)
+          for (; group < p.w; ++group) flush(group);
+        group = p.w;
+        line_group = -1;
+      }
+      if (p.x < 0) break;
+      const int kt = p.z, row = p.y * kTile + t;
+      if (line_group != group) {
+        sync_all();  // the previous group's line is no longer read
+        const int d0 = kt * kTile - tile_pos(mk, p.y);
+        if (tid < 2 * kTile - 1)
+          line_s[tid] = __ldg(rel_line(args.b.rel, p.x % mk.H) + (d0 - (kTile - 1) + tid));
+        sync_all();
+        line_group = group;
+      }
+      const float nl = lse_next == -INFINITY ? -INFINITY : -lse_next * kLog2e, nd = -d_next;
+      const int bh = p.x;
+      look_ahead(n + 1);
+      if (!ok) break;
       const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
-      const int kv_len = kv_len_of(mk, w.b);
       int lo = 0, lim = kTile;
-      const bool masked = tile_needs_element_mask<kRel>(mk, w.qt(), kt, kv_len);
+      const bool masked = tile_needs_element_mask<kRel>(mk, p.y, kt, kv_len);
       if (masked) visible_keys(mk, row + mk.q_off, kt, kv_len, lo, lim);
       const uint32_t x = n & 1u;
       if (!mbar_wait_warp(s_full[x], (n >> 1) & 1u, tmo, abort_flag)) {
@@ -374,56 +459,53 @@ __global__ void __launch_bounds__(kNearThreads, 1)
         ok = false;
         break;
       }
-      ++n;
       tc_fence_after();
-      const uint32_t tS = tmem + lane_base + 256u * x + 64u * wg;
+      const uint32_t tS = tmem + lane_base + 256u * x + 32u * wg;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        uint32_t sr[32], dr[32];
-        tmem_ld32(tS + 32 * half, sr);
-        tmem_ld32(tS + 128 + 32 * half, dr);
-        uint4 kw[2];
-        if constexpr (DROPOUT) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-            kw[g] = dropout_keep16(args.b.drop, static_cast<uint32_t>(ridx),
-                                   static_cast<uint32_t>(kt * 8 + 4 * wg + 2 * half + g));
-        }
+        uint32_t sr[16], dr[16];
+        tmem_ld16(tS + 16 * half, sr);
+        tmem_ld16(tS + 128 + 16 * half, dr);
+        uint4 k4;
+        if constexpr (DROPOUT)
+          k4 = dropout_keep16(args.b.drop,
+                              static_cast<uint32_t>(bh) * static_cast<uint32_t>(N) +
+                                  static_cast<uint32_t>(row),
+                              static_cast<uint32_t>(kt * 8 + 2 * wg + half));
         tmem_ld_wait();
         if (half == 1) {
           tc_fence_before();
           mbar_arrive(s_free[x]);
         }
-        const int c0 = 64 * wg + 32 * half;
-        const float* lp = line_s + (127 + 32 * half - t);
+        const int c0 = 32 * wg + 16 * half;
+        const float* lp = line_s + (127 + c0 - t);
         if (masked) {
           // (a key behind the length may hold anything in V)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
+          for (int c = 0; c < 16; ++c) {
             const bool see = c0 + c >= lo && c0 + c < lim;
             sr[c] = see ? sr[c] : 0xFF800000u;  // -inf
             dr[c] = see ? dr[c] : 0u;
           }
         }
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
+        for (int c = 0; c < 16; c += 2) {
           float x0, x1, a0, a1;
           f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2,
                            f2_add(f2_pack(lp[c], lp[c + 1]), nl2)),
                     x0, x1);
           if constexpr (DROPOUT) {
-            const uint4 k4 = kw[c >> 4];
-            const uint32_t wd = (c & 15) < 4 ? k4.x : (c & 15) < 8 ? k4.y : (c & 15) < 12 ? k4.z : k4.w;
+            const uint32_t wd = c < 4 ? k4.x : c < 8 ? k4.y : c < 12 ? k4.z : k4.w;
             dr[c] &= prmt(wd, 0u, (8u | (c & 3)) * 0x1111u);
             dr[c + 1] &= prmt(wd, 0u, (8u | ((c + 1) & 3)) * 0x1111u);
           }
           const uint64_t t2 =
               f2_fma(ks2, f2_pack(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd2);
           f2_unpack(f2_fma(f2_pack(ex2_approx(x0), ex2_approx(x1)), t2,
-                           f2_pack(acc[32 * half + c], acc[32 * half + c + 1])),
+                           f2_pack(acc[16 * half + c], acc[16 * half + c + 1])),
                     a0, a1);
-          acc[32 * half + c] = a0;
-          acc[32 * half + c + 1] = a1;
+          acc[16 * half + c] = a0;
+          acc[16 * half + c + 1] = a1;
         }
       }
     }
@@ -437,12 +519,12 @@ __global__ void __launch_bounds__(kNearThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------ table
-// One warp per table entry (bucket n of head h): it goes over all distances a near tile can hold
-// and adds those that map to the bucket, then the far fields.
+// ------------------------------------------------------------------ sums by distance
 constexpr int kMaxDiags = 640;
+constexpr int kOver = 2 * (kTile - 1);  // a near tile reaches that far past either end
 
-__global__ void __launch_bounds__(256) rel_table_kernel(const RelGradArgs a, int ctas, int chunks) {
+// Four threads per distance, one for each warpgroup's part of the diagonals' sums.
+__global__ void __launch_bounds__(256) rel_line_kernel(const RelGradArgs a, int ctas) {
   __shared__ long long start[kMaxDiags + 1];  // first pair of each group, within a head
   const NearList l = near_list(a);
   for (int g = threadIdx.x; g <= l.n_diag; g += 256) {
@@ -451,41 +533,71 @@ __global__ void __launch_bounds__(256) rel_table_kernel(const RelGradArgs a, int
     start[g] = n * l.B;
   }
   __syncthreads();
-  const int n = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, h = blockIdx.y;
-  if (n >= a.num_buckets) return;
   const long long per_head = start[l.n_diag];
   const long long per = max(1ll, near_per_cta(per_head * a.b.mask.H, ctas));
-  const int left = a.b.rel.left, right = a.b.rel.right, off = a.b.mask.q_off;
-  constexpr int kOver = 2 * (kTile - 1);  // a near tile reaches that far past either end
-  double sum = 0.0;
-  for (int x = lane; l.n_diag > 0 && x < left + right + 1 + 2 * kOver; x += 32) {
+  const int left = a.b.rel.left, right = a.b.rel.right, off = a.b.mask.q_off, h = blockIdx.y;
+  const int x = blockIdx.x * 64 + static_cast<int>(threadIdx.x >> 2), k = threadIdx.x & 3;
+  const int length = left + right + 1 + 2 * kOver;
+  float sum = 0.f;
+  if (x < length) {
     const int dist = x - left - kOver;
-    if (__ldg(a.map + clamp_distance(dist, left, right) + left) != n) continue;
-    const int e = dist + off + (kTile - 1);
-    const int diag = (e >= 0 ? e / kTile : -((-e + kTile - 1) / kTile)) - l.first;  // the last
-    for (int g = max(diag - 1, 0); g <= min(diag, l.n_diag - 1); ++g) {
-      const int at = dist - ((l.first + g) * kTile - off) + (kTile - 1);
-      if (at > 2 * (kTile - 1) || start[g + 1] == start[g]) continue;
+    const int last = floor_tiles(dist + off + (kTile - 1)) - l.first;  // group that reaches it last
+    for (int g = max(last - 1, 0); g <= min(last, l.n_diag - 1); ++g) {
+      const int e = dist - ((l.first + g) * kTile - off) + (kTile - 1) - 32 * k;
+      if (e < 0 || e >= 159 || start[g + 1] == start[g]) continue;
       const long long p0 = h * per_head + start[g], p1 = h * per_head + start[g + 1] - 1;
-      for (int c = static_cast<int>(p0 / per); c <= static_cast<int>(p1 / per); ++c) {
-        const float* s = a.diag_sums +
-                         (static_cast<size_t>(h) * l.n_diag + g + c) * kRelDiagFloats;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (at >= 32 * k && at < 32 * k + 159) sum += s[160 * k + at - 32 * k];
+      const int c1 = static_cast<int>(p1 / per);
+      const float* s = a.diag_sums + (static_cast<size_t>(h) * l.n_diag + g) * kRelDiagFloats +
+                       160 * k + e;
+#pragma unroll 4
+      for (int c = static_cast<int>(p0 / per); c <= c1; ++c)
+        sum += s[static_cast<size_t>(c) * kRelDiagFloats];
+    }
+  }
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  if (x < length && k == 0) a.line_sums[static_cast<size_t>(h) * length + x] = sum;
+}
+
+// ------------------------------------------------------------------ table
+// A block takes 32 buckets of a head, a lane each; its warps share the distances.
+__global__ void __launch_bounds__(256) rel_table_kernel(const RelGradArgs a, int chunks) {
+  __shared__ Sum part[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
+  const int n = blockIdx.x * 32 + lane;
+  const int left = a.b.rel.left, right = a.b.rel.right;
+  const int length = left + right + 1 + 2 * kOver;
+  const float* line = a.line_sums + static_cast<size_t>(h) * length;
+  Sum sum;
+  // 32 distances at a time, a lane each, then one after another for all buckets
+  for (int x0 = warp * 32; x0 < length; x0 += 256) {
+    const int x = x0 + lane;
+    const float v = x < length ? __ldg(line + x) : 0.f;
+    const int m = __ldg(a.map + clamp_distance(min(x, length - 1) - left - kOver, left, right) + left);
+    if (__any_sync(0xffffffffu, (m & ~31) == (n & ~31))) {
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const float vi = __shfl_sync(0xffffffffu, v, i);
+        const int mi = __shfl_sync(0xffffffffu, m, i);
+        sum.add(mi == n ? vi : 0.f);
       }
     }
   }
-  for (int side = 0; side < 2; ++side) {
-    if (__ldg(a.map + (side ? left + right : 0)) != n) continue;
-    for (int i = lane; i < a.b.mask.B * chunks; i += 32) {
-      const size_t bh = static_cast<size_t>(i / chunks) * a.b.mask.H + h;
-      sum += a.far_sums[(bh * chunks + i % chunks) * 2 + side];
-    }
+  // the far fields: even warps the left one's batch rows, odd warps the right one's
+  const int side = warp & 1;
+  Sum far;
+  for (int i = (warp >> 1) * 32 + lane; i < a.b.mask.B * chunks; i += 128) {
+    const size_t bh = static_cast<size_t>(i / chunks) * a.b.mask.H + h;
+    far.add(a.far_sums[(bh * chunks + i % chunks) * 2 + side]);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) a.dtable[static_cast<size_t>(n) * a.b.mask.H + h] = static_cast<float>(sum);
+  far.add_lanes();
+  if (__ldg(a.map + (side ? left + right : 0)) == n) sum.add(far);
+  part[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && n < a.num_buckets) {
+    for (int w = 1; w < 8; ++w) sum.add(part[w][lane]);
+    a.dtable[static_cast<size_t>(n) * a.b.mask.H + h] = sum.hi + sum.lo;
+  }
 }
 
 template <int D, bool DROPOUT>
@@ -526,7 +638,11 @@ cudaError_t launch_rel_grad(const CUtensorMap& tq, const CUtensorMap& tk, const 
                   : launch_near<128, false>(tq, tk, tv, tdo, a, ctas, stream);
   }
   if (e != cudaSuccess) return e;
-  rel_table_kernel<<<dim3((a.num_buckets + 7) / 8, m.H), 256, 0, stream>>>(a, ctas, chunks);
+  const int length = a.b.rel.left + a.b.rel.right + 1 + 2 * kOver;
+  rel_line_kernel<<<dim3((length + 63) / 64, m.H), 256, 0, stream>>>(a, ctas);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  rel_table_kernel<<<dim3((a.num_buckets + 31) / 32, m.H), 256, 0, stream>>>(a, chunks);
   return cudaGetLastError();
 }
 

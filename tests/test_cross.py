@@ -359,8 +359,8 @@ def test_c_entry_points_refuse_on_the_host():
     assert bwd(nb=1 << 17) == fa.FA_ERR_UNSUPPORTED
     need = fa.fa_bwd_cross_workspace_size(1, 4, 5, 9, 64, False, 0, True, 3, 3)
     assert bwd(ws=none) == bwd(wsb=need - 1) == bwd(ws=off) == fa.FA_ERR_WORKSPACE
-    # no table gradient: D alone, 20 floats
-    assert fa.fa_bwd_cross_workspace_size(1, 4, 5, 9, 64) == 256 < need
+    # no table gradient: D, 20 floats, and a list of up to 4 key tiles with their number
+    assert fa.fa_bwd_cross_workspace_size(1, 4, 5, 9, 64) == 512 < need
     assert fa.fa_bwd_cross_workspace_size(1, 4, 0, 9, 64) == 0
     assert fa.fa_bwd_cross_workspace_size(1, 4, 5, 9, 64, False, 0, True, -1, 3) == 0
 
