@@ -201,6 +201,9 @@ int fa_rel_line_length(int left, int right);
 fa_status fa_rel_bias(const void* table, int table_type, const int32_t* map, int left, int right,
                       int num_buckets, int H, float* lines, void* stream);
 
+/* fa_rel_bias with its arguments in a block (see fa_paged_attn_block). */
+fa_status fa_rel_bias_block(const int64_t* args, void* stream);
+
 /* Host helper: the usual map of distances to num_buckets buckets. Of half = num_buckets buckets
  * (num_buckets / 2 if bidirectional: keys behind the query's position take the second half), the
  * first half / 2 hold one distance each, the others share the distances up to max_distance by
@@ -297,8 +300,11 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, voi
 
 /* fa_decode with a bias by relative position: rel_lines as for fa_fwd_cross, row i of batch b at
  * position L_b - Nq + i. What the caches hold at and behind L_b, NaN and infinities too, does not
- * matter. Workspace and errors as fa_decode, plus FA_ERR_INVALID_ARG when rel_lines is null or Nk
- * is above 2^28. */
+ * matter. The key tiles within the lengths are divided among num_ctas CTAs (0: one per SM, and
+ * whole heads where Nk is at most 512) by the lengths found on the device, so a captured call may be
+ * replayed with other lengths. workspace: fa_decode_rel_workspace_size(...) bytes. Errors as
+ * fa_decode, plus FA_ERR_INVALID_ARG when rel_lines is null or Nk is above 2^28. */
+size_t fa_decode_rel_workspace_size(int B, int H, int H_kv, int Nq, int Nk, int d, int num_ctas);
 fa_status fa_decode_rel(const void* q, const void* k_cache, const void* v_cache, void* o,
                         float* lse, int B, int H, int H_kv, int Nq, int Nk, int d, float scale,
                         int causal, int window_left, const int32_t* seqlens_k,

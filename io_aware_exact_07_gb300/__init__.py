@@ -50,8 +50,9 @@ EXPORTS = (
     "fa_bwd_workspace_size", "fa_bwd_preprocess",
     "fa_bwd_dkdv", "fa_bwd_dq", "fa_decode", "fa_decode_workspace_size",
     "fa_fwd_cross", "fa_bwd_cross", "fa_bwd_cross_workspace_size", "fa_decode_rel",
+    "fa_decode_rel_workspace_size",
     "fa_fwd_cross_block", "fa_bwd_cross_block", "fa_decode_rel_block",
-    "fa_rel_line_length", "fa_rel_bias", "fa_rel_buckets",
+    "fa_rel_line_length", "fa_rel_bias", "fa_rel_bias_block", "fa_rel_buckets",
     "fa_paged_write", "fa_paged_read", "fa_paged_attn", "fa_paged_workspace_size",
     "fa_paged_write_block", "fa_paged_read_block", "fa_paged_attn_block",
     "fa_fp8_workspace_size", "fa_fp8_vt_stride", "fa_fp8_quantize", "fa_fwd_fp8",
@@ -129,6 +130,8 @@ def load(build_if_missing: bool = False):
         lib.fa_bwd_cross.argtypes = ([vp] * 9 + [i] * 6 + [f, i, i, i, i, f, u64, u64, vp, vp, i, i,
                                                            vp, i, vp, vp, sz, vp])
         lib.fa_bwd_cross.restype = i
+        lib.fa_decode_rel_workspace_size.argtypes = [i, i, i, i, i, i, i]
+        lib.fa_decode_rel_workspace_size.restype = sz
         lib.fa_decode_rel.argtypes = ([vp] * 5 + [i] * 6 + [f, i, i, vp, vp, i, i, i, vp, sz, vp])
         lib.fa_decode_rel.restype = i
         lib.fa_rel_line_length.argtypes = [i, i]
@@ -144,7 +147,8 @@ def load(build_if_missing: bool = False):
         lib.fa_paged_read.argtypes = [vp] * 4 + cache + [i, i, vp, vp, vp]
         lib.fa_paged_read.restype = i
         for f_block in (lib.fa_paged_write_block, lib.fa_paged_read_block, lib.fa_paged_attn_block,
-                        lib.fa_fwd_cross_block, lib.fa_bwd_cross_block, lib.fa_decode_rel_block):
+                        lib.fa_fwd_cross_block, lib.fa_bwd_cross_block, lib.fa_decode_rel_block,
+                        lib.fa_rel_bias_block):
             f_block.argtypes = [ctypes.c_char_p, vp]
             f_block.restype = i
         lib.fa_paged_workspace_size.argtypes = [i, i, i, i, i]
@@ -422,6 +426,10 @@ def fa_bwd_cross(q, k, v, o, dout, lse, dq, dk, dv, B, H, H_kv, Nq, Nk, d, scale
                                _seqlens_ptr(seqlens_k, B), _ptr(rel_lines), int(rel_left),
                                int(rel_right), _ptr(rel_map), int(num_buckets), _ptr(dtable),
                                _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def fa_decode_rel_workspace_size(B, H, H_kv, Nq, Nk, d, num_ctas=0) -> int:
+    return int(load().fa_decode_rel_workspace_size(B, H, H_kv, Nq, Nk, d, num_ctas))
 
 
 def fa_decode_rel(q, k_cache, v_cache, o, lse, B, H, H_kv, Nq, Nk, d, scale, rel_lines, rel_left,
@@ -744,29 +752,29 @@ def rel_buckets(num_buckets=32, max_distance=128, bidirectional=True, device="cu
 def rel_bias(table, buckets, stream=None):
     """Lay out a bias table [num_buckets, H] (fp32 or bf16, one learned bias per bucket and query
     head) for fwd, bwd and decode (fa_rel_bias). Do so again after the table changes."""
-    dev = table.get_device()
-    m, left = buckets.map, buckets.left
-    if (table.dim() != 2 or table.shape[0] != buckets.num_buckets or dev < 0
-            or table.dtype not in (torch.float32, torch.bfloat16) or not table.is_contiguous()):
-        raise ValueError("table must be a contiguous fp32 or bf16 CUDA tensor "
-                         f"[{buckets.num_buckets}, H]")
+    dev, dtype, shape = table.get_device(), table.dtype, table.shape
+    m, left, rows = buckets
+    if (len(shape) != 2 or shape[0] != rows or dev < 0
+            or dtype not in (torch.float32, torch.bfloat16) or not table.is_contiguous()):
+        raise ValueError(f"table must be a contiguous fp32 or bf16 CUDA tensor [{rows}, H]")
     if (m.dtype != torch.int32 or m.dim() != 1 or not m.is_contiguous() or m.get_device() != dev
             or not 0 <= left < m.numel()):
         raise ValueError("the map must be contiguous int32 on the table's device, and hold "
                          "distance 0")
-    H = table.shape[1]
-    length = fa_rel_line_length(left, buckets.right)
+    H, right = shape[1], m.numel() - 1 - left
     with _memory_on(stream, dev):
-        lines = table.new_empty((H, length), dtype=torch.float32)
-    kind = FA_TABLE_F32 if table.dtype == torch.float32 else FA_TABLE_BF16
-    with torch.cuda.device(dev):
-        st = fa_rel_bias(table, kind, m, left, buckets.right, buckets.num_buckets, H, lines,
-                         stream)
-    _check(st, "fa_rel_bias")
-    _given_out(stream, dev, lines)
+        lines = table.new_empty((H, left + right + 1 + _REL_PAD), dtype=torch.float32)
+    _call("fa_rel_bias_block", dev, stream,
+          _REL_BIAS_BLOCK(table.data_ptr(),
+                          FA_TABLE_F32 if dtype == torch.float32 else FA_TABLE_BF16, m.data_ptr(),
+                          left, right, rows, H, lines.data_ptr()))
+    if stream is not None:
+        _given_out(stream, dev, lines)
     return RelBias(lines, buckets)
 
 
+_REL_PAD = 512  # a line's floats beyond its distances (fa_rel_line_length)
+_REL_BIAS_BLOCK = struct.Struct("=8q").pack
 _FWD_CROSS_BLOCK = struct.Struct("=11qd4qdQQ4q").pack
 _BWD_CROSS_BLOCK = struct.Struct("=15qd4qdQQ9q").pack
 _DECODE_REL_BLOCK = struct.Struct("=11qd9q").pack
@@ -789,7 +797,7 @@ def _cross_args(q, k, v, scale, seqlens_k, rel):
     bias = (0, 0, 0)
     if rel is not None:
         left, right = rel.buckets.left, rel.buckets.right
-        if (rel.lines.shape != (H, left + right + 513) or rel.lines.dtype != torch.float32
+        if (rel.lines.shape != (H, left + right + 1 + _REL_PAD) or rel.lines.dtype != torch.float32
                 or rel.lines.get_device() != dev or not rel.lines.is_contiguous()):
             raise ValueError(f"rel_bias must come from rel_bias() with a table of {H} heads, on "
                              "q's device")
@@ -856,14 +864,15 @@ def _bwd_cross(q, k, v, o, dout, lse, scale, causal, dropout_p, seed, offset, bl
     return out
 
 
-_decode_workspace_bytes = functools.lru_cache(maxsize=4096)(
-    lambda dev, *sizes: fa_decode_workspace_size(*sizes))
+@functools.lru_cache(maxsize=4096)
+def _decode_rel_workspace_bytes(sizes, num_ctas, dev):
+    with torch.cuda.device(dev):  # depends on the device's number of SMs
+        return fa_decode_rel_workspace_size(*sizes, num_ctas)
 
 
 def _decode_rel(q, k_cache, v_cache, scale, causal, seqlens_k, num_ctas, stream, window_left, rel):
     sizes, scale, sl, bias, dev = _cross_args(q, k_cache, v_cache, scale, seqlens_k, rel)
-    with torch.cuda.device(dev):  # the split depends on the device's number of SMs
-        ws_bytes = _decode_workspace_bytes(dev, *sizes, num_ctas)
+    ws_bytes = _decode_rel_workspace_bytes(sizes, num_ctas, dev)
     with _memory_on(stream, dev):
         o = torch.empty_like(q)
         lse = q.new_empty(q.shape[:3], dtype=torch.float32)

@@ -555,23 +555,28 @@ size_t fa_decode_workspace_size(int B, int H, int H_kv, int Nq, int Nk, int d, i
   return decode_ws_bytes(B, H, Nq, d, p);
 }
 
-static fa_status check_lines(const float* lines, int left, int right);
+// Checks that the decode calls share.
+static fa_status check_decode(const void* q, const void* k, const void* v, const void* o,
+                              const float* lse, float scale, int window_left,
+                              const int32_t* seqlens_k) {
+  if (window_left < -1) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, o})
+    if (!p || !aligned16(p)) return FA_ERR_INVALID_ARG;
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(seqlens_k) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
 
-static fa_status decode_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
-                             float* lse, int B, int H, int H_kv, int Nq, int Nk, int d,
-                             float scale, int causal, int window_left, const int32_t* seqlens_k,
-                             int num_ctas, const fa::RelParams& rel, void* workspace,
-                             size_t workspace_bytes, void* stream) {
+fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                    int B, int H, int H_kv, int Nq, int Nk, int d, float scale, int causal,
+                    int window_left, const int32_t* seqlens_k, int num_ctas, void* workspace,
+                    size_t workspace_bytes, void* stream) {
   DecodePlan p;
   fa_status st = decode_plan(B, H, H_kv, Nq, Nk, d, num_ctas, &p);
   if (st != FA_OK) return st;
-  if (window_left < -1) return FA_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
-  if (!q || !k_cache || !v_cache || !o || !lse) return FA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o))
-    return FA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(seqlens_k) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  if ((st = check_decode(q, k_cache, v_cache, o, lse, scale, window_left, seqlens_k)) != FA_OK)
+    return st;
   const size_t ws = decode_ws_bytes(B, H, Nq, d, p);
   if (ws > 0 && (workspace == nullptr || workspace_bytes < ws || !aligned16(workspace)))
     return FA_ERR_WORKSPACE;
@@ -597,7 +602,9 @@ static fa_status decode_impl(const void* q, const void* k_cache, const void* v_c
   a.sync = make_sync(di, kStallForward);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  a.rel = rel;
+  a.rel = fa::RelParams{};
+  a.whole = 0;
+  a.pieces = nullptr;
   const size_t slots = static_cast<size_t>(B) * H * Nq * p.seg_max;
   a.o_part = ws > 0 ? static_cast<float*>(workspace) : nullptr;
   a.lse_part = ws > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
@@ -609,14 +616,77 @@ static fa_status decode_impl(const void* q, const void* k_cache, const void* v_c
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
-                    int B, int H, int H_kv, int Nq, int Nk, int d, float scale, int causal,
-                    int window_left, const int32_t* seqlens_k, int num_ctas, void* workspace,
-                    size_t workspace_bytes, void* stream) {
-  return decode_impl(q, k_cache, v_cache, o, lse, B, H, H_kv, Nq, Nk, d, scale, causal,
-                     window_left, seqlens_k, num_ctas, fa::RelParams{}, workspace,
-                     workspace_bytes, stream);
+// Workspace of fa_paged_attn: one header per CTA, then the pieces' lse and outputs.
+struct PagedWorkspace {
+  int ctas, rows;
+  bool whole;  // a step over few keys: no head is cut, nothing is left behind
+  size_t lse_off, o_off, bytes;
+};
+static PagedWorkspace paged_workspace(int G, int d, int max_q, long long max_keys, int num_sms) {
+  PagedWorkspace w;
+  const long long rows = static_cast<long long>(G) * max_q;
+  w.whole = rows <= fa::kStepRows && max_keys <= fa::kWholeKeys;
+  w.ctas = num_sms < 256 ? num_sms : 256;  // the chunk kernel plans with a thread per CTA
+  w.rows = rows <= fa::kStepRows ? static_cast<int>((rows + 7) / 8 * 8) : fa::kTile;
+  const size_t slots = 2 * static_cast<size_t>(w.ctas) * w.rows;
+  w.lse_off = round256(static_cast<size_t>(w.ctas) * 16);
+  w.o_off = w.lse_off + round256(slots * sizeof(float));
+  w.bytes = w.whole ? 0 : w.o_off + round256(slots * d * sizeof(float));
+  return w;
 }
+
+// Plan of fa_decode_rel: the CTAs find their shares from the lengths on the device. Few query rows
+// per K/V head run on the paged cache's step kernel, more as tiles of 128 rows. us with the one and
+// the other: d = 64, 32 ragged sequences of up to 4096 keys, 16 K/V heads, 1 row 53 and 84, 16 rows
+// 76 and 87, 20 rows 96 and 87; 4 of up to 500 keys 16 rows 10.2 and 10.5; d = 128, the same with 8
+// K/V heads 8 rows 55.7 and 55.4, 12 rows 63 and 56; 1 of 131001 keys 8 rows 87 and 91, 16 89 and 91.
+struct RelDecodePlan {
+  bool step;
+  int grid, whole;
+  PagedWorkspace w;                // step
+  size_t lse_off, pieces_off, bytes;
+};
+
+static fa_status rel_decode_plan(int B, int H, int Hkv, int Nq, int Nk, int d, int num_ctas,
+                                 RelDecodePlan* p) {
+  DecodePlan q;  // for its checks
+  const fa_status st = decode_plan(B, H, Hkv, Nq, Nk, d, num_ctas > 0 ? num_ctas : 1, &q);
+  if (st != FA_OK) return st;
+  if (num_ctas < 0 || Nk > kMaxAxis) return FA_ERR_INVALID_ARG;
+  int ctas = num_ctas;
+  if (ctas == 0) {
+    DeviceInfo* di = nullptr;
+    const fa_status dev = device_info(&di);
+    if (dev != FA_OK) return dev;
+    ctas = di->num_sms;
+  }
+  const long long heads = static_cast<long long>(B) * Hkv;
+  const size_t rows = static_cast<size_t>(H / Hkv) * Nq;
+  p->step = rows <= (d == 64 ? 16 : 8);
+  if (p->step) {
+    p->w = paged_workspace(H / Hkv, d, Nq, num_ctas > 0 ? kMaxAxis : Nk, ctas);
+    p->grid = p->w.ctas;
+    p->whole = p->w.whole;
+    p->bytes = p->w.bytes;
+    return FA_OK;
+  }
+  p->whole = num_ctas == 0 && Nk <= fa::kWholeKeys;
+  const long long most = p->whole ? heads : heads * q.n_t;
+  p->grid = static_cast<int>(ctas < most ? ctas : most);
+  const size_t slots = (heads + p->grid) * rows;
+  p->lse_off = round256(slots * d * sizeof(float));
+  p->pieces_off = p->lse_off + round256(slots * sizeof(float));
+  p->bytes = p->whole ? 0 : p->pieces_off + round256(heads * sizeof(int2));
+  return FA_OK;
+}
+
+size_t fa_decode_rel_workspace_size(int B, int H, int H_kv, int Nq, int Nk, int d, int num_ctas) {
+  RelDecodePlan p;
+  if (rel_decode_plan(B, H, H_kv, Nq, Nk, d, num_ctas, &p) != FA_OK) return 0;
+  return p.bytes;
+}
+
+static fa_status check_lines(const float* lines, int left, int right);
 
 fa_status fa_decode_rel(const void* q, const void* k_cache, const void* v_cache, void* o,
                         float* lse, int B, int H, int H_kv, int Nq, int Nk, int d, float scale,
@@ -625,10 +695,77 @@ fa_status fa_decode_rel(const void* q, const void* k_cache, const void* v_cache,
                         void* workspace, size_t workspace_bytes, void* stream) {
   fa_status st = check_lines(rel_lines, rel_left, rel_right);
   if (st != FA_OK) return st;
-  if (Nk > kMaxAxis) return FA_ERR_INVALID_ARG;
-  return decode_impl(q, k_cache, v_cache, o, lse, B, H, H_kv, Nq, Nk, d, scale, causal,
-                     window_left, seqlens_k, num_ctas, fa::RelParams{rel_lines, rel_left, rel_right},
-                     workspace, workspace_bytes, stream);
+  RelDecodePlan p;
+  if ((st = rel_decode_plan(B, H, H_kv, Nq, Nk, d, num_ctas, &p)) != FA_OK) return st;
+  if ((st = check_decode(q, k_cache, v_cache, o, lse, scale, window_left, seqlens_k)) != FA_OK)
+    return st;
+  if (p.bytes > 0 && (workspace == nullptr || workspace_bytes < p.bytes || !aligned16(workspace)))
+    return FA_ERR_WORKSPACE;
+  DeviceInfo* di = nullptr;
+  if ((st = device_info(&di)) != FA_OK) return st;
+  const fa::RelParams rel{rel_lines, rel_left, rel_right};
+  if (window_left >= Nk) window_left = -1;  // hides nothing
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (p.step) {
+    fa::PagedAttnArgs a = {};
+    a.c.k = static_cast<uint8_t*>(const_cast<void*>(k_cache));
+    a.c.v = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+    a.c.Hkv = H_kv;
+    a.c.d = d;
+    a.c.stride_page = static_cast<long long>(H_kv) * Nk * d;
+    a.c.stride_head = static_cast<long long>(Nk) * d;
+    a.c.stride_row = d;
+    a.c.kv_lens = seqlens_k;
+    a.c.B = B;
+    a.c.T = B * Nq;
+    a.c.max_q = Nq;
+    a.c.status = di->status;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.H = H;
+    a.G = H / H_kv;
+    a.o = static_cast<__nv_bfloat16*>(o);
+    a.lse = lse;
+    a.scale_log2 = scale * fa::kLog2e;
+    a.causal = causal ? 1 : 0;
+    a.wl = window_left;
+    a.whole = p.whole;
+    if (!p.whole) {
+      a.headers = ws;
+      a.lse_part = reinterpret_cast<float*>(ws + p.w.lse_off);
+      a.o_part = reinterpret_cast<float*>(ws + p.w.o_off);
+    }
+    a.rel = rel;
+    a.Nk = Nk;
+    return fa::launch_rel_step(a, p.grid, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  }
+  CUtensorMap tq, tk, tv;
+  if (!encode_map(&tq, q, 1, B * H * Nq, d) || !encode_map(&tk, k_cache, B * H_kv, Nk, d) ||
+      !encode_map(&tv, v_cache, B * H_kv, Nk, d))
+    return FA_ERR_CUDA;
+  fa::DecodeArgs a = {};
+  a.B = B;
+  a.H = H;
+  a.Hkv = H_kv;
+  a.Nq = Nq;
+  a.Nk = Nk;
+  a.causal = causal ? 1 : 0;
+  a.wl = window_left;
+  a.seqlens_k = seqlens_k;
+  a.scale_log2 = scale * fa::kLog2e;
+  a.sync = make_sync(di, kStallForward);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.rel = rel;
+  a.whole = p.whole;
+  if (!p.whole) {
+    a.o_part = reinterpret_cast<float*>(ws);
+    a.lse_part = reinterpret_cast<float*>(ws + p.lse_off);
+    a.pieces = reinterpret_cast<int2*>(ws + p.pieces_off);
+  }
+  cudaError_t e = fa::launch_decode(tq, tk, tv, a, d, p.grid, s);
+  if (e == cudaSuccess && !p.whole) e = fa::launch_decode_combine(a, d, s);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 static fa_status check_lines(const float* lines, int left, int right) {
@@ -1117,25 +1254,6 @@ fa_status fa_paged_read(const void* k_pages, const void* v_pages, const uint8_t*
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// Workspace of fa_paged_attn: one header per CTA, then the pieces' lse and outputs.
-struct PagedWorkspace {
-  int ctas, rows;
-  bool whole;  // a step over few keys: no head is cut, nothing is left behind
-  size_t lse_off, o_off, bytes;
-};
-static PagedWorkspace paged_workspace(int G, int d, int max_q, long long max_keys, int num_sms) {
-  PagedWorkspace w;
-  const long long rows = static_cast<long long>(G) * max_q;
-  w.whole = rows <= fa::kStepRows && max_keys <= fa::kWholeKeys;
-  w.ctas = num_sms < 256 ? num_sms : 256;  // the chunk kernel plans with a thread per CTA
-  w.rows = rows <= fa::kStepRows ? static_cast<int>((rows + 7) / 8 * 8) : fa::kTile;
-  const size_t slots = 2 * static_cast<size_t>(w.ctas) * w.rows;
-  w.lse_off = round256(static_cast<size_t>(w.ctas) * 16);
-  w.o_off = w.lse_off + round256(slots * sizeof(float));
-  w.bytes = w.whole ? 0 : w.o_off + round256(slots * d * sizeof(float));
-  return w;
-}
-
 size_t fa_paged_workspace_size(int H, int H_kv, int d, int max_q, int max_keys) {
   DeviceInfo* di = nullptr;
   if (H < 1 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128) || max_q < 1 ||
@@ -1269,6 +1387,11 @@ fa_status fa_bwd_cross_block(const int64_t* x, void* stream) {
                       static_cast<uint64_t>(x[22]), i32(23), static_cast<float*>(p(24)), n(25),
                       n(26), i32(27), n(28), static_cast<float*>(p(29)), p(30),
                       static_cast<size_t>(x[31]), stream);
+}
+
+fa_status fa_rel_bias_block(const int64_t* x, void* stream) {
+  FA_BLOCK_INTS(1, 3, 4, 5, 6)
+  return fa_rel_bias(p(0), n(1), i32(2), n(3), n(4), n(5), n(6), static_cast<float*>(p(7)), stream);
 }
 
 fa_status fa_decode_rel_block(const int64_t* x, void* stream) {

@@ -21,6 +21,7 @@
 
 #include "fa_common.cuh"
 #include "fa_kernels.h"
+#include "fa_launch.cuh"
 
 namespace fa {
 
@@ -706,11 +707,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
-template <typename K>
-cudaError_t set_smem(K kern, int bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 }  // namespace
 
 cudaError_t launch_bwd_preprocess(const BwdArgs& a, int d, int num_sms, cudaStream_t stream) {
@@ -742,7 +738,9 @@ static cudaError_t launch_dkdv_impl(const CUtensorMap& tq, const CUtensorMap& tk
   };
   auto kern = a.mask.Hkv != a.mask.H ? pick(std::true_type{}) : pick(std::false_type{});
   constexpr int kSmem = DkdvLayout<D, DROP>::kSmemBytes;
-  cudaError_t e = set_smem(kern, kSmem);
+  static std::atomic<unsigned long long> ready[2][4];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem, 0,
+                             ready[a.mask.Hkv != a.mask.H][a.mode]);
   if (e != cudaSuccess) return e;
   kern<<<grid, kBwdThreads, kSmem, stream>>>(tq, tk, tv, tdo, a);
   return cudaGetLastError();

@@ -22,6 +22,7 @@
 
 #include "fa_common.cuh"
 #include "fa_kernels.h"
+#include "fa_launch.cuh"
 
 namespace fa {
 
@@ -1393,22 +1394,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Shared-memory opt-in, and a check that the kernel was built for the
-// register count its in-kernel reallocation assumes: launched with fewer
-// registers per thread, the compute warpgroups' increase could never be granted
-// and would wait forever, so such a kernel is refused instead of launched.
-template <typename K>
-cudaError_t set_smem_split(K kern, int bytes, bool realloc) {
-  if (realloc) {
-    cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs < kRegsLaunch || attr.maxThreadsPerBlock < kThreads)
-      return cudaErrorInvalidConfiguration;
-  }
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
+// (The launches below check that a kernel was built for the register count its in-kernel
+// reallocation assumes: launched with fewer registers per thread, the compute warpgroups' increase
+// could never be granted and would wait forever, so such a kernel is refused instead of launched.)
 template <int D>
 cudaError_t launch_dkdv_split_d(const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, const CUtensorMap& tdo, const BwdArgs& a,
@@ -1424,7 +1412,9 @@ cudaError_t launch_dkdv_split_d(const CUtensorMap& tq, const CUtensorMap& tk,
   const std::false_type no;
   auto kern = a.mask.Hkv != a.mask.H ? (dropout ? pick(yes, yes) : pick(no, yes))
                                      : (dropout ? pick(yes, no) : pick(no, no));
-  cudaError_t e = set_smem_split(kern, DkdvL<D>::kSmemBytes, true);
+  static std::atomic<unsigned long long> ready[2][2][4];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), DkdvL<D>::kSmemBytes, kRegsLaunch,
+                             ready[a.mask.Hkv != a.mask.H][dropout][a.mode]);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, DkdvL<D>::kSmemBytes, stream>>>(tq, tk, tv, tdo, a);
   return cudaGetLastError();
@@ -1445,7 +1435,9 @@ cudaError_t launch_dq_split_d(const CUtensorMap& tq, const CUtensorMap& tk, cons
   const bool realloc = dropout ? DqRealloc<D, true, kPlain>::value
                        : a.mode == kRel ? DqRealloc<D, false, kRel>::value
                                         : DqRealloc<D, false, kPlain>::value;
-  cudaError_t e = set_smem_split(kern, DqL<D>::kSmemBytes, realloc);
+  static std::atomic<unsigned long long> ready[2][4];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), DqL<D>::kSmemBytes,
+                             realloc ? kRegsLaunch : 0, ready[dropout][a.mode]);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, DqL<D>::kSmemBytes, stream>>>(tq, tk, tv, tdo, a);
   return cudaGetLastError();

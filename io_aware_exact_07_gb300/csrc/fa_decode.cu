@@ -29,6 +29,7 @@
 
 #include "fa_common.cuh"
 #include "fa_decode.h"
+#include "fa_launch.cuh"
 
 namespace fa {
 
@@ -76,6 +77,7 @@ struct DecBars {
 // head and their number.
 struct Piece {
   int bkv, j0, j1, seg, n_seg;
+  int starts;  // RelWalk: number of the head's pieces where this is its first, else 0
 };
 
 // Valid cache length of batch row b, clamped to [0, Nk].
@@ -110,6 +112,138 @@ __device__ __forceinline__ long long make_piece(const DecodeArgs& a, int cta, lo
   p.seg = cta - c0;
   p.n_seg = c1 - c0 + 1;
   return end;
+}
+
+// The pieces of a CTA's run over the flattened pairs.
+struct PlainWalk {
+  long long pos, hi;
+  __device__ __forceinline__ bool next(const DecodeArgs& a, Piece& p) {
+    if (pos >= hi) return false;
+    pos = make_piece(a, blockIdx.x, pos, hi, p);
+    return true;
+  }
+};
+
+// Key tiles [lo, hi) that batch row b has to read. A head is listed with its tiles and the cost of
+// starting and finishing a piece in front of them, in tiles: the softmax warps wait for a piece's
+// last product and write its rows before they go on. (32 sequences of up to 4096 keys, 16 K/V heads,
+// 20 rows, d = 64, a cost of 2, 4, 6: 77, 74 and 72 us; d = 128, 8 K/V heads: 58, 55, 53.)
+constexpr int kPieceTiles = 6;
+struct RowTiles {
+  int lo, hi;
+  __device__ __forceinline__ int listed() const { return kPieceTiles + hi - lo; }
+};
+__device__ __forceinline__ RowTiles row_tiles(const DecodeArgs& a, int b) {
+  const int L = cache_len(a, b);
+  RowTiles t{0, (L + kTile - 1) / kTile};
+  if (a.wl >= 0) t.lo = min(t.hi, max(0, L - a.Nq - a.wl) / kTile);
+  return t;
+}
+
+// The same over the pairs within the lengths, for the bias by relative position, by K/V head and
+// then batch row, so that a CTA's heads have unlike lengths: batch row, K/V head of it, and how far
+// the head's tiles are done; `left` pairs remain (whole: heads).
+struct RelWalk {
+  int b, h, done, left, per;
+  __device__ __forceinline__ bool next(const DecodeArgs& a, Piece& p) {
+    if (left <= 0) return false;
+    if (a.whole) {
+      const int head = b * a.Hkv + h;
+      const RowTiles t = row_tiles(a, b);
+      p = Piece{head, t.lo, t.hi, 0, 1, 1};
+      --left;
+      const int then = head + static_cast<int>(gridDim.x);
+      b = then / a.Hkv;
+      h = then - b * a.Hkv;
+      return true;
+    }
+    while (left > 0) {
+      const RowTiles t = row_tiles(a, b);
+      const int listed = t.listed(), n = min(left, listed - done);
+      const int from = done - kPieceTiles, to = from + n;  // tiles of the head
+      p.bkv = b * a.Hkv + h;
+      p.j0 = t.lo + max(0, from);
+      p.j1 = t.lo + max(0, to);
+      p.seg = h * a.B + b + static_cast<int>(blockIdx.x);  // heads in the list's order
+      p.n_seg = from <= 0 && t.lo + to == t.hi ? 1 : 2;
+      p.starts = from <= 0 ? 1 + (t.hi - t.lo - max(0, to) + per - 1) / per : 0;
+      // a head without tiles is written where its list begins, another where it has tiles
+      const bool mine = p.j1 > p.j0 || (t.lo == t.hi && done == 0);
+      if (t.lo == t.hi) p.n_seg = p.starts = 1;
+      left -= n;
+      done += n;
+      if (done == listed) {
+        done = 0;
+        if (++b == a.B) {
+          b = 0;
+          ++h;
+        }
+      }
+      if (mine) return true;
+    }
+    return false;
+  }
+};
+
+// This CTA's walk, found by the whole block; `scratch` holds 2 * kDecThreads + 8 words.
+__device__ __forceinline__ RelWalk rel_walk(const DecodeArgs& a, int* scratch) {
+  const int tid = threadIdx.x, cta = blockIdx.x, ctas = gridDim.x;
+  RelWalk w{0, 0, 0, 0, 1};
+  if (a.whole) {
+    w.b = cta / a.Hkv;
+    w.h = cta - w.b * a.Hkv;
+    w.left = (a.B * a.Hkv - cta + ctas - 1) / ctas;
+    return w;
+  }
+  // thread t sums up the batch rows [t chunk, (t + 1) chunk), warp 0 the threads before each
+  const int chunk = (a.B + kDecThreads - 1) / kDecThreads;
+  const int b0 = min(a.B, tid * chunk), b1 = min(a.B, b0 + chunk);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += row_tiles(a, b).listed();
+  scratch[tid] = mine;
+  __syncthreads();
+  int* before = scratch + kDecThreads;
+  int* found = before + kDecThreads;  // [0]: all batch rows; [1 ..]: the CTA's first pair
+  if (tid < 32) {
+    constexpr int kPer = kDecThreads / 32;
+    int sum = 0;
+    for (int i = 0; i < kPer; ++i) sum += scratch[tid * kPer + i];
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (tid >= o) upto += x;
+    }
+    int at = upto - sum;
+    for (int i = 0; i < kPer; ++i) {
+      before[tid * kPer + i] = at;
+      at += scratch[tid * kPer + i];
+    }
+    if (tid == 31) found[0] = upto;
+  }
+  __syncthreads();
+  const int total = found[0] * a.Hkv;  // (B * Hkv * n_t and the pieces' costs stay below 2^31)
+  w.per = (total + ctas - 1) / ctas;
+  const int lo = min(total, cta * w.per);
+  w.left = min(w.per, total - lo);
+  int at = before[tid];
+  const int first = lo % found[0];
+  if (w.left > 0 && first >= at && first < at + mine) {
+    for (int b = b0;; ++b) {
+      const int n = row_tiles(a, b).listed();
+      if (first < at + n) {
+        found[1] = b;
+        found[2] = first - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  w.b = found[1];
+  w.h = lo / found[0];
+  w.done = found[2];
+  return w;
 }
 
 }  // namespace
@@ -192,6 +326,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint64_t tmo = args.sync.timeout_ns;
+  if constexpr (REL) pdl_launch_dependents();
+  // (the rings are not in use yet)
+  const auto first = [&]() {
+    if constexpr (REL) {
+      return rel_walk(args, reinterpret_cast<int*>(smem + L::kKOff));
+    } else {
+      return PlainWalk{lo, hi};
+    }
+  }();
+  if constexpr (REL) {
+    // what the walk left in the ring comes before the copies into it
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
   auto fail = [&](void) {
     *abort_flag = 1;
     record_error(args.sync.status, kStatusTimeout);
@@ -209,9 +357,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       uint32_t it = 0, k_arms = 0, v_arms = 0, q_arms = 0;
       bool ok = true;
       int np = 0;
-      for (long long pos = lo; pos < hi && ok; ++np) {
-        Piece pc;
-        pos = make_piece(args, blockIdx.x, pos, hi, pc);
+      auto walk = first;
+      for (Piece pc; ok && walk.next(args, pc); ++np) {
         if (np > 0 && !mbar_wait(bars.q_empty, (np - 1) & 1, tmo, abort_flag)) {
           fail();
           ok = false;
@@ -270,9 +417,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       // Test hook: a barrier that nothing completes, so the bounded wait runs out.
       if (args.sync.inject_stall && !mbar_wait(bars.stall, 0, tmo, abort_flag)) ok = false;
       int np = 0;
-      for (long long pos = lo; pos < hi && ok; ++np) {
-        Piece pc;
-        pos = make_piece(args, blockIdx.x, pos, hi, pc);
+      auto walk = first;
+      for (Piece pc; ok && walk.next(args, pc); ++np) {
         if (!mbar_wait(bars.q_full, np & 1, tmo, abort_flag)) {
           ok = false;
           break;
@@ -319,9 +465,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       int n_full = 0;  // pieces with at least one key tile so far (O handshakes)
-      for (long long pos = lo; pos < hi && ok;) {
-        Piece pc;
-        pos = make_piece(args, blockIdx.x, pos, hi, pc);
+      auto walk = first;
+      for (Piece pc; ok && walk.next(args, pc);) {
         for (int j = pc.j0; j < pc.j1; ++j) {
           const int s = it % L::kStages;
           const uint32_t x = it % kSBufs;
@@ -368,9 +513,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     bool ok = true;
     int np = 0;
     int n_full = 0;  // pieces with at least one key tile so far
-    for (long long pos = lo; pos < hi && ok; ++np) {
-      Piece pc;
-      pos = make_piece(args, blockIdx.x, pos, hi, pc);
+    auto walk = first;
+    for (Piece pc; ok && walk.next(args, pc); ++np) {
       const int Lb = cache_len(args, pc.bkv / args.Hkv);
       int vis = Lb;  // keys [key_lo, vis) are visible to this row
       if (args.causal) {
@@ -525,6 +669,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const float inv = (l_sum > 0.f) ? 1.f / l_sum : 0.f;
       const float lse = (l_sum > 0.f) ? (m_ref + __log2f(l_sum)) * kLn2 : -INFINITY;
       const bool direct = pc.n_seg == 1;
+      const size_t slot = REL ? static_cast<size_t>(pc.seg) * M + r : row * args.seg_max + pc.seg;
+      if (REL && r == 0 && pc.starts > 0 && args.pieces != nullptr)
+        args.pieces[pc.bkv] = make_int2(static_cast<int>(blockIdx.x), pc.starts);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -548,8 +695,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          float4* dst = reinterpret_cast<float4*>(
-              args.o_part + (row * args.seg_max + pc.seg) * D + c * 32);
+          float4* dst = reinterpret_cast<float4*>(args.o_part + slot * D + c * 32);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             dst[k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
@@ -561,7 +707,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (direct)
           args.lse[row] = lse;
         else
-          args.lse_part[row * args.seg_max + pc.seg] = lse;
+          args.lse_part[slot] = lse;
       }
       if (any) {  // O may now be overwritten by the next piece's first PV
         tc_fence_before();
@@ -583,7 +729,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 // lse_s = m_s + ln l_s and normalised O_s, the whole-cache result is
 // O = sum_s e^{lse_s - m} O_s / sum_s e^{lse_s - m}, lse = m + ln sum_s e^{lse_s - m},
 // m = max_s lse_s (the two-block merge of the online softmax applied piecewise).
-template <int D>
+template <int D, bool REL>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     fa_decode_combine_kernel(const DecodeArgs a) {
   constexpr int kPer = D / 32;  // columns per lane
@@ -592,21 +738,35 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const long long row = static_cast<long long>(blockIdx.x) * kCombineWarps + warp;
   if (row >= rows) return;
   const int M = (a.H / a.Hkv) * a.Nq;
-  const long long head0 = (row / M) * a.n_t;
-  const int n_seg = static_cast<int>((head0 + a.n_t - 1) / a.per_cta - head0 / a.per_cta) + 1;
+  int n_seg;
+  size_t slot0, step;  // slots of the row's pieces
+  if constexpr (REL) {
+    pdl_wait();  // this kernel may have begun before the pieces are written
+    const int bkv = static_cast<int>(row / M);
+    const int2 p = a.pieces[bkv];
+    n_seg = p.y;
+    const int b = bkv / a.Hkv, rank = (bkv - b * a.Hkv) * a.B + b;  // in the list's order
+    slot0 = static_cast<size_t>(rank + p.x) * M + static_cast<size_t>(row % M);
+    step = M;
+  } else {
+    const long long head0 = (row / M) * a.n_t;
+    n_seg = static_cast<int>((head0 + a.n_t - 1) / a.per_cta - head0 / a.per_cta) + 1;
+    slot0 = static_cast<size_t>(row) * a.seg_max;
+    step = 1;
+  }
   if (n_seg == 1) return;  // finished by its only CTA
-  const float* lp = a.lse_part + row * a.seg_max;
+  const float* lp = a.lse_part + slot0;
   float m = -INFINITY;
-  for (int s = 0; s < n_seg; ++s) m = fmaxf(m, lp[s]);
+  for (int s = 0; s < n_seg; ++s) m = fmaxf(m, lp[s * step]);
   float acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
   float den = 0.f;
   if (m != -INFINITY) {
     for (int s = 0; s < n_seg; ++s) {
-      const float w = ex2_approx((lp[s] - m) * kLog2e);  // 0 for an empty piece
+      const float w = ex2_approx((lp[s * step] - m) * kLog2e);  // 0 for an empty piece
       den += w;
-      const float* op = a.o_part + (row * a.seg_max + s) * D + lane * kPer;
+      const float* op = a.o_part + (slot0 + s * step) * D + lane * kPer;
       if constexpr (kPer == 4) {
         const float4 v = *reinterpret_cast<const float4*>(op);
         acc[0] += w * v.x;
@@ -637,9 +797,9 @@ template <int D, bool REL>
 static cudaError_t launch_decode_d(const CUtensorMap& tq, const CUtensorMap& tk,
                                    const CUtensorMap& tv, const DecodeArgs& a, int grid,
                                    cudaStream_t stream) {
+  static std::atomic<unsigned long long> ready{0};
   auto kern = fa_decode_kernel<D, REL>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       DecL<D>::kSmemBytes);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), DecL<D>::kSmemBytes, 0, ready);
   if (e != cudaSuccess) return e;
   kern<<<grid, kDecThreads, DecL<D>::kSmemBytes, stream>>>(tq, tk, tv, a);
   return cudaGetLastError();
@@ -659,10 +819,16 @@ cudaError_t launch_decode_combine(const DecodeArgs& a, int d, cudaStream_t strea
   const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
   const long long blocks = (rows + kCombineWarps - 1) / kCombineWarps;
   if (blocks <= 0) return cudaSuccess;
+  const unsigned n = static_cast<unsigned>(blocks);
+  if (a.rel.lines != nullptr)
+    return d == 64 ? launch_merge(fa_decode_combine_kernel<64, true>, dim3(n), kCombineWarps * 32,
+                                  stream, a)
+                   : launch_merge(fa_decode_combine_kernel<128, true>, dim3(n), kCombineWarps * 32,
+                                  stream, a);
   if (d == 64)
-    fa_decode_combine_kernel<64><<<static_cast<unsigned>(blocks), kCombineWarps * 32, 0, stream>>>(a);
+    fa_decode_combine_kernel<64, false><<<n, kCombineWarps * 32, 0, stream>>>(a);
   else
-    fa_decode_combine_kernel<128><<<static_cast<unsigned>(blocks), kCombineWarps * 32, 0, stream>>>(a);
+    fa_decode_combine_kernel<128, false><<<n, kCombineWarps * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -28,7 +28,13 @@ struct DecodeArgs {
   float* lse;                   // [B, H, Nq]
   float* o_part;                // [B*H*Nq, seg_max, d] fp32 (heads cut by CTA boundaries)
   float* lse_part;              // [B*H*Nq, seg_max]
-  RelParams rel;                // bias by relative position; lines null: none
+  // With a bias by relative position (rel.lines set) the work list has the key tiles within the
+  // cache lengths only, at least one per head; n_t, per_cta and seg_max are not used.
+  RelParams rel;
+  int whole;                    // a CTA takes whole heads, every gridDim.x-th
+  int2* pieces;                 // [B * Hkv]: the first CTA of a head and the number of its CTAs; its
+                                // pieces' results are in slots (head, in the list's order) + CTA
+                                // of o_part, lse_part
 };
 
 cudaError_t launch_decode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

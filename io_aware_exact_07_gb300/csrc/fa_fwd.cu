@@ -32,6 +32,7 @@
 
 #include "fa_common.cuh"
 #include "fa_kernels.h"
+#include "fa_launch.cuh"
 
 namespace fa {
 
@@ -806,12 +807,9 @@ static cudaError_t launch_fwd_impl(const CUtensorMap& tq, const CUtensorMap& tk,
   // The in-kernel register reallocation assumes kRegsLaunch registers per thread
   // at launch: with fewer, the softmax warpgroups' increase could never be
   // granted and would wait forever, so such a kernel is refused.
-  cudaFuncAttributes attr;
-  cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-  if (e != cudaSuccess) return e;
-  if (attr.numRegs < kRegsLaunch || attr.maxThreadsPerBlock < kFwdThreads)
-    return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+  static std::atomic<unsigned long long> ready[4];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), L::kSmemBytes, kRegsLaunch,
+                             ready[a.mode]);
   if (e != cudaSuccess) return e;
   kern<<<grid, kFwdThreads, L::kSmemBytes, stream>>>(tq, tk, tv, a);
   return cudaGetLastError();

@@ -34,6 +34,7 @@
 
 #include "fa_common.cuh"
 #include "fa_kernels.h"
+#include "fa_launch.cuh"
 
 namespace fa {
 
@@ -853,12 +854,9 @@ static cudaError_t launch_fwd128_impl(const CUtensorMap& tq, const CUtensorMap& 
   // The in-kernel register reallocation assumes kRegsLaunch registers per thread
   // at launch: with fewer, the softmax warpgroups' increase could never be
   // granted and would wait forever, so such a kernel is refused.
-  cudaFuncAttributes attr;
-  cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-  if (e != cudaSuccess) return e;
-  if (attr.numRegs < kRegsLaunch || attr.maxThreadsPerBlock < kThreads)
-    return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout::kSmemBytes);
+  static std::atomic<unsigned long long> ready[4];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Layout::kSmemBytes, kRegsLaunch,
+                             ready[a.mode]);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, Layout::kSmemBytes, stream>>>(tq, tk, tv, a);
   return cudaGetLastError();

@@ -216,6 +216,11 @@ struct PagedAttnArgs {
   float* o_part;
   float* lse_part;
   SyncParams sync;
+  // Steps over a contiguous cache with a bias by relative position (launch_rel_step): c.k and c.v
+  // are [B, Hkv, Nk, d] bf16 in its strides (a sequence a page), c.kv_lens may be null (Nk each)
+  // and is clamped to [0, Nk]; q, o and lse are [B, H, max_q, ..].
+  RelParams rel;
+  int Nk;
 };
 constexpr int kStepRows = 24;   // most query rows per K/V head of the step kernel
 // Page tables with room for so many keys: heads are not cut, and neither the merge nor its
@@ -226,6 +231,7 @@ constexpr int kWholeKeys = 512;
 cudaError_t launch_paged_write(const PagedWriteArgs& a, bool e4m3, cudaStream_t stream);
 cudaError_t launch_paged_read(const PagedReadArgs& a, bool e4m3, cudaStream_t stream);
 cudaError_t launch_paged_step(const PagedAttnArgs& a, bool e4m3, int ctas, cudaStream_t stream);
+cudaError_t launch_rel_step(const PagedAttnArgs& a, int ctas, cudaStream_t stream);
 // tq: [T, H, d] with boxes of (64 columns, H / Hkv heads, 128 / (H / Hkv) tokens); tk, tv:
 // [num_pages, Hkv, page_size, d] with boxes of 64 bf16 columns or d codes times box_rows rows.
 cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

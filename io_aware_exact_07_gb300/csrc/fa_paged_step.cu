@@ -33,6 +33,9 @@
 //    one cut by a run's end leaves normalised pieces, merged by a second, small kernel with
 //    the two-block rule of the online softmax. Where the page table has room for few keys,
 //    runs are of whole heads and there is nothing to merge.
+//  - The instances for a bias by relative position (REL) read a contiguous bf16 cache. Nearly all
+//    keys lie left of the range of distances, where the bias is one number per head: it goes into
+//    the multiplication that brings the scores to log2 units.
 #include "fa_paged_plan.cuh"
 
 namespace fa {
@@ -189,15 +192,24 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& a, const PagedSeq& 
   return r;
 }
 
-// A place in the list of (sequence, K/V head, key block).
-template <int kBlock>
+// A place in the list of (sequence, K/V head, key block), or for REL of (K/V head, sequence, key
+// block): neighbouring heads then have unlike lengths, and no CTA gets only short ones, each of
+// which costs it a merge of its warps' states.
+template <bool REL>
+__device__ __forceinline__ PagedSeq seq_of(const PagedAttnArgs& a, int b) {
+  if constexpr (!REL) return paged_attn_seq(a.c, b);
+  const int len = a.c.kv_lens == nullptr ? a.Nk : a.c.kv_lens[b];
+  return PagedSeq{b * a.c.max_q, a.c.max_q, min(max(len, 0), a.Nk)};
+}
+
+template <int kBlock, bool REL>
 struct Walk {
   int b, h;          // sequence (B past the end), K/V head
   int blk, end;      // key block, end of the sequence's blocks
   int first;
   PagedSeq s;
   __device__ __forceinline__ void load(const PagedAttnArgs& a) {
-    s = paged_attn_seq(a.c, b);
+    s = seq_of<REL>(a, b);
     const Span sp = span_of<kBlock>(a, s);
     first = sp.first;
     end = first + sp.n;
@@ -205,6 +217,20 @@ struct Walk {
   // Next place; past the last sequence an empty one that is never left.
   __device__ __forceinline__ void next(const PagedAttnArgs& a) {
     if (b >= a.c.B || ++blk < end) return;
+    if constexpr (REL) {  // (every sequence has a block)
+      if (++b == a.c.B && h + 1 < a.c.Hkv) {
+        b = 0;
+        ++h;
+      }
+      if (b < a.c.B) {
+        load(a);
+        blk = first;
+      } else {
+        s.nq = s.len = first = blk = 0;
+        end = 0x7FFFFFFF;
+      }
+      return;
+    }
     if (++h == a.c.Hkv) {
       h = 0;
       do {
@@ -221,12 +247,23 @@ struct Walk {
   }
 };
 
+// Row of o and lse of token t and query head `head`, of the sequence (REL) or of the one whose
+// first token is t0.
+template <bool REL>
+__device__ __forceinline__ long long step_row(const PagedAttnArgs& a, int seq_or_t0, int t, int head) {
+  if constexpr (REL)
+    return (static_cast<long long>(seq_or_t0) * a.H + head) * a.c.max_q + t;
+  else
+    return static_cast<long long>(seq_or_t0 + t) * a.H + head;
+}
+
 }  // namespace
 
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, bool REL>
 __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step_kernel(const PagedAttnArgs a) {
+  static_assert(!REL || !E4M3, "a bias goes with a bf16 cache");
   using L = StepL<D, E4M3, NT>;
-  using Walk = Walk<L::kBlock>;
+  using Walk = Walk<L::kBlock, REL>;
   constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kBlock = L::kBlock;
   constexpr int kU = L::kU, kChunk = L::kChunk;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -247,10 +284,10 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   int most = 0, heads = 0;  // blocks of this thread's longest sequence, its K/V heads
   auto weight = [&](int b) -> long long {
     if (b >= a.c.B) return 0;
-    const int n = span_of<kBlock>(a, paged_attn_seq(a.c, b)).n;
+    const int n = span_of<kBlock>(a, seq_of<REL>(a, b)).n;
     most = max(most, n);
     if (n > 0) heads += a.c.Hkv;
-    return static_cast<long long>(whole ? min(n, 1) : n) * a.c.Hkv;
+    return static_cast<long long>(whole ? min(n, 1) : n) * (REL ? 1 : a.c.Hkv);
   };
   long long total = 0, x0 = 0;
   auto add_up = [&]() {
@@ -262,6 +299,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
       block_scan<kWarps>(x, plan->warp_sums, &sum);
       total += sum;
     }
+    if constexpr (REL) total *= a.c.Hkv;
   };
   add_up();
   long long per = (total + gridDim.x - 1) / gridDim.x;
@@ -290,15 +328,17 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   }
   {
     long long base = 0;
-    for (int b0 = 0; b0 < a.c.B && base <= lo; b0 += kThreads) {
+    const long long per_head = REL ? total / a.c.Hkv : 0;
+    const long long first = REL ? lo % per_head : lo;
+    for (int b0 = 0; b0 < a.c.B && base <= first; b0 += kThreads) {
       const long long x = b0 == 0 ? x0 : weight(b0 + tid);
       long long sum;
       const long long at = base + block_scan<kWarps>(x, plan->warp_sums, &sum);
-      if (at <= lo && lo < at + x) {
-        const long long n = x / a.c.Hkv;  // blocks (1 if whole) of a head
+      if (at <= first && first < at + x) {
+        const long long n = REL ? x : x / a.c.Hkv;  // blocks (1 if whole) of a head
         plan->b = b0 + tid;
-        plan->rem_h = static_cast<int>((lo - at) / n);
-        plan->rem_blk = static_cast<int>((lo - at) % n);
+        plan->rem_h = static_cast<int>(REL ? lo / per_head : (lo - at) / n);
+        plan->rem_blk = static_cast<int>((first - at) % n);
       }
       base += sum;
     }
@@ -330,7 +370,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
 #pragma unroll
     for (int g = 0; g < kU; ++g) {
       const int j = chunk_of(lw) + g * kGroup;
-      lpage[g] = j < lw.s.len ? paged_page(a.c, lw.b, j) : -1;
+      lpage[g] = j >= lw.s.len ? -1 : REL ? lw.b : paged_page(a.c, lw.b, j);
     }
   };
   find_pages();
@@ -339,7 +379,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
     for (int g = 0; g < kU; ++g) {
       const int j = chunk_of(lw) + g * kGroup;
       const int have = lpage[g] >= 0 ? lw.s.len - j : 0;  // rows of the group that the cache holds
-      const int slot = page_row(a.c, j);
+      const int slot = REL ? j : page_row(a.c, j);
       const int page = lpage[g] >= 0 ? lpage[g] : 0;
       const long long at = (page * a.c.stride_page + lw.h * a.c.stride_head +
                             (slot + lrow) * a.c.stride_row) * kEs + lunit * 16;
@@ -372,7 +412,10 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
   };
   auto q_load = [&](const Walk& w, int r, int col) {
     const int t = r / G;
-    const __nv_bfloat16* p = a.q + (w.s.t0 + t) * a.q_stride + (w.h * G + (r - t * G)) * D;
+    const int head = w.h * G + (r - t * G);
+    const __nv_bfloat16* p =
+        REL ? a.q + (static_cast<long long>(w.b * a.H + head) * a.c.max_q + t) * D
+            : a.q + (w.s.t0 + t) * a.q_stride + head * D;
     return r < w.s.nq * G ? *reinterpret_cast<const uint4*>(p + col) : make_uint4(0u, 0u, 0u, 0u);
   };
   // e4m3: Q's rows as f16, each times 2^k that puts its largest magnitude (bf16 bits `top`)
@@ -392,6 +435,22 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
     };
     return make_uint4(one(x.x), one(x.y), one(x.z), one(x.w));
   };
+  // REL: a row's line of biases, and its bias left of the range of distances (0 for rows beyond
+  // the last)
+  auto line_of = [&](int h, int r) { return rel_line(a.rel, h * G + r % G); };
+  float far[NT][2] = {};
+  auto load_far = [&](const Walk& w) {
+    if constexpr (REL) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = n * 8 + 2 * c4 + e;
+          far[n][e] = r < w.s.nq * G ? __ldg(line_of(w.h, r) - a.rel.left) : 0.f;
+        }
+    }
+  };
+  load_far(cw);
   float c_row[NT][2];  // what a row's scores are multiplied with, rows 2 c4, 2 c4 + 1 of each eight
   // Q in registers ...
   constexpr int kQRegs = L::kQShared ? 1 : D / 32;
@@ -597,11 +656,24 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
             v_inv[g][e] = pow2i(127 - kUp - kDown - vb);
           }
         }
+        // REL: keys within the range of distances of some row, or right of it, have their own
+        // biases
+        const bool own_bias = REL && j0 + g * kGroup + kGroup - 1 - pos0 > -a.rel.left;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[g][n][e] = (s[g][n][e] + s2[g][n][e]) * (c_row[n][e & 1] * k_scale[e >> 1]) + v_exp[e >> 1];
+          for (int e = 0; e < 4; ++e) {
+            if (own_bias) {
+              const int r = n * 8 + 2 * c4 + (e & 1);
+              const int dist = j0 + g * kGroup + g8 + (e >> 1) * 8 - (pos0 + r / G);
+              const float b = __ldg(line_of(cw.h, r < cw.s.nq * G ? r : 0) +
+                                    max(-a.rel.left, min(dist, a.rel.right)));
+              s[g][n][e] = (s[g][n][e] + s2[g][n][e]) * c_row[n][e & 1] + b;
+              continue;
+            }
+            s[g][n][e] = (s[g][n][e] + s2[g][n][e]) * (c_row[n][e & 1] * k_scale[e >> 1]) +
+                         (REL ? far[n][e & 1] : v_exp[e >> 1]);
+          }
       }
       constexpr float kLift = E4M3 ? kF16Lift : 0.f;
       const int last_lo = a.wl >= 0 ? cw.s.len - 1 - a.wl : 0;  // first key of the last token
@@ -827,7 +899,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
         const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l) + (E4M3 ? kDown : 0);  // log2
         if (direct) {
           const int t = r / G;
-          const long long row = static_cast<long long>(cw.s.t0 + t) * a.H + cw.h * G + (r - t * G);
+          const long long row = step_row<REL>(a, REL ? cw.b : cw.s.t0, t, cw.h * G + (r - t * G));
           *reinterpret_cast<uint2*>(a.o + row * D + d0) = make_uint2(
               pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
           if (d0 == 0) a.lse[row] = lse2 * kLn2;
@@ -840,7 +912,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
       }
       if (first_piece && starts_mid) ended0 = ends;
       if (!ends && from_start) {
-        slot1_row = cw.s.t0;
+        slot1_row = REL ? cw.b : cw.s.t0;
         slot1_h = cw.h;
         slot1_rows = M;
       }
@@ -848,6 +920,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
       clear();
       piece_blk = nw.blk;
       if (more) {
+        load_far(nw);
         if constexpr (L::kQShared) {
           ready_q_shared();
         } else {
@@ -871,7 +944,7 @@ __global__ void __launch_bounds__(StepL<D, E4M3, NT>::kThreads, 1) fa_paged_step
 // takes query row r of the head that CTA c's run began and did not end; the next CTAs'
 // pieces follow until one ends it. In the order of the pieces, so always the same result. A
 // piece whose lse is a NaN takes no part in the maximum, and makes the sums NaN.
-template <int D>
+template <int D, bool REL>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_step_merge_kernel(const PagedAttnArgs a, int ctas,
                                                                        int rows) {
   constexpr int kPer = D / 32;
@@ -927,7 +1000,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_step_merge_kernel(c
       l += dens[w];
     }
     const int t = r / G;
-    const long long row = static_cast<long long>(hd.row0 + t) * a.H + hd.h * G + (r - t * G);
+    const long long row = step_row<REL>(a, hd.row0, t, hd.h * G + (r - t * G));
     a.o[row * D + tid] = __float2bfloat16(l == 0.f ? 0.f : y / l);
     if (tid == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
   }
@@ -935,25 +1008,25 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_step_merge_kernel(c
 
 namespace {
 
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, bool REL>
 cudaError_t launch_impl(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   using L = StepL<D, E4M3, NT>;
-  auto kern = fa_paged_step_kernel<D, E4M3, NT>;
+  auto kern = fa_paged_step_kernel<D, E4M3, NT, REL>;
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), L::kSmemBytes, 0, ready);
   if (e != cudaSuccess) return e;
   kern<<<ctas, L::kThreads, L::kSmemBytes, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.whole) return e;
-  return launch_merge(fa_paged_step_merge_kernel<D>, dim3(ctas, a.G * a.c.max_q),
+  return launch_merge(fa_paged_step_merge_kernel<D, REL>, dim3(ctas, a.G * a.c.max_q),
                       kMergeWarps * 32, stream, a, ctas, int(L::kRows));
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool REL = false>
 cudaError_t launch_rows(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   const int rows = a.G * a.c.max_q;
-  return rows <= 8    ? launch_impl<D, E4M3, 1>(a, ctas, stream)
-         : rows <= 16 ? launch_impl<D, E4M3, 2>(a, ctas, stream)
-                      : launch_impl<D, E4M3, 3>(a, ctas, stream);
+  return rows <= 8    ? launch_impl<D, E4M3, 1, REL>(a, ctas, stream)
+         : rows <= 16 ? launch_impl<D, E4M3, 2, REL>(a, ctas, stream)
+                      : launch_impl<D, E4M3, 3, REL>(a, ctas, stream);
 }
 
 }  // namespace
@@ -962,6 +1035,11 @@ cudaError_t launch_paged_step(const PagedAttnArgs& a, bool e4m3, int ctas, cudaS
   if (a.c.d == 64)
     return e4m3 ? launch_rows<64, true>(a, ctas, stream) : launch_rows<64, false>(a, ctas, stream);
   return e4m3 ? launch_rows<128, true>(a, ctas, stream) : launch_rows<128, false>(a, ctas, stream);
+}
+
+cudaError_t launch_rel_step(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
+  return a.c.d == 64 ? launch_rows<64, false, true>(a, ctas, stream)
+                     : launch_rows<128, false, true>(a, ctas, stream);
 }
 
 }  // namespace fa

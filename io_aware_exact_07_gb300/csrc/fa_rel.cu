@@ -27,6 +27,7 @@
 
 #include "fa_common.cuh"
 #include "fa_kernels.h"
+#include "fa_launch.cuh"
 
 namespace fa {
 
@@ -605,8 +606,8 @@ cudaError_t launch_near(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
                         const CUtensorMap& tdo, const RelGradArgs& a, int ctas,
                         cudaStream_t stream) {
   auto kern = rel_near_kernel<D, DROPOUT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       NearL<D>::kSmemBytes);
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), NearL<D>::kSmemBytes, 0, ready);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kNearThreads, NearL<D>::kSmemBytes, stream>>>(tq, tk, tv, tdo, a);
   return cudaGetLastError();

@@ -278,23 +278,35 @@ def check_step(B, H, Hkv, Nq, Nk, d, lens=None, rule=(32, 128, False), causal=Tr
 
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("Nq,G", [(1, 1), (1, 4), (5, 4), (33, 3)])
+@pytest.mark.parametrize("Nq,G", [(1, 1), (1, 4), (3, 4), (5, 4), (24, 1), (5, 5), (33, 3), (128, 1)])
 def test_step(Nq, G, d):
     check_step(3, 2 * G, 2, Nq, 700, d, lens=[700, 300, 129], junk=math.nan, seed=21)
 
 
 @gpu
-@pytest.mark.parametrize("num_ctas", [1, 7, 50])
+@pytest.mark.parametrize("Nq", [3, 20])
+@pytest.mark.parametrize("num_ctas", [1, 7, 50, 1000])
 @pytest.mark.parametrize("rule", [(32, 128, True), (8, 20, False), (64, 1000, True)])
-def test_step_however_it_is_split(rule, num_ctas):
-    check_step(2, 4, 2, 3, 1000, 64, lens=[1000, 555], rule=rule, num_ctas=num_ctas,
+def test_step_however_it_is_split(rule, num_ctas, Nq):
+    check_step(2, 4, 2, Nq, 1000, 64, lens=[1000, 555], rule=rule, num_ctas=num_ctas,
                causal=num_ctas != 7, seed=22, table_type=torch.bfloat16)
 
 
 @gpu
+@pytest.mark.parametrize("Nq", [1, 30])
+def test_step_of_many_ragged_sequences(Nq):
+    # more batch rows than threads plan with at once, none without a length among them
+    lens = [(37 * i) % 301 for i in range(600)]
+    check_step(600, 1, 1, Nq, 300, 64, lens=lens, seed=24)
+    check_step(70, 2, 2, Nq, 900, 128, lens=[(113 * i) % 901 for i in range(70)], seed=25)
+
+
+@gpu
+@pytest.mark.parametrize("Nq", [2, 40])
 @pytest.mark.parametrize("d", [64, 128])
-def test_step_with_a_window_and_the_shortest_caches(d):
-    check_step(5, 2, 2, 2, 300, d, lens=[0, 1, 2, 128, 300], junk=math.inf, window=100, seed=23)
+def test_step_with_a_window_and_the_shortest_caches(d, Nq):
+    check_step(5, 2, 2, Nq, 300, d, lens=[0, 1, 2, 128, 300], junk=math.inf, window=100, seed=23)
+    check_step(5, 2, 2, Nq, 700, d, lens=[0, 1, 2, 640, 700], junk=math.nan, window=100, seed=26)
 
 
 # ---------------------------------------------------------------- the map of distances
@@ -377,6 +389,14 @@ def test_c_entry_points_refuse_on_the_host():
                                  3, 4, None, 0, None)
     assert step(lines=none) == step(left=-2) == step(Nk=(1 << 28) + 1) == bad
     assert step(Nq=65) == step(d=32) == fa.FA_ERR_UNSUPPORTED
+    assert step() == fa.FA_ERR_WORKSPACE  # a number of CTAs: heads may be cut
+    # 4 CTAs, a header and two pieces of 8 rows each: 4 x 16 bytes, 64 floats, 64 x 64 floats
+    assert fa.fa_decode_rel_workspace_size(1, 4, 2, 1, 9, 64, 4) == 256 + 256 + 16384
+    # tiles of 128 rows: 2 heads and 2 CTAs of 26 rows, 104 x 64 and 104 floats, 2 pieces' numbers
+    assert fa.fa_decode_rel_workspace_size(1, 4, 2, 13, 9, 64, 4) == 104 * 256 + 512 + 256
+    assert fa.fa_decode_rel_workspace_size(1, 4, 2, 5, 9, 128, 4) == 40 * 512 + 256 + 256
+    assert fa.fa_decode_rel_workspace_size(1, 4, 2, 65, 9, 64, 4) == 0
+    assert fa._REL_PAD == fa.fa_rel_line_length(0, 0) - 1
     # the block forms refuse integers beyond their parameters' range
     assert lib.fa_fwd_cross_block(None, None) == bad
     block = fa._FWD_CROSS_BLOCK(*[1 << 20] * 5, 1, 4, 2, 5, 1 << 33, 64, 0.125, 0, 0, -1, -1, 0.0, 0, 0,
