@@ -736,6 +736,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           break;
         }
         ++pv_cnt;
+      } else if (unit_count > 0 &&
+                 !mbar_wait_warp(bars.o_free[x], (unit_count - 1) & 1, tmo, abort_flag)) {
+        // Without key tiles nothing else holds these warps back: their arrivals for later units
+        // would stand in for the PV issuer's, and it would wait for phases that have passed.
+        fail();
+        ok = false;
+        break;
       }
       tc_fence_after();
       const bool row_ok = row < N;
