@@ -1026,6 +1026,7 @@ fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool drop = a.drop.p8 > 0;
   cudaError_t e = fa::launch_bwd_preprocess(a, d, di->num_sms, s);
+  if (e == cudaSuccess) e = fa::launch_row_d(m[0], m[1], m[2], m[3], a, d, drop, di->num_sms, s);
   if (e == cudaSuccess) {
     a.sync.inject_stall = take_stall(kStallDkdv);
     e = fa::launch_bwd_dkdv(m[0], m[1], m[2], m[3], a, d, drop, di->num_sms, s);

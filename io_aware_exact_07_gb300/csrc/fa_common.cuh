@@ -291,6 +291,15 @@ __device__ __forceinline__ TileRun free_query_tiles(const MaskParams& m, int kt,
   return r;
 }
 
+// kCross, kRel: the key tiles that a query tile at position p0 sees some key of (tile_valid).
+__device__ __forceinline__ TileRun seen_key_tiles(const MaskParams& m, int p0, int n_kv) {
+  TileRun r{0, n_kv};
+  if (m.causal) r.hi = min(r.hi, floor_tiles(p0 + kTile - 1) + 1);
+  if (m.wr >= 0) r.hi = min(r.hi, floor_tiles(p0 + kTile - 1 + m.wr) + 1);
+  if (m.wl >= 0) r.lo = max(0, ceil_tiles(p0 - m.wl - (kTile - 1)));
+  return r;
+}
+
 // kRel: the tiles along one axis whose block of n queries x n keys lies within reach of the
 // diagonal, at distance d0 + 128 i for key tile i: before them it is far to the left, behind them
 // far to the right.

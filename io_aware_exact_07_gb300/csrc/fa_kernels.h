@@ -110,6 +110,12 @@ cudaError_t launch_rel_grad(const CUtensorMap& tq, const CUtensorMap& tk, const 
                             const CUtensorMap& tdo, const RelGradArgs& a, int d, bool dropout,
                             int num_sms, cudaStream_t stream);
 
+// kCross, kRel: D of the query tiles whose rows see one key tile, from their scores (nothing is
+// launched where there can be none). After launch_bwd_preprocess, whose D it replaces.
+cudaError_t launch_row_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                         const CUtensorMap& tdo, const BwdArgs& a, int d, bool dropout,
+                         int num_sms, cudaStream_t stream);
+
 cudaError_t launch_debug_dropout(uint8_t* keep, int B, int H, int N, const DropParams& d,
                                  cudaStream_t stream);
 

@@ -22,6 +22,11 @@
 // Sums are fp32, over few values each; the long ones at the end keep what each addition rounds off
 // (Knuth's two-sum): this GPU adds fp64 at a 64th of the rate.
 // No atomics: the order of every sum is fixed.
+//
+// The kernel of the near tiles also serves the backward pass of all calls with positions: for query
+// tiles whose rows see one key tile it forms D_i itself, before the other kernels use it. There the
+// rounding of O is most of what dQ and dK are off (5 keys: 0.37 % of dQ; with the D of the scores
+// 0.24 % are left, as with many keys).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -155,10 +160,11 @@ struct NearWalk {
   int n;           // query tiles of the group
 
   __device__ NearWalk(const NearList& list, int H, int ctas, int cta) : l(list) {
+    left = h = g = b = i = n = 0;
+    if (ctas == 0) return;
     const long long per_head = l.head_total(), total = per_head * H;
     const long long per = near_per_cta(total, ctas), at = per * cta;
     left = max(0ll, min(per, total - at));
-    h = g = b = i = n = 0;
     if (left == 0) return;
     h = static_cast<int>(at / per_head);
     long long rest = at % per_head;
@@ -210,7 +216,7 @@ struct NearL {
   static constexpr int kDiagOff = kStages * 2 * T;
   static constexpr int kLineOff = kDiagOff + 2 * kTile * kDiagPitch * 4;
   static constexpr int kBarOff = kLineOff + 256 * 4;
-  static constexpr int kNumBars = 2 * kStages + 4 + kPairSlots + 1;
+  static constexpr int kNumBars = 2 * kStages + 4 + kPairSlots + 1 + 5;
   static constexpr int kPairOff = kBarOff + (kNumBars + 1) / 2 * 16;
   static constexpr int kMiscOff = kPairOff + kPairSlots * 32;
   // no slack for rounding the base up: the kernel checks its alignment
@@ -218,7 +224,8 @@ struct NearL {
   static_assert(kSmemBytes <= 232448, "shared memory exceeds the per-block limit");
 };
 
-template <int D, bool DROPOUT>
+// ROWS: instead of the near pairs' sums, D of the rows that see one key tile (launch_row_d).
+template <int D, bool DROPOUT, bool ROWS>
 __global__ void __launch_bounds__(kNearThreads, 1)
     rel_near_kernel(const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k,
@@ -246,6 +253,7 @@ __global__ void __launch_bounds__(kNearThreads, 1)
   const BarRun s_free{s_full.base + 16u};
   const BarRun pair_full{s_free.base + 16u};
   const uint32_t drain = pair_full.base + 8u * kPairSlots;
+  const BarRun meet{drain + 8u};  // the compute warps; then each warpgroup
   int4* pairs = reinterpret_cast<int4*>(smem + L::kPairOff);
   if (tid == 0) {
     *abort_flag = 0;
@@ -259,6 +267,7 @@ __global__ void __launch_bounds__(kNearThreads, 1)
     }
     for (int s = 0; s < kPairSlots; ++s) mbar_init(pair_full[s], 1);
     mbar_init(drain, 1);
+    for (int i = 0; i < 5; ++i) mbar_init(meet[i], i == 0 ? kNearCompute : 128);
     fence_mbar_init();
   }
   if (warp == kNearMmaWarp) {
@@ -279,7 +288,7 @@ __global__ void __launch_bounds__(kNearThreads, 1)
   if (warp == kNearProducerWarp) {
     if (lane == 0) {
       const NearList list = near_list(args);
-      NearWalk w(list, mk.H, gridDim.x, blockIdx.x);
+      NearWalk w(list, mk.H, ROWS ? 0 : gridDim.x, blockIdx.x);
       const int first_group = w.left > 0 ? w.group() : -1;
       uint32_t it = 0;
       bool ok = true;
@@ -294,11 +303,8 @@ __global__ void __launch_bounds__(kNearThreads, 1)
         mbar_arrive(pair_full[slot]);
         return true;
       };
-      for (; w.left > 0 && ok; w.next()) {
-        group = w.group();
-        const int kv_len = kv_len_of(mk, w.b), qt = w.qt(), kt = w.kt();
-        if (!tile_valid<kRel>(mk, qt, kt, list.n_q, (kv_len + kTile - 1) / kTile)) continue;
-        const int bh = w.b * mk.H + w.h, kvh = kv_head(mk, bh);
+      auto bring = [&](int bh, int qt, int kt, int kv_len) {
+        const int kvh = kv_head(mk, bh);
         for (int half = 0; half < 2; ++half, ++it) {
           const int s = it % L::kStages;
           if (half == 0 ? !hand_on(bh, qt, kt, kv_len)
@@ -313,6 +319,22 @@ __global__ void __launch_bounds__(kNearThreads, 1)
             tma_load_3d(sRing + (2 * s + 1) * T + c * 16384, half ? &tm_v : &tm_k, c * 64,
                         kt * kTile, kvh, full[s]);
           }
+        }
+      };
+      if constexpr (ROWS) {
+        const int units = mk.B * mk.H * list.n_q;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+          const int bh = u / list.n_q, qt = u - bh * list.n_q, kv_len = kv_len_of(mk, bh / mk.H);
+          const TileRun seen =
+              seen_key_tiles(mk, tile_pos(mk, qt), (kv_len + kTile - 1) / kTile);
+          if (seen.hi - seen.lo == 1) bring(bh, qt, seen.lo, kv_len);
+        }
+      } else {
+        for (; w.left > 0 && ok; w.next()) {
+          group = w.group();
+          const int kv_len = kv_len_of(mk, w.b), qt = w.qt(), kt = w.kt();
+          if (tile_valid<kRel>(mk, qt, kt, list.n_q, (kv_len + kTile - 1) / kTile))
+            bring(w.b * mk.H + w.h, qt, kt, kv_len);
         }
       }
       if (!ok || !hand_on(-1, 0, 0, 0)) fail();
@@ -371,8 +393,18 @@ __global__ void __launch_bounds__(kNearThreads, 1)
     const float c_log2 = args.b.scale_log2;
     const uint64_t c2 = f2_pack(c_log2, c_log2);
     const uint64_t ks2 = f2_pack(args.b.drop.keep_scale, args.b.drop.keep_scale);
-    auto sync_wg = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory"); };
-    auto sync_all = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kNearCompute) : "memory"); };
+    // Barriers with a limit, as every wait here (a warp that gave up does not come to them).
+    bool ok = true;
+    uint32_t n_all = 0, n_wg = 0;
+    auto meet_at = [&](uint32_t bar, uint32_t n) {
+      mbar_arrive(bar);
+      if (!mbar_wait_warp(bar, n & 1u, tmo, abort_flag)) {
+        fail();
+        ok = false;
+      }
+    };
+    auto sync_wg = [&]() { meet_at(meet[1 + wg], n_wg++); };
+    auto sync_all = [&]() { meet_at(meet[0], n_all++); };
     float acc[32];
 #pragma unroll
     for (int c = 0; c < 32; ++c) acc[c] = 0.f;
@@ -402,7 +434,6 @@ __global__ void __launch_bounds__(kNearThreads, 1)
     int4 p = make_int4(-1, 0, 0, -1), p_next;  // the pair, and the one after it
     int kv_len = 0, kv_next = 0;
     float lse_next = 0.f, d_next = 0.f;        // lse and D of the next pair's row
-    bool ok = true;
     auto look_ahead = [&](uint32_t n) {
       const uint32_t slot = n % kPairSlots;
       if (!mbar_wait_warp(pair_full[slot], (n / kPairSlots) & 1u, tmo, abort_flag)) {
@@ -418,9 +449,13 @@ __global__ void __launch_bounds__(kNearThreads, 1)
       if (p_next.x >= 0 && row < N) {
         const size_t i = static_cast<size_t>(p_next.x) * N + row;
         lse_next = args.b.lse[i];
-        d_next = args.b.dsum[i];
+        if constexpr (!ROWS) d_next = args.b.dsum[i];
       }
     };
+    if (ROWS && args.b.mode != kRel) {  // no bias
+      if (tid < 2 * kTile - 1) line_s[tid] = 0.f;
+      sync_all();
+    }
     look_ahead(0);
     const int first_group = ok ? pairs[1].y : -1;
     // the sums of the groups that this CTA's pairs begin and end with, and of those between, are
@@ -438,15 +473,19 @@ __global__ void __launch_bounds__(kNearThreads, 1)
       }
       if (p.x < 0) break;
       const int kt = p.z, row = p.y * kTile + t;
-      if (line_group != group) {
-        sync_all();  // the previous group's line is no longer read
+      if (ROWS ? args.b.mode == kRel : line_group != group) {
+        sync_all();  // the line before it is no longer read
         const int d0 = kt * kTile - tile_pos(mk, p.y);
-        if (tid < 2 * kTile - 1)
-          line_s[tid] = __ldg(rel_line(args.b.rel, p.x % mk.H) + (d0 - (kTile - 1) + tid));
+        if (tid < 2 * kTile - 1) {
+          int dist = d0 - (kTile - 1) + tid;  // (ROWS: of any tile)
+          if constexpr (ROWS) dist = clamp_distance(dist, args.b.rel.left, args.b.rel.right);
+          line_s[tid] = __ldg(rel_line(args.b.rel, p.x % mk.H) + dist);
+        }
         sync_all();
         line_group = group;
       }
-      const float nl = lse_next == -INFINITY ? -INFINITY : -lse_next * kLog2e, nd = -d_next;
+      const float nl = lse_next == -INFINITY ? -INFINITY : -lse_next * kLog2e;
+      const float nd = ROWS ? 0.f : -d_next;  // (the sum of P Z dP / (1-p) is D)
       const int bh = p.x;
       look_ahead(n + 1);
       if (!ok) break;
@@ -509,8 +548,22 @@ __global__ void __launch_bounds__(kNearThreads, 1)
           acc[16 * half + c + 1] = a1;
         }
       }
+      if constexpr (ROWS) {  // the row's sum over its four warpgroups
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          sum[c & 3] += acc[c];
+          acc[c] = 0.f;
+        }
+        float* part = reinterpret_cast<float*>(smem + L::kDiagOff) + (n & 1u) * 4 * kTile;
+        part[wg * kTile + t] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        sync_all();
+        if (wg == 0 && row < N)
+          args.b.dsum[static_cast<size_t>(bh) * N + row] =
+              (part[t] + part[kTile + t]) + (part[2 * kTile + t] + part[3 * kTile + t]);
+      }
     }
-    if (group >= 0 && ok) flush(group);
+    if (!ROWS && group >= 0 && ok) flush(group);
   }
   tc_fence_before();
   __syncthreads();
@@ -601,11 +654,11 @@ __global__ void __launch_bounds__(256) rel_table_kernel(const RelGradArgs a, int
   }
 }
 
-template <int D, bool DROPOUT>
+template <int D, bool DROPOUT, bool ROWS>
 cudaError_t launch_near(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         const CUtensorMap& tdo, const RelGradArgs& a, int ctas,
                         cudaStream_t stream) {
-  auto kern = rel_near_kernel<D, DROPOUT>;
+  auto kern = rel_near_kernel<D, DROPOUT, ROWS>;
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), NearL<D>::kSmemBytes, 0, ready);
   if (e != cudaSuccess) return e;
@@ -613,7 +666,32 @@ cudaError_t launch_near(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   return cudaGetLastError();
 }
 
+template <bool ROWS>
+cudaError_t launch_near_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const CUtensorMap& tdo, const RelGradArgs& a, int d, bool dropout,
+                          int ctas, cudaStream_t stream) {
+  if (d == 64)
+    return dropout ? launch_near<64, true, ROWS>(tq, tk, tv, tdo, a, ctas, stream)
+                   : launch_near<64, false, ROWS>(tq, tk, tv, tdo, a, ctas, stream);
+  return dropout ? launch_near<128, true, ROWS>(tq, tk, tv, tdo, a, ctas, stream)
+                 : launch_near<128, false, ROWS>(tq, tk, tv, tdo, a, ctas, stream);
+}
+
 }  // namespace
+
+cudaError_t launch_row_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                         const CUtensorMap& tdo, const BwdArgs& b, int d, bool dropout,
+                         int num_sms, cudaStream_t stream) {
+  const MaskParams& m = b.mask;
+  // causal: rows of a tile from position -127 to 0 on see the first key tile alone
+  if (m.seqlens_k == nullptr && m.Nk > kTile && m.wl < 0 && m.wr < 0 && !(m.causal && m.q_off <= 0))
+    return cudaSuccess;
+  RelGradArgs a = {};
+  a.b = b;
+  const long long units = static_cast<long long>(m.B) * m.H * ((m.N + kTile - 1) / kTile);
+  const int ctas = static_cast<int>(units < num_sms ? units : num_sms);
+  return launch_near_d<true>(tq, tk, tv, tdo, a, d, dropout, ctas, stream);
+}
 
 cudaError_t launch_rel_lines(const RelLinesArgs& a, cudaStream_t stream) {
   const int stride = a.left + a.right + 1 + 2 * kRelPad;
@@ -630,14 +708,8 @@ cudaError_t launch_rel_grad(const CUtensorMap& tq, const CUtensorMap& tk, const 
   rel_rows_kernel<<<chunks * m.B * m.H, 256, 0, stream>>>(a, chunks);
   cudaError_t e = cudaGetLastError();
   const int ctas = num_sms < kRelMaxCtas ? num_sms : kRelMaxCtas;
-  if (e == cudaSuccess && a.n_diag > 0) {
-    if (d == 64)
-      e = dropout ? launch_near<64, true>(tq, tk, tv, tdo, a, ctas, stream)
-                  : launch_near<64, false>(tq, tk, tv, tdo, a, ctas, stream);
-    else
-      e = dropout ? launch_near<128, true>(tq, tk, tv, tdo, a, ctas, stream)
-                  : launch_near<128, false>(tq, tk, tv, tdo, a, ctas, stream);
-  }
+  if (e == cudaSuccess && a.n_diag > 0)
+    e = launch_near_d<false>(tq, tk, tv, tdo, a, d, dropout, ctas, stream);
   if (e != cudaSuccess) return e;
   const int length = a.b.rel.left + a.b.rel.right + 1 + 2 * kOver;
   rel_line_kernel<<<dim3((length + 63) / 64, m.H), 256, 0, stream>>>(a, ctas);

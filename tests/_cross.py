@@ -40,9 +40,10 @@ def keep_bits(B, H, Nq, Nk, p, seed, offset):
 
 
 def plain(q, k, v, do=None, scale=None, causal=False, q_offset=0, window=(-1, -1), lens=None,
-          bias=None, keep=None, p8=0, starts=None):
+          bias=None, keep=None, p8=0, starts=None, exact_d=False):
     """q, do [B, H, Nq, d], k, v [B, H_kv, Nk, d] (any type), lens: list of key lengths or None,
-    bias(h, distances) -> biases, starts: positions of the first queries instead of q_offset.
+    bias(h, distances) -> biases, starts: positions of the first queries instead of q_offset,
+    exact_d: the bounds leave out what a D from the rounded O costs.
     Returns o, lse, (dq, dk, dv, S's gradient), and the bounds of the kernels' errors by name."""
     B, H, Nq, d = q.shape
     Hkv, Nk = k.shape[1], k.shape[2]
@@ -90,7 +91,11 @@ def plain(q, k, v, do=None, scale=None, causal=False, q_offset=0, window=(-1, -1
             dP = Z * (g @ vh.T)
             dS = P * (dP - D)
             # D comes from the rounded O; what it costs dS, and dS's own rounding
-            e = HALF * ((g * o).abs().sum(1, keepdim=True) * P + dS.abs())
+            e = HALF * dS.abs()
+            if exact_d:  # fp32: the scores' error (see table_grad), and D's sum
+                e = e + 2.0 ** -17 * P * (dP.abs() + (P * dP.abs()).sum(1, keepdim=True))
+            else:
+                e = e + HALF * (g * o).abs().sum(1, keepdim=True) * P
             out["ds"][b, h], tol["ds"][b, h] = dS, P * (dP.abs() + D.abs())
             out["dv"][b, h // G] += (P * Z).T @ g
             tol["dv"][b, h // G] += HALF * ((P * Z).T @ g.abs())

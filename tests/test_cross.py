@@ -120,6 +120,57 @@ def test_grouped_heads_and_dropout(d):
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", [dict(Nk=5), dict(Nk=128, rule=(8, 16, True)), dict(Nk=2, p=0.3),
+                                  dict(Nk=300, lens=[3, 300, 0], rule=(8, 16, True)),
+                                  dict(Nk=300, causal=True, q_offset=-40),
+                                  dict(Nk=900, window=(20, 10), q_offset=300)])
+def test_few_keys_lose_nothing_to_the_rounding_of_o(case, d):
+    """Rows that see one key tile: dQ and dK are off by what dS and they themselves are rounded,
+    2^-8 of each at most, not by what the rounded O would cost D."""
+    case = dict(case)
+    Nk, p, lens = case.pop("Nk"), case.pop("p", 0.0), case.pop("lens", [300] * 3)
+    rule, window = case.pop("rule", None), case.get("window", (-1, -1))
+    q, k, v, do = draw(3, 2, 2, 150, Nk, d, seed=50)
+    lens = [min(n, Nk) for n in lens]
+    kw = dict(case, seqlens_k=torch.tensor(lens, dtype=torch.int32, device="cuda"), dropout_p=p,
+              seed=3)
+    bias = None
+    if rule is not None:
+        table = torch.randn((rule[0], 2), generator=torch.Generator().manual_seed(1))
+        kw["rel_bias"] = fa.rel_bias(table.cuda(), fa.rel_buckets(*rule))
+        of = torch.tensor([bucket(rule, x) for x in range(-600, 601)])
+        bias = lambda h, x: table[:, h].double()[of[x + 600]]
+    dev = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.fwd(*dev[:3], **kw)
+    grads = fa.bwd(*dev[:3], o, dev[3], lse, **kw)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == fa.FA_OK
+    keep = keep_bits(3, 2, 150, Nk, p, 3, 0) if p > 0 else None
+    want, tol = plain(q, k, v, do, lens=lens, bias=bias, keep=keep, p8=oracle.p8(p),
+                      exact_d=True, window=window, causal=case.get("causal", False),
+                      q_offset=case.get("q_offset", 0))
+    one = torch.zeros(3, 150, dtype=torch.bool)  # rows whose tile of queries sees one key tile
+    for b in range(3):
+        for t0 in range(0, 150, 128):
+            pos = t0 + case.get("q_offset", 0)
+            see = range(-(-lens[b] // 128))
+            if case.get("causal"):
+                see = [j for j in see if 128 * j <= pos + 127]
+            if window[0] >= 0:
+                see = [j for j in see if 128 * j + 127 >= pos - window[0] and
+                       128 * j <= pos + 127 + window[1]]
+            one[b, t0:t0 + 128] = len(see) == 1
+    for b in range(3):
+        if one[b].any():
+            within("dq", grads[0][b][:, one[b].cuda()], want["dq"][b][:, one[b]],
+                   tol["dq"][b][:, one[b]])
+        if one[b].all():
+            within("dk", grads[1][b], want["dk"][b], tol["dk"][b])
+    assert one.any()
+
+
+@gpu
 def test_more_units_than_multiprocessors():
     check(40, 4, 4, 140, 260, 64, lens=[7 * i % 261 for i in range(40)], seed=7)
 
@@ -127,8 +178,8 @@ def test_more_units_than_multiprocessors():
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
 def test_equal_lengths_are_the_usual_calls(d):
-    # an offset of the keys' own positions, and a window that hides nothing: the plain kernels'
-    # results, bit by bit
+    # keys that the causal mask hides: the plain kernels' results, bit by bit, but for what comes
+    # from a D of the scores instead of the rounded O (rows that see one key tile)
     q, k, v, do = (x.cuda() for x in draw(2, 2, 2, 300, 300, d, 8))
     o, lse = fa.fwd(q, k, v, causal=True)
     out = (o, lse) + fa.bwd(q, k, v, o, do, lse, causal=True)
@@ -137,8 +188,11 @@ def test_equal_lengths_are_the_usual_calls(d):
     o2, lse2 = fa.fwd(q, kk, vv, causal=True)
     dq, dk, dv = fa.bwd(q, kk, vv, o2, do, lse2, causal=True)
     assert dk[:, :, 300:].eq(0).all() and dv[:, :, 300:].eq(0).all()
-    for a, b in zip(out, (o2, lse2, dq, dk[:, :, :300], dv[:, :, :300])):
-        assert torch.equal(a, b)
+    assert torch.equal(out[0], o2) and torch.equal(out[1], lse2)
+    assert torch.equal(out[2][:, :, 128:], dq[:, :, 128:])
+    assert torch.equal(out[4], dv[:, :, :300])
+    # the first row's weight is 1 whatever its score: no gradient, where the rounded O leaves some
+    assert dq[:, :, 0].abs().max() < 1e-6 < out[2][:, :, 0].abs().max() + 1e-6
 
 
 # ---------------------------------------------------------------- bias by relative position
