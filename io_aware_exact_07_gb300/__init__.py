@@ -763,7 +763,7 @@ def rel_bias(table, buckets, stream=None):
                          "distance 0")
     H, right = shape[1], m.numel() - 1 - left
     with _memory_on(stream, dev):
-        lines = table.new_empty((H, left + right + 1 + _REL_PAD), dtype=torch.float32)
+        lines = table.new_empty((H, _line_length(left, right)), dtype=torch.float32)
     _call("fa_rel_bias_block", dev, stream,
           _REL_BIAS_BLOCK(table.data_ptr(),
                           FA_TABLE_F32 if dtype == torch.float32 else FA_TABLE_BF16, m.data_ptr(),
@@ -773,11 +773,14 @@ def rel_bias(table, buckets, stream=None):
     return RelBias(lines, buckets)
 
 
-_REL_PAD = 512  # a line's floats beyond its distances (fa_rel_line_length)
 _REL_BIAS_BLOCK = struct.Struct("=8q").pack
 _FWD_CROSS_BLOCK = struct.Struct("=11qd4qdQQ4q").pack
 _BWD_CROSS_BLOCK = struct.Struct("=15qd4qdQQ9q").pack
 _DECODE_REL_BLOCK = struct.Struct("=11qd9q").pack
+
+
+def _line_length(left, right):  # fa_rel_line_length, without the call
+    return 5 * ((left + right + 516) & ~3)
 
 
 def _cross_args(q, k, v, scale, seqlens_k, rel):
@@ -797,7 +800,7 @@ def _cross_args(q, k, v, scale, seqlens_k, rel):
     bias = (0, 0, 0)
     if rel is not None:
         left, right = rel.buckets.left, rel.buckets.right
-        if (rel.lines.shape != (H, left + right + 1 + _REL_PAD) or rel.lines.dtype != torch.float32
+        if (rel.lines.shape != (H, _line_length(left, right)) or rel.lines.dtype != torch.float32
                 or rel.lines.get_device() != dev or not rel.lines.is_contiguous()):
             raise ValueError(f"rel_bias must come from rel_bias() with a table of {H} heads, on "
                              "q's device")

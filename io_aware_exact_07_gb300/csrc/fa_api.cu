@@ -769,7 +769,7 @@ fa_status fa_decode_rel(const void* q, const void* k_cache, const void* v_cache,
 }
 
 static fa_status check_lines(const float* lines, int left, int right) {
-  if (lines == nullptr || (reinterpret_cast<uintptr_t>(lines) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  if (lines == nullptr || !aligned16(lines)) return FA_ERR_INVALID_ARG;
   if (left < 0 || right < 0 || left >= kMaxDistances || right >= kMaxDistances)
     return FA_ERR_INVALID_ARG;
   return left + right + 1 <= kMaxDistances ? FA_OK : FA_ERR_UNSUPPORTED;

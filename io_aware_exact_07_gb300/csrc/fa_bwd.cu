@@ -550,7 +550,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               if constexpr (REL) {  // each element's own bias
                 if (near.has(qt)) {
                   const int d0 = kt * kTile - tile_pos(mk, qt);
-                  rel_add<64, -1>(rel_line(args.rel, bh % mk.H) + (d0 + r - 64 * wg), c_log2, sr);
+                  rel_add<64, -1, 8>(args.rel, rel_line(args.rel, bh % mk.H), d0 + r - 64 * wg,
+                                     c_log2, reinterpret_cast<float*>(sr));
                   cs = 1.f;
                 }
               }

@@ -535,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if constexpr (REL) {  // each element's own bias
                 const int d0 = kt * kTile - tile_pos(mk, qt);
                 if (!rel_far(args.rel, d0)) {
-                  rel_add<32, -1>(rel_line(args.rel, bh % mk.H) + (d0 + r - 32 * wg), c_log2, sr);
+                  rel_add<32, -1, 8>(args.rel, rel_line(args.rel, bh % mk.H), d0 + r - 32 * wg,
+                                     c_log2, reinterpret_cast<float*>(sr));
                   cs = 1.f;
                 }
               }
@@ -1208,7 +1209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t cs2 = c2;
             if constexpr (REL) {
               if (own_bias) {
-                rel_add<32, 1>(head.line + (j * kTile - tile_pos(mk, qt) + 32 * wg - t), c_log2, sr);
+                rel_add<32, 1, 8>(args.rel, head.line, j * kTile - tile_pos(mk, qt) + 32 * wg - t,
+                               c_log2, reinterpret_cast<float*>(sr));
                 cs2 = f2_pack(1.f, 1.f);
               }
             }

@@ -579,18 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               far = j < near.lo ? head.left : head.right;
             } else {
               const int d0 = j * kTile - tile_pos(mk, uc.qt);
-              const float* lp = head.line + (d0 - t);
-              const uint64_t cl2 = f2_pack(c_log2, c_log2);
-#pragma unroll
-              for (int c = 0; c < 128; c += 32) {
-                float b[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) b[k] = __ldg(lp + c + k);
-#pragma unroll
-                for (int k = 0; k < 32; k += 2)
-                  f2_unpack(f2_fma(f2_pack(s[c + k], s[c + k + 1]), cl2, f2_pack(b[k], b[k + 1])),
-                            s[c + k], s[c + k + 1]);
-              }
+              rel_add<128, 1, 16>(args.rel, head.line, d0 - t, c_log2, s);
               cs = 1.f;
             }
           }

@@ -73,7 +73,9 @@ __global__ void __launch_bounds__(256) rel_lines_kernel(const RelLinesArgs a) {
   const RelParams r{nullptr, a.left, a.right};
   const int e = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y;
   if (e >= r.stride()) return;
-  const int n = __ldg(a.map + clamp_distance(e - a.left - kRelPad, a.left, a.right) + a.left);
+  const int w = e - r.pitch();  // of the windows
+  const int dist = (w < 0 ? e : (w >> 2) + (w & 3)) - a.left - kRelPad;
+  const int n = __ldg(a.map + clamp_distance(dist, a.left, a.right) + a.left);
   float x = 0.f;
   if (n < 0 || n >= a.num_buckets) {
     record_error(a.status, kStatusInvalid);
@@ -420,9 +422,14 @@ __global__ void __launch_bounds__(kNearThreads, 1)
           for (int c = 0; c < 32; ++c) diag[t * kDiagPitch + c] = acc[c];
           sync_wg();
           for (int e = t; e < 159; e += 128) {
-            float x = 0.f;
-            for (int c = max(0, e - 127); c <= min(31, e); ++c)
-              x += diag[(c + 127 - e) * kDiagPitch + c];
+            // elements (c + 127 - e, c); four sums, so that the loads do not wait for one another
+            const int lo = max(0, e - 127), hi = min(31, e);
+            const float* at = diag + (127 - e) * kDiagPitch;
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c >= lo && c <= hi) y[c & 3] += at[c * (kDiagPitch + 1)];
+            const float x = (y[0] + y[1]) + (y[2] + y[3]);
             out[e] = x;
           }
         }
@@ -694,7 +701,7 @@ cudaError_t launch_row_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
 }
 
 cudaError_t launch_rel_lines(const RelLinesArgs& a, cudaStream_t stream) {
-  const int stride = a.left + a.right + 1 + 2 * kRelPad;
+  const int stride = RelParams{nullptr, a.left, a.right}.stride();
   rel_lines_kernel<<<dim3((stride + 255) / 256, a.H), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }

@@ -450,7 +450,8 @@ def test_c_entry_points_refuse_on_the_host():
     assert fa.fa_decode_rel_workspace_size(1, 4, 2, 13, 9, 64, 4) == 104 * 256 + 512 + 256
     assert fa.fa_decode_rel_workspace_size(1, 4, 2, 5, 9, 128, 4) == 40 * 512 + 256 + 256
     assert fa.fa_decode_rel_workspace_size(1, 4, 2, 65, 9, 64, 4) == 0
-    assert fa._REL_PAD == fa.fa_rel_line_length(0, 0) - 1
+    for left, right in ((0, 0), (3, 0), (5, 6), (1000, 1001)):
+        assert fa._line_length(left, right) == fa.fa_rel_line_length(left, right)
     # the block forms refuse integers beyond their parameters' range
     assert lib.fa_fwd_cross_block(None, None) == bad
     block = fa._FWD_CROSS_BLOCK(*[1 << 20] * 5, 1, 4, 2, 5, 1 << 33, 64, 0.125, 0, 0, -1, -1, 0.0, 0, 0,
