@@ -762,6 +762,7 @@ fa_status fa_decode_rel(const void* q, const void* k_cache, const void* v_cache,
     a.o_part = reinterpret_cast<float*>(ws);
     a.lse_part = reinterpret_cast<float*>(ws + p.lse_off);
     a.pieces = reinterpret_cast<int2*>(ws + p.pieces_off);
+    a.ctas = p.grid;
   }
   cudaError_t e = fa::launch_decode(tq, tk, tv, a, d, p.grid, s);
   if (e == cudaSuccess && !p.whole) e = fa::launch_decode_combine(a, d, s);

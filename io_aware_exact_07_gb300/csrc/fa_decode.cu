@@ -744,6 +744,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     pdl_wait();  // this kernel may have begun before the pieces are written
     const int bkv = static_cast<int>(row / M);
     const int2 p = a.pieces[bkv];
+    // (a launch that gave up on a wait has not written all of them)
+    if (p.x < 0 || p.x >= a.ctas || p.y < 1 || p.y > a.ctas - p.x) return;
     n_seg = p.y;
     const int b = bkv / a.Hkv, rank = (bkv - b * a.Hkv) * a.B + b;  // in the list's order
     slot0 = static_cast<size_t>(rank + p.x) * M + static_cast<size_t>(row % M);

@@ -35,6 +35,7 @@ struct DecodeArgs {
   int2* pieces;                 // [B * Hkv]: the first CTA of a head and the number of its CTAs; its
                                 // pieces' results are in slots (head, in the list's order) + CTA
                                 // of o_part, lse_part
+  int ctas;                     // that walk the list
 };
 
 cudaError_t launch_decode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
