@@ -156,10 +156,13 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
  *   dtable: null, or fp32 [num_buckets, H], the gradient of the bias table: entry (n, h) is the
  *   sum of dS of head h over the pairs whose distance maps to n (rel_map: as given to
  *   fa_rel_bias; entries outside [0, num_buckets) take part in no sum). Written whole. Its sums
- *   are fp32 within a tile pair's row or place and fp64 across them, and are taken with the D of
- *   the unrounded O.
- * Every output is deterministic. fa_bwd_cross runs the kernels of fa_bwd, and for dtable three
- * more: row sums, the tiles near the diagonal, the sums by bucket. workspace:
+ *   are fp32, the last ones (over distances and over the keys beyond the range) with what each
+ *   addition rounds off kept, and are taken with the D of the unrounded O.
+ * Every output is deterministic on one device. fa_bwd_cross runs the kernels of fa_bwd; one that
+ * takes the D of rows whose tile sees a single key tile from their scores, since few weights leave
+ * nothing over which O's rounding would even out (not launched where no row can be one); and
+ * for dtable four more: row sums, the tiles near the diagonal, the sums by distance, those by
+ * bucket. workspace:
  * fa_bwd_cross_workspace_size(...) bytes (rel_grad: whether dtable is wanted), 16-byte aligned;
  * its contents on entry do not matter; calls that may overlap need one each.
  * Errors: FA_ERR_INVALID_ARG (as for fa_fwd and fa_bwd; Nq or Nk above 2^28, |q_offset| above
@@ -185,13 +188,13 @@ fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* 
 /* A learned bias of the scores by relative position, in buckets of distances: key j gets
  * table[map[clamp(j - p, -left, right) + left], h] from the query at position p in head h.
  * fa_rel_bias lays it out for the attention calls, a line of fa_rel_line_length(left, right)
- * floats per head, in log2 units (0 where left or right is out of range):
+ * floats per head (0 where left or right is out of range), in log2 units and in an order of its own:
  *   table: [num_buckets, H], fp32 (FA_TABLE_F32) or bf16 (FA_TABLE_BF16), contiguous, device;
  *          finite or -inf (which hides the bucket's keys)
  *   map:   int32 [left + right + 1], device: the bucket of distances -left .. right. An entry
  *          outside [0, num_buckets) gives a bias of 0 and is reported as FA_ERR_INVALID_ARG by
  *          fa_device_status.
- *   lines: fp32 [H, fa_rel_line_length(left, right)], device
+ *   lines: fp32 [H, fa_rel_line_length(left, right)], device, 16-byte aligned
  * A line holds the table's values as they were: lay it out again after the table changes.
  * Errors: FA_ERR_INVALID_ARG (null or unaligned pointers, sizes below 1, left or right below 0),
  * FA_ERR_UNSUPPORTED (left + right + 1 or num_buckets above 65536, H above 65535, type),
@@ -542,10 +545,12 @@ void fa_set_wait_timeout_ns(uint64_t ns);
  * FA_ERR_TIMEOUT recorded; the hook is consumed by that launch and later
  * launches run normally. mode selects the launch:
  *   1: the next forward-type kernel (fa_fwd and its _gqa / _window forms,
- *      fa_decode, fa_fwd_fp8, fa_fwd_fp8_gqa, fa_paged_attn with more than 24
- *      query rows per K/V head: with fewer its kernel waits for nothing);
+ *      fa_fwd_cross, fa_decode, fa_fwd_fp8, fa_fwd_fp8_gqa, and, with enough
+ *      query rows per K/V head, fa_paged_attn (more than 24) and fa_decode_rel
+ *      (more than 16 at d = 64, 8 at d = 128): with fewer their kernel waits for
+ *      nothing);
  *   2: the next dK/dV kernel (fa_bwd and its _gqa / _window / _noalloc forms,
- *      fa_bwd_dkdv);
+ *      fa_bwd_cross, fa_bwd_dkdv);
  *   3: the next dQ kernel (the same backward calls, fa_bwd_dq).
  * mode 0 (or any other value) clears it. */
 void fa_test_inject_stall(int mode);
