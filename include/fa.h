@@ -161,8 +161,8 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
  * Every output is deterministic on one device. fa_bwd_cross runs the kernels of fa_bwd; one that
  * takes the D of rows whose tile sees a single key tile from their scores, since few weights leave
  * nothing over which O's rounding would even out (not launched where no row can be one); and
- * for dtable four more: row sums, the tiles near the diagonal, the sums by distance, those by
- * bucket. workspace:
+ * for dtable three more: the tiles near the diagonal, the sums by distance and beyond the range,
+ * those by bucket. workspace:
  * fa_bwd_cross_workspace_size(...) bytes (rel_grad: whether dtable is wanted), 16-byte aligned;
  * its contents on entry do not matter; calls that may overlap need one each.
  * Errors: FA_ERR_INVALID_ARG (as for fa_fwd and fa_bwd; Nq or Nk above 2^28, |q_offset| above

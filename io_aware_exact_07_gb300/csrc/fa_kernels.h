@@ -94,7 +94,7 @@ struct RelLinesArgs {
 cudaError_t launch_rel_lines(const RelLinesArgs& a, cudaStream_t stream);
 
 struct RelGradArgs {
-  BwdArgs b;             // dsum becomes the D of the unrounded O
+  BwdArgs b;             // with the dQ kernel's row_sums
   const int32_t* map;
   int num_buckets;
   float* dtable;         // [num_buckets, H]

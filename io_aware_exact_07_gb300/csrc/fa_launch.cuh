@@ -29,20 +29,29 @@ inline cudaError_t allow_smem(const void* kern, int bytes, int regs,
   return e;
 }
 
-// Launches the merge of a kernel just launched on `stream`. It may be scheduled while that
+// Launches what follows a kernel just launched on `stream`. It may be scheduled while that
 // one runs; its blocks wait for its end (pdl_wait) before they read anything.
 template <typename... P, typename... A>
-cudaError_t launch_merge(void (*kern)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+cudaError_t launch_next(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                        const A&... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// The merge of a kernel's pieces.
+template <typename... P, typename... A>
+cudaError_t launch_merge(void (*kern)(P...), dim3 grid, int threads, cudaStream_t stream,
+                         const A&... args) {
+  return launch_next(kern, grid, threads, 0, stream, args...);
 }
 
 }  // namespace fa

@@ -12,12 +12,11 @@
 // (the weights of a row sum to one), so D_i + R_i is the D of the unrounded O, and the sum of dS
 // over a set of keys of the row is corrected by -R_i times their weights' sum. The dQ kernel
 // leaves R_i and the sums of dS and P over the tiles beyond either end of the range:
-//   rel_rows    adds R to D and sums up the two far fields;
-//   rel_near    recomputes dS on the tiles near the diagonal. For a fixed kt - qt every tile has
-//               the same distance at the same place, so a CTA adds tiles of a head and kt - qt,
-//               over batch rows and query tiles, element by element in registers and forms the
-//               sums along the diagonals once, when it moves on;
-//   rel_line    adds the diagonals' sums up by distance;
+//   rel_near    recomputes dS on the tiles near the diagonal, with D + R. For a fixed kt - qt every
+//               tile has the same distance at the same place, so a CTA adds tiles of a head and
+//               kt - qt, over batch rows and query tiles, element by element in registers and
+//               forms the sums along the diagonals once, when it moves on;
+//   rel_sums    adds the diagonals' sums up by distance, and the rows' sums of the two far fields;
 //   rel_table   adds the distances and the far fields up by bucket.
 // Sums are fp32, over few values each; the long ones at the end keep what each addition rounds off
 // (Knuth's two-sum): this GPU adds fp64 at a 64th of the rate.
@@ -89,8 +88,8 @@ __global__ void __launch_bounds__(256) rel_lines_kernel(const RelLinesArgs a) {
 
 // ------------------------------------------------------------------ rows
 // One block takes kRelRows query rows of a head (b, h).
-__global__ void __launch_bounds__(256) rel_rows_kernel(const RelGradArgs a, int chunks) {
-  const int bh = blockIdx.x / chunks, chunk = blockIdx.x % chunks, N = a.b.mask.N;
+__device__ __forceinline__ void rows_sums(const RelGradArgs& a, int chunks, int block) {
+  const int bh = block / chunks, chunk = block % chunks, N = a.b.mask.N;
   const size_t rows = static_cast<size_t>(a.b.mask.B) * a.b.mask.H * N;
   float left = 0.f, right = 0.f;
   static_assert(kRelRows == 256, "a thread per row");
@@ -103,7 +102,6 @@ __global__ void __launch_bounds__(256) rel_rows_kernel(const RelGradArgs a, int 
       const float* p = a.b.row_sums + 4 * rows * k + idx;
       s[k] = (p[0] + p[rows]) + (p[2 * rows] + p[3 * rows]);
     }
-    a.b.dsum[idx] += s[0];
     // (a row that sees no key has sums of zero)
     left = fmaf(-s[0], 1.f - s[3], s[1]);
     right = fmaf(-s[0], s[4], s[2]);
@@ -121,7 +119,7 @@ __global__ void __launch_bounds__(256) rel_rows_kernel(const RelGradArgs a, int 
   __syncthreads();
   if (threadIdx.x < 2) {
     const float* x = part[threadIdx.x];
-    a.far_sums[static_cast<size_t>(blockIdx.x) * 2 + threadIdx.x] =
+    a.far_sums[static_cast<size_t>(block) * 2 + threadIdx.x] =
         ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
   }
 }
@@ -277,6 +275,7 @@ __global__ void __launch_bounds__(kNearThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  pdl_wait();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -438,6 +437,7 @@ __global__ void __launch_bounds__(kNearThreads, 1)
 #pragma unroll
       for (int c = 0; c < 32; ++c) acc[c] = 0.f;
     };
+    const size_t rows = static_cast<size_t>(mk.B) * mk.H * N;
     int4 p = make_int4(-1, 0, 0, -1), p_next;  // the pair, and the one after it
     int kv_len = 0, kv_next = 0;
     float lse_next = 0.f, d_next = 0.f;        // lse and D of the next pair's row
@@ -456,7 +456,10 @@ __global__ void __launch_bounds__(kNearThreads, 1)
       if (p_next.x >= 0 && row < N) {
         const size_t i = static_cast<size_t>(p_next.x) * N + row;
         lse_next = args.b.lse[i];
-        if constexpr (!ROWS) d_next = args.b.dsum[i];
+        if constexpr (!ROWS) {  // the D of the unrounded O: D and the row's sum of dS
+          const float* p = args.b.row_sums + i;
+          d_next = args.b.dsum[i] + ((p[0] + p[rows]) + (p[2 * rows] + p[3 * rows]));
+        }
       }
     };
     if (ROWS && args.b.mode != kRel) {  // no bias
@@ -585,7 +588,7 @@ constexpr int kMaxDiags = 640;
 constexpr int kOver = 2 * (kTile - 1);  // a near tile reaches that far past either end
 
 // Four threads per distance, one for each warpgroup's part of the diagonals' sums.
-__global__ void __launch_bounds__(256) rel_line_kernel(const RelGradArgs a, int ctas) {
+__device__ __forceinline__ void line_sums(const RelGradArgs& a, int ctas, int block, int h) {
   __shared__ long long start[kMaxDiags + 1];  // first pair of each group, within a head
   const NearList l = near_list(a);
   for (int g = threadIdx.x; g <= l.n_diag; g += 256) {
@@ -596,8 +599,8 @@ __global__ void __launch_bounds__(256) rel_line_kernel(const RelGradArgs a, int 
   __syncthreads();
   const long long per_head = start[l.n_diag];
   const long long per = max(1ll, near_per_cta(per_head * a.b.mask.H, ctas));
-  const int left = a.b.rel.left, right = a.b.rel.right, off = a.b.mask.q_off, h = blockIdx.y;
-  const int x = blockIdx.x * 64 + static_cast<int>(threadIdx.x >> 2), k = threadIdx.x & 3;
+  const int left = a.b.rel.left, right = a.b.rel.right, off = a.b.mask.q_off;
+  const int x = block * 64 + static_cast<int>(threadIdx.x >> 2), k = threadIdx.x & 3;
   const int length = left + right + 1 + 2 * kOver;
   float sum = 0.f;
   if (x < length) {
@@ -620,12 +623,25 @@ __global__ void __launch_bounds__(256) rel_line_kernel(const RelGradArgs a, int 
   if (x < length && k == 0) a.line_sums[static_cast<size_t>(h) * length + x] = sum;
 }
 
+// The far fields' sums and those by distance need nothing of one another: one launch (4 us less
+// at B = 16, H = 16, N = 1024 than one each).
+__global__ void __launch_bounds__(256)
+    rel_sums_kernel(const RelGradArgs a, int ctas, int chunks, int line_blocks) {
+  const int block = blockIdx.x, n = line_blocks * a.b.mask.H;
+  pdl_wait();
+  if (block < n)
+    line_sums(a, ctas, block % line_blocks, block / line_blocks);
+  else
+    rows_sums(a, chunks, block - n);
+}
+
 // ------------------------------------------------------------------ table
 // A block takes 32 buckets of a head, a lane each; its warps share the distances.
 __global__ void __launch_bounds__(256) rel_table_kernel(const RelGradArgs a, int chunks) {
   __shared__ Sum part[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
   const int n = blockIdx.x * 32 + lane;
+  pdl_wait();
   const int left = a.b.rel.left, right = a.b.rel.right;
   const int length = left + right + 1 + 2 * kOver;
   const float* line = a.line_sums + static_cast<size_t>(h) * length;
@@ -669,8 +685,7 @@ cudaError_t launch_near(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), NearL<D>::kSmemBytes, 0, ready);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kNearThreads, NearL<D>::kSmemBytes, stream>>>(tq, tk, tv, tdo, a);
-  return cudaGetLastError();
+  return launch_next(kern, dim3(ctas), kNearThreads, NearL<D>::kSmemBytes, stream, tq, tk, tv, tdo, a);
 }
 
 template <bool ROWS>
@@ -712,18 +727,17 @@ cudaError_t launch_rel_grad(const CUtensorMap& tq, const CUtensorMap& tk, const 
   if (a.n_diag > kMaxDiags) return cudaErrorInvalidValue;
   const MaskParams& m = a.b.mask;
   const int chunks = (m.N + kRelRows - 1) / kRelRows;
-  rel_rows_kernel<<<chunks * m.B * m.H, 256, 0, stream>>>(a, chunks);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
   const int ctas = num_sms < kRelMaxCtas ? num_sms : kRelMaxCtas;
-  if (e == cudaSuccess && a.n_diag > 0)
+  if (a.n_diag > 0)
     e = launch_near_d<false>(tq, tk, tv, tdo, a, d, dropout, ctas, stream);
   if (e != cudaSuccess) return e;
   const int length = a.b.rel.left + a.b.rel.right + 1 + 2 * kOver;
-  rel_line_kernel<<<dim3((length + 63) / 64, m.H), 256, 0, stream>>>(a, ctas);
-  e = cudaGetLastError();
+  const int line_blocks = (length + 63) / 64;
+  e = launch_next(rel_sums_kernel, dim3((line_blocks + chunks * m.B) * m.H), 256, 0, stream, a, ctas,
+                  chunks, line_blocks);
   if (e != cudaSuccess) return e;
-  rel_table_kernel<<<dim3((a.num_buckets + 31) / 32, m.H), 256, 0, stream>>>(a, chunks);
-  return cudaGetLastError();
+  return launch_next(rel_table_kernel, dim3((a.num_buckets + 31) / 32, m.H), 256, 0, stream, a, chunks);
 }
 
 }  // namespace fa
