@@ -162,7 +162,9 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
  * takes the D of rows whose tile sees a single key tile from their scores, since few weights leave
  * nothing over which O's rounding would even out (not launched where no row can be one); and
  * for dtable three more: the tiles near the diagonal, the sums by distance and beyond the range,
- * those by bucket. workspace:
+ * those by bucket. Where there are few key tiles (B*H_kv*ceil(Nk/128) well below the number of SMs)
+ * the dK/dV kernel's CTAs share the queries of each and another kernel adds up their parts, which
+ * the workspace has room for (at most 304 * d KB). workspace:
  * fa_bwd_cross_workspace_size(...) bytes (rel_grad: whether dtable is wanted), 16-byte aligned;
  * its contents on entry do not matter; calls that may overlap need one each.
  * Errors: FA_ERR_INVALID_ARG (as for fa_fwd and fa_bwd; Nq or Nk above 2^28, |q_offset| above

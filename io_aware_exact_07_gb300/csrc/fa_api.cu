@@ -353,6 +353,7 @@ static fa_status bwd_prepare(const void* q, const void* k, const void* v, const 
   a->mode = wl >= 0 || wr >= 0 ? fa::kWindow : fa::kPlain;
   a->rel = fa::RelParams{};
   a->row_sums = nullptr;
+  a->pieces = 1;
   a->key_tiles = nullptr;
   return FA_OK;
 }
@@ -926,20 +927,30 @@ fa_status fa_fwd_cross(const void* q, const void* k, const void* v, void* o, flo
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// Workspace of fa_bwd_cross: D, the list of key tiles, and for the gradient of a bias table what the dQ kernel leaves of
-// each query row, the near tiles' diagonal sums and the far fields' sums.
+// Workspace of fa_bwd_cross: D, the list of key tiles, the parts of dK and dV where key tiles are cut
+// into pieces, and for the gradient of a bias table what the dQ kernel leaves of each query row, the
+// near tiles' diagonal sums and the far fields' sums.
 struct CrossWorkspace {
   int first, n_diag;  // near tile pairs: kt - qt = first .. first + n_diag - 1
-  size_t tiles_off, rows_off, diag_off, line_off, far_off, bytes;
+  size_t tiles_off, part_off, rows_off, diag_off, line_off, far_off, bytes;
 };
-static CrossWorkspace cross_workspace(int B, int H, int Nq, int Nk, int causal, int q_offset,
+static CrossWorkspace cross_workspace(int B, int H, int Nq, int Nk, int d, int causal, int q_offset,
                                       bool grad, int left, int right) {
   CrossWorkspace w = {};
   const size_t rows = static_cast<size_t>(B) * H * Nq;
   w.tiles_off = round256(rows * sizeof(float));
   // (room for a K/V head per query head)
   const size_t tiles = static_cast<size_t>(B) * H * ((static_cast<size_t>(Nk) + fa::kTile - 1) / fa::kTile);
-  w.bytes = w.tiles_off + round256((tiles + 1) * sizeof(int32_t));
+  w.part_off = w.tiles_off + round256((tiles + 1) * sizeof(int32_t));
+  w.bytes = w.part_off;
+  // pieces have two query tiles or more, and for all H_kv there are at most kMaxPieces
+  const size_t k_tiles = (static_cast<size_t>(Nk) + fa::kTile - 1) / fa::kTile;
+  const size_t q_tiles = (static_cast<size_t>(Nq) + fa::kTile - 1) / fa::kTile;
+  if (2 * B * k_tiles <= fa::kMaxPieces) {
+    size_t units = tiles * q_tiles / 2;
+    if (units > fa::kMaxPieces) units = fa::kMaxPieces;
+    w.bytes += units * 2 * fa::kTile * d * sizeof(float);
+  }
   if (!grad) return w;
   w.rows_off = w.bytes;
   w.diag_off = w.rows_off + round256(rows * 4 * fa::kRelRowSums * sizeof(float));
@@ -972,7 +983,7 @@ size_t fa_bwd_cross_workspace_size(int B, int H, int Nq, int Nk, int d, int caus
       static_cast<long long>(B) * H * Nq >= (1ll << 31))
     return 0;
   if (rel_grad && fa_rel_line_length(rel_left, rel_right) == 0) return 0;
-  return cross_workspace(B, H, Nq, Nk, causal, q_offset, rel_grad != 0, rel_left, rel_right).bytes;
+  return cross_workspace(B, H, Nq, Nk, d, causal, q_offset, rel_grad != 0, rel_left, rel_right).bytes;
 }
 
 fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* o,
@@ -1000,7 +1011,7 @@ fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* 
       return FA_ERR_INVALID_ARG;
     if (num_buckets > kMaxDistances) return FA_ERR_UNSUPPORTED;
   }
-  const CrossWorkspace w = cross_workspace(B, H, Nq, Nk, a.mask.causal, q_offset, grad, rel_left,
+  const CrossWorkspace w = cross_workspace(B, H, Nq, Nk, d, a.mask.causal, q_offset, grad, rel_left,
                                            rel_right);
   if (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace))
     return FA_ERR_WORKSPACE;
@@ -1024,6 +1035,10 @@ fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* 
   a.dv = static_cast<__nv_bfloat16*>(dv);
   a.row_sums = grad ? reinterpret_cast<float*>(ws + w.rows_off) : nullptr;
   a.key_tiles = seqlens_k != nullptr ? reinterpret_cast<int32_t*>(ws + w.tiles_off) : nullptr;
+  a.pieces = fa::dkdv_pieces(
+      static_cast<long long>(B) * H_kv * ((Nk + fa::kTile - 1) / fa::kTile),
+      static_cast<long long>(H / H_kv) * ((Nq + fa::kTile - 1) / fa::kTile));
+  a.dkdv_part = reinterpret_cast<float*>(ws + w.part_off);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool drop = a.drop.p8 > 0;
   cudaError_t e = fa::launch_bwd_preprocess(a, d, di->num_sms, s);
@@ -1032,6 +1047,7 @@ fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* 
     a.sync.inject_stall = take_stall(kStallDkdv);
     e = fa::launch_bwd_dkdv(m[0], m[1], m[2], m[3], a, d, drop, di->num_sms, s);
   }
+  if (e == cudaSuccess && a.pieces > 1) e = fa::launch_dkdv_merge(a, d, s);
   if (e == cudaSuccess) {
     a.sync.inject_stall = take_stall(kStallDq);
     e = fa::launch_bwd_dq(m[0], m[1], m[2], m[3], a, d, drop, di->num_sms, s);

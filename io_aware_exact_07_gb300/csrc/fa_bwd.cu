@@ -141,7 +141,7 @@ struct DkdvLayout {
   __device__ static constexpr uint32_t col_dpt() { return static_cast<uint32_t>(2 * D + 128); }
 };
 
-template <int D, bool DROPOUT, bool GQA, int MODE>
+template <int D, bool DROPOUT, bool GQA, int MODE, bool PIECES = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int Nk = CROSS ? mk.Nk : N;         // keys
   const int n_q = (N + kTile - 1) / kTile;  // query tiles
   const int n_t = CROSS ? (Nk + kTile - 1) / kTile : n_q;  // key tiles
-  const int n_units = CROSS ? key_tile_count(args, n_t) : mk.B * mk.Hkv * n_t;
+  const int n_units = CROSS ? key_tile_units<PIECES>(args, n_t) : mk.B * mk.Hkv * n_t;
   const int G = GQA ? mk.H / mk.Hkv : 1;  // query heads per K/V head
 
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int unit_count = 0;
     for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-      const int e = CROSS ? key_tile_at(args, u) : u;
+      const int e = CROSS ? key_tile_at<PIECES>(args, u) : u;
       const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
       const int b = bhk / mk.Hkv;
       const int kv_len = kv_len_of(mk, b);
@@ -282,6 +282,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if constexpr (REL) head = rel_head(args.rel, bh % mk.H);
         for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
           uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
+          if constexpr (PIECES)
+            bits &= piece_bits(args, sched_unit(unit_count), kt,
+                               bh - group_first_head<GQA>(mk, bhk), G, n_q, chunk);
           while (bits != 0u) {
             const int qt = chunk * 32 + (__ffs(bits) - 1);
             bits &= bits - 1;
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     };
     for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-      const int e = CROSS ? key_tile_at(args, u) : u;
+      const int e = CROSS ? key_tile_at<PIECES>(args, u) : u;
       const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
       const int b = bhk / mk.Hkv;
       const int kv_len = kv_len_of(mk, b);
@@ -379,6 +382,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
              ++bh) {  // the query heads sharing this K/V head
         for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
           uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
+          if constexpr (PIECES)
+            bits &= piece_bits(args, sched_unit(unit_count), kt,
+                               bh - group_first_head<GQA>(mk, bhk), G, n_q, chunk);
           while (bits != 0u) {
             bits &= bits - 1;
             const int sq = it % L::kQStages, sd = it % L::kDOStages;
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int unit_count = 0;
     for (int u = sched_unit(0); u < n_units && ok; u = sched_unit(++unit_count)) {
-      const int e = CROSS ? key_tile_at(args, u) : u;
+      const int e = CROSS ? key_tile_at<PIECES>(args, u) : u;
       const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
       const int b = bhk / mk.Hkv;
       const int kv_len = kv_len_of(mk, b);
@@ -500,6 +506,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
              ++bh) {  // the query heads sharing this K/V head
         for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
           uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
+          if constexpr (PIECES)
+            bits &= piece_bits(args, sched_unit(unit_count), kt,
+                               bh - group_first_head<GQA>(mk, bhk), G, n_q, chunk);
           while (bits != 0u) {
             const int qt = chunk * 32 + (__ffs(bits) - 1);
             bits &= bits - 1;
@@ -685,6 +694,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = 0u;
         }
+        if constexpr (PIECES) {
+          float4* part = reinterpret_cast<float4*>(
+              args.dkdv_part +
+              ((static_cast<size_t>(sched_unit(unit_count)) * 2 + (wg == 0)) * kTile + r) * D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            part[k] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                  __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+          continue;
+        }
         uint32_t pk[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k)
@@ -738,10 +757,15 @@ static cudaError_t launch_dkdv_impl(const CUtensorMap& tq, const CUtensorMap& tk
                                : fa_bwd_dkdv_kernel<D, DROP, G, kPlain>;
   };
   auto kern = a.mask.Hkv != a.mask.H ? pick(std::true_type{}) : pick(std::false_type{});
+  int kind = a.mask.Hkv != a.mask.H;
+  if (a.pieces > 1) {
+    kern = a.mode == kRel ? fa_bwd_dkdv_kernel<D, DROP, true, kRel, true>
+                          : fa_bwd_dkdv_kernel<D, DROP, true, kCross, true>;
+    kind = 2;
+  }
   constexpr int kSmem = DkdvLayout<D, DROP>::kSmemBytes;
-  static std::atomic<unsigned long long> ready[2][4];
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem, 0,
-                             ready[a.mask.Hkv != a.mask.H][a.mode]);
+  static std::atomic<unsigned long long> ready[3][4];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem, 0, ready[kind][a.mode]);
   if (e != cudaSuccess) return e;
   kern<<<grid, kBwdThreads, kSmem, stream>>>(tq, tk, tv, tdo, a);
   return cudaGetLastError();
@@ -751,12 +775,51 @@ cudaError_t launch_bwd_dkdv(const CUtensorMap& tq, const CUtensorMap& tk, const 
                             const CUtensorMap& tdo, const BwdArgs& a, int d, bool dropout,
                             int num_sms, cudaStream_t stream) {
   const int n_t = (a.mask.Nk + kTile - 1) / kTile;
-  const long long units = static_cast<long long>(a.mask.B) * a.mask.Hkv * n_t;  // (K/V head, key tile)
+  // (K/V head, key tile, piece)
+  const long long units = static_cast<long long>(a.mask.B) * a.mask.Hkv * n_t * a.pieces;
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
   if (grid <= 0) return cudaSuccess;
   if (d == 64) return launch_bwd_dkdv_split(tq, tk, tv, tdo, a, d, dropout, num_sms, stream);
   return dropout ? launch_dkdv_impl<128, true>(tq, tk, tv, tdo, a, grid, stream)
                  : launch_dkdv_impl<128, false>(tq, tk, tv, tdo, a, grid, stream);
+}
+
+// dK and dV of the listed key tiles from their pieces, a block 8 KB of a piece at a time.
+template <int D>
+__global__ void __launch_bounds__(256) dkdv_merge_kernel(const BwdArgs a) {
+  constexpr int kBlocks = 2 * kTile * D / 4 / 256;  // per key tile
+  pdl_wait();
+  const int n_t = (a.mask.Nk + kTile - 1) / kTile;
+  const int tile = blockIdx.x / kBlocks, at = (blockIdx.x % kBlocks) * 256 + threadIdx.x;
+  if (tile * a.pieces >= key_tile_units<true>(a, n_t)) return;
+  const int e = key_tile_at<true>(a, tile * a.pieces), bhk = e / n_t, kt = e % n_t;
+  const bool is_dv = at >= kTile * D / 4;
+  const int row = at / (D / 4) - (is_dv ? kTile : 0), col = at % (D / 4) * 4;
+  if (kt * kTile + row >= a.mask.Nk) return;
+  const float4* p = reinterpret_cast<const float4*>(a.dkdv_part) +
+                    static_cast<size_t>(tile) * a.pieces * (2 * kTile * D / 4) + at;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < a.pieces; ++i) {
+    const float4 x = p[static_cast<size_t>(i) * (2 * kTile * D / 4)];
+    sum.x += x.x;
+    sum.y += x.y;
+    sum.z += x.z;
+    sum.w += x.w;
+  }
+  const float mult = is_dv ? a.drop.keep_scale : a.scale;
+  uint2 w;
+  w.x = pack_bf16x2(sum.x * mult, sum.y * mult);
+  w.y = pack_bf16x2(sum.z * mult, sum.w * mult);
+  *reinterpret_cast<uint2*>((is_dv ? a.dv : a.dk) +
+                            (static_cast<size_t>(bhk) * a.mask.Nk + kt * kTile + row) * D + col) = w;
+}
+
+cudaError_t launch_dkdv_merge(const BwdArgs& a, int d, cudaStream_t stream) {
+  const int tiles = a.mask.B * a.mask.Hkv * ((a.mask.Nk + kTile - 1) / kTile);
+  const int blocks = tiles * (2 * kTile * d / 4 / 256);
+  return d == 64 ? launch_next(dkdv_merge_kernel<64>, dim3(blocks), 256, 0, stream, a)
+                 : launch_next(dkdv_merge_kernel<128>, dim3(blocks), 256, 0, stream, a);
 }
 
 cudaError_t launch_bwd_dq(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

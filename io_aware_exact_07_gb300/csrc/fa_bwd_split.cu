@@ -127,7 +127,7 @@ struct DkdvBars {
   uint32_t stall;  // test hook: never completed
 };
 
-template <int D, bool DROPOUT, bool GQA, int MODE>
+template <int D, bool DROPOUT, bool GQA, int MODE, bool PIECES = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_bwd_dkdv_split_kernel(const __grid_constant__ CUtensorMap tm_q,
                              const __grid_constant__ CUtensorMap tm_k,
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int Nk = CROSS ? mk.Nk : N;                        // keys
   const int n_q = (N + kTile - 1) / kTile;                 // query tiles
   const int n_t = CROSS ? (Nk + kTile - 1) / kTile : n_q;  // key tiles
-  const int n_units = CROSS ? key_tile_count(args, n_t) : mk.B * mk.Hkv * n_t;
+  const int n_units = CROSS ? key_tile_units<PIECES>(args, n_t) : mk.B * mk.Hkv * n_t;
   const int G = GQA ? mk.H / mk.Hkv : 1;  // query heads per K/V head
   // rotated schedule under key padding (where the list has its empty units too)
   const bool rot = mk.seqlens_k != nullptr && !CROSS;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int unit_count = 0;
       for (int u = sched_unit(0, rot); u < n_units && ok; u = sched_unit(++unit_count, rot)) {
-        const int e = CROSS ? key_tile_at(args, u) : u;
+        const int e = CROSS ? key_tile_at<PIECES>(args, u) : u;
         const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
         const int kv_len = kv_len_of(mk, bhk / mk.Hkv);
         const int n_kv = (kv_len + kTile - 1) / kTile;
@@ -260,6 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (REL) head = rel_head(args.rel, bh % mk.H);
           for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
             uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
+            if constexpr (PIECES)
+              bits &= piece_bits(args, sched_unit(unit_count, rot), kt,
+                                 bh - group_first_head<GQA>(mk, bhk), G, n_q, chunk);
             while (bits != 0u) {
               const int qt = chunk * 32 + (__ffs(bits) - 1);
               bits &= bits - 1;
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
       int unit_count = 0;
       for (int u = sched_unit(0, rot); u < n_units && ok; u = sched_unit(++unit_count, rot)) {
-        const int e = CROSS ? key_tile_at(args, u) : u;
+        const int e = CROSS ? key_tile_at<PIECES>(args, u) : u;
         const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
         const int kv_len = kv_len_of(mk, bhk / mk.Hkv);
         const int n_kv = (kv_len + kTile - 1) / kTile;
@@ -342,7 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
                ++bh) {  // the query heads sharing this K/V head
           for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
-            const uint32_t vbits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
+            uint32_t vbits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
+            if constexpr (PIECES)
+              vbits &= piece_bits(args, sched_unit(unit_count, rot), kt,
+                                 bh - group_first_head<GQA>(mk, bhk), G, n_q, chunk);
             if (leader) {
               for (uint32_t bits = vbits; bits != 0u && ok; bits &= bits - 1) {
                 const int s = it % L::kStages;
@@ -385,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int unit_count = 0;
       for (int u = sched_unit(0, rot); u < n_units && ok; u = sched_unit(++unit_count, rot)) {
-        const int e = CROSS ? key_tile_at(args, u) : u;
+        const int e = CROSS ? key_tile_at<PIECES>(args, u) : u;
         const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
         const int kv_len = kv_len_of(mk, bhk / mk.Hkv);
         const int n_kv = (kv_len + kTile - 1) / kTile;
@@ -393,7 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int bh = group_first_head<GQA>(mk, bhk), bh_end = bh + G; bh < bh_end && ok;
                ++bh) {  // the query heads sharing this K/V head
           for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
-            const uint32_t vbits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
+            uint32_t vbits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
+            if constexpr (PIECES)
+              vbits &= piece_bits(args, sched_unit(unit_count, rot), kt,
+                                 bh - group_first_head<GQA>(mk, bhk), G, n_q, chunk);
             if (leader) {
               for (uint32_t bits = vbits; bits != 0u && ok; bits &= bits - 1) {
                 const int s = it % L::kStages;
@@ -461,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int unit_count = 0;
     for (int u = sched_unit(0, rot); u < n_units && ok; u = sched_unit(++unit_count, rot)) {
-      const int e = CROSS ? key_tile_at(args, u) : u;
+      const int e = CROSS ? key_tile_at<PIECES>(args, u) : u;
         const int bhk = e / n_t, kt = e % n_t;  // K/V head, key tile
       const int kv_len = kv_len_of(mk, bhk / mk.Hkv);
       const int n_kv = (kv_len + kTile - 1) / kTile;
@@ -477,6 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1)
              ++bh) {  // the query heads sharing this K/V head
         for (int chunk = 0; chunk * 32 < n_q && ok; ++chunk) {
           uint32_t bits = warp_valid_bits_t<MODE>(mk, kt, chunk, n_q, n_kv);
+          if constexpr (PIECES)
+            bits &= piece_bits(args, sched_unit(unit_count, rot), kt,
+                               bh - group_first_head<GQA>(mk, bhk), G, n_q, chunk);
           while (bits != 0u && ok) {
             const int qt = chunk * 32 + (__ffs(bits) - 1);
             bits &= bits - 1;
@@ -682,6 +694,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = 0u;
+        }
+        if constexpr (PIECES) {
+          tc_fence_before();
+          mbar_arrive(bars.acc_free);
+          float4* part = reinterpret_cast<float4*>(
+              args.dkdv_part +
+              ((static_cast<size_t>(sched_unit(unit_count)) * 2 + is_dv) * kTile + r) * D +
+              kHalf * (wg & 1));
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            part[k] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                  __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+          continue;
         }
         uint32_t pk[16];
 #pragma unroll
@@ -1414,9 +1439,19 @@ cudaError_t launch_dkdv_split_d(const CUtensorMap& tq, const CUtensorMap& tk,
   const std::false_type no;
   auto kern = a.mask.Hkv != a.mask.H ? (dropout ? pick(yes, yes) : pick(no, yes))
                                      : (dropout ? pick(yes, no) : pick(no, no));
-  static std::atomic<unsigned long long> ready[2][2][4];
+  int kind = a.mask.Hkv != a.mask.H;
+  if (a.pieces > 1) {
+    auto cut = [&](auto drop) {
+      constexpr bool DR = decltype(drop)::value;
+      return a.mode == kRel ? fa_bwd_dkdv_split_kernel<D, DR, true, kRel, true>
+                            : fa_bwd_dkdv_split_kernel<D, DR, true, kCross, true>;
+    };
+    kern = dropout ? cut(yes) : cut(no);
+    kind = 2;
+  }
+  static std::atomic<unsigned long long> ready[3][2][4];
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), DkdvL<D>::kSmemBytes, kRegsLaunch,
-                             ready[a.mask.Hkv != a.mask.H][dropout][a.mode]);
+                             ready[kind][dropout][a.mode]);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, DkdvL<D>::kSmemBytes, stream>>>(tq, tk, tv, tdo, a);
   return cudaGetLastError();
@@ -1451,7 +1486,7 @@ cudaError_t launch_bwd_dkdv_split(const CUtensorMap& tq, const CUtensorMap& tk,
                                   const CUtensorMap& tv, const CUtensorMap& tdo, const BwdArgs& a,
                                   int d, bool dropout, int num_sms, cudaStream_t stream) {
   const int n_t = (a.mask.Nk + kTile - 1) / kTile;
-  const long long units = static_cast<long long>(a.mask.B) * a.mask.Hkv * n_t;  // (K/V head, key tile)
+  const long long units = static_cast<long long>(a.mask.B) * a.mask.Hkv * n_t * a.pieces;
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
   if (grid <= 0) return cudaSuccess;
   if (d != 64) return cudaErrorInvalidValue;  // head dimension 128 runs the single-issuer kernel

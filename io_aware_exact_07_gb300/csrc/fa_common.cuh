@@ -308,6 +308,16 @@ __device__ __forceinline__ TileRun free_query_tiles(const MaskParams& m, int kt,
   return r;
 }
 
+// kCross, kRel: the query tiles that see some key of key tile kt (tile_valid).
+__device__ __forceinline__ TileRun seeing_query_tiles(const MaskParams& m, int kt, int n_q) {
+  TileRun r{0, n_q};
+  const int k0 = kt * kTile - m.q_off;
+  if (m.causal) r.lo = max(r.lo, ceil_tiles(k0 - (kTile - 1)));
+  if (m.wr >= 0) r.lo = max(r.lo, ceil_tiles(k0 - m.wr - (kTile - 1)));
+  if (m.wl >= 0) r.hi = min(r.hi, floor_tiles(k0 + (kTile - 1) + m.wl) + 1);
+  return r;
+}
+
 // kCross, kRel: the key tiles that a query tile at position p0 sees some key of (tile_valid).
 __device__ __forceinline__ TileRun seen_key_tiles(const MaskParams& m, int p0, int n_kv) {
   TileRun r{0, n_kv};

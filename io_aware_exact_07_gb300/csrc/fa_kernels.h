@@ -42,14 +42,59 @@ struct BwdArgs {
   // many as the first entry says), so that the CTAs of the key-tile kernel get even shares. The
   // preprocess kernel lists them, and zeroes the gradients of whole tiles behind the lengths.
   int32_t* key_tiles;
+  // kCross, kRel: the key-tile kernel's units per key tile, each with an even share of the query
+  // tiles that see it (dkdv_pieces), and for more than one their dK and dV before scaling, fp32
+  // [unit][dK, dV][128][d], which launch_dkdv_merge adds up in order.
+  int pieces;
+  float* dkdv_part;
 };
 
-__device__ __forceinline__ int key_tile_count(const BwdArgs& a, int tiles) {
-  return a.key_tiles != nullptr ? a.key_tiles[0] : a.mask.B * a.mask.Hkv * tiles;
+// Unit u of the key-tile kernel is the list's key tile u, in its PIECES instances piece u % pieces
+// of key tile u / pieces.
+template <bool PIECES>
+__device__ __forceinline__ int key_tile_units(const BwdArgs& a, int tiles) {
+  return (a.key_tiles != nullptr ? a.key_tiles[0] : a.mask.B * a.mask.Hkv * tiles) *
+         (PIECES ? a.pieces : 1);
 }
+template <bool PIECES>
 __device__ __forceinline__ int key_tile_at(const BwdArgs& a, int u) {
-  return a.key_tiles != nullptr ? a.key_tiles[1 + u] : u;
+  const int i = PIECES ? u / a.pieces : u;
+  return a.key_tiles != nullptr ? a.key_tiles[1 + i] : i;
 }
+// The query tiles 32 chunk .. 32 chunk + 31 of the g-th query head of unit u that its piece has.
+__device__ __forceinline__ uint32_t piece_bits(const BwdArgs& a, int u, int kt, int g, int G,
+                                               int n_q, int chunk) {
+  const TileRun run = seeing_query_tiles(a.mask, kt, n_q);
+  const int n = max(0, run.hi - run.lo), piece = u % a.pieces;
+  const long long total = static_cast<long long>(n) * G;
+  const int from = static_cast<int>(total * piece / a.pieces) - g * n;
+  const int to = static_cast<int>(total * (piece + 1) / a.pieces) - g * n;
+  const int lo = run.lo + min(max(from, 0), n) - 32 * chunk;
+  const int hi = run.lo + min(max(to, 0), n) - 32 * chunk;
+  const uint32_t below_lo = lo <= 0 ? 0u : (lo >= 32 ? ~0u : (1u << lo) - 1u);
+  const uint32_t below_hi = hi <= 0 ? 0u : (hi >= 32 ? ~0u : (1u << hi) - 1u);
+  return below_hi & ~below_lo;
+}
+
+// Few key tiles (a short memory, few K/V heads) leave most SMs without a unit: their units are cut
+// into pieces where the longest CTA's steps (query tiles, kUnitSteps per unit, kMergeSteps for the
+// merge) become fewer. At most kMaxPieces units. (B=7 H=16 H_kv=4, 95 keys, 6763 queries, d=64: 94 us
+// with the merge against 367. These are instances of their own: with the pieces in all instances those
+// that do without took 3 to 19 % longer.)
+constexpr int kMaxPieces = 304;     // two for each SM
+constexpr int kPieceSms = 152;
+inline int dkdv_pieces(long long key_tiles, long long query_tiles) {
+  constexpr long long kUnitSteps = 3, kMergeSteps = 6;
+  auto steps = [&](long long s) {
+    return (key_tiles * s + kPieceSms - 1) / kPieceSms * ((query_tiles + s - 1) / s + kUnitSteps) +
+           (s > 1 ? kMergeSteps : 0);
+  };
+  int best = 1;
+  for (long long s = 2; s * key_tiles <= kMaxPieces && 2 * s <= query_tiles; ++s)
+    if (steps(s) < steps(best)) best = static_cast<int>(s);
+  return best;
+}
+cudaError_t launch_dkdv_merge(const BwdArgs& a, int d, cudaStream_t stream);
 
 // Sums over the keys of a query row: dS, dS left of the range of distances, dS right of it, P
 // not left of it, P right of it.

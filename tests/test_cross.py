@@ -119,6 +119,22 @@ def test_grouped_heads_and_dropout(d):
     check(2, 6, 2, 140, 200, d, p=0.2, lens=[77, 200], seed=6)
 
 
+# few key tiles, whose query tiles are shared among CTAs: of one and several query heads, with masks
+# that leave some tiles and CTAs nothing
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", [
+    dict(B=1, H=2, Hkv=2, Nq=2500, Nk=95), dict(B=2, H=6, Hkv=2, Nq=900, Nk=200, lens=[0, 150]),
+    dict(B=1, H=4, Hkv=1, Nq=1300, Nk=300, causal=True, q_offset=-700),
+    dict(B=1, H=1, Hkv=1, Nq=5000, Nk=260, window=(100, 60), q_offset=-400),
+    dict(B=2, H=2, Hkv=2, Nq=1700, Nk=130, p=0.2, lens=[130, 40]),
+    dict(B=2, H=4, Hkv=4, Nq=1500, Nk=150, lens=[129, 3], rule=(8, 100, True), junk=math.nan),
+    dict(B=1, H=3, Hkv=1, Nq=1100, Nk=270, causal=True, q_offset=20, rule=(32, 128, False)),
+    dict(B=1, H=1, Hkv=1, Nq=8200, Nk=1)])
+def test_few_key_tiles_and_many_queries(case, d):
+    check(d=d, seed=60, **case)
+
+
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("case", [dict(Nk=5), dict(Nk=128, rule=(8, 16, True)), dict(Nk=2, p=0.3),
