@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kNearThreads, 1)
     const size_t rows = static_cast<size_t>(mk.B) * mk.H * N;
     int4 p = make_int4(-1, 0, 0, -1), p_next;  // the pair, and the one after it
     int kv_len = 0, kv_next = 0;
-    float lse_next = 0.f, d_next = 0.f;        // lse and D of the next pair's row
+    float lse_next = 0.f, d_next = 0.f, r_next[4];  // lse, D and dS sums of the next pair's row
     auto look_ahead = [&](uint32_t n) {
       const uint32_t slot = n % kPairSlots;
       if (!mbar_wait_warp(pair_full[slot], (n / kPairSlots) & 1u, tmo, abort_flag)) {
@@ -452,13 +452,15 @@ __global__ void __launch_bounds__(kNearThreads, 1)
       kv_next = pairs[2 * slot + 1].x;
       const int row = p_next.y * kTile + t;
       lse_next = -INFINITY;
-      d_next = 0.f;
+      d_next = r_next[0] = r_next[1] = r_next[2] = r_next[3] = 0.f;
       if (p_next.x >= 0 && row < N) {
         const size_t i = static_cast<size_t>(p_next.x) * N + row;
         lse_next = args.b.lse[i];
-        if constexpr (!ROWS) {  // the D of the unrounded O: D and the row's sum of dS
+        if constexpr (!ROWS) {  // the D of the unrounded O is D and the row's sum of dS
           const float* p = args.b.row_sums + i;
-          d_next = args.b.dsum[i] + ((p[0] + p[rows]) + (p[2 * rows] + p[3 * rows]));
+          d_next = args.b.dsum[i];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) r_next[w] = p[w * rows];
         }
       }
     };
@@ -495,7 +497,8 @@ __global__ void __launch_bounds__(kNearThreads, 1)
         line_group = group;
       }
       const float nl = lse_next == -INFINITY ? -INFINITY : -lse_next * kLog2e;
-      const float nd = ROWS ? 0.f : -d_next;  // (the sum of P Z dP / (1-p) is D)
+      const float nd =  // (ROWS: the sum of P Z dP / (1-p) is D)
+          ROWS ? 0.f : -(d_next + ((r_next[0] + r_next[1]) + (r_next[2] + r_next[3])));
       const int bh = p.x;
       look_ahead(n + 1);
       if (!ok) break;
