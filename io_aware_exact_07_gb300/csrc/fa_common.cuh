@@ -193,7 +193,9 @@ __device__ __forceinline__ int key_tiles_upto(const MaskParams& m, int qt_end, i
 
 // kCross, kRel with key lengths: batch rows in falling order of their number of key tiles, so that
 // the alternation of sched_unit gives every CTA long units and short ones, the short ones last.
-// (Rows of a batch that is not ordered come as they are: more than kMaxOrdered make units enough.)
+// (Rows of a batch that is not ordered come as they are: more than kMaxOrdered make units enough.
+// With the list of key tiles of the dK/dV kernel, 448 queries over 300 to 1500 keys, B=16 H=16 d=64:
+// forward and backward 243 us, without either 293.)
 constexpr int kMaxOrdered = 256;
 __device__ __forceinline__ bool is_ordered(const MaskParams& m) {
   return m.seqlens_k != nullptr && m.B > 1 && m.B <= kMaxOrdered;

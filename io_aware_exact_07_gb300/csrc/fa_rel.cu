@@ -224,6 +224,11 @@ struct NearL {
   static_assert(kSmemBytes <= 232448, "shared memory exceeds the per-block limit");
 };
 
+// What bounds it: a pair of tiles takes 1.6 us at either head size (B=16 H=16 N=1024 d=64, 5632 pairs,
+// 62 us; 2000 keys, 2001 distances, d=128, 6400 pairs: 68), where its products need 0.06 (d = 64), its
+// exponentials 0.5 and its bytes from L2 0.5. The tensor pipe is active 11 % of cycles, warps issue in 46 %:
+// it is each warp's chain from the wait for S over two loads from tensor memory to the sums. Loading
+// the biases four at a time gained 1 us, forming the diagonals' sums in four parts 2.
 // ROWS: instead of the near pairs' sums, D of the rows that see one key tile (launch_row_d).
 template <int D, bool DROPOUT, bool ROWS>
 __global__ void __launch_bounds__(kNearThreads, 1)
