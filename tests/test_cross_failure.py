@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import io_aware_exact_07_gb300 as fa
-from tests._cross import bucket, plain, within
+from _cross import bucket, plain, within
 
 pytestmark = pytest.mark.gpu
 
