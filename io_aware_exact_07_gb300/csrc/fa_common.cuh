@@ -99,6 +99,11 @@ __device__ __forceinline__ float rel_far_bias(const RelParams& r, const RelHead&
   return rel_far_left(r, d0, n) ? x.left : (rel_far_right(r, d0, n) ? x.right : 0.f);
 }
 
+// Windows of four biases of a head, by the distance of the first.
+__device__ __forceinline__ const float4* rel_windows(const RelParams& r, const float* line) {
+  return reinterpret_cast<const float4*>(line - r.left - kRelPad + r.pitch()) + r.left + kRelPad;
+}
+
 // Adds to N scores of this thread their own biases and brings them to log2 units: the first one's
 // is at distance dist, the others STEP apart. AT_ONCE of them are loaded together (more cost the
 // backward kernels registers; with 8 at a time the forward above takes 110 us).
@@ -107,9 +112,7 @@ __device__ __forceinline__ void rel_add(const RelParams& r, const float* line, i
                                         float c_log2, float* s) {
   static_assert(STEP == 1 || STEP == -1, "keys or queries in order");
   const uint64_t c2 = f2_pack(c_log2, c_log2);
-  const int from = STEP == 1 ? dist : dist - 3;
-  const float4* lp =  // line - left - kRelPad + pitch: the windows
-      reinterpret_cast<const float4*>(line - r.left - kRelPad + r.pitch()) + r.left + kRelPad + from;
+  const float4* lp = rel_windows(r, line) + (STEP == 1 ? dist : dist - 3);
 #pragma unroll
   for (int i = 0; i < N; i += AT_ONCE) {
     float4 b[AT_ONCE / 4];
