@@ -128,3 +128,22 @@ def test_a_cache_of_more_than_2_31_elements(G):
         bound = 2.0 ** -8 * (p @ vh.abs() + want.abs()) + 2.0 ** -18
         assert ((o[0, h, 0].double() - want).abs() - bound * (1 + 2.0 ** -9)).max() <= 0
         assert abs(lse[0, h, 0].double() - s.logsumexp(0)) <= 5e-4
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_hidden_keys_of_any_size(d):
+    """Keys that the causal mask hides from some rows or all, with scores whose weights overflow."""
+    g = torch.Generator().manual_seed(d)
+    r = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16)
+    q, k, v, do = r(2, 2, 100, d), r(2, 2, 300, d), r(2, 2, 300, d), r(2, 2, 100, d)
+    k[:, :, 200:] *= 4096
+    v[:, :, 200:] *= 4096
+    gpu = [t.cuda() for t in (q, k, v, do)]
+    kw = dict(causal=True, q_offset=100)
+    o, lse = fa.fwd(*gpu[:3], **kw)
+    grads = fa.bwd(*gpu[:3], o, gpu[3], lse, **kw)
+    torch.cuda.synchronize()
+    want, tol = plain(q, k, v, do, **kw)
+    within("o", o, want["o"], tol["o"])
+    for n, x in zip(("dq", "dk", "dv"), grads):
+        within(n, x, want[n], tol[n])
