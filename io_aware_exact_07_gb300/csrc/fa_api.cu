@@ -946,7 +946,7 @@ static CrossWorkspace cross_workspace(int B, int H, int Nq, int Nk, int d, int c
   // pieces have two query tiles or more, and for all H_kv there are at most kMaxPieces
   const size_t k_tiles = (static_cast<size_t>(Nk) + fa::kTile - 1) / fa::kTile;
   const size_t q_tiles = (static_cast<size_t>(Nq) + fa::kTile - 1) / fa::kTile;
-  if (2 * B * k_tiles <= fa::kMaxPieces) {
+  if (2 * B * k_tiles <= fa::kMaxPieces && H * q_tiles >= fa::kMinCutTiles) {
     size_t units = tiles * q_tiles / 2;
     if (units > fa::kMaxPieces) units = fa::kMaxPieces;
     w.bytes += units * 2 * fa::kTile * d * sizeof(float);

@@ -83,6 +83,7 @@ __device__ __forceinline__ uint32_t piece_bits(const BwdArgs& a, int u, int kt, 
 // that do without took 3 to 19 % longer.)
 constexpr int kMaxPieces = 304;     // two for each SM
 constexpr int kPieceSms = 152;
+constexpr int kMinCutTiles = 10;    // fewer query tiles of a unit: no cut leaves fewer steps
 inline int dkdv_pieces(long long key_tiles, long long query_tiles) {
   constexpr long long kUnitSteps = 3, kMergeSteps = 6;
   auto steps = [&](long long s) {
@@ -90,6 +91,7 @@ inline int dkdv_pieces(long long key_tiles, long long query_tiles) {
            (s > 1 ? kMergeSteps : 0);
   };
   int best = 1;
+  if (query_tiles < kMinCutTiles) return best;
   for (long long s = 2; s * key_tiles <= kMaxPieces && 2 * s <= query_tiles; ++s)
     if (steps(s) < steps(best)) best = static_cast<int>(s);
   return best;
