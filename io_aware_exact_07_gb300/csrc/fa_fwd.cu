@@ -718,21 +718,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (!ok) break;
       // ---- epilogue: O = acc * keep_scale / l, lse = (m + log2 l) * ln 2
       // the last PV of this unit has completed once its pv_done phase has
-      if (n_done > 0) {
-        if (!mbar_wait_warp(bars.pv_done[x], pv_cnt & 1, tmo, abort_flag)) {
-          fail();
-          ok = false;
-          break;
-        }
-        ++pv_cnt;
-      } else if (unit_count > 0 &&
-                 !mbar_wait_warp(bars.o_free[x], (unit_count - 1) & 1, tmo, abort_flag)) {
-        // Without key tiles nothing else holds these warps back: their arrivals for later units
-        // would stand in for the PV issuer's, and it would wait for phases that have passed.
+      // Without key tiles nothing else holds these warps back: their arrivals for later units
+      // would stand in for the PV issuer's, and it would wait for phases that have passed. They
+      // wait for the unit in front.
+      if (!mbar_wait_warp(n_done > 0 ? bars.pv_done[x] : bars.o_free[x],
+                          (n_done > 0 ? pv_cnt : unit_count + 1) & 1, tmo, abort_flag)) {
         fail();
         ok = false;
         break;
       }
+      if (n_done > 0) ++pv_cnt;
       tc_fence_after();
       const bool row_ok = row < N;
       const float inv = (l_sum > 0.f) ? args.drop.keep_scale / l_sum : 0.f;
