@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(256) rel_table_kernel(const RelGradArgs a, int
   // 32 distances at a time, a lane each, then one after another for all buckets
   for (int x0 = warp * 32; x0 < length; x0 += 256) {
     const int x = x0 + lane;
-    const float v = x < length ? __ldg(line + x) : 0.f;
+    const float v = x < length ? line[x] : 0.f;  // (of the kernel in front: no __ldg)
     const int m = __ldg(a.map + clamp_distance(min(x, length - 1) - left - kOver, left, right) + left);
     if (__any_sync(0xffffffffu, (m & ~31) == (n & ~31))) {
 #pragma unroll 8
