@@ -192,7 +192,10 @@ fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* 
  * fa_rel_bias lays it out for the attention calls, a line of fa_rel_line_length(left, right)
  * floats per head (0 where left or right is out of range), in log2 units and in an order of its own:
  *   table: [num_buckets, H], fp32 (FA_TABLE_F32) or bf16 (FA_TABLE_BF16), contiguous, device;
- *          finite or -inf (which hides the bucket's keys)
+ *          an entry of -2^15 or lower, -inf among them, hides the bucket's keys (a row whose keys
+ *          are all hidden sees none); one above 2^15 counts as 2^15 and is reported as
+ *          FA_ERR_INVALID_ARG by fa_device_status. Between them a weight is off by what fp32 scores of
+ *          that size round, a few times 2^-24 of the score.
  *   map:   int32 [left + right + 1], device: the bucket of distances -left .. right. An entry
  *          outside [0, num_buckets) gives a bias of 0 and is reported as FA_ERR_INVALID_ARG by
  *          fa_device_status.

@@ -751,7 +751,9 @@ def rel_buckets(num_buckets=32, max_distance=128, bidirectional=True, device="cu
 
 def rel_bias(table, buckets, stream=None):
     """Lay out a bias table [num_buckets, H] (fp32 or bf16, one learned bias per bucket and query
-    head) for fwd, bwd and decode (fa_rel_bias). Do so again after the table changes."""
+    head) for fwd, bwd and decode (fa_rel_bias). Do so again after the table changes. Entries of
+    -2^15 or lower, -inf among them, hide their bucket's keys; entries above 2^15 are reported by
+    fa_device_status()."""
     dev, dtype, shape = table.get_device(), table.dtype, table.shape
     m, left, rows = buckets
     if (len(shape) != 2 or shape[0] != rows or dev < 0

@@ -38,6 +38,7 @@ namespace fa {
 namespace {
 
 constexpr unsigned kStatusInvalid = 1u;
+constexpr float kRelMaxBias = 32768.f;  // entries of a table
 
 __device__ __forceinline__ int clamp_distance(int x, int left, int right) {
   return x < -left ? -left : (x > right ? right : x);
@@ -82,6 +83,13 @@ __global__ void __launch_bounds__(256) rel_lines_kernel(const RelLinesArgs a) {
     const size_t at = static_cast<size_t>(n) * a.H + h;
     x = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.table)[at])
                : static_cast<const float*>(a.table)[at];
+    // fp32 scores and lse tell keys of such a bias apart to 2^-9 (a weight to less than the half step
+    // of bf16 that it is rounded by), and worse beyond: lower entries hide, higher ones are refused
+    if (x <= -kRelMaxBias) x = -INFINITY;
+    if (x > kRelMaxBias) {
+      record_error(a.status, kStatusInvalid);
+      x = kRelMaxBias;
+    }
   }
   a.lines[static_cast<size_t>(h) * r.stride() + e] = x * kLog2e;
 }
