@@ -1037,7 +1037,7 @@ fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* 
   a.key_tiles = seqlens_k != nullptr ? reinterpret_cast<int32_t*>(ws + w.tiles_off) : nullptr;
   a.pieces = fa::dkdv_pieces(
       static_cast<long long>(B) * H_kv * ((Nk + fa::kTile - 1) / fa::kTile),
-      static_cast<long long>(H / H_kv) * ((Nq + fa::kTile - 1) / fa::kTile));
+      static_cast<long long>(H / H_kv) * ((Nq + fa::kTile - 1) / fa::kTile), di->num_sms);
   a.dkdv_part = reinterpret_cast<float*>(ws + w.part_off);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool drop = a.drop.p8 > 0;

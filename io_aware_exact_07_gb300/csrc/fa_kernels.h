@@ -80,16 +80,15 @@ __device__ __forceinline__ uint32_t piece_bits(const BwdArgs& a, int u, int kt, 
 
 // Few key tiles (a short memory, few K/V heads) leave most SMs without a unit: their units are cut
 // into pieces where the longest CTA's steps (query tiles, kUnitSteps per unit, kMergeSteps for the
-// merge) become fewer. At most kMaxPieces units. (B=7 H=16 H_kv=4, 95 keys, 6763 queries, d=64: 94 us
-// with the merge against 367. These are instances of their own: with the pieces in all instances those
-// that do without took 3 to 19 % longer.)
-constexpr int kMaxPieces = 304;     // two for each SM
-constexpr int kPieceSms = 152;
+// merge) become fewer. At most kMaxPieces units. The tiles are counted by the keys' length, not by the
+// batch's lengths, which are on the device. (B=7 H=16 H_kv=4, 95 keys, 6763 queries, d=64: 94 us with
+// the merge against 367. They are instances of their own, so that the others keep their registers.)
+constexpr int kMaxPieces = 304;     // what the workspace has room for
 constexpr int kMinCutTiles = 10;    // fewer query tiles of a unit: no cut leaves fewer steps
-inline int dkdv_pieces(long long key_tiles, long long query_tiles) {
+inline int dkdv_pieces(long long key_tiles, long long query_tiles, int num_sms) {
   constexpr long long kUnitSteps = 3, kMergeSteps = 6;
   auto steps = [&](long long s) {
-    return (key_tiles * s + kPieceSms - 1) / kPieceSms * ((query_tiles + s - 1) / s + kUnitSteps) +
+    return (key_tiles * s + num_sms - 1) / num_sms * ((query_tiles + s - 1) / s + kUnitSteps) +
            (s > 1 ? kMergeSteps : 0);
   };
   int best = 1;
