@@ -663,7 +663,7 @@ static fa_status rel_decode_plan(int B, int H, int Hkv, int Nq, int Nk, int d, i
   }
   const long long heads = static_cast<long long>(B) * Hkv;
   const size_t rows = static_cast<size_t>(H / Hkv) * Nq;
-  p->step = rows <= (d == 64 ? 16 : 8);
+  p->step = rows <= static_cast<size_t>(fa::rel_step_rows(d));
   if (p->step) {
     p->w = paged_workspace(H / Hkv, d, Nq, num_ctas > 0 ? kMaxAxis : Nk, ctas);
     p->grid = p->w.ctas;

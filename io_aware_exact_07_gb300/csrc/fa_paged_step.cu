@@ -1021,12 +1021,12 @@ cudaError_t launch_impl(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
                       kMergeWarps * 32, stream, a, ctas, int(L::kRows));
 }
 
-template <int D, bool E4M3, bool REL = false>
+template <int D, bool E4M3>
 cudaError_t launch_rows(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
   const int rows = a.G * a.c.max_q;
-  return rows <= 8    ? launch_impl<D, E4M3, 1, REL>(a, ctas, stream)
-         : rows <= 16 ? launch_impl<D, E4M3, 2, REL>(a, ctas, stream)
-                      : launch_impl<D, E4M3, 3, REL>(a, ctas, stream);
+  return rows <= 8    ? launch_impl<D, E4M3, 1, false>(a, ctas, stream)
+         : rows <= 16 ? launch_impl<D, E4M3, 2, false>(a, ctas, stream)
+                      : launch_impl<D, E4M3, 3, false>(a, ctas, stream);
 }
 
 }  // namespace
@@ -1038,8 +1038,12 @@ cudaError_t launch_paged_step(const PagedAttnArgs& a, bool e4m3, int ctas, cudaS
 }
 
 cudaError_t launch_rel_step(const PagedAttnArgs& a, int ctas, cudaStream_t stream) {
-  return a.c.d == 64 ? launch_rows<64, false, true>(a, ctas, stream)
-                     : launch_rows<128, false, true>(a, ctas, stream);
+  static_assert(rel_step_rows(64) == 16 && rel_step_rows(128) == 8, "an instance per eight rows");
+  const int rows = a.G * a.c.max_q;
+  if (rows > rel_step_rows(a.c.d)) return cudaErrorInvalidValue;
+  if (a.c.d == 128) return launch_impl<128, false, 1, true>(a, ctas, stream);
+  return rows <= 8 ? launch_impl<64, false, 1, true>(a, ctas, stream)
+                   : launch_impl<64, false, 2, true>(a, ctas, stream);
 }
 
 }  // namespace fa
