@@ -158,6 +158,10 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
  *   fa_rel_bias; entries outside [0, num_buckets) take part in no sum). Written whole. Its sums
  *   are fp32, the last ones (over distances and over the keys beyond the range) with what each
  *   addition rounds off kept, and are taken with the D of the unrounded O.
+ * fa_bwd_cross: o and lse are fa_fwd_cross's outputs for the same inputs and options, over all the
+ * keys that they were computed from. (D is formed from the scores where a query tile sees a single key
+ * tile, without a look at o, and dtable rests on a row's weights summing to one: with the o and lse of an
+ * attention whose keys are divided among several calls these gradients would be wrong.)
  * Every output is deterministic on one device. fa_bwd_cross runs the kernels of fa_bwd; one that
  * takes the D of rows whose tile sees a single key tile from their scores, since few weights leave
  * nothing over which O's rounding would even out (not launched where no row can be one); and

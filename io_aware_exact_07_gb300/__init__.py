@@ -581,6 +581,8 @@ def fwd(q, k, v, scale=None, causal=False, dropout_p=0.0, seed=0, offset=0, bloc
     have fewer heads than q, fa_fwd_window when window = (left, right) is
     set; fa_fwd_cross when k and v have another length, q_offset is the position of
     the first query on the key axis, or rel_bias is a bias from rel_bias()).
+    With keys of another length the causal mask and the window count from there too: query i is
+    at key i + q_offset (q_offset = Nk - Nq puts the queries at the last keys).
     Returns (o, lse)."""
     _check_qkv(q, k, v)
     if rel_bias is not None or q_offset != 0 or k.shape[2] != q.shape[2]:
@@ -613,7 +615,8 @@ def bwd(q, k, v, o, dout, lse, scale=None, causal=False, dropout_p=0.0, seed=0, 
     """Allocate dQ, dK, dV (and the workspace if not given) and run fa_bwd
     (fa_bwd_gqa when k and v have fewer heads than q, fa_bwd_window when
     window = (left, right) is set, fa_bwd_cross as fwd). With a rel_bias and rel_grad the
-    gradient of its table follows, fp32 [num_buckets, H]: (dq, dk, dv, dtable)."""
+    gradient of its table follows, fp32 [num_buckets, H]: (dq, dk, dv, dtable). o and lse are fwd's
+    for the same arguments; those of keys divided among several calls give wrong gradients."""
     _check_qkv(q, k, v, o, dout)
     if rel_bias is not None or q_offset != 0 or k.shape[2] != q.shape[2]:
         return _bwd_cross(q, k, v, o, dout, lse, scale, causal, dropout_p, seed, offset,
