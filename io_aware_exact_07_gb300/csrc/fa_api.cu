@@ -201,8 +201,8 @@ fa::DropParams make_drop(float p, uint64_t seed, uint64_t offset) {
   // Philox4x32 key schedule (Salmon et al., SC'11): the key grows by the two
   // Weyl constants every round.
   for (int r = 0; r < 10; ++r) {
-    d.rk_lo[r] = d.seed_lo + static_cast<uint32_t>(r) * 0x9E3779B9u;
-    d.rk_hi[r] = d.seed_hi + static_cast<uint32_t>(r) * 0xBB67AE85u;
+    d.rk[r].x = d.seed_lo + static_cast<uint32_t>(r) * 0x9E3779B9u;
+    d.rk[r].y = d.seed_hi + static_cast<uint32_t>(r) * 0xBB67AE85u;
   }
   return d;
 }

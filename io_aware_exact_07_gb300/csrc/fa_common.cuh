@@ -135,8 +135,9 @@ struct DropParams {
   uint32_t seed_lo, seed_hi, off_lo, off_hi;
   // Philox round keys, (seed_lo + r W0, seed_hi + r W1) mod 2^32 for rounds
   // r = 0..9, filled on the host so that a kernel reads them as constant
-  // operands instead of bumping the key every round.
-  uint32_t rk_lo[10], rk_hi[10];
+  // operands instead of bumping the key every round. Pairs on 16-byte boundaries: dQ of H=16
+  // N=16384 d=64 takes 2454 us; as two arrays 2533 to 2555, by where they happen to begin.
+  alignas(16) uint2 rk[10];
 };
 
 struct SyncParams {
@@ -441,7 +442,7 @@ __device__ __forceinline__ uint4 philox4x32_10_rk(uint4 c, const DropParams& d) 
     const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c.z;
     const uint32_t lo0 = static_cast<uint32_t>(p0), hi0 = static_cast<uint32_t>(p0 >> 32);
     const uint32_t lo1 = static_cast<uint32_t>(p1), hi1 = static_cast<uint32_t>(p1 >> 32);
-    c = make_uint4(hi1 ^ c.y ^ d.rk_lo[r], lo1, hi0 ^ c.w ^ d.rk_hi[r], lo0);
+    c = make_uint4(hi1 ^ c.y ^ d.rk[r].x, lo1, hi0 ^ c.w ^ d.rk[r].y, lo0);
   }
   return c;
 }

@@ -22,9 +22,7 @@ struct FwdArgs {
 
 struct BwdArgs {
   MaskParams mask;
-  // (at a multiple of 16 bytes: with the dropout kernels' constants 8 bytes off it, dQ of H=16 N=16384
-  // d=64 took 2553 us instead of 2529. The forward does not mind.)
-  alignas(16) DropParams drop;
+  DropParams drop;
   SyncParams sync;
   float scale;       // softmax scale (dK and dQ are multiplied by it)
   float scale_log2;  // scale * log2(e)
